@@ -64,7 +64,9 @@ typedef enum {
   SF_ERR_TIMEOUT = -5      /* a bounded host wait ran out                    */
 } sf_status;
 
-typedef enum { SF_BF16 = 0, SF_FP32 = 1 } sf_dtype;
+/* SF_E4M3: 8-bit floats (4 exponent bits, 3 fraction bits, largest value 448),
+ * taken only where a call says so. */
+typedef enum { SF_BF16 = 0, SF_FP32 = 1, SF_E4M3 = 2 } sf_dtype;
 
 /* AdamW hyper-parameters.  Given in double; the library derives the fp32
  * constants the kernels use (1-beta1, 1-beta2, 1-lr*wd, lr/(1-beta1^t),
@@ -367,6 +369,98 @@ sf_status lce_forward_backward(const void* H, const void* W, const int32_t* labe
  * memory `val` (after lsp_projector_fit_step they differ from the values
  * the projector was created with).  Out-of-range ids read as 0. */
 sf_status lsp_projector_export_values(lsp_projector p, float* val, void* stream);
+
+/* ------------------------------------------------------------------------
+ * (d) The output end of a training step: what turns the last block's output
+ * into the loss and its gradients into the gradients that the update (a)
+ * takes.  Dropout and the residual's addition, the norm, the output layer's
+ * cross-entropy by pieces of the vocabulary.
+ *
+ * A row-major matrix: row i starts ld elements after row i - 1, ld >= cols.
+ * Any alignment and ld are accepted unless a call says otherwise; rows whose
+ * units of 8 columns are aligned to their size (ld a multiple of 8; base 16
+ * bytes in bf16, 32 in fp32, 8 in e4m3) take one wide access per unit.
+ * An output may be the very matrix (same data, ld and type) of an input of
+ * the same size; other overlaps are undefined.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  void* data;
+  int64_t rows, cols, ld;
+  int32_t dtype; /* sf_dtype */
+} sf_matrix;
+
+/* Dropout's generator: Philox-4x32 with 10 rounds (Salmon et al., "Parallel
+ * random numbers: as easy as 1, 2, 3", 2011).  The mask is a function of
+ * seed, offset, row and column only:
+ *   key     = (seed mod 2^32, seed / 2^32)
+ *   counter = (b mod 2^32, b / 2^32, o mod 2^32, o / 2^32),
+ *             b = row * ceil(cols / 8) + col / 8,  o = offset + *device_offset
+ *   16 bits of column c: the low (c even) or high half of word (c mod 8) / 2.
+ * A column is kept where its bits are at least t = round(65536 p); kept
+ * values are multiplied by 65536 / (65536 - t).  Give every dropout of every
+ * step an offset of its own.  device_offset (device uint64, or NULL) is read
+ * when the kernel runs, so a captured graph draws new masks on each replay. */
+typedef struct {
+  uint64_t seed, offset;
+  const uint64_t* device_offset;
+} sf_rng;
+
+/* y = residual + m o x f (y = m o x f without a residual): f and the mask m
+ * as above.  Its own backward pass: dx = the same call on dy without a
+ * residual (the residual's gradient is dy).  A dropped element contributes
+ * exactly 0, a NaN or infinity included.
+ *   x, y, residual : SF_BF16 or SF_FP32; residual (NULL: none) has y's type.
+ *   p              : 0..1; below 2^-17 nothing is dropped and rng may be NULL.
+ * fp32 arithmetic, one rounding at the end.  Errors: SF_ERR_INVALID for a
+ * NULL or misshaped matrix, p outside [0, 1], p > 0 without rng. */
+sf_status sf_dropout(const sf_matrix* x, const sf_matrix* residual,
+                     const sf_matrix* y, double p, const sf_rng* rng,
+                     void* stream);
+
+/* s = residual + dropout(x);  rstd = 1 / sqrt(mean(s^2) + eps);  h = s rstd gain
+ * over rows of 1..16384 columns (SF_ERR_UNSUPPORTED beyond).
+ *   x        : SF_BF16 or SF_FP32.      residual : NULL (s = dropout(x)), or
+ *              SF_BF16 or SF_FP32.      gain : [cols], gain_dtype bf16 or fp32.
+ *   sum      : receives s, residual's type; NULL: not written.
+ *   h        : receives h, x's type; NULL: not written.
+ *   h8       : receives h in e4m3, h8_scale its scales (fp32, dense [rows]
+ *              [ceil(cols / group)], or [rows] with group 0); NULL: not
+ *              written.  Per group of `group` (32, 64, 128; 0: the row)
+ *              columns scale = max(max |h| / 448, 2^-126) and the stored
+ *              value is h / scale rounded to e4m3, so h is about value *
+ *              scale.  A NaN makes its group's scale NaN.
+ *   rstd     : fp32 [rows], for the backward pass; NULL: not written.
+ * At least one of h and h8.  The norm is taken of s in fp32, before s is
+ * rounded to its stored type; h and h8 are each rounded once, from fp32. */
+sf_status sf_add_rmsnorm_forward(const sf_matrix* x, const sf_matrix* residual,
+                                 const void* gain, sf_dtype gain_dtype,
+                                 double eps, double p, const sf_rng* rng,
+                                 const sf_matrix* sum, const sf_matrix* h,
+                                 const sf_matrix* h8, float* h8_scale,
+                                 int32_t group, float* rstd, void* stream);
+
+/* The gradients of that call: with n = s rstd,
+ *   ds = dsum + rstd (dh gain - n mean(dh gain n))
+ *   dresidual = ds,  dx = m o ds f (the forward call's p and rng),
+ *   dgain_j = sum over rows of dh_j n_j.
+ *   dh        : gradient of h.            sum, rstd : as the forward wrote them.
+ *   dsum      : gradient that reaches s from elsewhere (the residual stream's
+ *               later use), sum's type; NULL: none.
+ *   dresidual : sum's type;  dx : dh's type;  dgain : [cols], dgain_dtype bf16
+ *               or fp32.  Each may be NULL, not all.
+ *   ws        : device scratch of ws_bytes >= sf_add_rmsnorm_workspace_bytes(
+ *               rows, cols), 16-byte aligned; only read with dgain.
+ * fp32 arithmetic; dgain's sum runs in a fixed order (no atomics). */
+size_t sf_add_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
+
+sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum,
+                                  const void* gain, sf_dtype gain_dtype,
+                                  const float* rstd, const sf_matrix* dsum,
+                                  double p, const sf_rng* rng,
+                                  const sf_matrix* dresidual,
+                                  const sf_matrix* dx, void* dgain,
+                                  sf_dtype dgain_dtype, void* ws,
+                                  size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * (c) Layer-sliding window.

@@ -1,0 +1,198 @@
+// Row-wise access shared by the dropout and norm kernels: a thread's unit is
+// eight consecutive columns of a row (one 16-byte load in bf16, one 32-byte
+// load in fp32), and the counter-based generator gives one unit's random
+// bits per evaluation.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "common.h"
+
+namespace sf {
+
+template <typename T>
+struct Unit;
+template <>
+struct Unit<__nv_bfloat16> {
+  uint32_t w[4];
+};
+template <>
+struct Unit<float> {
+  float f[8];
+};
+
+__device__ __forceinline__ void unpack(const Unit<__nv_bfloat16>& u, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u.w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u.w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void unpack(const Unit<float>& u, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = u.f[i];
+}
+__device__ __forceinline__ void pack(const float (&v)[8], Unit<__nv_bfloat16>& u) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);   // round to nearest even
+    u.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+__device__ __forceinline__ void pack(const float (&v)[8], Unit<float>& u) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u.f[i] = v[i];
+}
+
+// Whole-unit accesses.  Not the read-only path: outputs may be their inputs.
+__device__ __forceinline__ void ld_unit(const __nv_bfloat16* p, Unit<__nv_bfloat16>& u) {
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.w[0]), "=r"(u.w[1]), "=r"(u.w[2]), "=r"(u.w[3])
+               : "l"(p));
+}
+__device__ __forceinline__ void ld_unit(const float* p, Unit<float>& u) {
+  asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(u.f[0]), "=f"(u.f[1]), "=f"(u.f[2]), "=f"(u.f[3]), "=f"(u.f[4]), "=f"(u.f[5]), "=f"(u.f[6]),
+                 "=f"(u.f[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void st_unit(__nv_bfloat16* p, const Unit<__nv_bfloat16>& u) {
+  asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(u.w[0]), "r"(u.w[1]), "r"(u.w[2]), "r"(u.w[3])
+               : "memory");
+}
+__device__ __forceinline__ void st_unit(float* p, const Unit<float>& u) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(u.f[0]), "f"(u.f[1]),
+               "f"(u.f[2]), "f"(u.f[3]), "f"(u.f[4]), "f"(u.f[5]), "f"(u.f[6]), "f"(u.f[7])
+               : "memory");
+}
+
+// The first n (0..8) elements of a unit; the others read as zero.  VEC: the
+// unit is aligned, so a whole one is one access.
+template <bool VEC>
+__device__ __forceinline__ void load_unit(const __nv_bfloat16* p, int n, Unit<__nv_bfloat16>& u) {
+  if (VEC && n == 8) {
+    ld_unit(p, u);
+    return;
+  }
+  const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = 2 * i < n ? q[2 * i] : 0u, hi = 2 * i + 1 < n ? q[2 * i + 1] : 0u;
+    u.w[i] = lo | (hi << 16);
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void load_unit(const float* p, int n, Unit<float>& u) {
+  if (VEC && n == 8) {
+    ld_unit(p, u);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u.f[i] = i < n ? p[i] : 0.0f;
+}
+template <bool VEC>
+__device__ __forceinline__ void store_unit(__nv_bfloat16* p, int n, const float (&v)[8]) {
+  Unit<__nv_bfloat16> u;
+  pack(v, u);
+  if (VEC && n == 8) {
+    st_unit(p, u);
+    return;
+  }
+  uint16_t* q = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (2 * i < n) q[2 * i] = (uint16_t)(u.w[i] & 0xFFFFu);
+    if (2 * i + 1 < n) q[2 * i + 1] = (uint16_t)(u.w[i] >> 16);
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_unit(float* p, int n, const float (&v)[8]) {
+  if (VEC && n == 8) {
+    Unit<float> u;
+    pack(v, u);
+    st_unit(p, u);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) p[i] = v[i];
+}
+
+// Dropout's constants: an element is kept where its 16 random bits are at
+// least `threshold` = round(65536 p), and kept values are multiplied by
+// factor = 65536 / (65536 - threshold), so the expectation is exact for the
+// probability threshold / 65536 that is really used (within 2^-17 of p).
+// threshold = 0: no dropout.
+struct DropConsts {
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* device_offset;   // added to offset when not null
+  float factor;
+  uint32_t threshold;
+};
+
+sf_status make_drop_consts(double p, const sf_rng* rng, DropConsts* out);
+
+// The generator's per-call words: key and the upper counter half.
+struct DropKey {
+  uint32_t k0, k1, c2, c3;
+};
+__device__ __forceinline__ DropKey drop_key(const DropConsts& d) {
+  uint64_t off = d.offset;
+  if (d.device_offset) off += *d.device_offset;
+  return DropKey{(uint32_t)d.seed, (uint32_t)(d.seed >> 32), (uint32_t)off, (uint32_t)(off >> 32)};
+}
+
+// Philox-4x32 with 10 rounds (Salmon, Moraes, Dror, Shaw: "Parallel random
+// numbers: as easy as 1, 2, 3", 2011): 128 bits for the unit with index b,
+// 16 per column.  Eight columns share one evaluation, so a column costs 2.5
+// 32 x 32 -> 64 multiplications; with 32 bits a column (twice that) the
+// bf16 kernels would be bound by the multiplier and not by memory.
+__device__ __forceinline__ void drop_unit(float (&v)[8], uint64_t b, const DropKey& key, uint32_t threshold,
+                                          float factor) {
+  uint32_t c0 = (uint32_t)b, c1 = (uint32_t)(b >> 32), c2 = key.c2, c3 = key.c3, k0 = key.k0, k1 = key.k1;
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t m0 = (uint64_t)c0 * 0xD2511F53u, m1 = (uint64_t)c2 * 0xCD9E8D57u;
+    const uint32_t n0 = (uint32_t)(m1 >> 32) ^ c1 ^ k0, n2 = (uint32_t)(m0 >> 32) ^ c3 ^ k1;
+    c0 = n0;
+    c1 = (uint32_t)m1;
+    c2 = n2;
+    c3 = (uint32_t)m0;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  const uint32_t w[4] = {c0, c1, c2, c3};
+  // a dropped element is 0 whatever its value (a NaN or infinity included)
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = (w[j] & 0xFFFFu) >= threshold ? v[2 * j] * factor : 0.0f;
+    v[2 * j + 1] = (w[j] >> 16) >= threshold ? v[2 * j + 1] * factor : 0.0f;
+  }
+}
+
+// A matrix argument as the kernels see it.
+template <typename T>
+__device__ __forceinline__ T* row_ptr(void* base, int64_t ld, int64_t row) {
+  return static_cast<T*>(base) + row * ld;
+}
+template <typename T>
+__device__ __forceinline__ const T* row_ptr(const void* base, int64_t ld, int64_t row) {
+  return static_cast<const T*>(base) + row * ld;
+}
+
+// Checks a matrix argument on the host: shape, leading dimension and type.
+// `want_rows` / `want_cols` < 0 accept any size.  dtypes: a mask of 1 << sf_dtype.
+sf_status check_matrix(const sf_matrix* m, const char* name, int64_t want_rows, int64_t want_cols, unsigned dtypes);
+
+inline size_t dtype_bytes(int32_t t) { return t == SF_FP32 ? 4 : t == SF_BF16 ? 2 : 1; }
+
+// Whether every unit of the matrix starts on a whole-unit boundary.
+inline bool units_aligned(const sf_matrix* m) {
+  if (!m) return true;
+  const size_t unit = 8 * dtype_bytes(m->dtype);
+  return reinterpret_cast<uintptr_t>(m->data) % unit == 0 && (m->ld % 8 == 0 || m->rows <= 1);
+}
+
+}  // namespace sf

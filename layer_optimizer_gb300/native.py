@@ -14,7 +14,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libsfopt.so")
 
 SF_OK, SF_ERR_INVALID, SF_ERR_CUDA, SF_ERR_OOM, SF_ERR_UNSUPPORTED, SF_ERR_TIMEOUT = 0, -1, -2, -3, -4, -5
-SF_BF16, SF_FP32 = 0, 1
+SF_BF16, SF_FP32, SF_E4M3 = 0, 1, 2
 SF_MAX_TENSORS_PER_LAUNCH = 48
 
 # Every symbol include/sfopt.h declares.
@@ -31,6 +31,7 @@ EXPORTS = [
     "sf_gemm_abt_bf16", "sf_gemm_bf16", "sf_bench_gather_rate", "sf_bench_tmem_rate", "sf_bench_l2_gather_rate",
     "lce_workspace_bytes", "lce_forward_backward",
     "sf_test_device_wait_runs_out",
+    "sf_dropout", "sf_add_rmsnorm_forward", "sf_add_rmsnorm_workspace_bytes", "sf_add_rmsnorm_backward",
 ]
 
 
@@ -69,6 +70,15 @@ class lsp_layer(ctypes.Structure):
                 ("W", ctypes.c_void_p), ("w_dtype", ctypes.c_int), ("w_bf16_mirror", ctypes.c_void_p),
                 ("m", ctypes.c_int64), ("n", ctypes.c_int64), ("m_host", ctypes.c_void_p),
                 ("v_host", ctypes.c_void_p)]
+
+
+class sf_matrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
+class sf_rng(ctypes.Structure):
+    _fields_ = [("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("device_offset", ctypes.c_void_p)]
 
 
 _P = ctypes.c_void_p
@@ -123,6 +133,12 @@ _SIGS = {
     "lce_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64]),
     "sf_test_device_wait_runs_out": (_ST, [_I64, _P]),
     "lce_forward_backward": (_ST, [_P, _P, _P, _I64, _I64, _I64, _I64, _I32, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "sf_dropout": (_ST, [_P, _P, _P, ctypes.c_double, _P, _P]),
+    "sf_add_rmsnorm_forward": (_ST, [_P, _P, _P, _INT, ctypes.c_double, ctypes.c_double, _P, _P, _P, _P, _P, _I32, _P,
+                                     _P]),
+    "sf_add_rmsnorm_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "sf_add_rmsnorm_backward": (_ST, [_P, _P, _P, _INT, _P, _P, ctypes.c_double, _P, _P, _P, _P, _INT, _P,
+                                      ctypes.c_size_t, _P]),
 }
 
 _lib = None
@@ -331,6 +347,97 @@ def lce_workspace_bytes(n_tokens, d, vocab, chunk):
 def lce_forward_backward(H, W, labels, N, D, V, chunk, ignore_index, loss, dH, dW, ws, ws_bytes, stream=None):
     _check(load().lce_forward_backward(_addr(H), _addr(W), _addr(labels), N, D, V, chunk, ignore_index, _addr(loss),
                                        _addr(dH), _addr(dW), _addr(ws), ws_bytes, _stream(stream)))
+
+
+# ------------------------------------------------------------------ (d) ----
+
+_DTYPES = None
+
+
+def _dtype(t, name):
+    """sf_dtype of a torch tensor."""
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.bfloat16: SF_BF16, torch.float32: SF_FP32, torch.float8_e4m3fn: SF_E4M3}
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise SfError(SF_ERR_UNSUPPORTED, f"{name}: {t.dtype} is not taken here") from None
+
+
+def _reachable(t, name):
+    if not (t.is_cuda or t.is_pinned()):
+        raise SfError(SF_ERR_INVALID, f"{name} must be in device or pinned host memory")
+
+
+def matrix(t, name="matrix"):
+    """sf_matrix of a 2D torch tensor with unit column stride (None stays None; an sf_matrix stays itself)."""
+    if t is None or isinstance(t, sf_matrix):
+        return t
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise SfError(SF_ERR_INVALID, f"{name} must be two-dimensional with unit column stride")
+    _reachable(t, name)
+    rows, cols = t.shape
+    return sf_matrix(t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else max(cols, t.stride(0)), _dtype(t, name))
+
+
+def _ref(m):
+    return None if m is None else ctypes.byref(m)
+
+
+def _vector(t, n, name, dtypes=None):
+    """Address of a dense device vector of n elements (None and addresses pass)."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.numel() != n or not t.is_contiguous():
+        raise SfError(SF_ERR_INVALID, f"{name} must be dense with {n} elements")
+    if dtypes is not None and str(t.dtype) not in dtypes:
+        raise SfError(SF_ERR_UNSUPPORTED, f"{name}: {t.dtype} is not taken here")
+    _reachable(t, name)
+    return t.data_ptr()
+
+
+_F32 = ("torch.float32",)
+
+
+def rng(seed, offset=0, device_offset=None):
+    """sf_rng: the generator of one dropout call (device_offset: int64 tensor of one element, or None)."""
+    return sf_rng(seed, offset, _vector(device_offset, 1, "device_offset", ("torch.int64", "torch.uint64")))
+
+
+def sf_dropout(x, y, p, rng=None, residual=None, stream=None):
+    """y = residual + dropout(x) (y = dropout(x) without a residual); tensors or sf_matrix."""
+    x, y, residual = matrix(x, "x"), matrix(y, "y"), matrix(residual, "residual")
+    _check(load().sf_dropout(_ref(x), _ref(residual), _ref(y), float(p), _ref(rng), _stream(stream)))
+
+
+def sf_add_rmsnorm_forward(x, residual, gain, eps, sum=None, h=None, h8=None, h8_scale=None, group=0, rstd=None, p=0.0,
+                           rng=None, stream=None):
+    """s = residual + dropout(x), its root-mean-square norm h, and h in e4m3 with scales; tensors or sf_matrix."""
+    x, residual, sum = matrix(x, "x"), matrix(residual, "residual"), matrix(sum, "sum")
+    h, h8 = matrix(h, "h"), matrix(h8, "h8")
+    groups = -(-x.cols // group) if group > 0 else 1
+    _check(load().sf_add_rmsnorm_forward(
+        _ref(x), _ref(residual), _vector(gain, x.cols, "gain"), _dtype(gain, "gain"), float(eps), float(p), _ref(rng),
+        _ref(sum), _ref(h), _ref(h8), _vector(h8_scale, x.rows * groups, "h8_scale", _F32), group,
+        _vector(rstd, x.rows, "rstd", _F32), _stream(stream)))
+
+
+def sf_add_rmsnorm_workspace_bytes(rows, cols):
+    return load().sf_add_rmsnorm_workspace_bytes(rows, cols)
+
+
+def sf_add_rmsnorm_backward(dh, sum, gain, rstd, dsum=None, dresidual=None, dx=None, dgain=None, p=0.0, rng=None,
+                            ws=None, stream=None):
+    """The gradients of sf_add_rmsnorm_forward (ws: a uint8 workspace tensor, needed with dgain)."""
+    dh, sum, dsum = matrix(dh, "dh"), matrix(sum, "sum"), matrix(dsum, "dsum")
+    dresidual, dx = matrix(dresidual, "dresidual"), matrix(dx, "dx")
+    _check(load().sf_add_rmsnorm_backward(
+        _ref(dh), _ref(sum), _vector(gain, dh.cols, "gain"), _dtype(gain, "gain"),
+        _vector(rstd, dh.rows, "rstd", _F32), _ref(dsum), float(p), _ref(rng), _ref(dresidual), _ref(dx),
+        _vector(dgain, dh.cols, "dgain"), SF_FP32 if dgain is None else _dtype(dgain, "dgain"), _addr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
 
 
 # ------------------------------------------------------------------ (c) ----
