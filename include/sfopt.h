@@ -462,6 +462,41 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum,
                                   sf_dtype dgain_dtype, void* ws,
                                   size_t ws_bytes, void* stream);
 
+/* The linear cross-entropy of lce_forward_backward by pieces of the
+ * vocabulary: the same loss and gradients, without keeping any token's
+ * logits.  The log-sum-exp is taken tile by tile as the logits leave the
+ * tensor cores; the gradient is formed one piece of the vocabulary after the
+ * other, so the workspace holds one N x piece block of bf16 whatever V, and
+ * each row of dW is written once.
+ *   H      : [N][D], W : [V][D], both SF_BF16, 16-byte aligned base and rows
+ *            (ld a multiple of 8); any N, D, V >= 1.
+ *   labels : device int32 [N]; ignore_index and labels outside [0, V) as in
+ *            lce_forward_backward.
+ *   piece  : vocabulary rows per piece, a multiple of 256; 0: as many as 512
+ *            MB of workspace hold (at least 2048).  Larger pieces compute
+ *            fewer logits twice; the last piece's never are.
+ *   grad_scale : multiplies dH and dW (1 for the loss's own gradient; 1 / k
+ *            for one of k accumulated micro-batches), not the losses.
+ *   loss   : device fp32 [1]: mean over the labelled tokens (0 if none), or NULL.
+ *   token_loss : device fp32 [N], 0 for unlabelled tokens; or NULL.
+ *   dH, dW : [N][D], [V][D], each SF_BF16 or SF_FP32, 16-byte aligned base and
+ *            rows; either or both may be NULL.
+ *   ws     : device scratch of ws_bytes >= lce_vocab_workspace_bytes(N, D, V,
+ *            piece), 256-byte aligned.
+ * Logits, exponentials and sums in fp32; dZ rounded to bf16 before the two
+ * gradient products (the last piece's passes through one more bf16 rounding,
+ * its label's entry does not); dH is summed over pieces in fp32 and rounded
+ * once.  Deterministic. */
+size_t lce_vocab_workspace_bytes(int64_t n_tokens, int64_t d, int64_t vocab,
+                                 int64_t piece);
+
+sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W,
+                                     const int32_t* labels, int64_t piece,
+                                     int32_t ignore_index, double grad_scale,
+                                     float* loss, float* token_loss,
+                                     const sf_matrix* dH, const sf_matrix* dW,
+                                     void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------------
  * (c) Layer-sliding window.
  *

@@ -67,6 +67,12 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // path with plain loads or are rejected.
 bool on_current_device(const void* p);
 
+// Checks a matrix argument on the host: shape, leading dimension and type.
+// want_rows / want_cols < 0 accept any size.  dtypes: a mask of 1 << sf_dtype.
+sf_status check_matrix(const sf_matrix* m, const char* name, int64_t want_rows, int64_t want_cols, unsigned dtypes);
+
+inline size_t dtype_bytes(int32_t t) { return t == SF_FP32 ? 4 : t == SF_BF16 ? 2 : 1; }
+
 // Default bound for host waits, in milliseconds (SF_TIMEOUT_MS or 600 s).
 int64_t default_timeout_ms();
 
@@ -129,6 +135,37 @@ constexpr int kTcTileN = 256;
 sf_status tc_gemm(const void* A, bool a_mn, const void* B, bool b_mn, float* C, int64_t M, int64_t N, int64_t K,
                   int64_t lda, int64_t ldb, int64_t ldc, float alpha, bool accumulate, cudaStream_t s,
                   float2* row_stats = nullptr);
+
+// The same GEMM with the epilogues of the vocabulary-piece cross-entropy.
+enum TcEpilogue : int {
+  kTcF32 = 0,    // C fp32, as above
+  kTcSplit = 1,  // C fp32 [splits][M][ldc]: partial products over parts of K
+  kTcBf16 = 2,   // C bf16
+  kTcStats = 3,  // row_stats, label_logit, and with `store` C = exp(A B^T - tile maximum) in bf16
+  kTcGrad = 4    // C = (exp(A B^T - lse) - onehot(label)) * factor in bf16; 0 where lse is +infinity
+};
+struct TcJob {
+  const void* A = nullptr;
+  const void* B = nullptr;
+  bool a_mn = false, b_mn = false;
+  int64_t M = 0, N = 0, K = 0, lda = 0, ldb = 0;
+  TcEpilogue epi = kTcF32;
+  void* C = nullptr;               // fp32 or bf16 by the epilogue; null: not written (kTcStats without store)
+  int64_t ldc = 0;
+  float alpha = 1.0f;
+  bool accumulate = false;         // fp32 epilogues
+  int splits = 1;                  // kTcSplit
+  float2* row_stats = nullptr;     // kTcF32: [M][tiles]; kTcStats: [M][stats_ld], tile col0 / 256 + t
+  int32_t stats_ld = 0;
+  int32_t col0 = 0;                // vocabulary id of column 0 (a multiple of 256)
+  bool store = false;
+  const int32_t* labels = nullptr; // [M] (kTcStats, kTcGrad); ids outside the product's columns match nothing
+  float* label_logit = nullptr;    // [M]
+  const float* lse = nullptr;      // [M]
+  const float* factor = nullptr;   // device, one value
+  uint32_t* zero = nullptr;        // device word that the launch sets to 0 (kTcStats)
+};
+sf_status tc_gemm(const TcJob& job, cudaStream_t s);
 
 sf_status make_adam_consts(const sf_adamw_hparams* hp, int64_t step, bool with_decay,
                            AdamConsts* out);

@@ -98,26 +98,6 @@ sf_status make_drop_consts(double p, const sf_rng* rng, DropConsts* out) {
   return SF_OK;
 }
 
-sf_status check_matrix(const sf_matrix* m, const char* name, int64_t want_rows, int64_t want_cols, unsigned dtypes) {
-  if (!m) return fail(SF_ERR_INVALID, "%s is NULL", name);
-  if (m->rows < 0 || m->cols < 0) return fail(SF_ERR_INVALID, "%s: negative size", name);
-  if (m->dtype < 0 || m->dtype > 31 || !(dtypes >> m->dtype & 1u))
-    return fail(SF_ERR_UNSUPPORTED, "%s: type %d is not taken here", name, (int)m->dtype);
-  if ((want_rows >= 0 && m->rows != want_rows) || (want_cols >= 0 && m->cols != want_cols))
-    return fail(SF_ERR_INVALID, "%s is %lld x %lld, expected %lld x %lld", name, (long long)m->rows,
-                (long long)m->cols, (long long)(want_rows >= 0 ? want_rows : m->rows),
-                (long long)(want_cols >= 0 ? want_cols : m->cols));
-  if (m->rows && m->cols) {
-    if (!m->data) return fail(SF_ERR_INVALID, "%s: data is NULL", name);
-    if (m->ld < m->cols && m->rows > 1) return fail(SF_ERR_INVALID, "%s: ld %lld is below its %lld columns", name,
-                                                    (long long)m->ld, (long long)m->cols);
-    if (reinterpret_cast<uintptr_t>(m->data) % dtype_bytes(m->dtype))
-      return fail(SF_ERR_INVALID, "%s: data is not aligned to its type", name);
-    if (m->ld > INT64_MAX / 4 / m->rows) return fail(SF_ERR_UNSUPPORTED, "%s: sizes too large", name);
-  }
-  return SF_OK;
-}
-
 }  // namespace sf
 
 extern "C" {

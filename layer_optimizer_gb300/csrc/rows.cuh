@@ -182,12 +182,6 @@ __device__ __forceinline__ const T* row_ptr(const void* base, int64_t ld, int64_
   return static_cast<const T*>(base) + row * ld;
 }
 
-// Checks a matrix argument on the host: shape, leading dimension and type.
-// `want_rows` / `want_cols` < 0 accept any size.  dtypes: a mask of 1 << sf_dtype.
-sf_status check_matrix(const sf_matrix* m, const char* name, int64_t want_rows, int64_t want_cols, unsigned dtypes);
-
-inline size_t dtype_bytes(int32_t t) { return t == SF_FP32 ? 4 : t == SF_BF16 ? 2 : 1; }
-
 // Whether every unit of the matrix starts on a whole-unit boundary.
 inline bool units_aligned(const sf_matrix* m) {
   if (!m) return true;

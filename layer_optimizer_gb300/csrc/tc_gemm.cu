@@ -235,6 +235,16 @@ struct TcGemmArgs {
   int32_t a_mn, b_mn;    // operand stored MN-major ([K][M], [K][N]) instead of K-major:
                          // 1 loaded as two 2D boxes, 2 as one 3D box (MN a multiple of 64)
   float2* row_stats;     // optional [M][n_tiles]: per row and column tile, (max, sum exp(c - max)) of C
+  int32_t splits;        // parts of the sum over K, each a product of its own (kTcSplit: C is [splits][M][N])
+  // softmax epilogues (kTcStats, kTcGrad)
+  int32_t stats_ld;      // tiles of a row of row_stats (kTcStats)
+  int32_t col0;          // vocabulary id of column 0, a multiple of the tile width
+  int32_t store;         // kTcStats: also write exp(c - tile maximum) to C
+  const int32_t* labels; // [M]
+  float* label_logit;    // [M]: receives C at each row's label (kTcStats)
+  const float* lse;      // [M] (kTcGrad)
+  const float* factor;   // one value (kTcGrad)
+  uint32_t* zero;        // set to 0 by the launch (kTcStats)
 };
 
 // Folds 32 values of a row into a running (max, sum of exp(x - max)):
@@ -254,6 +264,57 @@ __device__ __forceinline__ void fold_row_stats(const float (&x)[32], int valid, 
   s = acc;
 }
 
+// 2^x of the exponential unit (|relative error| about 2^-22); arguments here
+// are differences to a row's maximum or log-sum-exp, so at most 0 up to
+// rounding.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.44269504f;
+
+// Writes 32 values of this lane's row, rounded to bf16, into half `half`
+// (0: columns 0-31, 1: 32-63) of a warp's 32-row x 64-column staging box,
+// 128-byte swizzled.
+__device__ __forceinline__ void stage_bf16(uint32_t buf, int lane, int half, const float (&v)[32]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * q + 2 * i], v[8 * q + 2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + (uint32_t)lane * 128u +
+                                                                  (uint32_t)(((4 * half + q) ^ (lane & 7)) * 16)),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
+  }
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   map),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
+// The epilogue (template argument EPI) decides what becomes of a tile:
+//   kTcF32    C (fp32) stored or added to, optional row statistics;
+//   kTcSplit  fp32 partial products [splits][M][N], stored or added to;
+//   kTcBf16   C rounded to bf16;
+//   kTcStats  per row and tile the maximum and sum of exponentials, the
+//             label's logit, and optionally exp(c - maximum) in bf16: the
+//             logits themselves never leave tensor memory;
+//   kTcGrad   (exp(c - lse) - [column is the label]) * factor in bf16, 0 for
+//             an unlabelled row.
+template <int EPI>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_tc_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
               const __grid_constant__ CUtensorMap map_c, const TcGemmArgs g) {
@@ -272,11 +333,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();              // 0: issues the MMAs, 1: its peer
   const int pair = blockIdx.x / kPair, n_pairs = gridDim.x / kPair;
-  const int nk = (g.K + kBK - 1) / kBK;
+  const int nk_all = (g.K + kBK - 1) / kBK;
   const int m_tiles = (g.M + kPair * kBM - 1) / (kPair * kBM);   // 256-row tiles
   const int n_tiles = (g.N + kBN - 1) / kBN;
   const int tiles = m_tiles * n_tiles;
+  // work items: the tiles, once per part of K; part p takes the K slabs
+  // [nk_all p / splits, nk_all (p + 1) / splits)
+  const int splits = EPI == kTcSplit ? g.splits : 1;
+  const int items = tiles * splits;
+  auto slab0 = [&](int part) { return EPI == kTcSplit ? (int)((int64_t)nk_all * part / splits) : 0; };
+  auto slab1 = [&](int part) { return EPI == kTcSplit ? (int)((int64_t)nk_all * (part + 1) / splits) : nk_all; };
 
+  if (EPI == kTcStats && blockIdx.x == 0 && threadIdx.x == 0 && g.zero) *g.zero = 0;
   if (threadIdx.x == 0) {
     prefetch_tensormap(&map_a);
     prefetch_tensormap(&map_b);
@@ -310,11 +378,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       int s = 0, issued = 0;
       uint32_t pass = 0;
       bool failed = false;
-      for (int t = pair; t < tiles && !failed; t += n_pairs) {
+      for (int it = pair; it < items && !failed; it += n_pairs) {
+        const int part = EPI == kTcSplit ? it / tiles : 0, t = EPI == kTcSplit ? it % tiles : it;
         const int mt = g.n_fast ? t / n_tiles : t % m_tiles, nt = g.n_fast ? t % n_tiles : t / m_tiles;
         const int m0 = mt * (kPair * kBM) + (int)rank * kBM;
         const int nb = nt * kBN + (int)rank * kBRows;
-        for (int kb = 0; kb < nk; ++kb) {
+        const int k1 = slab1(part);
+        for (int kb = slab0(part); kb < k1; ++kb) {
           if (issued >= kStages && !mbar_wait_cluster(&empty[s], pass ^ 1u)) {
             failed = true;
             break;
@@ -361,14 +431,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       int s = 0, j = 0;
       uint32_t pass = 0;
       bool failed = false;
-      for (int t = pair; t < tiles && !failed; t += n_pairs, ++j) {
+      for (int it = pair; it < items && !failed; it += n_pairs, ++j) {
+        const int part = EPI == kTcSplit ? it / tiles : 0, k0 = slab0(part), k1 = slab1(part);
         const int b = j & 1;
         const uint32_t use = (uint32_t)(j >> 1);
         // both epilogues have read this accumulator buffer out (its previous use)
         if (use > 0 && !mbar_wait_cluster(&tempty[b], (use - 1u) & 1u)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem + (uint32_t)(b * kTmemCols);
-        for (int kb = 0; kb < nk; ++kb) {
+        for (int kb = k0; kb < k1; ++kb) {
           if (!mbar_wait_cluster(&full[s], pass)) {
             failed = true;
             break;
@@ -379,7 +450,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint64_t bdesc = g.b_mn ? umma_desc_mn_sw128(a_addr + kStageA) : umma_desc_sw128(a_addr + kStageA);
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
-            tc_mma(d_tmem, adesc + a_step * (uint32_t)k, bdesc + b_step * (uint32_t)k, idesc, (kb | k) != 0 ? 1u : 0u);
+            tc_mma(d_tmem, adesc + a_step * (uint32_t)k, bdesc + b_step * (uint32_t)k, idesc, kb != k0 || k != 0 ? 1u : 0u);
           tc_commit_pair(empty_a + 8u * (uint32_t)s);
           if (++s == kStages) {
             s = 0;
@@ -397,7 +468,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t stg = smem_u32(staging) + (uint32_t)(warp - 2) * 8192u;
     const uint32_t tempty_lead = cluster_addr(smem_u32(tempty), 0);
     int j = 0, boxes = 0;
-    for (int t = pair; t < tiles; t += n_pairs, ++j) {
+    for (int it = pair; it < items; it += n_pairs, ++j) {
+      const int part = EPI == kTcSplit ? it / tiles : 0, t = EPI == kTcSplit ? it % tiles : it;
       const int mt = g.n_fast ? t / n_tiles : t % m_tiles, nt = g.n_fast ? t % n_tiles : t / m_tiles;
       const int m0 = mt * (kPair * kBM) + (int)rank * kBM, n0 = nt * kBN;
       const int b = j & 1;
@@ -405,7 +477,124 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tc_fence_after();
       const uint32_t acc = tmem + (uint32_t)(b * kTmemCols) + lane_off;
       const int row = m0 + 32 * quarter + lane;
-      if (g.tma) {
+      if constexpr (EPI == kTcStats || EPI == kTcGrad || EPI == kTcBf16) {
+        // 32 x 64 bf16 boxes through the same two staging buffers per warp
+        const int row0 = m0 + 32 * quarter;
+        const bool row_on = row < g.M;
+        float ref = 0.0f, sum = 0.0f, f = 0.0f;
+        int label = -1;                    // the label's column within the tile, if it is one
+        if constexpr (EPI != kTcBf16) {
+          if (row_on) label = (int)((uint32_t)g.labels[row] - (uint32_t)(g.col0 + n0));
+        }
+        if constexpr (EPI == kTcGrad) {
+          // lse = +infinity marks an unlabelled row
+          ref = row_on ? g.lse[row] : INFINITY;
+          f = *g.factor;
+        }
+        if constexpr (EPI == kTcStats) {
+          float m = -INFINITY;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kBN; c0 += 32) {
+            uint32_t r[32];
+            __syncwarp();
+            tmem_ld32(acc + (uint32_t)c0, r);
+            tmem_ld_wait();
+            const int valid = g.N - (n0 + c0);
+#pragma unroll
+            for (int jj = 0; jj < 32; ++jj)
+              if (jj < valid) m = fmaxf(m, __uint_as_float(r[jj]));
+            if ((unsigned)(label - c0) < 32u) {
+#pragma unroll
+              for (int jj = 0; jj < 32; ++jj)
+                if (label - c0 == jj) g.label_logit[row] = __uint_as_float(r[jj]);
+            }
+          }
+          ref = m == -INFINITY ? 0.0f : m;
+          if (row_on) g.row_stats[(int64_t)row * g.stats_ld + (g.col0 + n0) / kBN].x = m;
+        }
+#pragma unroll 1
+        for (int c0 = 0; c0 < kBN; c0 += 32) {
+          uint32_t r[32];
+          float x[32];
+          __syncwarp();
+          tmem_ld32(acc + (uint32_t)c0, r);
+          tmem_ld_wait();
+          if constexpr (EPI == kTcBf16) {
+#pragma unroll
+            for (int jj = 0; jj < 32; ++jj) x[jj] = g.alpha * __uint_as_float(r[jj]);
+          } else {
+#pragma unroll
+            for (int jj = 0; jj < 32; ++jj) x[jj] = exp2_approx((__uint_as_float(r[jj]) - ref) * kLog2e);
+            if constexpr (EPI == kTcStats) {
+              // four short chains a chunk, then one addition per chunk
+              const int valid = g.N - (n0 + c0);
+              float part4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+              for (int jj = 0; jj < 32; ++jj)
+                if (jj < valid) part4[jj & 3] += x[jj];
+              sum += (part4[0] + part4[1]) + (part4[2] + part4[3]);
+              if (!g.store) continue;
+            } else {
+              if ((unsigned)(label - c0) < 32u) {
+#pragma unroll
+                for (int jj = 0; jj < 32; ++jj)
+                  if (label - c0 == jj) x[jj] -= 1.0f;
+              }
+#pragma unroll
+              for (int jj = 0; jj < 32; ++jj) x[jj] = ref == INFINITY ? 0.0f : x[jj] * f;
+            }
+          }
+          const int half = (c0 >> 5) & 1;
+          const uint32_t buf = stg + (uint32_t)(boxes & 1) * 4096u;
+          if (half == 0 && boxes >= 2) {
+            if (lane == 0) bulk_wait_read_1();
+            __syncwarp();
+          }
+          stage_bf16(buf, lane, half, x);
+          if (half == 1) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              const int col = n0 + c0 - 32;
+              if (row0 < g.M && col < g.N) tma_store_2d(&map_c, buf, col, row0);
+              bulk_commit();
+            }
+            __syncwarp();
+            ++boxes;
+          }
+        }
+        if constexpr (EPI == kTcStats) {
+          if (row_on) g.row_stats[(int64_t)row * g.stats_ld + (g.col0 + n0) / kBN].y = sum;
+        }
+      } else if constexpr (EPI == kTcSplit) {
+        const int row0 = m0 + 32 * quarter;
+#pragma unroll 1
+        for (int ci = 0; ci < kBN / 32; ++ci, ++boxes) {
+          uint32_t r[32];
+          tmem_ld32(acc + (uint32_t)(32 * ci), r);
+          tmem_ld_wait();
+          const uint32_t buf = stg + (uint32_t)(boxes & 1) * 4096u;
+          if (boxes >= 2) {
+            if (lane == 0) bulk_wait_read_1();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            sts_f4(buf + (uint32_t)lane * 128u + (uint32_t)((q ^ (lane & 7)) * 16), g.alpha * __uint_as_float(r[4 * q]),
+                   g.alpha * __uint_as_float(r[4 * q + 1]), g.alpha * __uint_as_float(r[4 * q + 2]),
+                   g.alpha * __uint_as_float(r[4 * q + 3]));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < g.M && n0 + 32 * ci < g.N) {
+              if (g.accumulate) tma_reduce_add_3d(&map_c, buf, n0 + 32 * ci, row0, part);
+              else tma_store_3d(&map_c, buf, n0 + 32 * ci, row0, part);
+            }
+            bulk_commit();
+          }
+          __syncwarp();
+        }
+      } else if (g.tma) {
         // 32 x 32 boxes through two 4 KB staging buffers per warp, 128-byte
         // swizzled to match the store's tensor map (conflict-free 16-byte
         // writes); one thread stores or reduce-adds each box, and a buffer
@@ -509,6 +698,32 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
+// The same for partial products [splits][M][N] (3D, boxes 32 x 32 x 1) ...
+sf_status make_map_split(CUtensorMap* map, float* C, int64_t M, int64_t N, int64_t ldc, int64_t splits) {
+  cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)splits};
+  cuuint64_t strides[2] = {(cuuint64_t)(ldc * 4), (cuuint64_t)(M * ldc * 4)};
+  cuuint32_t box[3] = {32, 32, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, C, dims, strides, box, estr,
+                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SF_ERR_CUDA, "cuTensorMapEncodeTiled (partial C) failed (%d)", (int)r);
+  return SF_OK;
+}
+
+// ... and for a bf16 C (boxes 32 rows x 64 columns).
+sf_status make_map_c16(CUtensorMap* map, void* C, int64_t M, int64_t N, int64_t ldc) {
+  cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
+  cuuint64_t strides[1] = {(cuuint64_t)(ldc * 2)};
+  cuuint32_t box[2] = {64, 32};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, C, dims, strides, box, estr,
+                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SF_ERR_CUDA, "cuTensorMapEncodeTiled (bf16 C) failed (%d)", (int)r);
+  return SF_OK;
+}
+
 sf_status make_map_c(CUtensorMap* map, float* C, int64_t M, int64_t N, int64_t ldc) {
   cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
   cuuint64_t strides[1] = {(cuuint64_t)(ldc * 4)};
@@ -565,7 +780,8 @@ sf_status resident_pairs(cudaLaunchConfig_t* cfg, int* out) {
   if (it == cache.end()) {
     int n = 0;
     cfg->gridDim = dim3((unsigned)(kPair * std::max(1, sm_count() / kPair)));
-    SF_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_tc_gemm, cfg), "cudaOccupancyMaxActiveClusters (k_tc_gemm)");
+    SF_TRY(allow_dynamic_smem(reinterpret_cast<const void*>(&k_tc_gemm<kTcF32>), kGemmSmem));
+    SF_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_tc_gemm<kTcF32>, cfg), "cudaOccupancyMaxActiveClusters (k_tc_gemm)");
     if (n < 1) return fail(SF_ERR_UNSUPPORTED, "no cluster of two GEMM CTAs fits on this device");
     it = cache.emplace(dev, n).first;
   }
@@ -579,53 +795,106 @@ sf_status resident_pairs(cudaLaunchConfig_t* cfg, int* out) {
 sf_status tc_gemm(const void* A, bool a_mn, const void* B, bool b_mn, float* C, int64_t M, int64_t N, int64_t K,
                   int64_t lda, int64_t ldb, int64_t ldc, float alpha, bool accumulate, cudaStream_t s,
                   float2* row_stats) {
-  if (!A || !B || !C) return fail(SF_ERR_INVALID, "A, B or C is NULL");
-  if (M < 1 || N < 1 || K < 1) return fail(SF_ERR_INVALID, "M, N, K must be >= 1");
-  if (M > INT32_MAX - 2 * kPair * kBM || N > INT32_MAX - kBN || K > INT32_MAX - kBK)
+  TcJob j;
+  j.A = A;
+  j.a_mn = a_mn;
+  j.B = B;
+  j.b_mn = b_mn;
+  j.C = C;
+  j.M = M;
+  j.N = N;
+  j.K = K;
+  j.lda = lda;
+  j.ldb = ldb;
+  j.ldc = ldc;
+  j.alpha = alpha;
+  j.accumulate = accumulate;
+  j.row_stats = row_stats;
+  return tc_gemm(j, s);
+}
+
+sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
+  const bool writes = j.epi != kTcStats || j.store;      // whether C is written
+  if (!j.A || !j.B || (writes && !j.C)) return fail(SF_ERR_INVALID, "A, B or C is NULL");
+  if (j.M < 1 || j.N < 1 || j.K < 1) return fail(SF_ERR_INVALID, "M, N, K must be >= 1");
+  if (j.M > INT32_MAX - 2 * kPair * kBM || j.N > INT32_MAX - kBN || j.K > INT32_MAX - kBK)
     return fail(SF_ERR_UNSUPPORTED, "M, N, K must be below 2^31");
-  if (lda < (a_mn ? M : K) || ldb < (b_mn ? N : K) || ldc < N)
+  if (j.lda < (j.a_mn ? j.M : j.K) || j.ldb < (j.b_mn ? j.N : j.K) || (writes && j.ldc < j.N))
     return fail(SF_ERR_INVALID, "leading dimensions must be >= the stored rows' length (lda: K or M, ldb: K or N; "
                                 "ldc: N)");
-  if ((lda * 2) % 16 || (ldb * 2) % 16 || (reinterpret_cast<uintptr_t>(A) % 16) ||
-      (reinterpret_cast<uintptr_t>(B) % 16))
+  if ((j.lda * 2) % 16 || (j.ldb * 2) % 16 || (reinterpret_cast<uintptr_t>(j.A) % 16) ||
+      (reinterpret_cast<uintptr_t>(j.B) % 16))
     return fail(SF_ERR_UNSUPPORTED, "A and B need 16-byte aligned bases and rows (lda, ldb multiples of 8)");
   if (!tensor_map_encoder()) return fail(SF_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled is not available");
   // the tensor maps below may only address this device's own memory
-  if (!on_current_device(A) || !on_current_device(B) || !on_current_device(C))
+  if (!on_current_device(j.A) || !on_current_device(j.B) || (writes && !on_current_device(j.C)))
     return fail(SF_ERR_INVALID, "A, B and C must be device memory of the current device");
   CUtensorMap ma, mb;
   int a_form = 0, b_form = 0;      // 0 K-major, 1 MN-major in 2D boxes, 2 MN-major in 3D boxes
-  if (a_mn) {
-    a_form = make_map_mn3d(&ma, A, M, K, lda) ? 2 : 1;
-    if (a_form == 1) SF_TRY(make_map(&ma, A, M, K, lda, kBK));
+  if (j.a_mn) {
+    a_form = make_map_mn3d(&ma, j.A, j.M, j.K, j.lda) ? 2 : 1;
+    if (a_form == 1) SF_TRY(make_map(&ma, j.A, j.M, j.K, j.lda, kBK));
   } else {
-    SF_TRY(make_map(&ma, A, K, M, lda, kBM));
+    SF_TRY(make_map(&ma, j.A, j.K, j.M, j.lda, kBM));
   }
-  if (b_mn) {
-    b_form = make_map_mn3d(&mb, B, N, K, ldb) ? 2 : 1;
-    if (b_form == 1) SF_TRY(make_map(&mb, B, N, K, ldb, kBK));
+  if (j.b_mn) {
+    b_form = make_map_mn3d(&mb, j.B, j.N, j.K, j.ldb) ? 2 : 1;
+    if (b_form == 1) SF_TRY(make_map(&mb, j.B, j.N, j.K, j.ldb, kBK));
   } else {
-    SF_TRY(make_map(&mb, B, K, N, ldb, kBRows));
+    SF_TRY(make_map(&mb, j.B, j.K, j.N, j.ldb, kBRows));
   }
-  TcGemmArgs g;
-  g.C = C;
-  g.ldc = ldc;
-  g.M = (int32_t)M;
-  g.N = (int32_t)N;
-  g.K = (int32_t)K;
-  g.alpha = alpha;
-  g.accumulate = accumulate ? 1 : 0;
-  g.vec = (ldc % 4 == 0) && (reinterpret_cast<uintptr_t>(C) % 16 == 0) ? 1 : 0;
-  g.tma = g.vec;
-  g.n_fast = M > N ? 1 : 0;
+  TcGemmArgs g{};
+  g.C = static_cast<float*>(j.C);
+  g.ldc = j.ldc;
+  g.M = (int32_t)j.M;
+  g.N = (int32_t)j.N;
+  g.K = (int32_t)j.K;
+  g.alpha = j.alpha;
+  g.accumulate = j.accumulate ? 1 : 0;
+  g.n_fast = j.M > j.N ? 1 : 0;
   g.a_mn = a_form;
   g.b_mn = b_form;
-  g.row_stats = row_stats;
-  CUtensorMap mc = ma;       // unused unless g.tma
-  if (g.tma) SF_TRY(make_map_c(&mc, C, M, N, ldc));
-  SF_TRY(allow_dynamic_smem(reinterpret_cast<const void*>(&k_tc_gemm), kGemmSmem));
-  const int64_t tiles = ((M + kPair * kBM - 1) / (kPair * kBM)) * ((N + kBN - 1) / kBN);
-  if (tiles > INT32_MAX) return fail(SF_ERR_UNSUPPORTED, "too many tiles");
+  g.row_stats = j.row_stats;
+  g.splits = j.epi == kTcSplit ? j.splits : 1;
+  g.stats_ld = j.stats_ld;
+  g.col0 = j.col0;
+  g.store = j.store ? 1 : 0;
+  g.labels = j.labels;
+  g.label_logit = j.label_logit;
+  g.lse = j.lse;
+  g.factor = j.factor;
+  g.zero = j.zero;
+  const bool c_aligned = reinterpret_cast<uintptr_t>(j.C) % 16 == 0;
+  CUtensorMap mc = ma;       // unused unless C is written by tensor stores
+  const void* kernel = nullptr;
+  switch (j.epi) {
+    case kTcF32:
+      g.vec = j.ldc % 4 == 0 && c_aligned ? 1 : 0;
+      g.tma = g.vec;
+      if (g.tma) SF_TRY(make_map_c(&mc, g.C, j.M, j.N, j.ldc));
+      kernel = reinterpret_cast<const void*>(&k_tc_gemm<kTcF32>);
+      break;
+    case kTcSplit:
+      if (j.splits < 1 || j.splits > (j.K + kBK - 1) / kBK) return fail(SF_ERR_INVALID, "splits must lie in 1..slabs of K");
+      if (j.ldc % 4 || !c_aligned) return fail(SF_ERR_UNSUPPORTED, "partial products need 16-byte aligned rows");
+      SF_TRY(make_map_split(&mc, g.C, j.M, j.N, j.ldc, j.splits));
+      kernel = reinterpret_cast<const void*>(&k_tc_gemm<kTcSplit>);
+      break;
+    case kTcBf16:
+    case kTcGrad:
+    case kTcStats:
+      if (writes) {
+        if (j.ldc % 8 || !c_aligned) return fail(SF_ERR_UNSUPPORTED, "a bf16 C needs 16-byte aligned rows");
+        SF_TRY(make_map_c16(&mc, j.C, j.M, j.N, j.ldc));
+      }
+      kernel = j.epi == kTcBf16   ? reinterpret_cast<const void*>(&k_tc_gemm<kTcBf16>)
+               : j.epi == kTcGrad ? reinterpret_cast<const void*>(&k_tc_gemm<kTcGrad>)
+                                  : reinterpret_cast<const void*>(&k_tc_gemm<kTcStats>);
+      break;
+  }
+  SF_TRY(allow_dynamic_smem(kernel, kGemmSmem));
+  const int64_t items = ((j.M + kPair * kBM - 1) / (kPair * kBM)) * ((j.N + kBN - 1) / kBN) * g.splits;
+  if (items > INT32_MAX) return fail(SF_ERR_UNSUPPORTED, "too many tiles");
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -639,8 +908,9 @@ sf_status tc_gemm(const void* A, bool a_mn, const void* B, bool b_mn, float* C, 
   cfg.numAttrs = 1;
   int pairs = 0;
   SF_TRY(resident_pairs(&cfg, &pairs));
-  cfg.gridDim = dim3((unsigned)(kPair * std::min<int64_t>(tiles, pairs)));
-  SF_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_tc_gemm, ma, mb, mc, g), "launch k_tc_gemm");
+  cfg.gridDim = dim3((unsigned)(kPair * std::min<int64_t>(items, pairs)));
+  void* args[] = {&ma, &mb, &mc, &g};
+  SF_CUDA_TRY(cudaLaunchKernelExC(&cfg, kernel, args), "launch k_tc_gemm");
   return SF_OK;
 }
 

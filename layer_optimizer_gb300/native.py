@@ -32,6 +32,7 @@ EXPORTS = [
     "lce_workspace_bytes", "lce_forward_backward",
     "sf_test_device_wait_runs_out",
     "sf_dropout", "sf_add_rmsnorm_forward", "sf_add_rmsnorm_workspace_bytes", "sf_add_rmsnorm_backward",
+    "lce_vocab_workspace_bytes", "lce_vocab_forward_backward",
 ]
 
 
@@ -133,6 +134,9 @@ _SIGS = {
     "lce_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64]),
     "sf_test_device_wait_runs_out": (_ST, [_I64, _P]),
     "lce_forward_backward": (_ST, [_P, _P, _P, _I64, _I64, _I64, _I64, _I32, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "lce_vocab_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64]),
+    "lce_vocab_forward_backward": (_ST, [_P, _P, _P, _I64, _I32, ctypes.c_double, _P, _P, _P, _P, _P, ctypes.c_size_t,
+                                         _P]),
     "sf_dropout": (_ST, [_P, _P, _P, ctypes.c_double, _P, _P]),
     "sf_add_rmsnorm_forward": (_ST, [_P, _P, _P, _INT, ctypes.c_double, ctypes.c_double, _P, _P, _P, _P, _P, _I32, _P,
                                      _P]),
@@ -437,6 +441,20 @@ def sf_add_rmsnorm_backward(dh, sum, gain, rstd, dsum=None, dresidual=None, dx=N
         _ref(dh), _ref(sum), _vector(gain, dh.cols, "gain"), _dtype(gain, "gain"),
         _vector(rstd, dh.rows, "rstd", _F32), _ref(dsum), float(p), _ref(rng), _ref(dresidual), _ref(dx),
         _vector(dgain, dh.cols, "dgain"), SF_FP32 if dgain is None else _dtype(dgain, "dgain"), _addr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def lce_vocab_workspace_bytes(n_tokens, d, vocab, piece=0):
+    return load().lce_vocab_workspace_bytes(n_tokens, d, vocab, piece)
+
+
+def lce_vocab_forward_backward(H, W, labels, loss=None, token_loss=None, dH=None, dW=None, ws=None, piece=0,
+                               ignore_index=-100, grad_scale=1.0, stream=None):
+    """Linear cross-entropy by pieces of the vocabulary (ws: a uint8 workspace tensor); tensors or sf_matrix."""
+    H, W, dH, dW = matrix(H, "H"), matrix(W, "W"), matrix(dH, "dH"), matrix(dW, "dW")
+    _check(load().lce_vocab_forward_backward(
+        _ref(H), _ref(W), _vector(labels, H.rows, "labels", ("torch.int32",)), piece, ignore_index, float(grad_scale),
+        _vector(loss, 1, "loss", _F32), _vector(token_loss, H.rows, "token_loss", _F32), _ref(dH), _ref(dW), _addr(ws),
         0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
 
 
