@@ -124,6 +124,7 @@ int read_and_clear_device_error();
 int read_and_clear_device_error_adamw();
 int read_and_clear_device_error_gemm();
 int read_and_clear_device_error_lce();
+int read_and_clear_device_error_norm();
 
 // C = alpha A B^T (+ C) on the tensor cores (tc_gemm.cu): A bf16 [M][lda]
 // row-major (K-major) or, with a_mn, [K][lda] (MN-major: A^T stored);

@@ -25,61 +25,65 @@ struct DropoutArgs {
   int64_t units;        // rows * units_per_row
   int64_t per_row;      // units per row
   int64_t cols;
-  int64_t step_rows, step_units;   // the grid's stride as rows and units of a row
+  int32_t per_thread;   // units a thread takes, 1..kUnits
   DropConsts d;
 };
 
-template <typename TX, typename TY, bool RES, bool VEC>
+// A block takes per_thread * 256 consecutive units.  FLAT: dense rows of whole
+// units, so a unit's place follows from its index; otherwise one division a
+// unit finds its row.
+template <typename TX, typename TY, bool RES, bool VEC, bool FLAT>
 __global__ void __launch_bounds__(kThreads) k_dropout(const DropoutArgs a) {
   const DropKey key = drop_key(a.d);
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
-  int64_t b = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  int64_t row = b / a.per_row, u = b - row * a.per_row;
-  while (b < a.units) {
-    Unit<TX> x[kUnits];
-    Unit<TY> r[kUnits];
-    int64_t rows[kUnits], cols[kUnits], at[kUnits];
-    int n[kUnits];
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      at[k] = b;
-      rows[k] = row;
-      cols[k] = 8 * u;
-      n[k] = b < a.units ? (int)min((int64_t)8, a.cols - 8 * u) : 0;
-      if (n[k]) {
-        load_unit<VEC>(row_ptr<TX>(a.x, a.ldx, row) + 8 * u, n[k], x[k]);
-        if (RES) load_unit<VEC>(row_ptr<TY>(a.r, a.ldr, row) + 8 * u, n[k], r[k]);
-      }
-      // the next unit of this thread, without a division
-      b += stride;
-      row += a.step_rows;
-      u += a.step_units;
-      if (u >= a.per_row) {
-        u -= a.per_row;
-        ++row;
-      }
+  const int64_t b0 = (int64_t)blockIdx.x * (a.per_thread * kThreads) + threadIdx.x;
+  Unit<TX> x[kUnits];
+  Unit<TY> r[kUnits];
+  // the unit's row and first column; columns of it (0 past the end)
+  auto place = [&](int k, int64_t& row, int64_t& c) {
+    const int64_t b = b0 + k * kThreads;
+    if (k >= a.per_thread || b >= a.units) return 0;
+    if (FLAT) {
+      row = 0;
+      c = 8 * b;
+      return 8;
     }
+    row = a.units <= INT32_MAX ? (int64_t)((uint32_t)b / (uint32_t)a.per_row) : b / a.per_row;
+    c = 8 * (b - row * a.per_row);
+    return (int)min((int64_t)8, a.cols - c);
+  };
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      if (!n[k]) continue;
-      float v[8];
-      unpack(x[k], v);
-      if (a.d.threshold) drop_unit(v, (uint64_t)at[k], key, a.d.threshold, a.d.factor);
-      if (RES) {
-        float w[8];
-        unpack(r[k], w);
+  for (int k = 0; k < kUnits; ++k) {
+    int64_t row, c;
+    const int n = place(k, row, c);
+    if (!n) continue;
+    load_unit<VEC>(row_ptr<TX>(a.x, a.ldx, row) + c, n, x[k]);
+    if (RES) load_unit<VEC>(row_ptr<TY>(a.r, a.ldr, row) + c, n, r[k]);
+  }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += w[i];
-      }
-      store_unit<VEC>(row_ptr<TY>(a.y, a.ldy, rows[k]) + cols[k], n[k], v);
+  for (int k = 0; k < kUnits; ++k) {
+    int64_t row, c;
+    const int n = place(k, row, c);
+    if (!n) continue;
+    F8 v = unpack(x[k]);
+    if (a.d.threshold) drop_unit(v, (uint64_t)(b0 + k * kThreads), key, a.d.threshold, a.d.factor);
+    if (RES) {
+      const F8 w = unpack(r[k]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v.p[i] = add2(v.p[i], w.p[i]);
     }
+    store_unit<VEC>(row_ptr<TY>(a.y, a.ldy, row) + c, n, v);
   }
 }
 
+template <typename TX, typename TY, bool RES>
+const void* pick(bool vec, bool flat) {
+  return flat  ? (const void*)&k_dropout<TX, TY, RES, true, true>
+         : vec ? (const void*)&k_dropout<TX, TY, RES, true, false>
+               : (const void*)&k_dropout<TX, TY, RES, false, false>;
+}
 template <typename TX, typename TY>
-const void* pick(bool res, bool vec) {
-  if (res) return vec ? (const void*)&k_dropout<TX, TY, true, true> : (const void*)&k_dropout<TX, TY, true, false>;
-  return vec ? (const void*)&k_dropout<TX, TY, false, true> : (const void*)&k_dropout<TX, TY, false, false>;
+const void* pick(bool res, bool vec, bool flat) {
+  return res ? pick<TX, TY, true>(vec, flat) : pick<TX, TY, false>(vec, flat);
 }
 
 }  // namespace
@@ -127,17 +131,16 @@ sf_status sf_dropout(const sf_matrix* x, const sf_matrix* residual, const sf_mat
   a.per_row = ceil_div<int64_t>(x->cols, 8);
   a.units = a.per_row * x->rows;
   const bool vec = units_aligned(x) && units_aligned(residual) && units_aligned(y);
-  const int64_t want = ceil_div<int64_t>(a.units, (int64_t)kThreads * kUnits);
-  // one unit a thread while that leaves SMs idle, then up to eight resident blocks an SM
-  const int64_t most = (int64_t)sm_count() * 8;
-  const int64_t grid = want > most ? most : std::min(ceil_div<int64_t>(a.units, kThreads), most);
-  const int64_t stride = grid * kThreads;
-  a.step_rows = stride / a.per_row;
-  a.step_units = stride % a.per_row;
+  auto dense = [&](const sf_matrix* m) { return !m || m->ld == m->cols || m->rows == 1; };
+  const bool flat = vec && x->cols % 8 == 0 && dense(x) && dense(residual) && dense(y);
+  // one unit a thread while that leaves SMs idle, else four loads in flight
+  a.per_thread = (int32_t)std::clamp<int64_t>(a.units / ((int64_t)kThreads * sm_count() * 4), 1, kUnits);
+  const int64_t grid = ceil_div<int64_t>(a.units, (int64_t)kThreads * a.per_thread);
+  if (grid > INT32_MAX) return fail(SF_ERR_UNSUPPORTED, "sizes too large");
+  using B = __nv_bfloat16;
   const void* k = x->dtype == SF_BF16
-                      ? (y->dtype == SF_BF16 ? pick<__nv_bfloat16, __nv_bfloat16>(residual, vec)
-                                             : pick<__nv_bfloat16, float>(residual, vec))
-                      : (y->dtype == SF_BF16 ? pick<float, __nv_bfloat16>(residual, vec) : pick<float, float>(residual, vec));
+                      ? (y->dtype == SF_BF16 ? pick<B, B>(residual, vec, flat) : pick<B, float>(residual, vec, flat))
+                      : (y->dtype == SF_BF16 ? pick<float, B>(residual, vec, flat) : pick<float, float>(residual, vec, flat));
   void* args[] = {&a};
   SF_CUDA_TRY(cudaLaunchKernel(k, dim3((unsigned)grid), dim3(kThreads), args, 0, as_stream(stream)), "launch k_dropout");
   return SF_OK;

@@ -16,6 +16,7 @@
 
 #include <algorithm>
 
+#include "ptx.cuh"
 #include "rows.cuh"
 
 namespace sf {
@@ -37,35 +38,43 @@ struct FwdArgs {
   int64_t ldx, ldr, lds, ldh, ldq;
   int64_t rows;
   int32_t cols, per_row;
-  int32_t tpr_log2;
+  int32_t tpr;           // threads a row: a power of two up to 64, or the whole block (a multiple of 32)
+  int32_t rpb;           // rows a block
   int32_t gain_fp32;
-  int32_t group_lanes;   // lanes (units) of a scale group; 0: one scale a row
+  int32_t group_log2;    // columns of a scale group; 0: one scale a row
   int32_t n_groups;
   float eps, inv_cols;
   DropConsts d;
 };
 
-// Eight gains from column c on (served by L1 after a row or two).
-__device__ __forceinline__ void load_gain(const void* g, int fp32, int64_t c, int n, float (&v)[8]) {
+// Eight gains from column c on (served by L1 after a row or two).  VEC: gains
+// are aligned to their units.
+template <bool VEC>
+__device__ __forceinline__ F8 load_gain(const void* g, int fp32, int c, int n) {
   if (fp32) {
     const float* p = static_cast<const float*>(g) + c;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? __ldg(p + i) : 0.0f;
-  } else {
-    const uint16_t* p = static_cast<const uint16_t*>(g) + c;
-    if (n == 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-      }
+    Unit<float> u;
+    if (VEC && n == 8) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(p)), y = __ldg(reinterpret_cast<const float4*>(p) + 1);
+      u.f[0] = x.x, u.f[1] = x.y, u.f[2] = x.z, u.f[3] = x.w;
+      u.f[4] = y.x, u.f[5] = y.y, u.f[6] = y.z, u.f[7] = y.w;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < n ? __uint_as_float((uint32_t)__ldg(p + i) << 16) : 0.0f;
+      for (int i = 0; i < 8; ++i) u.f[i] = i < n ? __ldg(p + i) : 0.0f;
     }
+    return unpack(u);
   }
+  const uint16_t* p = static_cast<const uint16_t*>(g) + c;
+  Unit<__nv_bfloat16> u;
+  if (VEC && n == 8) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+    u.w[0] = w.x, u.w[1] = w.y, u.w[2] = w.z, u.w[3] = w.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      u.w[i] = (2 * i < n ? (uint32_t)__ldg(p + 2 * i) : 0u) | (2 * i + 1 < n ? (uint32_t)__ldg(p + 2 * i + 1) << 16 : 0u);
+  }
+  return unpack(u);
 }
 
 // Maximum that keeps a NaN: a NaN in a group must reach its scale.
@@ -84,7 +93,7 @@ __device__ __forceinline__ float row_reduce(float v, int tpr, float* red) {
     v = MAX ? max_nan(v, w) : v + w;
   }
   if (tpr <= 32) return v;
-  const int warp = threadIdx.x >> 5, n = tpr >> 5, first = warp & ~(n - 1);
+  const int warp = threadIdx.x >> 5, n = tpr >> 5, first = warp - warp % n;
   if ((threadIdx.x & 31) == 0) red[warp] = v;
   __syncthreads();
   float t = red[first];
@@ -92,92 +101,106 @@ __device__ __forceinline__ float row_reduce(float v, int tpr, float* red) {
   return t;
 }
 
-__device__ __forceinline__ float group_scale(float amax) { return max_nan(__fdiv_rn(amax, 448.0f), 1.17549435e-38f); }
+// A group's scale and its reciprocal (of the exponential unit's neighbour:
+// within an ulp, far below e4m3's 2^-4 steps; 2^-126 and infinity included).
+__device__ __forceinline__ float group_scale(float amax, float* inv) {
+  const float s = max_nan(amax * (1.0f / 448.0f), 1.17549435e-38f);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(*inv) : "f"(s));
+  return s;
+}
 
 template <typename TA, typename TS, bool VEC>
-__global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_fwd(const FwdArgs a) {
+__global__ void __maxnreg__(sizeof(TA) + sizeof(TS) == 4 ? 64 : 80) k_add_rmsnorm_fwd(const FwdArgs a) {
   __shared__ float red[2][kMaxThreads / 32];
-  const int tpr = 1 << a.tpr_log2, t = threadIdx.x & (tpr - 1);
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> a.tpr_log2) + (threadIdx.x >> a.tpr_log2);
+  const int tpr = a.tpr, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
+  const int64_t row = (int64_t)blockIdx.x * a.rpb + lane_row;
   const bool on = row < a.rows;
   int n[kK];
-  float s[kK][8];
+  F8 s[kK];
   {
     Unit<TA> x[kK];
     Unit<TS> r[kK];
+    const TA* xp = row_ptr<TA>(a.x, a.ldx, row);
+    const TS* rp = row_ptr<TS>(a.r, a.ldr, row);
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
       const int c = 8 * (t + k * tpr);
       n[k] = on ? max(0, min(8, a.cols - c)) : 0;
       if (n[k]) {
-        load_unit<VEC>(row_ptr<TA>(a.x, a.ldx, row) + c, n[k], x[k]);
-        if (a.r) load_unit<VEC>(row_ptr<TS>(a.r, a.ldr, row) + c, n[k], r[k]);
+        load_unit<VEC>(xp + c, n[k], x[k]);
+        if (a.r) load_unit<VEC>(rp + c, n[k], r[k]);
       }
     }
     const DropKey key = a.d.threshold ? drop_key(a.d) : DropKey{};
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[k][i] = 0.0f;
+      for (int i = 0; i < 4; ++i) s[k].p[i] = 0;
       if (!n[k]) continue;
-      unpack(x[k], s[k]);
+      s[k] = unpack(x[k]);
       if (a.d.threshold)
         drop_unit(s[k], (uint64_t)(row * a.per_row + t + k * tpr), key, a.d.threshold, a.d.factor);
       if (a.r) {
-        float w[8];
-        unpack(r[k], w);
+        const F8 w = unpack(r[k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[k][i] += w[i];
+        for (int i = 0; i < 4; ++i) s[k].p[i] = add2(s[k].p[i], w.p[i]);
       }
     }
   }
-  float sum = 0.0f;
+  uint64_t sum2 = 0;
+  TS* sp = row_ptr<TS>(a.s, a.lds, row);
 #pragma unroll
   for (int k = 0; k < kK; ++k) {
-    const int c = 8 * (t + k * tpr);
-    if (a.s && n[k]) store_unit<VEC>(row_ptr<TS>(a.s, a.lds, row) + c, n[k], s[k]);
+    if (a.s && n[k]) store_unit<VEC>(sp + 8 * (t + k * tpr), n[k], s[k]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(s[k][i], s[k][i], sum);
+    for (int i = 0; i < 4; ++i) sum2 = fma2(s[k].p[i], s[k].p[i], sum2);
   }
-  sum = row_reduce<false>(sum, tpr, red[0]);
+  const float sum = row_reduce<false>(f2(sum2).x + f2(sum2).y, tpr, red[0]);
   const float rstd = rsqrtf(fmaf(sum, a.inv_cols, a.eps));
   if (a.rstd && on && t == 0) a.rstd[row] = rstd;
+  const uint64_t rstd2 = f2(rstd, rstd);
   float amax = 0.0f;
+  TA* hp = row_ptr<TA>(a.h, a.ldh, row);
 #pragma unroll
   for (int k = 0; k < kK; ++k) {
     const int c = 8 * (t + k * tpr);
     if (n[k]) {
-      float g[8];
-      load_gain(a.gain, a.gain_fp32, c, n[k], g);
+      const F8 g = load_gain<VEC>(a.gain, a.gain_fp32, c, n[k]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[k][i] = s[k][i] * rstd * g[i];
-      if (a.h) store_unit<VEC>(row_ptr<TA>(a.h, a.ldh, row) + c, n[k], s[k]);
+      for (int i = 0; i < 4; ++i) s[k].p[i] = mul2(mul2(s[k].p[i], rstd2), g.p[i]);
+      if (a.h) store_unit<VEC>(hp + c, n[k], s[k]);
     }
     if (a.q) {
       float m = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(i < n[k] ? s[k][i] : 0.0f));
+      for (int i = 0; i < 4; ++i) {
+        // past a ragged row's end the sum is 0 and so is the gain
+        const float2 v = f2(s[k].p[i]);
+        m = max_nan(m, max_nan(fabsf(v.x), fabsf(v.y)));
+      }
+      if (n[k] == 0) m = 0.0f;
       amax = max_nan(amax, m);
-      if (a.group_lanes) {
-        for (int o = a.group_lanes >> 1; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float sc = group_scale(m), inv = __fdiv_rn(1.0f, sc);
-        if (n[k]) {
-          if ((t & (a.group_lanes - 1)) == 0) a.scale[row * a.n_groups + (t + k * tpr) / a.group_lanes] = sc;
+      if (a.group_log2) {
+        const int lanes = 1 << (a.group_log2 - 3);
+        for (int o = lanes >> 1; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float inv;
+        const float sc = group_scale(m, &inv);
+        if (n[k] && (t & (lanes - 1)) == 0) a.scale[row * a.n_groups + (c >> a.group_log2)] = sc;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[k][i] *= inv;
-        }
+        for (int i = 0; i < 4; ++i) s[k].p[i] = mul2(s[k].p[i], f2(inv, inv));
       }
     }
   }
   if (!a.q) return;
-  if (!a.group_lanes) {
+  if (!a.group_log2) {
     amax = row_reduce<true>(amax, tpr, red[1]);
-    const float sc = group_scale(amax), inv = __fdiv_rn(1.0f, sc);
+    float inv;
+    const float sc = group_scale(amax, &inv);
     if (on && t == 0) a.scale[row] = sc;
 #pragma unroll
     for (int k = 0; k < kK; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[k][i] *= inv;
+      for (int i = 0; i < 4; ++i) s[k].p[i] = mul2(s[k].p[i], f2(inv, inv));
   }
 #pragma unroll
   for (int k = 0; k < kK; ++k) {
@@ -186,8 +209,8 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_fwd(const FwdArgs a
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       // saturating, so |h| / scale just above 448 by rounding stays 448
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(s[k][4 * i], s[k][4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(s[k][4 * i + 2], s[k][4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(f2(s[k].p[2 * i]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(f2(s[k].p[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
       w[i] = lo | hi << 16;
     }
     uint8_t* p = row_ptr<uint8_t>(a.q, a.ldq, row) + 8 * (t + k * tpr);
@@ -219,24 +242,38 @@ struct BwdArgs {
   int64_t lddh, lds, lddsum, lddr, lddx;
   int64_t rows;
   int32_t cols, per_row;
-  int32_t tpr_log2;
+  int32_t tpr, rpb;      // as in FwdArgs
   int32_t gain_fp32;
   float inv_cols;
   DropConsts d;
 };
 
+// One unit's share of a row's sums: with w = dh s (unscaled), dg gains w rstd
+// and the row's dot product sum dh g s gains w g.
+__device__ __forceinline__ void bwd_sums(const F8& dh, const F8& s, const F8& g, uint64_t rstd2, F8& acc, uint64_t& dot2) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t w = mul2(dh.p[i], s.p[i]);
+    acc.p[i] = fma2(w, rstd2, acc.p[i]);
+    dot2 = fma2(w, g.p[i], dot2);
+  }
+}
+
+// ds = dsum + rstd dh g + c s, c = -rstd^3 / cols * (the row's dot product).
+__device__ __forceinline__ F8 bwd_unit(const F8& dh, const F8& s, const F8& g, const F8& dsum, uint64_t rstd2, uint64_t c2) {
+  F8 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v.p[i] = fma2(mul2(dh.p[i], g.p[i]), rstd2, fma2(s.p[i], c2, dsum.p[i]));
+  return v;
+}
+
 template <typename TA, typename TS, bool VEC>
 __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a) {
   __shared__ float red[2][kMaxThreads / 32];
   extern __shared__ float comb[];      // [rows of a block][cols], only with several rows a block
-  const int tpr = 1 << a.tpr_log2, t = threadIdx.x & (tpr - 1), rpb = blockDim.x >> a.tpr_log2;
-  const int lane_row = threadIdx.x >> a.tpr_log2;
+  const int tpr = a.tpr, rpb = a.rpb, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
   const DropKey key = a.d.threshold ? drop_key(a.d) : DropKey{};
-  float acc[kK][8];
-#pragma unroll
-  for (int k = 0; k < kK; ++k)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[k][i] = 0.0f;
+  F8 acc[kK] = {};
   int parity = 0;
   for (int64_t base = (int64_t)blockIdx.x * rpb; base < a.rows; base += (int64_t)gridDim.x * rpb, parity ^= 1) {
     const int64_t row = base + lane_row;
@@ -255,66 +292,186 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
       }
     }
     const float rstd = on ? a.rstd[row] : 0.0f;
-    float dot = 0.0f;
+    const uint64_t rstd2 = f2(rstd, rstd);
+    uint64_t dot2 = 0;
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      if (!n[k]) continue;
-      float u[8], v[8], g[8];
-      unpack(dh[k], u);
-      unpack(s[k], v);
-      load_gain(a.gain, a.gain_fp32, 8 * (t + k * tpr), n[k], g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float w = u[i] * (v[i] * rstd);
-        acc[k][i] += w;
-        dot = fmaf(w, g[i], dot);
-      }
-    }
+    for (int k = 0; k < kK; ++k)
+      if (n[k])
+        bwd_sums(unpack(dh[k]), unpack(s[k]), load_gain<VEC>(a.gain, a.gain_fp32, 8 * (t + k * tpr), n[k]), rstd2, acc[k], dot2);
     // two alternating buffers: the next row's write cannot meet this row's reads
-    dot = row_reduce<false>(dot, tpr, red[parity]);
-    const float mean = dot * a.inv_cols;
+    const float dot = row_reduce<false>(f2(dot2).x + f2(dot2).y, tpr, red[parity]);
+    const float c = -rstd * (rstd * (rstd * dot * a.inv_cols));
+    const uint64_t c2 = f2(c, c);
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
       if (!n[k]) continue;
-      const int c = 8 * (t + k * tpr);
-      float u[8], v[8], g[8];
-      unpack(dh[k], u);
-      unpack(s[k], v);
-      load_gain(a.gain, a.gain_fp32, c, n[k], g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = rstd * (u[i] * g[i] - (v[i] * rstd) * mean);
-      if (a.dsum) {
-        unpack(ds[k], u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += u[i];
-      }
-      if (a.dr) store_unit<VEC>(row_ptr<TS>(a.dr, a.lddr, row) + c, n[k], v);
+      const int col = 8 * (t + k * tpr);
+      F8 v = bwd_unit(unpack(dh[k]), unpack(s[k]), load_gain<VEC>(a.gain, a.gain_fp32, col, n[k]), a.dsum ? unpack(ds[k]) : F8{},
+                      rstd2, c2);
+      if (a.dr) store_unit<VEC>(row_ptr<TS>(a.dr, a.lddr, row) + col, n[k], v);
       if (a.dx) {
         if (a.d.threshold)
           drop_unit(v, (uint64_t)(row * a.per_row + t + k * tpr), key, a.d.threshold, a.d.factor);
-        store_unit<VEC>(row_ptr<TA>(a.dx, a.lddx, row) + c, n[k], v);
+        store_unit<VEC>(row_ptr<TA>(a.dx, a.lddx, row) + col, n[k], v);
       }
     }
   }
   if (!a.part) return;
   float* part = a.part + (int64_t)blockIdx.x * a.cols;
-  if (rpb == 1) {
-#pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int c = 8 * (t + k * tpr);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < a.cols) part[c + i] = acc[k][i];
-    }
-    return;
-  }
 #pragma unroll
   for (int k = 0; k < kK; ++k) {
     const int c = 8 * (t + k * tpr);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < a.cols) comb[lane_row * a.cols + c + i] = acc[k][i];
+    if (c < a.cols) store_unit<false>((rpb == 1 ? part : comb + lane_row * a.cols) + c, min(8, a.cols - c), acc[k]);
   }
+  if (rpb == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+    float v = 0.0f;
+    for (int r = 0; r < rpb; ++r) v += comb[r * a.cols + c];
+    part[c] = v;
+  }
+}
+
+// A unit from shared memory.
+__device__ __forceinline__ void lds_unit(uint32_t p, Unit<__nv_bfloat16>& u) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.w[0]), "=r"(u.w[1]), "=r"(u.w[2]), "=r"(u.w[3])
+               : "r"(p));
+}
+__device__ __forceinline__ void lds_unit(uint32_t p, Unit<float>& u) {
+  const float4 a = lds_f4(p), b = lds_f4(p + 16);
+  u.f[0] = a.x, u.f[1] = a.y, u.f[2] = a.z, u.f[3] = a.w;
+  u.f[4] = b.x, u.f[5] = b.y, u.f[6] = b.z, u.f[7] = b.w;
+}
+
+constexpr int kMaxStages = 4;
+
+// The same backward pass with dh and s arriving by bulk copies: a ring of
+// `stages` stages of rpb rows each, filled ahead, so that loads are in flight
+// while a row is reduced and written; dsum comes straight into registers, one
+// row ahead.  (Loads into registers only, as above, leave the memory idle
+// between a row's loads and its writes: an SM holds too few rows at once.)
+// A thread reads its units from shared memory once for the row's sum and once
+// more for the outputs, so a row's stage is free when the next row's sum is
+// taken.  Rows are whole units here.
+template <typename TA, typename TS, int K>
+__global__ void __maxnreg__(K == 2 ? 80 : 128) k_add_rmsnorm_bwd_ring(const BwdArgs a, const int stages) {
+  __shared__ float red[2][kMaxThreads / 32];
+  __shared__ __align__(8) uint64_t full[kMaxStages];
+  extern __shared__ __align__(128) unsigned char ring[];
+  const int tpr = a.tpr, rpb = a.rpb, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
+  const uint32_t row_a = (uint32_t)a.cols * sizeof(TA), row_s = (uint32_t)a.cols * sizeof(TS);
+  const uint32_t off_s = row_a * rpb, stage_bytes = off_s + row_s * rpb;
+  const uint32_t ring0 = smem_u32(ring);
+  const int64_t step = (int64_t)gridDim.x * rpb, first = (int64_t)blockIdx.x * rpb;
+  // copies of the rows from `base` on into stage st, by the first warp
+  auto fill = [&](int64_t base, int st) {
+    const int n = (int)min((int64_t)rpb, a.rows - base);
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)n * (row_a + row_s));
+    __syncwarp();
+    for (int r = threadIdx.x; r < n; r += 32) {
+      unsigned char* at = ring + (size_t)st * stage_bytes;
+      bulk_load(at + (size_t)r * row_a, row_ptr<TA>(a.dh, a.lddh, base + r), row_a, &full[st]);
+      bulk_load(at + off_s + (size_t)r * row_s, row_ptr<TS>(a.s, a.lds, base + r), row_s, &full[st]);
+    }
+  };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init_cluster();
+  }
+  __syncthreads();
+  if (threadIdx.x < 32)
+    for (int i = 0; i < stages; ++i)
+      if (first + i * step < a.rows) fill(first + i * step, i);
+
+  const DropKey key = a.d.threshold ? drop_key(a.d) : DropKey{};
+  F8 acc[K] = {};
+  Unit<TS> ds[K];
+  auto load_dsum = [&](int64_t row) {
+    if (!a.dsum || row >= a.rows) return;
+    const TS* p = row_ptr<TS>(a.dsum, a.lddsum, row);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = 8 * (t + k * tpr);
+      if (c < a.cols) ld_unit(p + c, ds[k]);
+    }
+  };
+  // with two units a thread its gains stay in registers
+  F8 gain[K];
+  auto gain_at = [&](int k) {
+    const int c = 8 * (t + k * tpr);
+    return c < a.cols ? load_gain<true>(a.gain, a.gain_fp32, c, 8) : F8{};
+  };
+  if (K == 2) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) gain[k] = gain_at(k);
+  }
+  load_dsum(first + lane_row);
+  int st = 0, parity = 0;
+  uint32_t pass = 0;
+  bool dead = false;       // a wait ran out (recorded): go on without waiting, so that all threads still leave together
+  for (int64_t base = first; base < a.rows; base += step, parity ^= 1) {
+    const int64_t row = base + lane_row;
+    const bool on = row < a.rows;
+    const float rstd = on ? a.rstd[row] : 0.0f;
+    if (!dead) dead = !mbar_wait_u32(smem_u32(&full[st]), pass);
+    const uint32_t at_a = ring0 + (uint32_t)st * stage_bytes + (uint32_t)lane_row * row_a;
+    const uint32_t at_s = ring0 + (uint32_t)st * stage_bytes + off_s + (uint32_t)lane_row * row_s;
+    const uint64_t rstd2 = f2(rstd, rstd);
+    Unit<TA> dh;
+    Unit<TS> s;
+    uint64_t dot2 = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = 8 * (t + k * tpr);
+      if (!on || c >= a.cols) continue;
+      lds_unit(at_a + (uint32_t)c * sizeof(TA), dh);
+      lds_unit(at_s + (uint32_t)c * sizeof(TS), s);
+      bwd_sums(unpack(dh), unpack(s), K == 2 ? gain[k] : gain_at(k), rstd2, acc[k], dot2);
+    }
+    const float dot = row_reduce<false>(f2(dot2).x + f2(dot2).y, tpr, red[parity]);
+    if (tpr <= 32) __syncthreads();
+    // every thread is done with the row before: refill its stage
+    if (threadIdx.x < 32 && stages > 1 && base != first && base + (stages - 1) * step < a.rows)
+      fill(base + (stages - 1) * step, st == 0 ? stages - 1 : st - 1);
+    const float coef = -rstd * (rstd * (rstd * dot * a.inv_cols));
+    const uint64_t c2 = f2(coef, coef);
+    TS* dr = row_ptr<TS>(a.dr, a.lddr, row);
+    TA* dx = row_ptr<TA>(a.dx, a.lddx, row);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = 8 * (t + k * tpr);
+      if (!on || c >= a.cols) continue;
+      lds_unit(at_a + (uint32_t)c * sizeof(TA), dh);
+      lds_unit(at_s + (uint32_t)c * sizeof(TS), s);
+      F8 v = bwd_unit(unpack(dh), unpack(s), K == 2 ? gain[k] : gain_at(k), a.dsum ? unpack(ds[k]) : F8{}, rstd2, c2);
+      if (a.dr) store_unit<true>(dr + c, 8, v);
+      if (a.dx) {
+        if (a.d.threshold)
+          drop_unit(v, (uint64_t)(row * a.per_row + t + k * tpr), key, a.d.threshold, a.d.factor);
+        store_unit<true>(dx + c, 8, v);
+      }
+    }
+    load_dsum(row + step);
+    if (stages == 1) {
+      __syncthreads();
+      if (threadIdx.x < 32 && base + step < a.rows) fill(base + step, 0);
+    }
+    if (++st == stages) {
+      st = 0;
+      pass ^= 1u;
+    }
+  }
+  if (!a.part) return;
+  float* part = a.part + (int64_t)blockIdx.x * a.cols;
+  float* comb = reinterpret_cast<float*>(ring);      // every copy has landed and been read
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = 8 * (t + k * tpr);
+    if (c < a.cols) store_unit<false>((rpb == 1 ? part : comb + lane_row * a.cols) + c, 8, acc[k]);
+  }
+  if (rpb == 1) return;
   __syncthreads();
   for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
     float v = 0.0f;
@@ -346,12 +503,22 @@ __global__ void __launch_bounds__(1024) k_sum_partials(const float* __restrict__
 
 // Threads a row: enough that four units a thread cover it, at least 16 with
 // scale groups (a group of 128 columns is 16 units); while rows leave SMs
-// without work, one unit a thread.
-int pick_tpr_log2(int64_t rows, int64_t per_row, bool groups) {
-  int l = groups ? 4 : 2;
-  while (((int64_t)kK << l) < per_row) ++l;
-  while (rows < 2 * sm_count() && ((int64_t)1 << l) < per_row && l < 9) ++l;
-  return l;
+// without work, one unit a thread.  A row of up to 64 threads takes a power of
+// two and shares its block of 128; a longer one has a block of its own, of
+// whole warps (not rounded up further: 12288 columns take 384 threads, two
+// blocks of which fit an SM, where 512 would leave one).
+void pick_threads(int64_t rows, int64_t per_row, bool groups, int32_t* tpr, int32_t* rpb) {
+  const int64_t units = rows < 2 * sm_count() ? 1 : kK;
+  int64_t t = std::min<int64_t>(ceil_div<int64_t>(per_row, units), kMaxThreads);
+  if (t > 64) {
+    *tpr = (int32_t)ceil_div<int64_t>(t, 32) * 32;
+    *rpb = 1;
+    return;
+  }
+  int p = groups ? 16 : 4;
+  while (p < t) p *= 2;
+  *tpr = p;
+  *rpb = 128 / p;
 }
 
 constexpr int kMaxParts = 1024;   // blocks of the backward kernel, and so partial rows of dg
@@ -375,6 +542,46 @@ struct Bwd {
   static const void* ptr() { return (const void*)&k_add_rmsnorm_bwd<TA, TS, VEC>; }
 };
 
+// Rows shorter than this share a block's stage by the dozen: their copies are
+// too small to pay.
+constexpr int64_t kRingMinCols = 512;
+constexpr size_t kSmemPerSm = 220 << 10;
+
+template <typename TA, typename TS>
+const void* ring_kernel(int k) {
+  return k == 2 ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 2> : (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4>;
+}
+
+// Two units a thread up to 8192 columns (512 threads), four beyond; as many
+// blocks an SM as registers allow (two of 512 threads at most), the ring as
+// deep as shared memory allows.
+sf_status launch_ring(BwdArgs& a, int32_t ta, int32_t ts, cudaStream_t st, int64_t* parts) {
+  using B = __nv_bfloat16;
+  const int k = a.per_row <= 2 * kMaxThreads ? 2 : 4;
+  int t = ceil_div(a.per_row, k);
+  if (t > 64) {
+    a.tpr = ceil_div(t, 32) * 32;
+    a.rpb = 1;
+  } else {
+    int p = 32;
+    while (p < t) p *= 2;
+    a.tpr = p;
+    a.rpb = 128 / p;
+  }
+  const int threads = a.tpr * a.rpb;
+  const void* kernel = ta == SF_BF16 ? (ts == SF_BF16 ? ring_kernel<B, B>(k) : ring_kernel<B, float>(k))
+                                     : (ts == SF_BF16 ? ring_kernel<float, B>(k) : ring_kernel<float, float>(k));
+  const size_t stage = (size_t)a.rpb * a.cols * (dtype_bytes(ta) + dtype_bytes(ts));
+  int per_sm = std::max(1, std::min<int>(768 / threads, (int)(kSmemPerSm / (2 * stage))));
+  const int stages = (int)std::max<size_t>(1, std::min<size_t>(kMaxStages, kSmemPerSm / per_sm / stage));
+  const size_t smem = stage * stages;
+  SF_TRY(allow_dynamic_smem(kernel, smem));
+  *parts = std::min<int64_t>({ceil_div<int64_t>(a.rows, a.rpb), (int64_t)sm_count() * per_sm, kMaxParts});
+  void* args[] = {&a, const_cast<int*>(&stages)};
+  SF_CUDA_TRY(cudaLaunchKernel(kernel, dim3((unsigned)*parts), dim3(threads), args, smem, st), "launch k_add_rmsnorm_bwd_ring");
+  return SF_OK;
+}
+
 sf_status check_gain(const void* gain, int32_t dtype, const char* name) {
   if (!gain) return fail(SF_ERR_INVALID, "%s is NULL", name);
   if (dtype != SF_BF16 && dtype != SF_FP32) return fail(SF_ERR_UNSUPPORTED, "%s: type %d is not taken here", name, (int)dtype);
@@ -389,6 +596,14 @@ sf_status check_cols(int64_t cols) {
 }
 
 }  // namespace
+
+int read_and_clear_device_error_norm() {
+  int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof v) != cudaSuccess) return 0;
+  if (v) cudaMemcpyToSymbol(g_device_error, &z, sizeof z);
+  return v;
+}
+
 }  // namespace sf
 
 extern "C" {
@@ -432,15 +647,16 @@ sf_status sf_add_rmsnorm_forward(const sf_matrix* x, const sf_matrix* residual, 
   a.rows = rows;
   a.cols = (int32_t)cols;
   a.per_row = (int32_t)ceil_div<int64_t>(cols, 8);
-  a.group_lanes = group / 8;
+  a.group_log2 = group == 128 ? 7 : group == 64 ? 6 : group == 32 ? 5 : 0;
   a.n_groups = group ? (int32_t)ceil_div<int64_t>(cols, group) : 1;
   a.eps = (float)eps;
   a.inv_cols = (float)(1.0 / (double)cols);
-  a.tpr_log2 = pick_tpr_log2(rows, a.per_row, h8 != nullptr);
-  const int threads = std::max(128, 1 << a.tpr_log2);
-  const int64_t grid = ceil_div<int64_t>(rows, threads >> a.tpr_log2);
+  pick_threads(rows, a.per_row, h8 != nullptr, &a.tpr, &a.rpb);
+  const int threads = a.tpr * a.rpb;
+  const int64_t grid = ceil_div<int64_t>(rows, a.rpb);
   if (grid > INT32_MAX) return fail(SF_ERR_UNSUPPORTED, "too many rows");
-  const bool vec = units_aligned(x) && units_aligned(residual) && units_aligned(sum) && units_aligned(h) && units_aligned(h8);
+  const bool vec = units_aligned(x) && units_aligned(residual) && units_aligned(sum) && units_aligned(h) && units_aligned(h8) &&
+                   reinterpret_cast<uintptr_t>(gain) % (8 * dtype_bytes(gain_dtype)) == 0;
   const int32_t ts = residual ? residual->dtype : sum ? sum->dtype : x->dtype;
   void* args[] = {&a};
   SF_CUDA_TRY(cudaLaunchKernel(pick<Fwd>(x->dtype, ts, vec), dim3((unsigned)grid), dim3(threads), args, 0, as_stream(stream)),
@@ -493,21 +709,25 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum, con
   a.cols = (int32_t)cols;
   a.per_row = (int32_t)ceil_div<int64_t>(cols, 8);
   a.inv_cols = (float)(1.0 / (double)cols);
-  a.tpr_log2 = pick_tpr_log2(rows, a.per_row, false);
-  const int threads = std::max(128, 1 << a.tpr_log2), rpb = threads >> a.tpr_log2;
+  pick_threads(rows, a.per_row, false, &a.tpr, &a.rpb);
+  const int threads = a.tpr * a.rpb, rpb = a.rpb;
   const int64_t blocks = ceil_div<int64_t>(rows, rpb);
   const int64_t resident = (int64_t)sm_count() * std::max(1, 512 / threads);
   const int64_t grid = std::min({blocks, resident, (int64_t)kMaxParts});
   const size_t smem = dgain && rpb > 1 ? (size_t)rpb * cols * sizeof(float) : 0;   // <= 16 KB: rpb * cols <= 4096
-  const bool vec = units_aligned(dh) && units_aligned(sum) && units_aligned(dsum) && units_aligned(dresidual) && units_aligned(dx);
+  const bool vec = units_aligned(dh) && units_aligned(sum) && units_aligned(dsum) && units_aligned(dresidual) && units_aligned(dx) &&
+                   reinterpret_cast<uintptr_t>(gain) % (8 * dtype_bytes(gain_dtype)) == 0;
   cudaStream_t st = as_stream(stream);
-  if (grid) {
+  int64_t parts = grid;
+  if (vec && cols % 8 == 0 && cols >= kRingMinCols && rows >= 2 * sm_count()) {
+    SF_TRY(launch_ring(a, dh->dtype, sum->dtype, st, &parts));
+  } else if (grid) {
     void* args[] = {&a};
     SF_CUDA_TRY(cudaLaunchKernel(pick<Bwd>(dh->dtype, sum->dtype, vec), dim3((unsigned)grid), dim3(threads), args, smem, st),
                 "launch k_add_rmsnorm_bwd");
   }
   if (dgain) {
-    k_sum_partials<<<(unsigned)ceil_div<int64_t>(cols, 32), dim3(32, 32), 0, st>>>(a.part, (int)grid, (int)cols, dgain,
+    k_sum_partials<<<(unsigned)ceil_div<int64_t>(cols, 32), dim3(32, 32), 0, st>>>(a.part, (int)parts, (int)cols, dgain,
                                                                                   dgain_dtype == SF_FP32);
     SF_TRY(check_launch("k_sum_partials"));
   }

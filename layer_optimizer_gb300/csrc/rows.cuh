@@ -22,27 +22,66 @@ struct Unit<float> {
   float f[8];
 };
 
-__device__ __forceinline__ void unpack(const Unit<__nv_bfloat16>& u, float (&v)[8]) {
+// Eight fp32 values as four pairs: additions, products and fused
+// multiply-adds run on both values of a pair at once (each rounded to nearest
+// as two scalar ones would be), which halves the instructions of kernels that
+// would otherwise be bound by issue and not by memory.
+struct F8 {
+  uint64_t p[4];
+};
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ F8 unpack(const Unit<__nv_bfloat16>& u) {
+  F8 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v.p[i] = f2(__uint_as_float(u.w[i] << 16), __uint_as_float(u.w[i] & 0xFFFF0000u));
+  return v;
+}
+__device__ __forceinline__ F8 unpack(const Unit<float>& u) {
+  F8 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v.p[i] = f2(u.f[2 * i], u.f[2 * i + 1]);
+  return v;
+}
+__device__ __forceinline__ void pack(const F8& v, Unit<__nv_bfloat16>& u) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(u.w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(u.w[i] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ void unpack(const Unit<float>& u, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = u.f[i];
-}
-__device__ __forceinline__ void pack(const float (&v)[8], Unit<__nv_bfloat16>& u) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);   // round to nearest even
+    const float2 x = f2(v.p[i]);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);   // round to nearest even
     u.w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
 }
-__device__ __forceinline__ void pack(const float (&v)[8], Unit<float>& u) {
+__device__ __forceinline__ void pack(const F8& v, Unit<float>& u) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) u.f[i] = v[i];
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = f2(v.p[i]);
+    u.f[2 * i] = x.x;
+    u.f[2 * i + 1] = x.y;
+  }
 }
 
 // Whole-unit accesses.  Not the read-only path: outputs may be their inputs.
@@ -92,7 +131,7 @@ __device__ __forceinline__ void load_unit(const float* p, int n, Unit<float>& u)
   for (int i = 0; i < 8; ++i) u.f[i] = i < n ? p[i] : 0.0f;
 }
 template <bool VEC>
-__device__ __forceinline__ void store_unit(__nv_bfloat16* p, int n, const float (&v)[8]) {
+__device__ __forceinline__ void store_unit(__nv_bfloat16* p, int n, const F8& v) {
   Unit<__nv_bfloat16> u;
   pack(v, u);
   if (VEC && n == 8) {
@@ -107,16 +146,16 @@ __device__ __forceinline__ void store_unit(__nv_bfloat16* p, int n, const float 
   }
 }
 template <bool VEC>
-__device__ __forceinline__ void store_unit(float* p, int n, const float (&v)[8]) {
+__device__ __forceinline__ void store_unit(float* p, int n, const F8& v) {
+  Unit<float> u;
+  pack(v, u);
   if (VEC && n == 8) {
-    Unit<float> u;
-    pack(v, u);
     st_unit(p, u);
     return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (i < n) p[i] = v[i];
+    if (i < n) p[i] = u.f[i];
 }
 
 // Dropout's constants: an element is kept where its 16 random bits are at
@@ -149,8 +188,7 @@ __device__ __forceinline__ DropKey drop_key(const DropConsts& d) {
 // 16 per column.  Eight columns share one evaluation, so a column costs 2.5
 // 32 x 32 -> 64 multiplications; with 32 bits a column (twice that) the
 // bf16 kernels would be bound by the multiplier and not by memory.
-__device__ __forceinline__ void drop_unit(float (&v)[8], uint64_t b, const DropKey& key, uint32_t threshold,
-                                          float factor) {
+__device__ __forceinline__ void drop_unit(F8& v, uint64_t b, const DropKey& key, uint32_t threshold, float factor) {
   uint32_t c0 = (uint32_t)b, c1 = (uint32_t)(b >> 32), c2 = key.c2, c3 = key.c3, k0 = key.k0, k1 = key.k1;
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
@@ -164,11 +202,14 @@ __device__ __forceinline__ void drop_unit(float (&v)[8], uint64_t b, const DropK
     k1 += 0xBB67AE85u;
   }
   const uint32_t w[4] = {c0, c1, c2, c3};
-  // a dropped element is 0 whatever its value (a NaN or infinity included)
+  // half >= threshold, compared in the upper half of a word (threshold >= 1
+  // here, 65536 included); a dropped element is 0 whatever its value
+  const uint32_t limit = ((threshold - 1) << 16) | 0xFFFFu;
+  const uint64_t f = f2(factor, factor);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    v[2 * j] = (w[j] & 0xFFFFu) >= threshold ? v[2 * j] * factor : 0.0f;
-    v[2 * j + 1] = (w[j] >> 16) >= threshold ? v[2 * j + 1] * factor : 0.0f;
+    const float2 x = f2(mul2(v.p[j], f));
+    v.p[j] = f2((w[j] << 16) > limit ? x.x : 0.0f, w[j] > limit ? x.y : 0.0f);
   }
 }
 

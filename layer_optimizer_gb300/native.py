@@ -157,7 +157,8 @@ def load(path=None):
     if not os.path.exists(p):
         raise RuntimeError(f"{p} is missing: build it with `python -m layer_optimizer_gb300.build`")
     try:  # make sure a libcudart with the library's SONAME is in the process (torch ships one)
-        import torch  # noqa: F401
+        import torch
+        _DTYPES.update({torch.bfloat16: SF_BF16, torch.float32: SF_FP32, torch.float8_e4m3fn: SF_E4M3})
     except ImportError:
         pass
     lib = ctypes.CDLL(p)
@@ -355,18 +356,17 @@ def lce_forward_backward(H, W, labels, N, D, V, chunk, ignore_index, loss, dH, d
 
 # ------------------------------------------------------------------ (d) ----
 
-_DTYPES = None
+_DTYPES = {}      # sf_dtype by torch dtype (filled by load(), which imports torch)
 
 
 def _dtype(t, name):
     """sf_dtype of a torch tensor."""
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.bfloat16: SF_BF16, torch.float32: SF_FP32, torch.float8_e4m3fn: SF_E4M3}
     try:
         return _DTYPES[t.dtype]
     except KeyError:
+        load()
+        if t.dtype in _DTYPES:
+            return _DTYPES[t.dtype]
         raise SfError(SF_ERR_UNSUPPORTED, f"{name}: {t.dtype} is not taken here") from None
 
 
@@ -377,13 +377,19 @@ def _reachable(t, name):
 
 def matrix(t, name="matrix"):
     """sf_matrix of a 2D torch tensor with unit column stride (None stays None; an sf_matrix stays itself)."""
-    if t is None or isinstance(t, sf_matrix):
+    if t is None or type(t) is sf_matrix:
         return t
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2:
         raise SfError(SF_ERR_INVALID, f"{name} must be two-dimensional with unit column stride")
-    _reachable(t, name)
     rows, cols = t.shape
-    return sf_matrix(t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else max(cols, t.stride(0)), _dtype(t, name))
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise SfError(SF_ERR_INVALID, f"{name} must be two-dimensional with unit column stride")
+    if not t.is_cuda:
+        _reachable(t, name)
+    if rows <= 1 and ld < cols:
+        ld = cols
+    return sf_matrix(t.data_ptr(), rows, cols, ld, _dtype(t, name))
 
 
 def _ref(m):
@@ -392,13 +398,14 @@ def _ref(m):
 
 def _vector(t, n, name, dtypes=None):
     """Address of a dense device vector of n elements (None and addresses pass)."""
-    if t is None or isinstance(t, int):
+    if t is None or type(t) is int:
         return t
     if t.numel() != n or not t.is_contiguous():
         raise SfError(SF_ERR_INVALID, f"{name} must be dense with {n} elements")
     if dtypes is not None and str(t.dtype) not in dtypes:
         raise SfError(SF_ERR_UNSUPPORTED, f"{name}: {t.dtype} is not taken here")
-    _reachable(t, name)
+    if not t.is_cuda:
+        _reachable(t, name)
     return t.data_ptr()
 
 

@@ -208,7 +208,12 @@ def test_add_rmsnorm_forward_zero_rows_and_special_values():
     _close("h", h[5:], ref, 70 * U * np.abs(ref))
 
 
-@pytest.mark.parametrize("rows,cols,pad,lead", SHAPES)
+# enough aligned rows for the staged form: one and several rows a block, two and four units a thread, one stage
+STAGED = [(1000, 512, 0, 0), (777, 520, 8, 32), (610, 1024, 0, 0), (320, 4104, 24, 0), (310, 8192, 0, 0), (305, 12288, 0, 0),
+          (308, 16384, 0, 0)]
+
+
+@pytest.mark.parametrize("rows,cols,pad,lead", SHAPES + STAGED)
 @pytest.mark.parametrize("at,st,gt,dgt,stream_grad,p", [
     (BF, BF, BF, F32, True, 0.0), (BF, F32, F32, BF, True, 0.1), (F32, F32, F32, F32, False, 0.25), (F32, BF, BF, F32, True, 0.0),
 ])
