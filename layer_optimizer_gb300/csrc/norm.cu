@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
     }
   }
   if (!a.part) return;
+  griddep_launch_dependents();
   float* part = a.part + (int64_t)blockIdx.x * a.cols;
 #pragma unroll
   for (int k = 0; k < kK; ++k) {
@@ -344,36 +345,68 @@ __device__ __forceinline__ void lds_unit(uint32_t p, Unit<float>& u) {
   u.f[4] = b.x, u.f[5] = b.y, u.f[6] = b.z, u.f[7] = b.w;
 }
 
-constexpr int kMaxStages = 4;
+__device__ __forceinline__ void sts_unit(uint32_t p, const F8& v, __nv_bfloat16) {
+  Unit<__nv_bfloat16> u;
+  pack(v, u);
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(u.w[0]), "r"(u.w[1]), "r"(u.w[2]), "r"(u.w[3])
+               : "memory");
+}
+__device__ __forceinline__ void sts_unit(uint32_t p, const F8& v, float) {
+  asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(p), "l"(v.p[0]), "l"(v.p[1]) : "memory");
+  asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(p + 16), "l"(v.p[2]), "l"(v.p[3]) : "memory");
+}
+// Bulk copy of shared memory to global memory, of this thread's bulk group.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
 
-// The same backward pass with dh and s arriving by bulk copies: a ring of
-// `stages` stages of rpb rows each, filled ahead, so that loads are in flight
-// while a row is reduced and written; dsum comes straight into registers, one
-// row ahead.  (Loads into registers only, as above, leave the memory idle
-// between a row's loads and its writes: an SM holds too few rows at once.)
-// A thread reads its units from shared memory once for the row's sum and once
-// more for the outputs, so a row's stage is free when the next row's sum is
-// taken.  Rows are whole units here.
+constexpr int kMinStages = 3, kMaxStages = 4;
+
+// The same backward pass with whole rows moved by bulk copies, both ways, so
+// that threads address shared memory only.  A ring of `stages` stages of rpb
+// rows each (dh, s and dsum): a stage is filled ahead, its row is reduced, the
+// outputs overwrite the inputs in place (dx over dh, dresidual over s), a bulk
+// store takes them out, and the stage is filled again.  One barrier a row: past
+// the barrier of row i's sum every thread has also finished row i - 1's
+// outputs, which then leave, and row i - 2's have left, so its stage is
+// refilled.  With loads and stores of registers the kernel was bound by
+// instruction issue (49 instructions an element, 59 % of the copy rate).
 template <typename TA, typename TS, int K>
 __global__ void __maxnreg__(K == 2 ? 80 : 128) k_add_rmsnorm_bwd_ring(const BwdArgs a, const int stages) {
-  __shared__ float red[2][kMaxThreads / 32];
+  __shared__ __align__(16) float red[2][4][kMaxThreads / 32];    // [alternating][row of the block][warp of the row]
   __shared__ __align__(8) uint64_t full[kMaxStages];
   extern __shared__ __align__(128) unsigned char ring[];
   const int tpr = a.tpr, rpb = a.rpb, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
+  if (threadIdx.x < 2 * 4 * kMaxThreads / 32) (&red[0][0][0])[threadIdx.x] = 0.0f;     // blocks have 128 threads or more
   const uint32_t row_a = (uint32_t)a.cols * sizeof(TA), row_s = (uint32_t)a.cols * sizeof(TS);
-  const uint32_t off_s = row_a * rpb, stage_bytes = off_s + row_s * rpb;
+  const uint32_t off_s = row_a * rpb, off_d = off_s + row_s * rpb;
+  const uint32_t stage_bytes = off_d + (a.dsum ? row_s * rpb : 0u);
   const uint32_t ring0 = smem_u32(ring);
   const int64_t step = (int64_t)gridDim.x * rpb, first = (int64_t)blockIdx.x * rpb;
-  // copies of the rows from `base` on into stage st, by the first warp
+  // by the first warp: the copies of the rows from `base` on into stage st ...
   auto fill = [&](int64_t base, int st) {
     const int n = (int)min((int64_t)rpb, a.rows - base);
-    if (threadIdx.x == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)n * (row_a + row_s));
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)n * (row_a + row_s + (a.dsum ? row_s : 0u)));
     __syncwarp();
-    for (int r = threadIdx.x; r < n; r += 32) {
+    if ((int)threadIdx.x < n) {
       unsigned char* at = ring + (size_t)st * stage_bytes;
-      bulk_load(at + (size_t)r * row_a, row_ptr<TA>(a.dh, a.lddh, base + r), row_a, &full[st]);
-      bulk_load(at + off_s + (size_t)r * row_s, row_ptr<TS>(a.s, a.lds, base + r), row_s, &full[st]);
+      const int64_t row = base + threadIdx.x;
+      bulk_load(at + threadIdx.x * row_a, row_ptr<TA>(a.dh, a.lddh, row), row_a, &full[st]);
+      bulk_load(at + off_s + threadIdx.x * row_s, row_ptr<TS>(a.s, a.lds, row), row_s, &full[st]);
+      if (a.dsum) bulk_load(at + off_d + threadIdx.x * row_s, row_ptr<TS>(a.dsum, a.lddsum, row), row_s, &full[st]);
     }
+  };
+  // ... and those of its outputs to global memory (each lane its own row, so
+  // that the lane that fills a row's place knows when it has been read)
+  auto drain = [&](int64_t base, int st) {
+    const int n = (int)min((int64_t)rpb, a.rows - base);
+    if ((int)threadIdx.x < n) {
+      const uint32_t at = ring0 + (uint32_t)st * stage_bytes;
+      const int64_t row = base + threadIdx.x;
+      if (a.dx) bulk_store(row_ptr<TA>(a.dx, a.lddx, row), at + threadIdx.x * row_a, row_a);
+      if (a.dr) bulk_store(row_ptr<TS>(a.dr, a.lddr, row), at + off_s + threadIdx.x * row_s, row_s);
+    }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   };
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
@@ -385,90 +418,110 @@ __global__ void __maxnreg__(K == 2 ? 80 : 128) k_add_rmsnorm_bwd_ring(const BwdA
       if (first + i * step < a.rows) fill(first + i * step, i);
 
   const DropKey key = a.d.threshold ? drop_key(a.d) : DropKey{};
-  F8 acc[K] = {};
-  Unit<TS> ds[K];
-  auto load_dsum = [&](int64_t row) {
-    if (!a.dsum || row >= a.rows) return;
-    const TS* p = row_ptr<TS>(a.dsum, a.lddsum, row);
+  const int col0 = 8 * t, dcol = 8 * tpr;
+  bool in[K];
+  F8 acc[K] = {}, gain[K];      // with two units a thread its gains stay in registers
+  auto gain_at = [&](int k) { return in[k] ? load_gain<true>(a.gain, a.gain_fp32, col0 + k * dcol, 8) : F8{}; };
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = 8 * (t + k * tpr);
-      if (c < a.cols) ld_unit(p + c, ds[k]);
-    }
-  };
-  // with two units a thread its gains stay in registers
-  F8 gain[K];
-  auto gain_at = [&](int k) {
-    const int c = 8 * (t + k * tpr);
-    return c < a.cols ? load_gain<true>(a.gain, a.gain_fp32, c, 8) : F8{};
-  };
-  if (K == 2) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) gain[k] = gain_at(k);
+  for (int k = 0; k < K; ++k) {
+    in[k] = col0 + k * dcol < a.cols;
+    if (K == 2) gain[k] = gain_at(k);
   }
-  load_dsum(first + lane_row);
+  const uint32_t at_a0 = ring0 + (uint32_t)lane_row * row_a + (uint32_t)col0 * sizeof(TA);
+  const uint32_t at_s0 = ring0 + off_s + (uint32_t)lane_row * row_s + (uint32_t)col0 * sizeof(TS);
+  const uint32_t at_d0 = at_s0 + off_d - off_s;
+  const float* rp = a.rstd + first + lane_row;
+  float rstd_next = first + lane_row < a.rows ? *rp : 0.0f;
+  uint64_t unit = (uint64_t)((first + lane_row) * a.per_row + t);
+  uint32_t at = 0;         // offset of the row's stage
   int st = 0, parity = 0;
   uint32_t pass = 0;
   bool dead = false;       // a wait ran out (recorded): go on without waiting, so that all threads still leave together
-  for (int64_t base = first; base < a.rows; base += step, parity ^= 1) {
-    const int64_t row = base + lane_row;
-    const bool on = row < a.rows;
-    const float rstd = on ? a.rstd[row] : 0.0f;
+  int64_t base = first;
+  for (; base < a.rows; base += step, parity ^= 1) {
+    const bool on = base + lane_row < a.rows;
+    const float rstd = rstd_next;
+    rp += step;
+    if (base + step + lane_row < a.rows) rstd_next = *rp;
     if (!dead) dead = !mbar_wait_u32(smem_u32(&full[st]), pass);
-    const uint32_t at_a = ring0 + (uint32_t)st * stage_bytes + (uint32_t)lane_row * row_a;
-    const uint32_t at_s = ring0 + (uint32_t)st * stage_bytes + off_s + (uint32_t)lane_row * row_s;
     const uint64_t rstd2 = f2(rstd, rstd);
     Unit<TA> dh;
-    Unit<TS> s;
+    Unit<TS> s, ds;
     uint64_t dot2 = 0;
+    if (on) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = 8 * (t + k * tpr);
-      if (!on || c >= a.cols) continue;
-      lds_unit(at_a + (uint32_t)c * sizeof(TA), dh);
-      lds_unit(at_s + (uint32_t)c * sizeof(TS), s);
-      bwd_sums(unpack(dh), unpack(s), K == 2 ? gain[k] : gain_at(k), rstd2, acc[k], dot2);
-    }
-    const float dot = row_reduce<false>(f2(dot2).x + f2(dot2).y, tpr, red[parity]);
-    if (tpr <= 32) __syncthreads();
-    // every thread is done with the row before: refill its stage
-    if (threadIdx.x < 32 && stages > 1 && base != first && base + (stages - 1) * step < a.rows)
-      fill(base + (stages - 1) * step, st == 0 ? stages - 1 : st - 1);
-    const float coef = -rstd * (rstd * (rstd * dot * a.inv_cols));
-    const uint64_t c2 = f2(coef, coef);
-    TS* dr = row_ptr<TS>(a.dr, a.lddr, row);
-    TA* dx = row_ptr<TA>(a.dx, a.lddx, row);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = 8 * (t + k * tpr);
-      if (!on || c >= a.cols) continue;
-      lds_unit(at_a + (uint32_t)c * sizeof(TA), dh);
-      lds_unit(at_s + (uint32_t)c * sizeof(TS), s);
-      F8 v = bwd_unit(unpack(dh), unpack(s), K == 2 ? gain[k] : gain_at(k), a.dsum ? unpack(ds[k]) : F8{}, rstd2, c2);
-      if (a.dr) store_unit<true>(dr + c, 8, v);
-      if (a.dx) {
-        if (a.d.threshold)
-          drop_unit(v, (uint64_t)(row * a.per_row + t + k * tpr), key, a.d.threshold, a.d.factor);
-        store_unit<true>(dx + c, 8, v);
+      for (int k = 0; k < K; ++k) {
+        if (!in[k]) continue;
+        lds_unit(at_a0 + at + (uint32_t)(k * dcol) * sizeof(TA), dh);
+        lds_unit(at_s0 + at + (uint32_t)(k * dcol) * sizeof(TS), s);
+        bwd_sums(unpack(dh), unpack(s), K == 2 ? gain[k] : gain_at(k), rstd2, acc[k], dot2);
       }
     }
-    load_dsum(row + step);
-    if (stages == 1) {
-      __syncthreads();
-      if (threadIdx.x < 32 && base + step < a.rows) fill(base + step, 0);
+    // the row's sum: lanes by a butterfly, then all warps of the row (unused
+    // places hold 0) in one fixed tree
+    float dot = f2(dot2).x + f2(dot2).y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if ((threadIdx.x & 31) == 0) red[parity][lane_row][t >> 5] = dot;
+    __syncthreads();
+    if (threadIdx.x < 32 && base != first) {
+      const int prev = st == 0 ? stages - 1 : st - 1;
+      drain(base - step, prev);
+      // the outputs of the row before that have been read out of its stage
+      asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      if (base - first > step && base + (stages - 2) * step < a.rows)
+        fill(base + (stages - 2) * step, prev == 0 ? stages - 1 : prev - 1);
     }
+    {
+      uint64_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(&red[parity][lane_row][4 * i]);
+        w[i] = add2(f2(v.x, v.y), f2(v.z, v.w));
+      }
+      const float2 v = f2(add2(add2(w[0], w[1]), add2(w[2], w[3])));
+      dot = v.x + v.y;
+    }
+    const float coef = -rstd * (rstd * (rstd * dot * a.inv_cols));
+    const uint64_t c2 = f2(coef, coef);
+    if (on && (a.dr || a.dx)) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (!in[k]) continue;
+        const uint32_t pa = at_a0 + at + (uint32_t)(k * dcol) * sizeof(TA), ps = at_s0 + at + (uint32_t)(k * dcol) * sizeof(TS);
+        lds_unit(pa, dh);
+        lds_unit(ps, s);
+        if (a.dsum) lds_unit(at_d0 + at + (uint32_t)(k * dcol) * sizeof(TS), ds);
+        F8 v = bwd_unit(unpack(dh), unpack(s), K == 2 ? gain[k] : gain_at(k), a.dsum ? unpack(ds) : F8{}, rstd2, c2);
+        if (a.dr) sts_unit(ps, v, TS());
+        if (a.dx) {
+          if (a.d.threshold) drop_unit(v, unit + k * tpr, key, a.d.threshold, a.d.factor);
+          sts_unit(pa, v, TA());
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    unit += (uint64_t)(step * a.per_row);
+    at += stage_bytes;
     if (++st == stages) {
       st = 0;
+      at = 0;
       pass ^= 1u;
     }
   }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    drain(base - step, st == 0 ? stages - 1 : st - 1);       // the last row's outputs
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
   if (!a.part) return;
+  griddep_launch_dependents();
   float* part = a.part + (int64_t)blockIdx.x * a.cols;
-  float* comb = reinterpret_cast<float*>(ring);      // every copy has landed and been read
+  float* comb = reinterpret_cast<float*>(ring);      // every copy has landed, and every store has left
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c = 8 * (t + k * tpr);
+    const int c = col0 + k * dcol;
     if (c < a.cols) store_unit<false>((rpb == 1 ? part : comb + lane_row * a.cols) + c, 8, acc[k]);
   }
   if (rpb == 1) return;
@@ -482,13 +535,16 @@ __global__ void __maxnreg__(K == 2 ? 80 : 128) k_add_rmsnorm_bwd_ring(const BwdA
 
 // dg[c] = sum over the blocks' partial rows: 32 columns a block, 32 threads a
 // column, each over every 32nd partial, then a tree.
-__global__ void __launch_bounds__(1024) k_sum_partials(const float* __restrict__ part, int n_parts, int cols,
+__global__ void __launch_bounds__(1024) k_sum_partials(const float* part, int n_parts, int cols,
                                                        void* __restrict__ out, int out_fp32) {
   __shared__ float red[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;
   float v = 0.0f;
-  if (c < cols)
+  griddep_wait();
+  if (c < cols) {
+#pragma unroll 8
     for (int p = threadIdx.y; p < n_parts; p += 32) v += part[(int64_t)p * cols + c];
+  }
   red[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   v = red[threadIdx.x][threadIdx.y];       // column threadIdx.y, partial sum threadIdx.x
@@ -542,38 +598,47 @@ struct Bwd {
   static const void* ptr() { return (const void*)&k_add_rmsnorm_bwd<TA, TS, VEC>; }
 };
 
-// Rows shorter than this share a block's stage by the dozen: their copies are
-// too small to pay.
-constexpr int64_t kRingMinCols = 512;
-constexpr size_t kSmemPerSm = 220 << 10;
+constexpr size_t kSmemPerSm = 222 << 10;
+
+// Bytes of one row in the staged kernel's ring.
+inline size_t ring_row_bytes(int64_t cols, int32_t ta, int32_t ts, bool dsum) {
+  return (size_t)cols * (dtype_bytes(ta) + (dsum ? 2 : 1) * dtype_bytes(ts));
+}
+
+// The staged kernel takes aligned rows of whole units, long enough that a
+// block's few copies are worth their set-up and short enough that three fit
+// in shared memory, when there is more than one block's worth of rows an SM.
+inline bool ring_fits(int64_t rows, int64_t cols, int32_t ta, int32_t ts, bool dsum) {
+  return cols % 8 == 0 && cols >= 512 && rows >= 2 * sm_count() &&
+         kMinStages * ring_row_bytes(cols, ta, ts, dsum) <= kSmemPerSm;
+}
 
 template <typename TA, typename TS>
 const void* ring_kernel(int k) {
   return k == 2 ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 2> : (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4>;
 }
 
-// Two units a thread up to 8192 columns (512 threads), four beyond; as many
-// blocks an SM as registers allow (two of 512 threads at most), the ring as
-// deep as shared memory allows.
+// Two units a thread up to 1024 columns, four beyond (16384 x 4096 bf16, all
+// outputs: 137 us with four, 149 us with two: fewer barriers' worth of work a
+// row outweighs fewer warps); as many blocks an SM as registers (80 and 128 a
+// thread) and three stages each allow.
 sf_status launch_ring(BwdArgs& a, int32_t ta, int32_t ts, cudaStream_t st, int64_t* parts) {
   using B = __nv_bfloat16;
-  const int k = a.per_row <= 2 * kMaxThreads ? 2 : 4;
-  int t = ceil_div(a.per_row, k);
+  const int k = a.per_row <= 128 ? 2 : 4;
+  const int t = ceil_div(a.per_row, k);
   if (t > 64) {
     a.tpr = ceil_div(t, 32) * 32;
     a.rpb = 1;
   } else {
-    int p = 32;
-    while (p < t) p *= 2;
-    a.tpr = p;
-    a.rpb = 128 / p;
+    a.tpr = t > 32 ? 64 : 32;
+    a.rpb = 128 / a.tpr;
   }
   const int threads = a.tpr * a.rpb;
   const void* kernel = ta == SF_BF16 ? (ts == SF_BF16 ? ring_kernel<B, B>(k) : ring_kernel<B, float>(k))
                                      : (ts == SF_BF16 ? ring_kernel<float, B>(k) : ring_kernel<float, float>(k));
-  const size_t stage = (size_t)a.rpb * a.cols * (dtype_bytes(ta) + dtype_bytes(ts));
-  int per_sm = std::max(1, std::min<int>(768 / threads, (int)(kSmemPerSm / (2 * stage))));
-  const int stages = (int)std::max<size_t>(1, std::min<size_t>(kMaxStages, kSmemPerSm / per_sm / stage));
+  const size_t stage = a.rpb * ring_row_bytes(a.cols, ta, ts, a.dsum != nullptr);
+  const int per_sm = (int)std::max<size_t>(1, std::min<size_t>((k == 2 ? 768 : 512) / threads, kSmemPerSm / (kMinStages * stage + 1024)));
+  const int stages = (int)std::min<size_t>(kMaxStages, (kSmemPerSm / per_sm - 1024) / stage);
   const size_t smem = stage * stages;
   SF_TRY(allow_dynamic_smem(kernel, smem));
   *parts = std::min<int64_t>({ceil_div<int64_t>(a.rows, a.rpb), (int64_t)sm_count() * per_sm, kMaxParts});
@@ -719,7 +784,7 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum, con
                    reinterpret_cast<uintptr_t>(gain) % (8 * dtype_bytes(gain_dtype)) == 0;
   cudaStream_t st = as_stream(stream);
   int64_t parts = grid;
-  if (vec && cols % 8 == 0 && cols >= kRingMinCols && rows >= 2 * sm_count()) {
+  if (vec && ring_fits(rows, cols, dh->dtype, sum->dtype, dsum != nullptr)) {
     SF_TRY(launch_ring(a, dh->dtype, sum->dtype, st, &parts));
   } else if (grid) {
     void* args[] = {&a};
@@ -727,9 +792,9 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum, con
                 "launch k_add_rmsnorm_bwd");
   }
   if (dgain) {
-    k_sum_partials<<<(unsigned)ceil_div<int64_t>(cols, 32), dim3(32, 32), 0, st>>>(a.part, (int)parts, (int)cols, dgain,
-                                                                                  dgain_dtype == SF_FP32);
-    SF_TRY(check_launch("k_sum_partials"));
+    SF_CUDA_TRY(launch_pdl(k_sum_partials, dim3((unsigned)ceil_div<int64_t>(cols, 32)), dim3(32, 32), 0, st, a.part, (int)parts,
+                           (int)cols, dgain, (int)(dgain_dtype == SF_FP32)),
+                "launch k_sum_partials");
   }
   return SF_OK;
 }
