@@ -143,6 +143,7 @@ enum TcEpilogue : int {
   kTcSplit = 1,  // C fp32 [splits][M][ldc]: partial products over parts of K
   kTcBf16 = 2,   // C bf16
   kTcStats = 3,  // row_stats, label_logit, and with `store` C = exp(A B^T - tile maximum) in bf16
+  kTcRows = 5,   // C bf16 or fp32, product row i written to row row_map[i]
   kTcGrad = 4    // C = (exp(A B^T - lse) - onehot(label)) * factor in bf16; 0 where lse is +infinity
 };
 struct TcJob {
@@ -164,7 +165,12 @@ struct TcJob {
   float* label_logit = nullptr;    // [M]
   const float* lse = nullptr;      // [M]
   const float* factor = nullptr;   // device, one value
-  uint32_t* zero = nullptr;        // device word that the launch sets to 0 (kTcStats)
+  const int32_t* m_dev = nullptr;  // device-side M and K, at most the M and K above (not for kTcF32); an empty
+  const int32_t* k_dev = nullptr;  // sum gives zeros
+  const int32_t* row_map = nullptr;  // [M] (kTcRows)
+  bool out_fp32 = false;           // kTcRows
+  bool checked = false;            // the caller has checked that A, B and C are this device's memory
+  bool chained = false;            // launched as a programmatic dependent of the previous kernel in the stream
 };
 sf_status tc_gemm(const TcJob& job, cudaStream_t s);
 

@@ -199,17 +199,21 @@ LcePlan plan_lce(int64_t N, int64_t V, int64_t chunk) {
 //
 // The loss over all tokens and pieces of the vocabulary, for training steps
 // whose chunk x V logits would not fit beside the model:
+//   0. The n labelled tokens' rows of H are copied together (a token without a
+//      label has no loss and no gradient, so it costs nothing further, and a
+//      NaN in it reaches nothing).  n stays on the device: the products below
+//      read it there.
 //   1. Z = H W^T once, every tile reduced in the GEMM's epilogue to (max, sum
 //      exp) per row and the labels' logits: the logits never leave tensor
 //      memory.  The last piece's exponentials stay in the workspace.
-//   2. lse, the tokens' losses, n and the loss.
-//   3. Per piece, the last first: G = (softmax - onehot) * scale / n in bf16
-//      (the last piece: its exponentials rescaled; the others: Z again, with
-//      the gradient as the epilogue), dH += G W_piece, dW_piece = G^T H.
-// 8 - 2 / P times N D V flops for P pieces, against 6 when a token chunk's
-// logits are kept, but the workspace is one N x piece block of bf16 whatever
+//   2. lse, the tokens' losses, the loss; the last piece's exponentials become
+//      its gradient G = (softmax - onehot) * scale / n in bf16.
+//   3. Per piece, the last first: dH += G W_piece, dW_piece = G^T H; for the
+//      others G is formed first, as the epilogue of Z once more.
+// 8 - 2 / P times n D V flops for P pieces, against 6 when a token chunk's
+// logits are kept, but the workspace is one n x piece block of bf16 whatever
 // V, every row of dW is written once, in bf16 if asked (the type that the
-// AdamW step takes), and W is streamed P-independent times.
+// AdamW step takes), and dW is not read back for accumulation.
 
 constexpr int kPairsGb300 = 76;                       // CTA pairs of the GEMM's persistent grid (152 SMs)
 constexpr size_t kPieceBudget = (size_t)512 << 20;    // bytes of G that the default piece may take
@@ -221,132 +225,255 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
-// One warp per row: lse from the row's tile statistics (as k_lce_lse), its
-// loss; lse = +infinity marks an unlabelled row for the gradient.  The last
-// block to finish sums the losses in a fixed order and sets the gradient's
-// factor, so no further launch is needed.
-__global__ void __launch_bounds__(256) k_lce_finish(const float2* __restrict__ stats, int n_tiles, int64_t N, int64_t V,
-                                                    const float* __restrict__ label_logit,
-                                                    const int32_t* __restrict__ labels, int32_t ignore,
-                                                    double grad_scale, float* __restrict__ lse, float* row_loss,
-                                                    float* __restrict__ token_loss, float* __restrict__ factor,
-                                                    float* __restrict__ loss, uint32_t* counter) {
-  const int lane = threadIdx.x & 31;
-  const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (r < N) {
-    float m = -INFINITY, s = 0.0f;
-    for (int t = lane; t < n_tiles; t += 32) {
-      const float2 p = stats[r * n_tiles + t];
-      combine_stats(m, s, p.x, p.y);
-    }
+struct GatherArgs {
+  const uint16_t* H;       // [N][ldh]
+  int64_t ldh, N, D, V;
+  const int32_t* labels;
+  int32_t ignore;
+  double grad_scale;
+  uint16_t* Hc;            // [N][ldc]: the labelled rows in order, then zeros up to a multiple of 64 rows
+  int64_t ldc;
+  int32_t* label_c;        // [N]: their labels
+  int32_t* token;          // [N]: their token
+  int32_t* place;          // [N]: each token's row in Hc, or -1
+  int32_t* n_out;
+  float* factor;           // grad_scale / n (0 if n = 0)
+  uint32_t* counter;       // set to 0 for k_lce_rows
+  float* loss;             // set to 0 (the answer if n = 0); may be null
+  float* token_loss;       // set to 0 at unlabelled tokens; may be null
+  void* dH;                // unlabelled tokens' rows set to 0; may be null
+  int64_t lddh;
+  int32_t dh_fp32;
+};
+
+// One block per 8 tokens, a warp each.  Every block counts the labels before
+// its own and all labels (N words from L2), so no second launch and no order
+// between blocks is needed.
+__global__ void __launch_bounds__(256) k_lce_gather(const GatherArgs a) {
+  __shared__ int before_w[8], all_w[8], mine[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t0 = (int64_t)blockIdx.x * 8;
+  griddep_launch_dependents();
+  int before = 0, all = 0;
+  bool bad = false;
+  for (int64_t i = threadIdx.x; i < a.N; i += 256) {
+    const int32_t y = a.labels[i];
+    const bool on = labelled(y, a.ignore, a.V);
+    all += on;
+    before += on && i < t0;
+    bad |= !on && y != a.ignore;
+  }
+  if (bad && blockIdx.x == 0) atomicOr(&g_device_error, kDevErrIndex);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane & o) {
-        combine_stats(m2, s2, m, s);
-        m = m2;
-        s = s2;
-      } else {
-        combine_stats(m, s, m2, s2);
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  const int64_t tok = t0 + warp;
+  const int32_t y = tok < a.N ? a.labels[tok] : a.ignore;
+  const bool on = tok < a.N && labelled(y, a.ignore, a.V);
+  if (lane == 0) {
+    before_w[warp] = before;
+    all_w[warp] = all;
+    mine[warp] = on;
+  }
+  __syncthreads();
+  int n = 0, r = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    n += all_w[w];
+    r += before_w[w] + (w < warp ? mine[w] : 0);
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *a.n_out = n;
+    *a.factor = n > 0 ? (float)(a.grad_scale / (double)n) : 0.0f;
+    *a.counter = 0;
+    if (a.loss) *a.loss = 0.0f;
+  }
+  if (tok < a.N) {
+    if (lane == 0) {
+      a.place[tok] = on ? r : -1;
+      if (on) {
+        a.label_c[r] = y;
+        a.token[r] = (int32_t)tok;
+      } else if (a.token_loss) {
+        a.token_loss[tok] = 0.0f;
       }
     }
-    if (lane == 0) {
-      const int32_t y = labels[r];
-      const bool on = labelled(y, ignore, V);
-      if (!on && y != ignore) atomicOr(&g_device_error, kDevErrIndex);
-      const float l = m + logf(s), a = on ? l - label_logit[r] : 0.0f;
-      lse[r] = on ? l : INFINITY;
-      row_loss[r] = a;
-      if (token_loss) token_loss[r] = a;
+    // rows are 16-byte aligned; the last unit may hold columns beyond D, of the row's own padding
+    const int units = (int)((a.D + 7) / 8);
+    if (on) {
+      const uint4* from = reinterpret_cast<const uint4*>(a.H + tok * a.ldh);
+      uint4* to = reinterpret_cast<uint4*>(a.Hc + (int64_t)r * a.ldc);
+#pragma unroll 4
+      for (int u = lane; u < units; u += 32) {
+        if (u * 8 + 8 <= a.D) {
+          to[u] = from[u];
+        } else {
+          for (int c = u * 8; c < a.D; ++c) a.Hc[(int64_t)r * a.ldc + c] = a.H[tok * a.ldh + c];
+        }
+      }
+    } else if (a.dH) {
+      if (a.dh_fp32) {
+        float* p = static_cast<float*>(a.dH) + tok * a.lddh;
+        for (int c = lane; c < a.D; c += 32) p[c] = 0.0f;
+      } else {
+        uint16_t* p = static_cast<uint16_t*>(a.dH) + tok * a.lddh;
+        for (int c = lane; c < a.D; c += 32) p[c] = 0;
+      }
     }
   }
+  // the rows after the last labelled one, up to a whole K slab of dW's product
+  const int64_t end = min(a.N, (int64_t)(n + 63) / 64 * 64);
+  for (int64_t q = n + blockIdx.x; q < end; q += gridDim.x)
+    for (int c = threadIdx.x; c < a.D; c += 256) a.Hc[q * a.ldc + c] = 0;
+}
+
+struct RowsArgs {
+  const float2* stats;     // [N][n_tiles]
+  int32_t n_tiles;
+  const int32_t* n_dev;
+  const float* label_logit;
+  const int32_t* label_c;
+  const int32_t* token;
+  const float* factor;
+  __nv_bfloat16* G;        // [N][ldg], the last piece; may be null (no gradients)
+  int64_t ldg;
+  int32_t cols, col0;      // its columns
+  int32_t span;            // columns of a block
+  float* lse;              // [N]
+  float* row_loss;         // [N]
+  float* token_loss;       // by token; may be null
+  float* loss;             // may be null
+  uint32_t* counter;
+  int64_t N;
+};
+
+// One block per labelled row and span of columns: the row's lse from its tile
+// statistics, and the span of G, holding exp(z - tile maximum), becomes the
+// gradient: times exp(tile maximum - lse) * factor; the label's column comes
+// from its fp32 logit, because exp(z - lse) - 1 cancels where the model is
+// sure.  The span's loads are in flight while lse is taken (each block of a
+// row takes it again: a few hundred values).  4 bytes an element of G, against
+// 2 D flops for computing z again.  The blocks of the first span write the
+// row's loss, and the last of them sums all losses in a fixed order.
+constexpr int kSpanUnits = 8;
+__global__ void __launch_bounds__(256) k_lce_rows(const RowsArgs a) {
+  __shared__ float red_m[8], red_s[8];
   __shared__ bool last;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int n = *a.n_dev;
+  const int64_t r = blockIdx.x;
+  const int c0 = blockIdx.y * a.span + 8 * (int)threadIdx.x, c1 = min(a.cols, ((int)blockIdx.y + 1) * a.span);
+  if (r >= n) {
+    // rows that a K slab of dW's product still reads
+    if (a.G && r < (n + 63) / 64 * 64)
+      for (int c = c0; c < c1; c += 2048) *reinterpret_cast<uint4*>(a.G + r * a.ldg + c) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  uint4 v[kSpanUnits];
+  if (a.G) {
+#pragma unroll
+    for (int u = 0; u < kSpanUnits; ++u)
+      if (c0 + 2048 * u < c1) v[u] = *reinterpret_cast<const uint4*>(a.G + r * a.ldg + c0 + 2048 * u);
+  }
+  const float2* st = a.stats + r * a.n_tiles;
+  float m = -INFINITY, s = 0.0f;
+  for (int t = threadIdx.x; t < a.n_tiles; t += 256) {
+    const float2 p = st[t];
+    combine_stats(m, s, p.x, p.y);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    if (threadIdx.x & o) {
+      combine_stats(m2, s2, m, s);
+      m = m2;
+      s = s2;
+    } else {
+      combine_stats(m, s, m2, s2);
+    }
+  }
+  if ((threadIdx.x & 31) == 0) {
+    red_m[threadIdx.x >> 5] = m;
+    red_s[threadIdx.x >> 5] = s;
+  }
   __syncthreads();
+  m = red_m[0];
+  s = red_s[0];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) combine_stats(m, s, red_m[w], red_s[w]);
+  const float l = m + logf(s), zy = a.label_logit[r];
+  if (a.G) {
+    const float f = *a.factor;
+    const int y = a.label_c[r] - a.col0;
+    const float gy = (exp2_fast((zy - l) * kLog2eF) - 1.0f) * f;
+#pragma unroll
+    for (int u = 0; u < kSpanUnits; ++u) {
+      const int c = c0 + 2048 * u;
+      if (c >= c1) break;
+      const float tm = st[(a.col0 + c) / kTcTileN].x;
+      const float k = exp2_fast(((tm == -INFINITY ? 0.0f : tm) - l) * kLog2eF) * f;
+      const uint32_t in[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      uint32_t out[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x0 = __uint_as_float(in[i] << 16) * k, x1 = __uint_as_float(in[i] & 0xFFFF0000u) * k;
+        if (y == c + 2 * i) x0 = gy;
+        if (y == c + 2 * i + 1) x1 = gy;
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+        out[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(a.G + r * a.ldg + c) = make_uint4(out[0], out[1], out[2], out[3]);
+    }
+  }
+  if (blockIdx.y != 0) return;
   if (threadIdx.x == 0) {
+    a.lse[r] = l;
+    a.row_loss[r] = l - zy;
+    if (a.token_loss) a.token_loss[a.token[r]] = l - zy;
     __threadfence();
-    last = atomicAdd(counter, 1u) == gridDim.x - 1;
+    last = atomicAdd(a.counter, 1u) == (uint32_t)(n - 1);
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
-  __shared__ double sums[256];
-  __shared__ int64_t counts[256];
-  double a = 0.0;
-  int64_t c = 0;
-  for (int64_t i = threadIdx.x; i < N; i += 256) {
-    if (!labelled(labels[i], ignore, V)) continue;
-    ++c;
-    a += (double)__ldcg(row_loss + i);
-  }
-  sums[threadIdx.x] = a;
-  counts[threadIdx.x] = c;
-  __syncthreads();
-  for (int h = 128; h > 0; h >>= 1) {
-    if ((int)threadIdx.x < h) {
-      sums[threadIdx.x] += sums[threadIdx.x + h];
-      counts[threadIdx.x] += counts[threadIdx.x + h];
-    }
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) {
-    const double n = (double)counts[0];
-    *factor = n > 0 ? (float)(grad_scale / n) : 0.0f;
-    if (loss) *loss = n > 0 ? (float)(sums[0] / n) : 0.0f;
-  }
-}
-
-// G, holding exp(z - tile maximum), becomes the gradient: times
-// exp(tile maximum - lse) * factor; the label's column from its fp32 logit,
-// because exp(z - lse) - 1 cancels where the model is sure.  Eight columns a
-// thread; 4 bytes an element, against 2 D flops for computing z again.
-__global__ void __launch_bounds__(256) k_lce_rescale(__nv_bfloat16* __restrict__ G, int64_t ldg, int64_t rows, int cols,
-                                                     int col0, const float2* __restrict__ stats, int n_tiles,
-                                                     const float* __restrict__ lse,
-                                                     const float* __restrict__ label_logit,
-                                                     const int32_t* __restrict__ labels,
-                                                     const float* __restrict__ factor) {
-  const int j = 8 * (blockIdx.x * 256 + threadIdx.x);
-  if (j >= cols) return;
-  const float f = *factor;
-  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
-    uint4* p = reinterpret_cast<uint4*>(G + r * ldg + j);
-    const float l = lse[r];
-    if (l == INFINITY) {
-      *p = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    const uint4 w = *p;
-    const float m = stats[r * n_tiles + (col0 + j) / kTcTileN].x;
-    const float k = exp2_fast(((m == -INFINITY ? 0.0f : m) - l) * kLog2eF) * f;
-    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-    const int y = labels[r] - col0 - j;
-    uint32_t out[4];
+  __shared__ double sums[8];
+  double t = 0.0;
+  for (int i = threadIdx.x; i < n; i += 256) t += (double)__ldcg(a.row_loss + i);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float a = __uint_as_float(in[i] << 16) * k, b = __uint_as_float(in[i] & 0xFFFF0000u) * k;
-      if (y == 2 * i) a = (exp2_fast((label_logit[r] - l) * kLog2eF) - 1.0f) * f;
-      if (y == 2 * i + 1) b = (exp2_fast((label_logit[r] - l) * kLog2eF) - 1.0f) * f;
-      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-      out[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *p = make_uint4(out[0], out[1], out[2], out[3]);
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = t;
+  __syncthreads();
+  if (threadIdx.x == 0 && a.loss) {
+    t = 0.0;
+    for (int w = 0; w < 8; ++w) t += sums[w];
+    *a.loss = (float)(t / (double)n);
   }
 }
 
 // out [M][N] = sum over the parts [S][M][ld] in part order, rounded to bf16
-// or kept in fp32.  ld is a multiple of 4; out rows are 16-byte aligned.
-__global__ void __launch_bounds__(256) k_lce_sum_parts(const float* __restrict__ parts, int S, int64_t M, int64_t N,
-                                                       int64_t ld, void* __restrict__ out, int64_t ldo, int fp32) {
+// or kept in fp32; with `place`, out's row r is the parts' row place[r], zero
+// where that is -1.  ld is a multiple of 4; out rows are 16-byte aligned.
+__global__ void __launch_bounds__(256) k_lce_sum_parts(const float* parts, int S, int64_t M, int64_t N, int64_t ld,
+                                                       const int32_t* place, void* out, int64_t ldo, int fp32) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t per_row = (N + 3) / 4, total = M * per_row;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / per_row, c = 4 * (i - r * per_row);
-    float4 v = __ldcs(reinterpret_cast<const float4*>(parts + r * ld + c));
-    for (int s = 1; s < S; ++s) {
-      const float4 w = __ldcs(reinterpret_cast<const float4*>(parts + ((int64_t)s * M + r) * ld + c));
-      v.x += w.x;
-      v.y += w.y;
-      v.z += w.z;
-      v.w += w.w;
+    const int64_t from = place ? (int64_t)place[r] : r;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (from >= 0) {
+      v = __ldcs(reinterpret_cast<const float4*>(parts + from * ld + c));
+      for (int s = 1; s < S; ++s) {
+        const float4 w = __ldcs(reinterpret_cast<const float4*>(parts + ((int64_t)s * M + from) * ld + c));
+        v.x += w.x;
+        v.y += w.y;
+        v.z += w.z;
+        v.w += w.w;
+      }
     }
     const float x[4] = {v.x, v.y, v.z, v.w};
     const int n = (int)min((int64_t)4, N - c);
@@ -386,10 +513,11 @@ int pick_splits(int64_t M, int64_t N, int64_t K) {
 }
 
 struct VocabPlan {
-  int64_t pieces, piece, ldg, ldd;
+  int64_t pieces, piece, ldg, ldd, ldc;
   int n_tiles;
   int s_dh;                 // parts of dH's sum over a piece
-  size_t off_g, off_stats, off_lse, off_logit, off_loss, off_words, off_dh, off_dw, bytes;
+  bool dh_direct;           // dH goes to its rows from the product's epilogue
+  size_t off_h, off_g, off_stats, off_rows, off_words, off_dh, off_dw, bytes;
 };
 
 VocabPlan plan_vocab(int64_t N, int64_t D, int64_t V, int64_t piece) {
@@ -403,6 +531,7 @@ VocabPlan plan_vocab(int64_t N, int64_t D, int64_t V, int64_t piece) {
   p.piece = std::min(piece, V);
   p.ldg = ceil_div<int64_t>(p.piece, 64) * 64;
   p.ldd = ceil_div<int64_t>(D, 4) * 4;
+  p.ldc = ceil_div<int64_t>(D, 8) * 8;
   p.n_tiles = (int)ceil_div<int64_t>(V, kTcTileN);
   p.s_dh = pick_splits(N, D, p.piece);
   // the last piece may be shorter than a part count chosen for whole ones
@@ -414,16 +543,16 @@ VocabPlan plan_vocab(int64_t N, int64_t D, int64_t V, int64_t piece) {
     off = (off + bytes + 255) / 256 * 256;
     return o;
   };
+  p.dh_direct = p.pieces == 1 && p.s_dh == 1;
+  p.off_h = take((size_t)N * p.ldc * 2);
   p.off_g = take((size_t)N * p.ldg * 2);
   p.off_stats = take((size_t)N * p.n_tiles * 8);
-  p.off_lse = take((size_t)N * 4);
-  p.off_logit = take((size_t)N * 4);
-  p.off_loss = take((size_t)N * 4);
-  p.off_words = take(16);
-  // a product goes to its output straight from the epilogue only where the
-  // output's rows are whole 16-byte units: a tensor store writes whole ones
+  p.off_rows = take((size_t)N * 4 * 6);          // labels, tokens, places, label logits, lse, losses
+  p.off_words = take(16);                        // n, factor, counter
+  p.off_dh = take(p.dh_direct ? 0 : (size_t)p.s_dh * N * p.ldd * 4);
+  // dW goes to its rows straight from the epilogue only where they are whole
+  // 16-byte units: a tensor store writes whole ones
   const bool ragged = D % 8 != 0;
-  p.off_dh = take(p.pieces > 1 || p.s_dh > 1 || ragged ? (size_t)p.s_dh * N * p.ldd * 4 : 0);
   const int s1 = pick_splits(p.piece, D, N), s2 = pick_splits(last, D, N);
   p.off_dw = take(std::max(s1 > 1 || ragged ? (size_t)s1 * p.piece * p.ldd * 4 : 0,
                            s2 > 1 || ragged ? (size_t)s2 * last * p.ldd * 4 : 0));
@@ -431,12 +560,13 @@ VocabPlan plan_vocab(int64_t N, int64_t D, int64_t V, int64_t piece) {
   return p;
 }
 
-sf_status sum_parts(const float* parts, int S, int64_t M, int64_t N, int64_t ld, void* out, int64_t ldo, bool fp32,
-                    cudaStream_t s) {
+sf_status sum_parts(const float* parts, int S, int64_t M, int64_t N, int64_t ld, const int32_t* place, void* out,
+                    int64_t ldo, bool fp32, cudaStream_t s) {
   const int64_t want = ceil_div<int64_t>(M * ceil_div<int64_t>(N, 4), 256);
-  k_lce_sum_parts<<<(unsigned)std::min<int64_t>(want, (int64_t)sm_count() * 8), 256, 0, s>>>(parts, S, M, N, ld, out,
-                                                                                         ldo, fp32);
-  return check_launch("k_lce_sum_parts");
+  SF_CUDA_TRY(launch_pdl(k_lce_sum_parts, dim3((unsigned)std::min<int64_t>(want, (int64_t)sm_count() * 8)), dim3(256), 0, s,
+                         parts, S, M, N, ld, place, out, ldo, (int)fp32),
+              "launch k_lce_sum_parts");
+  return SF_OK;
 }
 
 }  // namespace
@@ -548,28 +678,68 @@ sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W, con
   const VocabPlan p = plan_vocab(N, D, V, piece);
   if (!ws || ws_bytes < p.bytes || reinterpret_cast<uintptr_t>(ws) % 256)
     return fail(SF_ERR_INVALID, "workspace needs %zu bytes, 256-byte aligned (got %zu)", p.bytes, ws_bytes);
+  if (!tensor_map_encoder()) return fail(SF_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled is not available");
+  // tensor maps and bulk stores may only address this device's own memory
+  const void* const dev[5] = {H->data, W->data, ws, dH ? dH->data : ws, dW ? dW->data : ws};
+  for (const void* q : dev)
+    if (!on_current_device(q))
+      return fail(SF_ERR_INVALID, "H, W, dH, dW and the workspace must be device memory of the current device");
   cudaStream_t s = as_stream(stream_);
   char* w = static_cast<char*>(ws);
+  uint16_t* Hc = reinterpret_cast<uint16_t*>(w + p.off_h);
   __nv_bfloat16* G = reinterpret_cast<__nv_bfloat16*>(w + p.off_g);
   float2* stats = reinterpret_cast<float2*>(w + p.off_stats);
-  float* lse = reinterpret_cast<float*>(w + p.off_lse);
-  float* label_logit = reinterpret_cast<float*>(w + p.off_logit);
-  float* row_loss = reinterpret_cast<float*>(w + p.off_loss);
-  float* factor = reinterpret_cast<float*>(w + p.off_words);
-  uint32_t* counter = reinterpret_cast<uint32_t*>(w + p.off_words + 4);
+  int32_t* label_c = reinterpret_cast<int32_t*>(w + p.off_rows);
+  int32_t* token = label_c + N;
+  int32_t* place = token + N;
+  float* label_logit = reinterpret_cast<float*>(place + N);
+  float* lse = label_logit + N;
+  float* row_loss = lse + N;
+  int32_t* n_dev = reinterpret_cast<int32_t*>(w + p.off_words);
+  float* factor = reinterpret_cast<float*>(n_dev + 1);
+  uint32_t* counter = reinterpret_cast<uint32_t*>(n_dev + 2);
   float* acc_dh = reinterpret_cast<float*>(w + p.off_dh);
   float* acc_dw = reinterpret_cast<float*>(w + p.off_dw);
   const uint16_t* Wb = static_cast<const uint16_t*>(W->data);
   const bool grads = dH || dW;
 
+  GatherArgs ga{};
+  ga.H = static_cast<const uint16_t*>(H->data);
+  ga.ldh = H->ld;
+  ga.N = N;
+  ga.D = D;
+  ga.V = V;
+  ga.labels = labels;
+  ga.ignore = ignore_index;
+  ga.grad_scale = grad_scale;
+  ga.Hc = Hc;
+  ga.ldc = p.ldc;
+  ga.label_c = label_c;
+  ga.token = token;
+  ga.place = place;
+  ga.n_out = n_dev;
+  ga.factor = factor;
+  ga.counter = counter;
+  ga.loss = loss;
+  ga.token_loss = token_loss;
+  if (dH && p.dh_direct) {
+    ga.dH = dH->data;
+    ga.lddh = dH->ld;
+    ga.dh_fp32 = dH->dtype == SF_FP32;
+  }
+  k_lce_gather<<<(unsigned)ceil_div<int64_t>(N, 8), 256, 0, s>>>(ga);
+  SF_TRY(check_launch("k_lce_gather"));
+
   // the logits of columns [v0, v0 + cols)
   TcJob z;
-  z.A = H->data;
-  z.lda = H->ld;
+  z.checked = z.chained = true;
+  z.A = Hc;
+  z.lda = p.ldc;
   z.ldb = W->ld;
   z.M = N;
+  z.m_dev = n_dev;
   z.K = D;
-  z.labels = labels;
+  z.labels = label_c;
   z.C = G;
   z.ldc = p.ldg;
   z.row_stats = stats;
@@ -580,7 +750,6 @@ sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W, con
   const int64_t last0 = (p.pieces - 1) * p.piece;      // the last piece's first column
   const int64_t kept0 = grads ? last0 : V;             // columns from here on keep their exponentials
   z.epi = kTcStats;
-  z.zero = counter;
   if (kept0 > 0) {
     z.B = Wb;
     z.N = kept0;
@@ -593,23 +762,38 @@ sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W, con
     z.store = true;
     SF_TRY(tc_gemm(z, s));
   }
-  k_lce_finish<<<(unsigned)ceil_div<int64_t>(N, 8), 256, 0, s>>>(stats, p.n_tiles, N, V, label_logit, labels,
-                                                                 ignore_index, grad_scale, lse, row_loss, token_loss,
-                                                                 factor, loss, counter);
-  SF_TRY(check_launch("k_lce_finish"));
+  RowsArgs ra{};
+  ra.stats = stats;
+  ra.n_tiles = p.n_tiles;
+  ra.n_dev = n_dev;
+  ra.label_logit = label_logit;
+  ra.label_c = label_c;
+  ra.token = token;
+  ra.factor = factor;
+  ra.lse = lse;
+  ra.row_loss = row_loss;
+  ra.token_loss = token_loss;
+  ra.loss = loss;
+  ra.counter = counter;
+  ra.N = N;
+  ra.span = 2048;
+  int64_t spans = 1;
+  if (grads) {
+    ra.G = G;
+    ra.ldg = p.ldg;
+    ra.cols = (int32_t)(V - kept0);
+    ra.col0 = (int32_t)kept0;
+    // few rows: short spans, so that there are blocks for every SM
+    while (ra.span < 2048 * kSpanUnits && N * ceil_div<int64_t>(ra.cols, 2 * ra.span) >= 1024) ra.span *= 2;
+    spans = ceil_div<int64_t>(ra.cols, ra.span);
+  }
+  SF_CUDA_TRY(launch_pdl(k_lce_rows, dim3((unsigned)N, (unsigned)spans), dim3(256), 0, s, ra), "launch k_lce_rows");
   if (!grads) return SF_OK;
 
-  auto whole = [&](const sf_matrix* m) { return D * (int64_t)dtype_bytes(m->dtype) % 16 == 0; };
-  const bool dh_direct = dH && p.s_dh == 1 && (p.pieces == 1 || dH->dtype == SF_FP32) && whole(dH);
   for (int64_t q = p.pieces - 1; q >= 0; --q) {
     const int64_t v0 = q * p.piece, cols = std::min(p.piece, V - v0);
     const bool first = q == p.pieces - 1;
-    if (first) {
-      const dim3 grid((unsigned)ceil_div<int64_t>(cols, 2048), (unsigned)std::min<int64_t>(N, 65535));
-      k_lce_rescale<<<grid, 256, 0, s>>>(G, p.ldg, N, (int)cols, (int)v0, stats, p.n_tiles, lse, label_logit, labels,
-                                         factor);
-      SF_TRY(check_launch("k_lce_rescale"));
-    } else {
+    if (!first) {
       z.epi = kTcGrad;
       z.B = Wb + v0 * W->ld;
       z.N = cols;
@@ -619,43 +803,55 @@ sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W, con
     if (dH) {
       // dH += G W_piece: W is [K = cols][N = D] as stored
       TcJob j;
+      j.checked = j.chained = true;
       j.A = G;
       j.lda = p.ldg;
       j.B = Wb + v0 * W->ld;
       j.ldb = W->ld;
       j.b_mn = true;
       j.M = N;
+      j.m_dev = n_dev;
       j.N = D;
       j.K = cols;
-      j.accumulate = !first;
-      if (dh_direct) {
-        j.epi = dH->dtype == SF_FP32 ? kTcF32 : kTcBf16;
+      if (p.dh_direct) {
+        j.epi = kTcRows;
+        j.row_map = token;
+        j.out_fp32 = dH->dtype == SF_FP32;
         j.C = dH->data;
         j.ldc = dH->ld;
       } else {
         j.epi = kTcSplit;
         j.splits = p.s_dh;
+        j.accumulate = !first;
         j.C = acc_dh;
         j.ldc = p.ldd;
       }
       SF_TRY(tc_gemm(j, s));
     }
     if (dW) {
-      // dW_piece = G^T H: G is [K = N][M = cols], H is [K = N][N = D] as stored
+      // dW_piece = G^T H: G is [K = n][M = cols], H is [K = n][N = D] as stored
       TcJob j;
+      j.checked = j.chained = true;
       j.A = G;
       j.lda = p.ldg;
       j.a_mn = true;
-      j.B = H->data;
-      j.ldb = H->ld;
+      j.B = Hc;
+      j.ldb = p.ldc;
       j.b_mn = true;
       j.M = cols;
       j.N = D;
       j.K = N;
+      j.k_dev = n_dev;
+      const bool fp32 = dW->dtype == SF_FP32;
       void* out = static_cast<char*>(dW->data) + v0 * dW->ld * (int64_t)dtype_bytes(dW->dtype);
       j.splits = pick_splits(cols, D, N);
-      if (j.splits == 1 && whole(dW)) {
-        j.epi = dW->dtype == SF_FP32 ? kTcF32 : kTcBf16;
+      if (j.splits == 1 && !fp32 && D % 8 == 0) {
+        j.epi = kTcBf16;
+        j.C = out;
+        j.ldc = dW->ld;
+        SF_TRY(tc_gemm(j, s));
+      } else if (j.splits == 1 && fp32 && D % 4 == 0) {
+        j.epi = kTcSplit;            // one part, straight to its place
         j.C = out;
         j.ldc = dW->ld;
         SF_TRY(tc_gemm(j, s));
@@ -664,12 +860,12 @@ sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W, con
         j.C = acc_dw;
         j.ldc = p.ldd;
         SF_TRY(tc_gemm(j, s));
-        SF_TRY(sum_parts(acc_dw, j.splits, cols, D, p.ldd, out, dW->ld, dW->dtype == SF_FP32, s));
+        SF_TRY(sum_parts(acc_dw, j.splits, cols, D, p.ldd, nullptr, out, dW->ld, fp32, s));
       }
     }
   }
-  if (dH && !dh_direct)
-    SF_TRY(sum_parts(acc_dh, p.s_dh, N, D, p.ldd, dH->data, dH->ld, dH->dtype == SF_FP32, s));
+  if (dH && !p.dh_direct)
+    SF_TRY(sum_parts(acc_dh, p.s_dh, N, D, p.ldd, place, dH->data, dH->ld, dH->dtype == SF_FP32, s));
   return SF_OK;
 }
 

@@ -244,7 +244,10 @@ struct TcGemmArgs {
   float* label_logit;    // [M]: receives C at each row's label (kTcStats)
   const float* lse;      // [M] (kTcGrad)
   const float* factor;   // one value (kTcGrad)
-  uint32_t* zero;        // set to 0 by the launch (kTcStats)
+  const int32_t* m_dev;  // device-side M (<= M) and K (<= K) where not null
+  const int32_t* k_dev;
+  const int32_t* row_map;  // kTcRows: C's row of each product row
+  int32_t out_fp32;        // kTcRows: C is fp32 (else bf16)
 };
 
 // Folds 32 values of a row into a running (max, sum of exp(x - max)):
@@ -309,6 +312,7 @@ __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, uint32
 //   kTcF32    C (fp32) stored or added to, optional row statistics;
 //   kTcSplit  fp32 partial products [splits][M][N], stored or added to;
 //   kTcBf16   C rounded to bf16;
+//   kTcRows   C in bf16 or fp32, row i of the product to row row_map[i];
 //   kTcStats  per row and tile the maximum and sum of exponentials, the
 //             label's logit, and optionally exp(c - maximum) in bf16: the
 //             logits themselves never leave tensor memory;
@@ -333,18 +337,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();              // 0: issues the MMAs, 1: its peer
   const int pair = blockIdx.x / kPair, n_pairs = gridDim.x / kPair;
-  const int nk_all = (g.K + kBK - 1) / kBK;
-  const int m_tiles = (g.M + kPair * kBM - 1) / (kPair * kBM);   // 256-row tiles
-  const int n_tiles = (g.N + kBN - 1) / kBN;
-  const int tiles = m_tiles * n_tiles;
-  // work items: the tiles, once per part of K; part p takes the K slabs
-  // [nk_all p / splits, nk_all (p + 1) / splits)
-  const int splits = EPI == kTcSplit ? g.splits : 1;
-  const int items = tiles * splits;
-  auto slab0 = [&](int part) { return EPI == kTcSplit ? (int)((int64_t)nk_all * part / splits) : 0; };
-  auto slab1 = [&](int part) { return EPI == kTcSplit ? (int)((int64_t)nk_all * (part + 1) / splits) : nk_all; };
-
-  if (EPI == kTcStats && blockIdx.x == 0 && threadIdx.x == 0 && g.zero) *g.zero = 0;
   if (threadIdx.x == 0) {
     prefetch_tensormap(&map_a);
     prefetch_tensormap(&map_b);
@@ -367,13 +359,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  griddep_launch_dependents();           // (a no-op unless the next launch asks for it)
+  griddep_wait();                        // what earlier launches wrote is visible from here on
+  const int M = g.m_dev ? *g.m_dev : g.M, K = g.k_dev ? *g.k_dev : g.K;
+  const int nk_all = (K + kBK - 1) / kBK;
+  const int m_tiles = (M + kPair * kBM - 1) / (kPair * kBM);   // 256-row tiles
+  const int n_tiles = (g.N + kBN - 1) / kBN;
+  const int tiles = m_tiles * n_tiles;
+  // work items: the tiles, once per part of K; part p takes the K slabs
+  // [nk_all p / splits, nk_all (p + 1) / splits)
+  const int splits = EPI == kTcSplit ? g.splits : 1;
+  const int items = tiles * splits;
+  auto slab0 = [&](int part) { return EPI == kTcSplit ? (int)((int64_t)nk_all * part / splits) : 0; };
+  auto slab1 = [&](int part) { return EPI == kTcSplit ? (int)((int64_t)nk_all * (part + 1) / splits) : nk_all; };
+
+
   // tiles t = pair, + n_pairs, ...; the index runs fastest along the
   // dimension whose operand is the smaller one, so the pairs working at the
   // same time share the tile of the larger operand and it streams from
   // memory about once, while the smaller one is re-read from L2
   if (warp == 0) {
     if (lane == 0) {
-      griddep_wait();
       const uint32_t full_lead = cluster_addr(smem_u32(full), 0);
       int s = 0, issued = 0;
       uint32_t pass = 0;
@@ -477,10 +483,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tc_fence_after();
       const uint32_t acc = tmem + (uint32_t)(b * kTmemCols) + lane_off;
       const int row = m0 + 32 * quarter + lane;
+      const bool empty = slab0(part) >= slab1(part);     // nothing to sum: the accumulator was not written
       if constexpr (EPI == kTcStats || EPI == kTcGrad || EPI == kTcBf16) {
         // 32 x 64 bf16 boxes through the same two staging buffers per warp
         const int row0 = m0 + 32 * quarter;
-        const bool row_on = row < g.M;
+        const bool row_on = row < M;
         float ref = 0.0f, sum = 0.0f, f = 0.0f;
         int label = -1;                    // the label's column within the tile, if it is one
         if constexpr (EPI != kTcBf16) {
@@ -521,7 +528,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           tmem_ld_wait();
           if constexpr (EPI == kTcBf16) {
 #pragma unroll
-            for (int jj = 0; jj < 32; ++jj) x[jj] = g.alpha * __uint_as_float(r[jj]);
+            for (int jj = 0; jj < 32; ++jj) x[jj] = empty ? 0.0f : g.alpha * __uint_as_float(r[jj]);
           } else {
 #pragma unroll
             for (int jj = 0; jj < 32; ++jj) x[jj] = exp2_approx((__uint_as_float(r[jj]) - ref) * kLog2e);
@@ -556,7 +563,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             __syncwarp();
             if (lane == 0) {
               const int col = n0 + c0 - 32;
-              if (row0 < g.M && col < g.N) tma_store_2d(&map_c, buf, col, row0);
+              // a gradient's rows are also read as whole K slabs of 64: zeros past M
+              const int rows = EPI == kTcGrad ? (M + 63) & ~63 : M;
+              if (row0 < rows && col < g.N) tma_store_2d(&map_c, buf, col, row0);
               bulk_commit();
             }
             __syncwarp();
@@ -573,6 +582,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           uint32_t r[32];
           tmem_ld32(acc + (uint32_t)(32 * ci), r);
           tmem_ld_wait();
+          if (empty) {
+#pragma unroll
+            for (int jj = 0; jj < 32; ++jj) r[jj] = 0;
+          }
           const uint32_t buf = stg + (uint32_t)(boxes & 1) * 4096u;
           if (boxes >= 2) {
             if (lane == 0) bulk_wait_read_1();
@@ -586,13 +599,52 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (row0 < g.M && n0 + 32 * ci < g.N) {
+            if (row0 < M && n0 + 32 * ci < g.N) {
               if (g.accumulate) tma_reduce_add_3d(&map_c, buf, n0 + 32 * ci, row0, part);
               else tma_store_3d(&map_c, buf, n0 + 32 * ci, row0, part);
             }
             bulk_commit();
           }
           __syncwarp();
+        }
+      } else if constexpr (EPI == kTcRows) {
+        // each lane writes its own row's 32 columns: 64 or 128 consecutive bytes
+        const bool row_on = row < M;
+        const int64_t dst = row_on ? (int64_t)g.row_map[row] * g.ldc : 0;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kBN; c0 += 32) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld32(acc + (uint32_t)c0, r);
+          tmem_ld_wait();
+          const int col = n0 + c0, n = min(32, g.N - col);
+          if (!row_on || n <= 0) continue;
+          if (g.out_fp32) {
+            float* p = g.C + dst + col;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 v = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                           __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+              if (4 * q + 4 <= n) *reinterpret_cast<float4*>(p + 4 * q) = v;
+            }
+#pragma unroll
+            for (int jj = 0; jj < 32; ++jj)
+              if (jj >= (n & ~3) && jj < n) p[jj] = __uint_as_float(r[jj]);
+          } else {
+            __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(g.C) + dst + col;
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+              w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (8 * q + 8 <= n) *reinterpret_cast<uint4*>(p + 8 * q) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+#pragma unroll
+            for (int jj = 0; jj < 32; ++jj)
+              if (jj >= (n & ~7) && jj < n) p[jj] = __float2bfloat16_rn(__uint_as_float(r[jj]));
+          }
         }
       } else if (g.tma) {
         // 32 x 32 boxes through two 4 KB staging buffers per warp, 128-byte
@@ -827,7 +879,7 @@ sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
     return fail(SF_ERR_UNSUPPORTED, "A and B need 16-byte aligned bases and rows (lda, ldb multiples of 8)");
   if (!tensor_map_encoder()) return fail(SF_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled is not available");
   // the tensor maps below may only address this device's own memory
-  if (!on_current_device(j.A) || !on_current_device(j.B) || (writes && !on_current_device(j.C)))
+  if (!j.checked && (!on_current_device(j.A) || !on_current_device(j.B) || (writes && !on_current_device(j.C))))
     return fail(SF_ERR_INVALID, "A, B and C must be device memory of the current device");
   CUtensorMap ma, mb;
   int a_form = 0, b_form = 0;      // 0 K-major, 1 MN-major in 2D boxes, 2 MN-major in 3D boxes
@@ -863,7 +915,10 @@ sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
   g.label_logit = j.label_logit;
   g.lse = j.lse;
   g.factor = j.factor;
-  g.zero = j.zero;
+  g.m_dev = j.m_dev;
+  g.k_dev = j.k_dev;
+  g.row_map = j.row_map;
+  g.out_fp32 = j.out_fp32 ? 1 : 0;
   const bool c_aligned = reinterpret_cast<uintptr_t>(j.C) % 16 == 0;
   CUtensorMap mc = ma;       // unused unless C is written by tensor stores
   const void* kernel = nullptr;
@@ -879,6 +934,10 @@ sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
       if (j.ldc % 4 || !c_aligned) return fail(SF_ERR_UNSUPPORTED, "partial products need 16-byte aligned rows");
       SF_TRY(make_map_split(&mc, g.C, j.M, j.N, j.ldc, j.splits));
       kernel = reinterpret_cast<const void*>(&k_tc_gemm<kTcSplit>);
+      break;
+    case kTcRows:
+      if (!c_aligned || j.ldc * (j.out_fp32 ? 4 : 2) % 16) return fail(SF_ERR_UNSUPPORTED, "C needs 16-byte aligned rows");
+      kernel = reinterpret_cast<const void*>(&k_tc_gemm<kTcRows>);
       break;
     case kTcBf16:
     case kTcGrad:
@@ -896,11 +955,13 @@ sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
   const int64_t items = ((j.M + kPair * kBM - 1) / (kPair * kBM)) * ((j.N + kBN - 1) / kBN) * g.splits;
   if (items > INT32_MAX) return fail(SF_ERR_UNSUPPORTED, "too many tiles");
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kPair;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = kGemmSmem;
   cfg.stream = s;
@@ -908,6 +969,7 @@ sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
   cfg.numAttrs = 1;
   int pairs = 0;
   SF_TRY(resident_pairs(&cfg, &pairs));
+  if (j.chained) cfg.numAttrs = 2;
   cfg.gridDim = dim3((unsigned)(kPair * std::min<int64_t>(items, pairs)));
   void* args[] = {&ma, &mb, &mc, &g};
   SF_CUDA_TRY(cudaLaunchKernelExC(&cfg, kernel, args), "launch k_tc_gemm");

@@ -164,6 +164,34 @@ def test_unlabelled_ids_and_bad_labels():
     _check(H, W, bad, out)
 
 
+def _run_prepared(H, W, y, piece):
+    N, D, V = H.shape[0], H.shape[1], W.shape[0]
+    wsb = native.lce_vocab_workspace_bytes(N, D, V, piece)
+    ws = torch.full((wsb,), 0xFF, dtype=torch.uint8, device=DEV)
+    out = (torch.empty(1, device=DEV), torch.empty(N, device=DEV), torch.empty(N, D, dtype=BF, device=DEV),
+           torch.empty(V, D, dtype=BF, device=DEV))
+    native.lce_vocab_forward_backward(H.to(DEV), W.to(DEV), y.to(DEV), loss=out[0], token_loss=out[1], dH=out[2], dW=out[3],
+                                      ws=ws, piece=piece)
+    native.sf_sync_status()
+    return out
+
+
+@pytest.mark.parametrize("N,labelled", [(1000, 1), (1000, 64), (1000, 65), (1000, 97), (1000, 257), (513, 512), (70, 70)])
+@pytest.mark.parametrize("piece", [0, 256])
+def test_mostly_unlabelled_tokens(N, labelled, piece):
+    # prompts masked out: the labelled tokens alone count, wherever they stand; what the others hold reaches nothing
+    D, V = 72, 700
+    H, W, y = _case(N, D, V, labelled + N, N - labelled)
+    clean = _run_prepared(H, W, y, piece)
+    _check(H, W, y, clean)
+    off = y == -100
+    bad = H.clone()
+    bad[off] = float("nan")
+    bad[off.nonzero()[::2, 0]] = float("inf")
+    for a, b in zip(clean, _run_prepared(bad, W, y, piece)):
+        assert torch.equal(a, b)
+
+
 def test_outputs_left_out_grad_scale_and_repeatability():
     H, W, y = _case(300, 128, 1500, 21, 30)
     full = _run(H, W, y, 512)
