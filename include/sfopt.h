@@ -472,9 +472,9 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum,
  *            (ld a multiple of 8); any N, D, V >= 1.
  *   labels : device int32 [N]; ignore_index and labels outside [0, V) as in
  *            lce_forward_backward.
- *   piece  : vocabulary rows per piece, a multiple of 256; 0: as many as 512
- *            MB of workspace hold (at least 2048).  Larger pieces compute
- *            fewer logits twice; the last piece's never are.
+ *   piece  : vocabulary rows per piece, a multiple of 256; 0: as many as 1 GiB
+ *            of bf16 holds (at least 2048).  Larger pieces compute fewer
+ *            logits twice; the last piece's never are.
  *   grad_scale : multiplies dH and dW (1 for the loss's own gradient; 1 / k
  *            for one of k accumulated micro-batches), not the losses.
  *   loss   : device fp32 [1]: mean over the labelled tokens (0 if none), or NULL.

@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       const uint32_t full_lead = cluster_addr(smem_u32(full), 0);
+      const int a_mn = g.a_mn, b_mn = g.b_mn;
       int s = 0, issued = 0;
       uint32_t pass = 0;
       bool failed = false;
@@ -398,17 +399,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(kPair * kStageBytes));
           const uint32_t st = smem_base + (uint32_t)s * kStageBytes;
           const uint32_t bar = full_lead + 8u * (uint32_t)s;
-          if (g.a_mn == 2) {
+          if (a_mn == 2) {
             tma_load_3d_pair(st, &map_a, bar, 0, kb * kBK, m0 >> 6);
-          } else if (g.a_mn) {
+          } else if (a_mn) {
             tma_load_2d_pair(st, &map_a, bar, m0, kb * kBK);
             tma_load_2d_pair(st + kMnBox, &map_a, bar, m0 + 64, kb * kBK);
           } else {
             tma_load_2d_pair(st, &map_a, bar, kb * kBK, m0);
           }
-          if (g.b_mn == 2) {
+          if (b_mn == 2) {
             tma_load_3d_pair(st + kStageA, &map_b, bar, 0, kb * kBK, nb >> 6);
-          } else if (g.b_mn) {
+          } else if (b_mn) {
             tma_load_2d_pair(st + kStageA, &map_b, bar, nb, kb * kBK);
             tma_load_2d_pair(st + kStageA + kMnBox, &map_b, bar, nb + 64, kb * kBK);
           } else {
@@ -432,8 +433,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (lane == 0 && rank == 0) {
       // K-16 step in descriptor units (16 bytes): 32 bytes along a K-major
       // row, 16 rows of 128 bytes down an MN-major box
-      const uint32_t a_step = g.a_mn ? 128u : 2u, b_step = g.b_mn ? 128u : 2u;
-      const uint32_t idesc = kIdesc | ((g.a_mn ? 1u : 0u) << 15) | ((g.b_mn ? 1u : 0u) << 16);
+      const bool a_mn = g.a_mn != 0, b_mn = g.b_mn != 0;
+      const uint32_t a_step = a_mn ? 128u : 2u, b_step = b_mn ? 128u : 2u;
+      const uint32_t idesc = kIdesc | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16);
       int s = 0, j = 0;
       uint32_t pass = 0;
       bool failed = false;
@@ -452,8 +454,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
           tc_fence_after();
           const uint32_t a_addr = smem_base + (uint32_t)s * kStageBytes;
-          const uint64_t adesc = g.a_mn ? umma_desc_mn_sw128(a_addr) : umma_desc_sw128(a_addr);
-          const uint64_t bdesc = g.b_mn ? umma_desc_mn_sw128(a_addr + kStageA) : umma_desc_sw128(a_addr + kStageA);
+          const uint64_t adesc = a_mn ? umma_desc_mn_sw128(a_addr) : umma_desc_sw128(a_addr);
+          const uint64_t bdesc = b_mn ? umma_desc_mn_sw128(a_addr + kStageA) : umma_desc_sw128(a_addr + kStageA);
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
             tc_mma(d_tmem, adesc + a_step * (uint32_t)k, bdesc + b_step * (uint32_t)k, idesc, kb != k0 || k != 0 ? 1u : 0u);
