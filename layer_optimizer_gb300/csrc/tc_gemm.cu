@@ -927,7 +927,9 @@ sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
   switch (j.epi) {
     case kTcF32:
       g.vec = j.ldc % 4 == 0 && c_aligned ? 1 : 0;
-      g.tma = g.vec;
+      // a tensor store writes whole 16-byte units: past a ragged N it would
+      // reach the padding of C's rows
+      g.tma = g.vec && j.N % 4 == 0 ? 1 : 0;
       if (g.tma) SF_TRY(make_map_c(&mc, g.C, j.M, j.N, j.ldc));
       kernel = reinterpret_cast<const void*>(&k_tc_gemm<kTcF32>);
       break;
