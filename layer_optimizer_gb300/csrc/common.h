@@ -144,7 +144,7 @@ enum TcEpilogue : int {
   kTcBf16 = 2,   // C bf16
   kTcStats = 3,  // row_stats, label_logit, and with `store` C = exp(A B^T - tile maximum) in bf16
   kTcRows = 5,   // C bf16 or fp32, product row i written to row row_map[i]
-  kTcGrad = 4    // C = (exp(A B^T - lse) - onehot(label)) * factor in bf16; 0 where lse is +infinity
+  kTcGrad = 4    // C = exp(A B^T - lse) - onehot(label) in bf16, 0 in rows past M
 };
 struct TcJob {
   const void* A = nullptr;
@@ -164,7 +164,7 @@ struct TcJob {
   const int32_t* labels = nullptr; // [M] (kTcStats, kTcGrad); ids outside the product's columns match nothing
   float* label_logit = nullptr;    // [M]
   const float* lse = nullptr;      // [M]
-  const float* factor = nullptr;   // device, one value
+  const float* scale = nullptr;    // device, one value: multiplies alpha (kTcSplit, kTcBf16, kTcRows)
   const int32_t* m_dev = nullptr;  // device-side M and K, at most the M and K above (not for kTcF32); an empty
   const int32_t* k_dev = nullptr;  // sum gives zeros
   const int32_t* row_map = nullptr;  // [M] (kTcRows)

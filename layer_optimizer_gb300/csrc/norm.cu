@@ -101,12 +101,13 @@ __device__ __forceinline__ float row_reduce(float v, int tpr, float* red) {
   return t;
 }
 
-// A group's scale and its reciprocal (of the exponential unit's neighbour:
-// within an ulp, far below e4m3's 2^-4 steps; 2^-126 and infinity included).
+// A group's scale, and its reciprocal from the maximum itself: one rounding
+// and not two, so that h times it is as near to h / scale as a division.  (The
+// scale, to which nothing is rounded, does without a second division.)
 __device__ __forceinline__ float group_scale(float amax, float* inv) {
-  const float s = max_nan(amax * (1.0f / 448.0f), 1.17549435e-38f);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(*inv) : "f"(s));
-  return s;
+  amax = max_nan(amax, 448.0f * 1.17549435e-38f);
+  *inv = __fdiv_rn(448.0f, amax);
+  return max_nan(amax * (1.0f / 448.0f), 1.17549435e-38f);
 }
 
 template <typename TA, typename TS, bool VEC>

@@ -243,7 +243,7 @@ struct TcGemmArgs {
   const int32_t* labels; // [M]
   float* label_logit;    // [M]: receives C at each row's label (kTcStats)
   const float* lse;      // [M] (kTcGrad)
-  const float* factor;   // one value (kTcGrad)
+  const float* scale;    // kTcSplit, kTcBf16, kTcRows: one device value that multiplies alpha (may be null)
   const int32_t* m_dev;  // device-side M (<= M) and K (<= K) where not null
   const int32_t* k_dev;
   const int32_t* row_map;  // kTcRows: C's row of each product row
@@ -316,8 +316,7 @@ __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, uint32
 //   kTcStats  per row and tile the maximum and sum of exponentials, the
 //             label's logit, and optionally exp(c - maximum) in bf16: the
 //             logits themselves never leave tensor memory;
-//   kTcGrad   (exp(c - lse) - [column is the label]) * factor in bf16, 0 for
-//             an unlabelled row.
+//   kTcGrad   exp(c - lse) - [column is the label] in bf16, 0 in rows past M.
 template <int EPI>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_tc_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -486,20 +485,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const uint32_t acc = tmem + (uint32_t)(b * kTmemCols) + lane_off;
       const int row = m0 + 32 * quarter + lane;
       const bool empty = slab0(part) >= slab1(part);     // nothing to sum: the accumulator was not written
+      const float alpha = EPI != kTcF32 && g.scale ? g.alpha * *g.scale : g.alpha;
       if constexpr (EPI == kTcStats || EPI == kTcGrad || EPI == kTcBf16) {
         // 32 x 64 bf16 boxes through the same two staging buffers per warp
         const int row0 = m0 + 32 * quarter;
         const bool row_on = row < M;
-        float ref = 0.0f, sum = 0.0f, f = 0.0f;
+        float ref = 0.0f, sum = 0.0f;
         int label = -1;                    // the label's column within the tile, if it is one
         if constexpr (EPI != kTcBf16) {
           if (row_on) label = (int)((uint32_t)g.labels[row] - (uint32_t)(g.col0 + n0));
         }
-        if constexpr (EPI == kTcGrad) {
-          // lse = +infinity marks an unlabelled row
-          ref = row_on ? g.lse[row] : INFINITY;
-          f = *g.factor;
-        }
+        if constexpr (EPI == kTcGrad) ref = row_on ? g.lse[row] : INFINITY;      // exp(-infinity) = 0 past M
         if constexpr (EPI == kTcStats) {
           float m = -INFINITY;
 #pragma unroll 1
@@ -530,7 +526,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           tmem_ld_wait();
           if constexpr (EPI == kTcBf16) {
 #pragma unroll
-            for (int jj = 0; jj < 32; ++jj) x[jj] = empty ? 0.0f : g.alpha * __uint_as_float(r[jj]);
+            for (int jj = 0; jj < 32; ++jj) x[jj] = empty ? 0.0f : alpha * __uint_as_float(r[jj]);
           } else {
 #pragma unroll
             for (int jj = 0; jj < 32; ++jj) x[jj] = exp2_approx((__uint_as_float(r[jj]) - ref) * kLog2e);
@@ -550,7 +546,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                   if (label - c0 == jj) x[jj] -= 1.0f;
               }
 #pragma unroll
-              for (int jj = 0; jj < 32; ++jj) x[jj] = ref == INFINITY ? 0.0f : x[jj] * f;
+              for (int jj = 0; jj < 32; ++jj) x[jj] = row_on ? x[jj] : 0.0f;
             }
           }
           const int half = (c0 >> 5) & 1;
@@ -595,9 +591,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            sts_f4(buf + (uint32_t)lane * 128u + (uint32_t)((q ^ (lane & 7)) * 16), g.alpha * __uint_as_float(r[4 * q]),
-                   g.alpha * __uint_as_float(r[4 * q + 1]), g.alpha * __uint_as_float(r[4 * q + 2]),
-                   g.alpha * __uint_as_float(r[4 * q + 3]));
+            sts_f4(buf + (uint32_t)lane * 128u + (uint32_t)((q ^ (lane & 7)) * 16), alpha * __uint_as_float(r[4 * q]),
+                   alpha * __uint_as_float(r[4 * q + 1]), alpha * __uint_as_float(r[4 * q + 2]),
+                   alpha * __uint_as_float(r[4 * q + 3]));
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -621,6 +617,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           tmem_ld_wait();
           const int col = n0 + c0, n = min(32, g.N - col);
           if (!row_on || n <= 0) continue;
+#pragma unroll
+          for (int jj = 0; jj < 32; ++jj) r[jj] = __float_as_uint(alpha * __uint_as_float(r[jj]));
           if (g.out_fp32) {
             float* p = g.C + dst + col;
 #pragma unroll
@@ -916,7 +914,7 @@ sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
   g.labels = j.labels;
   g.label_logit = j.label_logit;
   g.lse = j.lse;
-  g.factor = j.factor;
+  g.scale = j.scale;
   g.m_dev = j.m_dev;
   g.k_dev = j.k_dev;
   g.row_map = j.row_map;
