@@ -47,7 +47,15 @@ namespace sf {
 namespace {
 
 constexpr int kPair = 2;                       // CTAs per tile (cta_group::2)
-constexpr int kBM = 128, kBN = 256, kBK = 64, kStages = 6;
+constexpr int kBM = 128, kBN = 256, kBK = 64;
+// Ring stages, and epilogue staging boxes per warp.  A bf16 C is written at
+// twice the rows per byte and often after few K slabs (dW over few tokens), so
+// its epilogue bounds the tile: it gets 16 boxes in flight for one stage less.
+template <int EPI>
+struct TcStages {
+  static constexpr int kRing = EPI == kTcBf16 ? 5 : 6;
+  static constexpr int kBoxes = EPI == kTcBf16 ? 4 : 2;
+};
 constexpr int kBRows = kBN / kPair;            // rows of B held by one CTA
 constexpr int kStageA = kBM * kBK * 2;         // 16 KB
 constexpr int kStageB = kBRows * kBK * 2;      // 16 KB
@@ -55,8 +63,9 @@ constexpr int kStageBytes = kStageA + kStageB;
 constexpr int kMnBox = 64 * kBK * 2;           // an MN-major box: 64 MN x 64 K bf16 = 8 KB
 constexpr int kTmemCols = 256;                 // one accumulator; two are allocated
 constexpr int kGemmThreads = 192;
-constexpr int kStagingBytes = 4 * 2 * 4096;    // epilogue: 4 warps x 2 boxes of 32 x 32 fp32
-constexpr size_t kGemmSmem = (size_t)kStages * kStageBytes + kStagingBytes + 1024 + 256;
+// the ring and the epilogue's boxes of 4 KB (32 rows x 128 bytes) for 4 warps: the same for both shares
+constexpr size_t kGemmSmem = (size_t)6 * kStageBytes + 4 * 2 * 4096 + 1024 + 256;
+static_assert(kStageBytes == 4 * 2 * 4096, "one ring stage is worth two boxes a warp");
 
 // Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator
 // (bits 4-5 = 1), A and B bf16 (bits 7-9 and 10-12 = 1), A and B K-major
@@ -200,6 +209,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld_wait();
+// 64 columns, waited for once.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+  uint32_t (&lo)[32] = reinterpret_cast<uint32_t (&)[32]>(r[0]);
+  uint32_t (&hi)[32] = reinterpret_cast<uint32_t (&)[32]>(r[32]);
+  tmem_ld32(taddr, lo);
+  tmem_ld32(taddr + 32u, hi);
+  tmem_ld_wait();
+}
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // Tensor store / reduce-add of a shared-memory box into global memory
@@ -216,6 +234,8 @@ __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, uint32
                : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void bulk_wait_read_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -323,9 +343,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               const __grid_constant__ CUtensorMap map_c, const TcGemmArgs g) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  // [ring: kStages x (A 16 KB + B 16 KB)] [epilogue staging: 4 warps x 2 x 4 KB] [barriers]
+  constexpr int kStages = TcStages<EPI>::kRing, kBoxes = TcStages<EPI>::kBoxes;
+  // [ring: kStages x (A 16 KB + B 16 KB)] [epilogue staging: 4 warps x kBoxes x 4 KB] [barriers]
   unsigned char* staging = smem + (size_t)kStages * kStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kStagingBytes);   // used in the first CTA
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + 4 * kBoxes * 4096);   // used in the first CTA
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;     // [2] accumulator buffer b holds a finished tile
   uint64_t* tempty = tfull + 2;          // [2] both CTAs have read buffer b out (first CTA)
@@ -472,7 +493,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // CTA's half of the tile
     const int quarter = warp & 3;
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
-    const uint32_t stg = smem_u32(staging) + (uint32_t)(warp - 2) * 8192u;
+    const uint32_t stg = smem_u32(staging) + (uint32_t)(warp - 2) * (kBoxes * 4096u);
     const uint32_t tempty_lead = cluster_addr(smem_u32(tempty), 0);
     int j = 0, boxes = 0;
     for (int it = pair; it < items; it += n_pairs, ++j) {
@@ -487,7 +508,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const bool empty = slab0(part) >= slab1(part);     // nothing to sum: the accumulator was not written
       const float alpha = EPI != kTcF32 && g.scale ? g.alpha * *g.scale : g.alpha;
       if constexpr (EPI == kTcStats || EPI == kTcGrad || EPI == kTcBf16) {
-        // 32 x 64 bf16 boxes through the same two staging buffers per warp
+        // 32 x 64 bf16 boxes through the warp's staging buffers
         const int row0 = m0 + 32 * quarter;
         const bool row_on = row < M;
         float ref = 0.0f, sum = 0.0f;
@@ -499,18 +520,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if constexpr (EPI == kTcStats) {
           float m = -INFINITY;
 #pragma unroll 1
-          for (int c0 = 0; c0 < kBN; c0 += 32) {
-            uint32_t r[32];
+          for (int c0 = 0; c0 < kBN; c0 += 64) {
+            uint32_t r[64];
             __syncwarp();
-            tmem_ld32(acc + (uint32_t)c0, r);
-            tmem_ld_wait();
+            tmem_ld64(acc + (uint32_t)c0, r);
             const int valid = g.N - (n0 + c0);
 #pragma unroll
-            for (int jj = 0; jj < 32; ++jj)
+            for (int jj = 0; jj < 64; ++jj)
               if (jj < valid) m = fmaxf(m, __uint_as_float(r[jj]));
-            if ((unsigned)(label - c0) < 32u) {
+            if ((unsigned)(label - c0) < 64u) {
 #pragma unroll
-              for (int jj = 0; jj < 32; ++jj)
+              for (int jj = 0; jj < 64; ++jj)
                 if (label - c0 == jj) g.label_logit[row] = __uint_as_float(r[jj]);
             }
           }
@@ -518,57 +538,56 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (row_on) g.row_stats[(int64_t)row * g.stats_ld + (g.col0 + n0) / kBN].x = m;
         }
 #pragma unroll 1
-        for (int c0 = 0; c0 < kBN; c0 += 32) {
-          uint32_t r[32];
-          float x[32];
+        for (int c0 = 0; c0 < kBN; c0 += 64, ++boxes) {
+          uint32_t r[64];
           __syncwarp();
-          tmem_ld32(acc + (uint32_t)c0, r);
-          tmem_ld_wait();
-          if constexpr (EPI == kTcBf16) {
+          tmem_ld64(acc + (uint32_t)c0, r);
+          const uint32_t buf = stg + (uint32_t)(boxes % kBoxes) * 4096u;
+          const bool out = EPI != kTcStats || g.store;
+          if (out && boxes >= kBoxes) {
+            if (lane == 0) bulk_wait_read<kBoxes - 1>();
+            __syncwarp();
+          }
 #pragma unroll
-            for (int jj = 0; jj < 32; ++jj) x[jj] = empty ? 0.0f : alpha * __uint_as_float(r[jj]);
-          } else {
+          for (int half = 0; half < 2; ++half) {
+            const int c1 = c0 + 32 * half;
+            float x[32];
+            if constexpr (EPI == kTcBf16) {
 #pragma unroll
-            for (int jj = 0; jj < 32; ++jj) x[jj] = exp2_approx((__uint_as_float(r[jj]) - ref) * kLog2e);
-            if constexpr (EPI == kTcStats) {
-              // four short chains a chunk, then one addition per chunk
-              const int valid = g.N - (n0 + c0);
-              float part4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-              for (int jj = 0; jj < 32; ++jj)
-                if (jj < valid) part4[jj & 3] += x[jj];
-              sum += (part4[0] + part4[1]) + (part4[2] + part4[3]);
-              if (!g.store) continue;
+              for (int jj = 0; jj < 32; ++jj) x[jj] = empty ? 0.0f : alpha * __uint_as_float(r[32 * half + jj]);
             } else {
-              if ((unsigned)(label - c0) < 32u) {
+#pragma unroll
+              for (int jj = 0; jj < 32; ++jj) x[jj] = exp2_approx((__uint_as_float(r[32 * half + jj]) - ref) * kLog2e);
+              if constexpr (EPI == kTcStats) {
+                // four short chains a chunk, then one addition per chunk
+                const int valid = g.N - (n0 + c1);
+                float part4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int jj = 0; jj < 32; ++jj)
-                  if (label - c0 == jj) x[jj] -= 1.0f;
-              }
+                  if (jj < valid) part4[jj & 3] += x[jj];
+                sum += (part4[0] + part4[1]) + (part4[2] + part4[3]);
+              } else {
+                if ((unsigned)(label - c1) < 32u) {
 #pragma unroll
-              for (int jj = 0; jj < 32; ++jj) x[jj] = row_on ? x[jj] : 0.0f;
+                  for (int jj = 0; jj < 32; ++jj)
+                    if (label - c1 == jj) x[jj] -= 1.0f;
+                }
+#pragma unroll
+                for (int jj = 0; jj < 32; ++jj) x[jj] = row_on ? x[jj] : 0.0f;
+              }
             }
+            if (out) stage_bf16(buf, lane, half, x);
           }
-          const int half = (c0 >> 5) & 1;
-          const uint32_t buf = stg + (uint32_t)(boxes & 1) * 4096u;
-          if (half == 0 && boxes >= 2) {
-            if (lane == 0) bulk_wait_read_1();
-            __syncwarp();
+          if (!out) continue;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            // a gradient's rows are also read as whole K slabs of 64: zeros past M
+            const int rows = EPI == kTcGrad ? (M + 63) & ~63 : M;
+            if (row0 < rows && n0 + c0 < g.N) tma_store_2d(&map_c, buf, n0 + c0, row0);
+            bulk_commit();
           }
-          stage_bf16(buf, lane, half, x);
-          if (half == 1) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              const int col = n0 + c0 - 32;
-              // a gradient's rows are also read as whole K slabs of 64: zeros past M
-              const int rows = EPI == kTcGrad ? (M + 63) & ~63 : M;
-              if (row0 < rows && col < g.N) tma_store_2d(&map_c, buf, col, row0);
-              bulk_commit();
-            }
-            __syncwarp();
-            ++boxes;
-          }
+          __syncwarp();
         }
         if constexpr (EPI == kTcStats) {
           if (row_on) g.row_stats[(int64_t)row * g.stats_ld + (g.col0 + n0) / kBN].y = sum;
