@@ -34,7 +34,7 @@ struct DropoutArgs {
 // unit finds its row.
 template <typename TX, typename TY, bool RES, bool VEC, bool FLAT>
 __global__ void __launch_bounds__(kThreads) k_dropout(const DropoutArgs a) {
-  const DropKey key = drop_key(a.d);
+  const DropWords words = drop_words(a.d);
   const int64_t b0 = (int64_t)blockIdx.x * (a.per_thread * kThreads) + threadIdx.x;
   Unit<TX> x[kUnits];
   Unit<TY> r[kUnits];
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const DropoutArgs a) {
     const int n = place(k, row, c);
     if (!n) continue;
     F8 v = unpack(x[k]);
-    if (a.d.threshold) drop_unit(v, (uint64_t)(b0 + k * kThreads), key, a.d.threshold, a.d.factor);
+    if (a.d.threshold) drop_unit(v, (uint64_t)(b0 + k * kThreads), words, a.d);
     if (RES) {
       const F8 w = unpack(r[k]);
 #pragma unroll
@@ -94,7 +94,11 @@ sf_status make_drop_consts(double p, const sf_rng* rng, DropConsts* out) {
   if (t && !rng) return fail(SF_ERR_INVALID, "p > 0 needs a generator (rng is NULL)");
   *out = DropConsts{};
   if (!t) return SF_OK;
-  out->seed = rng->seed;
+  uint32_t k0 = (uint32_t)rng->seed, k1 = (uint32_t)(rng->seed >> 32);
+  for (int r = 0; r < 10; ++r, k0 += 0x9E3779B9u, k1 += 0xBB67AE85u) {
+    out->key[2 * r] = k0;
+    out->key[2 * r + 1] = k1;
+  }
   out->offset = rng->offset;
   out->device_offset = rng->device_offset;
   out->threshold = t;

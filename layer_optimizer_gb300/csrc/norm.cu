@@ -132,7 +132,7 @@ __global__ void __maxnreg__(sizeof(TA) + sizeof(TS) == 4 ? 64 : 80) k_add_rmsnor
         if (a.r) load_unit<VEC>(rp + c, n[k], r[k]);
       }
     }
-    const DropKey key = a.d.threshold ? drop_key(a.d) : DropKey{};
+    const DropWords words = a.d.threshold ? drop_words(a.d) : DropWords{};
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
 #pragma unroll
@@ -140,7 +140,7 @@ __global__ void __maxnreg__(sizeof(TA) + sizeof(TS) == 4 ? 64 : 80) k_add_rmsnor
       if (!n[k]) continue;
       s[k] = unpack(x[k]);
       if (a.d.threshold)
-        drop_unit(s[k], (uint64_t)(row * a.per_row + t + k * tpr), key, a.d.threshold, a.d.factor);
+        drop_unit(s[k], (uint64_t)(row * a.per_row + t + k * tpr), words, a.d);
       if (a.r) {
         const F8 w = unpack(r[k]);
 #pragma unroll
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
   __shared__ float red[2][kMaxThreads / 32];
   extern __shared__ float comb[];      // [rows of a block][cols], only with several rows a block
   const int tpr = a.tpr, rpb = a.rpb, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
-  const DropKey key = a.d.threshold ? drop_key(a.d) : DropKey{};
+  const DropWords words = a.d.threshold ? drop_words(a.d) : DropWords{};
   F8 acc[kK] = {};
   int parity = 0;
   for (int64_t base = (int64_t)blockIdx.x * rpb; base < a.rows; base += (int64_t)gridDim.x * rpb, parity ^= 1) {
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
       if (a.dr) store_unit<VEC>(row_ptr<TS>(a.dr, a.lddr, row) + col, n[k], v);
       if (a.dx) {
         if (a.d.threshold)
-          drop_unit(v, (uint64_t)(row * a.per_row + t + k * tpr), key, a.d.threshold, a.d.factor);
+          drop_unit(v, (uint64_t)(row * a.per_row + t + k * tpr), words, a.d);
         store_unit<VEC>(row_ptr<TA>(a.dx, a.lddx, row) + col, n[k], v);
       }
     }
@@ -372,8 +372,8 @@ constexpr int kMinStages = 3, kMaxStages = 4;
 // outputs, which then leave, and row i - 2's have left, so its stage is
 // refilled.  With loads and stores of registers the kernel was bound by
 // instruction issue (49 instructions an element, 59 % of the copy rate).
-template <typename TA, typename TS, int K>
-__global__ void __maxnreg__(K == 2 ? 80 : 128) k_add_rmsnorm_bwd_ring(const BwdArgs a, const int stages) {
+template <typename TA, typename TS, int K, bool KEEP>
+__global__ void __maxnreg__(K == 2 ? 80 : KEEP ? 168 : 128) k_add_rmsnorm_bwd_ring(const BwdArgs a, const int stages) {
   __shared__ __align__(16) float red[2][4][kMaxThreads / 32];    // [alternating][row of the block][warp of the row]
   __shared__ __align__(8) uint64_t full[kMaxStages];
   extern __shared__ __align__(128) unsigned char ring[];
@@ -418,15 +418,15 @@ __global__ void __maxnreg__(K == 2 ? 80 : 128) k_add_rmsnorm_bwd_ring(const BwdA
     for (int i = 0; i < stages; ++i)
       if (first + i * step < a.rows) fill(first + i * step, i);
 
-  const DropKey key = a.d.threshold ? drop_key(a.d) : DropKey{};
+  const DropWords words = a.d.threshold ? drop_words(a.d) : DropWords{};
   const int col0 = 8 * t, dcol = 8 * tpr;
   bool in[K];
-  F8 acc[K] = {}, gain[K];      // with two units a thread its gains stay in registers
+  F8 acc[K] = {}, gain[K];      // KEEP: a thread's gains stay in registers
   auto gain_at = [&](int k) { return in[k] ? load_gain<true>(a.gain, a.gain_fp32, col0 + k * dcol, 8) : F8{}; };
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     in[k] = col0 + k * dcol < a.cols;
-    if (K == 2) gain[k] = gain_at(k);
+    if (KEEP) gain[k] = gain_at(k);
   }
   const uint32_t at_a0 = ring0 + (uint32_t)lane_row * row_a + (uint32_t)col0 * sizeof(TA);
   const uint32_t at_s0 = ring0 + off_s + (uint32_t)lane_row * row_s + (uint32_t)col0 * sizeof(TS);
@@ -455,7 +455,7 @@ __global__ void __maxnreg__(K == 2 ? 80 : 128) k_add_rmsnorm_bwd_ring(const BwdA
         if (!in[k]) continue;
         lds_unit(at_a0 + at + (uint32_t)(k * dcol) * sizeof(TA), dh);
         lds_unit(at_s0 + at + (uint32_t)(k * dcol) * sizeof(TS), s);
-        bwd_sums(unpack(dh), unpack(s), K == 2 ? gain[k] : gain_at(k), rstd2, acc[k], dot2);
+        bwd_sums(unpack(dh), unpack(s), KEEP ? gain[k] : gain_at(k), rstd2, acc[k], dot2);
       }
     }
     // the row's sum: lanes by a butterfly, then all warps of the row (unused
@@ -493,10 +493,10 @@ __global__ void __maxnreg__(K == 2 ? 80 : 128) k_add_rmsnorm_bwd_ring(const BwdA
         lds_unit(pa, dh);
         lds_unit(ps, s);
         if (a.dsum) lds_unit(at_d0 + at + (uint32_t)(k * dcol) * sizeof(TS), ds);
-        F8 v = bwd_unit(unpack(dh), unpack(s), K == 2 ? gain[k] : gain_at(k), a.dsum ? unpack(ds) : F8{}, rstd2, c2);
+        F8 v = bwd_unit(unpack(dh), unpack(s), KEEP ? gain[k] : gain_at(k), a.dsum ? unpack(ds) : F8{}, rstd2, c2);
         if (a.dr) sts_unit(ps, v, TS());
         if (a.dx) {
-          if (a.d.threshold) drop_unit(v, unit + k * tpr, key, a.d.threshold, a.d.factor);
+          if (a.d.threshold) drop_unit(v, unit + k * tpr, words, a.d);
           sts_unit(pa, v, TA());
         }
       }
@@ -615,14 +615,17 @@ inline bool ring_fits(int64_t rows, int64_t cols, int32_t ta, int32_t ts, bool d
 }
 
 template <typename TA, typename TS>
-const void* ring_kernel(int k) {
-  return k == 2 ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 2> : (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4>;
+const void* ring_kernel(int k, bool keep) {
+  return k == 2 ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 2, true>
+         : keep ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4, true>
+                : (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4, false>;
 }
 
 // Two units a thread up to 1024 columns, four beyond (16384 x 4096 bf16, all
 // outputs: 137 us with four, 149 us with two: fewer barriers' worth of work a
-// row outweighs fewer warps); as many blocks an SM as registers (80 and 128 a
-// thread) and three stages each allow.
+// row outweighs fewer warps), and the gains in registers where a block's
+// registers allow (118 us, against 130 us read from L1 in both passes); as many
+// blocks an SM as registers and three stages each allow.
 sf_status launch_ring(BwdArgs& a, int32_t ta, int32_t ts, cudaStream_t st, int64_t* parts) {
   using B = __nv_bfloat16;
   const int k = a.per_row <= 128 ? 2 : 4;
@@ -635,10 +638,11 @@ sf_status launch_ring(BwdArgs& a, int32_t ta, int32_t ts, cudaStream_t st, int64
     a.rpb = 128 / a.tpr;
   }
   const int threads = a.tpr * a.rpb;
-  const void* kernel = ta == SF_BF16 ? (ts == SF_BF16 ? ring_kernel<B, B>(k) : ring_kernel<B, float>(k))
-                                     : (ts == SF_BF16 ? ring_kernel<float, B>(k) : ring_kernel<float, float>(k));
+  const bool keep = threads <= 384;
+  const void* kernel = ta == SF_BF16 ? (ts == SF_BF16 ? ring_kernel<B, B>(k, keep) : ring_kernel<B, float>(k, keep))
+                                     : (ts == SF_BF16 ? ring_kernel<float, B>(k, keep) : ring_kernel<float, float>(k, keep));
   const size_t stage = a.rpb * ring_row_bytes(a.cols, ta, ts, a.dsum != nullptr);
-  const int per_sm = (int)std::max<size_t>(1, std::min<size_t>((k == 2 ? 768 : 512) / threads, kSmemPerSm / (kMinStages * stage + 1024)));
+  const int per_sm = (int)std::max<size_t>(1, std::min<size_t>((k == 2 ? 768 : keep ? 384 : 512) / threads, kSmemPerSm / (kMinStages * stage + 1024)));
   const int stages = (int)std::min<size_t>(kMaxStages, (kSmemPerSm / per_sm - 1024) / stage);
   const size_t smem = stage * stages;
   SF_TRY(allow_dynamic_smem(kernel, smem));

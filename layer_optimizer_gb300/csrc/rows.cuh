@@ -164,7 +164,7 @@ __device__ __forceinline__ void store_unit(float* p, int n, const F8& v) {
 // probability threshold / 65536 that is really used (within 2^-17 of p).
 // threshold = 0: no dropout.
 struct DropConsts {
-  uint64_t seed;
+  uint32_t key[20];                // the rounds' keys, from the seed
   uint64_t offset;
   const uint64_t* device_offset;   // added to offset when not null
   float factor;
@@ -173,39 +173,38 @@ struct DropConsts {
 
 sf_status make_drop_consts(double p, const sf_rng* rng, DropConsts* out);
 
-// The generator's per-call words: key and the upper counter half.
-struct DropKey {
-  uint32_t k0, k1, c2, c3;
+// The upper counter half, the same for a whole call.
+struct DropWords {
+  uint32_t c2, c3;
 };
-__device__ __forceinline__ DropKey drop_key(const DropConsts& d) {
+__device__ __forceinline__ DropWords drop_words(const DropConsts& d) {
   uint64_t off = d.offset;
   if (d.device_offset) off += *d.device_offset;
-  return DropKey{(uint32_t)d.seed, (uint32_t)(d.seed >> 32), (uint32_t)off, (uint32_t)(off >> 32)};
+  return DropWords{(uint32_t)off, (uint32_t)(off >> 32)};
 }
 
 // Philox-4x32 with 10 rounds (Salmon, Moraes, Dror, Shaw: "Parallel random
 // numbers: as easy as 1, 2, 3", 2011): 128 bits for the unit with index b,
 // 16 per column.  Eight columns share one evaluation, so a column costs 2.5
 // 32 x 32 -> 64 multiplications; with 32 bits a column (twice that) the
-// bf16 kernels would be bound by the multiplier and not by memory.
-__device__ __forceinline__ void drop_unit(F8& v, uint64_t b, const DropKey& key, uint32_t threshold, float factor) {
-  uint32_t c0 = (uint32_t)b, c1 = (uint32_t)(b >> 32), c2 = key.c2, c3 = key.c3, k0 = key.k0, k1 = key.k1;
+// bf16 kernels would be bound by the multiplier and not by memory.  The round
+// keys come ready from the host: a fifth of the generator's instructions.
+__device__ __forceinline__ void drop_unit(F8& v, uint64_t b, const DropWords& w2, const DropConsts& d) {
+  uint32_t c0 = (uint32_t)b, c1 = (uint32_t)(b >> 32), c2 = w2.c2, c3 = w2.c3;
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t m0 = (uint64_t)c0 * 0xD2511F53u, m1 = (uint64_t)c2 * 0xCD9E8D57u;
-    const uint32_t n0 = (uint32_t)(m1 >> 32) ^ c1 ^ k0, n2 = (uint32_t)(m0 >> 32) ^ c3 ^ k1;
+    const uint32_t n0 = (uint32_t)(m1 >> 32) ^ c1 ^ d.key[2 * r], n2 = (uint32_t)(m0 >> 32) ^ c3 ^ d.key[2 * r + 1];
     c0 = n0;
     c1 = (uint32_t)m1;
     c2 = n2;
     c3 = (uint32_t)m0;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   const uint32_t w[4] = {c0, c1, c2, c3};
   // half >= threshold, compared in the upper half of a word (threshold >= 1
   // here, 65536 included); a dropped element is 0 whatever its value
-  const uint32_t limit = ((threshold - 1) << 16) | 0xFFFFu;
-  const uint64_t f = f2(factor, factor);
+  const uint32_t limit = ((d.threshold - 1) << 16) | 0xFFFFu;
+  const uint64_t f = f2(d.factor, d.factor);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 x = f2(mul2(v.p[j], f));
