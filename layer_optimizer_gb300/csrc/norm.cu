@@ -111,7 +111,7 @@ __device__ __forceinline__ float group_scale(float amax, float* inv) {
 }
 
 template <typename TA, typename TS, bool VEC>
-__global__ void __maxnreg__(sizeof(TA) + sizeof(TS) == 4 ? 64 : 80) k_add_rmsnorm_fwd(const FwdArgs a) {
+__global__ void __maxnreg__(sizeof(TA) + sizeof(TS) == 4 ? 72 : 80) k_add_rmsnorm_fwd(const FwdArgs a) {
   __shared__ float red[2][kMaxThreads / 32];
   const int tpr = a.tpr, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
   const int64_t row = (int64_t)blockIdx.x * a.rpb + lane_row;
@@ -789,7 +789,10 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum, con
                    reinterpret_cast<uintptr_t>(gain) % (8 * dtype_bytes(gain_dtype)) == 0;
   cudaStream_t st = as_stream(stream);
   int64_t parts = grid;
-  if (vec && ring_fits(rows, cols, dh->dtype, sum->dtype, dsum != nullptr)) {
+  // bulk copies take this device's own memory only (pinned host rows go the plain way)
+  auto local = [](const sf_matrix* m) { return !m || on_current_device(m->data); };
+  if (vec && ring_fits(rows, cols, dh->dtype, sum->dtype, dsum != nullptr) && local(dh) && local(sum) && local(dsum) &&
+      local(dresidual) && local(dx)) {
     SF_TRY(launch_ring(a, dh->dtype, sum->dtype, st, &parts));
   } else if (grid) {
     void* args[] = {&a};
