@@ -22,9 +22,11 @@ struct DropoutArgs {
   const void* r;
   void* y;
   int64_t ldx, ldr, ldy;
-  int64_t units;        // rows * units_per_row
-  int64_t per_row;      // units per row
-  int64_t cols;
+  int64_t units;        // rows * per_row
+  int64_t per_row;      // units a row may touch
+  int64_t counters;     // generator units per row
+  int32_t cols;         // (not FLAT)
+  int32_t shift;        // kShifted
   int32_t per_thread;   // units a thread takes, 1..kUnits
   DropConsts d;
 };
@@ -32,58 +34,70 @@ struct DropoutArgs {
 // A block takes per_thread * 256 consecutive units.  FLAT: dense rows of whole
 // units, so a unit's place follows from its index; otherwise one division a
 // unit finds its row.
-template <typename TX, typename TY, bool RES, bool VEC, bool FLAT>
+template <typename TX, typename TY, bool RES, int MODE, bool FLAT>
 __global__ void __launch_bounds__(kThreads) k_dropout(const DropoutArgs a) {
   const DropWords words = drop_words(a.d);
   const int64_t b0 = (int64_t)blockIdx.x * (a.per_thread * kThreads) + threadIdx.x;
   Unit<TX> x[kUnits];
   Unit<TY> r[kUnits];
-  // the unit's row and first column; columns of it (0 past the end)
-  auto place = [&](int k, int64_t& row, int64_t& c) {
+  // the k-th unit's row, unit of the row, the row's shift, and its columns
+  auto place = [&](int k, int64_t& row, int& u, int& m) {
     const int64_t b = b0 + k * kThreads;
-    if (k >= a.per_thread || b >= a.units) return 0;
-    if (FLAT) {
-      row = 0;
-      c = 8 * b;
-      return 8;
-    }
+    if (k >= a.per_thread || b >= a.units) return Span{0, 0, 0};
     row = a.units <= INT32_MAX ? (int64_t)((uint32_t)b / (uint32_t)a.per_row) : b / a.per_row;
-    c = 8 * (b - row * a.per_row);
-    return (int)min((int64_t)8, a.cols - c);
+    u = (int)(b - row * a.per_row);
+    m = MODE == kShifted ? (int)(row * a.shift) & 7 : 0;
+    return unit_span<MODE>(u, m, a.cols);
   };
 #pragma unroll
   for (int k = 0; k < kUnits; ++k) {
-    int64_t row, c;
-    const int n = place(k, row, c);
-    if (!n) continue;
-    load_unit<VEC>(row_ptr<TX>(a.x, a.ldx, row) + c, n, x[k]);
-    if (RES) load_unit<VEC>(row_ptr<TY>(a.r, a.ldr, row) + c, n, r[k]);
+    if (FLAT) {
+      const int64_t b = b0 + k * kThreads;
+      if (k >= a.per_thread || b >= a.units) continue;
+      ld_unit(static_cast<const TX*>(a.x) + 8 * b, x[k]);
+      if (RES) ld_unit(static_cast<const TY*>(a.r) + 8 * b, r[k]);
+    } else {
+      int64_t row = 0;
+      int u = 0, m = 0;
+      const Span s = place(k, row, u, m);
+      if (!s.some()) continue;
+      load_unit<MODE>(row_ptr<TX>(a.x, a.ldx, row) + s.c, s.lo, s.hi, x[k]);
+      if (RES) load_unit<MODE>(row_ptr<TY>(a.r, a.ldr, row) + s.c, s.lo, s.hi, r[k]);
+    }
   }
 #pragma unroll
   for (int k = 0; k < kUnits; ++k) {
-    int64_t row, c;
-    const int n = place(k, row, c);
-    if (!n) continue;
+    const int64_t b = b0 + k * kThreads;
+    int64_t row = 0;
+    int u = 0, m = 0;
+    Span s = {0, 0, 8};
+    if (FLAT) {
+      if (k >= a.per_thread || b >= a.units) continue;
+    } else {
+      s = place(k, row, u, m);
+      if (!s.some()) continue;
+    }
     F8 v = unpack(x[k]);
-    if (a.d.threshold) drop_unit(v, (uint64_t)(b0 + k * kThreads), words, a.d);
+    if (a.d.threshold) drop_unit<MODE>(v, (uint64_t)(FLAT ? b : row * a.counters + u), m, words, a.d);
     if (RES) {
       const F8 w = unpack(r[k]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v.p[i] = add2(v.p[i], w.p[i]);
     }
-    store_unit<VEC>(row_ptr<TY>(a.y, a.ldy, row) + c, n, v);
+    store_unit<MODE>(FLAT ? static_cast<TY*>(a.y) + 8 * b : row_ptr<TY>(a.y, a.ldy, row) + s.c, s.lo, s.hi, v);
   }
 }
 
 template <typename TX, typename TY, bool RES>
-const void* pick(bool vec, bool flat) {
-  return flat  ? (const void*)&k_dropout<TX, TY, RES, true, true>
-         : vec ? (const void*)&k_dropout<TX, TY, RES, true, false>
-               : (const void*)&k_dropout<TX, TY, RES, false, false>;
+const void* pick(RowMode mode, bool flat) {
+  return flat               ? (const void*)&k_dropout<TX, TY, RES, kAligned, true>
+         : mode == kAligned ? (const void*)&k_dropout<TX, TY, RES, kAligned, false>
+         : mode == kShifted ? (const void*)&k_dropout<TX, TY, RES, kShifted, false>
+                            : (const void*)&k_dropout<TX, TY, RES, kScalar, false>;
 }
 template <typename TX, typename TY>
-const void* pick(bool res, bool vec, bool flat) {
-  return res ? pick<TX, TY, true>(vec, flat) : pick<TX, TY, false>(vec, flat);
+const void* pick(bool res, RowMode mode, bool flat) {
+  return res ? pick<TX, TY, true>(mode, flat) : pick<TX, TY, false>(mode, flat);
 }
 
 }  // namespace
@@ -131,20 +145,24 @@ sf_status sf_dropout(const sf_matrix* x, const sf_matrix* residual, const sf_mat
   a.ldx = x->ld;
   a.ldr = residual ? residual->ld : 0;
   a.ldy = y->ld;
-  a.cols = x->cols;
-  a.per_row = ceil_div<int64_t>(x->cols, 8);
-  a.units = a.per_row * x->rows;
-  const bool vec = units_aligned(x) && units_aligned(residual) && units_aligned(y);
+  const sf_matrix* const all[3] = {x, residual, y};
+  const RowMode mode = row_mode(all, &a.shift);
   auto dense = [&](const sf_matrix* m) { return !m || m->ld == m->cols || m->rows == 1; };
-  const bool flat = vec && x->cols % 8 == 0 && dense(x) && dense(residual) && dense(y);
+  const bool flat = mode == kAligned && x->cols % 8 == 0 && dense(x) && dense(residual) && dense(y);
+  if (!flat && x->cols > INT32_MAX / 2)
+    return fail(SF_ERR_UNSUPPORTED, "rows of over 2^30 columns need dense, aligned matrices and a multiple of 8 columns");
+  a.cols = (int32_t)std::min<int64_t>(x->cols, INT32_MAX);
+  a.counters = ceil_div<int64_t>(x->cols, 8);
+  a.per_row = a.counters + (mode == kShifted ? 1 : 0);
+  a.units = a.per_row * x->rows;
   // one unit a thread while that leaves SMs idle, else four loads in flight
   a.per_thread = (int32_t)std::clamp<int64_t>(a.units / ((int64_t)kThreads * sm_count() * 4), 1, kUnits);
   const int64_t grid = ceil_div<int64_t>(a.units, (int64_t)kThreads * a.per_thread);
   if (grid > INT32_MAX) return fail(SF_ERR_UNSUPPORTED, "sizes too large");
   using B = __nv_bfloat16;
   const void* k = x->dtype == SF_BF16
-                      ? (y->dtype == SF_BF16 ? pick<B, B>(residual, vec, flat) : pick<B, float>(residual, vec, flat))
-                      : (y->dtype == SF_BF16 ? pick<float, B>(residual, vec, flat) : pick<float, float>(residual, vec, flat));
+                      ? (y->dtype == SF_BF16 ? pick<B, B>(residual, mode, flat) : pick<B, float>(residual, mode, flat))
+                      : (y->dtype == SF_BF16 ? pick<float, B>(residual, mode, flat) : pick<float, float>(residual, mode, flat));
   void* args[] = {&a};
   SF_CUDA_TRY(cudaLaunchKernel(k, dim3((unsigned)grid), dim3(kThreads), args, 0, as_stream(stream)), "launch k_dropout");
   return SF_OK;

@@ -38,6 +38,7 @@ struct FwdArgs {
   int64_t ldx, ldr, lds, ldh, ldq;
   int64_t rows;
   int32_t cols, per_row;
+  int32_t shift;         // kShifted
   int32_t tpr;           // threads a row: a power of two up to 64, or the whole block (a multiple of 32)
   int32_t rpb;           // rows a block
   int32_t gain_fp32;
@@ -47,32 +48,36 @@ struct FwdArgs {
   DropConsts d;
 };
 
-// Eight gains from column c on (served by L1 after a row or two).  VEC: gains
-// are aligned to their units.
-template <bool VEC>
-__device__ __forceinline__ F8 load_gain(const void* g, int fp32, int c, int n) {
+// A unit's gains (served by L1 after a row or two).  kAligned: gains are aligned
+// to their units.
+template <int MODE>
+__device__ __forceinline__ F8 load_gain(const void* g, int fp32, const Span& s) {
   if (fp32) {
-    const float* p = static_cast<const float*>(g) + c;
+    const float* p = static_cast<const float*>(g) + s.c;
     Unit<float> u;
-    if (VEC && n == 8) {
+    if (MODE == kAligned && s.hi == 8) {
       const float4 x = __ldg(reinterpret_cast<const float4*>(p)), y = __ldg(reinterpret_cast<const float4*>(p) + 1);
       u.f[0] = x.x, u.f[1] = x.y, u.f[2] = x.z, u.f[3] = x.w;
       u.f[4] = y.x, u.f[5] = y.y, u.f[6] = y.z, u.f[7] = y.w;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u.f[i] = i < n ? __ldg(p + i) : 0.0f;
+      for (int i = 0; i < 8; ++i) u.f[i] = i >= s.lo && i < s.hi ? __ldg(p + i) : 0.0f;
     }
     return unpack(u);
   }
-  const uint16_t* p = static_cast<const uint16_t*>(g) + c;
+  const uint16_t* p = static_cast<const uint16_t*>(g) + s.c;
   Unit<__nv_bfloat16> u;
-  if (VEC && n == 8) {
+  if (MODE == kAligned && s.hi == 8) {
     const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
     u.w[0] = w.x, u.w[1] = w.y, u.w[2] = w.z, u.w[3] = w.w;
+  } else if (MODE == kShifted && s.lo == 0 && s.hi == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u.w[i] = (uint32_t)__ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      u.w[i] = (2 * i < n ? (uint32_t)__ldg(p + 2 * i) : 0u) | (2 * i + 1 < n ? (uint32_t)__ldg(p + 2 * i + 1) << 16 : 0u);
+      u.w[i] = (2 * i >= s.lo && 2 * i < s.hi ? (uint32_t)__ldg(p + 2 * i) : 0u) |
+               (2 * i + 1 >= s.lo && 2 * i + 1 < s.hi ? (uint32_t)__ldg(p + 2 * i + 1) << 16 : 0u);
   }
   return unpack(u);
 }
@@ -110,13 +115,14 @@ __device__ __forceinline__ float group_scale(float amax, float* inv) {
   return max_nan(amax * (1.0f / 448.0f), 1.17549435e-38f);
 }
 
-template <typename TA, typename TS, bool VEC>
+template <typename TA, typename TS, int MODE>
 __global__ void __maxnreg__(sizeof(TA) + sizeof(TS) == 4 ? 72 : 80) k_add_rmsnorm_fwd(const FwdArgs a) {
   __shared__ float red[2][kMaxThreads / 32];
   const int tpr = a.tpr, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
   const int64_t row = (int64_t)blockIdx.x * a.rpb + lane_row;
   const bool on = row < a.rows;
-  int n[kK];
+  const int m = MODE == kShifted ? (int)(row * a.shift) & 7 : 0;
+  auto span = [&](int k) { return unit_span<MODE>(t + k * tpr, m, on ? a.cols : 0); };
   F8 s[kK];
   {
     Unit<TA> x[kK];
@@ -125,22 +131,19 @@ __global__ void __maxnreg__(sizeof(TA) + sizeof(TS) == 4 ? 72 : 80) k_add_rmsnor
     const TS* rp = row_ptr<TS>(a.r, a.ldr, row);
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
-      const int c = 8 * (t + k * tpr);
-      n[k] = on ? max(0, min(8, a.cols - c)) : 0;
-      if (n[k]) {
-        load_unit<VEC>(xp + c, n[k], x[k]);
-        if (a.r) load_unit<VEC>(rp + c, n[k], r[k]);
-      }
+      const Span p = span(k);
+      if (!p.some()) continue;
+      load_unit<MODE>(xp + p.c, p.lo, p.hi, x[k]);
+      if (a.r) load_unit<MODE>(rp + p.c, p.lo, p.hi, r[k]);
     }
     const DropWords words = a.d.threshold ? drop_words(a.d) : DropWords{};
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[k].p[i] = 0;
-      if (!n[k]) continue;
+      if (!span(k).some()) continue;
       s[k] = unpack(x[k]);
-      if (a.d.threshold)
-        drop_unit(s[k], (uint64_t)(row * a.per_row + t + k * tpr), words, a.d);
+      if (a.d.threshold) drop_unit<MODE>(s[k], (uint64_t)(row * a.per_row + t + k * tpr), m, words, a.d);
       if (a.r) {
         const F8 w = unpack(r[k]);
 #pragma unroll
@@ -152,7 +155,8 @@ __global__ void __maxnreg__(sizeof(TA) + sizeof(TS) == 4 ? 72 : 80) k_add_rmsnor
   TS* sp = row_ptr<TS>(a.s, a.lds, row);
 #pragma unroll
   for (int k = 0; k < kK; ++k) {
-    if (a.s && n[k]) store_unit<VEC>(sp + 8 * (t + k * tpr), n[k], s[k]);
+    const Span p = span(k);
+    if (a.s && p.some()) store_unit<MODE>(sp + p.c, p.lo, p.hi, s[k]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum2 = fma2(s[k].p[i], s[k].p[i], sum2);
   }
@@ -164,29 +168,29 @@ __global__ void __maxnreg__(sizeof(TA) + sizeof(TS) == 4 ? 72 : 80) k_add_rmsnor
   TA* hp = row_ptr<TA>(a.h, a.ldh, row);
 #pragma unroll
   for (int k = 0; k < kK; ++k) {
-    const int c = 8 * (t + k * tpr);
-    if (n[k]) {
-      const F8 g = load_gain<VEC>(a.gain, a.gain_fp32, c, n[k]);
+    const Span p = span(k);
+    if (p.some()) {
+      const F8 g = load_gain<MODE>(a.gain, a.gain_fp32, p);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[k].p[i] = mul2(mul2(s[k].p[i], rstd2), g.p[i]);
-      if (a.h) store_unit<VEC>(hp + c, n[k], s[k]);
+      if (a.h) store_unit<MODE>(hp + p.c, p.lo, p.hi, s[k]);
     }
     if (a.q) {
-      float m = 0.0f;
+      float top = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        // past a ragged row's end the sum is 0 and so is the gain
+        // outside a ragged row the sum is 0 and so is the gain
         const float2 v = f2(s[k].p[i]);
-        m = max_nan(m, max_nan(fabsf(v.x), fabsf(v.y)));
+        top = max_nan(top, max_nan(fabsf(v.x), fabsf(v.y)));
       }
-      if (n[k] == 0) m = 0.0f;
-      amax = max_nan(amax, m);
+      if (!p.some()) top = 0.0f;
+      amax = max_nan(amax, top);
       if (a.group_log2) {
         const int lanes = 1 << (a.group_log2 - 3);
-        for (int o = lanes >> 1; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = lanes >> 1; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
         float inv;
-        const float sc = group_scale(m, &inv);
-        if (n[k] && (t & (lanes - 1)) == 0) a.scale[row * a.n_groups + (c >> a.group_log2)] = sc;
+        const float sc = group_scale(top, &inv);
+        if (p.some() && (t & (lanes - 1)) == 0) a.scale[row * a.n_groups + (p.c >> a.group_log2)] = sc;
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[k].p[i] = mul2(s[k].p[i], f2(inv, inv));
       }
@@ -205,7 +209,8 @@ __global__ void __maxnreg__(sizeof(TA) + sizeof(TS) == 4 ? 72 : 80) k_add_rmsnor
   }
 #pragma unroll
   for (int k = 0; k < kK; ++k) {
-    if (!n[k]) continue;
+    const Span part = span(k);
+    if (!part.some()) continue;
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -214,13 +219,13 @@ __global__ void __maxnreg__(sizeof(TA) + sizeof(TS) == 4 ? 72 : 80) k_add_rmsnor
       const uint32_t hi = __nv_cvt_float2_to_fp8x2(f2(s[k].p[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
       w[i] = lo | hi << 16;
     }
-    uint8_t* p = row_ptr<uint8_t>(a.q, a.ldq, row) + 8 * (t + k * tpr);
-    if (VEC && n[k] == 8) {
+    uint8_t* p = row_ptr<uint8_t>(a.q, a.ldq, row) + part.c;
+    if (MODE != kScalar && part.lo == 0 && part.hi == 8) {
       *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < n[k]) p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+        if (i >= part.lo && i < part.hi) p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
     }
   }
 }
@@ -268,7 +273,7 @@ __device__ __forceinline__ F8 bwd_unit(const F8& dh, const F8& s, const F8& g, c
   return v;
 }
 
-template <typename TA, typename TS, bool VEC>
+template <typename TA, typename TS, int MODE>
 __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a) {
   __shared__ float red[2][kMaxThreads / 32];
   extern __shared__ float comb[];      // [rows of a block][cols], only with several rows a block
@@ -287,9 +292,9 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
       const int c = 8 * (t + k * tpr);
       n[k] = on ? max(0, min(8, a.cols - c)) : 0;
       if (n[k]) {
-        load_unit<VEC>(row_ptr<TA>(a.dh, a.lddh, row) + c, n[k], dh[k]);
-        load_unit<VEC>(row_ptr<TS>(a.s, a.lds, row) + c, n[k], s[k]);
-        if (a.dsum) load_unit<VEC>(row_ptr<TS>(a.dsum, a.lddsum, row) + c, n[k], ds[k]);
+        load_unit<MODE>(row_ptr<TA>(a.dh, a.lddh, row) + c, 0, n[k], dh[k]);
+        load_unit<MODE>(row_ptr<TS>(a.s, a.lds, row) + c, 0, n[k], s[k]);
+        if (a.dsum) load_unit<MODE>(row_ptr<TS>(a.dsum, a.lddsum, row) + c, 0, n[k], ds[k]);
       }
     }
     const float rstd = on ? a.rstd[row] : 0.0f;
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
 #pragma unroll
     for (int k = 0; k < kK; ++k)
       if (n[k])
-        bwd_sums(unpack(dh[k]), unpack(s[k]), load_gain<VEC>(a.gain, a.gain_fp32, 8 * (t + k * tpr), n[k]), rstd2, acc[k], dot2);
+        bwd_sums(unpack(dh[k]), unpack(s[k]), load_gain<MODE>(a.gain, a.gain_fp32, Span{8 * (t + k * tpr), 0, n[k]}), rstd2, acc[k], dot2);
     // two alternating buffers: the next row's write cannot meet this row's reads
     const float dot = row_reduce<false>(f2(dot2).x + f2(dot2).y, tpr, red[parity]);
     const float c = -rstd * (rstd * (rstd * dot * a.inv_cols));
@@ -307,13 +312,13 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
     for (int k = 0; k < kK; ++k) {
       if (!n[k]) continue;
       const int col = 8 * (t + k * tpr);
-      F8 v = bwd_unit(unpack(dh[k]), unpack(s[k]), load_gain<VEC>(a.gain, a.gain_fp32, col, n[k]), a.dsum ? unpack(ds[k]) : F8{},
+      F8 v = bwd_unit(unpack(dh[k]), unpack(s[k]), load_gain<MODE>(a.gain, a.gain_fp32, Span{col, 0, n[k]}), a.dsum ? unpack(ds[k]) : F8{},
                       rstd2, c2);
-      if (a.dr) store_unit<VEC>(row_ptr<TS>(a.dr, a.lddr, row) + col, n[k], v);
+      if (a.dr) store_unit<MODE>(row_ptr<TS>(a.dr, a.lddr, row) + col, 0, n[k], v);
       if (a.dx) {
         if (a.d.threshold)
-          drop_unit(v, (uint64_t)(row * a.per_row + t + k * tpr), words, a.d);
-        store_unit<VEC>(row_ptr<TA>(a.dx, a.lddx, row) + col, n[k], v);
+          drop_unit<MODE>(v, (uint64_t)(row * a.per_row + t + k * tpr), 0, words, a.d);
+        store_unit<MODE>(row_ptr<TA>(a.dx, a.lddx, row) + col, 0, n[k], v);
       }
     }
   }
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
 #pragma unroll
   for (int k = 0; k < kK; ++k) {
     const int c = 8 * (t + k * tpr);
-    if (c < a.cols) store_unit<false>((rpb == 1 ? part : comb + lane_row * a.cols) + c, min(8, a.cols - c), acc[k]);
+    if (c < a.cols) store_unit<kScalar>((rpb == 1 ? part : comb + lane_row * a.cols) + c, 0, min(8, a.cols - c), acc[k]);
   }
   if (rpb == 1) return;
   __syncthreads();
@@ -422,7 +427,7 @@ __global__ void __maxnreg__(K == 2 ? 80 : KEEP ? 168 : 128) k_add_rmsnorm_bwd_ri
   const int col0 = 8 * t, dcol = 8 * tpr;
   bool in[K];
   F8 acc[K] = {}, gain[K];      // KEEP: a thread's gains stay in registers
-  auto gain_at = [&](int k) { return in[k] ? load_gain<true>(a.gain, a.gain_fp32, col0 + k * dcol, 8) : F8{}; };
+  auto gain_at = [&](int k) { return in[k] ? load_gain<kAligned>(a.gain, a.gain_fp32, Span{col0 + k * dcol, 0, 8}) : F8{}; };
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     in[k] = col0 + k * dcol < a.cols;
@@ -496,7 +501,7 @@ __global__ void __maxnreg__(K == 2 ? 80 : KEEP ? 168 : 128) k_add_rmsnorm_bwd_ri
         F8 v = bwd_unit(unpack(dh), unpack(s), KEEP ? gain[k] : gain_at(k), a.dsum ? unpack(ds) : F8{}, rstd2, c2);
         if (a.dr) sts_unit(ps, v, TS());
         if (a.dx) {
-          if (a.d.threshold) drop_unit(v, unit + k * tpr, words, a.d);
+          if (a.d.threshold) drop_unit<kAligned>(v, unit + k * tpr, 0, words, a.d);
           sts_unit(pa, v, TA());
         }
       }
@@ -523,7 +528,7 @@ __global__ void __maxnreg__(K == 2 ? 80 : KEEP ? 168 : 128) k_add_rmsnorm_bwd_ri
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = col0 + k * dcol;
-    if (c < a.cols) store_unit<false>((rpb == 1 ? part : comb + lane_row * a.cols) + c, 8, acc[k]);
+    if (c < a.cols) store_unit<kScalar>((rpb == 1 ? part : comb + lane_row * a.cols) + c, 0, 8, acc[k]);
   }
   if (rpb == 1) return;
   __syncthreads();
@@ -581,23 +586,34 @@ void pick_threads(int64_t rows, int64_t per_row, bool groups, int32_t* tpr, int3
 constexpr int kMaxParts = 1024;   // blocks of the backward kernel, and so partial rows of dg
 constexpr unsigned kTypes = 1u << SF_BF16 | 1u << SF_FP32;
 
-template <template <typename, typename, bool> class K>
-const void* pick(int32_t ta, int32_t ts, bool vec) {
-  using B = __nv_bfloat16;
-  if (ta == SF_BF16)
-    return ts == SF_BF16 ? (vec ? K<B, B, true>::ptr() : K<B, B, false>::ptr())
-                         : (vec ? K<B, float, true>::ptr() : K<B, float, false>::ptr());
-  return ts == SF_BF16 ? (vec ? K<float, B, true>::ptr() : K<float, B, false>::ptr())
-                       : (vec ? K<float, float, true>::ptr() : K<float, float, false>::ptr());
-}
-template <typename TA, typename TS, bool VEC>
+template <typename TA, typename TS>
 struct Fwd {
-  static const void* ptr() { return (const void*)&k_add_rmsnorm_fwd<TA, TS, VEC>; }
+  static const void* ptr(RowMode mode) {
+    return mode == kAligned   ? (const void*)&k_add_rmsnorm_fwd<TA, TS, kAligned>
+           : mode == kShifted ? (const void*)&k_add_rmsnorm_fwd<TA, TS, kShifted>
+                              : (const void*)&k_add_rmsnorm_fwd<TA, TS, kScalar>;
+  }
 };
-template <typename TA, typename TS, bool VEC>
+template <typename TA, typename TS>
 struct Bwd {
-  static const void* ptr() { return (const void*)&k_add_rmsnorm_bwd<TA, TS, VEC>; }
+  static const void* ptr(RowMode mode) {
+    // shifted rows gain nothing here (16384 x 4095: 375 us, 349 element by element)
+    return mode == kAligned ? (const void*)&k_add_rmsnorm_bwd<TA, TS, kAligned> : (const void*)&k_add_rmsnorm_bwd<TA, TS, kScalar>;
+  }
 };
+template <template <typename, typename> class K>
+const void* pick(int32_t ta, int32_t ts, RowMode mode) {
+  using B = __nv_bfloat16;
+  if (ta == SF_BF16) return ts == SF_BF16 ? K<B, B>::ptr(mode) : K<B, float>::ptr(mode);
+  return ts == SF_BF16 ? K<float, B>::ptr(mode) : K<float, float>::ptr(mode);
+}
+// The mode of a call: kAligned also wants the gains on their units.
+template <size_t N>
+RowMode call_mode(const sf_matrix* const (&ms)[N], const void* gain, int32_t gain_dtype, int* shift) {
+  const RowMode mode = row_mode(ms, shift);
+  return mode == kAligned && reinterpret_cast<uintptr_t>(gain) % (8 * dtype_bytes(gain_dtype)) ? kShifted : mode;
+}
+
 
 constexpr size_t kSmemPerSm = 222 << 10;
 
@@ -721,15 +737,18 @@ sf_status sf_add_rmsnorm_forward(const sf_matrix* x, const sf_matrix* residual, 
   a.n_groups = group ? (int32_t)ceil_div<int64_t>(cols, group) : 1;
   a.eps = (float)eps;
   a.inv_cols = (float)(1.0 / (double)cols);
-  pick_threads(rows, a.per_row, h8 != nullptr, &a.tpr, &a.rpb);
+  const sf_matrix* const all[5] = {x, residual, sum, h, h8};
+  RowMode mode = call_mode(all, gain, gain_dtype, &a.shift);
+  // a shifted row may touch one unit more, which four units a thread have to
+  // cover, and its units straddle scale groups
+  if (mode == kShifted && ((h8 && group) || cols > kMaxCols - 8)) mode = kScalar;
+  pick_threads(rows, a.per_row + (mode == kShifted ? 1 : 0), h8 != nullptr, &a.tpr, &a.rpb);
   const int threads = a.tpr * a.rpb;
   const int64_t grid = ceil_div<int64_t>(rows, a.rpb);
   if (grid > INT32_MAX) return fail(SF_ERR_UNSUPPORTED, "too many rows");
-  const bool vec = units_aligned(x) && units_aligned(residual) && units_aligned(sum) && units_aligned(h) && units_aligned(h8) &&
-                   reinterpret_cast<uintptr_t>(gain) % (8 * dtype_bytes(gain_dtype)) == 0;
   const int32_t ts = residual ? residual->dtype : sum ? sum->dtype : x->dtype;
   void* args[] = {&a};
-  SF_CUDA_TRY(cudaLaunchKernel(pick<Fwd>(x->dtype, ts, vec), dim3((unsigned)grid), dim3(threads), args, 0, as_stream(stream)),
+  SF_CUDA_TRY(cudaLaunchKernel(pick<Fwd>(x->dtype, ts, mode), dim3((unsigned)grid), dim3(threads), args, 0, as_stream(stream)),
               "launch k_add_rmsnorm_fwd");
   return SF_OK;
 }
@@ -785,18 +804,19 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum, con
   const int64_t resident = (int64_t)sm_count() * std::max(1, 512 / threads);
   const int64_t grid = std::min({blocks, resident, (int64_t)kMaxParts});
   const size_t smem = dgain && rpb > 1 ? (size_t)rpb * cols * sizeof(float) : 0;   // <= 16 KB: rpb * cols <= 4096
-  const bool vec = units_aligned(dh) && units_aligned(sum) && units_aligned(dsum) && units_aligned(dresidual) && units_aligned(dx) &&
-                   reinterpret_cast<uintptr_t>(gain) % (8 * dtype_bytes(gain_dtype)) == 0;
+  const sf_matrix* const all[5] = {dh, sum, dsum, dresidual, dx};
+  int shift = 0;
+  const RowMode mode = call_mode(all, gain, gain_dtype, &shift);
   cudaStream_t st = as_stream(stream);
   int64_t parts = grid;
   // bulk copies take this device's own memory only (pinned host rows go the plain way)
   auto local = [](const sf_matrix* m) { return !m || on_current_device(m->data); };
-  if (vec && ring_fits(rows, cols, dh->dtype, sum->dtype, dsum != nullptr) && local(dh) && local(sum) && local(dsum) &&
+  if (mode == kAligned && ring_fits(rows, cols, dh->dtype, sum->dtype, dsum != nullptr) && local(dh) && local(sum) && local(dsum) &&
       local(dresidual) && local(dx)) {
     SF_TRY(launch_ring(a, dh->dtype, sum->dtype, st, &parts));
   } else if (grid) {
     void* args[] = {&a};
-    SF_CUDA_TRY(cudaLaunchKernel(pick<Bwd>(dh->dtype, sum->dtype, vec), dim3((unsigned)grid), dim3(threads), args, smem, st),
+    SF_CUDA_TRY(cudaLaunchKernel(pick<Bwd>(dh->dtype, sum->dtype, mode), dim3((unsigned)grid), dim3(threads), args, smem, st),
                 "launch k_add_rmsnorm_bwd");
   }
   if (dgain) {

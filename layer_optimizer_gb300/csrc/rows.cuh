@@ -106,56 +106,77 @@ __device__ __forceinline__ void st_unit(float* p, const Unit<float>& u) {
                : "memory");
 }
 
-// The first n (0..8) elements of a unit; the others read as zero.  VEC: the
-// unit is aligned, so a whole one is one access.
-template <bool VEC>
-__device__ __forceinline__ void load_unit(const __nv_bfloat16* p, int n, Unit<__nv_bfloat16>& u) {
-  if (VEC && n == 8) {
+// How a matrix's rows meet its units in memory:
+//   kAligned  every row starts on a unit: unit u holds columns 8 u .. 8 u + 7;
+//   kShifted  row i starts m = i * shift mod 8 columns past a unit, m the same
+//             for all operands (dense rows of an odd length, for example): unit
+//             u holds columns 8 u - m .. 8 u - m + 7, so that whole units are
+//             one access here too (16384 x 4095 bf16: norm with dropout 186 us,
+//             against 278 us element by element);
+//   kScalar   anything else, element by element.
+enum RowMode : int { kScalar = 0, kAligned = 1, kShifted = 2 };
+
+// The first column of a unit, and which of its eight lie in the row.
+struct Span {
+  int c, lo, hi;
+  __device__ __forceinline__ bool some() const { return hi > lo; }
+};
+template <int MODE>
+__device__ __forceinline__ Span unit_span(int u, int m, int cols) {
+  Span s;
+  s.c = 8 * u - (MODE == kShifted ? m : 0);
+  s.lo = MODE == kShifted ? max(0, -s.c) : 0;
+  s.hi = min(8, cols - s.c);
+  return s;
+}
+
+// The columns lo .. hi - 1 of a unit; the others read as zero.
+template <int MODE>
+__device__ __forceinline__ void load_unit(const __nv_bfloat16* p, int lo, int hi, Unit<__nv_bfloat16>& u) {
+  if (MODE != kScalar && lo == 0 && hi == 8) {
     ld_unit(p, u);
     return;
   }
   const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = 2 * i < n ? q[2 * i] : 0u, hi = 2 * i + 1 < n ? q[2 * i + 1] : 0u;
-    u.w[i] = lo | (hi << 16);
+    const uint32_t a = 2 * i >= lo && 2 * i < hi ? q[2 * i] : 0u, b = 2 * i + 1 >= lo && 2 * i + 1 < hi ? q[2 * i + 1] : 0u;
+    u.w[i] = a | (b << 16);
   }
 }
-template <bool VEC>
-__device__ __forceinline__ void load_unit(const float* p, int n, Unit<float>& u) {
-  if (VEC && n == 8) {
+template <int MODE>
+__device__ __forceinline__ void load_unit(const float* p, int lo, int hi, Unit<float>& u) {
+  if (MODE != kScalar && lo == 0 && hi == 8) {
     ld_unit(p, u);
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) u.f[i] = i < n ? p[i] : 0.0f;
+  for (int i = 0; i < 8; ++i) u.f[i] = i >= lo && i < hi ? p[i] : 0.0f;
 }
-template <bool VEC>
-__device__ __forceinline__ void store_unit(__nv_bfloat16* p, int n, const F8& v) {
+template <int MODE>
+__device__ __forceinline__ void store_unit(__nv_bfloat16* p, int lo, int hi, const F8& v) {
   Unit<__nv_bfloat16> u;
   pack(v, u);
-  if (VEC && n == 8) {
+  if (MODE != kScalar && lo == 0 && hi == 8) {
     st_unit(p, u);
     return;
   }
   uint16_t* q = reinterpret_cast<uint16_t*>(p);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (2 * i < n) q[2 * i] = (uint16_t)(u.w[i] & 0xFFFFu);
-    if (2 * i + 1 < n) q[2 * i + 1] = (uint16_t)(u.w[i] >> 16);
-  }
+  for (int i = 0; i < 8; ++i)
+    if (i >= lo && i < hi) q[i] = (uint16_t)(u.w[i >> 1] >> (16 * (i & 1)));
 }
-template <bool VEC>
-__device__ __forceinline__ void store_unit(float* p, int n, const F8& v) {
+template <int MODE>
+__device__ __forceinline__ void store_unit(float* p, int lo, int hi, const F8& v) {
   Unit<float> u;
   pack(v, u);
-  if (VEC && n == 8) {
+  if (MODE != kScalar && lo == 0 && hi == 8) {
     st_unit(p, u);
     return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (i < n) p[i] = u.f[i];
+    if (i >= lo && i < hi) p[i] = u.f[i];
 }
 
 // Dropout's constants: an element is kept where its 16 random bits are at
@@ -189,7 +210,7 @@ __device__ __forceinline__ DropWords drop_words(const DropConsts& d) {
 // 32 x 32 -> 64 multiplications; with 32 bits a column (twice that) the
 // bf16 kernels would be bound by the multiplier and not by memory.  The round
 // keys come ready from the host: a fifth of the generator's instructions.
-__device__ __forceinline__ void drop_unit(F8& v, uint64_t b, const DropWords& w2, const DropConsts& d) {
+__device__ __forceinline__ void drop_bits(uint64_t b, const DropWords& w2, const DropConsts& d, uint32_t (&w)[4]) {
   uint32_t c0 = (uint32_t)b, c1 = (uint32_t)(b >> 32), c2 = w2.c2, c3 = w2.c3;
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
@@ -200,7 +221,33 @@ __device__ __forceinline__ void drop_unit(F8& v, uint64_t b, const DropWords& w2
     c2 = n2;
     c3 = (uint32_t)m0;
   }
-  const uint32_t w[4] = {c0, c1, c2, c3};
+  w[0] = c0, w[1] = c1, w[2] = c2, w[3] = c3;
+}
+
+// Applies the mask to a unit whose columns start m below counter b's eight:
+// with a shift, its bits come from the counters b - 1 and b.
+template <int MODE>
+__device__ __forceinline__ void drop_unit(F8& v, uint64_t b, int m, const DropWords& w2, const DropConsts& d) {
+  uint32_t w[4];
+  drop_bits(b, w2, d, w);
+  if (MODE == kShifted && m) {
+    uint32_t before[4], x[9];
+    drop_bits(b - 1, w2, d, before);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = before[i];
+      x[4 + i] = w[i];
+    }
+    x[8] = 0;
+    // eight halves from half 8 - m (1..7) of the sixteen on
+    const int from = 8 - m;
+#pragma unroll
+    for (int i = 0; i < 7; ++i) x[i] = from & 4 ? x[i + 2] : x[i];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) x[i] = from & 2 ? x[i + 1] : x[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], from & 1 ? 16 : 0);
+  }
   // half >= threshold, compared in the upper half of a word (threshold >= 1
   // here, 65536 included); a dropped element is 0 whatever its value
   const uint32_t limit = ((d.threshold - 1) << 16) | 0xFFFFu;
@@ -222,11 +269,22 @@ __device__ __forceinline__ const T* row_ptr(const void* base, int64_t ld, int64_
   return static_cast<const T*>(base) + row * ld;
 }
 
-// Whether every unit of the matrix starts on a whole-unit boundary.
-inline bool units_aligned(const sf_matrix* m) {
-  if (!m) return true;
-  const size_t unit = 8 * dtype_bytes(m->dtype);
-  return reinterpret_cast<uintptr_t>(m->data) % unit == 0 && (m->ld % 8 == 0 || m->rows <= 1);
+// The mode that all of `ms` (null entries skipped) allow together, and the
+// columns (mod 8) by which each row starts further past a unit than the one
+// before.
+template <size_t N>
+inline RowMode row_mode(const sf_matrix* const (&ms)[N], int* shift) {
+  *shift = -1;
+  for (const sf_matrix* m : ms) {
+    if (!m || m->rows < 1) continue;
+    if (reinterpret_cast<uintptr_t>(m->data) % (8 * dtype_bytes(m->dtype))) return kScalar;
+    if (m->rows == 1) continue;
+    const int d = (int)(m->ld & 7);
+    if (*shift >= 0 && *shift != d) return kScalar;
+    *shift = d;
+  }
+  if (*shift < 0) *shift = 0;
+  return *shift ? kShifted : kAligned;
 }
 
 }  // namespace sf

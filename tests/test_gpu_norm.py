@@ -74,7 +74,12 @@ SHAPES = [
 ]
 
 
-@pytest.mark.parametrize("rows,cols,pad,lead", SHAPES)
+# rows that start at every place of a unit, several of them a thread in the backward pass
+SHIFTED = [(2500, 1021, 0, 0), (5000, 61, 0, 0), (700, 4095, 0, 0), (620, 513, 5, 0), (400, 130, 1, 0), (40, 16375, 0, 0),
+           (40, 16377, 0, 0), (700, 3, 0, 0), (500, 9, 0, 0), (333, 15, 2, 0)]
+
+
+@pytest.mark.parametrize("rows,cols,pad,lead", SHAPES + SHIFTED)
 @pytest.mark.parametrize("xt,yt,res,p", [(BF, BF, False, 0.1), (BF, F32, True, 0.5), (F32, BF, True, 0.01), (F32, F32, False, 0.25),
                                          (BF, BF, True, 0.0)])
 def test_dropout_matches_oracle(rows, cols, pad, lead, xt, yt, res, p):
@@ -144,7 +149,7 @@ def _forward_refs(x, r, gain, p, group):
     return s, mag, h, rstd, rel, eh
 
 
-@pytest.mark.parametrize("rows,cols,pad,lead", SHAPES)
+@pytest.mark.parametrize("rows,cols,pad,lead", SHAPES + SHIFTED)
 @pytest.mark.parametrize("at,st,gt,res,p,group", [
     (BF, BF, BF, True, 0.0, None), (BF, F32, F32, True, 0.1, 128), (F32, F32, F32, True, 0.0, 0), (F32, BF, BF, True, 0.5, 32),
     (BF, BF, F32, False, 0.0, 64),
@@ -213,7 +218,7 @@ STAGED = [(1000, 512, 0, 0), (777, 520, 8, 32), (610, 1024, 0, 0), (320, 4104, 2
           (308, 16384, 0, 0)]
 
 
-@pytest.mark.parametrize("rows,cols,pad,lead", SHAPES + STAGED)
+@pytest.mark.parametrize("rows,cols,pad,lead", SHAPES + SHIFTED + STAGED)
 @pytest.mark.parametrize("at,st,gt,dgt,stream_grad,p", [
     (BF, BF, BF, F32, True, 0.0), (BF, F32, F32, BF, True, 0.1), (F32, F32, F32, F32, False, 0.25), (F32, BF, BF, F32, True, 0.0),
 ])
@@ -267,8 +272,8 @@ def test_add_rmsnorm_backward_many_rows_and_no_rows():
     assert not dg.any()
 
 
-def test_sum_and_outputs_in_place():
-    rows, cols = 130, 520
+@pytest.mark.parametrize("rows,cols", [(130, 520), (400, 517)])
+def test_sum_and_outputs_in_place(rows, cols):
     x, r = synth.normal((rows, cols), 1.0, 5, dtype=BF).to(DEV), synth.normal((rows, cols), 1.0, 6, dtype=BF).to(DEV)
     gain = torch.ones(cols, dtype=BF, device=DEV)
     s, h = torch.empty_like(r), torch.empty_like(x)
