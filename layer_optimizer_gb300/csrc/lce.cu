@@ -260,8 +260,13 @@ __global__ void __launch_bounds__(256) k_lce_gather(const GatherArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t0 = (int64_t)blockIdx.x * 8;
   griddep_launch_dependents();
+  // this warp's row on its way to L2 while the labels are counted
+  if (t0 + warp < a.N)
+    for (int64_t c = 64 * lane; c < a.D; c += 64 * 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.H + (t0 + warp) * a.ldh + c));
   int before = 0, all = 0;
   bool bad = false;
+#pragma unroll 8
   for (int64_t i = threadIdx.x; i < a.N; i += 256) {
     const int32_t y = a.labels[i];
     const bool on = labelled(y, a.ignore, a.V);
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(256) k_lce_gather(const GatherArgs a) {
     if (on) {
       const uint4* from = reinterpret_cast<const uint4*>(a.H + tok * a.ldh);
       uint4* to = reinterpret_cast<uint4*>(a.Hc + (int64_t)r * a.ldc);
-#pragma unroll 4
+#pragma unroll 8
       for (int u = lane; u < units; u += 32) {
         if (u * 8 + 8 <= a.D) {
           to[u] = from[u];
@@ -419,15 +424,19 @@ __global__ void __launch_bounds__(256) k_lce_rows(const RowsArgs a) {
       if (c >= c1) break;
       const float tm = st[(a.col0 + c) / kTcTileN].x;
       const float k = exp2_fast(((tm == -INFINITY ? 0.0f : tm) - l) * kLog2eF);
+      const uint64_t k2 = pack_f2(k, k);
       const uint32_t in[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
       uint32_t out[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x0 = __uint_as_float(in[i] << 16) * k, x1 = __uint_as_float(in[i] & 0xFFFF0000u) * k;
-        if (y == c + 2 * i) x0 = gy;
-        if (y == c + 2 * i + 1) x1 = gy;
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-        out[i] = *reinterpret_cast<const uint32_t*>(&h);
+      for (int i = 0; i < 4; ++i)
+        out[i] = bf16x2_rn(fmul2(pack_f2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xFFFF0000u)), k2));
+      if ((unsigned)(y - c) < 8u) {
+        const uint32_t g = __bfloat16_as_ushort(__float2bfloat16_rn(gy));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (y - c == 2 * i) out[i] = (out[i] & 0xFFFF0000u) | g;
+          if (y - c == 2 * i + 1) out[i] = (out[i] & 0xFFFFu) | g << 16;
+        }
       }
       *reinterpret_cast<uint4*>(a.G + r * a.ldg + c) = make_uint4(out[0], out[1], out[2], out[3]);
     }
