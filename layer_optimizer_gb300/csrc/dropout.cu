@@ -4,9 +4,14 @@
 // where it is used and never stored: the backward pass is the same call on
 // the gradient, and the norm kernels apply the same mask inside their pass.
 //
-// Elementwise, one read of x (and r) and one write of y; bound by HBM where
-// the 2.5 wide multiplications an element that the generator costs stay
-// below the multiplier's rate.
+// Elementwise, one read of x (and r) and one write of y; HBM bounds it.  A
+// block takes 1024 consecutive units of eight columns, four loads of each
+// operand in flight a thread (a persistent grid with two resident blocks an SM
+// was 40 % slower), and products and additions go two at a time, so that the
+// generator's 2.5 wide multiplications an element stay in the shadow of the
+// loads: 16384 x 4096 bf16 with a bf16 residual 59.8 us, 6.7 TB/s, the copy
+// rate.  Rows that start off a unit cost a second generator evaluation a unit
+// (16384 x 4095: 126 us).
 #include <algorithm>
 
 #include "rows.cuh"
