@@ -254,6 +254,7 @@ struct BwdArgs {
   void* dr;             // may be null
   void* dx;             // may be null
   float* part;          // [grid][cols], null without dg
+  int32_t ring_dsum;    // staged form: dsum comes through the ring (else from memory, prefetched into L2)
   int64_t lddh, lds, lddsum, lddr, lddx;
   int64_t rows;
   int32_t cols, per_row;
@@ -395,20 +396,21 @@ __global__ void __maxnreg__(K == 2 ? 80 : KEEP ? 168 : 128) k_add_rmsnorm_bwd_ri
   if (threadIdx.x < 2 * 4 * kMaxThreads / 32) (&red[0][0][0])[threadIdx.x] = 0.0f;     // blocks have 128 threads or more
   const uint32_t row_a = (uint32_t)a.cols * sizeof(TA), row_s = (uint32_t)a.cols * sizeof(TS);
   const uint32_t off_s = row_a * rpb, off_d = off_s + row_s * rpb;
-  const uint32_t stage_bytes = off_d + (a.dsum ? row_s * rpb : 0u);
+  const bool ring_d = a.dsum && a.ring_dsum;
+  const uint32_t stage_bytes = off_d + (ring_d ? row_s * rpb : 0u);
   const uint32_t ring0 = smem_u32(ring);
   const int64_t step = (int64_t)gridDim.x * rpb, first = (int64_t)blockIdx.x * rpb;
   // by the first warp: the copies of the rows from `base` on into stage st ...
   auto fill = [&](int64_t base, int st) {
     const int n = (int)min((int64_t)rpb, a.rows - base);
-    if (threadIdx.x == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)n * (row_a + row_s + (a.dsum ? row_s : 0u)));
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)n * (row_a + row_s + (ring_d ? row_s : 0u)));
     __syncwarp();
     if ((int)threadIdx.x < n) {
       unsigned char* at = ring + (size_t)st * stage_bytes;
       const int64_t row = base + threadIdx.x;
       bulk_load(at + threadIdx.x * row_a, row_ptr<TA>(a.dh, a.lddh, row), row_a, &full[st]);
       bulk_load(at + off_s + threadIdx.x * row_s, row_ptr<TS>(a.s, a.lds, row), row_s, &full[st]);
-      if (a.dsum) bulk_load(at + off_d + threadIdx.x * row_s, row_ptr<TS>(a.dsum, a.lddsum, row), row_s, &full[st]);
+      if (ring_d) bulk_load(at + off_d + threadIdx.x * row_s, row_ptr<TS>(a.dsum, a.lddsum, row), row_s, &full[st]);
     }
   };
   // ... and those of its outputs to global memory (each lane its own row, so
@@ -457,7 +459,15 @@ __global__ void __maxnreg__(K == 2 ? 80 : KEEP ? 168 : 128) k_add_rmsnorm_bwd_ri
     const bool on = base + lane_row < a.rows;
     const float rstd = rstd_next;
     rp += step;
-    if (base + step + lane_row < a.rows) rstd_next = *rp;
+    if (base + step + lane_row < a.rows) {
+      rstd_next = *rp;
+      if (a.dsum && !ring_d) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (in[k])
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(row_ptr<TS>(a.dsum, a.lddsum, base + step + lane_row) + col0 + k * dcol));
+      }
+    }
     if (!dead) dead = !mbar_wait_u32(smem_u32(&full[st]), pass);
     const uint64_t rstd2 = f2(rstd, rstd);
     Unit<TA> dh;
@@ -506,7 +516,8 @@ __global__ void __maxnreg__(K == 2 ? 80 : KEEP ? 168 : 128) k_add_rmsnorm_bwd_ri
         const uint32_t pa = at_a0 + at + (uint32_t)(k * dcol) * sizeof(TA), ps = at_s0 + at + (uint32_t)(k * dcol) * sizeof(TS);
         lds_unit(pa, dh);
         lds_unit(ps, s);
-        if (a.dsum) lds_unit(at_d0 + at + (uint32_t)(k * dcol) * sizeof(TS), ds);
+        if (ring_d) lds_unit(at_d0 + at + (uint32_t)(k * dcol) * sizeof(TS), ds);
+        else if (a.dsum) ld_unit(row_ptr<TS>(a.dsum, a.lddsum, base + lane_row) + col0 + k * dcol, ds);
         F8 v = bwd_unit(unpack(dh), unpack(s), KEEP ? gain[k] : gain_at(k), a.dsum ? unpack(ds) : F8{}, rstd2, c2);
         if (a.dr) sts_unit(ps, v, TS());
         if (a.dx) {
@@ -633,10 +644,12 @@ inline size_t ring_row_bytes(int64_t cols, int32_t ta, int32_t ts, bool dsum) {
 
 // The staged kernel takes aligned rows of whole units, long enough that a
 // block's few copies are worth their set-up and short enough that three fit
-// in shared memory, when there is more than one block's worth of rows an SM.
-inline bool ring_fits(int64_t rows, int64_t cols, int32_t ta, int32_t ts, bool dsum) {
+// in shared memory (without dsum if need be: 8192 x 12288 bf16, fp32 stream,
+// 293 us, against 382 us with loads into registers), when there is more than
+// one block's worth of rows an SM.
+inline bool ring_fits(int64_t rows, int64_t cols, int32_t ta, int32_t ts) {
   return cols % 8 == 0 && cols >= 512 && rows >= 2 * sm_count() &&
-         kMinStages * ring_row_bytes(cols, ta, ts, dsum) <= kSmemPerSm;
+         kMinStages * ring_row_bytes(cols, ta, ts, false) <= kSmemPerSm - 1024;
 }
 
 template <typename TA, typename TS>
@@ -666,7 +679,8 @@ sf_status launch_ring(BwdArgs& a, int32_t ta, int32_t ts, cudaStream_t st, int64
   const bool keep = threads <= 384;
   const void* kernel = ta == SF_BF16 ? (ts == SF_BF16 ? ring_kernel<B, B>(k, keep) : ring_kernel<B, float>(k, keep))
                                      : (ts == SF_BF16 ? ring_kernel<float, B>(k, keep) : ring_kernel<float, float>(k, keep));
-  const size_t stage = a.rpb * ring_row_bytes(a.cols, ta, ts, a.dsum != nullptr);
+  a.ring_dsum = a.dsum && kMinStages * a.rpb * ring_row_bytes(a.cols, ta, ts, true) <= kSmemPerSm - 1024;
+  const size_t stage = a.rpb * ring_row_bytes(a.cols, ta, ts, a.ring_dsum);
   const int per_sm = (int)std::max<size_t>(1, std::min<size_t>((k == 2 ? 768 : keep ? 384 : 512) / threads, kSmemPerSm / (kMinStages * stage + 1024)));
   const int stages = (int)std::min<size_t>(kMaxStages, (kSmemPerSm / per_sm - 1024) / stage);
   const size_t smem = stage * stages;
@@ -820,7 +834,7 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum, con
   int64_t parts = grid;
   // bulk copies take this device's own memory only (pinned host rows go the plain way)
   auto local = [](const sf_matrix* m) { return !m || on_current_device(m->data); };
-  if (mode == kAligned && ring_fits(rows, cols, dh->dtype, sum->dtype, dsum != nullptr) && local(dh) && local(sum) && local(dsum) &&
+  if (mode == kAligned && ring_fits(rows, cols, dh->dtype, sum->dtype) && local(dh) && local(sum) && local(dsum) &&
       local(dresidual) && local(dx)) {
     SF_TRY(launch_ring(a, dh->dtype, sum->dtype, st, &parts));
   } else if (grid) {
