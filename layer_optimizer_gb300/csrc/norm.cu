@@ -258,6 +258,7 @@ struct BwdArgs {
   int64_t lddh, lds, lddsum, lddr, lddx;
   int64_t rows;
   int32_t cols, per_row;
+  int32_t shift;         // kShifted
   int32_t tpr, rpb;      // as in FwdArgs
   int32_t gain_fp32;
   float inv_cols;
@@ -283,72 +284,6 @@ __device__ __forceinline__ F8 bwd_unit(const F8& dh, const F8& s, const F8& g, c
   return v;
 }
 
-template <typename TA, typename TS, int MODE>
-__global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a) {
-  __shared__ float red[2][kMaxThreads / 32];
-  extern __shared__ float comb[];      // [rows of a block][cols], only with several rows a block
-  const int tpr = a.tpr, rpb = a.rpb, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
-  const DropWords words = a.d.threshold ? drop_words(a.d) : DropWords{};
-  F8 acc[kK] = {};
-  int parity = 0;
-  for (int64_t base = (int64_t)blockIdx.x * rpb; base < a.rows; base += (int64_t)gridDim.x * rpb, parity ^= 1) {
-    const int64_t row = base + lane_row;
-    const bool on = row < a.rows;
-    Unit<TA> dh[kK];
-    Unit<TS> s[kK], ds[kK];
-    int n[kK];
-#pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int c = 8 * (t + k * tpr);
-      n[k] = on ? max(0, min(8, a.cols - c)) : 0;
-      if (n[k]) {
-        load_unit<MODE>(row_ptr<TA>(a.dh, a.lddh, row) + c, 0, n[k], dh[k]);
-        load_unit<MODE>(row_ptr<TS>(a.s, a.lds, row) + c, 0, n[k], s[k]);
-        if (a.dsum) load_unit<MODE>(row_ptr<TS>(a.dsum, a.lddsum, row) + c, 0, n[k], ds[k]);
-      }
-    }
-    const float rstd = on ? a.rstd[row] : 0.0f;
-    const uint64_t rstd2 = f2(rstd, rstd);
-    uint64_t dot2 = 0;
-#pragma unroll
-    for (int k = 0; k < kK; ++k)
-      if (n[k])
-        bwd_sums(unpack(dh[k]), unpack(s[k]), load_gain<MODE>(a.gain, a.gain_fp32, Span{8 * (t + k * tpr), 0, n[k]}), rstd2, acc[k], dot2);
-    // two alternating buffers: the next row's write cannot meet this row's reads
-    const float dot = row_reduce<false>(f2(dot2).x + f2(dot2).y, tpr, red[parity]);
-    const float c = -rstd * (rstd * (rstd * dot * a.inv_cols));
-    const uint64_t c2 = f2(c, c);
-#pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      if (!n[k]) continue;
-      const int col = 8 * (t + k * tpr);
-      F8 v = bwd_unit(unpack(dh[k]), unpack(s[k]), load_gain<MODE>(a.gain, a.gain_fp32, Span{col, 0, n[k]}), a.dsum ? unpack(ds[k]) : F8{},
-                      rstd2, c2);
-      if (a.dr) store_unit<MODE>(row_ptr<TS>(a.dr, a.lddr, row) + col, 0, n[k], v);
-      if (a.dx) {
-        if (a.d.threshold)
-          drop_unit<MODE>(v, (uint64_t)(row * a.per_row + t + k * tpr), 0, words, a.d);
-        store_unit<MODE>(row_ptr<TA>(a.dx, a.lddx, row) + col, 0, n[k], v);
-      }
-    }
-  }
-  if (!a.part) return;
-  griddep_launch_dependents();
-  float* part = a.part + (int64_t)blockIdx.x * a.cols;
-#pragma unroll
-  for (int k = 0; k < kK; ++k) {
-    const int c = 8 * (t + k * tpr);
-    if (c < a.cols) store_unit<kScalar>((rpb == 1 ? part : comb + lane_row * a.cols) + c, 0, min(8, a.cols - c), acc[k]);
-  }
-  if (rpb == 1) return;
-  __syncthreads();
-  for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-    float v = 0.0f;
-    for (int r = 0; r < rpb; ++r) v += comb[r * a.cols + c];
-    part[c] = v;
-  }
-}
-
 // A unit from shared memory.
 __device__ __forceinline__ void lds_unit(uint32_t p, Unit<__nv_bfloat16>& u) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -359,6 +294,90 @@ __device__ __forceinline__ void lds_unit(uint32_t p, Unit<float>& u) {
   const float4 a = lds_f4(p), b = lds_f4(p + 16);
   u.f[0] = a.x, u.f[1] = a.y, u.f[2] = a.z, u.f[3] = a.w;
   u.f[4] = b.x, u.f[5] = b.y, u.f[6] = b.z, u.f[7] = b.w;
+}
+
+// Rows that start off a unit (kShifted): the grid's step is a multiple of
+// eight rows, so all rows of a thread start the same m columns past a unit and
+// its units hold the same columns in each of them.  Their gains are laid out
+// once, at the same shift and zero outside the row, in shared memory.
+template <typename TA, typename TS, int MODE>
+__global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a) {
+  __shared__ float red[2][kMaxThreads / 32];
+  extern __shared__ __align__(16) float comb[];      // with several rows a block, or shifted: [rows of a block][cols + 8 or more]
+  const int tpr = a.tpr, rpb = a.rpb, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
+  const DropWords words = a.d.threshold ? drop_words(a.d) : DropWords{};
+  const int m = MODE == kShifted ? (int)(((int64_t)blockIdx.x * rpb + lane_row) * a.shift) & 7 : 0;
+  float* mine = comb + lane_row * (8 * a.per_row + 8);
+  if (MODE == kShifted) {
+    for (int k = 0; k < kK; ++k) {
+      const Span p = unit_span<MODE>(t + k * tpr, m, a.cols);
+      if (!p.some()) continue;
+      Unit<float> u;
+      pack(load_gain<MODE>(a.gain, a.gain_fp32, p), u);
+      for (int i = 0; i < 8; ++i) mine[p.c + m + i] = u.f[i];
+    }
+  }
+  auto gain_at = [&](const Span& p) {
+    if (MODE != kShifted) return load_gain<MODE>(a.gain, a.gain_fp32, p);
+    Unit<float> u;
+    lds_unit(smem_u32(mine + p.c + m), u);
+    return unpack(u);
+  };
+  F8 acc[kK] = {};
+  int parity = 0;
+  for (int64_t base = (int64_t)blockIdx.x * rpb; base < a.rows; base += (int64_t)gridDim.x * rpb, parity ^= 1) {
+    const int64_t row = base + lane_row;
+    auto span = [&](int k) { return unit_span<MODE>(t + k * tpr, m, row < a.rows ? a.cols : 0); };
+    Unit<TA> dh[kK];
+    Unit<TS> s[kK], ds[kK];
+#pragma unroll
+    for (int k = 0; k < kK; ++k) {
+      const Span p = span(k);
+      if (!p.some()) continue;
+      load_unit<MODE>(row_ptr<TA>(a.dh, a.lddh, row) + p.c, p.lo, p.hi, dh[k]);
+      load_unit<MODE>(row_ptr<TS>(a.s, a.lds, row) + p.c, p.lo, p.hi, s[k]);
+      if (a.dsum) load_unit<MODE>(row_ptr<TS>(a.dsum, a.lddsum, row) + p.c, p.lo, p.hi, ds[k]);
+    }
+    const float rstd = row < a.rows ? a.rstd[row] : 0.0f;
+    const uint64_t rstd2 = f2(rstd, rstd);
+    uint64_t dot2 = 0;
+#pragma unroll
+    for (int k = 0; k < kK; ++k) {
+      const Span p = span(k);
+      if (p.some()) bwd_sums(unpack(dh[k]), unpack(s[k]), gain_at(p), rstd2, acc[k], dot2);
+    }
+    // two alternating buffers: the next row's write cannot meet this row's reads
+    const float dot = row_reduce<false>(f2(dot2).x + f2(dot2).y, tpr, red[parity]);
+    const float c = -rstd * (rstd * (rstd * dot * a.inv_cols));
+    const uint64_t c2 = f2(c, c);
+#pragma unroll
+    for (int k = 0; k < kK; ++k) {
+      const Span p = span(k);
+      if (!p.some()) continue;
+      F8 v = bwd_unit(unpack(dh[k]), unpack(s[k]), gain_at(p), a.dsum ? unpack(ds[k]) : F8{}, rstd2, c2);
+      if (a.dr) store_unit<MODE>(row_ptr<TS>(a.dr, a.lddr, row) + p.c, p.lo, p.hi, v);
+      if (a.dx) {
+        if (a.d.threshold) drop_unit<MODE>(v, (uint64_t)(row * a.per_row + t + k * tpr), m, words, a.d);
+        store_unit<MODE>(row_ptr<TA>(a.dx, a.lddx, row) + p.c, p.lo, p.hi, v);
+      }
+    }
+  }
+  if (!a.part) return;
+  griddep_launch_dependents();
+  if (rpb > 1) __syncthreads();      // the gains have been read
+  float* part = a.part + (int64_t)blockIdx.x * a.cols;
+#pragma unroll
+  for (int k = 0; k < kK; ++k) {
+    const Span p = unit_span<MODE>(t + k * tpr, m, a.cols);
+    if (p.some()) store_unit<kScalar>((rpb == 1 ? part : mine) + p.c, p.lo, p.hi, acc[k]);
+  }
+  if (rpb == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+    float v = 0.0f;
+    for (int r = 0; r < rpb; ++r) v += comb[r * (8 * a.per_row + 8) + c];
+    part[c] = v;
+  }
 }
 
 __device__ __forceinline__ void sts_unit(uint32_t p, const F8& v, __nv_bfloat16) {
@@ -387,41 +406,66 @@ constexpr int kMinStages = 3, kMaxStages = 4;
 // outputs, which then leave, and row i - 2's have left, so its stage is
 // refilled.  With loads and stores of registers the kernel was bound by
 // instruction issue (49 instructions an element, 59 % of the copy rate).
-template <typename TA, typename TS, int K, bool KEEP>
-__global__ void __maxnreg__(K == 2 ? 80 : KEEP ? 168 : 128) k_add_rmsnorm_bwd_ring(const BwdArgs a, const int stages) {
+// SHIFT: rows that start off a unit, as above.  A copy brings the 16-byte units
+// that hold any of the row, so that units lie in shared memory as in memory;
+// of the first and last one, the columns outside the row are set to zero, and
+// those inside are written to memory by their threads, the rest by bulk stores
+// (16384 x 4095 bf16: 165 us, with dropout 252, against 349 element by element).
+template <typename TA, typename TS, int K, bool KEEP, bool SHIFT>
+__global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) k_add_rmsnorm_bwd_ring(const BwdArgs a, const int stages) {
+  constexpr int MODE = SHIFT ? kShifted : kAligned;
   __shared__ __align__(16) float red[2][4][kMaxThreads / 32];    // [alternating][row of the block][warp of the row]
   __shared__ __align__(8) uint64_t full[kMaxStages];
   extern __shared__ __align__(128) unsigned char ring[];
   const int tpr = a.tpr, rpb = a.rpb, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
   if (threadIdx.x < 2 * 4 * kMaxThreads / 32) (&red[0][0][0])[threadIdx.x] = 0.0f;     // blocks have 128 threads or more
-  const uint32_t row_a = (uint32_t)a.cols * sizeof(TA), row_s = (uint32_t)a.cols * sizeof(TS);
+  // a row's place holds whole units
+  const uint32_t slot = SHIFT ? 8u * a.per_row + 8u : (uint32_t)a.cols;
+  const uint32_t row_a = slot * sizeof(TA), row_s = slot * sizeof(TS);
   const uint32_t off_s = row_a * rpb, off_d = off_s + row_s * rpb;
   const bool ring_d = a.dsum && a.ring_dsum;
   const uint32_t stage_bytes = off_d + (ring_d ? row_s * rpb : 0u);
   const uint32_t ring0 = smem_u32(ring);
   const int64_t step = (int64_t)gridDim.x * rpb, first = (int64_t)blockIdx.x * rpb;
-  // by the first warp: the copies of the rows from `base` on into stage st ...
+  // by the first warp, a lane a row: the copies of the rows from `base` on
+  // into stage st ...
+  const int m_lane = SHIFT ? (int)((first + threadIdx.x) * a.shift) & 7 : 0;
+  auto head = [&](uint32_t size) { return (m_lane * size) & ~15u; };                              // of a row's place
+  auto tail = [&](uint32_t size) { return ((m_lane + a.cols) * size + 15u) & ~15u; };
+  auto bring = [&](unsigned char* at, const void* row, uint32_t size, int st) {
+    if (SHIFT) bulk_load(at + head(size), static_cast<const unsigned char*>(row) - m_lane * size + head(size), tail(size) - head(size), &full[st]);
+    else bulk_load(at, row, a.cols * size, &full[st]);
+  };
   auto fill = [&](int64_t base, int st) {
     const int n = (int)min((int64_t)rpb, a.rows - base);
-    if (threadIdx.x == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)n * (row_a + row_s + (ring_d ? row_s : 0u)));
+    uint32_t bytes = (uint32_t)n * (row_a + row_s + (ring_d ? row_s : 0u));
+    if (SHIFT)
+      bytes = __reduce_add_sync(0xffffffffu, (int)threadIdx.x < n ? tail(sizeof(TA)) - head(sizeof(TA)) + (ring_d ? 2u : 1u) * (tail(sizeof(TS)) - head(sizeof(TS)))
+                                                                  : 0u);
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&full[st], bytes);
     __syncwarp();
     if ((int)threadIdx.x < n) {
       unsigned char* at = ring + (size_t)st * stage_bytes;
       const int64_t row = base + threadIdx.x;
-      bulk_load(at + threadIdx.x * row_a, row_ptr<TA>(a.dh, a.lddh, row), row_a, &full[st]);
-      bulk_load(at + off_s + threadIdx.x * row_s, row_ptr<TS>(a.s, a.lds, row), row_s, &full[st]);
-      if (ring_d) bulk_load(at + off_d + threadIdx.x * row_s, row_ptr<TS>(a.dsum, a.lddsum, row), row_s, &full[st]);
+      bring(at + threadIdx.x * row_a, row_ptr<TA>(a.dh, a.lddh, row), sizeof(TA), st);
+      bring(at + off_s + threadIdx.x * row_s, row_ptr<TS>(a.s, a.lds, row), sizeof(TS), st);
+      if (ring_d) bring(at + off_d + threadIdx.x * row_s, row_ptr<TS>(a.dsum, a.lddsum, row), sizeof(TS), st);
     }
   };
   // ... and those of its outputs to global memory (each lane its own row, so
   // that the lane that fills a row's place knows when it has been read)
+  auto take = [&](unsigned char* row, uint32_t at, uint32_t size) {
+    const uint32_t u0 = m_lane ? 8 : 0, u1 = (m_lane + a.cols) & ~7;      // whole units
+    if (SHIFT) bulk_store(row + (int)(u0 - m_lane) * (int)size, at + u0 * size, (u1 - u0) * size);
+    else bulk_store(row, at, a.cols * size);
+  };
   auto drain = [&](int64_t base, int st) {
     const int n = (int)min((int64_t)rpb, a.rows - base);
     if ((int)threadIdx.x < n) {
       const uint32_t at = ring0 + (uint32_t)st * stage_bytes;
       const int64_t row = base + threadIdx.x;
-      if (a.dx) bulk_store(row_ptr<TA>(a.dx, a.lddx, row), at + threadIdx.x * row_a, row_a);
-      if (a.dr) bulk_store(row_ptr<TS>(a.dr, a.lddr, row), at + off_s + threadIdx.x * row_s, row_s);
+      if (a.dx) take(reinterpret_cast<unsigned char*>(row_ptr<TA>(a.dx, a.lddx, row)), at + threadIdx.x * row_a, sizeof(TA));
+      if (a.dr) take(reinterpret_cast<unsigned char*>(row_ptr<TS>(a.dr, a.lddr, row)), at + off_s + threadIdx.x * row_s, sizeof(TS));
     }
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   };
@@ -436,14 +480,32 @@ __global__ void __maxnreg__(K == 2 ? 80 : KEEP ? 168 : 128) k_add_rmsnorm_bwd_ri
 
   const DropWords words = a.d.threshold ? drop_words(a.d) : DropWords{};
   const int col0 = 8 * t, dcol = 8 * tpr;
+  const int m = SHIFT ? (int)((first + lane_row) * a.shift) & 7 : 0;
+  auto span = [&](int k) { return unit_span<MODE>(t + k * tpr, m, a.cols); };
   bool in[K];
   F8 acc[K] = {}, gain[K];      // KEEP: a thread's gains stay in registers
-  auto gain_at = [&](int k) { return in[k] ? load_gain<kAligned>(a.gain, a.gain_fp32, Span{col0 + k * dcol, 0, 8}) : F8{}; };
+  auto gain_at = [&](int k) { return in[k] ? load_gain<MODE>(a.gain, a.gain_fp32, span(k)) : F8{}; };
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    in[k] = col0 + k * dcol < a.cols;
+    in[k] = span(k).some();
     if (KEEP) gain[k] = gain_at(k);
   }
+  // a unit of a row's place, without what is not the row's
+  auto lds_row = [&](uint32_t at, int k, auto& u) {
+    lds_unit(at, u);
+    F8 v = unpack(u);
+    if (SHIFT) {
+      const Span p = span(k);
+      if (p.lo > 0 || p.hi < 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = f2(v.p[i]);
+          v.p[i] = f2(2 * i >= p.lo && 2 * i < p.hi ? x.x : 0.0f, 2 * i + 1 >= p.lo && 2 * i + 1 < p.hi ? x.y : 0.0f);
+        }
+      }
+    }
+    return v;
+  };
   const uint32_t at_a0 = ring0 + (uint32_t)lane_row * row_a + (uint32_t)col0 * sizeof(TA);
   const uint32_t at_s0 = ring0 + off_s + (uint32_t)lane_row * row_s + (uint32_t)col0 * sizeof(TS);
   const uint32_t at_d0 = at_s0 + off_d - off_s;
@@ -465,7 +527,7 @@ __global__ void __maxnreg__(K == 2 ? 80 : KEEP ? 168 : 128) k_add_rmsnorm_bwd_ri
 #pragma unroll
         for (int k = 0; k < K; ++k)
           if (in[k])
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(row_ptr<TS>(a.dsum, a.lddsum, base + step + lane_row) + col0 + k * dcol));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(row_ptr<TS>(a.dsum, a.lddsum, base + step + lane_row) + span(k).c + span(k).lo));
       }
     }
     if (!dead) dead = !mbar_wait_u32(smem_u32(&full[st]), pass);
@@ -477,9 +539,9 @@ __global__ void __maxnreg__(K == 2 ? 80 : KEEP ? 168 : 128) k_add_rmsnorm_bwd_ri
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (!in[k]) continue;
-        lds_unit(at_a0 + at + (uint32_t)(k * dcol) * sizeof(TA), dh);
-        lds_unit(at_s0 + at + (uint32_t)(k * dcol) * sizeof(TS), s);
-        bwd_sums(unpack(dh), unpack(s), KEEP ? gain[k] : gain_at(k), rstd2, acc[k], dot2);
+        const F8 g = lds_row(at_a0 + at + (uint32_t)(k * dcol) * sizeof(TA), k, dh);
+        const F8 n = lds_row(at_s0 + at + (uint32_t)(k * dcol) * sizeof(TS), k, s);
+        bwd_sums(g, n, KEEP ? gain[k] : gain_at(k), rstd2, acc[k], dot2);
       }
     }
     // the row's sum: lanes by a butterfly, then all warps of the row (unused
@@ -514,15 +576,21 @@ __global__ void __maxnreg__(K == 2 ? 80 : KEEP ? 168 : 128) k_add_rmsnorm_bwd_ri
       for (int k = 0; k < K; ++k) {
         if (!in[k]) continue;
         const uint32_t pa = at_a0 + at + (uint32_t)(k * dcol) * sizeof(TA), ps = at_s0 + at + (uint32_t)(k * dcol) * sizeof(TS);
+        const Span p = span(k);
+        const bool whole = !SHIFT || (p.lo == 0 && p.hi == 8);
         lds_unit(pa, dh);
         lds_unit(ps, s);
         if (ring_d) lds_unit(at_d0 + at + (uint32_t)(k * dcol) * sizeof(TS), ds);
-        else if (a.dsum) ld_unit(row_ptr<TS>(a.dsum, a.lddsum, base + lane_row) + col0 + k * dcol, ds);
+        else if (a.dsum) load_unit<MODE>(row_ptr<TS>(a.dsum, a.lddsum, base + lane_row) + p.c, p.lo, p.hi, ds);
         F8 v = bwd_unit(unpack(dh), unpack(s), KEEP ? gain[k] : gain_at(k), a.dsum ? unpack(ds) : F8{}, rstd2, c2);
-        if (a.dr) sts_unit(ps, v, TS());
+        if (a.dr) {
+          if (whole) sts_unit(ps, v, TS());
+          else store_unit<MODE>(row_ptr<TS>(a.dr, a.lddr, base + lane_row) + p.c, p.lo, p.hi, v);
+        }
         if (a.dx) {
-          if (a.d.threshold) drop_unit<kAligned>(v, unit + k * tpr, 0, words, a.d);
-          sts_unit(pa, v, TA());
+          if (a.d.threshold) drop_unit<MODE>(v, unit + k * tpr, m, words, a.d);
+          if (whole) sts_unit(pa, v, TA());
+          else store_unit<MODE>(row_ptr<TA>(a.dx, a.lddx, base + lane_row) + p.c, p.lo, p.hi, v);
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -547,8 +615,8 @@ __global__ void __maxnreg__(K == 2 ? 80 : KEEP ? 168 : 128) k_add_rmsnorm_bwd_ri
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c = col0 + k * dcol;
-    if (c < a.cols) store_unit<kScalar>((rpb == 1 ? part : comb + lane_row * a.cols) + c, 0, 8, acc[k]);
+    const Span p = span(k);
+    if (in[k]) store_unit<kScalar>((rpb == 1 ? part : comb + lane_row * a.cols) + p.c, p.lo, p.hi, acc[k]);
   }
   if (rpb == 1) return;
   __syncthreads();
@@ -604,6 +672,15 @@ void pick_threads(int64_t rows, int64_t per_row, bool groups, int32_t* tpr, int3
 }
 
 constexpr int kMaxParts = 1024;   // blocks of the backward kernel, and so partial rows of dg
+
+// Blocks of a persistent grid over `blocks` blocks' worth of rows: a multiple
+// of eight if there is more than one pass, so that a thread's rows all start
+// the same number of columns past a unit.
+inline int64_t grid_blocks(int64_t blocks, int64_t resident) {
+  const int64_t most = std::min<int64_t>(resident, kMaxParts);
+  return blocks <= most ? blocks : std::max<int64_t>(8, most / 8 * 8);
+}
+
 constexpr unsigned kTypes = 1u << SF_BF16 | 1u << SF_FP32;
 
 template <typename TA, typename TS>
@@ -617,8 +694,9 @@ struct Fwd {
 template <typename TA, typename TS>
 struct Bwd {
   static const void* ptr(RowMode mode) {
-    // shifted rows gain nothing here (16384 x 4095: 375 us, 349 element by element)
-    return mode == kAligned ? (const void*)&k_add_rmsnorm_bwd<TA, TS, kAligned> : (const void*)&k_add_rmsnorm_bwd<TA, TS, kScalar>;
+    return mode == kAligned   ? (const void*)&k_add_rmsnorm_bwd<TA, TS, kAligned>
+           : mode == kShifted ? (const void*)&k_add_rmsnorm_bwd<TA, TS, kShifted>
+                              : (const void*)&k_add_rmsnorm_bwd<TA, TS, kScalar>;
   }
 };
 template <template <typename, typename> class K>
@@ -638,8 +716,8 @@ RowMode call_mode(const sf_matrix* const (&ms)[N], const void* gain, int32_t gai
 constexpr size_t kSmemPerSm = 222 << 10;
 
 // Bytes of one row in the staged kernel's ring.
-inline size_t ring_row_bytes(int64_t cols, int32_t ta, int32_t ts, bool dsum) {
-  return (size_t)cols * (dtype_bytes(ta) + (dsum ? 2 : 1) * dtype_bytes(ts));
+inline size_t ring_row_bytes(int64_t cols, bool shifted, int32_t ta, int32_t ts, bool dsum) {
+  return (size_t)(shifted ? (cols + 15) / 8 * 8 : cols) * (dtype_bytes(ta) + (dsum ? 2 : 1) * dtype_bytes(ts));
 }
 
 // The staged kernel takes aligned rows of whole units, long enough that a
@@ -647,16 +725,20 @@ inline size_t ring_row_bytes(int64_t cols, int32_t ta, int32_t ts, bool dsum) {
 // in shared memory (without dsum if need be: 8192 x 12288 bf16, fp32 stream,
 // 293 us, against 382 us with loads into registers), when there is more than
 // one block's worth of rows an SM.
-inline bool ring_fits(int64_t rows, int64_t cols, int32_t ta, int32_t ts) {
-  return cols % 8 == 0 && cols >= 512 && rows >= 2 * sm_count() &&
-         kMinStages * ring_row_bytes(cols, ta, ts, false) <= kSmemPerSm - 1024;
+inline bool ring_fits(int64_t rows, int64_t cols, RowMode mode, int32_t ta, int32_t ts) {
+  return (mode == kShifted || (mode == kAligned && cols % 8 == 0)) && cols >= 512 && rows >= 2 * sm_count() &&
+         kMinStages * ring_row_bytes(cols, mode == kShifted, ta, ts, false) <= kSmemPerSm - 1024;
 }
 
 template <typename TA, typename TS>
-const void* ring_kernel(int k, bool keep) {
-  return k == 2 ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 2, true>
-         : keep ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4, true>
-                : (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4, false>;
+const void* ring_kernel(int k, bool keep, bool shifted) {
+  if (shifted)
+    return k == 2 ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 2, true, true>
+           : keep ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4, true, true>
+                  : (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4, false, true>;
+  return k == 2 ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 2, true, false>
+         : keep ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4, true, false>
+                : (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4, false, false>;
 }
 
 // Two units a thread up to 1024 columns, four beyond (16384 x 4096 bf16, all
@@ -664,10 +746,11 @@ const void* ring_kernel(int k, bool keep) {
 // row outweighs fewer warps), and the gains in registers where a block's
 // registers allow (118 us, against 130 us read from L1 in both passes); as many
 // blocks an SM as registers and three stages each allow.
-sf_status launch_ring(BwdArgs& a, int32_t ta, int32_t ts, cudaStream_t st, int64_t* parts) {
+sf_status launch_ring(BwdArgs& a, bool shifted, int32_t ta, int32_t ts, cudaStream_t st, int64_t* parts) {
   using B = __nv_bfloat16;
-  const int k = a.per_row <= 128 ? 2 : 4;
-  const int t = ceil_div(a.per_row, k);
+  const int units = a.per_row + (shifted ? 1 : 0);
+  const int k = units <= 128 ? 2 : 4;
+  const int t = ceil_div(units, k);
   if (t > 64) {
     a.tpr = ceil_div(t, 32) * 32;
     a.rpb = 1;
@@ -677,15 +760,15 @@ sf_status launch_ring(BwdArgs& a, int32_t ta, int32_t ts, cudaStream_t st, int64
   }
   const int threads = a.tpr * a.rpb;
   const bool keep = threads <= 384;
-  const void* kernel = ta == SF_BF16 ? (ts == SF_BF16 ? ring_kernel<B, B>(k, keep) : ring_kernel<B, float>(k, keep))
-                                     : (ts == SF_BF16 ? ring_kernel<float, B>(k, keep) : ring_kernel<float, float>(k, keep));
-  a.ring_dsum = a.dsum && kMinStages * a.rpb * ring_row_bytes(a.cols, ta, ts, true) <= kSmemPerSm - 1024;
-  const size_t stage = a.rpb * ring_row_bytes(a.cols, ta, ts, a.ring_dsum);
-  const int per_sm = (int)std::max<size_t>(1, std::min<size_t>((k == 2 ? 768 : keep ? 384 : 512) / threads, kSmemPerSm / (kMinStages * stage + 1024)));
+  const void* kernel = ta == SF_BF16 ? (ts == SF_BF16 ? ring_kernel<B, B>(k, keep, shifted) : ring_kernel<B, float>(k, keep, shifted))
+                                     : (ts == SF_BF16 ? ring_kernel<float, B>(k, keep, shifted) : ring_kernel<float, float>(k, keep, shifted));
+  a.ring_dsum = a.dsum && kMinStages * a.rpb * ring_row_bytes(a.cols, shifted, ta, ts, true) <= kSmemPerSm - 1024;
+  const size_t stage = a.rpb * ring_row_bytes(a.cols, shifted, ta, ts, a.ring_dsum);
+  const int per_sm = (int)std::max<size_t>(1, std::min<size_t>((k == 2 && !shifted ? 768 : keep && k == 4 ? 384 : 512) / threads, kSmemPerSm / (kMinStages * stage + 1024)));
   const int stages = (int)std::min<size_t>(kMaxStages, (kSmemPerSm / per_sm - 1024) / stage);
   const size_t smem = stage * stages;
   SF_TRY(allow_dynamic_smem(kernel, smem));
-  *parts = std::min<int64_t>({ceil_div<int64_t>(a.rows, a.rpb), (int64_t)sm_count() * per_sm, kMaxParts});
+  *parts = grid_blocks(ceil_div<int64_t>(a.rows, a.rpb), (int64_t)sm_count() * per_sm);
   void* args[] = {&a, const_cast<int*>(&stages)};
   SF_CUDA_TRY(cudaLaunchKernel(kernel, dim3((unsigned)*parts), dim3(threads), args, smem, st), "launch k_add_rmsnorm_bwd_ring");
   return SF_OK;
@@ -821,25 +904,26 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum, con
   a.cols = (int32_t)cols;
   a.per_row = (int32_t)ceil_div<int64_t>(cols, 8);
   a.inv_cols = (float)(1.0 / (double)cols);
-  pick_threads(rows, a.per_row, false, &a.tpr, &a.rpb);
-  const int threads = a.tpr * a.rpb, rpb = a.rpb;
-  const int64_t blocks = ceil_div<int64_t>(rows, rpb);
-  const int64_t resident = (int64_t)sm_count() * std::max(1, 512 / threads);
-  const int64_t grid = std::min({blocks, resident, (int64_t)kMaxParts});
-  const size_t smem = dgain && rpb > 1 ? (size_t)rpb * cols * sizeof(float) : 0;   // <= 16 KB: rpb * cols <= 4096
   const sf_matrix* const all[5] = {dh, sum, dsum, dresidual, dx};
-  int shift = 0;
-  const RowMode mode = call_mode(all, gain, gain_dtype, &shift);
+  RowMode mode = call_mode(all, gain, gain_dtype, &a.shift);
+  if (mode == kShifted && cols > kMaxCols - 8) mode = kScalar;      // as in the forward pass
+  pick_threads(rows, a.per_row + (mode == kShifted ? 1 : 0), false, &a.tpr, &a.rpb);
+  const int threads = a.tpr * a.rpb, rpb = a.rpb;
+  const int64_t grid = grid_blocks(ceil_div<int64_t>(rows, rpb), (int64_t)sm_count() * std::max(1, 512 / threads));
+  // a few KB with several rows a block, up to 64 KB shifted
+  const size_t smem = mode == kShifted || (dgain && rpb > 1) ? (size_t)rpb * (8 * a.per_row + 8) * sizeof(float) : 0;
   cudaStream_t st = as_stream(stream);
   int64_t parts = grid;
   // bulk copies take this device's own memory only (pinned host rows go the plain way)
   auto local = [](const sf_matrix* m) { return !m || on_current_device(m->data); };
-  if (mode == kAligned && ring_fits(rows, cols, dh->dtype, sum->dtype) && local(dh) && local(sum) && local(dsum) &&
+  if (ring_fits(rows, cols, mode, dh->dtype, sum->dtype) && local(dh) && local(sum) && local(dsum) &&
       local(dresidual) && local(dx)) {
-    SF_TRY(launch_ring(a, dh->dtype, sum->dtype, st, &parts));
+    SF_TRY(launch_ring(a, mode == kShifted, dh->dtype, sum->dtype, st, &parts));
   } else if (grid) {
     void* args[] = {&a};
-    SF_CUDA_TRY(cudaLaunchKernel(pick<Bwd>(dh->dtype, sum->dtype, mode), dim3((unsigned)grid), dim3(threads), args, smem, st),
+    const void* kernel = pick<Bwd>(dh->dtype, sum->dtype, mode);
+    if (smem > (48 << 10)) SF_TRY(allow_dynamic_smem(kernel, smem));
+    SF_CUDA_TRY(cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3(threads), args, smem, st),
                 "launch k_add_rmsnorm_bwd");
   }
   if (dgain) {

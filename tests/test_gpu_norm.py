@@ -216,9 +216,12 @@ def test_add_rmsnorm_forward_zero_rows_and_special_values():
 # enough aligned rows for the staged form: one and several rows a block, two and four units a thread, one stage
 STAGED = [(1000, 512, 0, 0), (777, 520, 8, 32), (610, 1024, 0, 0), (320, 4104, 24, 0), (310, 8192, 0, 0), (305, 12288, 0, 0),
           (308, 16384, 0, 0)]
+# the same for rows that start off a unit, at every step between rows
+STAGED_SHIFTED = [(2500, 515, 0, 0), (4000, 1013, 0, 0), (3333, 1030, 0, 0), (950, 4100, 0, 0), (1400, 2043, 3, 16),
+                  (640, 6001, 0, 0), (620, 12285, 0, 0), (400, 16373, 0, 0)]
 
 
-@pytest.mark.parametrize("rows,cols,pad,lead", SHAPES + SHIFTED + STAGED)
+@pytest.mark.parametrize("rows,cols,pad,lead", SHAPES + SHIFTED + STAGED + STAGED_SHIFTED)
 @pytest.mark.parametrize("at,st,gt,dgt,stream_grad,p", [
     (BF, BF, BF, F32, True, 0.0), (BF, F32, F32, BF, True, 0.1), (F32, F32, F32, F32, False, 0.25), (F32, BF, BF, F32, True, 0.0),
 ])
@@ -272,7 +275,32 @@ def test_add_rmsnorm_backward_many_rows_and_no_rows():
     assert not dg.any()
 
 
-@pytest.mark.parametrize("rows,cols", [(130, 520), (400, 517)])
+@pytest.mark.parametrize("st", [BF, F32])
+@pytest.mark.parametrize("rows,cols,pad", [(37, 1021, 2), (2500, 1021, 6), (700, 63, 4), (650, 4100, 1), (40, 16369, 4)])
+def test_what_lies_beside_the_rows_stays_out(rows, cols, pad, st):
+    # the same rows in a buffer whose padding is NaN
+    def both(dtype, seed, std):
+        v, _ = _rows(rows, cols, pad, dtype, seed, std)
+        w = torch.full((rows, cols + pad), float("nan"), dtype=dtype, device=DEV)[:, :cols]
+        w.copy_(v)
+        return v, w
+    dh, s, ds = both(BF, 71, 1e-3), both(st, 72, 1.5), both(st, 73, 1e-3)
+    gain = (1.0 + synth.normal((cols,), 0.2, 74)).to(DEV)
+    rstd = torch.rsqrt(s[0].float().square().mean(dim=1) + EPS)
+    ws = torch.empty(native.sf_add_rmsnorm_workspace_bytes(rows, cols), dtype=torch.uint8, device=DEV)
+    outs = []
+    for i in range(2):
+        dr, dx = _rows(rows, cols, pad, st)[0], _rows(rows, cols, pad, BF)[0]
+        dg = torch.empty(cols, device=DEV)
+        native.sf_add_rmsnorm_backward(dh[i], s[i], gain, rstd, dsum=ds[i], dresidual=dr, dx=dx, dgain=dg, p=0.1,
+                                       rng=native.rng(SEED, OFF), ws=ws)
+        outs.append((dr, dx, dg))
+    native.sf_sync_status()
+    for a, b in zip(*outs):
+        assert torch.equal(a, b) and bool(torch.isfinite(a).all())
+
+
+@pytest.mark.parametrize("rows,cols", [(130, 520), (400, 517), (2500, 1021)])
 def test_sum_and_outputs_in_place(rows, cols):
     x, r = synth.normal((rows, cols), 1.0, 5, dtype=BF).to(DEV), synth.normal((rows, cols), 1.0, 6, dtype=BF).to(DEV)
     gain = torch.ones(cols, dtype=BF, device=DEV)
