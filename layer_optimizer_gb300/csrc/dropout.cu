@@ -10,8 +10,8 @@
 // was 40 % slower), and products and additions go two at a time, so that the
 // generator's 2.5 wide multiplications an element stay in the shadow of the
 // loads: 16384 x 4096 bf16 with a bf16 residual 59.8 us, 6.7 TB/s, the copy
-// rate.  Rows that start off a unit cost a second generator evaluation a unit
-// (16384 x 4095: 126 us).
+// rate.  In rows that start off a unit, each unit's bits come from two
+// evaluations, its own and the neighbouring lane's (16384 x 4095: 100 us).
 #include <algorithm>
 
 #include "rows.cuh"
@@ -33,6 +33,8 @@ struct DropoutArgs {
   int32_t cols;         // (not FLAT)
   int32_t shift;        // kShifted
   int32_t per_thread;   // units a thread takes, 1..kUnits
+  uint32_t div_mul;     // b / per_row = (mulhi(b, div_mul) + b) >> div_shift for b < 2^31
+  int32_t div_shift;    // (Granlund and Montgomery, "Division by invariant integers using multiplication", 1994)
   DropConsts d;
 };
 
@@ -42,14 +44,18 @@ struct DropoutArgs {
 template <typename TX, typename TY, bool RES, int MODE, bool FLAT>
 __global__ void __launch_bounds__(kThreads) k_dropout(const DropoutArgs a) {
   const DropWords words = drop_words(a.d);
-  const int64_t b0 = (int64_t)blockIdx.x * (a.per_thread * kThreads) + threadIdx.x;
+  const int lane = threadIdx.x & 31;
+  // shifted: a warp's units are consecutive, so that the lanes can hand the
+  // generator's words on; otherwise a block's are
+  const int64_t b0 = (int64_t)blockIdx.x * (a.per_thread * kThreads) + (MODE == kShifted ? (threadIdx.x - lane) * a.per_thread + lane : threadIdx.x);
+  constexpr int kStep = MODE == kShifted ? 32 : kThreads;
   Unit<TX> x[kUnits];
   Unit<TY> r[kUnits];
   // the k-th unit's row, unit of the row, the row's shift, and its columns
   auto place = [&](int k, int64_t& row, int& u, int& m) {
-    const int64_t b = b0 + k * kThreads;
+    const int64_t b = b0 + k * kStep;
     if (k >= a.per_thread || b >= a.units) return Span{0, 0, 0};
-    row = a.units <= INT32_MAX ? (int64_t)((uint32_t)b / (uint32_t)a.per_row) : b / a.per_row;
+    row = a.units <= INT32_MAX ? (int64_t)((__umulhi((uint32_t)b, a.div_mul) + (uint32_t)b) >> a.div_shift) : b / a.per_row;
     u = (int)(b - row * a.per_row);
     m = MODE == kShifted ? (int)(row * a.shift) & 7 : 0;
     return unit_span<MODE>(u, m, a.cols);
@@ -57,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const DropoutArgs a) {
 #pragma unroll
   for (int k = 0; k < kUnits; ++k) {
     if (FLAT) {
-      const int64_t b = b0 + k * kThreads;
+      const int64_t b = b0 + k * kStep;
       if (k >= a.per_thread || b >= a.units) continue;
       ld_unit(static_cast<const TX*>(a.x) + 8 * b, x[k]);
       if (RES) ld_unit(static_cast<const TY*>(a.r) + 8 * b, r[k]);
@@ -70,20 +76,35 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const DropoutArgs a) {
       if (RES) load_unit<MODE>(row_ptr<TY>(a.r, a.ldr, row) + s.c, s.lo, s.hi, r[k]);
     }
   }
-#pragma unroll
-  for (int k = 0; k < kUnits; ++k) {
-    const int64_t b = b0 + k * kThreads;
+  ShiftedBits bits;
+  if (MODE == kShifted && a.d.threshold) {
+    // the counter before the warp's first unit's, if that does not begin a row
     int64_t row = 0;
     int u = 0, m = 0;
+    place(0, row, u, m);
+    const int64_t before = __shfl_sync(0xffffffffu, u ? row * a.counters + u - 1 : (int64_t)-1, 0);
+    if (before >= 0) bits.start((uint64_t)before, words, a.d);
+  }
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    const int64_t b = b0 + k * kStep;
+    int64_t row = 0;
+    int u = 0, m = 0;
+    uint32_t w[4];
     Span s = {0, 0, 8};
     if (FLAT) {
       if (k >= a.per_thread || b >= a.units) continue;
     } else {
       s = place(k, row, u, m);
+      if (MODE == kShifted && a.d.threshold && k < a.per_thread)
+        bits.next((uint64_t)(row * a.counters + u), lane, 32, m, words, a.d, w);
       if (!s.some()) continue;
     }
     F8 v = unpack(x[k]);
-    if (a.d.threshold) drop_unit<MODE>(v, (uint64_t)(FLAT ? b : row * a.counters + u), m, words, a.d);
+    if (a.d.threshold) {
+      if (MODE == kShifted) drop_apply(v, w, a.d);
+      else drop_unit(v, (uint64_t)(FLAT ? b : row * a.counters + u), words, a.d);
+    }
     if (RES) {
       const F8 w = unpack(r[k]);
 #pragma unroll
@@ -160,6 +181,9 @@ sf_status sf_dropout(const sf_matrix* x, const sf_matrix* residual, const sf_mat
   a.counters = ceil_div<int64_t>(x->cols, 8);
   a.per_row = a.counters + (mode == kShifted ? 1 : 0);
   a.units = a.per_row * x->rows;
+  while ((int64_t)1 << a.div_shift < a.per_row) ++a.div_shift;
+  if (a.div_shift < 32)
+    a.div_mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << a.div_shift) - (uint64_t)a.per_row)) / (uint64_t)a.per_row + 1);
   // one unit a thread while that leaves SMs idle, else four loads in flight
   a.per_thread = (int32_t)std::clamp<int64_t>(a.units / ((int64_t)kThreads * sm_count() * 4), 1, kUnits);
   const int64_t grid = ceil_div<int64_t>(a.units, (int64_t)kThreads * a.per_thread);

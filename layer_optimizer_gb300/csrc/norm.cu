@@ -10,11 +10,12 @@
 // over the row by shuffles and one shared-memory step, and h is written from
 // the registers.  Bound by HBM: a bf16 row moves 8 bytes a column (x, r, s,
 // h).  What it took to get there: registers few enough for 24 and more warps
-// an SM (72 a thread in bf16; at 96 the same kernel takes 90 us instead of
-// 81.5), blocks of whole warps rather than powers of two, fp32 arithmetic in
-// pairs, one division a scale group.  16384 x 4096 bf16 81.5 us (6.6 TB/s);
-// 8192 x 12288, fp32 stream, e4m3 with 128-column groups 168 us (6.6 TB/s);
-// one row of 4096 3.3 us.  Dropout on: 96 us at 16384 x 4096.
+// an SM (72 a thread in bf16; at 96 the same kernel takes 90 us instead of 81;
+// rows that start off a unit get 96 all the same, or they spill), blocks of
+// whole warps rather than powers of two, fp32 arithmetic in pairs, one
+// division a scale group.  16384 x 4096 bf16 81 us (6.6 TB/s); 8192 x 12288,
+// fp32 stream, e4m3 with 128-column groups 168 us (6.6 TB/s); one row of 4096
+// 3.3 us.  Dropout on: 91 us at 16384 x 4096, 169 at 16384 x 4095.
 //
 // The norm is taken of s in fp32, before s is rounded to its stored type, so
 // storing s in bf16 costs h no precision; the backward pass uses the stored s.
@@ -47,6 +48,7 @@ struct FwdArgs {
   int32_t shift;         // kShifted
   int32_t tpr;           // threads a row: a power of two up to 64, or the whole block (a multiple of 32)
   int32_t rpb;           // rows a block
+  int32_t units;         // units a thread, 1..kK
   int32_t gain_fp32;
   int32_t group_log2;    // columns of a scale group; 0: one scale a row
   int32_t n_groups;
@@ -88,6 +90,18 @@ __device__ __forceinline__ F8 load_gain(const void* g, int fp32, const Span& s) 
   return unpack(u);
 }
 
+// A thread's units of a row: first + k * step.  Shifted: the units of 32
+// lanes (or of a shorter row's) are consecutive, for ShiftedBits; otherwise
+// those of the whole row's threads.
+struct UnitWalk {
+  int first, step, lane;      // lane: among those
+  template <int MODE>
+  __device__ __forceinline__ static UnitWalk of(int t, int tpr, int units) {
+    const int w = min(tpr, 32), lane = t & (w - 1);
+    return MODE == kShifted ? UnitWalk{(t - lane) * units + lane, w, lane} : UnitWalk{t, tpr, lane};
+  }
+};
+
 // Maximum that keeps a NaN: a NaN in a group must reach its scale.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -122,13 +136,14 @@ __device__ __forceinline__ float group_scale(float amax, float* inv) {
 }
 
 template <typename TA, typename TS, int MODE>
-__global__ void __maxnreg__(sizeof(TA) + sizeof(TS) == 4 ? 72 : 80) k_add_rmsnorm_fwd(const FwdArgs a) {
+__global__ void __maxnreg__(MODE == kShifted ? 96 : sizeof(TA) + sizeof(TS) == 4 ? 72 : 80) k_add_rmsnorm_fwd(const FwdArgs a) {
   __shared__ float red[2][kMaxThreads / 32];
   const int tpr = a.tpr, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
   const int64_t row = (int64_t)blockIdx.x * a.rpb + lane_row;
   const bool on = row < a.rows;
   const int m = MODE == kShifted ? (int)(row * a.shift) & 7 : 0;
-  auto span = [&](int k) { return unit_span<MODE>(t + k * tpr, m, on ? a.cols : 0); };
+  const UnitWalk at = UnitWalk::of<MODE>(t, tpr, a.units);
+  auto span = [&](int k) { return unit_span<MODE>(at.first + k * at.step, m, (MODE != kShifted || k < a.units) && on ? a.cols : 0); };
   F8 s[kK];
   {
     Unit<TA> x[kK];
@@ -143,13 +158,23 @@ __global__ void __maxnreg__(sizeof(TA) + sizeof(TS) == 4 ? 72 : 80) k_add_rmsnor
       if (a.r) load_unit<MODE>(rp + p.c, p.lo, p.hi, r[k]);
     }
     const DropWords words = a.d.threshold ? drop_words(a.d) : DropWords{};
+    const uint64_t b0 = (uint64_t)(row * a.per_row + at.first);
+    ShiftedBits bits;
+    if (MODE == kShifted && a.d.threshold && t > at.lane) bits.start(b0 - at.lane - 1, words, a.d);
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[k].p[i] = 0;
+      if (MODE == kShifted && k >= a.units) continue;
+      uint32_t w[4];
+      if (MODE == kShifted && a.d.threshold)
+        bits.next(b0 + k * at.step, at.lane, min(tpr, 32), m, words, a.d, w);
       if (!span(k).some()) continue;
       s[k] = unpack(x[k]);
-      if (a.d.threshold) drop_unit<MODE>(s[k], (uint64_t)(row * a.per_row + t + k * tpr), m, words, a.d);
+      if (a.d.threshold) {
+        if (MODE == kShifted) drop_apply(s[k], w, a.d);
+        else drop_unit(s[k], b0 + k * at.step, words, a.d);
+      }
       if (a.r) {
         const F8 w = unpack(r[k]);
 #pragma unroll
@@ -181,7 +206,7 @@ __global__ void __maxnreg__(sizeof(TA) + sizeof(TS) == 4 ? 72 : 80) k_add_rmsnor
       for (int i = 0; i < 4; ++i) s[k].p[i] = mul2(mul2(s[k].p[i], rstd2), g.p[i]);
       if (a.h) store_unit<MODE>(hp + p.c, p.lo, p.hi, s[k]);
     }
-    if (a.q) {
+    if (a.q && k < a.units) {
       float top = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -259,7 +284,7 @@ struct BwdArgs {
   int64_t rows;
   int32_t cols, per_row;
   int32_t shift;         // kShifted
-  int32_t tpr, rpb;      // as in FwdArgs
+  int32_t tpr, rpb, units;      // as in FwdArgs
   int32_t gain_fp32;
   float inv_cols;
   DropConsts d;
@@ -308,9 +333,10 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
   const DropWords words = a.d.threshold ? drop_words(a.d) : DropWords{};
   const int m = MODE == kShifted ? (int)(((int64_t)blockIdx.x * rpb + lane_row) * a.shift) & 7 : 0;
   float* mine = comb + lane_row * (8 * a.per_row + 8);
+  const UnitWalk at = UnitWalk::of<MODE>(t, tpr, a.units);
   if (MODE == kShifted) {
-    for (int k = 0; k < kK; ++k) {
-      const Span p = unit_span<MODE>(t + k * tpr, m, a.cols);
+    for (int k = 0; k < a.units; ++k) {
+      const Span p = unit_span<MODE>(at.first + k * at.step, m, a.cols);
       if (!p.some()) continue;
       Unit<float> u;
       pack(load_gain<MODE>(a.gain, a.gain_fp32, p), u);
@@ -327,7 +353,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
   int parity = 0;
   for (int64_t base = (int64_t)blockIdx.x * rpb; base < a.rows; base += (int64_t)gridDim.x * rpb, parity ^= 1) {
     const int64_t row = base + lane_row;
-    auto span = [&](int k) { return unit_span<MODE>(t + k * tpr, m, row < a.rows ? a.cols : 0); };
+    auto span = [&](int k) { return unit_span<MODE>(at.first + k * at.step, m, (MODE != kShifted || k < a.units) && row < a.rows ? a.cols : 0); };
     Unit<TA> dh[kK];
     Unit<TS> s[kK], ds[kK];
 #pragma unroll
@@ -350,14 +376,24 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
     const float dot = row_reduce<false>(f2(dot2).x + f2(dot2).y, tpr, red[parity]);
     const float c = -rstd * (rstd * (rstd * dot * a.inv_cols));
     const uint64_t c2 = f2(c, c);
+    const bool drop = a.dx && a.d.threshold;
+    const uint64_t b0 = (uint64_t)(row * a.per_row + at.first);
+    ShiftedBits bits;
+    if (MODE == kShifted && drop && t > at.lane) bits.start(b0 - at.lane - 1, words, a.d);
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
       const Span p = span(k);
+      uint32_t w[4];
+      if (MODE == kShifted && drop && k < a.units)
+        bits.next(b0 + k * at.step, at.lane, min(tpr, 32), m, words, a.d, w);
       if (!p.some()) continue;
       F8 v = bwd_unit(unpack(dh[k]), unpack(s[k]), gain_at(p), a.dsum ? unpack(ds[k]) : F8{}, rstd2, c2);
       if (a.dr) store_unit<MODE>(row_ptr<TS>(a.dr, a.lddr, row) + p.c, p.lo, p.hi, v);
       if (a.dx) {
-        if (a.d.threshold) drop_unit<MODE>(v, (uint64_t)(row * a.per_row + t + k * tpr), m, words, a.d);
+        if (drop) {
+          if (MODE == kShifted) drop_apply(v, w, a.d);
+          else drop_unit(v, b0 + k * at.step, words, a.d);
+        }
         store_unit<MODE>(row_ptr<TA>(a.dx, a.lddx, row) + p.c, p.lo, p.hi, v);
       }
     }
@@ -368,7 +404,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
   float* part = a.part + (int64_t)blockIdx.x * a.cols;
 #pragma unroll
   for (int k = 0; k < kK; ++k) {
-    const Span p = unit_span<MODE>(t + k * tpr, m, a.cols);
+    const Span p = unit_span<MODE>(at.first + k * at.step, m, k < a.units ? a.cols : 0);
     if (p.some()) store_unit<kScalar>((rpb == 1 ? part : mine) + p.c, p.lo, p.hi, acc[k]);
   }
   if (rpb == 1) return;
@@ -410,7 +446,7 @@ constexpr int kMinStages = 3, kMaxStages = 4;
 // that hold any of the row, so that units lie in shared memory as in memory;
 // of the first and last one, the columns outside the row are set to zero, and
 // those inside are written to memory by their threads, the rest by bulk stores
-// (16384 x 4095 bf16: 165 us, with dropout 252, against 349 element by element).
+// (16384 x 4095 bf16: 170 us, with dropout 221, against 349 element by element).
 template <typename TA, typename TS, int K, bool KEEP, bool SHIFT>
 __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) k_add_rmsnorm_bwd_ring(const BwdArgs a, const int stages) {
   constexpr int MODE = SHIFT ? kShifted : kAligned;
@@ -479,29 +515,28 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
       if (first + i * step < a.rows) fill(first + i * step, i);
 
   const DropWords words = a.d.threshold ? drop_words(a.d) : DropWords{};
-  const int col0 = 8 * t, dcol = 8 * tpr;
+  const UnitWalk walk = UnitWalk::of<MODE>(t, tpr, a.units);
+  const int col0 = 8 * walk.first, dcol = 8 * walk.step;
   const int m = SHIFT ? (int)((first + lane_row) * a.shift) & 7 : 0;
-  auto span = [&](int k) { return unit_span<MODE>(t + k * tpr, m, a.cols); };
+  auto span = [&](int k) { return unit_span<MODE>(walk.first + k * walk.step, m, !SHIFT || k < a.units ? a.cols : 0); };
   bool in[K];
   F8 acc[K] = {}, gain[K];      // KEEP: a thread's gains stay in registers
-  auto gain_at = [&](int k) { return in[k] ? load_gain<MODE>(a.gain, a.gain_fp32, span(k)) : F8{}; };
+  auto gain_at = [&](int k) {
+    return in[k] ? load_gain<MODE>(a.gain, a.gain_fp32, SHIFT ? span(k) : Span{col0 + k * dcol, 0, 8}) : F8{};
+  };
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    in[k] = span(k).some();
+    in[k] = SHIFT ? span(k).some() : col0 + k * dcol < a.cols;
     if (KEEP) gain[k] = gain_at(k);
   }
-  // a unit of a row's place, without what is not the row's
-  auto lds_row = [&](uint32_t at, int k, auto& u) {
-    lds_unit(at, u);
-    F8 v = unpack(u);
-    if (SHIFT) {
-      const Span p = span(k);
-      if (p.lo > 0 || p.hi < 8) {
+  // of a unit at the row's ends, the columns that are the row's
+  auto trim = [&](F8 v, int k) {
+    const Span p = span(k);
+    if (SHIFT && (p.lo > 0 || p.hi < 8)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x = f2(v.p[i]);
-          v.p[i] = f2(2 * i >= p.lo && 2 * i < p.hi ? x.x : 0.0f, 2 * i + 1 >= p.lo && 2 * i + 1 < p.hi ? x.y : 0.0f);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = f2(v.p[i]);
+        v.p[i] = f2(2 * i >= p.lo && 2 * i < p.hi ? x.x : 0.0f, 2 * i + 1 >= p.lo && 2 * i + 1 < p.hi ? x.y : 0.0f);
       }
     }
     return v;
@@ -511,7 +546,7 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
   const uint32_t at_d0 = at_s0 + off_d - off_s;
   const float* rp = a.rstd + first + lane_row;
   float rstd_next = first + lane_row < a.rows ? *rp : 0.0f;
-  uint64_t unit = (uint64_t)((first + lane_row) * a.per_row + t);
+  uint64_t unit = (uint64_t)((first + lane_row) * a.per_row + walk.first);
   uint32_t at = 0;         // offset of the row's stage
   int st = 0, parity = 0;
   uint32_t pass = 0;
@@ -527,7 +562,7 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
 #pragma unroll
         for (int k = 0; k < K; ++k)
           if (in[k])
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(row_ptr<TS>(a.dsum, a.lddsum, base + step + lane_row) + span(k).c + span(k).lo));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(row_ptr<TS>(a.dsum, a.lddsum, base + step + lane_row) + (SHIFT ? span(k).c + span(k).lo : col0 + k * dcol)));
       }
     }
     if (!dead) dead = !mbar_wait_u32(smem_u32(&full[st]), pass);
@@ -539,9 +574,9 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (!in[k]) continue;
-        const F8 g = lds_row(at_a0 + at + (uint32_t)(k * dcol) * sizeof(TA), k, dh);
-        const F8 n = lds_row(at_s0 + at + (uint32_t)(k * dcol) * sizeof(TS), k, s);
-        bwd_sums(g, n, KEEP ? gain[k] : gain_at(k), rstd2, acc[k], dot2);
+        lds_unit(at_a0 + at + (uint32_t)(k * dcol) * sizeof(TA), dh);
+        lds_unit(at_s0 + at + (uint32_t)(k * dcol) * sizeof(TS), s);
+        bwd_sums(trim(unpack(dh), k), trim(unpack(s), k), KEEP ? gain[k] : gain_at(k), rstd2, acc[k], dot2);
       }
     }
     // the row's sum: lanes by a butterfly, then all warps of the row (unused
@@ -571,9 +606,14 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
     }
     const float coef = -rstd * (rstd * (rstd * dot * a.inv_cols));
     const uint64_t c2 = f2(coef, coef);
-    if (on && (a.dr || a.dx)) {
+    if (on && (a.dr || a.dx)) {      // (the same for a whole warp)
+      const bool drop = SHIFT && a.dx && a.d.threshold;
+      ShiftedBits bits;
+      if (SHIFT && drop && t > walk.lane) bits.start(unit - walk.lane - 1, words, a.d);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
+        uint32_t w[4];
+        if (SHIFT && drop && 8 * (walk.first - walk.lane + k * walk.step) < a.cols + 7) bits.next(unit + k * walk.step, walk.lane, 32, m, words, a.d, w);
         if (!in[k]) continue;
         const uint32_t pa = at_a0 + at + (uint32_t)(k * dcol) * sizeof(TA), ps = at_s0 + at + (uint32_t)(k * dcol) * sizeof(TS);
         const Span p = span(k);
@@ -581,14 +621,18 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
         lds_unit(pa, dh);
         lds_unit(ps, s);
         if (ring_d) lds_unit(at_d0 + at + (uint32_t)(k * dcol) * sizeof(TS), ds);
-        else if (a.dsum) load_unit<MODE>(row_ptr<TS>(a.dsum, a.lddsum, base + lane_row) + p.c, p.lo, p.hi, ds);
+        else if (a.dsum && SHIFT) load_unit<MODE>(row_ptr<TS>(a.dsum, a.lddsum, base + lane_row) + p.c, p.lo, p.hi, ds);
+        else if (a.dsum) ld_unit(row_ptr<TS>(a.dsum, a.lddsum, base + lane_row) + col0 + k * dcol, ds);
         F8 v = bwd_unit(unpack(dh), unpack(s), KEEP ? gain[k] : gain_at(k), a.dsum ? unpack(ds) : F8{}, rstd2, c2);
         if (a.dr) {
           if (whole) sts_unit(ps, v, TS());
           else store_unit<MODE>(row_ptr<TS>(a.dr, a.lddr, base + lane_row) + p.c, p.lo, p.hi, v);
         }
         if (a.dx) {
-          if (a.d.threshold) drop_unit<MODE>(v, unit + k * tpr, m, words, a.d);
+          if (a.d.threshold) {
+            if (SHIFT) drop_apply(v, w, a.d);
+            else drop_unit(v, unit + k * walk.step, words, a.d);
+          }
           if (whole) sts_unit(pa, v, TA());
           else store_unit<MODE>(row_ptr<TA>(a.dx, a.lddx, base + lane_row) + p.c, p.lo, p.hi, v);
         }
@@ -657,18 +701,19 @@ __global__ void __launch_bounds__(1024) k_sum_partials(const float* part, int n_
 // two and shares its block of 128; a longer one has a block of its own, of
 // whole warps (not rounded up further: 12288 columns take 384 threads, two
 // blocks of which fit an SM, where 512 would leave one).
-void pick_threads(int64_t rows, int64_t per_row, bool groups, int32_t* tpr, int32_t* rpb) {
+void pick_threads(int64_t rows, int64_t per_row, bool groups, int32_t* tpr, int32_t* rpb, int32_t* n) {
   const int64_t units = rows < 2 * sm_count() ? 1 : kK;
   int64_t t = std::min<int64_t>(ceil_div<int64_t>(per_row, units), kMaxThreads);
   if (t > 64) {
     *tpr = (int32_t)ceil_div<int64_t>(t, 32) * 32;
     *rpb = 1;
-    return;
+  } else {
+    int p = groups ? 16 : 4;
+    while (p < t) p *= 2;
+    *tpr = p;
+    *rpb = 128 / p;
   }
-  int p = groups ? 16 : 4;
-  while (p < t) p *= 2;
-  *tpr = p;
-  *rpb = 128 / p;
+  *n = (int32_t)ceil_div<int64_t>(per_row, *tpr);
 }
 
 constexpr int kMaxParts = 1024;   // blocks of the backward kernel, and so partial rows of dg
@@ -758,6 +803,7 @@ sf_status launch_ring(BwdArgs& a, bool shifted, int32_t ta, int32_t ts, cudaStre
     a.tpr = t > 32 ? 64 : 32;
     a.rpb = 128 / a.tpr;
   }
+  a.units = ceil_div(units, a.tpr);
   const int threads = a.tpr * a.rpb;
   const bool keep = threads <= 384;
   const void* kernel = ta == SF_BF16 ? (ts == SF_BF16 ? ring_kernel<B, B>(k, keep, shifted) : ring_kernel<B, float>(k, keep, shifted))
@@ -848,7 +894,7 @@ sf_status sf_add_rmsnorm_forward(const sf_matrix* x, const sf_matrix* residual, 
   // a shifted row may touch one unit more, which four units a thread have to
   // cover, and its units straddle scale groups
   if (mode == kShifted && ((h8 && group) || cols > kMaxCols - 8)) mode = kScalar;
-  pick_threads(rows, a.per_row + (mode == kShifted ? 1 : 0), h8 != nullptr, &a.tpr, &a.rpb);
+  pick_threads(rows, a.per_row + (mode == kShifted ? 1 : 0), h8 != nullptr, &a.tpr, &a.rpb, &a.units);
   const int threads = a.tpr * a.rpb;
   const int64_t grid = ceil_div<int64_t>(rows, a.rpb);
   if (grid > INT32_MAX) return fail(SF_ERR_UNSUPPORTED, "too many rows");
@@ -907,7 +953,7 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum, con
   const sf_matrix* const all[5] = {dh, sum, dsum, dresidual, dx};
   RowMode mode = call_mode(all, gain, gain_dtype, &a.shift);
   if (mode == kShifted && cols > kMaxCols - 8) mode = kScalar;      // as in the forward pass
-  pick_threads(rows, a.per_row + (mode == kShifted ? 1 : 0), false, &a.tpr, &a.rpb);
+  pick_threads(rows, a.per_row + (mode == kShifted ? 1 : 0), false, &a.tpr, &a.rpb, &a.units);
   const int threads = a.tpr * a.rpb, rpb = a.rpb;
   const int64_t grid = grid_blocks(ceil_div<int64_t>(rows, rpb), (int64_t)sm_count() * std::max(1, 512 / threads));
   // a few KB with several rows a block, up to 64 KB shifted

@@ -111,7 +111,7 @@ __device__ __forceinline__ void st_unit(float* p, const Unit<float>& u) {
 //   kShifted  row i starts m = i * shift mod 8 columns past a unit, m the same
 //             for all operands (dense rows of an odd length, for example): unit
 //             u holds columns 8 u - m .. 8 u - m + 7, so that whole units are
-//             one access here too (16384 x 4095 bf16: norm with dropout 186 us,
+//             one access here too (16384 x 4095 bf16: norm with dropout 169 us,
 //             against 278 us element by element);
 //   kScalar   anything else, element by element.
 enum RowMode : int { kScalar = 0, kAligned = 1, kShifted = 2 };
@@ -224,30 +224,8 @@ __device__ __forceinline__ void drop_bits(uint64_t b, const DropWords& w2, const
   w[0] = c0, w[1] = c1, w[2] = c2, w[3] = c3;
 }
 
-// Applies the mask to a unit whose columns start m below counter b's eight:
-// with a shift, its bits come from the counters b - 1 and b.
-template <int MODE>
-__device__ __forceinline__ void drop_unit(F8& v, uint64_t b, int m, const DropWords& w2, const DropConsts& d) {
-  uint32_t w[4];
-  drop_bits(b, w2, d, w);
-  if (MODE == kShifted && m) {
-    uint32_t before[4], x[9];
-    drop_bits(b - 1, w2, d, before);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = before[i];
-      x[4 + i] = w[i];
-    }
-    x[8] = 0;
-    // eight halves from half 8 - m (1..7) of the sixteen on
-    const int from = 8 - m;
-#pragma unroll
-    for (int i = 0; i < 7; ++i) x[i] = from & 4 ? x[i + 2] : x[i];
-#pragma unroll
-    for (int i = 0; i < 6; ++i) x[i] = from & 2 ? x[i + 1] : x[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], from & 1 ? 16 : 0);
-  }
+// Applies the mask with a unit's 128 bits.
+__device__ __forceinline__ void drop_apply(F8& v, const uint32_t (&w)[4], const DropConsts& d) {
   // half >= threshold, compared in the upper half of a word (threshold >= 1
   // here, 65536 included); a dropped element is 0 whatever its value
   const uint32_t limit = ((d.threshold - 1) << 16) | 0xFFFFu;
@@ -258,6 +236,43 @@ __device__ __forceinline__ void drop_unit(F8& v, uint64_t b, int m, const DropWo
     v.p[j] = f2((w[j] << 16) > limit ? x.x : 0.0f, w[j] > limit ? x.y : 0.0f);
   }
 }
+__device__ __forceinline__ void drop_unit(F8& v, uint64_t b, const DropWords& w2, const DropConsts& d) {
+  uint32_t w[4];
+  drop_bits(b, w2, d, w);
+  drop_apply(v, w, d);
+}
+
+// The bits of units whose columns start m below counter b's eight: they come
+// from the counters b - 1 and b.  `width` neighbouring lanes take neighbouring
+// units, and lane 0 the one after the last lane's of the call before, so each
+// counter is evaluated once and handed to the next lane (16384 x 4095 bf16,
+// dropout and addition 100 us, with two evaluations a unit 123).  All lanes of a warp call `next` together.
+struct ShiftedBits {
+  uint32_t carry[4];      // lane 0: the words of the counter before its next unit's
+  __device__ __forceinline__ void start(uint64_t before, const DropWords& w2, const DropConsts& d) { drop_bits(before, w2, d, carry); }
+  __device__ __forceinline__ void next(uint64_t b, int lane, int width, int m, const DropWords& w2, const DropConsts& d, uint32_t (&w)[4]) {
+    uint32_t x[9];
+    drop_bits(b, w2, d, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t from_left = __shfl_sync(0xffffffffu, w[i], lane == 0 ? width - 1 : lane - 1, width);
+      x[i] = lane == 0 ? carry[i] : from_left;
+      x[4 + i] = w[i];
+      carry[i] = from_left;
+    }
+    // eight halves from half 8 - m (1..8) of the sixteen on
+    const int from = 8 - m;
+    x[8] = 0;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) x[i] = from & 8 ? x[i + 4] : x[i];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) x[i] = from & 4 ? x[i + 2] : x[i];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) x[i] = from & 2 ? x[i + 1] : x[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], from & 1 ? 16 : 0);
+  }
+};
 
 // A matrix argument as the kernels see it.
 template <typename T>
