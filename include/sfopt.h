@@ -474,7 +474,8 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum,
  *            lce_forward_backward.
  *   piece  : vocabulary rows per piece, a multiple of 256; 0: as many as 1 GiB
  *            of bf16 holds (at least 2048).  Larger pieces compute fewer
- *            logits twice; the last piece's never are.
+ *            logits twice; the last piece's never are, unless D is at most 512
+ *            and it has over 2^26 of them, when that is faster.
  *   grad_scale : multiplies dH and dW (1 for the loss's own gradient; 1 / k
  *            for one of k accumulated micro-batches), not the losses.
  *   loss   : device fp32 [1]: mean over the labelled tokens (0 if none), or NULL.
@@ -484,8 +485,8 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum,
  *   ws     : device scratch of ws_bytes >= lce_vocab_workspace_bytes(N, D, V,
  *            piece), 256-byte aligned.
  * Logits, exponentials and sums in fp32; dZ rounded to bf16 before the two
- * gradient products (the last piece's passes through one more bf16 rounding,
- * its label's entry does not); dH is summed over pieces in fp32 and rounded
+ * gradient products (where the last piece's logits are not computed again it
+ * passes through one more bf16 rounding, its label's entry does not); dH is summed over pieces in fp32 and rounded
  * once.  Deterministic. */
 size_t lce_vocab_workspace_bytes(int64_t n_tokens, int64_t d, int64_t vocab,
                                  int64_t piece);

@@ -133,6 +133,7 @@ int read_and_clear_device_error_norm();
 // 256-column tile, the maximum of the row's values and the sum of
 // exp(value - maximum).
 constexpr int kTcTileN = 256;
+constexpr int kTcStatCols = 128;     // columns of one entry of kTcStats' statistics
 sf_status tc_gemm(const void* A, bool a_mn, const void* B, bool b_mn, float* C, int64_t M, int64_t N, int64_t K,
                   int64_t lda, int64_t ldb, int64_t ldc, float alpha, bool accumulate, cudaStream_t s,
                   float2* row_stats = nullptr);

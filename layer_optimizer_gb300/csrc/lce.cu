@@ -205,7 +205,8 @@ LcePlan plan_lce(int64_t N, int64_t V, int64_t chunk) {
 //      read it there.
 //   1. Z = H W^T once, every tile reduced in the GEMM's epilogue to (max, sum
 //      exp) per row and the labels' logits: the logits never leave tensor
-//      memory.  The last piece's exponentials stay in the workspace.
+//      memory.  The last piece's exponentials stay in the workspace (short
+//      rows apart, whose logits are cheaper to compute again).
 //   2. lse, the tokens' losses, the loss; the last piece's exponentials become
 //      its gradient G = softmax - onehot in bf16.  The factor scale / n stays
 //      out of G: a label's entry is close to -1 / n for every token, and its
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(256) k_lce_rows(const RowsArgs a) {
     for (int u = 0; u < kSpanUnits; ++u) {
       const int c = c0 + 2048 * u;
       if (c >= c1) break;
-      const float tm = st[(a.col0 + c) / kTcTileN].x;
+      const float tm = st[(a.col0 + c) / kTcStatCols].x;
       const float k = exp2_fast(((tm == -INFINITY ? 0.0f : tm) - l) * kLog2eF);
       const uint64_t k2 = pack_f2(k, k);
       const uint32_t in[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
@@ -466,21 +467,29 @@ __global__ void __launch_bounds__(256) k_lce_rows(const RowsArgs a) {
   }
 }
 
-// out [M][N] = sum over the parts [S][M][ld] in part order, rounded to bf16
-// or kept in fp32; with `place`, out's row r is the parts' row place[r], zero
-// where that is -1.  ld is a multiple of 4; out rows are 16-byte aligned.
+// out [M][N] = sum over the parts [S][M][ld], rounded to bf16 or kept in fp32;
+// with `place`, out's row r is the parts' row place[r], zero where that is -1.
+// ld is a multiple of 4; out rows are 16-byte aligned.  A block takes 32 or 256
+// groups of four columns; with eight parts and more, eight threads share a
+// group, each over every eighth part, and their sums are added in order
+// (6 tokens, 64 columns, 62 parts: the whole loss 46 us, with one thread a
+// group 57).
+template <int G>
 __global__ void __launch_bounds__(256) k_lce_sum_parts(const float* parts, int S, int64_t M, int64_t N, int64_t ld,
                                                        const int32_t* place, void* out, int64_t ldo, int fp32) {
+  __shared__ float4 sums[G == 1 ? 1 : G][32];
   griddep_launch_dependents();
   griddep_wait();
+  constexpr int kGroups = 256 / G;
+  const int x = threadIdx.x % kGroups, y = threadIdx.x / kGroups;
   const int64_t per_row = (N + 3) / 4, total = M * per_row;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / per_row, c = 4 * (i - r * per_row);
-    const int64_t from = place ? (int64_t)place[r] : r;
+  for (int64_t base = (int64_t)blockIdx.x * kGroups; base < total; base += (int64_t)gridDim.x * kGroups) {
+    const int64_t i = base + x, r = i / per_row, c = 4 * (i - r * per_row);
+    const int64_t from = i >= total ? -1 : place ? (int64_t)place[r] : r;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (from >= 0) {
-      v = __ldcs(reinterpret_cast<const float4*>(parts + from * ld + c));
-      for (int s = 1; s < S; ++s) {
+#pragma unroll 4
+      for (int s = y; s < S; s += G) {
         const float4 w = __ldcs(reinterpret_cast<const float4*>(parts + ((int64_t)s * M + from) * ld + c));
         v.x += w.x;
         v.y += w.y;
@@ -488,21 +497,36 @@ __global__ void __launch_bounds__(256) k_lce_sum_parts(const float* parts, int S
         v.w += w.w;
       }
     }
-    const float x[4] = {v.x, v.y, v.z, v.w};
+    if (G > 1) {
+      __syncthreads();
+      sums[y % G][x % 32] = v;
+      __syncthreads();
+      if (y > 0) continue;
+#pragma unroll
+      for (int q = 1; q < G; ++q) {
+        const float4 w = sums[q][x % 32];
+        v.x += w.x;
+        v.y += w.y;
+        v.z += w.z;
+        v.w += w.w;
+      }
+    }
+    if (i >= total) continue;
+    const float e[4] = {v.x, v.y, v.z, v.w};
     const int n = (int)min((int64_t)4, N - c);
     if (fp32) {
       float* p = static_cast<float*>(out) + r * ldo + c;
       if (n == 4) *reinterpret_cast<float4*>(p) = v;
       else
-        for (int q = 0; q < n; ++q) p[q] = x[q];
+        for (int q = 0; q < n; ++q) p[q] = e[q];
     } else {
       __nv_bfloat16* p = static_cast<__nv_bfloat16*>(out) + r * ldo + c;
       if (n == 4) {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(e[0], e[1]), hi = __floats2bfloat162_rn(e[2], e[3]);
         *reinterpret_cast<uint2*>(p) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
       } else {
-        for (int q = 0; q < n; ++q) p[q] = __float2bfloat16_rn(x[q]);
+        for (int q = 0; q < n; ++q) p[q] = __float2bfloat16_rn(e[q]);
       }
     }
   }
@@ -525,6 +549,14 @@ int pick_splits(int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
+// Whether the last piece's exponentials are kept (written once, read and
+// written again by the rows kernel) or its logits computed again, which is
+// cheaper for short rows and many logits.  Kept / again, us: 4000 x 64000
+// logits of rows of 256 599 / 522, of 512 734 / 689, of 768 897 / 909; rows
+// of 64 by 65536 outputs, 2048 tokens 311 / 273, 1024 tokens 170 / 171, 512
+// tokens 88 / 102.
+inline bool keeps_exponentials(int64_t N, int64_t D, int64_t cols) { return D > 512 || N * cols <= (int64_t)1 << 26; }
+
 struct VocabPlan {
   int64_t pieces, piece, ldg, ldd, ldc;
   int n_tiles;
@@ -545,7 +577,7 @@ VocabPlan plan_vocab(int64_t N, int64_t D, int64_t V, int64_t piece) {
   p.ldg = ceil_div<int64_t>(p.piece, 64) * 64;
   p.ldd = ceil_div<int64_t>(D, 4) * 4;
   p.ldc = ceil_div<int64_t>(D, 8) * 8;
-  p.n_tiles = (int)ceil_div<int64_t>(V, kTcTileN);
+  p.n_tiles = (int)ceil_div<int64_t>(V, kTcStatCols);
   p.s_dh = pick_splits(N, D, p.piece);
   // the last piece may be shorter than a part count chosen for whole ones
   const int64_t last = V - (p.pieces - 1) * p.piece;
@@ -575,9 +607,11 @@ VocabPlan plan_vocab(int64_t N, int64_t D, int64_t V, int64_t piece) {
 
 sf_status sum_parts(const float* parts, int S, int64_t M, int64_t N, int64_t ld, const int32_t* place, void* out,
                     int64_t ldo, bool fp32, cudaStream_t s) {
-  const int64_t want = ceil_div<int64_t>(M * ceil_div<int64_t>(N, 4), 256);
-  SF_CUDA_TRY(launch_pdl(k_lce_sum_parts, dim3((unsigned)std::min<int64_t>(want, (int64_t)sm_count() * 8)), dim3(256), 0, s,
-                         parts, S, M, N, ld, place, out, ldo, (int)fp32),
+  const bool shared = S >= 8;
+  const int64_t want = ceil_div<int64_t>(M * ceil_div<int64_t>(N, 4), shared ? 32 : 256);
+  SF_CUDA_TRY(launch_pdl(shared ? k_lce_sum_parts<8> : k_lce_sum_parts<1>,
+                         dim3((unsigned)std::min<int64_t>(want, (int64_t)sm_count() * 8)), dim3(256), 0, s, parts, S, M, N, ld,
+                         place, out, ldo, (int)fp32),
               "launch k_lce_sum_parts");
   return SF_OK;
 }
@@ -675,7 +709,7 @@ sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W, con
   const int64_t V = W->rows;
   if (N < 1 || D < 1 || V < 1) return fail(SF_ERR_INVALID, "H and W need at least one row and column");
   if (!labels) return fail(SF_ERR_INVALID, "labels is NULL");
-  if (N > INT32_MAX / 2 || D > INT32_MAX / 2 || V > INT32_MAX / 2) return fail(SF_ERR_UNSUPPORTED, "sizes too large");
+  if (N > INT32_MAX / 2 || D > INT32_MAX / 2 || V > INT32_MAX / 4) return fail(SF_ERR_UNSUPPORTED, "sizes too large");
   if (piece < 0 || piece % kTcTileN) return fail(SF_ERR_INVALID, "piece must be 0 or a positive multiple of 256");
   if (!(grad_scale - grad_scale == 0.0)) return fail(SF_ERR_INVALID, "grad_scale must be finite");
   const sf_matrix* const ins[2] = {H, W};
@@ -760,7 +794,8 @@ sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W, con
   z.label_logit = label_logit;
   z.lse = lse;
   const int64_t last0 = (p.pieces - 1) * p.piece;      // the last piece's first column
-  const int64_t kept0 = grads ? last0 : V;             // columns from here on keep their exponentials
+  // columns from here on keep their exponentials
+  const int64_t kept0 = grads && keeps_exponentials(N, D, V - last0) ? last0 : V;
   z.epi = kTcStats;
   if (kept0 > 0) {
     z.B = Wb;
@@ -789,7 +824,7 @@ sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W, con
   ra.N = N;
   ra.span = 2048;
   int64_t spans = 1;
-  if (grads) {
+  if (kept0 < V) {
     ra.G = G;
     ra.ldg = p.ldg;
     ra.cols = (int32_t)(V - kept0);
@@ -804,7 +839,7 @@ sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W, con
   for (int64_t q = p.pieces - 1; q >= 0; --q) {
     const int64_t v0 = q * p.piece, cols = std::min(p.piece, V - v0);
     const bool first = q == p.pieces - 1;
-    if (!first) {
+    if (!first || kept0 == V) {
       z.epi = kTcGrad;
       z.B = Wb + v0 * W->ld;
       z.N = cols;

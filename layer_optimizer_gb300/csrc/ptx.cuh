@@ -201,6 +201,11 @@ __device__ __forceinline__ void ffma2(uint64_t& acc, uint64_t x, uint64_t v) {
 }
 
 // a * b on both fp32 lanes (IEEE product, round to nearest even).
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));

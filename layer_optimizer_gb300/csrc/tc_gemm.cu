@@ -26,7 +26,7 @@
 //                epilogues have released; tcgen05.commit frees a stage in
 //                both CTAs when its MMAs are done and, after a tile's last
 //                slab, hands the accumulator to both epilogues;
-//   warps 2..5   epilogue: each reads its 32 TMEM lanes (rows) with
+//   warps 2..    epilogue: each reads its 32 TMEM lanes (rows) with
 //                tcgen05.ld and writes (or reduce-adds into) C by tensor
 //                stores from shared memory, while the next tile's MMAs run
 //                into the other accumulator.
@@ -54,13 +54,18 @@ namespace {
 
 constexpr int kPair = 2;                       // CTAs per tile (cta_group::2)
 constexpr int kBM = 128, kBN = 256, kBK = 64;
-// Ring stages, and epilogue staging boxes per warp.  A bf16 C is written at
-// twice the rows per byte and often after few K slabs (dW over few tokens), so
-// its epilogue bounds the tile: it gets 16 boxes in flight for one stage less.
+// Ring stages, epilogue warps, and staging boxes per warp.  The epilogues that
+// write bf16 bound the tile after few K slabs (dW over few tokens, logits of
+// short rows), so eight warps share the tile's columns there (cross-entropy of
+// 262 x 112 x 89236 81 us, with four warps 84; 4463 x 112 x 33329 362 and 384;
+// with 16 boxes and one stage less, long rows lose: 1003 x 2048 x 50001 448
+// us against 429).
 template <int EPI>
 struct TcStages {
-  static constexpr int kRing = EPI == kTcBf16 ? 5 : 6;
-  static constexpr int kBoxes = EPI == kTcBf16 ? 4 : 2;
+  static constexpr int kRing = 6;
+  static constexpr int kWarps = EPI == kTcBf16 || EPI == kTcStats || EPI == kTcGrad ? 8 : 4;
+  static constexpr int kBoxes = 8 / kWarps;
+  static constexpr int kThreads = 64 + 32 * kWarps;
 };
 constexpr int kBRows = kBN / kPair;            // rows of B held by one CTA
 constexpr int kStageA = kBM * kBK * 2;         // 16 KB
@@ -68,10 +73,8 @@ constexpr int kStageB = kBRows * kBK * 2;      // 16 KB
 constexpr int kStageBytes = kStageA + kStageB;
 constexpr int kMnBox = 64 * kBK * 2;           // an MN-major box: 64 MN x 64 K bf16 = 8 KB
 constexpr int kTmemCols = 256;                 // one accumulator; two are allocated
-constexpr int kGemmThreads = 192;
-// the ring and the epilogue's boxes of 4 KB (32 rows x 128 bytes) for 4 warps: the same for both shares
-constexpr size_t kGemmSmem = (size_t)6 * kStageBytes + 4 * 2 * 4096 + 1024 + 256;
-static_assert(kStageBytes == 4 * 2 * 4096, "one ring stage is worth two boxes a warp");
+// the ring and the epilogue's boxes of 4 KB (32 rows x 128 bytes)
+constexpr size_t kGemmSmem = (size_t)TcStages<kTcF32>::kRing * kStageBytes + 8 * 4096 + 1024 + 256;
 
 // Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator
 // (bits 4-5 = 1), A and B bf16 (bits 7-9 and 10-12 = 1), A and B K-major
@@ -344,15 +347,15 @@ __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, uint32
 //             logits themselves never leave tensor memory;
 //   kTcGrad   exp(c - lse) - [column is the label] in bf16, 0 in rows past M.
 template <int EPI>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(TcStages<EPI>::kThreads, 1)
     k_tc_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
               const __grid_constant__ CUtensorMap map_c, const TcGemmArgs g) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  constexpr int kStages = TcStages<EPI>::kRing, kBoxes = TcStages<EPI>::kBoxes;
-  // [ring: kStages x (A 16 KB + B 16 KB)] [epilogue staging: 4 warps x kBoxes x 4 KB] [barriers]
+  constexpr int kStages = TcStages<EPI>::kRing, kBoxes = TcStages<EPI>::kBoxes, kWarps = TcStages<EPI>::kWarps;
+  // [ring: kStages x (A 16 KB + B 16 KB)] [epilogue staging: kWarps x kBoxes x 4 KB] [barriers]
   unsigned char* staging = smem + (size_t)kStages * kStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + 4 * kBoxes * 4096);   // used in the first CTA
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kWarps * kBoxes * 4096);   // used in the first CTA
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;     // [2] accumulator buffer b holds a finished tile
   uint64_t* tempty = tfull + 2;          // [2] both CTAs have read buffer b out (first CTA)
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 4 * kPair);  // one arrival per epilogue warp of the pair
+      mbar_init(&tempty[b], kWarps * kPair);  // one arrival per epilogue warp of the pair
     }
     fence_mbar_init_cluster();
   }
@@ -519,94 +522,120 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const bool empty = slab0(part) >= slab1(part);     // nothing to sum: the accumulator was not written
       const float alpha = EPI != kTcF32 && g.scale ? g.alpha * *g.scale : g.alpha;
       if constexpr (EPI == kTcStats || EPI == kTcGrad || EPI == kTcBf16) {
-        // 32 x 64 bf16 boxes through the warp's staging buffers
+        // 32 x 64 bf16 boxes through the warp's staging buffers; the columns go
+        // by halves of a tile, one entry of the statistics each, shared out
+        // over the warps of a row, as far as C has them
+        static_assert(kBN == 2 * kTcStatCols, "two entries of the statistics a tile");
         const int row0 = m0 + 32 * quarter;
         const bool row_on = row < M;
-        float ref = 0.0f, sum = 0.0f;
+        // a gradient's rows are also read as whole K slabs of 64: zeros past M
+        const bool stored = row0 < (EPI == kTcGrad ? (M + 63) & ~63 : M) && (EPI != kTcStats || g.store);
         int label = -1;                    // the label's column within the tile, if it is one
+        float ref = 0.0f;                  // what the exponents are taken relative to
         if constexpr (EPI != kTcBf16) {
           if (row_on) label = (int)((uint32_t)g.labels[row] - (uint32_t)(g.col0 + n0));
         }
-        if constexpr (EPI == kTcGrad) ref = row_on ? g.lse[row] : INFINITY;      // exp(-infinity) = 0 past M
-        if constexpr (EPI == kTcStats) {
-          float m = -INFINITY;
+        if constexpr (EPI == kTcGrad) ref = row_on ? g.lse[row] : 0.0f;
 #pragma unroll 1
-          for (int c0 = 0; c0 < kBN; c0 += 64) {
+        for (int first = (warp - 2) / 4 * kTcStatCols; first < min(kBN, g.N - n0); first += kWarps / 4 * kTcStatCols) {
+          const int end = min(first + kTcStatCols, g.N - n0);
+          float m = -INFINITY;
+          if constexpr (EPI == kTcStats) {
+#pragma unroll 1
+            for (int c0 = first; c0 < end; c0 += 64) {
+              uint32_t r[64];
+              __syncwarp();
+              tmem_ld64(acc + (uint32_t)c0, r);
+              if (c0 + 64 <= end) {
+#pragma unroll
+                for (int jj = 0; jj < 64; jj += 2) m = fmaxf(fmaxf(m, __uint_as_float(r[jj])), __uint_as_float(r[jj + 1]));
+              } else {
+#pragma unroll
+                for (int jj = 0; jj < 64; ++jj)
+                  if (jj < end - c0) m = fmaxf(m, __uint_as_float(r[jj]));
+              }
+              if ((unsigned)(label - c0) < 64u) {
+#pragma unroll
+                for (int jj = 0; jj < 64; ++jj)
+                  if (label - c0 == jj) g.label_logit[row] = __uint_as_float(r[jj]);
+              }
+            }
+            ref = m == -INFINITY ? 0.0f : m;
+          }
+          // exponentials of pairs: exp2((c - ref) log2 e); kTcBf16 multiplies by alpha
+          const uint64_t minus_ref = pack_f2(-ref, -ref), factor = pack_f2(kLog2e, kLog2e), by = pack_f2(alpha, alpha);
+          uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+          for (int c0 = first; c0 < end; c0 += 64) {
             uint32_t r[64];
             __syncwarp();
             tmem_ld64(acc + (uint32_t)c0, r);
-            const int valid = g.N - (n0 + c0);
-#pragma unroll
-            for (int jj = 0; jj < 64; ++jj)
-              if (jj < valid) m = fmaxf(m, __uint_as_float(r[jj]));
-            if ((unsigned)(label - c0) < 64u) {
-#pragma unroll
-              for (int jj = 0; jj < 64; ++jj)
-                if (label - c0 == jj) g.label_logit[row] = __uint_as_float(r[jj]);
+            const uint32_t buf = stg + (uint32_t)(boxes % kBoxes) * 4096u;
+            if (stored && boxes >= kBoxes) {
+              if (lane == 0) bulk_wait_read<kBoxes - 1>();
+              __syncwarp();
             }
-          }
-          ref = m == -INFINITY ? 0.0f : m;
-          if (row_on) g.row_stats[(int64_t)row * g.stats_ld + (g.col0 + n0) / kBN].x = m;
-        }
-#pragma unroll 1
-        for (int c0 = 0; c0 < kBN; c0 += 64, ++boxes) {
-          uint32_t r[64];
-          __syncwarp();
-          tmem_ld64(acc + (uint32_t)c0, r);
-          const uint32_t buf = stg + (uint32_t)(boxes % kBoxes) * 4096u;
-          const bool out = EPI != kTcStats || g.store;
-          if (out && boxes >= kBoxes) {
-            if (lane == 0) bulk_wait_read<kBoxes - 1>();
-            __syncwarp();
-          }
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int c1 = c0 + 32 * half;
-            float x[32];
-            if constexpr (EPI == kTcBf16) {
+            for (int half = 0; half < 2; ++half) {
+              const int c1 = c0 + 32 * half;
+              float x[32];
 #pragma unroll
-              for (int jj = 0; jj < 32; ++jj) x[jj] = empty ? 0.0f : alpha * __uint_as_float(r[32 * half + jj]);
-            } else {
+              for (int jj = 0; jj < 32; jj += 2) {
+                const uint64_t v = pack_f2(__uint_as_float(r[32 * half + jj]), __uint_as_float(r[32 * half + jj + 1]));
+                const float2 w = unpack_f2(EPI == kTcBf16 ? fmul2(v, by) : fmul2(fadd2(v, minus_ref), factor));
+                x[jj] = EPI == kTcBf16 ? w.x : exp2_approx(w.x);
+                x[jj + 1] = EPI == kTcBf16 ? w.y : exp2_approx(w.y);
+              }
+              if constexpr (EPI == kTcBf16) {
+                if (empty) {
 #pragma unroll
-              for (int jj = 0; jj < 32; ++jj) x[jj] = exp2_approx((__uint_as_float(r[32 * half + jj]) - ref) * kLog2e);
-              if constexpr (EPI == kTcStats) {
-                // four short chains a chunk, then one addition per chunk
-                const int valid = g.N - (n0 + c1);
-                float part4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                  for (int jj = 0; jj < 32; ++jj) x[jj] = 0.0f;
+                }
+              } else if constexpr (EPI == kTcStats) {
+                // short chains, then one addition of them
+                const int valid = end - c1;
+                uint64_t part[2] = {0, 0};
+                if (valid >= 32) {
 #pragma unroll
-                for (int jj = 0; jj < 32; ++jj)
-                  if (jj < valid) part4[jj & 3] += x[jj];
-                sum += (part4[0] + part4[1]) + (part4[2] + part4[3]);
+                  for (int jj = 0; jj < 32; jj += 2) part[jj >> 1 & 1] = fadd2(part[jj >> 1 & 1], pack_f2(x[jj], x[jj + 1]));
+                } else {
+#pragma unroll
+                  for (int jj = 0; jj < 32; jj += 2)
+                    part[jj >> 1 & 1] = fadd2(part[jj >> 1 & 1], pack_f2(jj < valid ? x[jj] : 0.0f, jj + 1 < valid ? x[jj + 1] : 0.0f));
+                }
+                sum[half] = fadd2(sum[half], fadd2(part[0], part[1]));
               } else {
                 if ((unsigned)(label - c1) < 32u) {
 #pragma unroll
                   for (int jj = 0; jj < 32; ++jj)
                     if (label - c1 == jj) x[jj] -= 1.0f;
                 }
+                if (row0 + 32 > M) {
 #pragma unroll
-                for (int jj = 0; jj < 32; ++jj) x[jj] = row_on ? x[jj] : 0.0f;
+                  for (int jj = 0; jj < 32; ++jj) x[jj] = row_on ? x[jj] : 0.0f;
+                }
               }
+              if (stored) stage_bf16(buf, lane, half, x);
             }
-            if (out) stage_bf16(buf, lane, half, x);
+            if (!stored) continue;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&map_c, buf, n0 + c0, row0);
+              bulk_commit();
+            }
+            ++boxes;
+            __syncwarp();
           }
-          if (!out) continue;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            // a gradient's rows are also read as whole K slabs of 64: zeros past M
-            const int rows = EPI == kTcGrad ? (M + 63) & ~63 : M;
-            if (row0 < rows && n0 + c0 < g.N) tma_store_2d(&map_c, buf, n0 + c0, row0);
-            bulk_commit();
+          if constexpr (EPI == kTcStats) {
+            const float2 both = unpack_f2(fadd2(sum[0], sum[1]));
+            if (row_on) g.row_stats[(int64_t)row * g.stats_ld + (g.col0 + n0 + first) / kTcStatCols] = make_float2(m, both.x + both.y);
           }
-          __syncwarp();
-        }
-        if constexpr (EPI == kTcStats) {
-          if (row_on) g.row_stats[(int64_t)row * g.stats_ld + (g.col0 + n0) / kBN].y = sum;
         }
       } else if constexpr (EPI == kTcSplit) {
         const int row0 = m0 + 32 * quarter;
 #pragma unroll 1
-        for (int ci = 0; ci < kBN / 32; ++ci, ++boxes) {
+        for (int ci = 0; ci < kBN / 32 && n0 + 32 * ci < g.N; ++ci, ++boxes) {
           uint32_t r[32];
           tmem_ld32(acc + (uint32_t)(32 * ci), r);
           tmem_ld_wait();
@@ -627,7 +656,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (row0 < M && n0 + 32 * ci < g.N) {
+            if (row0 < M) {
               if (g.accumulate) tma_reduce_add_3d(&map_c, buf, n0 + 32 * ci, row0, part);
               else tma_store_3d(&map_c, buf, n0 + 32 * ci, row0, part);
             }
@@ -640,13 +669,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const bool row_on = row < M;
         const int64_t dst = row_on ? (int64_t)g.row_map[row] * g.ldc : 0;
 #pragma unroll 1
-        for (int c0 = 0; c0 < kBN; c0 += 32) {
+        for (int c0 = 0; c0 < kBN && n0 + c0 < g.N; c0 += 32) {
           uint32_t r[32];
           __syncwarp();
           tmem_ld32(acc + (uint32_t)c0, r);
           tmem_ld_wait();
           const int col = n0 + c0, n = min(32, g.N - col);
-          if (!row_on || n <= 0) continue;
+          if (!row_on) continue;
 #pragma unroll
           for (int jj = 0; jj < 32; ++jj) r[jj] = __float_as_uint(alpha * __uint_as_float(r[jj]));
           if (g.out_fp32) {
@@ -861,6 +890,9 @@ sf_status resident_pairs(cudaLaunchConfig_t* cfg, int* out) {
   auto it = cache.find(dev);
   if (it == cache.end()) {
     int n = 0;
+    cudaLaunchConfig_t one = *cfg;       // the same for all epilogues: shared memory allows one CTA an SM
+    cfg = &one;
+    cfg->blockDim = dim3(TcStages<kTcF32>::kThreads);
     cfg->gridDim = dim3((unsigned)(kPair * std::max(1, sm_count() / kPair)));
     SF_TRY(allow_dynamic_smem(reinterpret_cast<const void*>(&k_tc_gemm<kTcF32>), kGemmSmem));
     SF_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_tc_gemm<kTcF32>, cfg), "cudaOccupancyMaxActiveClusters (k_tc_gemm)");
@@ -952,6 +984,11 @@ sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
   const bool c_aligned = reinterpret_cast<uintptr_t>(j.C) % 16 == 0;
   CUtensorMap mc = ma;       // unused unless C is written by tensor stores
   const void* kernel = nullptr;
+  int threads = 0;
+  auto take = [&](const void* k, int n) {
+    kernel = k;
+    threads = n;
+  };
   switch (j.epi) {
     case kTcF32:
       g.vec = j.ldc % 4 == 0 && c_aligned ? 1 : 0;
@@ -959,17 +996,17 @@ sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
       // reach the padding of C's rows
       g.tma = g.vec && j.N % 4 == 0 ? 1 : 0;
       if (g.tma) SF_TRY(make_map_c(&mc, g.C, j.M, j.N, j.ldc));
-      kernel = reinterpret_cast<const void*>(&k_tc_gemm<kTcF32>);
+      take(reinterpret_cast<const void*>(&k_tc_gemm<kTcF32>), TcStages<kTcF32>::kThreads);
       break;
     case kTcSplit:
       if (j.splits < 1 || j.splits > (j.K + kBK - 1) / kBK) return fail(SF_ERR_INVALID, "splits must lie in 1..slabs of K");
       if (j.ldc % 4 || !c_aligned) return fail(SF_ERR_UNSUPPORTED, "partial products need 16-byte aligned rows");
       SF_TRY(make_map_split(&mc, g.C, j.M, j.N, j.ldc, j.splits));
-      kernel = reinterpret_cast<const void*>(&k_tc_gemm<kTcSplit>);
+      take(reinterpret_cast<const void*>(&k_tc_gemm<kTcSplit>), TcStages<kTcSplit>::kThreads);
       break;
     case kTcRows:
       if (!c_aligned || j.ldc * (j.out_fp32 ? 4 : 2) % 16) return fail(SF_ERR_UNSUPPORTED, "C needs 16-byte aligned rows");
-      kernel = reinterpret_cast<const void*>(&k_tc_gemm<kTcRows>);
+      take(reinterpret_cast<const void*>(&k_tc_gemm<kTcRows>), TcStages<kTcRows>::kThreads);
       break;
     case kTcBf16:
     case kTcGrad:
@@ -978,9 +1015,10 @@ sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
         if (j.ldc % 8 || !c_aligned) return fail(SF_ERR_UNSUPPORTED, "a bf16 C needs 16-byte aligned rows");
         SF_TRY(make_map_c16(&mc, j.C, j.M, j.N, j.ldc));
       }
-      kernel = j.epi == kTcBf16   ? reinterpret_cast<const void*>(&k_tc_gemm<kTcBf16>)
-               : j.epi == kTcGrad ? reinterpret_cast<const void*>(&k_tc_gemm<kTcGrad>)
-                                  : reinterpret_cast<const void*>(&k_tc_gemm<kTcStats>);
+      take(j.epi == kTcBf16   ? reinterpret_cast<const void*>(&k_tc_gemm<kTcBf16>)
+           : j.epi == kTcGrad ? reinterpret_cast<const void*>(&k_tc_gemm<kTcGrad>)
+                              : reinterpret_cast<const void*>(&k_tc_gemm<kTcStats>),
+           TcStages<kTcBf16>::kThreads);
       break;
   }
   SF_TRY(allow_dynamic_smem(kernel, kGemmSmem));
@@ -994,7 +1032,7 @@ sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(kGemmThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = kGemmSmem;
   cfg.stream = s;
   cfg.attrs = attr;

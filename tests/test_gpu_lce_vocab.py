@@ -110,6 +110,7 @@ def _check(H, W, y, got, grad_scale=1.0):
     (64, 72, 40000, 0, 8),          # few tokens, long vocabulary: dH's sum in parts
     (2048, 64, 300, 0, 64),         # many tokens, few outputs: dW's sum in parts
     (40, 32, 264, 0, 40),           # every token unlabelled
+    (8200, 16, 8200, 0, 70),        # short rows and many logits: the last piece's computed twice as well
 ])
 def test_matches_oracle(N, D, V, piece, unlabelled):
     H, W, y = _case(N, D, V, N + D + V, unlabelled)
