@@ -467,7 +467,8 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum,
  * logits.  The log-sum-exp is taken tile by tile as the logits leave the
  * tensor cores; the gradient is formed one piece of the vocabulary after the
  * other, so the workspace holds one N x piece block of bf16 whatever V, and
- * each row of dW is written once.
+ * each row of dW is written once.  At most 16 tokens (D a multiple of 8) are
+ * taken in one piece, their logits held in fp32: 64 bytes an output.
  *   H      : [N][D], W : [V][D], both SF_BF16, 16-byte aligned base and rows
  *            (ld a multiple of 8); any N, D, V >= 1.
  *   labels : device int32 [N]; ignore_index and labels outside [0, V) as in

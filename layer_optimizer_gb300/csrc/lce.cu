@@ -220,7 +220,8 @@ LcePlan plan_lce(int64_t N, int64_t V, int64_t chunk) {
 // in 2.2; the token-chunk form takes 28.8 ms in 0.40 GB, 16.4 in 3.6), against 6 when a token chunk's
 // logits are kept, but the workspace is one n x piece block of bf16 whatever
 // V, every row of dW is written once, in bf16 if asked (the type that the
-// AdamW step takes), and dW is not read back for accumulation.
+// AdamW step takes), and dW is not read back for accumulation.  Up to 16 tokens
+// take another form (lce_few.cuh).
 
 constexpr int kPairsGb300 = 76;                       // CTA pairs of the GEMM's persistent grid (152 SMs)
 constexpr size_t kPieceBudget = (size_t)1 << 30;      // bytes of G that the default piece may take
@@ -469,18 +470,17 @@ __global__ void __launch_bounds__(256) k_lce_rows(const RowsArgs a) {
 
 // out [M][N] = sum over the parts [S][M][ld], rounded to bf16 or kept in fp32;
 // with `place`, out's row r is the parts' row place[r], zero where that is -1.
-// ld is a multiple of 4; out rows are 16-byte aligned.  A block takes 32 or 256
-// groups of four columns; with eight parts and more, eight threads share a
-// group, each over every eighth part, and their sums are added in order
-// (6 tokens, 64 columns, 62 parts: the whole loss 46 us, with one thread a
+// ld is a multiple of 4; out rows are 16-byte aligned.  With eight parts and
+// more, G = 8 or 32 threads share a group of four columns, each over every G-th
+// part, and their sums are added in order (6 tokens, 64 columns, 62 parts: the whole loss 46 us, with one thread a
 // group 57).
 template <int G>
 __global__ void __launch_bounds__(256) k_lce_sum_parts(const float* parts, int S, int64_t M, int64_t N, int64_t ld,
                                                        const int32_t* place, void* out, int64_t ldo, int fp32) {
-  __shared__ float4 sums[G == 1 ? 1 : G][32];
+  constexpr int kGroups = 256 / G;
+  __shared__ float4 sums[G][G == 1 ? 1 : kGroups];
   griddep_launch_dependents();
   griddep_wait();
-  constexpr int kGroups = 256 / G;
   const int x = threadIdx.x % kGroups, y = threadIdx.x / kGroups;
   const int64_t per_row = (N + 3) / 4, total = M * per_row;
   for (int64_t base = (int64_t)blockIdx.x * kGroups; base < total; base += (int64_t)gridDim.x * kGroups) {
@@ -499,12 +499,12 @@ __global__ void __launch_bounds__(256) k_lce_sum_parts(const float* parts, int S
     }
     if (G > 1) {
       __syncthreads();
-      sums[y % G][x % 32] = v;
+      sums[y][x] = v;
       __syncthreads();
       if (y > 0) continue;
 #pragma unroll
       for (int q = 1; q < G; ++q) {
-        const float4 w = sums[q][x % 32];
+        const float4 w = sums[q][x];
         v.x += w.x;
         v.y += w.y;
         v.z += w.z;
@@ -607,9 +607,9 @@ VocabPlan plan_vocab(int64_t N, int64_t D, int64_t V, int64_t piece) {
 
 sf_status sum_parts(const float* parts, int S, int64_t M, int64_t N, int64_t ld, const int32_t* place, void* out,
                     int64_t ldo, bool fp32, cudaStream_t s) {
-  const bool shared = S >= 8;
-  const int64_t want = ceil_div<int64_t>(M * ceil_div<int64_t>(N, 4), shared ? 32 : 256);
-  SF_CUDA_TRY(launch_pdl(shared ? k_lce_sum_parts<8> : k_lce_sum_parts<1>,
+  const int g = S >= 64 ? 32 : S >= 8 ? 8 : 1;      // threads a group
+  const int64_t want = ceil_div<int64_t>(M * ceil_div<int64_t>(N, 4), 256 / g);
+  SF_CUDA_TRY(launch_pdl(g == 32 ? k_lce_sum_parts<32> : g == 8 ? k_lce_sum_parts<8> : k_lce_sum_parts<1>,
                          dim3((unsigned)std::min<int64_t>(want, (int64_t)sm_count() * 8)), dim3(256), 0, s, parts, S, M, N, ld,
                          place, out, ldo, (int)fp32),
               "launch k_lce_sum_parts");
@@ -617,6 +617,11 @@ sf_status sum_parts(const float* parts, int S, int64_t M, int64_t N, int64_t ld,
 }
 
 }  // namespace
+}  // namespace sf
+
+#include "lce_few.cuh"
+
+namespace sf {
 
 int read_and_clear_device_error_lce() {
   int v = 0, z = 0;
@@ -692,7 +697,7 @@ sf_status lce_forward_backward(const void* H, const void* W, const int32_t* labe
 
 size_t lce_vocab_workspace_bytes(int64_t n_tokens, int64_t d, int64_t vocab, int64_t piece) {
   if (n_tokens < 1 || d < 1 || vocab < 1 || piece < 0 || piece % sf::kTcTileN) return 0;
-  return sf::plan_vocab(n_tokens, d, vocab, piece).bytes;
+  return sf::few_tokens(n_tokens, d) ? sf::plan_few(n_tokens, d, vocab).bytes : sf::plan_vocab(n_tokens, d, vocab, piece).bytes;
 }
 
 sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W, const int32_t* labels, int64_t piece,
@@ -722,9 +727,9 @@ sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W, con
   for (const sf_matrix* m : outs)
     if (m && (m->ld * (int64_t)dtype_bytes(m->dtype) % 16 || reinterpret_cast<uintptr_t>(m->data) % 16 || m->ld < D))
       return fail(SF_ERR_UNSUPPORTED, "dH and dW need 16-byte aligned bases and rows");
-  const VocabPlan p = plan_vocab(N, D, V, piece);
-  if (!ws || ws_bytes < p.bytes || reinterpret_cast<uintptr_t>(ws) % 256)
-    return fail(SF_ERR_INVALID, "workspace needs %zu bytes, 256-byte aligned (got %zu)", p.bytes, ws_bytes);
+  const size_t need = lce_vocab_workspace_bytes(N, D, V, piece);
+  if (!ws || ws_bytes < need || reinterpret_cast<uintptr_t>(ws) % 256)
+    return fail(SF_ERR_INVALID, "workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
   if (!tensor_map_encoder()) return fail(SF_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled is not available");
   // tensor maps and bulk stores may only address this device's own memory
   const void* const dev[5] = {H->data, W->data, ws, dH ? dH->data : ws, dW ? dW->data : ws};
@@ -733,6 +738,36 @@ sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W, con
       return fail(SF_ERR_INVALID, "H, W, dH, dW and the workspace must be device memory of the current device");
   cudaStream_t s = as_stream(stream_);
   char* w = static_cast<char*>(ws);
+  if (few_tokens(N, D)) {
+    const FewPlan p = plan_few(N, D, V);
+    FewArgs a{};
+    a.H = static_cast<const uint16_t*>(H->data);
+    a.W = static_cast<const uint16_t*>(W->data);
+    a.ldh = H->ld;
+    a.ldw = W->ld;
+    a.V = V;
+    a.labels = labels;
+    a.N = (int32_t)N;
+    a.D = (int32_t)D;
+    a.ignore = ignore_index;
+    a.n_stats = p.n_stats;
+    a.grad_scale = grad_scale;
+    a.z = reinterpret_cast<float*>(w);
+    a.stats = reinterpret_cast<float2*>(w + p.off_stats);
+    a.label_logit = reinterpret_cast<float*>(w + p.off_logit);
+    a.loss = loss;
+    a.token_loss = token_loss;
+    a.part = dH ? reinterpret_cast<float*>(w + p.off_part) : nullptr;
+    if (dW) a.dW = dW->data, a.lddw = dW->ld, a.dw_fp32 = dW->dtype == SF_FP32;
+    a.rows_part = dH || dW ? p.rows_part : 0;
+    k_lce_few_logits<<<p.n_stats, 256, 0, s>>>(a);
+    SF_TRY(check_launch("k_lce_few_logits"));
+    const dim3 grid = dH || dW ? dim3((unsigned)p.blocks, (unsigned)ceil_div<int64_t>(D, 512)) : dim3(1);
+    SF_CUDA_TRY(launch_pdl(k_lce_few_grads, grid, dim3(256), 0, s, a), "launch k_lce_few_grads");
+    if (dH) SF_TRY(sum_parts(a.part, p.blocks, N, D, D, nullptr, dH->data, dH->ld, dH->dtype == SF_FP32, s));
+    return SF_OK;
+  }
+  const VocabPlan p = plan_vocab(N, D, V, piece);
   uint16_t* Hc = reinterpret_cast<uint16_t*>(w + p.off_h);
   __nv_bfloat16* G = reinterpret_cast<__nv_bfloat16*>(w + p.off_g);
   float2* stats = reinterpret_cast<float2*>(w + p.off_stats);

@@ -629,7 +629,9 @@ __global__ void __launch_bounds__(TcStages<EPI>::kThreads, 1)
           }
           if constexpr (EPI == kTcStats) {
             const float2 both = unpack_f2(fadd2(sum[0], sum[1]));
-            if (row_on) g.row_stats[(int64_t)row * g.stats_ld + (g.col0 + n0 + first) / kTcStatCols] = make_float2(m, both.x + both.y);
+            const float total = both.x + both.y;
+            if (m == -INFINITY && total != 0.0f) m = 0.0f;      // nothing but NaN: it must not be left out
+            if (row_on) g.row_stats[(int64_t)row * g.stats_ld + (g.col0 + n0 + first) / kTcStatCols] = make_float2(m, total);
           }
         }
       } else if constexpr (EPI == kTcSplit) {

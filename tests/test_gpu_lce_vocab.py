@@ -126,6 +126,37 @@ def test_output_types_strides_and_odd_widths(ht, wt, pad, opad, D, N, V, piece):
     _check(H, W, y, _run(H, W, y, piece, ht, wt, pad, opad))
 
 
+@pytest.mark.parametrize("N,D,V,unlabelled", [
+    (16, 8, 5, 0), (2, 32, 33, 0), (9, 40, 4099, 3), (16, 72, 2500, 4), (13, 136, 1000, 0), (5, 264, 70, 1), (3, 520, 777, 0),
+    (16, 1096, 3001, 15), (1, 4096, 600, 0), (16, 64, 12345, 16), (8, 2048, 130, 0),
+])
+@pytest.mark.parametrize("ht,wt,pad,opad", [(BF, BF, 0, 0), (F32, F32, 8, 8), (BF, F32, 16, 24), (F32, BF, 0, 8)])
+def test_few_tokens(N, D, V, unlabelled, ht, wt, pad, opad):
+    H, W, y = _case(N, D, V, N + D + V, unlabelled)
+    got = _run(H, W, y, 0, ht, wt, pad, opad)
+    _check(H, W, y, got)
+    off = y == -100
+    bad = H.clone()
+    bad[off] = float("nan")
+    for a, b in zip(got, _run(bad, W, y, 0, ht, wt, pad, opad)):
+        assert torch.equal(a, b)
+    only_h, only_w, none = (_run(H, W, y, 0, ht, wt, dh=d, dw=w) for d, w in ((True, False), (False, True), (False, False)))
+    assert torch.equal(only_h[2], got[2]) and torch.equal(only_w[3], got[3])
+    for r in (only_h, only_w, none):
+        assert torch.equal(r[0], got[0]) and torch.equal(r[1], got[1])
+    _check(H, W, y, _run(H, W, y, 0, ht, wt, pad, opad, grad_scale=-3.0), -3.0)
+
+
+@pytest.mark.parametrize("N", [3, 40])
+def test_outputs_that_are_all_nan_reach_every_loss(N):
+    # a run of vocabulary rows long enough to fill whole tiles
+    H, W, y = _case(N, 64, 2000, 77)
+    W[512:1100] = float("nan")
+    for piece in (0, 1024):
+        loss, tok, dH, _ = _run(H, W, y, piece)
+        assert bool(torch.isnan(loss).all()) and bool(torch.isnan(tok).all()) and bool(torch.isnan(dH.float()).all())
+
+
 def test_large_and_confident_logits():
     # logits of several hundred: exponentials of raw logits would overflow
     H, W, y = _case(100, 64, 600, 3, 4, hstd=8.0, wstd=2.0)
