@@ -10,12 +10,11 @@
 // over the row by shuffles and one shared-memory step, and h is written from
 // the registers.  Bound by HBM: a bf16 row moves 8 bytes a column (x, r, s,
 // h).  What it took to get there: registers few enough for 24 and more warps
-// an SM (72 a thread in bf16; at 96 the same kernel takes 90 us instead of 81;
-// rows that start off a unit get 96 all the same, or they spill), blocks of
-// whole warps rather than powers of two, fp32 arithmetic in pairs, one
+// an SM (72 a thread in bf16; at 96 the same kernel takes 90 us instead of
+// 81), blocks of whole warps rather than powers of two, fp32 arithmetic in pairs, one
 // division a scale group.  16384 x 4096 bf16 81 us (6.6 TB/s); 8192 x 12288,
 // fp32 stream, e4m3 with 128-column groups 168 us (6.6 TB/s); one row of 4096
-// 3.3 us.  Dropout on: 91 us at 16384 x 4096, 169 at 16384 x 4095.
+// 3.3 us.  Dropout on: 91 us at 16384 x 4096, 170 at 16384 x 4095 (129 off).
 //
 // The norm is taken of s in fp32, before s is rounded to its stored type, so
 // storing s in bf16 costs h no precision; the backward pass uses the stored s.
@@ -90,15 +89,14 @@ __device__ __forceinline__ F8 load_gain(const void* g, int fp32, const Span& s) 
   return unpack(u);
 }
 
-// A thread's units of a row: first + k * step.  Shifted: the units of 32
-// lanes (or of a shorter row's) are consecutive, for ShiftedBits; otherwise
-// those of the whole row's threads.
+// A thread's units of a row: first + k * step, those of the whole row's
+// threads beside one another, or (`handed`, for ShiftedBits) those of 32 lanes
+// (or of a shorter row's).
 struct UnitWalk {
   int first, step, lane;      // lane: among those
-  template <int MODE>
-  __device__ __forceinline__ static UnitWalk of(int t, int tpr, int units) {
+  __device__ __forceinline__ static UnitWalk of(bool handed, int t, int tpr, int units) {
     const int w = min(tpr, 32), lane = t & (w - 1);
-    return MODE == kShifted ? UnitWalk{(t - lane) * units + lane, w, lane} : UnitWalk{t, tpr, lane};
+    return handed ? UnitWalk{(t - lane) * units + lane, w, lane} : UnitWalk{t, tpr, lane};
   }
 };
 
@@ -135,14 +133,20 @@ __device__ __forceinline__ float group_scale(float amax, float* inv) {
   return max_nan(amax * (1.0f / 448.0f), 1.17549435e-38f);
 }
 
-template <typename TA, typename TS, int MODE>
-__global__ void __maxnreg__(MODE == kShifted ? 96 : sizeof(TA) + sizeof(TS) == 4 ? 72 : 80) k_add_rmsnorm_fwd(const FwdArgs a) {
+// DROP false: no dropout (otherwise as the arguments say); an instance of its
+// own for shifted rows, whose hand-over of the generator's words costs
+// registers (8192 x 6001 bf16 without dropout: 93 us, in one instance 109;
+// with dropout 108 at 80 registers, 120 at 96; fp32 7132 x 9409 195 and 203
+// the other way round).
+template <typename TA, typename TS, int MODE, bool DROP>
+__global__ void __maxnreg__(MODE == kShifted && DROP && sizeof(TA) == 4 ? 96 : sizeof(TA) + sizeof(TS) == 4 && !(MODE == kShifted && DROP) ? 72 : 80) k_add_rmsnorm_fwd(const FwdArgs a) {
   __shared__ float red[2][kMaxThreads / 32];
+  __shared__ float group_max[2][MODE == kShifted ? kMaxCols / 32 : 1];      // shifted rows: of a unit's own group, and of the one before
   const int tpr = a.tpr, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
   const int64_t row = (int64_t)blockIdx.x * a.rpb + lane_row;
   const bool on = row < a.rows;
   const int m = MODE == kShifted ? (int)(row * a.shift) & 7 : 0;
-  const UnitWalk at = UnitWalk::of<MODE>(t, tpr, a.units);
+  const UnitWalk at = UnitWalk::of(MODE == kShifted && DROP, t, tpr, a.units);
   auto span = [&](int k) { return unit_span<MODE>(at.first + k * at.step, m, (MODE != kShifted || k < a.units) && on ? a.cols : 0); };
   F8 s[kK];
   {
@@ -160,18 +164,18 @@ __global__ void __maxnreg__(MODE == kShifted ? 96 : sizeof(TA) + sizeof(TS) == 4
     const DropWords words = a.d.threshold ? drop_words(a.d) : DropWords{};
     const uint64_t b0 = (uint64_t)(row * a.per_row + at.first);
     ShiftedBits bits;
-    if (MODE == kShifted && a.d.threshold && t > at.lane) bits.start(b0 - at.lane - 1, words, a.d);
+    if (MODE == kShifted && DROP && t > at.lane) bits.start(b0 - at.lane - 1, words, a.d);
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[k].p[i] = 0;
       if (MODE == kShifted && k >= a.units) continue;
       uint32_t w[4];
-      if (MODE == kShifted && a.d.threshold)
+      if (MODE == kShifted && DROP)
         bits.next(b0 + k * at.step, at.lane, min(tpr, 32), m, words, a.d, w);
       if (!span(k).some()) continue;
       s[k] = unpack(x[k]);
-      if (a.d.threshold) {
+      if (DROP && a.d.threshold) {
         if (MODE == kShifted) drop_apply(s[k], w, a.d);
         else drop_unit(s[k], b0 + k * at.step, words, a.d);
       }
@@ -207,17 +211,32 @@ __global__ void __maxnreg__(MODE == kShifted ? 96 : sizeof(TA) + sizeof(TS) == 4
       if (a.h) store_unit<MODE>(hp + p.c, p.lo, p.hi, s[k]);
     }
     if (a.q && k < a.units) {
-      float top = 0.0f;
+      // shifted units: those that start a group hold its columns from m on,
+      // and before them the last m of the group before
+      const int lanes = 1 << (a.group_log2 - 3), u = at.first + k * at.step;
+      const bool edge = MODE == kShifted && a.group_log2 && m && (u & (lanes - 1)) == 0;
+      float top = 0.0f, carry = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // outside a ragged row the sum is 0 and so is the gain
         const float2 v = f2(s[k].p[i]);
-        top = max_nan(top, max_nan(fabsf(v.x), fabsf(v.y)));
+        if (edge) {
+          (2 * i < m ? carry : top) = max_nan(2 * i < m ? carry : top, fabsf(v.x));
+          (2 * i + 1 < m ? carry : top) = max_nan(2 * i + 1 < m ? carry : top, fabsf(v.y));
+        } else {
+          top = max_nan(top, max_nan(fabsf(v.x), fabsf(v.y)));
+        }
       }
       if (!p.some()) top = 0.0f;
       amax = max_nan(amax, top);
-      if (a.group_log2) {
-        const int lanes = 1 << (a.group_log2 - 3);
+      if (MODE == kShifted && a.group_log2) {
+        for (int o = lanes >> 1; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int group = u >> (a.group_log2 - 3);
+        if (p.some() && (u & (lanes - 1)) == 0) {
+          if (group < a.n_groups) group_max[0][lane_row * a.n_groups + group] = top;
+          if (edge && u) group_max[1][lane_row * a.n_groups + group - 1] = carry;
+        }
+      } else if (a.group_log2) {
         for (int o = lanes >> 1; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
         float inv;
         const float sc = group_scale(top, &inv);
@@ -228,7 +247,31 @@ __global__ void __maxnreg__(MODE == kShifted ? 96 : sizeof(TA) + sizeof(TS) == 4
     }
   }
   if (!a.q) return;
-  if (!a.group_log2) {
+  if (MODE == kShifted && a.group_log2) {
+    __syncthreads();
+    // a group's maximum, with its columns in the unit that starts the next one
+    auto scale_of = [&](int group, float* inv) {
+      float top = group_max[0][lane_row * a.n_groups + group];
+      if (m && ((group + 1) << a.group_log2) - m < a.cols) top = max_nan(top, group_max[1][lane_row * a.n_groups + group]);
+      return group_scale(top, inv);
+    };
+#pragma unroll
+    for (int k = 0; k < kK; ++k) {
+      if (!span(k).some()) continue;
+      const int lanes = 1 << (a.group_log2 - 3), u = at.first + k * at.step, group = u >> (a.group_log2 - 3);
+      const bool starts = (u & (lanes - 1)) == 0;
+      float inv = 0.0f;
+      if (group < a.n_groups) {
+        const float sc = scale_of(group, &inv);
+        if (starts) a.scale[row * a.n_groups + group] = sc;
+      }
+      float before = inv;
+      if (starts && m && u) scale_of(group - 1, &before);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        s[k].p[i] = mul2(s[k].p[i], f2(starts && 2 * i < m ? before : inv, starts && 2 * i + 1 < m ? before : inv));
+    }
+  } else if (!a.group_log2) {
     amax = row_reduce<true>(amax, tpr, red[1]);
     float inv;
     const float sc = group_scale(amax, &inv);
@@ -333,7 +376,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
   const DropWords words = a.d.threshold ? drop_words(a.d) : DropWords{};
   const int m = MODE == kShifted ? (int)(((int64_t)blockIdx.x * rpb + lane_row) * a.shift) & 7 : 0;
   float* mine = comb + lane_row * (8 * a.per_row + 8);
-  const UnitWalk at = UnitWalk::of<MODE>(t, tpr, a.units);
+  const UnitWalk at = UnitWalk::of(MODE == kShifted, t, tpr, a.units);
   if (MODE == kShifted) {
     for (int k = 0; k < a.units; ++k) {
       const Span p = unit_span<MODE>(at.first + k * at.step, m, a.cols);
@@ -515,7 +558,7 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
       if (first + i * step < a.rows) fill(first + i * step, i);
 
   const DropWords words = a.d.threshold ? drop_words(a.d) : DropWords{};
-  const UnitWalk walk = UnitWalk::of<MODE>(t, tpr, a.units);
+  const UnitWalk walk = UnitWalk::of(MODE == kShifted, t, tpr, a.units);
   const int col0 = 8 * walk.first, dcol = 8 * walk.step;
   const int m = SHIFT ? (int)((first + lane_row) * a.shift) & 7 : 0;
   auto span = [&](int k) { return unit_span<MODE>(walk.first + k * walk.step, m, !SHIFT || k < a.units ? a.cols : 0); };
@@ -730,25 +773,26 @@ constexpr unsigned kTypes = 1u << SF_BF16 | 1u << SF_FP32;
 
 template <typename TA, typename TS>
 struct Fwd {
-  static const void* ptr(RowMode mode) {
-    return mode == kAligned   ? (const void*)&k_add_rmsnorm_fwd<TA, TS, kAligned>
-           : mode == kShifted ? (const void*)&k_add_rmsnorm_fwd<TA, TS, kShifted>
-                              : (const void*)&k_add_rmsnorm_fwd<TA, TS, kScalar>;
+  static const void* ptr(RowMode mode, bool drop) {
+    return mode == kAligned           ? (const void*)&k_add_rmsnorm_fwd<TA, TS, kAligned, true>
+           : mode == kShifted && drop ? (const void*)&k_add_rmsnorm_fwd<TA, TS, kShifted, true>
+           : mode == kShifted         ? (const void*)&k_add_rmsnorm_fwd<TA, TS, kShifted, false>
+                                      : (const void*)&k_add_rmsnorm_fwd<TA, TS, kScalar, true>;
   }
 };
 template <typename TA, typename TS>
 struct Bwd {
-  static const void* ptr(RowMode mode) {
+  static const void* ptr(RowMode mode, bool) {
     return mode == kAligned   ? (const void*)&k_add_rmsnorm_bwd<TA, TS, kAligned>
            : mode == kShifted ? (const void*)&k_add_rmsnorm_bwd<TA, TS, kShifted>
                               : (const void*)&k_add_rmsnorm_bwd<TA, TS, kScalar>;
   }
 };
 template <template <typename, typename> class K>
-const void* pick(int32_t ta, int32_t ts, RowMode mode) {
+const void* pick(int32_t ta, int32_t ts, RowMode mode, bool drop) {
   using B = __nv_bfloat16;
-  if (ta == SF_BF16) return ts == SF_BF16 ? K<B, B>::ptr(mode) : K<B, float>::ptr(mode);
-  return ts == SF_BF16 ? K<float, B>::ptr(mode) : K<float, float>::ptr(mode);
+  if (ta == SF_BF16) return ts == SF_BF16 ? K<B, B>::ptr(mode, drop) : K<B, float>::ptr(mode, drop);
+  return ts == SF_BF16 ? K<float, B>::ptr(mode, drop) : K<float, float>::ptr(mode, drop);
 }
 // The mode of a call: kAligned also wants the gains on their units.
 template <size_t N>
@@ -891,16 +935,15 @@ sf_status sf_add_rmsnorm_forward(const sf_matrix* x, const sf_matrix* residual, 
   a.inv_cols = (float)(1.0 / (double)cols);
   const sf_matrix* const all[5] = {x, residual, sum, h, h8};
   RowMode mode = call_mode(all, gain, gain_dtype, &a.shift);
-  // a shifted row may touch one unit more, which four units a thread have to
-  // cover, and its units straddle scale groups
-  if (mode == kShifted && ((h8 && group) || cols > kMaxCols - 8)) mode = kScalar;
+  // a shifted row may touch one unit more, which four units a thread have to cover
+  if (mode == kShifted && cols > kMaxCols - 8) mode = kScalar;
   pick_threads(rows, a.per_row + (mode == kShifted ? 1 : 0), h8 != nullptr, &a.tpr, &a.rpb, &a.units);
   const int threads = a.tpr * a.rpb;
   const int64_t grid = ceil_div<int64_t>(rows, a.rpb);
   if (grid > INT32_MAX) return fail(SF_ERR_UNSUPPORTED, "too many rows");
   const int32_t ts = residual ? residual->dtype : sum ? sum->dtype : x->dtype;
   void* args[] = {&a};
-  SF_CUDA_TRY(cudaLaunchKernel(pick<Fwd>(x->dtype, ts, mode), dim3((unsigned)grid), dim3(threads), args, 0, as_stream(stream)),
+  SF_CUDA_TRY(cudaLaunchKernel(pick<Fwd>(x->dtype, ts, mode, a.d.threshold != 0), dim3((unsigned)grid), dim3(threads), args, 0, as_stream(stream)),
               "launch k_add_rmsnorm_fwd");
   return SF_OK;
 }
@@ -967,7 +1010,7 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum, con
     SF_TRY(launch_ring(a, mode == kShifted, dh->dtype, sum->dtype, st, &parts));
   } else if (grid) {
     void* args[] = {&a};
-    const void* kernel = pick<Bwd>(dh->dtype, sum->dtype, mode);
+    const void* kernel = pick<Bwd>(dh->dtype, sum->dtype, mode, a.d.threshold != 0);
     if (smem > (48 << 10)) SF_TRY(allow_dynamic_smem(kernel, smem));
     SF_CUDA_TRY(cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3(threads), args, smem, st),
                 "launch k_add_rmsnorm_bwd");
