@@ -392,9 +392,13 @@ __global__ void __launch_bounds__(256) k_lce_rows(const RowsArgs a) {
   }
   const float2* st = a.stats + r * a.n_tiles;
   float m = -INFINITY, s = 0.0f;
+  // the maximum first, so that the exponentials do not wait for one another
+#pragma unroll 4
+  for (int t = threadIdx.x; t < a.n_tiles; t += 256) m = fmaxf(m, st[t].x);
+#pragma unroll 4
   for (int t = threadIdx.x; t < a.n_tiles; t += 256) {
     const float2 p = st[t];
-    combine_stats(m, s, p.x, p.y);
+    s += p.x == -INFINITY ? 0.0f : p.y * expf(p.x - m);
   }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -470,8 +474,8 @@ __global__ void __launch_bounds__(256) k_lce_rows(const RowsArgs a) {
 
 // out [M][N] = sum over the parts [S][M][ld], rounded to bf16 or kept in fp32;
 // with `place`, out's row r is the parts' row place[r], zero where that is -1.
-// ld is a multiple of 4; out rows are 16-byte aligned.  With eight parts and
-// more, G = 8 or 32 threads share a group of four columns, each over every G-th
+// ld is a multiple of 4; out rows are 16-byte aligned.  For few groups of many
+// parts, G = 8 or 32 threads share a group of four columns, each over every G-th
 // part, and their sums are added in order (6 tokens, 64 columns, 62 parts: the whole loss 46 us, with one thread a
 // group 57).
 template <int G>
@@ -607,8 +611,11 @@ VocabPlan plan_vocab(int64_t N, int64_t D, int64_t V, int64_t piece) {
 
 sf_status sum_parts(const float* parts, int S, int64_t M, int64_t N, int64_t ld, const int32_t* place, void* out,
                     int64_t ldo, bool fp32, cudaStream_t s) {
-  const int g = S >= 64 ? 32 : S >= 8 ? 8 : 1;      // threads a group
-  const int64_t want = ceil_div<int64_t>(M * ceil_div<int64_t>(N, 4), 256 / g);
+  // threads a group: more than one where there are too few groups to fill the
+  // SMs (512 x 2048, nine parts, 262144 groups: the loss 5 % slower with eight)
+  const int64_t groups = M * ceil_div<int64_t>(N, 4);
+  const int g = groups >= (int64_t)sm_count() * 512 || S < 8 ? 1 : S < 64 ? 8 : 32;
+  const int64_t want = ceil_div<int64_t>(groups, 256 / g);
   SF_CUDA_TRY(launch_pdl(g == 32 ? k_lce_sum_parts<32> : g == 8 ? k_lce_sum_parts<8> : k_lce_sum_parts<1>,
                          dim3((unsigned)std::min<int64_t>(want, (int64_t)sm_count() * 8)), dim3(256), 0, s, parts, S, M, N, ld,
                          place, out, ldo, (int)fp32),

@@ -1017,10 +1017,9 @@ sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
         if (j.ldc % 8 || !c_aligned) return fail(SF_ERR_UNSUPPORTED, "a bf16 C needs 16-byte aligned rows");
         SF_TRY(make_map_c16(&mc, j.C, j.M, j.N, j.ldc));
       }
-      take(j.epi == kTcBf16   ? reinterpret_cast<const void*>(&k_tc_gemm<kTcBf16>)
-           : j.epi == kTcGrad ? reinterpret_cast<const void*>(&k_tc_gemm<kTcGrad>)
-                              : reinterpret_cast<const void*>(&k_tc_gemm<kTcStats>),
-           TcStages<kTcBf16>::kThreads);
+      if (j.epi == kTcBf16) take(reinterpret_cast<const void*>(&k_tc_gemm<kTcBf16>), TcStages<kTcBf16>::kThreads);
+      else if (j.epi == kTcGrad) take(reinterpret_cast<const void*>(&k_tc_gemm<kTcGrad>), TcStages<kTcGrad>::kThreads);
+      else take(reinterpret_cast<const void*>(&k_tc_gemm<kTcStats>), TcStages<kTcStats>::kThreads);
       break;
   }
   SF_TRY(allow_dynamic_smem(kernel, kGemmSmem));
