@@ -450,7 +450,9 @@ sf_status sf_add_rmsnorm_forward(const sf_matrix* x, const sf_matrix* residual,
  *               or fp32.  Each may be NULL, not all.
  *   ws        : device scratch of ws_bytes >= sf_add_rmsnorm_workspace_bytes(
  *               rows, cols), 16-byte aligned; only read with dgain.
- * fp32 arithmetic; dgain's sum runs in a fixed order (no atomics). */
+ * fp32 arithmetic; dgain's sum runs in a fixed order (no atomics).  Where rows
+ * do not start on 16 bytes, up to 14 bytes of the padding beside a row of dh,
+ * sum and dsum may be read (and ignored); nothing past a matrix's last element. */
 size_t sf_add_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
 
 sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum,

@@ -23,6 +23,7 @@
 #include <algorithm>
 
 #include "ptx.cuh"
+#include "row_span.h"
 #include "rows.cuh"
 
 namespace sf {
@@ -474,6 +475,13 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 
+// The columns that copy_span leaves out of the matrix's last row, into the row's
+// place at `at` (its first column at m).
+template <typename T>
+__device__ __forceinline__ void load_rest(unsigned char* at, const T* row, uint32_t m, uint32_t cols) {
+  for (uint32_t c = copy_span(m, cols, sizeof(T), true).end / sizeof(T); c < m + cols; ++c) reinterpret_cast<T*>(at)[c] = row[c - m];
+}
+
 constexpr int kMinStages = 3, kMaxStages = 4;
 
 // The same backward pass with whole rows moved by bulk copies, both ways, so
@@ -486,8 +494,8 @@ constexpr int kMinStages = 3, kMaxStages = 4;
 // refilled.  With loads and stores of registers the kernel was bound by
 // instruction issue (49 instructions an element, 59 % of the copy rate).
 // SHIFT: rows that start off a unit, as above.  A copy brings the 16-byte units
-// that hold any of the row, so that units lie in shared memory as in memory;
-// of the first and last one, the columns outside the row are set to zero, and
+// that hold any of the row (as far as the matrix goes: copy_span), so that units lie
+// in shared memory as in memory; of the first and last one, the columns outside the row are set to zero, and
 // those inside are written to memory by their threads, the rest by bulk stores
 // (16384 x 4095 bf16: 170 us, with dropout 221, against 349 element by element).
 template <typename TA, typename TS, int K, bool KEEP, bool SHIFT>
@@ -509,26 +517,33 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
   // by the first warp, a lane a row: the copies of the rows from `base` on
   // into stage st ...
   const int m_lane = SHIFT ? (int)((first + threadIdx.x) * a.shift) & 7 : 0;
-  auto head = [&](uint32_t size) { return (m_lane * size) & ~15u; };                              // of a row's place
-  auto tail = [&](uint32_t size) { return ((m_lane + a.cols) * size + 15u) & ~15u; };
-  auto bring = [&](unsigned char* at, const void* row, uint32_t size, int st) {
-    if (SHIFT) bulk_load(at + head(size), static_cast<const unsigned char*>(row) - m_lane * size + head(size), tail(size) - head(size), &full[st]);
+  auto bring = [&](unsigned char* at, const void* row, uint32_t size, int st, bool last) {
+    const CopySpan c = copy_span(m_lane, a.cols, size, last);
+    if (SHIFT) bulk_load(at + c.begin, static_cast<const unsigned char*>(row) - m_lane * size + c.begin, c.end - c.begin, &full[st]);
     else bulk_load(at, row, a.cols * size, &full[st]);
   };
   auto fill = [&](int64_t base, int st) {
     const int n = (int)min((int64_t)rpb, a.rows - base);
+    const int64_t row = base + threadIdx.x;
+    const bool mine = (int)threadIdx.x < n, last = row == a.rows - 1;
+    unsigned char* at = ring + (size_t)st * stage_bytes;
     uint32_t bytes = (uint32_t)n * (row_a + row_s + (ring_d ? row_s : 0u));
-    if (SHIFT)
-      bytes = __reduce_add_sync(0xffffffffu, (int)threadIdx.x < n ? tail(sizeof(TA)) - head(sizeof(TA)) + (ring_d ? 2u : 1u) * (tail(sizeof(TS)) - head(sizeof(TS)))
-                                                                  : 0u);
+    if (SHIFT) {
+      const CopySpan ca = copy_span(m_lane, a.cols, sizeof(TA), last), cs = copy_span(m_lane, a.cols, sizeof(TS), last);
+      bytes = __reduce_add_sync(0xffffffffu, mine ? ca.end - ca.begin + (ring_d ? 2u : 1u) * (cs.end - cs.begin) : 0u);
+      if (mine && last) {      // ordered before the readers by the arrival below
+        load_rest(at + threadIdx.x * row_a, row_ptr<TA>(a.dh, a.lddh, row), m_lane, a.cols);
+        load_rest(at + off_s + threadIdx.x * row_s, row_ptr<TS>(a.s, a.lds, row), m_lane, a.cols);
+        if (ring_d) load_rest(at + off_d + threadIdx.x * row_s, row_ptr<TS>(a.dsum, a.lddsum, row), m_lane, a.cols);
+      }
+      __syncwarp();
+    }
     if (threadIdx.x == 0) mbar_arrive_expect_tx(&full[st], bytes);
     __syncwarp();
-    if ((int)threadIdx.x < n) {
-      unsigned char* at = ring + (size_t)st * stage_bytes;
-      const int64_t row = base + threadIdx.x;
-      bring(at + threadIdx.x * row_a, row_ptr<TA>(a.dh, a.lddh, row), sizeof(TA), st);
-      bring(at + off_s + threadIdx.x * row_s, row_ptr<TS>(a.s, a.lds, row), sizeof(TS), st);
-      if (ring_d) bring(at + off_d + threadIdx.x * row_s, row_ptr<TS>(a.dsum, a.lddsum, row), sizeof(TS), st);
+    if (mine) {
+      bring(at + threadIdx.x * row_a, row_ptr<TA>(a.dh, a.lddh, row), sizeof(TA), st, last);
+      bring(at + off_s + threadIdx.x * row_s, row_ptr<TS>(a.s, a.lds, row), sizeof(TS), st, last);
+      if (ring_d) bring(at + off_d + threadIdx.x * row_s, row_ptr<TS>(a.dsum, a.lddsum, row), sizeof(TS), st, last);
     }
   };
   // ... and those of its outputs to global memory (each lane its own row, so
