@@ -576,6 +576,7 @@ VocabPlan plan_vocab(int64_t N, int64_t D, int64_t V, int64_t piece) {
     const int64_t most = std::max<int64_t>(2048, (int64_t)(kPieceBudget / 2) / N / 256 * 256);
     piece = ceil_div<int64_t>(ceil_div<int64_t>(V, ceil_div<int64_t>(V, most)), 256) * 256;
   }
+  piece = std::min(piece, ceil_div<int64_t>(V, 256) * 256);      // any piece of at least V is the whole vocabulary
   p.pieces = ceil_div<int64_t>(V, piece);
   p.piece = std::min(piece, V);
   p.ldg = ceil_div<int64_t>(p.piece, 64) * 64;
