@@ -392,6 +392,23 @@ def matrix(t, name="matrix"):
     return sf_matrix(t.data_ptr(), rows, cols, ld, _dtype(t, name))
 
 
+def _required(t, name):
+    """matrix() of an argument whose sizes the call needs."""
+    m = matrix(t, name)
+    if m is None:
+        raise SfError(SF_ERR_INVALID, f"{name} is NULL")
+    return m
+
+
+def _vector_dtype(t, name, dtype):
+    """sf_dtype of a vector: a tensor's own; an address comes with `dtype`."""
+    if type(t) is int:
+        if dtype is None:
+            raise SfError(SF_ERR_INVALID, f"{name} is an address: {name}_dtype says its type")
+        return dtype
+    return SF_FP32 if t is None else _dtype(t, name)
+
+
 def _ref(m):
     return None if m is None else ctypes.byref(m)
 
@@ -424,13 +441,15 @@ def sf_dropout(x, y, p, rng=None, residual=None, stream=None):
 
 
 def sf_add_rmsnorm_forward(x, residual, gain, eps, sum=None, h=None, h8=None, h8_scale=None, group=0, rstd=None, p=0.0,
-                           rng=None, stream=None):
-    """s = residual + dropout(x), its root-mean-square norm h, and h in e4m3 with scales; tensors or sf_matrix."""
-    x, residual, sum = matrix(x, "x"), matrix(residual, "residual"), matrix(sum, "sum")
+                           rng=None, stream=None, gain_dtype=None):
+    """s = residual + dropout(x), its root-mean-square norm h, and h in e4m3 with scales; tensors or sf_matrix
+    (vectors: tensors or addresses, gain's with gain_dtype)."""
+    x, residual, sum = _required(x, "x"), matrix(residual, "residual"), matrix(sum, "sum")
     h, h8 = matrix(h, "h"), matrix(h8, "h8")
     groups = -(-x.cols // group) if group > 0 else 1
     _check(load().sf_add_rmsnorm_forward(
-        _ref(x), _ref(residual), _vector(gain, x.cols, "gain"), _dtype(gain, "gain"), float(eps), float(p), _ref(rng),
+        _ref(x), _ref(residual), _vector(gain, x.cols, "gain"), _vector_dtype(gain, "gain", gain_dtype), float(eps), float(p),
+        _ref(rng),
         _ref(sum), _ref(h), _ref(h8), _vector(h8_scale, x.rows * groups, "h8_scale", _F32), group,
         _vector(rstd, x.rows, "rstd", _F32), _stream(stream)))
 
@@ -440,14 +459,15 @@ def sf_add_rmsnorm_workspace_bytes(rows, cols):
 
 
 def sf_add_rmsnorm_backward(dh, sum, gain, rstd, dsum=None, dresidual=None, dx=None, dgain=None, p=0.0, rng=None,
-                            ws=None, stream=None):
-    """The gradients of sf_add_rmsnorm_forward (ws: a uint8 workspace tensor, needed with dgain)."""
-    dh, sum, dsum = matrix(dh, "dh"), matrix(sum, "sum"), matrix(dsum, "dsum")
+                            ws=None, stream=None, gain_dtype=None, dgain_dtype=None):
+    """The gradients of sf_add_rmsnorm_forward (ws: a uint8 workspace tensor, needed with dgain; vectors: tensors or
+    addresses, gain's and dgain's with their types)."""
+    dh, sum, dsum = _required(dh, "dh"), matrix(sum, "sum"), matrix(dsum, "dsum")
     dresidual, dx = matrix(dresidual, "dresidual"), matrix(dx, "dx")
     _check(load().sf_add_rmsnorm_backward(
-        _ref(dh), _ref(sum), _vector(gain, dh.cols, "gain"), _dtype(gain, "gain"),
+        _ref(dh), _ref(sum), _vector(gain, dh.cols, "gain"), _vector_dtype(gain, "gain", gain_dtype),
         _vector(rstd, dh.rows, "rstd", _F32), _ref(dsum), float(p), _ref(rng), _ref(dresidual), _ref(dx),
-        _vector(dgain, dh.cols, "dgain"), SF_FP32 if dgain is None else _dtype(dgain, "dgain"), _addr(ws),
+        _vector(dgain, dh.cols, "dgain"), _vector_dtype(dgain, "dgain", dgain_dtype), _addr(ws),
         0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
 
 
@@ -458,7 +478,7 @@ def lce_vocab_workspace_bytes(n_tokens, d, vocab, piece=0):
 def lce_vocab_forward_backward(H, W, labels, loss=None, token_loss=None, dH=None, dW=None, ws=None, piece=0,
                                ignore_index=-100, grad_scale=1.0, stream=None):
     """Linear cross-entropy by pieces of the vocabulary (ws: a uint8 workspace tensor); tensors or sf_matrix."""
-    H, W, dH, dW = matrix(H, "H"), matrix(W, "W"), matrix(dH, "dH"), matrix(dW, "dW")
+    H, W, dH, dW = _required(H, "H"), matrix(W, "W"), matrix(dH, "dH"), matrix(dW, "dW")
     _check(load().lce_vocab_forward_backward(
         _ref(H), _ref(W), _vector(labels, H.rows, "labels", ("torch.int32",)), piece, ignore_index, float(grad_scale),
         _vector(loss, 1, "loss", _F32), _vector(token_loss, H.rows, "token_loss", _F32), _ref(dH), _ref(dW), _addr(ws),

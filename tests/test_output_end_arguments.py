@@ -16,3 +16,35 @@ def lib():
 def test_a_piece_beyond_the_vocabulary_is_the_whole_of_it(n, d, v, piece):
     # every size of at least V is one piece, up to the type's largest multiple of 256
     assert native.lce_vocab_workspace_bytes(n, d, v, piece) == native.lce_vocab_workspace_bytes(n, d, v, 1024)
+
+
+def _matrix(rows, cols, dtype, at=1 << 20):
+    return native.sf_matrix(at, rows, cols, cols, dtype)
+
+
+def test_vectors_given_by_address():
+    # no rows: every check runs and nothing is launched
+    x, s = _matrix(0, 64, native.SF_BF16), _matrix(0, 64, native.SF_FP32)
+    native.sf_add_rmsnorm_forward(x, s, 4096, 1e-5, h=x, rstd=4096, gain_dtype=native.SF_BF16)
+    native.sf_add_rmsnorm_backward(x, s, 4096, 4096, dx=x, gain_dtype=native.SF_FP32)
+    with pytest.raises(native.SfError, match="gain_dtype"):
+        native.sf_add_rmsnorm_forward(x, s, 4096, 1e-5, h=x)
+    with pytest.raises(native.SfError, match="dgain_dtype"):
+        native.sf_add_rmsnorm_backward(x, s, 4096, 4096, dx=x, gain_dtype=native.SF_BF16, dgain=4096)
+    # a bf16 gain may lie on 2 bytes, an fp32 one may not
+    native.sf_add_rmsnorm_forward(x, s, 4098, 1e-5, h=x, gain_dtype=native.SF_BF16)
+    with pytest.raises(native.SfError, match="gain is not aligned"):
+        native.sf_add_rmsnorm_forward(x, s, 4098, 1e-5, h=x, gain_dtype=native.SF_FP32)
+
+
+def test_missing_arguments_are_the_librarys_errors():
+    x = _matrix(0, 64, native.SF_BF16)
+    for call in (lambda: native.sf_dropout(None, x, 0.0), lambda: native.sf_dropout(x, None, 0.0),
+                 lambda: native.sf_add_rmsnorm_forward(None, None, 4096, 1e-5, h=x, gain_dtype=native.SF_BF16),
+                 lambda: native.sf_add_rmsnorm_forward(x, None, None, 1e-5, h=x),
+                 lambda: native.sf_add_rmsnorm_backward(None, x, 4096, 4096, dx=x, gain_dtype=native.SF_BF16),
+                 lambda: native.sf_add_rmsnorm_backward(x, None, 4096, 4096, dx=x, gain_dtype=native.SF_BF16),
+                 lambda: native.sf_add_rmsnorm_backward(x, x, None, 4096, dx=x),
+                 lambda: native.lce_vocab_forward_backward(None, x, 4096), lambda: native.lce_vocab_forward_backward(x, None, 4096)):
+        with pytest.raises(native.SfError, match="is NULL"):
+            call()
