@@ -382,6 +382,8 @@ sf_status lsp_projector_export_values(lsp_projector p, float* val, void* stream)
  * bytes in bf16, 32 in fp32, 8 in e4m3) take one wide access per unit.
  * An output may be the very matrix (same data, ld and type) of an input of
  * the same size; other overlaps are undefined.
+ * Vectors (gain, rstd, scales, labels, losses, device_offset) lie on a multiple
+ * of their element's size: SF_ERR_INVALID otherwise.
  * ---------------------------------------------------------------------- */
 typedef struct {
   void* data;

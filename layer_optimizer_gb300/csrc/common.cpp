@@ -79,6 +79,11 @@ sf_status check_matrix(const sf_matrix* m, const char* name, int64_t want_rows, 
   return SF_OK;
 }
 
+sf_status check_aligned(const void* p, size_t size, const char* name) {
+  if (reinterpret_cast<uintptr_t>(p) % size) return fail(SF_ERR_INVALID, "%s is not aligned to its type", name);
+  return SF_OK;
+}
+
 int usable_cores() {
   cpu_set_t set;
   CPU_ZERO(&set);

@@ -71,6 +71,9 @@ bool on_current_device(const void* p);
 // want_rows / want_cols < 0 accept any size.  dtypes: a mask of 1 << sf_dtype.
 sf_status check_matrix(const sf_matrix* m, const char* name, int64_t want_rows, int64_t want_cols, unsigned dtypes);
 
+// Checks on the host that a vector (null passes) lies on a multiple of its element's size.
+sf_status check_aligned(const void* p, size_t size, const char* name);
+
 inline size_t dtype_bytes(int32_t t) { return t == SF_FP32 ? 4 : t == SF_BF16 ? 2 : 1; }
 
 // Default bound for host waits, in milliseconds (SF_TIMEOUT_MS or 600 s).

@@ -134,6 +134,7 @@ sf_status make_drop_consts(double p, const sf_rng* rng, DropConsts* out) {
   if (t && !rng) return fail(SF_ERR_INVALID, "p > 0 needs a generator (rng is NULL)");
   *out = DropConsts{};
   if (!t) return SF_OK;
+  SF_TRY(check_aligned(rng->device_offset, sizeof(uint64_t), "device_offset"));
   uint32_t k0 = (uint32_t)rng->seed, k1 = (uint32_t)(rng->seed >> 32);
   for (int r = 0; r < 10; ++r, k0 += 0x9E3779B9u, k1 += 0xBB67AE85u) {
     out->key[2 * r] = k0;

@@ -724,6 +724,9 @@ sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W, con
   if (!labels) return fail(SF_ERR_INVALID, "labels is NULL");
   if (N > INT32_MAX / 2 || D > INT32_MAX / 2 || V > INT32_MAX / 4) return fail(SF_ERR_UNSUPPORTED, "sizes too large");
   if (piece < 0 || piece % kTcTileN) return fail(SF_ERR_INVALID, "piece must be 0 or a positive multiple of 256");
+  SF_TRY(check_aligned(labels, sizeof(int32_t), "labels"));
+  SF_TRY(check_aligned(loss, sizeof(float), "loss"));
+  SF_TRY(check_aligned(token_loss, sizeof(float), "token_loss"));
   if (!(grad_scale - grad_scale == 0.0)) return fail(SF_ERR_INVALID, "grad_scale must be finite");
   const sf_matrix* const ins[2] = {H, W};
   for (const sf_matrix* m : ins)

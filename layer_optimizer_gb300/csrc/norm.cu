@@ -882,8 +882,7 @@ sf_status launch_ring(BwdArgs& a, bool shifted, int32_t ta, int32_t ts, cudaStre
 sf_status check_gain(const void* gain, int32_t dtype, const char* name) {
   if (!gain) return fail(SF_ERR_INVALID, "%s is NULL", name);
   if (dtype != SF_BF16 && dtype != SF_FP32) return fail(SF_ERR_UNSUPPORTED, "%s: type %d is not taken here", name, (int)dtype);
-  if (reinterpret_cast<uintptr_t>(gain) % dtype_bytes(dtype)) return fail(SF_ERR_INVALID, "%s is not aligned to its type", name);
-  return SF_OK;
+  return check_aligned(gain, dtype_bytes(dtype), name);
 }
 
 sf_status check_cols(int64_t cols) {
@@ -927,7 +926,9 @@ sf_status sf_add_rmsnorm_forward(const sf_matrix* x, const sf_matrix* residual, 
     if (!h8_scale) return fail(SF_ERR_INVALID, "h8 needs h8_scale");
     if (group != 0 && group != 32 && group != 64 && group != 128)
       return fail(SF_ERR_INVALID, "group must be 0 (a scale per row), 32, 64 or 128 (got %d)", (int)group);
+    SF_TRY(check_aligned(h8_scale, sizeof(float), "h8_scale"));
   }
+  SF_TRY(check_aligned(rstd, sizeof(float), "rstd"));
   FwdArgs a{};
   SF_TRY(make_drop_consts(p, rng, &a.d));
   if (!rows) return SF_OK;
@@ -981,6 +982,7 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum, con
   SF_TRY(check_matrix(sum, "sum", rows, cols, kTypes));
   SF_TRY(check_gain(gain, gain_dtype, "gain"));
   if (!rstd && rows) return fail(SF_ERR_INVALID, "rstd is NULL");
+  SF_TRY(check_aligned(rstd, sizeof(float), "rstd"));
   if (dsum) SF_TRY(check_matrix(dsum, "dsum", rows, cols, 1u << sum->dtype));
   if (dresidual) SF_TRY(check_matrix(dresidual, "dresidual", rows, cols, 1u << sum->dtype));
   if (dx) SF_TRY(check_matrix(dx, "dx", rows, cols, 1u << dh->dtype));

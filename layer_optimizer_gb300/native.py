@@ -426,6 +426,17 @@ def _vector(t, n, name, dtypes=None):
     return t.data_ptr()
 
 
+def _workspace(ws):
+    """Address and size of a workspace tensor (None stays None)."""
+    if ws is None:
+        return None, 0
+    if not ws.is_contiguous():
+        raise SfError(SF_ERR_INVALID, "ws must be dense")
+    if not ws.is_cuda:
+        _reachable(ws, "ws")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 _F32 = ("torch.float32",)
 
 
@@ -467,8 +478,8 @@ def sf_add_rmsnorm_backward(dh, sum, gain, rstd, dsum=None, dresidual=None, dx=N
     _check(load().sf_add_rmsnorm_backward(
         _ref(dh), _ref(sum), _vector(gain, dh.cols, "gain"), _vector_dtype(gain, "gain", gain_dtype),
         _vector(rstd, dh.rows, "rstd", _F32), _ref(dsum), float(p), _ref(rng), _ref(dresidual), _ref(dx),
-        _vector(dgain, dh.cols, "dgain"), _vector_dtype(dgain, "dgain", dgain_dtype), _addr(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+        _vector(dgain, dh.cols, "dgain"), _vector_dtype(dgain, "dgain", dgain_dtype), *_workspace(ws),
+        _stream(stream)))
 
 
 def lce_vocab_workspace_bytes(n_tokens, d, vocab, piece=0):
@@ -481,8 +492,8 @@ def lce_vocab_forward_backward(H, W, labels, loss=None, token_loss=None, dH=None
     H, W, dH, dW = _required(H, "H"), matrix(W, "W"), matrix(dH, "dH"), matrix(dW, "dW")
     _check(load().lce_vocab_forward_backward(
         _ref(H), _ref(W), _vector(labels, H.rows, "labels", ("torch.int32",)), piece, ignore_index, float(grad_scale),
-        _vector(loss, 1, "loss", _F32), _vector(token_loss, H.rows, "token_loss", _F32), _ref(dH), _ref(dW), _addr(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+        _vector(loss, 1, "loss", _F32), _vector(token_loss, H.rows, "token_loss", _F32), _ref(dH), _ref(dW),
+        *_workspace(ws), _stream(stream)))
 
 
 # ------------------------------------------------------------------ (c) ----

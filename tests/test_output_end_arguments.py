@@ -48,3 +48,63 @@ def test_missing_arguments_are_the_librarys_errors():
                  lambda: native.lce_vocab_forward_backward(None, x, 4096), lambda: native.lce_vocab_forward_backward(x, None, 4096)):
         with pytest.raises(native.SfError, match="is NULL"):
             call()
+
+
+def test_vectors_off_their_type_are_refused():
+    # addresses that a kernel would fault on; no rows where the call would otherwise launch
+    x = _matrix(0, 64, native.SF_BF16)
+    q = _matrix(0, 64, native.SF_E4M3)
+    bf = dict(gain_dtype=native.SF_BF16)
+    odd = native.rng(1, 0, 4100)
+    calls = {
+        "rstd": [lambda: native.sf_add_rmsnorm_forward(x, None, 4096, 1e-5, h=x, rstd=4098, **bf),
+                 lambda: native.sf_add_rmsnorm_backward(x, x, 4096, 4098, dx=x, **bf)],
+        "h8_scale": [lambda: native.sf_add_rmsnorm_forward(x, None, 4096, 1e-5, h8=q, h8_scale=4098, **bf)],
+        "device_offset": [lambda: native.sf_dropout(x, x, 0.5, odd),
+                          lambda: native.sf_add_rmsnorm_forward(x, None, 4096, 1e-5, h=x, p=0.5, rng=odd, **bf),
+                          lambda: native.sf_add_rmsnorm_backward(x, x, 4096, 4096, dx=x, p=0.5, rng=odd, **bf)],
+    }
+    H, W = _matrix(20, 64, native.SF_BF16), _matrix(300, 64, native.SF_BF16)
+    for name in ("labels", "loss", "token_loss"):
+        kw = {"labels": 4096, name: 4098}
+        calls[name] = [lambda kw=kw: native.lce_vocab_forward_backward(H, W, **kw)]
+    for name, each in calls.items():
+        for call in each:
+            with pytest.raises(native.SfError, match=f"{name} is not aligned"):
+                call()
+
+
+class _Pageable:
+    """A workspace tensor in ordinary host memory."""
+    is_cuda = False
+
+    def is_pinned(self):
+        return False
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return 1 << 20
+
+    def element_size(self):
+        return 1
+
+    def data_ptr(self):
+        return 1 << 21
+
+
+class _Strided(_Pageable):
+    is_cuda = True
+
+    def is_contiguous(self):
+        return False
+
+
+@pytest.mark.parametrize("ws,match", [(_Pageable(), "device or pinned"), (_Strided(), "dense")])
+def test_workspaces_that_the_device_cannot_use_are_refused(ws, match):
+    x = _matrix(0, 64, native.SF_BF16)
+    with pytest.raises(native.SfError, match=f"ws must be .*{match}"):
+        native.sf_add_rmsnorm_backward(x, x, 4096, 4096, dx=x, ws=ws, gain_dtype=native.SF_BF16)
+    with pytest.raises(native.SfError, match=f"ws must be .*{match}"):
+        native.lce_vocab_forward_backward(_matrix(20, 64, native.SF_BF16), _matrix(300, 64, native.SF_BF16), 4096, ws=ws)
