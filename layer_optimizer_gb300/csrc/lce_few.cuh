@@ -318,8 +318,15 @@ __global__ void __launch_bounds__(256, 2) k_lce_few_grads(const FewArgs a) {
     const int q = g + (i < 2 ? 0 : 8), col = d0 + 16 * t + 8 * (i & 1);
     if (q >= a.N || col >= a.D) continue;
     float* p = a.part + ((int64_t)blockIdx.x * a.N + q) * a.D + col;
-    *reinterpret_cast<float4*>(p) = make_float4(f * acc[0][i], f * acc[1][i], f * acc[2][i], f * acc[3][i]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(f * acc[4][i], f * acc[5][i], f * acc[6][i], f * acc[7][i]);
+    // an unlabelled token's sums are 0 times W, which a NaN or an infinity in W turns into NaN: exactly 0 instead
+    const bool on = label[q] >= 0;
+    float4 lo = make_float4(0.0f, 0.0f, 0.0f, 0.0f), hi = lo;
+    if (on) {
+      lo = make_float4(f * acc[0][i], f * acc[1][i], f * acc[2][i], f * acc[3][i]);
+      hi = make_float4(f * acc[4][i], f * acc[5][i], f * acc[6][i], f * acc[7][i]);
+    }
+    *reinterpret_cast<float4*>(p) = lo;
+    *reinterpret_cast<float4*>(p + 4) = hi;
   }
 }
 
