@@ -391,7 +391,10 @@ def _reachable(t, name):
 
 
 def matrix(t, name="matrix"):
-    """sf_matrix of a 2D torch tensor with unit column stride (None stays None; an sf_matrix stays itself)."""
+    """sf_matrix of a 2D torch tensor with unit column stride (None stays None; an sf_matrix stays itself).
+
+    The structure keeps the tensor alive.
+    """
     if t is None or type(t) is sf_matrix:
         return t
     if t.dim() != 2:
@@ -404,7 +407,9 @@ def matrix(t, name="matrix"):
         _reachable(t, name)
     if rows <= 1 and ld < cols:
         ld = cols
-    return sf_matrix(t.data_ptr(), rows, cols, ld, _dtype(t, name))
+    m = sf_matrix(t.data_ptr(), rows, cols, ld, _dtype(t, name))
+    m.tensor = t
+    return m
 
 
 def _required(t, name):
@@ -456,8 +461,15 @@ _F32 = ("torch.float32",)
 
 
 def rng(seed, offset=0, device_offset=None):
-    """sf_rng: the generator of one dropout call (device_offset: int64 tensor of one element, or None)."""
-    return sf_rng(seed, offset, _vector(device_offset, 1, "device_offset", ("torch.int64", "torch.uint64")))
+    """sf_rng: the generator of one dropout call (device_offset: int64 tensor of one element, or None).
+
+    The structure keeps device_offset alive.  The kernel reads it when it runs,
+    so hold on to one of the two until then, and as long as a graph that
+    captured the call may be replayed.
+    """
+    r = sf_rng(seed, offset, _vector(device_offset, 1, "device_offset", ("torch.int64", "torch.uint64")))
+    r.device_offset_tensor = device_offset
+    return r
 
 
 def sf_dropout(x, y, p, rng=None, residual=None, stream=None):
