@@ -491,8 +491,9 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum,
  *            piece), 256-byte aligned.
  * Logits, exponentials and sums in fp32; dZ rounded to bf16 before the two
  * gradient products (where the last piece's logits are not computed again it
- * passes through one more bf16 rounding, its label's entry does not); dH is summed over pieces in fp32 and rounded
- * once.  Deterministic. */
+ * passes through one more bf16 rounding); a label's entry, softmax - 1, is taken
+ * from its logit without cancellation and rounded once, the same in every piece.
+ * dH is summed over pieces in fp32 and rounded once.  Deterministic. */
 size_t lce_vocab_workspace_bytes(int64_t n_tokens, int64_t d, int64_t vocab,
                                  int64_t piece);
 

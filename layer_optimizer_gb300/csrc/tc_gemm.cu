@@ -345,7 +345,7 @@ __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, uint32
 //   kTcStats  per row and tile the maximum and sum of exponentials, the
 //             label's logit, and optionally exp(c - maximum) in bf16: the
 //             logits themselves never leave tensor memory;
-//   kTcGrad   exp(c - lse) - [column is the label] in bf16, 0 in rows past M.
+//   kTcGrad   exp(c - lse), at the label expm1(c - lse), in bf16, 0 in rows past M.
 template <int EPI>
 __global__ void __launch_bounds__(TcStages<EPI>::kThreads, 1)
     k_tc_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -606,9 +606,15 @@ __global__ void __launch_bounds__(TcStages<EPI>::kThreads, 1)
                 sum[half] = fadd2(sum[half], fadd2(part[0], part[1]));
               } else {
                 if ((unsigned)(label - c1) < 32u) {
+                  // not the exponential - 1, which cancels where the model is sure
+                  float z = 0.0f;
 #pragma unroll
                   for (int jj = 0; jj < 32; ++jj)
-                    if (label - c1 == jj) x[jj] -= 1.0f;
+                    if (label - c1 == jj) z = __uint_as_float(r[32 * half + jj]);
+                  z = expm1f(z - ref);
+#pragma unroll
+                  for (int jj = 0; jj < 32; ++jj)
+                    if (label - c1 == jj) x[jj] = z;
                 }
                 if (row0 + 32 > M) {
 #pragma unroll
