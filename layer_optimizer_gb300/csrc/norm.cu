@@ -505,7 +505,8 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
   __shared__ __align__(8) uint64_t full[kMaxStages];
   extern __shared__ __align__(128) unsigned char ring[];
   const int tpr = a.tpr, rpb = a.rpb, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
-  if (threadIdx.x < 2 * 4 * kMaxThreads / 32) (&red[0][0][0])[threadIdx.x] = 0.0f;     // blocks have 128 threads or more
+  // (a block of 96 threads leaves rows 2 and 3 of red[1] alone: it has one row, so nothing reads them)
+  if (threadIdx.x < 2 * 4 * kMaxThreads / 32) (&red[0][0][0])[threadIdx.x] = 0.0f;
   // a row's place holds whole units
   const uint32_t slot = SHIFT ? 8u * a.per_row + 8u : (uint32_t)a.cols;
   const uint32_t row_a = slot * sizeof(TA), row_s = slot * sizeof(TS);
