@@ -476,7 +476,9 @@ sf_status sf_add_rmsnorm_backward(const sf_matrix* dh, const sf_matrix* sum,
  *   H      : [N][D], W : [V][D], both SF_BF16, 16-byte aligned base and rows
  *            (ld a multiple of 8); any N, D, V >= 1.
  *   labels : device int32 [N]; ignore_index and labels outside [0, V) as in
- *            lce_forward_backward.
+ *            lce_forward_backward.  They must not change while the call runs:
+ *            the results are undefined then (reported as an out-of-range index
+ *            where one arises).
  *   piece  : vocabulary rows per piece, a multiple of 256; 0: as many as 1 GiB
  *            of bf16 holds (at least 2048).  Larger pieces compute fewer
  *            logits twice; the last piece's never are, unless D is at most 512

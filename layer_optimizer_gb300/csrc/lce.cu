@@ -451,7 +451,12 @@ __global__ void __launch_bounds__(256) k_lce_rows(const RowsArgs a) {
   if (threadIdx.x == 0) {
     a.lse[r] = l;
     a.row_loss[r] = l - zy;
-    if (a.token_loss) a.token_loss[a.token[r]] = l - zy;
+    if (a.token_loss) {
+      // labels that change during the call can leave rows without a token
+      const int32_t t = a.token[r];
+      if (t >= 0 && t < a.N) a.token_loss[t] = l - zy;
+      else atomicOr(&g_device_error, kDevErrIndex);
+    }
     __threadfence();
     last = atomicAdd(a.counter, 1u) == (uint32_t)(n - 1);
   }

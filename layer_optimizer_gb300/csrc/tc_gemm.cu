@@ -674,8 +674,10 @@ __global__ void __launch_bounds__(TcStages<EPI>::kThreads, 1)
         }
       } else if constexpr (EPI == kTcRows) {
         // each lane writes its own row's 32 columns: 64 or 128 consecutive bytes
-        const bool row_on = row < M;
-        const int64_t dst = row_on ? (int64_t)g.row_map[row] * g.ldc : 0;
+        const int32_t to = row < M ? g.row_map[row] : -1;
+        const bool row_on = to >= 0 && to < g.M;      // a row map that is no map writes nothing
+        if (row < M && !row_on) atomicOr(&g_device_error, kDevErrIndex);
+        const int64_t dst = row_on ? (int64_t)to * g.ldc : 0;
 #pragma unroll 1
         for (int c0 = 0; c0 < kBN && n0 + c0 < g.N; c0 += 32) {
           uint32_t r[32];
