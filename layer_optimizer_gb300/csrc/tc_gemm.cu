@@ -258,7 +258,6 @@ struct TcGemmArgs {
   int32_t M, N, K;
   float alpha;
   int32_t accumulate;    // 1: C += alpha A B^T, 0: C = alpha A B^T
-  int32_t vec;           // C rows 16-byte aligned (float4 epilogue)
   int32_t tma;           // C written by tensor stores (reduce-add when accumulating) from shared memory
   int32_t n_fast;        // tile order: n fastest (A is the larger operand) or m fastest
   int32_t a_mn, b_mn;    // operand stored MN-major ([K][M], [K][N]) instead of K-major:
@@ -719,11 +718,15 @@ __global__ void __launch_bounds__(TcStages<EPI>::kThreads, 1)
         // 32 x 32 boxes through two 4 KB staging buffers per warp, 128-byte
         // swizzled to match the store's tensor map (conflict-free 16-byte
         // writes); one thread stores or reduce-adds each box, and a buffer
-        // is rewritten only once its previous store has read it
+        // is rewritten only once its previous store has read it.  A tensor store
+        // writes whole 16-byte units: of a C whose rows end inside one, the last
+        // columns' box goes element by element, so that the padding stays as it
+        // is (8192 x 8191 x 1024 in rows of 8192: 98 us, all of C that way 140, 8192 columns 99)
         const int row0 = m0 + 32 * quarter;
+        const int whole = g.N & 3 ? g.N & ~31 : INT32_MAX;      // boxes from here on
         float rm = -INFINITY, rs = 0.0f;
 #pragma unroll 1
-        for (int ci = 0; ci < kBN / 32; ++ci, ++boxes) {
+        for (int ci = 0; ci < kBN / 32; ++ci) {
           uint32_t r[32];
           tmem_ld32(acc + (uint32_t)(32 * ci), r);
           tmem_ld_wait();
@@ -732,6 +735,19 @@ __global__ void __launch_bounds__(TcStages<EPI>::kThreads, 1)
 #pragma unroll
             for (int jj = 0; jj < 32; ++jj) x[jj] = g.alpha * __uint_as_float(r[jj]);
             fold_row_stats(x, min(32, g.N - (n0 + 32 * ci)), rm, rs);
+          }
+          if (n0 + 32 * ci >= whole) {
+            if (row < g.M) {
+              float* p = g.C + (int64_t)row * g.ldc + n0 + 32 * ci;
+#pragma unroll
+              for (int jj = 0; jj < 32; ++jj)
+                if (n0 + 32 * ci + jj < g.N) {
+                  const float v = g.alpha * __uint_as_float(r[jj]);
+                  p[jj] = g.accumulate ? p[jj] + v : v;
+                }
+            }
+            __syncwarp();
+            continue;
           }
           const uint32_t buf = stg + (uint32_t)(boxes & 1) * 4096u;
           if (boxes >= 2) {
@@ -752,6 +768,7 @@ __global__ void __launch_bounds__(TcStages<EPI>::kThreads, 1)
             }
             bulk_commit();
           }
+          ++boxes;
           __syncwarp();
         }
         if (g.row_stats && row < g.M) g.row_stats[(int64_t)row * n_tiles + nt] = make_float2(rm, rs);
@@ -772,28 +789,11 @@ __global__ void __launch_bounds__(TcStages<EPI>::kThreads, 1)
             fold_row_stats(x, min(32, g.N - col0), rm, rs);
           }
           if (!row_on || col0 >= g.N) continue;
-          if (g.vec && col0 + 32 <= g.N) {
 #pragma unroll
-            for (int jj = 0; jj < 32; jj += 4) {
-              float4 v = make_float4(g.alpha * __uint_as_float(r[jj]), g.alpha * __uint_as_float(r[jj + 1]),
-                                     g.alpha * __uint_as_float(r[jj + 2]), g.alpha * __uint_as_float(r[jj + 3]));
-              float4* p = reinterpret_cast<float4*>(crow + col0 + jj);
-              if (g.accumulate) {
-                const float4 o = *p;
-                v.x += o.x;
-                v.y += o.y;
-                v.z += o.z;
-                v.w += o.w;
-              }
-              *p = v;
-            }
-          } else {
-#pragma unroll
-            for (int jj = 0; jj < 32; ++jj) {
-              if (col0 + jj < g.N) {
-                const float v = g.alpha * __uint_as_float(r[jj]);
-                crow[col0 + jj] = g.accumulate ? crow[col0 + jj] + v : v;
-              }
+          for (int jj = 0; jj < 32; ++jj) {
+            if (col0 + jj < g.N) {
+              const float v = g.alpha * __uint_as_float(r[jj]);
+              crow[col0 + jj] = g.accumulate ? crow[col0 + jj] + v : v;
             }
           }
         }
@@ -1001,10 +1001,7 @@ sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
   };
   switch (j.epi) {
     case kTcF32:
-      g.vec = j.ldc % 4 == 0 && c_aligned ? 1 : 0;
-      // a tensor store writes whole 16-byte units: past a ragged N it would
-      // reach the padding of C's rows
-      g.tma = g.vec && j.N % 4 == 0 ? 1 : 0;
+      g.tma = j.ldc % 4 == 0 && c_aligned ? 1 : 0;      // else element by element
       if (g.tma) SF_TRY(make_map_c(&mc, g.C, j.M, j.N, j.ldc));
       take(reinterpret_cast<const void*>(&k_tc_gemm<kTcF32>), TcStages<kTcF32>::kThreads);
       break;
