@@ -84,11 +84,7 @@ class _Pageable:
     def is_contiguous(self):
         return True
 
-    def numel(self):
-        return 1 << 20
-
-    def element_size(self):
-        return 1
+    nbytes = 1 << 20
 
     def data_ptr(self):
         return 1 << 21
