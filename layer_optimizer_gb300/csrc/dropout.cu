@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const DropoutArgs a) {
     if (RES) {
       const F8 w = unpack(r[k]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v.p[i] = add2(v.p[i], w.p[i]);
+      for (int i = 0; i < 4; ++i) v.p[i] = fadd2(v.p[i], w.p[i]);
     }
     store_unit<MODE>(FLAT ? static_cast<TY*>(a.y) + 8 * b : row_ptr<TY>(a.y, a.ldy, row) + s.c, s.lo, s.hi, v);
   }

@@ -225,13 +225,6 @@ LcePlan plan_lce(int64_t N, int64_t V, int64_t chunk) {
 
 constexpr int kPairsGb300 = 76;                       // CTA pairs of the GEMM's persistent grid (152 SMs)
 constexpr size_t kPieceBudget = (size_t)1 << 30;      // bytes of G that the default piece may take
-constexpr float kLog2eF = 1.44269504f;
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 
 struct GatherArgs {
   const uint16_t* H;       // [N][ldh]
@@ -429,7 +422,7 @@ __global__ void __launch_bounds__(256) k_lce_rows(const RowsArgs a) {
       const int c = c0 + 2048 * u;
       if (c >= c1) break;
       const float tm = st[(a.col0 + c) / kTcStatCols].x;
-      const float k = exp2_fast(((tm == -INFINITY ? 0.0f : tm) - l) * kLog2eF);
+      const float k = exp2_approx(((tm == -INFINITY ? 0.0f : tm) - l) * kLog2e);
       const uint64_t k2 = pack_f2(k, k);
       const uint32_t in[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
       uint32_t out[4];

@@ -183,7 +183,7 @@ __global__ void __maxnreg__(MODE == kShifted && DROP && sizeof(TA) == 4 ? 96 : s
       if (a.r) {
         const F8 w = unpack(r[k]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[k].p[i] = add2(s[k].p[i], w.p[i]);
+        for (int i = 0; i < 4; ++i) s[k].p[i] = fadd2(s[k].p[i], w.p[i]);
       }
     }
   }
@@ -194,12 +194,12 @@ __global__ void __maxnreg__(MODE == kShifted && DROP && sizeof(TA) == 4 ? 96 : s
     const Span p = span(k);
     if (a.s && p.some()) store_unit<MODE>(sp + p.c, p.lo, p.hi, s[k]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum2 = fma2(s[k].p[i], s[k].p[i], sum2);
+    for (int i = 0; i < 4; ++i) sum2 = fmadd2(s[k].p[i], s[k].p[i], sum2);
   }
-  const float sum = row_reduce<false>(f2(sum2).x + f2(sum2).y, tpr, red[0]);
+  const float sum = row_reduce<false>(unpack_f2(sum2).x + unpack_f2(sum2).y, tpr, red[0]);
   const float rstd = rsqrtf(fmaf(sum, a.inv_cols, a.eps));
   if (a.rstd && on && t == 0) a.rstd[row] = rstd;
-  const uint64_t rstd2 = f2(rstd, rstd);
+  const uint64_t rstd2 = pack_f2(rstd, rstd);
   float amax = 0.0f;
   TA* hp = row_ptr<TA>(a.h, a.ldh, row);
 #pragma unroll
@@ -208,7 +208,7 @@ __global__ void __maxnreg__(MODE == kShifted && DROP && sizeof(TA) == 4 ? 96 : s
     if (p.some()) {
       const F8 g = load_gain<MODE>(a.gain, a.gain_fp32, p);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[k].p[i] = mul2(mul2(s[k].p[i], rstd2), g.p[i]);
+      for (int i = 0; i < 4; ++i) s[k].p[i] = fmul2(fmul2(s[k].p[i], rstd2), g.p[i]);
       if (a.h) store_unit<MODE>(hp + p.c, p.lo, p.hi, s[k]);
     }
     if (a.q && k < a.units) {
@@ -220,7 +220,7 @@ __global__ void __maxnreg__(MODE == kShifted && DROP && sizeof(TA) == 4 ? 96 : s
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // outside a ragged row the sum is 0 and so is the gain
-        const float2 v = f2(s[k].p[i]);
+        const float2 v = unpack_f2(s[k].p[i]);
         if (edge) {
           (2 * i < m ? carry : top) = max_nan(2 * i < m ? carry : top, fabsf(v.x));
           (2 * i + 1 < m ? carry : top) = max_nan(2 * i + 1 < m ? carry : top, fabsf(v.y));
@@ -243,7 +243,7 @@ __global__ void __maxnreg__(MODE == kShifted && DROP && sizeof(TA) == 4 ? 96 : s
         const float sc = group_scale(top, &inv);
         if (p.some() && (t & (lanes - 1)) == 0) a.scale[row * a.n_groups + (p.c >> a.group_log2)] = sc;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[k].p[i] = mul2(s[k].p[i], f2(inv, inv));
+        for (int i = 0; i < 4; ++i) s[k].p[i] = fmul2(s[k].p[i], pack_f2(inv, inv));
       }
     }
   }
@@ -270,7 +270,7 @@ __global__ void __maxnreg__(MODE == kShifted && DROP && sizeof(TA) == 4 ? 96 : s
       if (starts && m && u) scale_of(group - 1, &before);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        s[k].p[i] = mul2(s[k].p[i], f2(starts && 2 * i < m ? before : inv, starts && 2 * i + 1 < m ? before : inv));
+        s[k].p[i] = fmul2(s[k].p[i], pack_f2(starts && 2 * i < m ? before : inv, starts && 2 * i + 1 < m ? before : inv));
     }
   } else if (!a.group_log2) {
     amax = row_reduce<true>(amax, tpr, red[1]);
@@ -280,7 +280,7 @@ __global__ void __maxnreg__(MODE == kShifted && DROP && sizeof(TA) == 4 ? 96 : s
 #pragma unroll
     for (int k = 0; k < kK; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[k].p[i] = mul2(s[k].p[i], f2(inv, inv));
+      for (int i = 0; i < 4; ++i) s[k].p[i] = fmul2(s[k].p[i], pack_f2(inv, inv));
   }
 #pragma unroll
   for (int k = 0; k < kK; ++k) {
@@ -290,8 +290,8 @@ __global__ void __maxnreg__(MODE == kShifted && DROP && sizeof(TA) == 4 ? 96 : s
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       // saturating, so |h| / scale just above 448 by rounding stays 448
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(f2(s[k].p[2 * i]), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(f2(s[k].p[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(unpack_f2(s[k].p[2 * i]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(unpack_f2(s[k].p[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
       w[i] = lo | hi << 16;
     }
     uint8_t* p = row_ptr<uint8_t>(a.q, a.ldq, row) + part.c;
@@ -339,9 +339,9 @@ struct BwdArgs {
 __device__ __forceinline__ void bwd_sums(const F8& dh, const F8& s, const F8& g, uint64_t rstd2, F8& acc, uint64_t& dot2) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint64_t w = mul2(dh.p[i], s.p[i]);
-    acc.p[i] = fma2(w, rstd2, acc.p[i]);
-    dot2 = fma2(w, g.p[i], dot2);
+    const uint64_t w = fmul2(dh.p[i], s.p[i]);
+    acc.p[i] = fmadd2(w, rstd2, acc.p[i]);
+    dot2 = fmadd2(w, g.p[i], dot2);
   }
 }
 
@@ -349,7 +349,7 @@ __device__ __forceinline__ void bwd_sums(const F8& dh, const F8& s, const F8& g,
 __device__ __forceinline__ F8 bwd_unit(const F8& dh, const F8& s, const F8& g, const F8& dsum, uint64_t rstd2, uint64_t c2) {
   F8 v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v.p[i] = fma2(mul2(dh.p[i], g.p[i]), rstd2, fma2(s.p[i], c2, dsum.p[i]));
+  for (int i = 0; i < 4; ++i) v.p[i] = fmadd2(fmul2(dh.p[i], g.p[i]), rstd2, fmadd2(s.p[i], c2, dsum.p[i]));
   return v;
 }
 
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
       if (a.dsum) load_unit<MODE>(row_ptr<TS>(a.dsum, a.lddsum, row) + p.c, p.lo, p.hi, ds[k]);
     }
     const float rstd = row < a.rows ? a.rstd[row] : 0.0f;
-    const uint64_t rstd2 = f2(rstd, rstd);
+    const uint64_t rstd2 = pack_f2(rstd, rstd);
     uint64_t dot2 = 0;
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
@@ -417,9 +417,9 @@ __global__ void __launch_bounds__(kMaxThreads) k_add_rmsnorm_bwd(const BwdArgs a
       if (p.some()) bwd_sums(unpack(dh[k]), unpack(s[k]), gain_at(p), rstd2, acc[k], dot2);
     }
     // two alternating buffers: the next row's write cannot meet this row's reads
-    const float dot = row_reduce<false>(f2(dot2).x + f2(dot2).y, tpr, red[parity]);
+    const float dot = row_reduce<false>(unpack_f2(dot2).x + unpack_f2(dot2).y, tpr, red[parity]);
     const float c = -rstd * (rstd * (rstd * dot * a.inv_cols));
-    const uint64_t c2 = f2(c, c);
+    const uint64_t c2 = pack_f2(c, c);
     const bool drop = a.dx && a.d.threshold;
     const uint64_t b0 = (uint64_t)(row * a.per_row + at.first);
     ShiftedBits bits;
@@ -594,8 +594,8 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
     if (SHIFT && (p.lo > 0 || p.hi < 8)) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 x = f2(v.p[i]);
-        v.p[i] = f2(2 * i >= p.lo && 2 * i < p.hi ? x.x : 0.0f, 2 * i + 1 >= p.lo && 2 * i + 1 < p.hi ? x.y : 0.0f);
+        const float2 x = unpack_f2(v.p[i]);
+        v.p[i] = pack_f2(2 * i >= p.lo && 2 * i < p.hi ? x.x : 0.0f, 2 * i + 1 >= p.lo && 2 * i + 1 < p.hi ? x.y : 0.0f);
       }
     }
     return v;
@@ -625,7 +625,7 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
       }
     }
     if (!dead) dead = !mbar_wait_u32(smem_u32(&full[st]), pass);
-    const uint64_t rstd2 = f2(rstd, rstd);
+    const uint64_t rstd2 = pack_f2(rstd, rstd);
     Unit<TA> dh;
     Unit<TS> s, ds;
     uint64_t dot2 = 0;
@@ -640,7 +640,7 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
     }
     // the row's sum: lanes by a butterfly, then all warps of the row (unused
     // places hold 0) in one fixed tree
-    float dot = f2(dot2).x + f2(dot2).y;
+    float dot = unpack_f2(dot2).x + unpack_f2(dot2).y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     if ((threadIdx.x & 31) == 0) red[parity][lane_row][t >> 5] = dot;
@@ -658,13 +658,13 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float4 v = *reinterpret_cast<const float4*>(&red[parity][lane_row][4 * i]);
-        w[i] = add2(f2(v.x, v.y), f2(v.z, v.w));
+        w[i] = fadd2(pack_f2(v.x, v.y), pack_f2(v.z, v.w));
       }
-      const float2 v = f2(add2(add2(w[0], w[1]), add2(w[2], w[3])));
+      const float2 v = unpack_f2(fadd2(fadd2(w[0], w[1]), fadd2(w[2], w[3])));
       dot = v.x + v.y;
     }
     const float coef = -rstd * (rstd * (rstd * dot * a.inv_cols));
-    const uint64_t c2 = f2(coef, coef);
+    const uint64_t c2 = pack_f2(coef, coef);
     if (on && (a.dr || a.dx)) {      // (the same for a whole warp)
       const bool drop = SHIFT && a.dx && a.d.threshold;
       ShiftedBits bits;

@@ -9,6 +9,8 @@
 #include <cuda.h>
 #include <stdint.h>
 
+#include "pairs.cuh"
+
 namespace sf {
 
 // Device-side error word of the including translation unit; bit values
@@ -183,41 +185,6 @@ __device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
   return v;
 }
 
-// Two fp32 lanes packed in 64 bits (low half = first element).
-__device__ __forceinline__ uint64_t pack_f2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpack_f2(uint64_t x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-// acc = x * v + acc on both fp32 lanes, each one IEEE fused multiply-add
-// rounded to nearest even (the same bits as two fmaf calls).
-__device__ __forceinline__ void ffma2(uint64_t& acc, uint64_t x, uint64_t v) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(x), "l"(v));
-}
-
-// a * b on both fp32 lanes (IEEE product, round to nearest even).
-__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-// a - b on both fp32 lanes (IEEE subtraction, round to nearest even).
-__device__ __forceinline__ uint64_t fsub2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // Both fp32 lanes rounded to bf16 (nearest even), low lane in the low half.
 __device__ __forceinline__ uint32_t bf16x2_rn(uint64_t x) {
   float lo, hi;

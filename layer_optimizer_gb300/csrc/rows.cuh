@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "common.h"
+#include "pairs.cuh"
 
 namespace sf {
 
@@ -29,48 +30,23 @@ struct Unit<float> {
 struct F8 {
   uint64_t p[4];
 };
-__device__ __forceinline__ uint64_t f2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 f2(uint64_t x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 
 __device__ __forceinline__ F8 unpack(const Unit<__nv_bfloat16>& u) {
   F8 v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v.p[i] = f2(__uint_as_float(u.w[i] << 16), __uint_as_float(u.w[i] & 0xFFFF0000u));
+  for (int i = 0; i < 4; ++i) v.p[i] = pack_f2(__uint_as_float(u.w[i] << 16), __uint_as_float(u.w[i] & 0xFFFF0000u));
   return v;
 }
 __device__ __forceinline__ F8 unpack(const Unit<float>& u) {
   F8 v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v.p[i] = f2(u.f[2 * i], u.f[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) v.p[i] = pack_f2(u.f[2 * i], u.f[2 * i + 1]);
   return v;
 }
 __device__ __forceinline__ void pack(const F8& v, Unit<__nv_bfloat16>& u) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 x = f2(v.p[i]);
+    const float2 x = unpack_f2(v.p[i]);
     const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);   // round to nearest even
     u.w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
@@ -78,7 +54,7 @@ __device__ __forceinline__ void pack(const F8& v, Unit<__nv_bfloat16>& u) {
 __device__ __forceinline__ void pack(const F8& v, Unit<float>& u) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 x = f2(v.p[i]);
+    const float2 x = unpack_f2(v.p[i]);
     u.f[2 * i] = x.x;
     u.f[2 * i + 1] = x.y;
   }
@@ -229,11 +205,11 @@ __device__ __forceinline__ void drop_apply(F8& v, const uint32_t (&w)[4], const 
   // half >= threshold, compared in the upper half of a word (threshold >= 1
   // here, 65536 included); a dropped element is 0 whatever its value
   const uint32_t limit = ((d.threshold - 1) << 16) | 0xFFFFu;
-  const uint64_t f = f2(d.factor, d.factor);
+  const uint64_t f = pack_f2(d.factor, d.factor);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 x = f2(mul2(v.p[j], f));
-    v.p[j] = f2((w[j] << 16) > limit ? x.x : 0.0f, w[j] > limit ? x.y : 0.0f);
+    const float2 x = unpack_f2(fmul2(v.p[j], f));
+    v.p[j] = pack_f2((w[j] << 16) > limit ? x.x : 0.0f, w[j] > limit ? x.y : 0.0f);
   }
 }
 __device__ __forceinline__ void drop_unit(F8& v, uint64_t b, const DropWords& w2, const DropConsts& d) {

@@ -295,16 +295,6 @@ __device__ __forceinline__ void fold_row_stats(const float (&x)[32], int valid, 
   s = acc;
 }
 
-// 2^x of the exponential unit (|relative error| about 2^-22); arguments here
-// are differences to a row's maximum or log-sum-exp, so at most 0 up to
-// rounding.
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-constexpr float kLog2e = 1.44269504f;
-
 // Writes 32 values of this lane's row, rounded to bf16, into half `half`
 // (0: columns 0-31, 1: 32-63) of a warp's 32-row x 64-column staging box,
 // 128-byte swizzled.
