@@ -21,6 +21,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "row_span.h"
@@ -497,7 +498,7 @@ constexpr int kMinStages = 3, kMaxStages = 4;
 // that hold any of the row (as far as the matrix goes: copy_span), so that units lie
 // in shared memory as in memory; of the first and last one, the columns outside the row are set to zero, and
 // those inside are written to memory by their threads, the rest by bulk stores
-// (16384 x 4095 bf16: 170 us, with dropout 221, against 349 element by element).
+// (16384 x 4095 bf16: 175 us, with dropout 226, against 349 element by element).
 template <typename TA, typename TS, int K, bool KEEP, bool SHIFT>
 __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) k_add_rmsnorm_bwd_ring(const BwdArgs a, const int stages) {
   constexpr int MODE = SHIFT ? kShifted : kAligned;
@@ -523,16 +524,20 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
     if (SHIFT) bulk_load(at + c.begin, static_cast<const unsigned char*>(row) - m_lane * size + c.begin, c.end - c.begin, &full[st]);
     else bulk_load(at, row, a.cols * size, &full[st]);
   };
-  auto fill = [&](int64_t base, int st) {
+  // (ENDS: the matrix's last row may be among them; see copy_span)
+  auto fill_rows = [&](int64_t base, int st, auto ends) {
+    constexpr bool ENDS = SHIFT && decltype(ends)::value;
     const int n = (int)min((int64_t)rpb, a.rows - base);
     const int64_t row = base + threadIdx.x;
-    const bool mine = (int)threadIdx.x < n, last = row == a.rows - 1;
+    const bool mine = (int)threadIdx.x < n, last = ENDS && mine && row == a.rows - 1;
     unsigned char* at = ring + (size_t)st * stage_bytes;
     uint32_t bytes = (uint32_t)n * (row_a + row_s + (ring_d ? row_s : 0u));
     if (SHIFT) {
       const CopySpan ca = copy_span(m_lane, a.cols, sizeof(TA), last), cs = copy_span(m_lane, a.cols, sizeof(TS), last);
       bytes = __reduce_add_sync(0xffffffffu, mine ? ca.end - ca.begin + (ring_d ? 2u : 1u) * (cs.end - cs.begin) : 0u);
-      if (mine && last) {      // ordered before the readers by the arrival below
+    }
+    if (ENDS) {
+      if (last) {      // ordered before the readers by the arrival below
         load_rest(at + threadIdx.x * row_a, row_ptr<TA>(a.dh, a.lddh, row), m_lane, a.cols);
         load_rest(at + off_s + threadIdx.x * row_s, row_ptr<TS>(a.s, a.lds, row), m_lane, a.cols);
         if (ring_d) load_rest(at + off_d + threadIdx.x * row_s, row_ptr<TS>(a.dsum, a.lddsum, row), m_lane, a.cols);
@@ -546,6 +551,12 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
       bring(at + off_s + threadIdx.x * row_s, row_ptr<TS>(a.s, a.lds, row), sizeof(TS), st, last);
       if (ring_d) bring(at + off_d + threadIdx.x * row_s, row_ptr<TS>(a.dsum, a.lddsum, row), sizeof(TS), st, last);
     }
+  };
+  // apart where a row is long (16384 x 4095 bf16 175 us, with dropout 228; in one form 181 and 236), in one form where
+  // rows are short (32714 x 596 fp32 80 and 86 us; apart 81 and 88)
+  auto fill = [&](int64_t base, int st) {
+    if (!SHIFT || K == 2 || base + rpb >= a.rows) fill_rows(base, st, std::true_type());
+    else fill_rows(base, st, std::false_type());
   };
   // ... and those of its outputs to global memory (each lane its own row, so
   // that the lane that fills a row's place knows when it has been read)
