@@ -14,7 +14,8 @@
 // 81), blocks of whole warps rather than powers of two, fp32 arithmetic in pairs, one
 // division a scale group.  16384 x 4096 bf16 81 us (6.6 TB/s); 8192 x 12288,
 // fp32 stream, e4m3 with 128-column groups 168 us (6.6 TB/s); one row of 4096
-// 3.3 us.  Dropout on: 91 us at 16384 x 4096, 170 at 16384 x 4095 (129 off).
+// 3.3 us.  Dropout on: 91 us at 16384 x 4096, 169 at 16384 x 4095 (128 off).
+// The fp32 and off-unit instances spill 4 to 84 bytes at these limits.
 //
 // The norm is taken of s in fp32, before s is rounded to its stored type, so
 // storing s in bf16 costs h no precision; the backward pass uses the stored s.
@@ -314,7 +315,9 @@ __global__ void __maxnreg__(MODE == kShifted && DROP && sizeof(TA) == 4 ? 96 : s
 // second small kernel (5 us at 456 x 4096, its launch overlapped), summed in
 // block order (no atomics).  This form, with loads into registers, serves few
 // rows, short, long and unaligned ones; 16384 x 4096 bf16 with dropout takes
-// it 165 us, against 118 us (5.7 TB/s) in the staged form further down.
+// it 165 us, against 118 us (5.7 TB/s) in the staged form further down.  Its 512
+// threads leave 128 registers, of which all instances but bf16 over bf16 spill
+// 36 to 424 bytes.
 struct BwdArgs {
   const void* dh;
   const void* s;
@@ -552,8 +555,8 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
       if (ring_d) bring(at + off_d + threadIdx.x * row_s, row_ptr<TS>(a.dsum, a.lddsum, row), sizeof(TS), st, last);
     }
   };
-  // apart where a row is long (16384 x 4095 bf16 175 us, with dropout 228; in one form 181 and 236), in one form where
-  // rows are short (32714 x 596 fp32 80 and 86 us; apart 81 and 88)
+  // apart where a row is long (16384 x 4095 bf16, called in turn, 175 us, with dropout 228; in one form 181 and 236), in
+  // one form where rows are short (32714 x 596 fp32 80 and 86 us; apart 81 and 88)
   auto fill = [&](int64_t base, int st) {
     if (!SHIFT || K == 2 || base + rpb >= a.rows) fill_rows(base, st, std::true_type());
     else fill_rows(base, st, std::false_type());
@@ -839,22 +842,24 @@ inline size_t ring_row_bytes(int64_t cols, bool shifted, int32_t ta, int32_t ts,
 // The staged kernel takes aligned rows of whole units, long enough that a
 // block's few copies are worth their set-up and short enough that three fit
 // in shared memory (without dsum if need be: 8192 x 12288 bf16, fp32 stream,
-// 293 us, against 382 us with loads into registers), when there is more than
+// 296 us, against 382 us with loads into registers), when there is more than
 // one block's worth of rows an SM.
 inline bool ring_fits(int64_t rows, int64_t cols, RowMode mode, int32_t ta, int32_t ts) {
   return (mode == kShifted || (mode == kAligned && cols % 8 == 0)) && cols >= 512 && rows >= 2 * sm_count() &&
          kMinStages * ring_row_bytes(cols, mode == kShifted, ta, ts, false) <= kSmemPerSm - 1024;
 }
 
+template <typename TA, typename TS, bool SHIFT>
+const void* ring_kernel(int k, bool keep) {
+  if (k == 2) return (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 2, true, SHIFT>;
+  // rows too long to keep their gains have over 12288 columns, of which the ring does not hold three in fp32 throughout
+  if constexpr (sizeof(TA) + sizeof(TS) < 8)
+    if (!keep) return (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4, false, SHIFT>;
+  return (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4, true, SHIFT>;
+}
 template <typename TA, typename TS>
 const void* ring_kernel(int k, bool keep, bool shifted) {
-  if (shifted)
-    return k == 2 ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 2, true, true>
-           : keep ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4, true, true>
-                  : (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4, false, true>;
-  return k == 2 ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 2, true, false>
-         : keep ? (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4, true, false>
-                : (const void*)&k_add_rmsnorm_bwd_ring<TA, TS, 4, false, false>;
+  return shifted ? ring_kernel<TA, TS, true>(k, keep) : ring_kernel<TA, TS, false>(k, keep);
 }
 
 // Two units a thread up to 1024 columns, four beyond (16384 x 4096 bf16, all
