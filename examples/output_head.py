@@ -11,8 +11,9 @@ One step runs, all on the device:
 dr and dx are what the blocks below take.  The dropout mask is drawn again in
 the backward pass from the step's offset, so nothing of it is kept; the
 cross-entropy keeps no logits; dgain and dW come in bf16, as the update wants
-them.  `checkpoint=True` keeps h in 8 bits with scales beside it, for a copy of
-the activations that crosses the host link in half the bytes.
+them.  `checkpoint=True` writes h in 8 bits with scales beside it as well, for a copy of
+the activations that crosses the host link in half the bytes; `restored()` is
+how such a copy is read back.
 
     python examples/output_head.py [--tokens N] [--hidden D] [--vocab V] [--steps K]
 """
@@ -66,6 +67,10 @@ class OutputHead:
         native.sf_add_rmsnorm_backward(self.dh, self.s, gain, self.rstd, dresidual=self.dr, dx=self.dx,
                                        dgain=self.grads[0], p=p, rng=rng, ws=self.norm_ws, stream=stream)
         return self.loss
+
+    def restored(self):
+        """h in fp32 from its 8-bit copy: the stored values times their groups' scales."""
+        return self.h8.float() * self.h8_scale.repeat_interleave(128, dim=1)[:, :self.hidden]
 
     def step(self, x, r, labels, hp, stream=None):
         """One training step; returns the loss (on the device) and leaves dr, dx for the blocks below."""

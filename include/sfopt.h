@@ -430,7 +430,10 @@ sf_status sf_dropout(const sf_matrix* x, const sf_matrix* residual,
  *              written.  Per group of `group` (32, 64, 128; 0: the row)
  *              columns scale = max(max |h| / 448, 2^-126) and the stored
  *              value is h / scale rounded to e4m3, so h is about value *
- *              scale.  A NaN makes its group's scale NaN.
+ *              scale.  (Scale and quotient are taken by multiplication: the
+ *              scale within one unit in its last place, and a quotient within
+ *              2^-22 of the middle between two e4m3 values may take either.)
+ *              A NaN makes its group's scale NaN.
  *   rstd     : fp32 [rows], for the backward pass; NULL: not written.
  * At least one of h and h8.  The norm is taken of s in fp32, before s is
  * rounded to its stored type; h and h8 are each rounded once, from fp32. */

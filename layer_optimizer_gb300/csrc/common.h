@@ -148,7 +148,7 @@ enum TcEpilogue : int {
   kTcBf16 = 2,   // C bf16
   kTcStats = 3,  // row_stats, label_logit, and with `store` C = exp(A B^T - tile maximum) in bf16
   kTcRows = 5,   // C bf16 or fp32, product row i written to row row_map[i]
-  kTcGrad = 4    // C = exp(A B^T - lse) - onehot(label) in bf16, 0 in rows past M
+  kTcGrad = 4    // C = softmax - onehot(label) in bf16 from A B^T and lse, 0 in rows past M
 };
 struct TcJob {
   const void* A = nullptr;
@@ -161,8 +161,9 @@ struct TcJob {
   float alpha = 1.0f;
   bool accumulate = false;         // fp32 epilogues
   int splits = 1;                  // kTcSplit
-  float2* row_stats = nullptr;     // kTcF32: [M][tiles]; kTcStats: [M][stats_ld], tile col0 / 256 + t
-  int32_t stats_ld = 0;
+  float2* row_stats = nullptr;     // kTcF32: [M][tiles of kTcTileN]; kTcStats: [M][stats_ld], one entry per kTcStatCols
+                                   // columns, at (col0 + column) / kTcStatCols
+  int32_t stats_ld = 0;            // at least ceil((col0 + N) / kTcStatCols)
   int32_t col0 = 0;                // vocabulary id of column 0 (a multiple of 256)
   bool store = false;
   const int32_t* labels = nullptr; // [M] (kTcStats, kTcGrad); ids outside the product's columns match nothing

@@ -215,9 +215,9 @@ LcePlan plan_lce(int64_t N, int64_t V, int64_t chunk) {
 //   3. Per piece, the last first: dH += f G W_piece, dW_piece = f G^T H, f =
 //      scale / n in fp32; for the others G is formed first, as the epilogue of
 //      Z once more.
-// 8 - 2 / P times n D V flops for P pieces (8192 x 4096 x 128256: 19.0 ms with
-// 16 pieces in 0.37 GB, 18.1 with 4 in 0.76, 17.2 with 2 in 1.29, 15.2 with one
-// in 2.2; the token-chunk form takes 28.8 ms in 0.40 GB, 16.4 in 3.6), against 6 when a token chunk's
+// 8 - 2 / P times n D V flops for P pieces (8192 x 4096 x 128256: 19.2 ms with
+// 16 pieces in 0.40 GB, 17.9 with 4 in 0.80, 16.9 with 2 in 1.32, 15.0 with one
+// in 2.2; the token-chunk form takes 28.5 ms in 0.40 GB, 16.4 in 3.6), against 6 when a token chunk's
 // logits are kept, but the workspace is one n x piece block of bf16 whatever
 // V, every row of dW is written once, in bf16 if asked (the type that the
 // AdamW step takes), and dW is not read back for accumulation.  Up to 16 tokens

@@ -1,7 +1,8 @@
 // The vocabulary-piece cross-entropy for at most 16 tokens: three launches that
 // stream W, instead of six around the tiled products, whose 256-row tiles would
 // be nearly empty.  Bound by W and dW (2 bytes an entry read twice and written
-// once) and, where those are small, by the launches.
+// once) and, where those are small, by latencies that add up: the second kernel reads W only once the
+// statistics are joined and z has become g (19 of 24 us at 16 x 1024 x 8000, for data worth 5).
 //   k_lce_few_logits  z = W h for 16 tokens at a time on the warp-level tensor
 //                     instruction (16 tokens fill one of its operands; the
 //                     products are far from bounding anything), z kept in fp32
@@ -14,8 +15,8 @@
 // the summed index, and which column of the output a lane's fragment stands
 // for, are free to choose, so fragments are what the lanes have loaded.
 // Against the tiled products: 16 x 1024 x 8000 24 us (39), 6 x 64 x 74225 23
-// (57), 1 x 4096 x 32000 181 (229; W twice at the copy rate and dW at the 4 TB/s
-// of writing alone: 144), 16 x 4096 x 128256 651 (645).  Fetching the next
+// (57), 1 x 4096 x 32000 180 (229; W twice at the copy rate and dW at the 4 TB/s
+// of writing alone: 144), 16 x 4096 x 128256 652 (645).  Fetching the next
 // rows into L2 ahead was slower (198 us at 1 x 4096 x 32000).
 #pragma once
 
@@ -330,7 +331,9 @@ __global__ void __launch_bounds__(256, 2) k_lce_few_grads(const FewArgs a) {
   }
 }
 
-// Whether a call takes this form.
+// Whether a call takes this form.  A rule on tokens and D alone: it gains most
+// where W is small (24 us against 39, see above) and loses 1 % at the largest (16 x 4096 x
+// 128256, 652 us against 645).
 inline bool few_tokens(int64_t N, int64_t D) { return N <= kFewTokens && D % 8 == 0 && D <= 1 << 20; }
 
 struct FewPlan {

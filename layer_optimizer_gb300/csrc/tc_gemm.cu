@@ -265,7 +265,7 @@ struct TcGemmArgs {
   float2* row_stats;     // optional [M][n_tiles]: per row and column tile, (max, sum exp(c - max)) of C
   int32_t splits;        // parts of the sum over K, each a product of its own (kTcSplit: C is [splits][M][N])
   // softmax epilogues (kTcStats, kTcGrad)
-  int32_t stats_ld;      // tiles of a row of row_stats (kTcStats)
+  int32_t stats_ld;      // entries of a row of row_stats (kTcStats)
   int32_t col0;          // vocabulary id of column 0, a multiple of the tile width
   int32_t store;         // kTcStats: also write exp(c - tile maximum) to C
   const int32_t* labels; // [M]
@@ -809,6 +809,19 @@ __global__ void __launch_bounds__(TcStages<EPI>::kThreads, 1)
   }
 }
 
+// Map of C's tensor stores: fp32, boxes of 32 rows x 32 columns.
+sf_status make_map_c(CUtensorMap* map, float* C, int64_t M, int64_t N, int64_t ldc) {
+  cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
+  cuuint64_t strides[1] = {(cuuint64_t)(ldc * 4)};
+  cuuint32_t box[2] = {32, 32};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, C, dims, strides, box, estr,
+                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SF_ERR_CUDA, "cuTensorMapEncodeTiled (C) failed (%d)", (int)r);
+  return SF_OK;
+}
+
 // The same for partial products [splits][M][N] (3D, boxes 32 x 32 x 1) ...
 sf_status make_map_split(CUtensorMap* map, float* C, int64_t M, int64_t N, int64_t ldc, int64_t splits) {
   cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)splits};
@@ -832,18 +845,6 @@ sf_status make_map_c16(CUtensorMap* map, void* C, int64_t M, int64_t N, int64_t 
                                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SF_ERR_CUDA, "cuTensorMapEncodeTiled (bf16 C) failed (%d)", (int)r);
-  return SF_OK;
-}
-
-sf_status make_map_c(CUtensorMap* map, float* C, int64_t M, int64_t N, int64_t ldc) {
-  cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
-  cuuint64_t strides[1] = {(cuuint64_t)(ldc * 4)};
-  cuuint32_t box[2] = {32, 32};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, C, dims, strides, box, estr,
-                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(SF_ERR_CUDA, "cuTensorMapEncodeTiled (C) failed (%d)", (int)r);
   return SF_OK;
 }
 
