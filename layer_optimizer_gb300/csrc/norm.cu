@@ -720,6 +720,10 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
       pass ^= 1u;
     }
   }
+  if (dead) {      // copies still under way land before their memory is used again or given up (waited for once more, bounded)
+    const int64_t n = ceil_div<int64_t>(a.rows - first, step);
+    for (int i = 0; i < stages && i < n; ++i) mbar_wait_u32(smem_u32(&full[i]), (uint32_t)((n - 1 - i) / stages) & 1u);
+  }
   __syncthreads();
   if (threadIdx.x < 32) {
     drain(base - step, st == 0 ? stages - 1 : st - 1);       // the last row's outputs
