@@ -555,10 +555,10 @@ __global__ void __maxnreg__(K == 2 && !SHIFT ? 80 : KEEP && K == 4 ? 168 : 128) 
       if (ring_d) bring(at + off_d + threadIdx.x * row_s, row_ptr<TS>(a.dsum, a.lddsum, row), sizeof(TS), st, last);
     }
   };
-  // apart where a row is long (16384 x 4095 bf16, called in turn, 175 us, with dropout 228; in one form 181 and 236), in
-  // one form where rows are short (32714 x 596 fp32 80 and 86 us; apart 81 and 88)
+  // two forms: a test for the last row in every copy costs long rows 3 % (16384 x 4095 bf16, pass after pass, 181 us, with
+  // dropout 236; this way 175 and 228), and short ones nothing (32714 x 597 fp32 83 and 93 us either way)
   auto fill = [&](int64_t base, int st) {
-    if (!SHIFT || K == 2 || base + rpb >= a.rows) fill_rows(base, st, std::true_type());
+    if (!SHIFT || base + rpb >= a.rows) fill_rows(base, st, std::true_type());
     else fill_rows(base, st, std::false_type());
   };
   // ... and those of its outputs to global memory (each lane its own row, so
