@@ -1,6 +1,6 @@
 """The staged norm backward at widths whose blocks have 96 threads (GPU).
 
-Rows of 2056 to 3072 columns take blocks of 96 threads, one row each; bounds and
+Rows of 257 to 384 units of eight columns take blocks of 96 threads, one row each; bounds and
 checks are those of test_gpu_norm.py.
 """
 
