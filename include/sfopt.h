@@ -64,9 +64,10 @@ typedef enum {
   SF_ERR_TIMEOUT = -5      /* a bounded host wait ran out                    */
 } sf_status;
 
-/* SF_E4M3: 8-bit floats (4 exponent bits, 3 fraction bits, largest value 448),
- * taken only where a call says so. */
-typedef enum { SF_BF16 = 0, SF_FP32 = 1, SF_E4M3 = 2 } sf_dtype;
+/* SF_E4M3: 8-bit floats (4 exponent bits, 3 fraction bits, largest value 448);
+ * SF_E8M0: powers of two, 2^(code - 127), code 255 NaN.  Each is taken only
+ * where a call says so. */
+typedef enum { SF_BF16 = 0, SF_FP32 = 1, SF_E4M3 = 2, SF_E8M0 = 3 } sf_dtype;
 
 /* AdamW hyper-parameters.  Given in double; the library derives the fp32
  * constants the kernels use (1-beta1, 1-beta2, 1-lr*wd, lr/(1-beta1^t),
@@ -508,6 +509,135 @@ sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W,
                                      float* loss, float* token_loss,
                                      const sf_matrix* dH, const sf_matrix* dW,
                                      void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * (e) 8-bit activation checkpoints and the end of a residual block: what a
+ * forward pass keeps for its backward pass (SlideFormer's activation
+ * checkpoints, at half the bytes of bf16 on the device and on the host link),
+ * and the operators that write and read it.
+ *
+ * A checkpoint of a matrix v holds e4m3 values and one scale per group of
+ * `group` (32, 64, 128; 0: the row) columns; v is about value * scale.  As
+ * written here a scale is 2^k in 8 bits (SF_E8M0), k the smallest k >= -126
+ * with max |v| <= 448 2^k over the group's finite entries, and a value is
+ * v / 2^k rounded once to the nearest e4m3 value, ties to even; infinities and
+ * NaN become NaN, whatever their group holds.  So value * scale is exact in
+ * bf16 and in fp32, within 2^-4 of v where |v| >= 2^-6 scale, and else within
+ * 2^-10 scale (an entry next to fp32's largest may round to infinity).
+ *
+ * Readers also take fp32 scales (SF_FP32), as sf_add_rmsnorm_forward writes
+ * them beside h8.  Matrices and vectors as in (d).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  sf_matrix values;    /* SF_E4M3 */
+  void* scale;         /* dense [rows][ceil(cols / group)], or [rows] with group 0 */
+  int32_t scale_dtype; /* SF_E8M0, or SF_FP32 where it is read */
+  int32_t group;       /* 32, 64, 128, or 0 */
+} sf_checkpoint;
+
+/* Writes x (SF_BF16 or SF_FP32) as a checkpoint; any number of columns. */
+sf_status sf_checkpoint_store(const sf_matrix* x, const sf_checkpoint* out,
+                              void* stream);
+
+/* y = value * scale [* row_factor_i] [* (gain_offset + gain_j)], rounded once
+ * to y's type (SF_BF16 or SF_FP32).
+ *   row_factor : fp32 [rows], or NULL.     gain : [cols], gain_dtype bf16 or
+ *                fp32, or NULL.
+ * With row_factor = rstd and the norm's gain, the checkpoint of a norm's input
+ * gives its output again. */
+sf_status sf_checkpoint_load(const sf_checkpoint* c, const float* row_factor,
+                             const void* gain, sf_dtype gain_dtype,
+                             double gain_offset, const sf_matrix* y,
+                             void* stream);
+
+/* The weight gradient of a linear layer y = X W^T from the checkpoint of its
+ * input:  dW = base + dY^T X,  dW_oi = base_oi + sum_t dY_to value_ti scale_t.
+ *   dY   : SF_BF16 [tokens][out].   c : [tokens][in].   Both 16-byte aligned
+ *          base and rows (SF_ERR_UNSUPPORTED otherwise), device memory of the
+ *          current device.
+ *   base : NULL (zero), or dW's type and sizes; may be dW itself, to add to it.
+ *   dW   : SF_BF16 or SF_FP32 [out][in].
+ *   ws   : device scratch of ws_bytes >= sf_checkpoint_wgrad_workspace_bytes(
+ *          tokens, out, in), 16-byte aligned; may be NULL where that is 0.
+ * Tensor cores, fp32 sums.  value * scale enters as bf16: exact with SF_E8M0
+ * scales, rounded once with SF_FP32 ones.  No token: dW = base (or 0).
+ * Deterministic. */
+size_t sf_checkpoint_wgrad_workspace_bytes(int64_t tokens, int64_t out,
+                                           int64_t in);
+
+sf_status sf_checkpoint_wgrad(const sf_matrix* dY, const sf_checkpoint* c,
+                              const sf_matrix* base, const sf_matrix* dW,
+                              void* ws, size_t ws_bytes, void* stream);
+
+/* The end of a residual block: the norm after the block, its gate, the
+ * residual's addition with its scales, and the norm before the next block.
+ *
+ *   n = x rstd_post (gain_offset + gain_post),  rstd_post = 1 / sqrt(mean(x^2) + eps)
+ *                                      (n = x without gain_post)
+ *   s = residual_scale r + block_scale gate n
+ *   h = s rstd_pre (gain_offset + gain_pre),    rstd_pre  = 1 / sqrt(mean(s^2) + eps)
+ *
+ * over rows of 1..16384 columns (SF_ERR_UNSUPPORTED beyond).  Row i takes row
+ * i / gate_span of the gate (an adaptive gate per sequence; gate_span 0: one
+ * row for all; 1: one for each).
+ *   x        : the block's output, SF_BF16 or SF_FP32.
+ *   residual : NULL (none), SF_BF16 or SF_FP32.
+ *   gain_post, gain_pre : [cols], gain_dtype bf16 or fp32.  Without gain_post
+ *              there is no norm after the block; h needs gain_pre.
+ *   gate     : NULL (1), or [ceil(rows / gate_span)][cols], bf16 or fp32.
+ *   sum, h   : receive s (residual's type) and h (x's type); each NULL: not written.
+ *   x8, sum8 : receive checkpoints of x and s; each NULL: not written.
+ *   rstd_post, rstd_pre : fp32 [rows], for the backward pass; NULL: not
+ *              written.  rstd_post needs gain_post, rstd_pre gain_pre.
+ * At least one of sum, h, x8 and sum8.  fp32 arithmetic; h and sum8 are taken
+ * of s before it is rounded; each output is rounded once. */
+typedef struct {
+  double eps;
+  double residual_scale;
+  double block_scale;
+  double gain_offset; /* 0, or 1 where gains are stored less one */
+  int64_t gate_span;
+} sf_sandwich;
+
+sf_status sf_sandwich_norm_forward(const sf_sandwich* p, const sf_matrix* x,
+                                   const sf_matrix* residual,
+                                   const void* gain_post, const void* gain_pre,
+                                   sf_dtype gain_dtype, const sf_matrix* gate,
+                                   const sf_matrix* sum, const sf_matrix* h,
+                                   const sf_checkpoint* x8,
+                                   const sf_checkpoint* sum8, float* rstd_post,
+                                   float* rstd_pre, void* stream);
+
+/* The gradients of that call, x and s given in full or as checkpoints (then
+ * the formulas take the restored values, with the forward pass's rstd):
+ *   d  = dsum + rstd_pre (dh g_pre - s rstd_pre^2 mean(dh g_pre s)),  g = gain_offset + gain
+ *   dresidual = residual_scale d
+ *   e  = block_scale d gate
+ *   dx = rstd_post (e g_post - x rstd_post^2 mean(e g_post x))   (dx = e without gain_post)
+ *   dgain_pre = sum over rows of dh s rstd_pre,  dgain_post of e x rstd_post
+ *   dgate     = sum over each span's rows of block_scale d n
+ *   dh   : gradient of h, x's type; NULL: h was not used (then dsum is needed,
+ *          and sum, gain_pre and rstd_pre are not).
+ *   dsum : gradient that reaches s from elsewhere, the sum's type; NULL: none.
+ *   x, x8 and sum, sum8 : at most one of each pair; x is needed with gain_post
+ *          or dgate (and dx, dgain_post or dgate wanted), sum with dh.
+ *   dresidual (the sum's type), dx (x's type), dgain_post, dgain_pre ([cols],
+ *          dgain_dtype bf16 or fp32), dgate (the gate's sizes, bf16 or fp32):
+ *          each NULL: not wanted, not all.
+ *   ws   : device scratch of ws_bytes >= sf_sandwich_norm_workspace_bytes(rows,
+ *          cols), 16-byte aligned; only used with a dgain or dgate.
+ * fp32 arithmetic, one rounding at the end; sums over rows run in a fixed
+ * order (no atomics). */
+size_t sf_sandwich_norm_workspace_bytes(int64_t rows, int64_t cols);
+
+sf_status sf_sandwich_norm_backward(
+    const sf_sandwich* p, const sf_matrix* dh, const sf_matrix* dsum,
+    const sf_matrix* x, const sf_checkpoint* x8, const sf_matrix* sum,
+    const sf_checkpoint* sum8, const void* gain_post, const void* gain_pre,
+    sf_dtype gain_dtype, const sf_matrix* gate, const float* rstd_post,
+    const float* rstd_pre, const sf_matrix* dresidual, const sf_matrix* dx,
+    void* dgain_post, void* dgain_pre, sf_dtype dgain_dtype,
+    const sf_matrix* dgate, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * (c) Layer-sliding window.

@@ -1,0 +1,203 @@
+// 8-bit checkpoints of a matrix: written (values and scales in one pass) and
+// read back, optionally times a factor per row and a gain per column.
+//
+// Both move three bytes an element with bf16 on the other side and are bound by HBM.
+#include <algorithm>
+
+#include "lanes.cuh"
+
+namespace sf {
+namespace {
+
+constexpr int kK = 4;               // steps a thread holds in registers
+constexpr int kMaxThreads = 512;
+
+struct CkArgs {
+  const void* x;         // store: the matrix; load: unused
+  void* y;               // load: the matrix
+  int64_t ldx;
+  int64_t rows;
+  int64_t cols;
+  Ck ck;
+  int32_t tpr, rpb, steps;      // threads a row, rows a block, segments of tpr * kK * 8 columns a row
+  const float* row_factor;
+  const void* gain;
+  int32_t gain_fp32;
+  float gain_offset;
+};
+
+// A row's segments of tpr * kK * 8 columns in turn.  One scale a row: of a
+// row longer than a segment the maximum is taken first, in a pass of its own.
+template <typename T, int LAY>
+__global__ void __launch_bounds__(kMaxThreads) k_checkpoint_store(const CkArgs a) {
+  __shared__ float red[kMaxThreads / 32];
+  const int tpr = a.tpr, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
+  const int64_t row = (int64_t)blockIdx.x * a.rpb + lane_row;
+  const bool on = row < a.rows;
+  const Lane l = lane_of<LAY>(t, tpr);
+  const int64_t seg = (int64_t)tpr * kK * 8;
+  const T* x = row_ptr<T>(a.x, a.ldx, on ? row : 0);
+  const bool one = a.ck.group_log2 == 0;
+  auto left = [&](int64_t s) { return on ? (int)min(a.cols - s * seg, seg) : 0; };      // columns of segment s
+  uint32_t code = 1;
+  F8 v[kK];
+  float top[1] = {0.0f};
+  if (one) {
+    for (int64_t s = 0; s < a.steps; ++s) {
+      const int n = left(s);
+#pragma unroll
+      for (int k = 0; k < kK; ++k) {
+        v[k] = l.c0(k) < n ? load8<LAY>(x + s * seg, l.c0(k), l.dj, n) : zero8();
+        top[0] = fmaxf(top[0], top_finite<0, 8>(v[k]));
+      }
+    }
+    row_reduce_n<1, 0>(top, tpr, red);
+    code = e8m0_of(top[0]);
+    if (on && t == 0) a.ck.s8[row] = (uint8_t)code;
+  }
+  for (int64_t s = 0; s < a.steps; ++s) {
+    const int n = left(s);
+    if (!one || a.steps > 1) {
+#pragma unroll
+      for (int k = 0; k < kK; ++k) v[k] = l.c0(k) < n ? load8<LAY>(x + s * seg, l.c0(k), l.dj, n) : zero8();
+    }
+    Ck ck = a.ck;
+    ck.q += s * seg;
+    if (!one) ck.s8 += (s * seg) >> ck.group_log2;
+#pragma unroll
+    for (int k = 0; k < kK; ++k) ck_store8<LAY>(ck, row, l.c0(k), l.dj, n, v[k], code);
+  }
+}
+
+template <typename T, int LAY>
+__global__ void __launch_bounds__(kMaxThreads) k_checkpoint_load(const CkArgs a) {
+  const int tpr = a.tpr, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
+  const int64_t row = (int64_t)blockIdx.x * a.rpb + lane_row;
+  if (row >= a.rows) return;
+  const Lane l = lane_of<LAY>(t, tpr);
+  const int64_t seg = (int64_t)tpr * kK * 8;
+  const float f = a.row_factor ? a.row_factor[row] : 1.0f;
+  const uint64_t f2 = pack_f2(f, f);
+  for (int64_t s = 0; s < a.steps; ++s) {
+    const int n = (int)min(a.cols - s * seg, seg);
+    Ck ck = a.ck;
+    ck.q += s * seg;
+    const int64_t at = ck.group_log2 ? (s * seg) >> ck.group_log2 : 0;
+    if (ck.s8) ck.s8 += at;
+    else ck.s32 += at;
+    F8 v[kK];
+#pragma unroll
+    for (int k = 0; k < kK; ++k)
+      if (l.c0(k) < n) v[k] = load8<LAY>(ck, row, l.c0(k), l.dj, n);
+#pragma unroll
+    for (int k = 0; k < kK; ++k) {
+      if (l.c0(k) >= n) continue;
+      if (a.row_factor) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[k].p[i] = fmul2(v[k].p[i], f2);
+      }
+      if (a.gain) {
+        const void* g = static_cast<const char*>(a.gain) + s * seg * (a.gain_fp32 ? 4 : 2);
+        const F8 w = load_vec<LAY>(g, a.gain_fp32, l.c0(k), l.dj, n, a.gain_offset);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[k].p[i] = fmul2(v[k].p[i], w.p[i]);
+      }
+      store8<LAY>(row_ptr<T>(a.y, a.ldx, row) + s * seg, l.c0(k), l.dj, n, v[k]);
+    }
+  }
+}
+
+// Threads a row: a power of two up to 64 (at least 16, a group of 128 columns), or whole warps.
+void pick_shape(CkArgs& a) {
+  const int64_t units = ceil_div<int64_t>(a.cols, 8);
+  const int64_t per = a.rows < 2 * sm_count() ? 1 : kK;
+  const int64_t t = std::min<int64_t>(ceil_div<int64_t>(units, per), kMaxThreads);
+  if (t > 64) {
+    a.tpr = (int32_t)ceil_div<int64_t>(t, 32) * 32;
+    a.rpb = 1;
+  } else {
+    int p = 16;
+    while (p < t) p *= 2;
+    a.tpr = p;
+    a.rpb = 128 / p;
+  }
+  a.steps = (int32_t)ceil_div<int64_t>(units, (int64_t)a.tpr * kK);
+}
+
+template <template <typename, int> class K>
+const void* pick_kernel(int32_t dtype, Lay lay) {
+  using B = __nv_bfloat16;
+  if (dtype == SF_BF16) return lay == kUnits ? K<B, kUnits>::ptr() : K<B, kStrided>::ptr();
+  return lay == kUnits ? K<float, kUnits>::ptr() : K<float, kStrided>::ptr();
+}
+template <typename T, int LAY>
+struct Store {
+  static const void* ptr() { return (const void*)&k_checkpoint_store<T, LAY>; }
+};
+template <typename T, int LAY>
+struct Load {
+  static const void* ptr() { return (const void*)&k_checkpoint_load<T, LAY>; }
+};
+
+constexpr unsigned kTypes = 1u << SF_BF16 | 1u << SF_FP32;
+
+sf_status launch(const void* kernel, CkArgs& a, void* stream, const char* what) {
+  const int64_t grid = ceil_div<int64_t>(a.rows, a.rpb);
+  if (grid > INT32_MAX) return fail(SF_ERR_UNSUPPORTED, "too many rows");
+  void* args[] = {&a};
+  SF_CUDA_TRY(cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3(a.tpr * a.rpb), args, 0, as_stream(stream)), what);
+  return SF_OK;
+}
+
+}  // namespace
+}  // namespace sf
+
+extern "C" {
+
+sf_status sf_checkpoint_store(const sf_matrix* x, const sf_checkpoint* out, void* stream) {
+  using namespace sf;
+  clear_error();
+  NvtxRange nvtx_range("sf_checkpoint_store");
+  SF_TRY(check_matrix(x, "x", -1, -1, kTypes));
+  SF_TRY(check_checkpoint(out, "checkpoint", x->rows, x->cols, true));
+  if (!x->rows || !x->cols) return SF_OK;
+  CkArgs a{};
+  a.x = x->data;
+  a.ldx = x->ld;
+  a.rows = x->rows;
+  a.cols = x->cols;
+  a.ck = device_ck(out);
+  pick_shape(a);
+  return launch(pick_kernel<Store>(x->dtype, on_units(x) && on_units(out) ? kUnits : kStrided), a, stream, "launch k_checkpoint_store");
+}
+
+sf_status sf_checkpoint_load(const sf_checkpoint* c, const float* row_factor, const void* gain, sf_dtype gain_dtype,
+                             double gain_offset, const sf_matrix* y, void* stream) {
+  using namespace sf;
+  clear_error();
+  NvtxRange nvtx_range("sf_checkpoint_load");
+  SF_TRY(check_matrix(y, "y", -1, -1, kTypes));
+  SF_TRY(check_checkpoint(c, "checkpoint", y->rows, y->cols, false));
+  SF_TRY(check_aligned(row_factor, sizeof(float), "row_factor"));
+  if (gain) {
+    if (gain_dtype != SF_BF16 && gain_dtype != SF_FP32) return fail(SF_ERR_UNSUPPORTED, "gain: type %d is not taken here", (int)gain_dtype);
+    SF_TRY(check_aligned(gain, dtype_bytes(gain_dtype), "gain"));
+    if (!(gain_offset >= -1e30 && gain_offset <= 1e30)) return fail(SF_ERR_INVALID, "gain_offset must be finite");
+  }
+  if (!y->rows || !y->cols) return SF_OK;
+  CkArgs a{};
+  a.y = y->data;
+  a.ldx = y->ld;
+  a.rows = y->rows;
+  a.cols = y->cols;
+  a.ck = device_ck(c);
+  a.row_factor = row_factor;
+  a.gain = gain;
+  a.gain_fp32 = gain_dtype == SF_FP32;
+  a.gain_offset = (float)gain_offset;
+  pick_shape(a);
+  const bool units = on_units(y) && on_units(c) && (!gain || on_units(gain, gain_dtype));
+  return launch(pick_kernel<Load>(y->dtype, units ? kUnits : kStrided), a, stream, "launch k_checkpoint_load");
+}
+
+}  // extern "C"

@@ -15,7 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libsfopt.so")
 
 SF_OK, SF_ERR_INVALID, SF_ERR_CUDA, SF_ERR_OOM, SF_ERR_UNSUPPORTED, SF_ERR_TIMEOUT = 0, -1, -2, -3, -4, -5
-SF_BF16, SF_FP32, SF_E4M3 = 0, 1, 2
+SF_BF16, SF_FP32, SF_E4M3, SF_E8M0 = 0, 1, 2, 3
 SF_MAX_TENSORS_PER_LAUNCH = 48
 
 # Every symbol include/sfopt.h declares.
@@ -34,6 +34,8 @@ EXPORTS = [
     "sf_test_device_wait_runs_out",
     "sf_dropout", "sf_add_rmsnorm_forward", "sf_add_rmsnorm_workspace_bytes", "sf_add_rmsnorm_backward",
     "lce_vocab_workspace_bytes", "lce_vocab_forward_backward",
+    "sf_checkpoint_store", "sf_checkpoint_load", "sf_checkpoint_wgrad_workspace_bytes", "sf_checkpoint_wgrad",
+    "sf_sandwich_norm_forward", "sf_sandwich_norm_workspace_bytes", "sf_sandwich_norm_backward",
 ]
 
 
@@ -81,6 +83,16 @@ class sf_matrix(ctypes.Structure):
 
 class sf_rng(ctypes.Structure):
     _fields_ = [("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("device_offset", ctypes.c_void_p)]
+
+
+class sf_checkpoint(ctypes.Structure):
+    _fields_ = [("values", sf_matrix), ("scale", ctypes.c_void_p), ("scale_dtype", ctypes.c_int32),
+                ("group", ctypes.c_int32)]
+
+
+class sf_sandwich(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_double), ("residual_scale", ctypes.c_double), ("block_scale", ctypes.c_double),
+                ("gain_offset", ctypes.c_double), ("gate_span", ctypes.c_int64)]
 
 
 _P = ctypes.c_void_p
@@ -144,6 +156,14 @@ _SIGS = {
     "sf_add_rmsnorm_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
     "sf_add_rmsnorm_backward": (_ST, [_P, _P, _P, _INT, _P, _P, ctypes.c_double, _P, _P, _P, _P, _INT, _P,
                                       ctypes.c_size_t, _P]),
+    "sf_checkpoint_store": (_ST, [_P, _P, _P]),
+    "sf_checkpoint_load": (_ST, [_P, _P, _P, _INT, ctypes.c_double, _P, _P]),
+    "sf_checkpoint_wgrad_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "sf_checkpoint_wgrad": (_ST, [_P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "sf_sandwich_norm_forward": (_ST, [_P, _P, _P, _P, _P, _INT, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "sf_sandwich_norm_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "sf_sandwich_norm_backward": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _INT, _P, _P, _P, _P, _P, _P, _P, _INT, _P,
+                                        _P, ctypes.c_size_t, _P]),
 }
 
 _lib = None
@@ -159,7 +179,8 @@ def load(path=None):
         raise RuntimeError(f"{p} is missing: build it with `python -m layer_optimizer_gb300.build`")
     try:  # make sure a libcudart with the library's SONAME is in the process (torch ships one)
         import torch
-        _DTYPES.update({torch.bfloat16: SF_BF16, torch.float32: SF_FP32, torch.float8_e4m3fn: SF_E4M3})
+        _DTYPES.update({torch.bfloat16: SF_BF16, torch.float32: SF_FP32, torch.float8_e4m3fn: SF_E4M3,
+                        torch.float8_e8m0fnu: SF_E8M0, torch.uint8: SF_E8M0})
     except ImportError:
         pass
     lib = ctypes.CDLL(p)
@@ -534,6 +555,100 @@ def lce_vocab_forward_backward(H, W, labels, loss=None, token_loss=None, dH=None
         _ref(H), _ref(W), _vector(labels, H.rows, "labels", ("torch.int32",)), piece, ignore_index, float(grad_scale),
         _vector(loss, 1, "loss", _F32), _vector(token_loss, H.rows, "token_loss", _F32), _ref(dH), _ref(dW), ws,
         ws_bytes, _stream(stream)))
+
+
+# ------------------------------------------------------------------ (e) ----
+
+def checkpoint(values, scale, group=0):
+    """sf_checkpoint of an e4m3 matrix and its scales (dense [rows, groups]; e8m0, as such or as uint8 codes, or fp32
+    where they are read).  The structure keeps both tensors alive."""
+    m = _required(values, "values")
+    c = sf_checkpoint(m, None, SF_E8M0, group)
+    if scale is not None:
+        groups = -(-m.cols // group) if group > 0 else 1
+        c.scale, c.scale_dtype = _vector(scale, m.rows * groups, "scale"), _dtype(scale, "scale")
+    c.tensors = values, scale
+    return c
+
+
+def _full_or_8(t, name):
+    """A matrix or a checkpoint, as the two arguments that the library takes for it."""
+    if type(t) is sf_checkpoint:
+        return None, ctypes.byref(t)
+    return _ref(_matrix(t, name)), None
+
+
+def sf_checkpoint_store(x, out, stream=None):
+    """Writes x as the checkpoint `out`."""
+    x = _matrix(x, "x")
+    _check(load().sf_checkpoint_store(_ref(x), _ref(out), _stream(stream)))
+
+
+def sf_checkpoint_load(c, y, row_factor=None, gain=None, gain_offset=0.0, stream=None, gain_dtype=None):
+    """y = the checkpoint's values, times row_factor per row and gain_offset + gain per column where given."""
+    y = _required(y, "y")
+    _check(load().sf_checkpoint_load(_ref(c), _vector(row_factor, y.rows, "row_factor", _F32), _vector(gain, y.cols, "gain"),
+                                     _vector_dtype(gain, "gain", gain_dtype), float(gain_offset), _ref(y), _stream(stream)))
+
+
+def sf_checkpoint_wgrad_workspace_bytes(tokens, out, in_):
+    return load().sf_checkpoint_wgrad_workspace_bytes(tokens, out, in_)
+
+
+def sf_checkpoint_wgrad(dY, c, dW, base=None, ws=None, stream=None):
+    """dW = base + dY^T X from the checkpoint c of X (base: None or dW itself, to add to it, or another matrix)."""
+    dY, dW, base = _matrix(dY, "dY"), _matrix(dW, "dW"), _matrix(base, "base")
+    ws, ws_bytes = _workspace(ws)
+    _check(load().sf_checkpoint_wgrad(_ref(dY), _ref(c), _ref(base), _ref(dW), ws, ws_bytes, _stream(stream)))
+
+
+def sandwich(eps, residual_scale=1.0, block_scale=1.0, gain_offset=0.0, gate_span=0):
+    """sf_sandwich: the constants of the end of a residual block (gate_span: rows a gate row serves, 0: all)."""
+    return sf_sandwich(eps, residual_scale, block_scale, gain_offset, gate_span)
+
+
+def sf_sandwich_norm_forward(p, x, residual=None, gain_post=None, gain_pre=None, gate=None, sum=None, h=None, x8=None,
+                             sum8=None, rstd_post=None, rstd_pre=None, stream=None, gain_dtype=None):
+    """s = residual_scale r + block_scale gate norm(x), h = norm(s), with checkpoints of x and s; tensors or sf_matrix,
+    x8 and sum8 from checkpoint() (vectors: tensors or addresses, the gains' with gain_dtype)."""
+    x = _required(x, "x")
+    residual, gate, sum, h = _matrix(residual, "residual"), _matrix(gate, "gate"), _matrix(sum, "sum"), _matrix(h, "h")
+    _check(load().sf_sandwich_norm_forward(
+        _ref(p), _ref(x), _ref(residual), _vector(gain_post, x.cols, "gain_post"), _vector(gain_pre, x.cols, "gain_pre"),
+        _one_dtype(gain_post, gain_pre, "gain", gain_dtype), _ref(gate), _ref(sum), _ref(h), _ref(x8), _ref(sum8),
+        _vector(rstd_post, x.rows, "rstd_post", _F32), _vector(rstd_pre, x.rows, "rstd_pre", _F32), _stream(stream)))
+
+
+def _one_dtype(a, b, name, dtype):
+    """The type of two vectors that have one."""
+    if a is None or b is None:
+        return _vector_dtype(b if a is None else a, name, dtype)
+    ta, tb = _vector_dtype(a, name, dtype), _vector_dtype(b, name, dtype)
+    if ta != tb:
+        raise SfError(SF_ERR_INVALID, f"{name}_post and {name}_pre must have one type")
+    return ta
+
+
+def sf_sandwich_norm_workspace_bytes(rows, cols):
+    return load().sf_sandwich_norm_workspace_bytes(rows, cols)
+
+
+def sf_sandwich_norm_backward(p, dh=None, dsum=None, x=None, sum=None, gain_post=None, gain_pre=None, gate=None,
+                              rstd_post=None, rstd_pre=None, dresidual=None, dx=None, dgain_post=None, dgain_pre=None,
+                              dgate=None, ws=None, stream=None, gain_dtype=None, dgain_dtype=None):
+    """The gradients of sf_sandwich_norm_forward; x and sum as tensors, sf_matrix or checkpoint() (ws: a uint8 workspace
+    tensor, needed with a dgain or dgate)."""
+    dh, dsum, gate, dgate = _matrix(dh, "dh"), _matrix(dsum, "dsum"), _matrix(gate, "gate"), _matrix(dgate, "dgate")
+    dresidual, dx = _matrix(dresidual, "dresidual"), _matrix(dx, "dx")
+    of = dh if dh is not None else _required(dsum, "dsum (or dh)")
+    (x, x8), (sum, sum8) = _full_or_8(x, "x"), _full_or_8(sum, "sum")
+    ws, ws_bytes = _workspace(ws)
+    _check(load().sf_sandwich_norm_backward(
+        _ref(p), _ref(dh), _ref(dsum), x, x8, sum, sum8, _vector(gain_post, of.cols, "gain_post"),
+        _vector(gain_pre, of.cols, "gain_pre"), _one_dtype(gain_post, gain_pre, "gain", gain_dtype), _ref(gate),
+        _vector(rstd_post, of.rows, "rstd_post", _F32), _vector(rstd_pre, of.rows, "rstd_pre", _F32), _ref(dresidual),
+        _ref(dx), _vector(dgain_post, of.cols, "dgain_post"), _vector(dgain_pre, of.cols, "dgain_pre"),
+        _one_dtype(dgain_post, dgain_pre, "dgain", dgain_dtype), _ref(dgate), ws, ws_bytes, _stream(stream)))
 
 
 # ------------------------------------------------------------------ (c) ----

@@ -23,6 +23,9 @@ against its definition:
 * ``bf16``   -- round-to-nearest-even to bfloat16 and ulp distance, from the
   IEEE-754 binary format definition.
 
+* ``checkpoint``, ``sandwich`` -- 8-bit activation checkpoints with weight
+  gradients from them, and the norms around a residual block with its gate.
+
 Parity status: every function is pinned by ``tests/test_oracle_*.py``
 (closed forms, brute force, identities, printed tables under
 ``tests/golden/``).  No function is "parity unpinned".
