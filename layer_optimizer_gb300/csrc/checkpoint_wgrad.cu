@@ -1,8 +1,31 @@
 // The weight gradient of a linear layer from the 8-bit checkpoint of its
-// input: dW = base + dY^T X, X = value * scale.
+// input: dW = base + dY^T X, X = value * scale, on the tensor cores.
+//
+// The pair form of tc_gemm.cu (256 x 256 tiles of dW by clusters of two CTAs,
+// tcgen05.mma into tensor memory), with X turned into bf16 on the way: a CTA's
+// 64-token slab of the checkpoint (64 x 128 values, 8 KB by TMA) is read from
+// shared memory by four converter warps, multiplied by its scales and written
+// as the swizzled MN-major operand that the MMA reads (16 KB).  So the
+// activations are never restored in memory, at 1 byte an element instead of
+// the 5 of a restore and a bf16 product.  With power-of-two scales value *
+// scale is exact in bf16.
+//
+// Sums: the tensor cores cut the low bits of their fp32 accumulator at every
+// step, which shrinks a long sum (measured on 4096 tokens 4e-6 of it, on 16384
+// 2e-5).  So a span of 512 tokens is summed there, and the epilogue's threads
+// add the spans in their registers, rounded to nearest, while the MMAs of the
+// next span fill the other accumulator: eight warps hold a tile's 32768 sums a
+// CTA, 128 a thread, for which they take registers from the other warps.
+//
+// Tiles that do not fill a whole wave of pairs are split over the tokens, so
+// that all pairs work on them; their parts go through the workspace and a
+// second kernel adds them in order.
 #include <algorithm>
+#include <map>
+#include <mutex>
 
 #include "lanes.cuh"
+#include "tc_pair.cuh"
 
 namespace sf {
 namespace {
@@ -19,6 +42,491 @@ struct WgradArgs {
 
 __device__ __forceinline__ float dw_at(const void* p, int fp32, int64_t i) {
   return fp32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+constexpr int kSpan = 8;                       // slabs that one accumulator sums
+constexpr int kRing = 6;                       // slabs of dY and of the checkpoint in flight
+constexpr int kSlots = 3;                      // converted slabs
+constexpr int kA = kBM * kBK * 2;              // 16 KB: 128 columns of dY
+constexpr int kB8 = 128 * kBK;                 // 8 KB: 128 columns of the checkpoint
+constexpr int kB = kBRows * kBK * 2;           // 16 KB: the same in bf16
+constexpr int kEpiWarps = 8;
+constexpr int kConvWarps = 4, kConvGroups = 2; // converter warps of a slab; the groups take slabs in turn
+constexpr int kTcThreads = 32 * (4 + kConvWarps * kConvGroups + kEpiWarps);
+constexpr size_t kTcSmem = (size_t)kRing * (kA + kB8) + (size_t)kSlots * kB + kEpiWarps * 4096 + 1024 + 256;
+constexpr int64_t kMaxParts = 160;             // parts of split tiles, 256 KB of workspace each
+constexpr int64_t kPartFloats = 2 * kBM * kBN;
+
+struct TcArgs {
+  int32_t out, in, tokens;
+  int32_t n_fast;            // tile order: columns fastest
+  int32_t whole, parts;      // tiles before `whole` are one item each, later ones `parts`
+  int32_t items;
+  int32_t tma;               // dW by tensor stores
+  int32_t base_vec;          // base in 16-byte loads
+  void* dw;
+  const void* base;
+  int64_t lddw, ldbase;
+  float* ws;
+  Ck ck;
+};
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 16 consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// An item: a tile of dW and the slabs of tokens to sum.
+struct Item {
+  int mt, nt, k0, k1, part;      // part < 0: a whole tile, else its place in the workspace
+};
+__device__ __forceinline__ Item item_of(const TcArgs& g, int it, int m_tiles, int n_tiles, int nk) {
+  Item i;
+  int t = it;
+  i.k0 = 0, i.k1 = nk, i.part = -1;
+  if (it >= g.whole) {
+    const int j = it - g.whole, p = j % g.parts;
+    t = g.whole + j / g.parts;
+    i.k0 = (int)((int64_t)nk * p / g.parts);
+    i.k1 = (int)((int64_t)nk * (p + 1) / g.parts);
+    i.part = j;
+  }
+  i.mt = g.n_fast ? t / n_tiles : t % m_tiles;
+  i.nt = g.n_fast ? t % n_tiles : t / m_tiles;
+  return i;
+}
+
+// FP32: dW's type.
+template <bool FP32>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    k_wgrad_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+               const __grid_constant__ CUtensorMap map_c, const TcArgs g, const int a_form) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  // [dY: kRing x 16 KB] [converted: kSlots x 16 KB] [staging: 8 x 4 KB] [checkpoint: kRing x 8 KB] [barriers]
+  const uint32_t ring_a = smem_u32(smem), conv = ring_a + kRing * kA, staging = conv + kSlots * kB;
+  const uint32_t ring_b = staging + kEpiWarps * 4096;
+  uint64_t* ready = reinterpret_cast<uint64_t*>(smem + kRing * (kA + kB8) + kSlots * kB + kEpiWarps * 4096);   // first CTA: dY landed, X converted, in both
+  uint64_t* land = ready + kRing;          // the CTA's own values landed
+  uint64_t* empty = land + kRing;          // the slab's MMAs are done
+  uint64_t* tfull = empty + kRing;         // [2] accumulator b holds a span
+  uint64_t* tempty = tfull + 2;            // [2] both CTAs have read accumulator b (first CTA)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x / kPair, n_pairs = gridDim.x / kPair;
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&map_a);
+    prefetch_tensormap(&map_b);
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(&ready[s], 1 + kPair * kConvWarps);
+      mbar_init(&land[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], kPair * kEpiWarps);
+    }
+    fence_mbar_init_cluster();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 2 * kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();
+
+  const int nk = (g.tokens + kBK - 1) / kBK;
+  const int m_tiles = (g.out + kPair * kBM - 1) / (kPair * kBM), n_tiles = (g.in + kBN - 1) / kBN;
+  if (warp < 4) {
+    regs_down<24>();
+    if (warp == 0 && lane == 0) {
+      const uint32_t ready_lead = cluster_addr(smem_u32(ready), 0);
+      int i = 0;
+      bool failed = false;
+      for (int it = pair; it < g.items && !failed; it += n_pairs) {
+        const Item w = item_of(g, it, m_tiles, n_tiles, nk);
+        const int m0 = w.mt * (kPair * kBM) + (int)rank * kBM, nb = w.nt * kBN + (int)rank * kBRows;
+        for (int kb = w.k0; kb < w.k1; ++kb, ++i) {
+          const int s = i % kRing;
+          if (i >= kRing && !mbar_wait_cluster(&empty[s], (uint32_t)(i / kRing - 1) & 1u)) {
+            failed = true;
+            break;
+          }
+          mbar_arrive_expect_tx(&land[s], kB8);
+          tma_load_2d(smem + (ring_b - ring_a) + s * kB8, &map_b, &land[s], nb, kb * kBK);
+          if (rank == 0) mbar_arrive_expect_tx(&ready[s], kPair * kA);
+          const uint32_t st = ring_a + (uint32_t)s * kA, bar = ready_lead + 8u * (uint32_t)s;
+          if (a_form == 2) {
+            tma_load_3d_pair(st, &map_a, bar, 0, kb * kBK, m0 >> 6);
+          } else {
+            tma_load_2d_pair(st, &map_a, bar, m0, kb * kBK);
+            tma_load_2d_pair(st + kMnBox, &map_a, bar, m0 + 64, kb * kBK);
+          }
+        }
+      }
+      // the last copies have landed before the pair can exit (immediate unless a wait ran out)
+      for (int j = i > kRing ? i - kRing : 0; j < i; ++j) {
+        mbar_wait(&land[j % kRing], (uint32_t)(j / kRing) & 1u);
+        if (rank == 0) mbar_wait_cluster(&ready[j % kRing], (uint32_t)(j / kRing) & 1u);
+      }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      const uint32_t idesc = kIdesc | (1u << 15) | (1u << 16);      // both operands MN-major
+      const uint32_t empty_a = smem_u32(empty), tfull_a = smem_u32(tfull);
+      int i = 0, j = 0;
+      bool failed = false;
+      for (int it = pair; it < g.items && !failed; it += n_pairs) {
+        const Item w = item_of(g, it, m_tiles, n_tiles, nk);
+        for (int k0 = w.k0; k0 < w.k1 && !failed; k0 += kSpan, ++j) {
+          const int b = j & 1, use = j >> 1, k1 = min(k0 + kSpan, w.k1);
+          if (use > 0 && !mbar_wait_cluster(&tempty[b], (uint32_t)(use - 1) & 1u)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem + (uint32_t)(b * kTmemCols);
+          for (int kb = k0; kb < k1; ++kb, ++i) {
+            const int s = i % kRing;
+            if (!mbar_wait_cluster(&ready[s], (uint32_t)(i / kRing) & 1u)) {
+              failed = true;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t adesc = umma_desc_mn_sw128(ring_a + (uint32_t)s * kA), bdesc = umma_desc_mn_sw128(conv + (uint32_t)(i % kSlots) * kB);
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k) tc_mma(d_tmem, adesc + 128u * k, bdesc + 128u * k, idesc, kb != k0 || k != 0 ? 1u : 0u);
+            tc_commit_pair(empty_a + 8u * (uint32_t)s);
+          }
+          tc_commit_pair(tfull_a + 8u * (uint32_t)b);
+        }
+      }
+    }
+  } else if (warp < 4 + kConvWarps * kConvGroups) {
+    regs_down<56>();
+    // a thread's 16 columns of tokens r, r + 16, r + 32, r + 48 of a slab
+    const int group = (warp - 4) / kConvWarps, tid = threadIdx.x & 127, cc = tid & 7, r0 = tid >> 3;
+    const uint32_t ready_lead = cluster_addr(smem_u32(ready), 0);
+    // the slabs of this group, one ahead
+    int it = pair, kb = 0;
+    Item w{};
+    auto enter = [&]() {
+      if (it < g.items) w = item_of(g, it, m_tiles, n_tiles, nk);
+      kb = w.k0;
+    };
+    auto advance = [&]() {
+      if (it < g.items && ++kb == w.k1) {
+        it += n_pairs;
+        enter();
+      }
+    };
+    // A slab's scales, as loaded: turned into fp32 when their values have come, so that nothing waits for them here.
+    // Past the last token or column the last one's are taken: the values there are zero (or, where the scale is NaN,
+    // not the only ones of their column that are).
+    auto scales = [&](uint32_t (&f)[4]) {
+      const int c = min(w.nt * kBN + (int)rank * kBRows + 16 * cc, g.in - 1) >> (g.ck.group_log2 ? g.ck.group_log2 : 31);
+      int64_t at[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) at[q] = (int64_t)min(kb * kBK + r0 + 16 * q, g.tokens - 1) * g.ck.n_groups + c;
+      if (g.ck.s8) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) f[q] = __ldg(g.ck.s8 + at[q]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) f[q] = __float_as_uint(__ldg(g.ck.s32 + at[q]));
+      }
+    };
+    const int odd = cc >> 2;        // the other half's lanes write their two units the other way round: no bank conflict
+    const uint32_t src0 = ring_b + 16u * cc + 128u * r0;
+    const uint32_t unit0 = 16u * ((2 * (cc & 3) + odd) ^ (r0 & 7)), unit1 = 16u * ((2 * (cc & 3) + 1 - odd) ^ (r0 & 7));
+    const uint32_t dst0 = conv + (uint32_t)odd * kMnBox + 128u * r0;
+    enter();
+    if (group) advance();
+    uint32_t next[4] = {};
+    if (it < g.items) scales(next);
+    for (int i = group; it < g.items; i += kConvGroups) {
+      const int s = i % kRing;
+      uint32_t f[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f[q] = next[q];
+      advance();
+      advance();
+      if (it < g.items) scales(next);
+      // the values have landed, and the slab that the slot held has been multiplied
+      if (!mbar_wait(&land[s], (uint32_t)(i / kRing) & 1u) ||
+          (i >= kSlots && !mbar_wait_cluster(&empty[(i - kSlots) % kRing], (uint32_t)((i - kSlots) / kRing) & 1u)))
+        break;
+      const uint32_t src = src0 + (uint32_t)s * kB8, dst = dst0 + (uint32_t)(i % kSlots) * kB;
+      int4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = lds_i4(src + 2048u * q);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t in[4] = {(uint32_t)v[q].x, (uint32_t)v[q].y, (uint32_t)v[q].z, (uint32_t)v[q].w};
+        const float scale = g.ck.s8 ? e8m0_value(f[q]) : __uint_as_float(f[q]);
+        const uint64_t f2 = pack_f2(scale, scale);
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 x = e4m3x2_value(in[e >> 1] >> (16 * (e & 1)) & 0xffffu);
+          o[e] = bf16x2_rn(fmul2(pack_f2(x.x, x.y), f2));
+        }
+        // (16 rows on, the swizzle is the same)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 2048u * q + unit0), "r"(odd ? o[4] : o[0]),
+                     "r"(odd ? o[5] : o[1]), "r"(odd ? o[6] : o[2]), "r"(odd ? o[7] : o[3]));
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 2048u * q + unit1), "r"(odd ? o[0] : o[4]),
+                     "r"(odd ? o[1] : o[5]), "r"(odd ? o[2] : o[6]), "r"(odd ? o[3] : o[7]));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive_local(&ready[s]);
+        else mbar_arrive_remote_release(ready_lead + 8u * (uint32_t)s);
+      }
+    }
+  } else {
+    regs_up<168>();
+    const int ew = warp - 4 - kConvWarps * kConvGroups, quarter = warp & 3, half = ew / 4;
+    const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
+    const uint32_t buf = staging + (uint32_t)ew * 4096u;
+    const uint32_t tempty_lead = cluster_addr(smem_u32(tempty), 0);
+    int j = 0;
+    bool failed = false;
+    for (int it = pair; it < g.items && !failed; it += n_pairs) {
+      const Item w = item_of(g, it, m_tiles, n_tiles, nk);
+      float acc[128];
+#pragma unroll
+      for (int e = 0; e < 128; ++e) acc[e] = 0.0f;
+      for (int k0 = w.k0; k0 < w.k1; k0 += kSpan, ++j) {
+        const int b = j & 1;
+        if (!mbar_wait_cluster(&tfull[b], (uint32_t)(j >> 1) & 1u)) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t at = tmem + (uint32_t)(b * kTmemCols + 128 * half) + lane_off;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint32_t r[16];
+          __syncwarp();
+          tmem_ld16(at + 16u * q, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[16 * q + e] += __uint_as_float(r[e]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive_local(&tempty[b]);
+          else mbar_arrive_remote_release(tempty_lead + 8u * (uint32_t)b);
+        }
+      }
+      if (failed) break;
+      const int row_in = (int)rank * kBM + 32 * quarter + lane;      // within the tile
+      const int row0 = w.mt * (kPair * kBM) + (int)rank * kBM + 32 * quarter, row = row0 + lane;
+      const int col0 = w.nt * kBN + 128 * half;
+      if (w.part >= 0) {      // [part][column / 4][row][4]: a warp's rows side by side
+        float4* p = reinterpret_cast<float4*>(g.ws) + ((int64_t)w.part * (kBN / 4) + 32 * half) * (kPair * kBM) + row_in;
+#pragma unroll
+        for (int q = 0; q < 32; ++q)
+          p[(int64_t)q * (kPair * kBM)] = make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+        continue;
+      }
+      constexpr int kUnit = FP32 ? 4 : 8;                            // elements of 16 bytes
+      constexpr int kBox = FP32 ? 32 : 64;                           // columns of a staging box
+      const int whole = g.in % kUnit ? g.in / kBox * kBox : INT32_MAX;      // a row's ragged end goes element by element
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c0 = col0 + 32 * q;
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = acc[32 * q + e];
+        if (g.base && row < g.out && c0 < g.in) {
+          const int n = min(32, g.in - c0);
+          if (FP32) {
+            const float* p = static_cast<const float*>(g.base) + (int64_t)row * g.ldbase + c0;
+            if (g.base_vec && n == 32) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 u = *reinterpret_cast<const float4*>(p + 4 * e);
+                v[4 * e] += u.x, v[4 * e + 1] += u.y, v[4 * e + 2] += u.z, v[4 * e + 3] += u.w;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e < n) v[e] += p[e];
+            }
+          } else {
+            const uint16_t* p = static_cast<const uint16_t*>(g.base) + (int64_t)row * g.ldbase + c0;
+            if (g.base_vec && n == 32) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint4 u = *reinterpret_cast<const uint4*>(p + 8 * e);
+                const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int f = 0; f < 4; ++f) v[8 * e + 2 * f] += __uint_as_float(x[f] << 16), v[8 * e + 2 * f + 1] += __uint_as_float(x[f] & 0xffff0000u);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e < n) v[e] += __uint_as_float((uint32_t)p[e] << 16);
+            }
+          }
+        }
+        if (!g.tma || c0 >= whole) {
+          if (row < g.out) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (c0 + e >= g.in) continue;
+              if (FP32) static_cast<float*>(g.dw)[(int64_t)row * g.lddw + c0 + e] = v[e];
+              else static_cast<__nv_bfloat16*>(g.dw)[(int64_t)row * g.lddw + c0 + e] = __float2bfloat16_rn(v[e]);
+            }
+          }
+          continue;
+        }
+        if (FP32 || q % 2 == 0) {      // the box's last store has been read out of it
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+        }
+        if (FP32) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            sts_f4(buf + (uint32_t)lane * 128u + (uint32_t)((e ^ (lane & 7)) * 16), v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        } else {
+          stage_bf16(buf, lane, q % 2, v);
+        }
+        if (FP32 || q % 2 == 1) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          const int x = FP32 ? c0 : c0 - 32;
+          if (lane == 0) {
+            if (row0 < g.out && x < g.in) tma_store_2d(&map_c, buf, x, row0);
+            bulk_commit();
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * kTmemCols);
+  }
+}
+
+// Adds the parts of the split tiles, in order: a block 32 rows x 32 columns of
+// a tile, turned in shared memory.
+__global__ void __launch_bounds__(256) k_wgrad_join(const TcArgs g, const int m_tiles, const int n_tiles, const int fp32) {
+  __shared__ float4 turn[8][33];
+  const int tile = g.whole + blockIdx.x / 64, sub = blockIdx.x % 64;
+  const int mt = g.n_fast ? tile / n_tiles : tile % m_tiles, nt = g.n_fast ? tile % n_tiles : tile / m_tiles;
+  const int r0 = sub / 8 * 32, q0 = sub % 8 * 8;      // rows, and columns / 4, within the tile
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  griddep_wait();
+  if (mt * 256 + r0 >= g.out || nt * kBN + 4 * q0 >= g.in) return;
+  const float4* p = reinterpret_cast<const float4*>(g.ws) + ((int64_t)(tile - g.whole) * g.parts * (kBN / 4) + q0 + w) * (kPair * kBM) + r0 + lane;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int i = 0; i < g.parts; ++i, p += kBN / 4 * kPair * kBM) {
+    const float4 u = *p;
+    v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+  }
+  turn[w][lane] = v;
+  __syncthreads();
+  const int r = threadIdx.x >> 3, q = threadIdx.x & 7;
+  const int64_t row = (int64_t)mt * 256 + r0 + r;
+  const int col = nt * kBN + 4 * (q0 + q);
+  if (row >= g.out) return;
+  v = turn[q][r];
+  const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (col + e >= g.in) continue;
+    float y = x[e];
+    if (g.base) y += dw_at(g.base, fp32, row * g.ldbase + col + e);
+    if (fp32) static_cast<float*>(g.dw)[row * g.lddw + col + e] = y;
+    else static_cast<__nv_bfloat16*>(g.dw)[row * g.lddw + col + e] = __float2bfloat16_rn(y);
+  }
+}
+
+// Map of the checkpoint's values: boxes of 128 columns x 64 tokens.
+sf_status make_map_values(CUtensorMap* map, const Ck& ck, int64_t in, int64_t tokens) {
+  cuuint64_t dims[2] = {(cuuint64_t)in, (cuuint64_t)tokens};
+  cuuint64_t strides[1] = {(cuuint64_t)ck.ld};
+  cuuint32_t box[2] = {128, (cuuint32_t)kBK};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, ck.q, dims, strides, box, estr,
+                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SF_ERR_CUDA, "cuTensorMapEncodeTiled (checkpoint) failed (%d)", (int)r);
+  return SF_OK;
+}
+
+// Clusters of two CTAs that fit on the device at once (cached per device).
+sf_status resident_pairs(int* out) {
+  static std::mutex mu;
+  static std::map<int, int> cache;
+  int dev = 0;
+  SF_CUDA_TRY(cudaGetDevice(&dev), "cudaGetDevice");
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = cache.find(dev);
+  if (it == cache.end()) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {kPair, 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.gridDim = dim3((unsigned)(kPair * std::max(1, sm_count() / kPair)));
+    cfg.dynamicSmemBytes = kTcSmem;
+    int n = 0;
+    SF_TRY(allow_dynamic_smem(reinterpret_cast<const void*>(&k_wgrad_tc<false>), kTcSmem));
+    SF_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_wgrad_tc<false>, &cfg), "cudaOccupancyMaxActiveClusters (k_wgrad_tc)");
+    if (n < 1) return fail(SF_ERR_UNSUPPORTED, "no cluster of two CTAs fits on this device");
+    it = cache.emplace(dev, n).first;
+  }
+  *out = it->second;
+  return SF_OK;
+}
+
+// Tiles that are one item each, and the parts of the others: whole waves of
+// tiles, and the rest split so that its rounds of parts take least time (a
+// part is at least a span of tokens; a pair's part costs about two slabs more
+// for the workspace).
+void plan(int64_t tiles, int nk, int pairs, TcArgs* g) {
+  const int64_t left = tiles % pairs;
+  g->whole = (int32_t)tiles;
+  g->parts = 1;
+  double best = nk;
+  for (int s = 2; left && s <= nk / kSpan && s * left <= kMaxParts; ++s) {
+    const double cost = (double)ceil_div<int64_t>(left * s, pairs) * ((double)nk / s + 2.0);
+    if (cost < 0.9 * best) {
+      best = cost;
+      g->parts = s;
+      g->whole = (int32_t)(tiles - left);
+    }
+  }
+  g->items = (int32_t)(g->whole + (tiles - g->whole) * g->parts);
 }
 
 // 64 x 64 tiles on the CUDA cores, 4 x 4 a thread, for operands that tensor
@@ -59,14 +567,72 @@ __global__ void __launch_bounds__(256) k_wgrad_plain(const WgradArgs a) {
     }
 }
 
+sf_status launch_tc(const WgradArgs& a, void* ws, cudaStream_t st) {
+  TcArgs g{};
+  g.out = (int32_t)a.out;
+  g.in = (int32_t)a.in;
+  g.tokens = (int32_t)a.tokens;
+  g.n_fast = a.out > a.in;
+  g.dw = a.dw;
+  g.base = a.base;
+  g.lddw = a.lddw;
+  g.ldbase = a.ldbase;
+  g.ws = static_cast<float*>(ws);
+  g.ck = a.ck;
+  const size_t size = a.fp32 ? 4 : 2;
+  g.base_vec = a.base && reinterpret_cast<uintptr_t>(a.base) % 16 == 0 && a.ldbase * size % 16 == 0;
+  g.tma = reinterpret_cast<uintptr_t>(a.dw) % 16 == 0 && a.lddw * size % 16 == 0 && on_current_device(a.dw);
+  const int64_t m_tiles = ceil_div<int64_t>(a.out, kPair * kBM), n_tiles = ceil_div<int64_t>(a.in, kBN);
+  if (m_tiles * n_tiles > INT32_MAX / 2) return fail(SF_ERR_UNSUPPORTED, "too many tiles");
+  int pairs = 0;
+  SF_TRY(resident_pairs(&pairs));
+  plan(m_tiles * n_tiles, (int)ceil_div<int64_t>(a.tokens, kBK), pairs, &g);
+  CUtensorMap ma, mb;
+  int a_form = make_map_mn3d(&ma, a.dy, a.out, a.tokens, a.ldy) ? 2 : 1;
+  if (a_form == 1) SF_TRY(make_map(&ma, a.dy, a.out, a.tokens, a.ldy, kBK));
+  SF_TRY(make_map_values(&mb, a.ck, a.in, a.tokens));
+  CUtensorMap mc = ma;       // unused unless dW is written by tensor stores
+  if (g.tma) SF_TRY(a.fp32 ? make_map_c(&mc, static_cast<float*>(a.dw), a.out, a.in, a.lddw) : make_map_c16(&mc, a.dw, a.out, a.in, a.lddw));
+  const void* kernel = a.fp32 ? (const void*)&k_wgrad_tc<true> : (const void*)&k_wgrad_tc<false>;
+  SF_TRY(allow_dynamic_smem(kernel, kTcSmem));
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {kPair, 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)(kPair * std::min<int64_t>(g.items, pairs)));
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = kTcSmem;
+  cfg.stream = st;
+  void* args[] = {&ma, &mb, &mc, &g, &a_form};
+  SF_CUDA_TRY(cudaLaunchKernelExC(&cfg, kernel, args), "launch k_wgrad_tc");
+  if (g.parts > 1)
+    SF_CUDA_TRY(launch_pdl(k_wgrad_join, dim3((unsigned)((m_tiles * n_tiles - g.whole) * 64)), dim3(256), 0, st, g, (int)m_tiles, (int)n_tiles, (int)a.fp32),
+                "launch k_wgrad_join");
+  return SF_OK;
+}
+
 }  // namespace
+
+int read_and_clear_device_error_wgrad() {
+  int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof v) != cudaSuccess) return 0;
+  if (v) cudaMemcpyToSymbol(g_device_error, &z, sizeof z);
+  return v;
+}
+
 }  // namespace sf
 
 extern "C" {
 
 size_t sf_checkpoint_wgrad_workspace_bytes(int64_t tokens, int64_t out, int64_t in) {
-  (void)tokens, (void)out, (void)in;
-  return 0;
+  using namespace sf;
+  if (tokens < 0 || out < 1 || in < 1) return 0;
+  const int64_t tiles = ceil_div<int64_t>(out, 2 * kBM) * ceil_div<int64_t>(in, kBN);
+  const int64_t parts = ceil_div<int64_t>(tokens, kBK) / kSpan;      // of a tile, at most
+  if (parts < 2) return 0;      // never split
+  return (size_t)(tiles < kMaxParts && parts < kMaxParts ? std::min(kMaxParts, tiles * parts) : kMaxParts) * kPartFloats * sizeof(float);
 }
 
 sf_status sf_checkpoint_wgrad(const sf_matrix* dY, const sf_checkpoint* c, const sf_matrix* base, const sf_matrix* dW,
@@ -95,6 +661,10 @@ sf_status sf_checkpoint_wgrad(const sf_matrix* dY, const sf_checkpoint* c, const
   a.in = in;
   a.fp32 = dW->dtype == SF_FP32;
   a.ck = device_ck(c);
+  if (tokens && dY->ld % 8 == 0 && c->values.ld % 16 == 0 && reinterpret_cast<uintptr_t>(dY->data) % 16 == 0 &&
+      reinterpret_cast<uintptr_t>(c->values.data) % 16 == 0 && tensor_map_encoder() && on_current_device(dY->data) &&
+      on_current_device(c->values.data))
+    return launch_tc(a, ws, as_stream(stream));
   const int64_t gx = ceil_div<int64_t>(in, kT), gy = ceil_div<int64_t>(out, kT);
   if (gy > 65535) return fail(SF_ERR_UNSUPPORTED, "out is too large");
   k_wgrad_plain<<<dim3((unsigned)gx, (unsigned)gy), 256, 0, as_stream(stream)>>>(a);

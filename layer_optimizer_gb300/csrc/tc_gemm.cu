@@ -46,14 +46,11 @@
 #include <map>
 #include <mutex>
 
-#include "common.h"
-#include "ptx.cuh"
+#include "tc_pair.cuh"
 
 namespace sf {
 namespace {
 
-constexpr int kPair = 2;                       // CTAs per tile (cta_group::2)
-constexpr int kBM = 128, kBN = 256, kBK = 64;
 // Ring stages, epilogue warps, and staging boxes per warp.  The epilogues that
 // write bf16 bound the tile after few K slabs (dW over few tokens, logits of
 // short rows), so eight warps share the tile's columns there (cross-entropy of
@@ -67,190 +64,11 @@ struct TcStages {
   static constexpr int kBoxes = 8 / kWarps;
   static constexpr int kThreads = 64 + 32 * kWarps;
 };
-constexpr int kBRows = kBN / kPair;            // rows of B held by one CTA
 constexpr int kStageA = kBM * kBK * 2;         // 16 KB
 constexpr int kStageB = kBRows * kBK * 2;      // 16 KB
 constexpr int kStageBytes = kStageA + kStageB;
-constexpr int kMnBox = 64 * kBK * 2;           // an MN-major box: 64 MN x 64 K bf16 = 8 KB
-constexpr int kTmemCols = 256;                 // one accumulator; two are allocated
 // the ring and the epilogue's boxes of 4 KB (32 rows x 128 bytes)
 constexpr size_t kGemmSmem = (size_t)TcStages<kTcF32>::kRing * kStageBytes + 8 * 4096 + 1024 + 256;
-
-// Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator
-// (bits 4-5 = 1), A and B bf16 (bits 7-9 and 10-12 = 1), A and B K-major
-// (bits 15, 16 = 0; set per launch for an MN-major operand), N >> 3 in
-// bits 17-22, M >> 4 in bits 24-28 (M = 256: the pair's rows).
-constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kBN >> 3) << 17) |
-                            ((uint32_t)((kPair * kBM) >> 4) << 24);
-
-// Shared-memory matrix descriptor of a K-major operand tile written by TMA
-// with 128-byte swizzling: rows of 128 bytes (64 bf16 of K), 8-row atoms of
-// 1024 bytes (stride-dimension offset), descriptor version 1, layout type 2.
-__device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t smem_addr) {
-  uint64_t d = (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)1 << 16;                 // leading-dimension offset (unused when swizzled)
-  d |= (uint64_t)(1024 >> 4) << 32;       // stride-dimension offset: 1024 bytes
-  d |= (uint64_t)1 << 46;                 // descriptor version
-  d |= (uint64_t)2 << 61;                 // 128-byte swizzle
-  return d;
-}
-
-// The same for an MN-major operand tile: TMA boxes of 64 MN-contiguous
-// elements (128 bytes) by 64 K rows, 128-byte swizzled, two of them side by
-// side for 128 rows of MN.  The canonical MN-major layout takes the offset
-// between 64-element MN blocks as the leading-dimension offset (one box,
-// 8192 bytes) and between 8-row K groups as the stride-dimension offset
-// (1024 bytes); a K-16 step advances the start by 16 rows = 2048 bytes.
-__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_addr) {
-  uint64_t d = (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(kMnBox >> 4) << 16;     // leading-dimension offset: next 64 MN elements
-  d |= (uint64_t)(1024 >> 4) << 32;       // stride-dimension offset: next 8 K rows
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
-// TMEM allocation of the CTA pair: one warp of each CTA issues these
-// together (the pair form requires both).
-__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// D[tmem] (+)= A B^T for one K-16 step over the pair (M 256: A rows from
-// both CTAs' shared memory at the descriptor's offset, B likewise, D rows
-// 0-127 into this CTA's TMEM and 128-255 into the peer's); accumulate = 0
-// overwrites D.
-__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Arrive on the barrier at shared offset `mbar` in both CTAs of the pair
-// once every tcgen05.mma issued so far by this thread is done.
-__device__ __forceinline__ void tc_commit_pair(uint32_t mbar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          mbar),
-      "h"((uint16_t)3)
-      : "memory");
-}
-
-// 2D tiled TMA load into this CTA's shared memory whose completion is
-// counted on the barrier at shared::cluster address `bar` (the pair form
-// lets it be the first CTA's barrier).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
-                                                 int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(y)
-      : "memory");
-}
-
-// The same with a 3D box (an MN-major operand: 64 MN x 64 K x two
-// 64-element MN blocks, stored block after block).
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
-                                                 int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t local, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
-  return r;
-}
-
-// Arrival on a barrier of another CTA of the cluster, ordering this
-// thread's earlier accesses (TMEM reads included, after
-// tcgen05.fence::before_thread_sync) at cluster scope.
-__device__ __forceinline__ void mbar_arrive_remote_release(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-
-// Bounded wait with cluster-scope acquire (arrivals from the peer CTA).
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
-  auto test = [&]() {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-  };
-  if (test()) return true;
-  const long long t0 = clock64();
-  for (;;) {
-    if (test()) return true;
-    if (clock64() - t0 > kWaitLimitCycles) {
-      atomicOr(&g_device_error, kDevErrTimeout);
-      return false;
-    }
-  }
-}
-
-// 32 consecutive fp32 columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld_wait();
-// 64 columns, waited for once.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
-  uint32_t (&lo)[32] = reinterpret_cast<uint32_t (&)[32]>(r[0]);
-  uint32_t (&hi)[32] = reinterpret_cast<uint32_t (&)[32]>(r[32]);
-  tmem_ld32(taddr, lo);
-  tmem_ld32(taddr + 32u, hi);
-  tmem_ld_wait();
-}
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-// Tensor store / reduce-add of a shared-memory box into global memory
-// (bulk async group of this thread), and the group waits.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
-               "r"(src), "r"(x), "r"(y)
-               : "memory");
-}
-__device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
-  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                   map),
-               "r"(src), "r"(x), "r"(y)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void bulk_wait_read_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void sts_f4(uint32_t a, float x, float y, float z, float w) {
-  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
-}
 
 struct TcGemmArgs {
   float* C;
@@ -293,25 +111,6 @@ __device__ __forceinline__ void fold_row_stats(const float (&x)[32], int valid, 
     if (j < valid) acc += expf(x[j] - mn);
   m = mn;
   s = acc;
-}
-
-// Writes 32 values of this lane's row, rounded to bf16, into half `half`
-// (0: columns 0-31, 1: 32-63) of a warp's 32-row x 64-column staging box,
-// 128-byte swizzled.
-__device__ __forceinline__ void stage_bf16(uint32_t buf, int lane, int half, const float (&v)[32]) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * q + 2 * i], v[8 * q + 2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + (uint32_t)lane * 128u +
-                                                                  (uint32_t)(((4 * half + q) ^ (lane & 7)) * 16)),
-                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                 : "memory");
-  }
 }
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
@@ -809,20 +608,7 @@ __global__ void __launch_bounds__(TcStages<EPI>::kThreads, 1)
   }
 }
 
-// Map of C's tensor stores: fp32, boxes of 32 rows x 32 columns.
-sf_status make_map_c(CUtensorMap* map, float* C, int64_t M, int64_t N, int64_t ldc) {
-  cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
-  cuuint64_t strides[1] = {(cuuint64_t)(ldc * 4)};
-  cuuint32_t box[2] = {32, 32};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, C, dims, strides, box, estr,
-                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(SF_ERR_CUDA, "cuTensorMapEncodeTiled (C) failed (%d)", (int)r);
-  return SF_OK;
-}
-
-// The same for partial products [splits][M][N] (3D, boxes 32 x 32 x 1) ...
+// Map of the tensor stores of partial products [splits][M][N]: fp32, 3D boxes of 32 x 32 x 1.
 sf_status make_map_split(CUtensorMap* map, float* C, int64_t M, int64_t N, int64_t ldc, int64_t splits) {
   cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)splits};
   cuuint64_t strides[2] = {(cuuint64_t)(ldc * 4), (cuuint64_t)(M * ldc * 4)};
@@ -833,51 +619,6 @@ sf_status make_map_split(CUtensorMap* map, float* C, int64_t M, int64_t N, int64
                                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SF_ERR_CUDA, "cuTensorMapEncodeTiled (partial C) failed (%d)", (int)r);
   return SF_OK;
-}
-
-// ... and for a bf16 C (boxes 32 rows x 64 columns).
-sf_status make_map_c16(CUtensorMap* map, void* C, int64_t M, int64_t N, int64_t ldc) {
-  cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
-  cuuint64_t strides[1] = {(cuuint64_t)(ldc * 2)};
-  cuuint32_t box[2] = {64, 32};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, C, dims, strides, box, estr,
-                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(SF_ERR_CUDA, "cuTensorMapEncodeTiled (bf16 C) failed (%d)", (int)r);
-  return SF_OK;
-}
-
-// bf16 operand map: a row-major [outer][ld] matrix read as boxes of 64
-// inner elements (128 bytes, swizzled) by box_outer rows.  K-major operands
-// have K inner (box_outer = their rows in a CTA), MN-major ones MN inner
-// (box_outer = 64 K rows).
-sf_status make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t ld, int box_outer) {
-  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
-  cuuint64_t strides[1] = {(cuuint64_t)(ld * 2)};
-  cuuint32_t box[2] = {64u, (cuuint32_t)box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
-                                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(SF_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
-  return SF_OK;
-}
-
-// An MN-major operand [K][ld] (MN inner, a multiple of 64) viewed in 3D as
-// {64 MN, K, MN / 64 blocks} with the blocks 128 bytes apart, so one box
-// {64, 64, 2} brings the 128 MN rows a CTA needs for a K slab (two 64 x 64
-// swizzled blocks, one after the other) in one copy.  Every address of the
-// view lies inside the matrix; false if the driver does not take the map.
-bool make_map_mn3d(CUtensorMap* map, const void* base, int64_t mn, int64_t K, int64_t ld) {
-  if (mn % 64) return false;
-  cuuint64_t dims[3] = {64u, (cuuint64_t)K, (cuuint64_t)(mn / 64)};
-  cuuint64_t strides[2] = {(cuuint64_t)(ld * 2), 128u};
-  cuuint32_t box[3] = {64u, (cuuint32_t)kBK, 2u};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-                              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Clusters of two GEMM CTAs that fit on the device at once (cached per

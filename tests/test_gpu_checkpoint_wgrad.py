@@ -46,7 +46,8 @@ def _run(tokens, out, cin, group, dt, acc, pad=0, lead=0, seed=0, in_place=False
 
 
 TOKENS_OUT_IN = [(1, 8, 16), (1, 1000, 4096), (7, 24, 48), (63, 128, 128), (64, 256, 256), (65, 264, 272), (200, 1000, 1008), (511, 256, 512),
-                 (512, 264, 256), (513, 512, 128), (1003, 1000, 1024), (2048, 256, 256), (2100, 40, 5008), (1500, 2000, 640)]
+                 (512, 264, 256), (513, 512, 128), (1003, 1000, 1024), (2048, 256, 256), (2100, 40, 5008), (1500, 2000, 640),
+                 (1030, 2600, 2048)]      # 88 tiles: a whole wave of pairs and 12 that are split
 
 
 @pytest.mark.parametrize("tokens,out,cin", TOKENS_OUT_IN)
