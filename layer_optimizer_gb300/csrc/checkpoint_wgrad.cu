@@ -45,15 +45,17 @@ __device__ __forceinline__ float dw_at(const void* p, int fp32, int64_t i) {
 }
 
 constexpr int kSpan = 8;                       // slabs that one accumulator sums
-constexpr int kRing = 6;                       // slabs of dY and of the checkpoint in flight
-constexpr int kSlots = 3;                      // converted slabs
+constexpr int kRing = 6;                       // slabs of dY in flight
+constexpr int kRing8 = 4;                      // slabs of the checkpoint
+constexpr int kSlots = 5;                      // converted slabs
 constexpr int kA = kBM * kBK * 2;              // 16 KB: 128 columns of dY
 constexpr int kB8 = 128 * kBK;                 // 8 KB: 128 columns of the checkpoint
 constexpr int kB = kBRows * kBK * 2;           // 16 KB: the same in bf16
 constexpr int kEpiWarps = 8;
 constexpr int kConvWarps = 4, kConvGroups = 2; // converter warps of a slab; the groups take slabs in turn
 constexpr int kTcThreads = 32 * (4 + kConvWarps * kConvGroups + kEpiWarps);
-constexpr size_t kTcSmem = (size_t)kRing * (kA + kB8) + (size_t)kSlots * kB + kEpiWarps * 4096 + 1024 + 256;
+constexpr int kStaging = 2048;                 // an epilogue warp's box: 32 rows of 64 bytes
+constexpr size_t kTcSmem = (size_t)kRing * kA + (size_t)kRing8 * kB8 + (size_t)kSlots * kB + kEpiWarps * kStaging + 1024 + 256;
 constexpr int64_t kMaxParts = 160;             // parts of split tiles, 256 KB of workspace each
 constexpr int64_t kPartFloats = 2 * kBM * kBN;
 
@@ -116,13 +118,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                const __grid_constant__ CUtensorMap map_c, const TcArgs g, const int a_form) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  // [dY: kRing x 16 KB] [converted: kSlots x 16 KB] [staging: 8 x 4 KB] [checkpoint: kRing x 8 KB] [barriers]
-  const uint32_t ring_a = smem_u32(smem), conv = ring_a + kRing * kA, staging = conv + kSlots * kB;
-  const uint32_t ring_b = staging + kEpiWarps * 4096;
-  uint64_t* ready = reinterpret_cast<uint64_t*>(smem + kRing * (kA + kB8) + kSlots * kB + kEpiWarps * 4096);   // first CTA: dY landed, X converted, in both
-  uint64_t* land = ready + kRing;          // the CTA's own values landed
-  uint64_t* empty = land + kRing;          // the slab's MMAs are done
-  uint64_t* tfull = empty + kRing;         // [2] accumulator b holds a span
+  // [dY: kRing x 16 KB] [converted: kSlots x 16 KB] [checkpoint: kRing8 x 8 KB] [staging: 8 x 2 KB] [barriers]
+  const uint32_t ring_a = smem_u32(smem), conv = ring_a + kRing * kA, ring_b = conv + kSlots * kB;
+  const uint32_t staging = ring_b + kRing8 * kB8;
+  uint64_t* ready = reinterpret_cast<uint64_t*>(smem + kRing * kA + kSlots * kB + kRing8 * kB8 + kEpiWarps * kStaging);   // first CTA: dY landed, X converted, in both
+  uint64_t* empty = ready + kRing;         // the slab's MMAs are done
+  uint64_t* land = empty + kRing;          // the CTA's own values landed
+  uint64_t* taken = land + kRing8;         // its converters have read them
+  uint64_t* tfull = taken + kRing8;        // [2] accumulator b holds a span
   uint64_t* tempty = tfull + 2;            // [2] both CTAs have read accumulator b (first CTA)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
 
@@ -134,8 +137,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     prefetch_tensormap(&map_b);
     for (int s = 0; s < kRing; ++s) {
       mbar_init(&ready[s], 1 + kPair * kConvWarps);
-      mbar_init(&land[s], 1);
       mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kRing8; ++s) {
+      mbar_init(&land[s], 1);
+      mbar_init(&taken[s], kConvWarps);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
@@ -159,19 +165,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     regs_down<24>();
     if (warp == 0 && lane == 0) {
       const uint32_t ready_lead = cluster_addr(smem_u32(ready), 0);
-      int i = 0;
+      int i = 0, landing = 0;
       bool failed = false;
       for (int it = pair; it < g.items && !failed; it += n_pairs) {
         const Item w = item_of(g, it, m_tiles, n_tiles, nk);
         const int m0 = w.mt * (kPair * kBM) + (int)rank * kBM, nb = w.nt * kBN + (int)rank * kBRows;
         for (int kb = w.k0; kb < w.k1; ++kb, ++i) {
-          const int s = i % kRing;
+          const int s = i % kRing, s8 = i % kRing8;
+          if (i >= kRing8 && !mbar_wait(&taken[s8], (uint32_t)(i / kRing8 - 1) & 1u)) {
+            failed = true;
+            break;
+          }
+          mbar_arrive_expect_tx(&land[s8], kB8);
+          tma_load_2d(smem + (ring_b - ring_a) + s8 * kB8, &map_b, &land[s8], nb, kb * kBK);
+          landing = i + 1;
           if (i >= kRing && !mbar_wait_cluster(&empty[s], (uint32_t)(i / kRing - 1) & 1u)) {
             failed = true;
             break;
           }
-          mbar_arrive_expect_tx(&land[s], kB8);
-          tma_load_2d(smem + (ring_b - ring_a) + s * kB8, &map_b, &land[s], nb, kb * kBK);
           if (rank == 0) mbar_arrive_expect_tx(&ready[s], kPair * kA);
           const uint32_t st = ring_a + (uint32_t)s * kA, bar = ready_lead + 8u * (uint32_t)s;
           if (a_form == 2) {
@@ -183,10 +194,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       // the last copies have landed before the pair can exit (immediate unless a wait ran out)
-      for (int j = i > kRing ? i - kRing : 0; j < i; ++j) {
-        mbar_wait(&land[j % kRing], (uint32_t)(j / kRing) & 1u);
-        if (rank == 0) mbar_wait_cluster(&ready[j % kRing], (uint32_t)(j / kRing) & 1u);
-      }
+      for (int j = landing > kRing8 ? landing - kRing8 : 0; j < landing; ++j) mbar_wait(&land[j % kRing8], (uint32_t)(j / kRing8) & 1u);
+      if (rank == 0)
+        for (int j = i > kRing ? i - kRing : 0; j < i; ++j) mbar_wait_cluster(&ready[j % kRing], (uint32_t)(j / kRing) & 1u);
     } else if (warp == 1 && lane == 0 && rank == 0) {
       const uint32_t idesc = kIdesc | (1u << 15) | (1u << 16);      // both operands MN-major
       const uint32_t empty_a = smem_u32(empty), tfull_a = smem_u32(tfull);
@@ -261,21 +271,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint32_t next[4] = {};
     if (it < g.items) scales(next);
     for (int i = group; it < g.items; i += kConvGroups) {
-      const int s = i % kRing;
+      const int s = i % kRing, s8 = i % kRing8;
       uint32_t f[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) f[q] = next[q];
       advance();
       advance();
       if (it < g.items) scales(next);
-      // the values have landed, and the slab that the slot held has been multiplied
-      if (!mbar_wait(&land[s], (uint32_t)(i / kRing) & 1u) ||
-          (i >= kSlots && !mbar_wait_cluster(&empty[(i - kSlots) % kRing], (uint32_t)((i - kSlots) / kRing) & 1u)))
-        break;
-      const uint32_t src = src0 + (uint32_t)s * kB8, dst = dst0 + (uint32_t)(i % kSlots) * kB;
+      if (!mbar_wait(&land[s8], (uint32_t)(i / kRing8) & 1u)) break;
+      const uint32_t src = src0 + (uint32_t)s8 * kB8, dst = dst0 + (uint32_t)(i % kSlots) * kB;
       int4 v[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = lds_i4(src + 2048u * q);
+      // the slab that the slot held has been multiplied
+      if (i >= kSlots && !mbar_wait_cluster(&empty[(i - kSlots) % kRing], (uint32_t)((i - kSlots) / kRing) & 1u)) break;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t in[4] = {(uint32_t)v[q].x, (uint32_t)v[q].y, (uint32_t)v[q].z, (uint32_t)v[q].w};
@@ -296,6 +305,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
+        // (not before: a copy into the values' place must find every load of them done, and that they are is certain
+        // only once they have been used)
+        mbar_arrive_local(&taken[s8]);
         if (rank == 0) mbar_arrive_local(&ready[s]);
         else mbar_arrive_remote_release(ready_lead + 8u * (uint32_t)s);
       }
@@ -304,7 +316,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     regs_up<168>();
     const int ew = warp - 4 - kConvWarps * kConvGroups, quarter = warp & 3, half = ew / 4;
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
-    const uint32_t buf = staging + (uint32_t)ew * 4096u;
+    const uint32_t buf = staging + (uint32_t)ew * kStaging;
     const uint32_t tempty_lead = cluster_addr(smem_u32(tempty), 0);
     int j = 0;
     bool failed = false;
@@ -349,8 +361,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         continue;
       }
       constexpr int kUnit = FP32 ? 4 : 8;                            // elements of 16 bytes
-      constexpr int kBox = FP32 ? 32 : 64;                           // columns of a staging box
-      const int whole = g.in % kUnit ? g.in / kBox * kBox : INT32_MAX;      // a row's ragged end goes element by element
+      constexpr int kBox = FP32 ? 16 : 32;                           // columns of a staging box
+      const int whole = g.in % kUnit ? g.in : INT32_MAX;      // a row's ragged end goes element by element
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int c0 = col0 + 32 * q;
@@ -389,7 +401,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
         }
-        if (!g.tma || c0 >= whole) {
+        if (!g.tma || c0 + 32 > whole) {
           if (row < g.out) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -400,23 +412,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           continue;
         }
-        if (FP32 || q % 2 == 0) {      // the box's last store has been read out of it
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-        }
-        if (FP32) {
+        // boxes of 32 rows x 64 bytes, 64-byte swizzled
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            sts_f4(buf + (uint32_t)lane * 128u + (uint32_t)((e ^ (lane & 7)) * 16), v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-        } else {
-          stage_bf16(buf, lane, q % 2, v);
-        }
-        if (FP32 || q % 2 == 1) {
+        for (int box = 0; box < 32 / kBox; ++box) {
+          if (lane == 0) bulk_wait_read<0>();      // the last store has been read out of it
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (FP32) o[e] = __float_as_uint(v[16 * box + 4 * u + e]);
+              else o[e] = bf16x2_rn(pack_f2(v[8 * u + 2 * e], v[8 * u + 2 * e + 1]));
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + (uint32_t)lane * 64u + (uint32_t)((u ^ (lane >> 1 & 3)) * 16)),
+                         "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                         : "memory");
+          }
           fence_proxy_async_smem();
           __syncwarp();
-          const int x = FP32 ? c0 : c0 - 32;
           if (lane == 0) {
-            if (row0 < g.out && x < g.in) tma_store_2d(&map_c, buf, x, row0);
+            if (row0 < g.out && c0 + kBox * box < g.in) tma_store_2d(&map_c, buf, c0 + kBox * box, row0);
             bulk_commit();
           }
           __syncwarp();
@@ -478,6 +494,20 @@ sf_status make_map_values(CUtensorMap* map, const Ck& ck, int64_t in, int64_t to
                                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SF_ERR_CUDA, "cuTensorMapEncodeTiled (checkpoint) failed (%d)", (int)r);
+  return SF_OK;
+}
+
+// Map of dW's stores: boxes of 32 rows x 64 bytes.
+sf_status make_map_dw(CUtensorMap* map, const WgradArgs& a) {
+  const size_t size = a.fp32 ? 4 : 2;
+  cuuint64_t dims[2] = {(cuuint64_t)a.in, (cuuint64_t)a.out};
+  cuuint64_t strides[1] = {(cuuint64_t)(a.lddw * size)};
+  cuuint32_t box[2] = {(cuuint32_t)(64 / size), 32};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = tensor_map_encoder()(map, a.fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.dw, dims, strides,
+                                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SF_ERR_CUDA, "cuTensorMapEncodeTiled (dW) failed (%d)", (int)r);
   return SF_OK;
 }
 
@@ -592,7 +622,7 @@ sf_status launch_tc(const WgradArgs& a, void* ws, cudaStream_t st) {
   if (a_form == 1) SF_TRY(make_map(&ma, a.dy, a.out, a.tokens, a.ldy, kBK));
   SF_TRY(make_map_values(&mb, a.ck, a.in, a.tokens));
   CUtensorMap mc = ma;       // unused unless dW is written by tensor stores
-  if (g.tma) SF_TRY(a.fp32 ? make_map_c(&mc, static_cast<float*>(a.dw), a.out, a.in, a.lddw) : make_map_c16(&mc, a.dw, a.out, a.in, a.lddw));
+  if (g.tma) SF_TRY(make_map_dw(&mc, a));
   const void* kernel = a.fp32 ? (const void*)&k_wgrad_tc<true> : (const void*)&k_wgrad_tc<false>;
   SF_TRY(allow_dynamic_smem(kernel, kTcSmem));
   cudaLaunchConfig_t cfg = {};

@@ -153,3 +153,29 @@ def test_same_bits_on_a_side_stream_and_in_a_graph():
     g.replay()
     native.sf_sync_status()
     assert torch.equal(dw[0], dw[1]) and torch.equal(dw[0], dw[2])
+
+
+def test_every_call_over_several_waves_gives_the_same_right_bits():
+    # more tiles than pairs, split ones among them, a base that keeps the epilogues behind the products
+    for tokens, out, cin, dt in ((2048, 4096, 4096, F32), (1030, 2600, 2048, F32), (640, 4352, 4352, BF)):
+        dy = torch.empty(tokens, out, dtype=BF, device=DEV)
+        x = torch.empty(tokens, cin, dtype=BF, device=DEV)
+        base = torch.empty(out, cin, dtype=dt, device=DEV)
+        for i, t in enumerate((dy, x, base)):
+            synth.fill_normal_(t, 1.0, 101 + i)
+        ck, q, scale = make_checkpoint(x, 64)
+        native.sf_checkpoint_load(ck, x)          # exact in bf16
+        ref = dy.double().t() @ x.double() + base.double()
+        mag = dy.double().abs().t() @ x.double().abs() + base.double().abs()
+        ws = torch.empty(max(16, native.sf_checkpoint_wgrad_workspace_bytes(tokens, out, cin)), dtype=torch.uint8, device=DEV)
+        first = None
+        for k in range(25):
+            ws.fill_(255)
+            dw = torch.full((out, cin), 7.0, dtype=dt, device=DEV)
+            native.sf_checkpoint_wgrad(dy, ck, dw, base=base, ws=ws)
+            if first is None:
+                first = dw
+                half = 2.0 ** -8 if dt == BF else 2.0 ** -24
+                assert bool(((dw.double() - ref).abs() <= _sum(tokens) * mag + half * ref.abs()).all())
+            assert torch.equal(dw, first), k
+        native.sf_sync_status()
