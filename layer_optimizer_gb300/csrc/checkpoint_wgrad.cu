@@ -91,6 +91,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+// Arrival on a barrier of the first CTA, ordered after this thread's earlier accesses of its own CTA's memory.  (The
+// form with a release at cluster scope takes over 1000 cycles: every slab's converters would wait for it.  What the
+// other CTA's MMA reads here is handed to the async proxy by the fence before.)
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
 // An item: a tile of dW and the slabs of tokens to sum.
 struct Item {
   int mt, nt, k0, k1, part;      // part < 0: a whole tile, else its place in the workspace
@@ -136,7 +143,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     prefetch_tensormap(&map_a);
     prefetch_tensormap(&map_b);
     for (int s = 0; s < kRing; ++s) {
-      mbar_init(&ready[s], 1 + kPair * kConvWarps);
+      mbar_init(&ready[s], 1 + kPair * kConvWarps);      // dY's copies, both CTAs' converters
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kRing8; ++s) {
@@ -283,8 +290,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int4 v[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = lds_i4(src + 2048u * q);
-      // the slab that the slot held has been multiplied
-      if (i >= kSlots && !mbar_wait_cluster(&empty[(i - kSlots) % kRing], (uint32_t)((i - kSlots) / kRing) & 1u)) break;
+      // The slab that the slot held has been multiplied.  (The commit orders the MMAs' reads before its arrival; a wait at
+      // cluster scope would also hold up the thread until its scale loads are there.)
+      if (i >= kSlots && !mbar_wait(&empty[(i - kSlots) % kRing], (uint32_t)((i - kSlots) / kRing) & 1u)) break;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t in[4] = {(uint32_t)v[q].x, (uint32_t)v[q].y, (uint32_t)v[q].z, (uint32_t)v[q].w};
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // only once they have been used)
         mbar_arrive_local(&taken[s8]);
         if (rank == 0) mbar_arrive_local(&ready[s]);
-        else mbar_arrive_remote_release(ready_lead + 8u * (uint32_t)s);
+        else mbar_arrive_pair(ready_lead + 8u * (uint32_t)s);
       }
     }
   } else {
