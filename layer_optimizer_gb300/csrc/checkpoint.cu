@@ -141,41 +141,18 @@ struct Load {
 
 constexpr unsigned kTypes = 1u << SF_BF16 | 1u << SF_FP32;
 
-sf_status launch(const void* kernel, CkArgs& a, void* stream, const char* what) {
+sf_status launch(const void* kernel, CkArgs& a, cudaStream_t stream, const char* what) {
   const int64_t grid = ceil_div<int64_t>(a.rows, a.rpb);
   if (grid > INT32_MAX) return fail(SF_ERR_UNSUPPORTED, "too many rows");
   void* args[] = {&a};
-  SF_CUDA_TRY(cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3(a.tpr * a.rpb), args, 0, as_stream(stream)), what);
+  SF_CUDA_TRY(cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3(a.tpr * a.rpb), args, 0, stream), what);
   return SF_OK;
 }
 
 }  // namespace
-}  // namespace sf
 
-extern "C" {
-
-sf_status sf_checkpoint_store(const sf_matrix* x, const sf_checkpoint* out, void* stream) {
-  using namespace sf;
-  clear_error();
-  NvtxRange nvtx_range("sf_checkpoint_store");
-  SF_TRY(check_matrix(x, "x", -1, -1, kTypes));
-  SF_TRY(check_checkpoint(out, "checkpoint", x->rows, x->cols, true));
-  if (!x->rows || !x->cols) return SF_OK;
-  CkArgs a{};
-  a.x = x->data;
-  a.ldx = x->ld;
-  a.rows = x->rows;
-  a.cols = x->cols;
-  a.ck = device_ck(out);
-  pick_shape(a);
-  return launch(pick_kernel<Store>(x->dtype, on_units(x) && on_units(out) ? kUnits : kStrided), a, stream, "launch k_checkpoint_store");
-}
-
-sf_status sf_checkpoint_load(const sf_checkpoint* c, const float* row_factor, const void* gain, sf_dtype gain_dtype,
-                             double gain_offset, const sf_matrix* y, void* stream) {
-  using namespace sf;
-  clear_error();
-  NvtxRange nvtx_range("sf_checkpoint_load");
+sf_status checkpoint_load(const sf_checkpoint* c, const float* row_factor, const void* gain, int32_t gain_dtype,
+                          double gain_offset, const sf_matrix* y, cudaStream_t stream) {
   SF_TRY(check_matrix(y, "y", -1, -1, kTypes));
   SF_TRY(check_checkpoint(c, "checkpoint", y->rows, y->cols, false));
   SF_TRY(check_aligned(row_factor, sizeof(float), "row_factor"));
@@ -198,6 +175,34 @@ sf_status sf_checkpoint_load(const sf_checkpoint* c, const float* row_factor, co
   pick_shape(a);
   const bool units = on_units(y) && on_units(c) && (!gain || on_units(gain, gain_dtype));
   return launch(pick_kernel<Load>(y->dtype, units ? kUnits : kStrided), a, stream, "launch k_checkpoint_load");
+}
+
+}  // namespace sf
+
+extern "C" {
+
+sf_status sf_checkpoint_store(const sf_matrix* x, const sf_checkpoint* out, void* stream) {
+  using namespace sf;
+  clear_error();
+  NvtxRange nvtx_range("sf_checkpoint_store");
+  SF_TRY(check_matrix(x, "x", -1, -1, kTypes));
+  SF_TRY(check_checkpoint(out, "checkpoint", x->rows, x->cols, true));
+  if (!x->rows || !x->cols) return SF_OK;
+  CkArgs a{};
+  a.x = x->data;
+  a.ldx = x->ld;
+  a.rows = x->rows;
+  a.cols = x->cols;
+  a.ck = device_ck(out);
+  pick_shape(a);
+  return launch(pick_kernel<Store>(x->dtype, on_units(x) && on_units(out) ? kUnits : kStrided), a, as_stream(stream), "launch k_checkpoint_store");
+}
+
+sf_status sf_checkpoint_load(const sf_checkpoint* c, const float* row_factor, const void* gain, sf_dtype gain_dtype,
+                             double gain_offset, const sf_matrix* y, void* stream) {
+  sf::clear_error();
+  sf::NvtxRange nvtx_range("sf_checkpoint_load");
+  return sf::checkpoint_load(c, row_factor, gain, gain_dtype, gain_offset, y, sf::as_stream(stream));
 }
 
 }  // extern "C"

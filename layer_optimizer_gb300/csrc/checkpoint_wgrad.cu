@@ -30,6 +30,10 @@
 namespace sf {
 namespace {
 
+#ifndef KRESTORE
+#define KRESTORE -1
+#endif
+constexpr int kRestore = KRESTORE;
 struct WgradArgs {
   const __nv_bfloat16* dy;   // [tokens][ldy]
   const void* base;          // [out][ldbase], may be null or dw
@@ -46,16 +50,21 @@ __device__ __forceinline__ float dw_at(const void* p, int fp32, int64_t i) {
 
 constexpr int kSpan = 8;                       // slabs that one accumulator sums
 constexpr int kRing = 6;                       // slabs of dY in flight
-constexpr int kRing8 = 4;                      // slabs of the checkpoint
-constexpr int kSlots = 5;                      // converted slabs
+constexpr int kRing8 = 6;                      // slabs of the checkpoint
+constexpr int kSlots = 4;                      // converted slabs
 constexpr int kA = kBM * kBK * 2;              // 16 KB: 128 columns of dY
 constexpr int kB8 = 128 * kBK;                 // 8 KB: 128 columns of the checkpoint
 constexpr int kB = kBRows * kBK * 2;           // 16 KB: the same in bf16
 constexpr int kEpiWarps = 8;
-constexpr int kConvWarps = 4, kConvGroups = 2; // converter warps of a slab; the groups take slabs in turn
-constexpr int kTcThreads = 32 * (4 + kConvWarps * kConvGroups + kEpiWarps);
+constexpr int kConvWarps = 4, kConvGroups = 3; // converter warps of a slab; the groups take slabs in turn
+// a group finds every phase of the barriers that it waits on
+static_assert(kRing % kConvGroups == 0 && kRing8 % kConvGroups == 0 && kSlots <= kRing, "the groups' slabs");
+template <bool FUSED>
+constexpr int kTcThreads = 32 * (4 + (FUSED ? kConvWarps * kConvGroups : 0) + kEpiWarps);
 constexpr int kStaging = 2048;                 // an epilogue warp's box: 32 rows of 64 bytes
-constexpr size_t kTcSmem = (size_t)kRing * kA + (size_t)kRing8 * kB8 + (size_t)kSlots * kB + kEpiWarps * kStaging + 1024 + 256;
+template <bool FUSED>
+constexpr size_t kTcSmem = (size_t)kRing * kA + (FUSED ? (size_t)kRing8 * kB8 + (size_t)kSlots * kB : (size_t)kRing * kB) +
+                           kEpiWarps * kStaging + 1024 + 256;
 constexpr int64_t kMaxParts = 160;             // parts of split tiles, 256 KB of workspace each
 constexpr int64_t kPartFloats = 2 * kBM * kBN;
 
@@ -82,13 +91,11 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// 16 consecutive fp32 columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+// 8 consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
 
 // Arrival on a barrier of the first CTA, ordered after this thread's earlier accesses of its own CTA's memory.  (The
@@ -118,17 +125,18 @@ __device__ __forceinline__ Item item_of(const TcArgs& g, int it, int m_tiles, in
   return i;
 }
 
-// FP32: dW's type.
-template <bool FP32>
-__global__ void __launch_bounds__(kTcThreads, 1)
+// FP32: dW's type.  FUSED: X converted here; else X is a bf16 matrix (map_b), copied like dY.
+template <bool FP32, bool FUSED>
+__global__ void __launch_bounds__(kTcThreads<FUSED>, 1)
     k_wgrad_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                const __grid_constant__ CUtensorMap map_c, const TcArgs g, const int a_form) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  // [dY: kRing x 16 KB] [converted: kSlots x 16 KB] [checkpoint: kRing8 x 8 KB] [staging: 8 x 2 KB] [barriers]
-  const uint32_t ring_a = smem_u32(smem), conv = ring_a + kRing * kA, ring_b = conv + kSlots * kB;
-  const uint32_t staging = ring_b + kRing8 * kB8;
-  uint64_t* ready = reinterpret_cast<uint64_t*>(smem + kRing * kA + kSlots * kB + kRing8 * kB8 + kEpiWarps * kStaging);   // first CTA: dY landed, X converted, in both
+  // [dY: kRing x 16 KB] [X in bf16: kX x 16 KB] [checkpoint: kRing8 x 8 KB] [staging: 8 x 2 KB] [barriers]
+  constexpr int kX = FUSED ? kSlots : kRing;
+  const uint32_t ring_a = smem_u32(smem), conv = ring_a + kRing * kA, ring_b = conv + kX * kB;
+  const uint32_t staging = ring_b + (FUSED ? kRing8 * kB8 : 0);
+  uint64_t* ready = reinterpret_cast<uint64_t*>(smem + kTcSmem<FUSED> - 1024 - 256);   // first CTA: dY and X are there, in both
   uint64_t* empty = ready + kRing;         // the slab's MMAs are done
   uint64_t* land = empty + kRing;          // the CTA's own values landed
   uint64_t* taken = land + kRing8;         // its converters have read them
@@ -136,14 +144,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* tempty = tfull + 2;            // [2] both CTAs have read accumulator b (first CTA)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x / kPair, n_pairs = gridDim.x / kPair;
   if (threadIdx.x == 0) {
     prefetch_tensormap(&map_a);
     prefetch_tensormap(&map_b);
     for (int s = 0; s < kRing; ++s) {
-      mbar_init(&ready[s], 1 + kPair * kConvWarps);      // dY's copies, both CTAs' converters
+      mbar_init(&ready[s], 1 + (FUSED ? kPair * kConvWarps : 0));      // the copies, both CTAs' converters
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kRing8; ++s) {
@@ -165,11 +173,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_launch_dependents();
+  if (!FUSED) griddep_wait();      // X is written by the kernel before
 
   const int nk = (g.tokens + kBK - 1) / kBK;
   const int m_tiles = (g.out + kPair * kBM - 1) / (kPair * kBM), n_tiles = (g.in + kBN - 1) / kBN;
   if (warp < 4) {
-    regs_down<24>();
+    if (FUSED) regs_down<24>();
     if (warp == 0 && lane == 0) {
       const uint32_t ready_lead = cluster_addr(smem_u32(ready), 0);
       int i = 0, landing = 0;
@@ -179,18 +188,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int m0 = w.mt * (kPair * kBM) + (int)rank * kBM, nb = w.nt * kBN + (int)rank * kBRows;
         for (int kb = w.k0; kb < w.k1; ++kb, ++i) {
           const int s = i % kRing, s8 = i % kRing8;
-          if (i >= kRing8 && !mbar_wait(&taken[s8], (uint32_t)(i / kRing8 - 1) & 1u)) {
-            failed = true;
-            break;
+          if (FUSED) {
+            if (i >= kRing8 && !mbar_wait(&taken[s8], (uint32_t)(i / kRing8 - 1) & 1u)) {
+              failed = true;
+              break;
+            }
+            mbar_arrive_expect_tx(&land[s8], kB8);
+            tma_load_2d(smem + (ring_b - ring_a) + s8 * kB8, &map_b, &land[s8], nb, kb * kBK);
+            landing = i + 1;
           }
-          mbar_arrive_expect_tx(&land[s8], kB8);
-          tma_load_2d(smem + (ring_b - ring_a) + s8 * kB8, &map_b, &land[s8], nb, kb * kBK);
-          landing = i + 1;
           if (i >= kRing && !mbar_wait_cluster(&empty[s], (uint32_t)(i / kRing - 1) & 1u)) {
             failed = true;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(&ready[s], kPair * kA);
+          if (rank == 0) mbar_arrive_expect_tx(&ready[s], kPair * (kA + (FUSED ? 0 : kB)));
           const uint32_t st = ring_a + (uint32_t)s * kA, bar = ready_lead + 8u * (uint32_t)s;
           if (a_form == 2) {
             tma_load_3d_pair(st, &map_a, bar, 0, kb * kBK, m0 >> 6);
@@ -198,6 +209,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tma_load_2d_pair(st, &map_a, bar, m0, kb * kBK);
             tma_load_2d_pair(st + kMnBox, &map_a, bar, m0 + 64, kb * kBK);
           }
+          if (!FUSED) tma_load_3d_pair(conv + (uint32_t)s * kB, &map_b, bar, 0, kb * kBK, nb >> 6);
         }
       }
       // the last copies have landed before the pair can exit (immediate unless a wait ran out)
@@ -226,7 +238,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               break;
             }
             tc_fence_after();
-            const uint64_t adesc = umma_desc_mn_sw128(ring_a + (uint32_t)s * kA), bdesc = umma_desc_mn_sw128(conv + (uint32_t)(i % kSlots) * kB);
+            const uint64_t adesc = umma_desc_mn_sw128(ring_a + (uint32_t)s * kA), bdesc = umma_desc_mn_sw128(conv + (uint32_t)(i % kX) * kB);
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k) tc_mma(d_tmem, adesc + 128u * k, bdesc + 128u * k, idesc, kb != k0 || k != 0 ? 1u : 0u);
             tc_commit_pair(empty_a + 8u * (uint32_t)s);
@@ -235,10 +247,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     }
-  } else if (warp < 4 + kConvWarps * kConvGroups) {
-    regs_down<56>();
-    // a thread's 16 columns of tokens r, r + 16, r + 32, r + 48 of a slab
-    const int group = (warp - 4) / kConvWarps, tid = threadIdx.x & 127, cc = tid & 7, r0 = tid >> 3;
+  } else if (FUSED && warp < 4 + kConvWarps * kConvGroups) {
+    if (FUSED) regs_down<48>();
+    // A thread's 16 columns of tokens r0, r0 + 16, r0 + 32, r0 + 48 of a slab.  Both sides are swizzled (16-byte unit ^
+    // row mod 8); eight neighbouring lanes take four units of two rows that differ in bits 0 and 2, so that neither
+    // their loads (units c) nor their stores (2 c, then 2 c + 1) meet in a bank.
+    const int group = (warp - 4) / kConvWarps, tid = threadIdx.x & 127;
+    const int cc = (tid & 3) | (tid >> 1 & 4), r0 = ((tid >> 4 & 3) ^ 5 * (tid >> 2 & 1)) + (tid >> 6) * 8;
     const uint32_t ready_lead = cluster_addr(smem_u32(ready), 0);
     // the slabs of this group, one ahead
     int it = pair, kb = 0;
@@ -269,12 +284,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int q = 0; q < 4; ++q) f[q] = __float_as_uint(__ldg(g.ck.s32 + at[q]));
       }
     };
-    const int odd = cc >> 2;        // the other half's lanes write their two units the other way round: no bank conflict
-    const uint32_t src0 = ring_b + 16u * cc + 128u * r0;
-    const uint32_t unit0 = 16u * ((2 * (cc & 3) + odd) ^ (r0 & 7)), unit1 = 16u * ((2 * (cc & 3) + 1 - odd) ^ (r0 & 7));
-    const uint32_t dst0 = conv + (uint32_t)odd * kMnBox + 128u * r0;
+    const uint32_t src0 = ring_b + 128u * r0 + 16u * (cc ^ (r0 & 7));
+    const uint32_t dst0 = conv + (uint32_t)(cc >> 2) * kMnBox + 128u * r0 + 16u * ((2 * (cc & 3)) ^ (r0 & 7));
     enter();
-    if (group) advance();
+    for (int k = 0; k < group; ++k) advance();
     uint32_t next[4] = {};
     if (it < g.items) scales(next);
     for (int i = group; it < g.items; i += kConvGroups) {
@@ -282,8 +295,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       uint32_t f[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) f[q] = next[q];
-      advance();
-      advance();
+#pragma unroll
+      for (int k = 0; k < kConvGroups; ++k) advance();
       if (it < g.items) scales(next);
       if (!mbar_wait(&land[s8], (uint32_t)(i / kRing8) & 1u)) break;
       const uint32_t src = src0 + (uint32_t)s8 * kB8, dst = dst0 + (uint32_t)(i % kSlots) * kB;
@@ -305,10 +318,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           o[e] = bf16x2_rn(fmul2(pack_f2(x.x, x.y), f2));
         }
         // (16 rows on, the swizzle is the same)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 2048u * q + unit0), "r"(odd ? o[4] : o[0]),
-                     "r"(odd ? o[5] : o[1]), "r"(odd ? o[6] : o[2]), "r"(odd ? o[7] : o[3]));
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 2048u * q + unit1), "r"(odd ? o[0] : o[4]),
-                     "r"(odd ? o[1] : o[5]), "r"(odd ? o[2] : o[6]), "r"(odd ? o[3] : o[7]));
+        const uint32_t to = dst + 2048u * q;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]));
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to ^ 16u), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]));
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -321,8 +333,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
   } else {
-    regs_up<168>();
-    const int ew = warp - 4 - kConvWarps * kConvGroups, quarter = warp & 3, half = ew / 4;
+    if (FUSED) regs_up<152>();
+    const int ew = warp - 4 - (FUSED ? kConvWarps * kConvGroups : 0), quarter = warp & 3, half = ew / 4;
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
     const uint32_t buf = staging + (uint32_t)ew * kStaging;
     const uint32_t tempty_lead = cluster_addr(smem_u32(tempty), 0);
@@ -342,13 +354,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
         const uint32_t at = tmem + (uint32_t)(b * kTmemCols + 128 * half) + lane_off;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          uint32_t r[16];
+        for (int q = 0; q < 16; ++q) {
+          uint32_t r[8];
           __syncwarp();
-          tmem_ld16(at + 16u * q, r);
+          tmem_ld8(at + 8u * q, r);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) acc[16 * q + e] += __uint_as_float(r[e]);
+          for (int e = 0; e < 8; ++e) acc[8 * q + e] += __uint_as_float(r[e]);
         }
         tc_fence_before();
         __syncwarp();
@@ -499,7 +511,7 @@ sf_status make_map_values(CUtensorMap* map, const Ck& ck, int64_t in, int64_t to
   cuuint32_t box[2] = {128, (cuuint32_t)kBK};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, ck.q, dims, strides, box, estr,
-                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SF_ERR_CUDA, "cuTensorMapEncodeTiled (checkpoint) failed (%d)", (int)r);
   return SF_OK;
@@ -519,7 +531,7 @@ sf_status make_map_dw(CUtensorMap* map, const WgradArgs& a) {
   return SF_OK;
 }
 
-// Clusters of two CTAs that fit on the device at once (cached per device).
+// Clusters of two CTAs that fit on the device at once (cached per device; one CTA an SM in either form).
 sf_status resident_pairs(int* out) {
   static std::mutex mu;
   static std::map<int, int> cache;
@@ -534,12 +546,13 @@ sf_status resident_pairs(int* out) {
     at[0].val.clusterDim = {kPair, 1, 1};
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cfg.blockDim = dim3(kTcThreads);
+    cfg.blockDim = dim3(kTcThreads<true>);
     cfg.gridDim = dim3((unsigned)(kPair * std::max(1, sm_count() / kPair)));
-    cfg.dynamicSmemBytes = kTcSmem;
+    cfg.dynamicSmemBytes = kTcSmem<true>;
     int n = 0;
-    SF_TRY(allow_dynamic_smem(reinterpret_cast<const void*>(&k_wgrad_tc<false>), kTcSmem));
-    SF_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_wgrad_tc<false>, &cfg), "cudaOccupancyMaxActiveClusters (k_wgrad_tc)");
+    const auto kernel = &k_wgrad_tc<false, true>;
+    SF_TRY(allow_dynamic_smem(reinterpret_cast<const void*>(kernel), kTcSmem<true>));
+    SF_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg), "cudaOccupancyMaxActiveClusters (k_wgrad_tc)");
     if (n < 1) return fail(SF_ERR_UNSUPPORTED, "no cluster of two CTAs fits on this device");
     it = cache.emplace(dev, n).first;
   }
@@ -605,7 +618,15 @@ __global__ void __launch_bounds__(256) k_wgrad_plain(const WgradArgs a) {
     }
 }
 
-sf_status launch_tc(const WgradArgs& a, void* ws, cudaStream_t st) {
+// Whether X is restored as a bf16 matrix first: three bytes an element more through memory, for a product whose
+// shared memory carries a third less.
+bool restores(int64_t tokens, int64_t out, int64_t in) { return kRestore >= 0 ? kRestore : (tokens >= 512 && out >= 2048 && in >= 256); }
+int64_t restored_ld(int64_t in) { return ceil_div<int64_t>(in, 64) * 64; }
+size_t restored_bytes(int64_t tokens, int64_t out, int64_t in) {
+  return restores(tokens, out, in) ? (size_t)tokens * restored_ld(in) * 2 + 255 & ~(size_t)255 : 0;
+}
+
+sf_status launch_tc(const WgradArgs& a, const sf_checkpoint* c, void* ws, cudaStream_t st) {
   TcArgs g{};
   g.out = (int32_t)a.out;
   g.in = (int32_t)a.in;
@@ -615,8 +636,9 @@ sf_status launch_tc(const WgradArgs& a, void* ws, cudaStream_t st) {
   g.base = a.base;
   g.lddw = a.lddw;
   g.ldbase = a.ldbase;
-  g.ws = static_cast<float*>(ws);
   g.ck = a.ck;
+  const bool fused = !restores(a.tokens, a.out, a.in);
+  g.ws = reinterpret_cast<float*>(static_cast<char*>(ws) + restored_bytes(a.tokens, a.out, a.in));
   const size_t size = a.fp32 ? 4 : 2;
   g.base_vec = a.base && reinterpret_cast<uintptr_t>(a.base) % 16 == 0 && a.ldbase * size % 16 == 0;
   g.tma = reinterpret_cast<uintptr_t>(a.dw) % 16 == 0 && a.lddw * size % 16 == 0 && on_current_device(a.dw);
@@ -628,20 +650,30 @@ sf_status launch_tc(const WgradArgs& a, void* ws, cudaStream_t st) {
   CUtensorMap ma, mb;
   int a_form = make_map_mn3d(&ma, a.dy, a.out, a.tokens, a.ldy) ? 2 : 1;
   if (a_form == 1) SF_TRY(make_map(&ma, a.dy, a.out, a.tokens, a.ldy, kBK));
-  SF_TRY(make_map_values(&mb, a.ck, a.in, a.tokens));
+  if (fused) {
+    SF_TRY(make_map_values(&mb, a.ck, a.in, a.tokens));
+  } else {
+    const sf_matrix x{ws, a.tokens, a.in, restored_ld(a.in), SF_BF16};
+    if (!make_map_mn3d(&mb, ws, x.ld, a.tokens, x.ld)) return fail(SF_ERR_CUDA, "cuTensorMapEncodeTiled (restored checkpoint) failed");
+    SF_TRY(checkpoint_load(c, nullptr, nullptr, SF_FP32, 0.0, &x, st));
+  }
   CUtensorMap mc = ma;       // unused unless dW is written by tensor stores
   if (g.tma) SF_TRY(make_map_dw(&mc, a));
-  const void* kernel = a.fp32 ? (const void*)&k_wgrad_tc<true> : (const void*)&k_wgrad_tc<false>;
-  SF_TRY(allow_dynamic_smem(kernel, kTcSmem));
+  const void* kernel = a.fp32 ? (fused ? (const void*)&k_wgrad_tc<true, true> : (const void*)&k_wgrad_tc<true, false>)
+                              : (fused ? (const void*)&k_wgrad_tc<false, true> : (const void*)&k_wgrad_tc<false, false>);
+  const size_t smem = fused ? kTcSmem<true> : kTcSmem<false>;
+  SF_TRY(allow_dynamic_smem(kernel, smem));
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim = {kPair, 1, 1};
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = fused ? 1 : 2;
   cfg.gridDim = dim3((unsigned)(kPair * std::min<int64_t>(g.items, pairs)));
-  cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = kTcSmem;
+  cfg.blockDim = dim3(fused ? kTcThreads<true> : kTcThreads<false>);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   void* args[] = {&ma, &mb, &mc, &g, &a_form};
   SF_CUDA_TRY(cudaLaunchKernelExC(&cfg, kernel, args), "launch k_wgrad_tc");
@@ -669,8 +701,9 @@ size_t sf_checkpoint_wgrad_workspace_bytes(int64_t tokens, int64_t out, int64_t 
   if (tokens < 0 || out < 1 || in < 1) return 0;
   const int64_t tiles = ceil_div<int64_t>(out, 2 * kBM) * ceil_div<int64_t>(in, kBN);
   const int64_t parts = ceil_div<int64_t>(tokens, kBK) / kSpan;      // of a tile, at most
-  if (parts < 2) return 0;      // never split
-  return (size_t)(tiles < kMaxParts && parts < kMaxParts ? std::min(kMaxParts, tiles * parts) : kMaxParts) * kPartFloats * sizeof(float);
+  const size_t x = restored_bytes(tokens, out, in);
+  if (parts < 2) return x;      // never split
+  return x + (size_t)(tiles < kMaxParts && parts < kMaxParts ? std::min(kMaxParts, tiles * parts) : kMaxParts) * kPartFloats * sizeof(float);
 }
 
 sf_status sf_checkpoint_wgrad(const sf_matrix* dY, const sf_checkpoint* c, const sf_matrix* base, const sf_matrix* dW,
@@ -702,7 +735,7 @@ sf_status sf_checkpoint_wgrad(const sf_matrix* dY, const sf_checkpoint* c, const
   if (tokens && dY->ld % 8 == 0 && c->values.ld % 16 == 0 && reinterpret_cast<uintptr_t>(dY->data) % 16 == 0 &&
       reinterpret_cast<uintptr_t>(c->values.data) % 16 == 0 && tensor_map_encoder() && on_current_device(dY->data) &&
       on_current_device(c->values.data))
-    return launch_tc(a, ws, as_stream(stream));
+    return launch_tc(a, c, ws, as_stream(stream));
   const int64_t gx = ceil_div<int64_t>(in, kT), gy = ceil_div<int64_t>(out, kT);
   if (gy > 65535) return fail(SF_ERR_UNSUPPORTED, "out is too large");
   k_wgrad_plain<<<dim3((unsigned)gx, (unsigned)gy), 256, 0, as_stream(stream)>>>(a);

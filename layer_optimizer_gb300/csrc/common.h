@@ -183,6 +183,10 @@ sf_status tc_gemm(const TcJob& job, cudaStream_t s);
 sf_status make_adam_consts(const sf_adamw_hparams* hp, int64_t step, bool with_decay,
                            AdamConsts* out);
 
+// sf_checkpoint_load within the library (checkpoint.cu).
+sf_status checkpoint_load(const sf_checkpoint* c, const float* row_factor, const void* gain, int32_t gain_dtype,
+                          double gain_offset, const sf_matrix* y, cudaStream_t stream);
+
 // The compressed AdamW step on the host cores for elements [b, e) of fp32
 // S, m, v -> dS (host_adamw.cpp): bitwise the device kernel's results.
 void host_adamw_compressed(const float* S, float* m, float* v, float* dS, int64_t b, int64_t e,
