@@ -47,10 +47,10 @@ struct Ck {
 
 __device__ __forceinline__ F8 zero8() { return F8{}; }
 
-// Eight columns from c0 on (those below cols; the others read as zero).
+// Eight columns from c0 on (those below cols; the others read as zero), as they
+// are stored: unpack() turns them into fp32.
 template <int LAY>
-__device__ __forceinline__ F8 load8(const __nv_bfloat16* row, int c0, int dj, int cols) {
-  Unit<__nv_bfloat16> u;
+__device__ __forceinline__ void load_raw(const __nv_bfloat16* row, int c0, int dj, int cols, Unit<__nv_bfloat16>& u) {
   if (LAY == kUnits) {
     load_unit<kAligned>(row + c0, 0, min(8, cols - c0), u);
   } else {
@@ -61,17 +61,20 @@ __device__ __forceinline__ F8 load8(const __nv_bfloat16* row, int c0, int dj, in
 #pragma unroll
     for (int i = 0; i < 4; ++i) u.w[i] = v[2 * i] | v[2 * i + 1] << 16;
   }
-  return unpack(u);
 }
 template <int LAY>
-__device__ __forceinline__ F8 load8(const float* row, int c0, int dj, int cols) {
-  Unit<float> u;
+__device__ __forceinline__ void load_raw(const float* row, int c0, int dj, int cols, Unit<float>& u) {
   if (LAY == kUnits) {
     load_unit<kAligned>(row + c0, 0, min(8, cols - c0), u);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) u.f[j] = c0 + j * dj < cols ? row[c0 + j * dj] : 0.0f;
   }
+}
+template <int LAY, typename T>
+__device__ __forceinline__ F8 load8(const T* row, int c0, int dj, int cols) {
+  Unit<T> u;
+  load_raw<LAY>(row, c0, dj, cols, u);
   return unpack(u);
 }
 template <int LAY>
@@ -177,38 +180,72 @@ __device__ __forceinline__ F8 load8(const Ck& k, int64_t row, int c0, int dj, in
     }
     return v;
   }
+  uint32_t x[8];
+  float s[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = c0 + j * dj < cols ? p[c0 + j * dj] : 0u;
+  if (k.group_log2 == 0) {
+    s[0] = ck_scale(k, row, 0);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) s[j] = s[0];
+  } else {      // one access a warp and group
+    const int64_t base = row * k.n_groups;
+    if (k.s8) {
+      uint32_t code[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) code[j] = c0 + j * dj < cols ? k.s8[base + ((c0 + j * dj) >> k.group_log2)] : 0u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = e8m0_value(code[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = c0 + j * dj < cols ? k.s32[base + ((c0 + j * dj) >> k.group_log2)] : 0.0f;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int c = c0 + 2 * i * dj, d = c + dj;
-    const float2 x = e4m3x2_value((c < cols ? (uint32_t)p[c] : 0u) | (d < cols ? (uint32_t)p[d] : 0u) << 8);
-    v.p[i] = fmul2(pack_f2(x.x, x.y), pack_f2(c < cols ? ck_scale(k, row, c) : 0.0f, d < cols ? ck_scale(k, row, d) : 0.0f));
+    const float2 y = e4m3x2_value(x[2 * i] | x[2 * i + 1] << 8);
+    v.p[i] = fmul2(pack_f2(y.x, y.y), pack_f2(s[2 * i], s[2 * i + 1]));
   }
   return v;
 }
 
-// The largest finite magnitude of elements j0 .. j0 + n - 1 of a thread's eight (those past the row are zero).
-template <int J0, int N>
-__device__ __forceinline__ float top_finite(const F8& v) {
+constexpr float kLargest = 3.402823466e38f;
+
+// The largest magnitude of a thread's eight values (those past the row are
+// zero), NaN left out.
+__device__ __forceinline__ float top8(const F8& v) {
+  float t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack_f2(v.p[i]);
+    t[i] = fmaxf(fabsf(x.x), fabsf(x.y));
+  }
+  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+// The same of the finite ones.
+__device__ __forceinline__ float top8_finite(const F8& v) {
   float top = 0.0f;
 #pragma unroll
-  for (int j = J0; j < J0 + N; ++j) {
+  for (int j = 0; j < 8; ++j) {
     const float2 x = unpack_f2(v.p[j >> 1]);
     const float a = fabsf(j & 1 ? x.y : x.x);
-    top = a <= 3.402823466e38f ? fmaxf(top, a) : top;
+    top = a <= kLargest ? fmaxf(top, a) : top;
   }
   return top;
 }
 
-// v / scale in e4m3, four codes a word.  What is not finite becomes NaN: v - v is 0 or NaN.
-__device__ __forceinline__ void e4m3_codes(const F8& v, uint64_t inv_lo, uint64_t inv_hi, uint32_t (&w)[2]) {
+// v / scale in e4m3, four codes a word.  A NaN stays one; an infinity becomes
+// one only where EXACT (v - v is 0 or NaN), which costs a subtraction a value.
+template <bool EXACT>
+__device__ __forceinline__ uint32_t e4m3_pair(uint64_t v, uint64_t inv) {
+  const uint64_t x = EXACT ? fmadd2(v, inv, fsub2(v, v)) : fmul2(v, inv);
+  return __nv_cvt_float2_to_fp8x2(unpack_f2(x), __NV_SATFINITE, __NV_E4M3);
+}
+template <bool EXACT>
+__device__ __forceinline__ void e4m3_codes(const F8& v, float inv, uint32_t (&w)[2]) {
+  const uint64_t i2 = pack_f2(inv, inv);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint64_t inv = i ? inv_hi : inv_lo;
-    const uint64_t a = v.p[2 * i], b = v.p[2 * i + 1];
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(unpack_f2(fmadd2(a, inv, fsub2(a, a))), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(unpack_f2(fmadd2(b, inv, fsub2(b, b))), __NV_SATFINITE, __NV_E4M3);
-    w[i] = lo | hi << 16;
-  }
+  for (int i = 0; i < 2; ++i) w[i] = e4m3_pair<EXACT>(v.p[2 * i], i2) | e4m3_pair<EXACT>(v.p[2 * i + 1], i2) << 16;
 }
 
 // Writes a thread's eight columns of a checkpoint's row.  Scale groups: every lane of the warp calls it together
@@ -220,16 +257,22 @@ __device__ __forceinline__ void ck_store8(const Ck& k, int64_t row, int c0, int 
   uint32_t w[2];
   if (LAY == kUnits) {
     uint32_t code = row_code;
+    bool infinite = !k.group_log2;      // (one scale a row: the caller has left infinities out of it)
     if (k.group_log2) {
       const int lanes = 1 << (k.group_log2 - 3);
-      float top = top_finite<0, 8>(v);
+      float top = top8(v);
       for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      infinite = __any_sync(0xffffffffu, top > kLargest);
+      if (infinite) {
+        top = top8_finite(v);
+        for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
       code = e8m0_of(top);
       if (c0 < cols && (c0 & ((1 << k.group_log2) - 1)) == 0) k.s8[row * k.n_groups + (c0 >> k.group_log2)] = (uint8_t)code;
     }
     if (c0 >= cols) return;
-    const float inv = e8m0_inverse(code);
-    e4m3_codes(v, pack_f2(inv, inv), pack_f2(inv, inv), w);
+    if (infinite) e4m3_codes<true>(v, e8m0_inverse(code), w);
+    else e4m3_codes<false>(v, e8m0_inverse(code), w);
     if (c0 + 8 <= cols) {
       asm volatile("st.global.v2.u32 [%0], {%1, %2};" ::"l"(p + c0), "r"(w[0]), "r"(w[1]) : "memory");
     } else {
@@ -249,7 +292,7 @@ __device__ __forceinline__ void ck_store8(const Ck& k, int64_t row, int c0, int 
     for (int j = 0; j < 8; ++j) {
       const float2 x = unpack_f2(v.p[j >> 1]);
       const float a = fabsf(j & 1 ? x.y : x.x);
-      top[j] = a <= 3.402823466e38f ? a : 0.0f;
+      top[j] = a <= kLargest ? a : 0.0f;
     }
     // elements of a group: dj = 32: 1, 2 or 4; shorter rows up to all eight
     const int per = min(8, (1 << k.group_log2) / dj);
@@ -268,7 +311,9 @@ __device__ __forceinline__ void ck_store8(const Ck& k, int64_t row, int c0, int 
         continue;
       }
       float t = top[j];
-      for (int o = dj >> 1; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+      if (dj == 32) t = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(t)));      // magnitudes order as their bits
+      else
+        for (int o = dj >> 1; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
       code[j] = e8m0_of(t);
       const int c = c0 + j * dj;
       if (c < cols && (c & ((1 << k.group_log2) - 1)) == 0) k.s8[row * k.n_groups + (c >> k.group_log2)] = (uint8_t)code[j];
@@ -277,12 +322,113 @@ __device__ __forceinline__ void ck_store8(const Ck& k, int64_t row, int c0, int 
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint64_t inv = pack_f2(e8m0_inverse(code[2 * i]), e8m0_inverse(code[2 * i + 1]));
-    const uint32_t two = __nv_cvt_float2_to_fp8x2(unpack_f2(fmadd2(v.p[i], inv, fsub2(v.p[i], v.p[i]))), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t two = e4m3_pair<true>(v.p[i], inv);
     const int c = c0 + 2 * i * dj;
     if (c < cols) p[c] = (uint8_t)two;
     if (c + dj < cols) p[c + dj] = (uint8_t)(two >> 8);
   }
 }
+
+// Wide units: 16 columns of a thread, of rows whose places all are multiples of
+// 32 bytes (16 of e4m3 values).
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void ld_once32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// 16 columns as stored, and as two F8.
+template <typename T>
+struct Wide {
+  static constexpr int kParts = sizeof(T);      // 16-byte words
+  uint4 w[kParts];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kParts; i += 2) ld_once32(p + i * 16 / sizeof(T), w[i], w[i + 1]);
+  }
+  __device__ __forceinline__ F8 half(int i) const {
+    if constexpr (sizeof(T) == 2) {
+      Unit<__nv_bfloat16> u;
+      u.w[0] = w[i].x, u.w[1] = w[i].y, u.w[2] = w[i].z, u.w[3] = w[i].w;
+      return unpack(u);
+    } else {
+      Unit<float> u;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        u.f[4 * j] = __uint_as_float(w[2 * i + j].x), u.f[4 * j + 1] = __uint_as_float(w[2 * i + j].y);
+        u.f[4 * j + 2] = __uint_as_float(w[2 * i + j].z), u.f[4 * j + 3] = __uint_as_float(w[2 * i + j].w);
+      }
+      return unpack(u);
+    }
+  }
+  // The largest magnitude; not at most kLargest where not all are finite (fp32: unless only NaN are not).
+  __device__ __forceinline__ float top() const {
+    if constexpr (sizeof(T) == 2) {      // magnitudes of bf16 values order as their bits do
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        m = max_u16x2(max_u16x2(m, w[i].x & 0x7fff7fffu), max_u16x2(max_u16x2(w[i].y & 0x7fff7fffu, w[i].z & 0x7fff7fffu), w[i].w & 0x7fff7fffu));
+      return __uint_as_float(max(m & 0xffff0000u, m << 16));
+    } else {
+      return fmaxf(top8(half(0)), top8(half(1)));
+    }
+  }
+};
+
+// Writes 16 columns of a checkpoint's row, as ck_store8 writes eight.  top: what
+// Wide::top() or top8() say of both halves.
+__device__ __forceinline__ void ck_store16(const Ck& k, int64_t row, int c, int cols, const F8& lo, const F8& hi, float top, uint32_t row_code) {
+  uint32_t code = row_code;
+  bool infinite = !k.group_log2;
+  if (k.group_log2) {
+    const int lanes = 1 << (k.group_log2 - 4);
+    infinite = __any_sync(0xffffffffu, !(top <= kLargest));
+    if (infinite) top = c < cols ? fmaxf(top8_finite(lo), top8_finite(hi)) : 0.0f;
+    for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    code = e8m0_of(top);
+    if (c < cols && (c & ((1 << k.group_log2) - 1)) == 0) k.s8[row * k.n_groups + (c >> k.group_log2)] = (uint8_t)code;
+  }
+  if (c >= cols) return;
+  const float inv = e8m0_inverse(code);
+  uint32_t w[2], x[2];
+  if (infinite) e4m3_codes<true>(lo, inv, w), e4m3_codes<true>(hi, inv, x);
+  else e4m3_codes<false>(lo, inv, w), e4m3_codes<false>(hi, inv, x);
+  asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(k.q + row * k.ld + c), "r"(w[0]), "r"(w[1]), "r"(x[0]), "r"(x[1]) : "memory");
+}
+
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const F8& lo, const F8& hi) {
+  Unit<__nv_bfloat16> a, b;
+  pack(lo, a);
+  pack(hi, b);
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.w[0]), "r"(a.w[1]), "r"(a.w[2]), "r"(a.w[3]), "r"(b.w[0]),
+               "r"(b.w[1]), "r"(b.w[2]), "r"(b.w[3])
+               : "memory");
+}
+__device__ __forceinline__ void store16(float* p, const F8& lo, const F8& hi) {
+  Unit<float> a, b;
+  pack(lo, a);
+  pack(hi, b);
+  st_unit(p, a);
+  st_unit(p + 8, b);
+}
+
+// Whether each row of `m` (null passes) starts on a wide unit, and ends on one.
+inline bool on_wide(const sf_matrix* m) {
+  if (!m || m->rows < 1) return true;
+  const uintptr_t unit = m->dtype == SF_E4M3 ? 16 : 32;
+  return m->cols % 16 == 0 && reinterpret_cast<uintptr_t>(m->data) % unit == 0 && (m->rows == 1 || m->ld % 16 == 0);
+}
+inline bool on_wide(const sf_checkpoint* c) { return !c || on_wide(&c->values); }
 
 // The sums (or, from index SUMS on, the maxima) of N values over the tpr
 // threads of a row, in a fixed order: lanes by a butterfly, then the row's

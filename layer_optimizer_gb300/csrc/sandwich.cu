@@ -12,8 +12,8 @@
 namespace sf {
 namespace {
 
-constexpr int kK = 4;               // steps per thread, forward
-constexpr int kMaxThreads = 512;
+constexpr int kK = 2;               // steps per thread of the register forms
+constexpr int kMaxThreads = 1024;
 constexpr int64_t kMaxCols = (int64_t)kMaxThreads * kK * 8;   // 16384
 
 // What both passes take of a call.
@@ -74,13 +74,16 @@ __global__ void __launch_bounds__(kMaxThreads) k_sandwich_fwd(const FwdArgs a) {
   const bool on = row < a.rows;
   const int cols = on ? a.cols : 0;
   const Lane l = lane_of<LAY>(t, tpr);
-  F8 x[kK], r[kK];
+  Unit<TA> x[kK];      // (zero past the row)
+  Unit<TS> r[kK];
+  const TA* xp = row_ptr<TA>(a.x, a.ldx, row);
+  const TS* rp = row_ptr<TS>(a.r, a.ldr, row);
 #pragma unroll
   for (int k = 0; k < kK; ++k) {
-    x[k] = r[k] = zero8();
+    x[k] = Unit<TA>{};
     if (l.c0(k) >= cols) continue;
-    x[k] = load8<LAY>(row_ptr<TA>(a.x, a.ldx, row), l.c0(k), l.dj, cols);
-    if (a.r) r[k] = load8<LAY>(row_ptr<TS>(a.r, a.ldr, row), l.c0(k), l.dj, cols);
+    load_raw<LAY>(xp, l.c0(k), l.dj, cols, x[k]);
+    if (a.r) load_raw<LAY>(rp, l.c0(k), l.dj, cols, r[k]);
   }
   const bool post = a.v.g_post != nullptr, x_row = a.x8.q && !a.x8.group_log2;
   float rho1 = 1.0f;
@@ -88,8 +91,9 @@ __global__ void __launch_bounds__(kMaxThreads) k_sandwich_fwd(const FwdArgs a) {
     float m[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
-      m[0] += dot8(x[k], x[k]);
-      if (x_row) m[1] = fmaxf(m[1], top_finite<0, 8>(x[k]));
+      const F8 v = unpack(x[k]);
+      m[0] += dot8(v, v);
+      if (x_row) m[1] = fmaxf(m[1], top8_finite(v));
     }
     row_reduce_n<2, 1>(m, tpr, red[0]);
     if (post) {
@@ -100,31 +104,33 @@ __global__ void __launch_bounds__(kMaxThreads) k_sandwich_fwd(const FwdArgs a) {
     if (a.x8.q) {
 #pragma unroll
       for (int k = 0; k < kK; ++k)
-        if (k < a.steps) ck_store8<LAY>(a.x8, row, l.c0(k), l.dj, cols, x[k], e8m0_of(m[1]));
+        if (k < a.steps) ck_store8<LAY>(a.x8, row, l.c0(k), l.dj, cols, unpack(x[k]), e8m0_of(m[1]));
     }
   } else if (a.x8.q) {
 #pragma unroll
     for (int k = 0; k < kK; ++k)
-      if (k < a.steps) ck_store8<LAY>(a.x8, row, l.c0(k), l.dj, cols, x[k], 1);
+      if (k < a.steps) ck_store8<LAY>(a.x8, row, l.c0(k), l.dj, cols, unpack(x[k]), 1);
   }
   if (!a.s && !a.h && !a.s8.q && !a.rho2) return;
   float m[2] = {0.0f, 0.0f};
   const bool s_row = a.s8.q && !a.s8.group_log2;
+  F8 s[kK];
 #pragma unroll
   for (int k = 0; k < kK; ++k) {
+    s[k] = zero8();
     if (l.c0(k) >= cols) continue;
-    F8 n = x[k];
+    F8 n = unpack(x[k]);
     if (post) n = mul8(scale8(n, rho1), load_vec<LAY>(a.v.g_post, a.v.gain_fp32, l.c0(k), l.dj, cols, a.v.offset));
     if (a.v.gate) n = mul8(n, load_vec<LAY>(gate_row(a.v, row), a.v.gate_fp32, l.c0(k), l.dj, cols, 0.0f));
     n = scale8(n, a.v.b);
     if (a.r) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) n.p[i] = fmadd2(r[k].p[i], pack_f2(a.v.a, a.v.a), n.p[i]);
+      for (int i = 0; i < 4; ++i) n.p[i] = fmadd2(unpack(r[k]).p[i], pack_f2(a.v.a, a.v.a), n.p[i]);
     }
-    x[k] = n;
+    s[k] = n;
     if (a.s) store8<LAY>(row_ptr<TS>(a.s, a.lds, row), l.c0(k), l.dj, cols, n);
     m[0] += dot8(n, n);
-    if (s_row) m[1] = fmaxf(m[1], top_finite<0, 8>(n));
+    if (s_row) m[1] = fmaxf(m[1], top8_finite(n));
   }
   const bool pre = a.h || a.rho2;
   if (pre || s_row) row_reduce_n<2, 1>(m, tpr, red[1]);
@@ -132,7 +138,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_sandwich_fwd(const FwdArgs a) {
   if (a.s8.q) {
 #pragma unroll
     for (int k = 0; k < kK; ++k)
-      if (k < a.steps) ck_store8<LAY>(a.s8, row, l.c0(k), l.dj, cols, x[k], e8m0_of(m[1]));
+      if (k < a.steps) ck_store8<LAY>(a.s8, row, l.c0(k), l.dj, cols, s[k], e8m0_of(m[1]));
   }
   if (!pre) return;
   const float rho2 = rsqrtf(fmaf(m[0], a.inv_cols, a.eps));
@@ -142,8 +148,244 @@ __global__ void __launch_bounds__(kMaxThreads) k_sandwich_fwd(const FwdArgs a) {
   for (int k = 0; k < kK; ++k) {
     if (l.c0(k) >= cols) continue;
     const F8 g = load_vec<LAY>(a.v.g_pre, a.v.gain_fp32, l.c0(k), l.dj, cols, a.v.offset);
-    store8<LAY>(row_ptr<TA>(a.h, a.ldh, row), l.c0(k), l.dj, cols, mul8(scale8(x[k], rho2), g));
+    store8<LAY>(row_ptr<TA>(a.h, a.ldh, row), l.c0(k), l.dj, cols, mul8(scale8(s[k], rho2), g));
   }
+}
+
+// The same with rows brought by bulk copies, for aligned rows of whole units:
+// a block takes neighbouring rows one after the other, `stages` of them on
+// their way into shared memory, so that loads never wait for a row's sums.
+// What the rows share (b gate g1, g2) stays in registers while the gate row is
+// the same.
+constexpr int kRingThreads = 768, kMaxStages = 8;
+
+// A block's sum of a value per lane and, where wanted, maximum of another one.
+// red: up to kRingThreads / 32 floats of each, those of warps that the block
+// has not zero; alternating between calls.
+constexpr int kRed = kRingThreads / 32;
+__device__ __forceinline__ float block_sum(float v, float* top, float (&red)[2][kRed]) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (top) *top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(*top)));      // magnitudes order as their bits
+  if ((threadIdx.x & 31) == 0) {
+    red[0][threadIdx.x >> 5] = v;
+    if (top) red[1][threadIdx.x >> 5] = *top;
+  }
+  __syncthreads();
+  uint64_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 x = *reinterpret_cast<const float4*>(&red[0][4 * i]);
+    w[i] = fadd2(pack_f2(x.x, x.y), pack_f2(x.z, x.w));
+  }
+  w[0] = fadd2(fadd2(w[0], w[1]), fadd2(w[2], w[3]));
+  if (blockDim.x > 512) {
+#pragma unroll
+    for (int i = 4; i < kRed / 4; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(&red[0][4 * i]);
+      w[0] = fadd2(w[0], fadd2(pack_f2(x.x, x.y), pack_f2(x.z, x.w)));
+    }
+  }
+  if (top) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRed; ++i) m = fmaxf(m, red[1][i]);
+    *top = m;
+  }
+  const float2 x = unpack_f2(w[0]);
+  return x.x + x.y;
+}
+// What a maximum over finite values starts from: infinity where one is not.
+__device__ __forceinline__ float top_or_inf(float top) { return top <= kLargest ? top : __uint_as_float(0x7f800000u); }
+
+template <typename T>
+struct LdsWide;      // 16 columns from shared memory
+template <>
+struct LdsWide<__nv_bfloat16> : Wide<__nv_bfloat16> {
+  __device__ __forceinline__ explicit LdsWide(uint32_t p) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int4 v = lds_i4(p + 16 * i);
+      w[i] = make_uint4(v.x, v.y, v.z, v.w);
+    }
+  }
+};
+template <>
+struct LdsWide<float> : Wide<float> {
+  __device__ __forceinline__ explicit LdsWide(uint32_t p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int4 v = lds_i4(p + 16 * i);
+      w[i] = make_uint4(v.x, v.y, v.z, v.w);
+    }
+  }
+};
+
+// C: wide units a thread.  With one of them g2 stays in registers too.
+template <typename TA, typename TS, int C, int REGS>
+__global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int stages) {
+  __shared__ __align__(16) float red[2][2][2][kRed];      // [row mod 2][which sum][sums, maxima]
+  __shared__ float redx[kRed];
+  __shared__ __align__(8) uint64_t full[kMaxStages];
+  extern __shared__ __align__(128) unsigned char ring[];
+  const int t = threadIdx.x, T = blockDim.x;
+  for (int i = t; i < 8 * kRed; i += T) (&red[0][0][0][0])[i] = 0.0f;
+  const uint32_t row_x = (uint32_t)a.cols * sizeof(TA), stage_bytes = row_x + (a.r ? (uint32_t)a.cols * sizeof(TS) : 0u);
+  const uint32_t ring0 = smem_u32(ring);
+  const int64_t first = a.rows * blockIdx.x / gridDim.x, end = a.rows * (blockIdx.x + 1) / gridDim.x;
+  auto fill = [&](int64_t row, int st) {      // by one thread
+    unsigned char* at = ring + (size_t)st * stage_bytes;
+    mbar_arrive_expect_tx(&full[st], stage_bytes);
+    bulk_load(at, row_ptr<TA>(a.x, a.ldx, row), row_x, &full[st]);
+    if (a.r) bulk_load(at + row_x, row_ptr<TS>(a.r, a.ldr, row), stage_bytes - row_x, &full[st]);
+  };
+  if (t == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init_cluster();
+    for (int i = 0; i < stages && first + i < end; ++i) fill(first + i, i);
+  }
+  __syncthreads();
+  const bool post = a.v.g_post != nullptr;
+  const bool x_row = a.x8.q && !a.x8.group_log2, s_row = a.s8.q && !a.s8.group_log2;
+  F8 w[C][2], g2[2];
+  auto vec = [&](const void* p, int fp32, int c, float add, F8 (&v)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) v[h] = load_vec<kUnits>(p, fp32, c + 8 * h, 1, a.cols, add);
+  };
+  if (C == 1 && a.h && 16 * t < a.cols) vec(a.v.g_pre, a.v.gain_fp32, 16 * t, a.v.offset, g2);
+  int64_t gate_end = first;      // rows from here on take another gate row
+  int64_t gate_at = a.v.gate ? first / a.v.span : 0;
+  int st = 0, parity = 0;
+  uint32_t phase = 0;
+  bool dead = false;      // a wait ran out (recorded): go on without waiting, so that all threads still leave together
+  for (int64_t row = first; row < end; ++row, parity ^= 1) {
+    if (row == gate_end) {
+      gate_end = a.v.gate ? (gate_at + 1) * a.v.span : end;
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int c = 16 * (t + k * T);
+        if (c >= a.cols) continue;
+        const uint64_t b2 = pack_f2(a.v.b, a.v.b);
+        w[k][0] = w[k][1] = F8{{b2, b2, b2, b2}};
+        F8 v[2];
+        if (post) {
+          vec(a.v.g_post, a.v.gain_fp32, c, a.v.offset, v);
+          w[k][0] = mul8(w[k][0], v[0]), w[k][1] = mul8(w[k][1], v[1]);
+        }
+        if (a.v.gate) {
+          vec(static_cast<const char*>(a.v.gate) + gate_at * a.v.ld_gate * (a.v.gate_fp32 ? 4 : 2), a.v.gate_fp32, c, 0.0f, v);
+          w[k][0] = mul8(w[k][0], v[0]), w[k][1] = mul8(w[k][1], v[1]);
+        }
+      }
+      ++gate_at;
+    }
+    if (!dead) dead = !mbar_wait_u32(smem_u32(&full[st]), phase);
+    const uint32_t at = ring0 + (uint32_t)st * stage_bytes;
+    float rho1 = 1.0f;
+    if (post || a.x8.q) {
+      float sum = 0.0f, top[1] = {0.0f};
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int c = 16 * (t + k * T);
+        const bool on = c < a.cols;      // (the others read the row's start and drop it)
+        const LdsWide<TA> x(at + (on ? c : 0) * (uint32_t)sizeof(TA));
+        const F8 lo = x.half(0), hi = x.half(1);
+        const float part = dot8(lo, lo) + dot8(hi, hi);
+        sum += on ? part : 0.0f;
+        if (x_row) top[0] = on ? fmaxf(top[0], top_or_inf(x.top())) : top[0];
+        else if (a.x8.q) ck_store16(a.x8, row, c, a.cols, lo, hi, on ? x.top() : 0.0f, 1);
+      }
+      if (post || x_row) sum = block_sum(sum, x_row ? top : nullptr, red[parity][0]);
+      if (post) {
+        rho1 = rsqrtf(fmaf(sum, a.inv_cols, a.eps));
+        if (a.rho1 && t == 0) a.rho1[row] = rho1;
+      }
+      if (x_row) {
+        if (top[0] > kLargest) {      // (the same for the block)
+          top[0] = 0.0f;
+#pragma unroll
+          for (int k = 0; k < C; ++k) {
+            const int c = 16 * (t + k * T);
+            if (c >= a.cols) continue;
+            const LdsWide<TA> x(at + c * (uint32_t)sizeof(TA));
+            top[0] = fmaxf(top[0], fmaxf(top8_finite(x.half(0)), top8_finite(x.half(1))));
+          }
+          row_reduce_n<1, 0>(top, T, redx);
+        }
+        const uint32_t code = e8m0_of(top[0]);
+        if (t == 0) a.x8.s8[row] = (uint8_t)code;
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+          const int c = 16 * (t + k * T);
+          if (c >= a.cols) continue;
+          const LdsWide<TA> x(at + c * (uint32_t)sizeof(TA));
+          ck_store16(a.x8, row, c, a.cols, x.half(0), x.half(1), 0.0f, code);
+        }
+      }
+    }
+    F8 s[C][2];
+    float sum = 0.0f, top[1] = {0.0f};
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      const int c = 16 * (t + k * T);
+      s[k][0] = s[k][1] = zero8();
+      if (c < a.cols) {
+        const LdsWide<TA> x(at + c * (uint32_t)sizeof(TA));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[k][h] = mul8(scale8(x.half(h), rho1), w[k][h]);
+        if (a.r) {
+          const LdsWide<TS> r(at + row_x + c * (uint32_t)sizeof(TS));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const F8 v = r.half(h);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[k][h].p[i] = fmadd2(v.p[i], pack_f2(a.v.a, a.v.a), s[k][h].p[i]);
+          }
+        }
+        if (a.s) store16(row_ptr<TS>(a.s, a.lds, row) + c, s[k][0], s[k][1]);
+      }
+      sum += dot8(s[k][0], s[k][0]) + dot8(s[k][1], s[k][1]);
+      if (s_row) top[0] = fmaxf(top[0], fmaxf(top8(s[k][0]), top8(s[k][1])));
+      else if (a.s8.q) ck_store16(a.s8, row, c, a.cols, s[k][0], s[k][1], fmaxf(top8(s[k][0]), top8(s[k][1])), 1);
+    }
+    // (a barrier in any case: the row has been read out of its stage)
+    const float rho2 = rsqrtf(fmaf(block_sum(sum, s_row ? top : nullptr, red[parity][1]), a.inv_cols, a.eps));
+    if (t == 0) {
+      if (row + stages < end) fill(row + stages, st);
+      if (a.rho2) a.rho2[row] = rho2;
+    }
+    if (s_row) {
+      if (top[0] > kLargest) {
+        top[0] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < C; ++k) top[0] = fmaxf(top[0], fmaxf(top8_finite(s[k][0]), top8_finite(s[k][1])));
+        __syncthreads();      // redx may still be read
+        row_reduce_n<1, 0>(top, T, redx);
+      }
+      const uint32_t code = e8m0_of(top[0]);
+      if (t == 0) a.s8.s8[row] = (uint8_t)code;
+#pragma unroll
+      for (int k = 0; k < C; ++k) ck_store16(a.s8, row, 16 * (t + k * T), a.cols, s[k][0], s[k][1], 0.0f, code);
+    }
+    if (a.h) {
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int c = 16 * (t + k * T);
+        if (c >= a.cols) continue;
+        if (C > 1) vec(a.v.g_pre, a.v.gain_fp32, c, a.v.offset, g2);
+        store16(row_ptr<TA>(a.h, a.ldh, row) + c, mul8(scale8(s[k][0], rho2), g2[0]), mul8(scale8(s[k][1], rho2), g2[1]));
+      }
+    }
+    if (++st == stages) {
+      st = 0;
+      phase ^= 1u;
+    }
+  }
+  if (dead && t == 0) {      // copies still under way land before their memory is given up (waited for once more, bounded)
+    const int64_t n = end - first;
+    for (int i = 0; i < stages && i < n; ++i) mbar_wait(&full[i], (uint32_t)((n - 1 - i) / stages) & 1u);
+  }
+  if (dead) __syncthreads();
 }
 
 // Backward.  With w = b gate g1 (the factor of x's norm in s) a row's sums
@@ -427,6 +669,43 @@ struct Bwd {
   static const void* ptr() { return (const void*)&k_sandwich_bwd<TA, TS, LAY>; }
 };
 
+// The staged form: wide units a thread, registers.
+constexpr int kFwdRegs1 = 80, kFwdRegs2 = 128;
+template <typename TA, typename TS>
+const void* fwd_ring(int c) {
+  return c == 1 ? (const void*)&k_sandwich_fwd_ring<TA, TS, 1, kFwdRegs1> : (const void*)&k_sandwich_fwd_ring<TA, TS, 2, kFwdRegs2>;
+}
+constexpr size_t kSmemPerSm = 224 << 10, kSmemBlock = 2 << 10;      // a block's static and reserved shared memory
+constexpr int kRingMinCols = 1024;
+
+struct RingShape {
+  int c = 0, threads = 0, per_sm = 0, stages = 0;
+};
+// One or two wide units a thread, whichever lets more threads, or as many in
+// more blocks, reside on an SM (bf16, 4 x 4096-token batches' worth of data: 8192
+// columns in two blocks of 256 threads 127 us, in one of 512 169; 12288 with an
+// fp32 stream in one of 768 threads 201 us, in one of 384 244).  At least three
+// stages each, two in long rows.  False where rows are too long, or too few or short
+// for it to pay (65536 x 512: 63 us, 51 with loads into registers; 32768 x 1024 50 and 54).
+bool ring_shape(int64_t rows, int64_t cols, size_t stage, int regs1, int regs2, RingShape* best) {
+  if (cols % 16 || cols < kRingMinCols || rows < 2 * sm_count()) return false;
+  for (int c = 1; c <= 2; ++c) {
+    RingShape s;
+    s.c = c;
+    s.threads = ceil_div(ceil_div((int)(cols / 16), c), 32) * 32;
+    const int regs = c == 1 ? regs1 : regs2;
+    int n = std::min(65536 / (regs * s.threads), 2048 / s.threads);
+    while (n > 1 && kSmemPerSm / n < kSmemBlock + 3 * stage) --n;
+    if (s.threads > kRingThreads || n < 1) continue;
+    s.per_sm = n;
+    s.stages = (int)std::min<size_t>(kMaxStages, (kSmemPerSm / n - kSmemBlock) / stage);
+    if (s.stages < 2) continue;
+    const int now = s.threads * n, was = best->threads * best->per_sm;
+    if (now > was || (now == was && n > best->per_sm)) *best = s;
+  }
+  return best->c > 0;
+}
+
 sf_status check_vector(const void* v, int32_t dtype, const char* name) {
   if (!v) return SF_OK;
   if (dtype != SF_BF16 && dtype != SF_FP32) return fail(SF_ERR_UNSUPPORTED, "%s: type %d is not taken here", name, (int)dtype);
@@ -464,6 +743,14 @@ sf_status check_common(const sf_sandwich* p, int64_t rows, int64_t cols, const v
 }
 
 }  // namespace
+
+int read_and_clear_device_error_sandwich() {
+  int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof v) != cudaSuccess) return 0;
+  if (v) cudaMemcpyToSymbol(g_device_error, &z, sizeof z);
+  return v;
+}
+
 }  // namespace sf
 
 extern "C" {
@@ -507,9 +794,27 @@ sf_status sf_sandwich_norm_forward(const sf_sandwich* p, const sf_matrix* x, con
   a.inv_cols = (float)(1.0 / (double)cols);
   const bool units = on_units(x) && on_units(residual) && on_units(sum) && on_units(h) && on_units(gate) && on_units(x8) &&
                      on_units(sum8) && on_units(gain_post, gain_dtype) && on_units(gain_pre, gain_dtype);
-  // as many threads a row as four steps need; one step while rows leave SMs without work
+  const int32_t ts = residual ? residual->dtype : sum ? sum->dtype : x->dtype;
+  void* args[] = {&a, nullptr};
+  // bulk copies take this device's own memory only
+  RingShape ring;
+  const size_t stage = (size_t)cols * (dtype_bytes(x->dtype) + (residual ? dtype_bytes(ts) : 0));
+  if (units && on_wide(x) && on_wide(residual) && on_wide(sum) && on_wide(h) && on_wide(x8) && on_wide(sum8) &&
+      ring_shape(rows, cols, stage, kFwdRegs1, kFwdRegs2, &ring) && (sum || h || sum8 || rstd_pre) && on_current_device(x->data) &&
+      (!residual || on_current_device(residual->data))) {
+    using B = __nv_bfloat16;
+    const void* kernel = x->dtype == SF_BF16 ? (ts == SF_BF16 ? fwd_ring<B, B>(ring.c) : fwd_ring<B, float>(ring.c))
+                                             : (ts == SF_BF16 ? fwd_ring<float, B>(ring.c) : fwd_ring<float, float>(ring.c));
+    SF_TRY(allow_dynamic_smem(kernel, stage * ring.stages));
+    args[1] = &ring.stages;
+    SF_CUDA_TRY(cudaLaunchKernel(kernel, dim3((unsigned)std::min<int64_t>(rows, (int64_t)sm_count() * ring.per_sm)), dim3(ring.threads), args,
+                                 stage * ring.stages, as_stream(stream)),
+                "launch k_sandwich_fwd_ring");
+    return SF_OK;
+  }
+  // as many threads a row as two steps need; one step while rows leave SMs without work
   const int64_t n = ceil_div<int64_t>(cols, 8);
-  const int64_t t = std::min<int64_t>(ceil_div<int64_t>(n, rows < 2 * sm_count() ? 1 : kK), kMaxThreads);
+  const int64_t t = std::min<int64_t>(ceil_div<int64_t>(n, rows < 2 * sm_count() ? 1 : kK), kMaxThreads);      // (1024 x 2 x 8 columns)
   if (t > 64) {
     a.tpr = (int32_t)ceil_div<int64_t>(t, 32) * 32;
     a.rpb = 1;
@@ -522,8 +827,6 @@ sf_status sf_sandwich_norm_forward(const sf_sandwich* p, const sf_matrix* x, con
   a.steps = (int32_t)ceil_div<int64_t>(n, a.tpr);
   const int64_t grid = ceil_div<int64_t>(rows, a.rpb);
   if (grid > INT32_MAX) return fail(SF_ERR_UNSUPPORTED, "too many rows");
-  const int32_t ts = residual ? residual->dtype : sum ? sum->dtype : x->dtype;
-  void* args[] = {&a};
   SF_CUDA_TRY(cudaLaunchKernel(pick_kernel<Fwd>(x->dtype, ts, units ? kUnits : kStrided), dim3((unsigned)grid),
                                dim3(a.tpr * a.rpb), args, 0, as_stream(stream)),
               "launch k_sandwich_fwd");

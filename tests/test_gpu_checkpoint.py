@@ -35,6 +35,22 @@ def test_store_is_the_oracles(rows, cols, pad, lead, xt, group):
     assert guard_ok(q, buf, lead)
 
 
+@pytest.mark.parametrize("cols", [96, 100, 75, 512])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("xt", [BF, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_what_is_not_finite_next_to_the_largest_value(cols, group, xt, bad):
+    # in every place around it: its scale and its group's other values are those of the finite ones
+    x = synth.normal((64, cols), 1.0, 4).to(xt).to(DEV)
+    for i in range(64):
+        x[i, i] = 300.0
+        x[i, (i + i % 7 + 1) % cols] = bad
+        x[i, (i + 64) % cols if i % 2 else (i + 33) % cols] = -bad
+    ck, q, scale, _ = new_checkpoint(64, cols, group)
+    native.sf_checkpoint_store(x, ck)
+    _same(q, scale, f64(x.float()), group)
+
+
 @pytest.mark.parametrize("cols", [96, 75])
 @pytest.mark.parametrize("group", [0, 32, 64, 128])
 @pytest.mark.parametrize("xt", [BF, F32])
