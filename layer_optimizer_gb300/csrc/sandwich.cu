@@ -40,9 +40,10 @@ struct FwdArgs {
   Vectors v;
 };
 
-__device__ __forceinline__ const void* gate_row(const Vectors& v, int64_t row) {
-  return static_cast<const char*>(v.gate) + row / v.span * v.ld_gate * (v.gate_fp32 ? 4 : 2);
+__device__ __forceinline__ const void* gate_row_of(const Vectors& v, int64_t k) {
+  return static_cast<const char*>(v.gate) + k * v.ld_gate * (v.gate_fp32 ? 4 : 2);
 }
+__device__ __forceinline__ const void* gate_row(const Vectors& v, int64_t row) { return gate_row_of(v, row / v.span); }
 
 __device__ __forceinline__ F8 mul8(const F8& a, const F8& b) {
   F8 r;
@@ -436,11 +437,12 @@ __device__ __forceinline__ void store_any(void* row, int fp32, int c0, int dj, i
   else store8<LAY>(static_cast<__nv_bfloat16*>(row), c0, dj, cols, v);
 }
 
-constexpr int kBwdThreads = 1024, kBwdK = 2;
+constexpr int kBwdThreads = 1024, kBwdFew = 256, kBwdK = 2;
 
-template <typename TA, typename TS, int LAY>
-__global__ void __launch_bounds__(kBwdThreads) k_sandwich_bwd(const BwdArgs a) {
-  __shared__ float red[2][3 * (kBwdThreads / 32)];
+// T: most threads of a block.  Up to 4096 columns kBwdFew, with 128 registers a thread; 1024 have 64 and spill.
+template <typename TA, typename TS, int LAY, int T>
+__global__ void __launch_bounds__(T, T == kBwdFew ? 2 : 1) k_sandwich_bwd(const BwdArgs a) {
+  __shared__ float red[2][3 * (T / 32)];
   const int tpr = a.tpr, lane_row = (int)threadIdx.x / tpr, t = (int)threadIdx.x - lane_row * tpr;
   const int64_t worker = (int64_t)blockIdx.x * a.rpb + lane_row;
   const Lane l = lane_of<LAY>(t, tpr);
@@ -561,6 +563,256 @@ __global__ void __launch_bounds__(kBwdThreads) k_sandwich_bwd(const BwdArgs a) {
   }
 }
 
+// The same backward pass with rows brought by bulk copies, as in the forward
+// form: a block is one worker, a thread holds a wide unit's sums, w and g2 in
+// registers.  A row is read from shared memory twice, for its sums and, past
+// the one barrier, for its outputs (dsum + rho2 dh g2 stays in registers
+// between); past that barrier every thread is also done with the row before,
+// whose stage is filled again.  For calls with dh, dsum or none, and x and s both in
+// full or both as checkpoints (KEPT).
+template <typename T>
+__device__ __forceinline__ void lds16(uint32_t p, F8 (&v)[2]) {
+  const LdsWide<T> u(p);
+  v[0] = u.half(0), v[1] = u.half(1);
+}
+// 16 e4m3 values from shared memory, times their scale.
+__device__ __forceinline__ void lds16_e4m3(uint32_t p, float scale, F8 (&v)[2]) {
+  const int4 q = lds_i4(p);
+  const uint32_t w[4] = {(uint32_t)q.x, (uint32_t)q.y, (uint32_t)q.z, (uint32_t)q.w};
+  const uint64_t s2 = pack_f2(scale, scale);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = e4m3x2_value(w[i >> 1] >> (16 * (i & 1)) & 0xffffu);
+    v[i >> 2].p[i & 3] = fmul2(pack_f2(x.x, x.y), s2);
+  }
+}
+
+constexpr int kBwdRingThreads = 512, kBwdRingRegs = 128;
+
+template <typename TA, typename TS, bool KEPT, bool POST>
+__global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const BwdArgs a, const int stages) {
+  constexpr int kWarps = kBwdRingThreads / 32, N = POST ? 3 : 1;
+  __shared__ __align__(16) float red[2][N][kWarps];
+  __shared__ __align__(8) uint64_t full[kMaxStages];
+  extern __shared__ __align__(128) unsigned char ring[];
+  const int t = threadIdx.x, c = 16 * t;
+  const bool on = c < a.cols;
+  for (int i = t; i < 2 * N * kWarps; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
+  const uint32_t size_a = (uint32_t)a.cols * sizeof(TA), size_s = (uint32_t)a.cols * sizeof(TS);
+  const uint32_t off_e = size_a, off_x = off_e + (a.dsum ? size_s : 0u), off_s = off_x + (KEPT ? (uint32_t)a.cols : size_a);
+  const uint32_t stage_bytes = off_s + (KEPT ? (uint32_t)a.cols : size_s);
+  const uint32_t ring0 = smem_u32(ring);
+  // this worker's rows (n of them, below 2^29): the part of a gate row, or every workers-th gate row
+  const int worker = blockIdx.x, workers = gridDim.x, span = (int)a.span, rows = (int)a.rows;
+  int row, n, left;      // the next row, the number of rows, those left in its item
+  if (a.many) {
+    const int items = (int)a.items, mine = (items - worker + workers - 1) / workers;
+    n = mine * span - (worker + (mine - 1) * workers == items - 1 ? items * span - rows : 0);
+    row = worker * span;
+    left = min(span, rows - row);
+  } else {
+    const int k = worker / a.parts, p = worker - k * a.parts, len = min(span, rows - k * span);
+    row = k * span + (int)((int64_t)len * p / a.parts);
+    left = n = k * span + (int)((int64_t)len * (p + 1) / a.parts) - row;
+  }
+  const int row0 = row;
+  auto row_at = [&](int j) {
+    if (!a.many) return row0 + j;
+    const int q = j / span;
+    return (worker + q * workers) * span + j - q * span;
+  };
+  auto fill = [&](int j, int st) {      // by one thread
+    const int64_t r = row_at(j);
+    unsigned char* at = ring + (size_t)st * stage_bytes;
+    mbar_arrive_expect_tx(&full[st], stage_bytes);
+    bulk_load(at, row_ptr<TA>(a.dh, a.lddh, r), size_a, &full[st]);
+    if (a.dsum) bulk_load(at + off_e, row_ptr<TS>(a.dsum, a.lddsum, r), size_s, &full[st]);
+    if (KEPT) {
+      bulk_load(at + off_x, a.x8.q + r * a.x8.ld, (uint32_t)a.cols, &full[st]);
+      bulk_load(at + off_s, a.s8.q + r * a.s8.ld, (uint32_t)a.cols, &full[st]);
+    } else {
+      bulk_load(at + off_x, row_ptr<TA>(a.x, a.ldx, r), size_a, &full[st]);
+      bulk_load(at + off_s, row_ptr<TS>(a.s, a.lds, r), size_s, &full[st]);
+    }
+  };
+  if (t == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init_cluster();
+    for (int i = 0; i < stages && i < n; ++i) fill(i, i);
+  }
+  __syncthreads();
+  F8 accT[2] = {}, accP[2] = {}, w[2], g2[2];
+  auto vec = [&](const void* p, int fp32, float add, F8 (&v)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) v[h] = load_vec<kUnits>(p, fp32, c + 8 * h, 1, a.cols, add);
+  };
+  auto load_w = [&](const void* gate) {      // gate g1
+    const uint64_t one = pack_f2(1.0f, 1.0f);
+    w[0] = w[1] = F8{{one, one, one, one}};
+    if (!on) return;
+    F8 v[2];
+    if (POST) vec(a.v.g_post, a.v.gain_fp32, a.v.offset, w);
+    if (gate) {
+      vec(gate, a.v.gate_fp32, 0.0f, v);
+      w[0] = mul8(w[0], v[0]), w[1] = mul8(w[1], v[1]);
+    }
+  };
+  if (on) vec(a.v.g_pre, a.v.gain_fp32, a.v.offset, g2);
+  // a gate row's T is complete (several items a worker)
+  auto flush = [&](int gate_row, bool first) {
+    const void* gate = gate_row_of(a.v, gate_row);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int ch = c + 8 * h;
+      if (on && a.dgate) {
+        F8 v = accT[h];
+        if (POST) v = mul8(v, load_vec<kUnits>(a.v.g_post, a.v.gain_fp32, ch, 1, a.cols, a.v.offset));
+        store_any<kUnits>(static_cast<char*>(a.dgate) + (int64_t)gate_row * a.lddgate * (a.dgate_fp32 ? 4 : 2), a.dgate_fp32, ch, 1, a.cols, v);
+      }
+      if (on && a.tpart) {      // this worker's own row, written and read by the same threads (on 16 bytes at least: no wide access)
+        float* part = a.tpart + (int64_t)worker * a.cols;
+        F8 v = first ? zero8() : load8<kStrided>(part, ch, 1, a.cols);
+        const F8 g = load_vec<kUnits>(gate, a.v.gate_fp32, ch, 1, a.cols, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v.p[i] = fmadd2(accT[h].p[i], g.p[i], v.p[i]);
+        store8<kStrided>(part, ch, 1, a.cols, v);
+      }
+      accT[h] = zero8();
+    }
+  };
+  // a row's rhos and scales come one row ahead
+  float rho1_next = 1.0f, rho2_next = 0.0f;
+  uint32_t sx_next = 0, ss_next = 0;
+  auto scale_raw = [&](const Ck& ck, int64_t r) {
+    const int64_t i = r * ck.n_groups + (ck.group_log2 && on ? c >> ck.group_log2 : 0);
+    return ck.s8 ? (uint32_t)ck.s8[i] : __float_as_uint(ck.s32[i]);
+  };
+  auto scale_value = [](const Ck& ck, uint32_t raw) { return ck.s8 ? e8m0_value(raw) : __uint_as_float(raw); };
+  auto prefetch = [&](int64_t r) {
+    if (POST) rho1_next = a.rho1[r];
+    rho2_next = a.rho2[r];
+    if (KEPT) sx_next = scale_raw(a.x8, r), ss_next = scale_raw(a.s8, r);
+  };
+  if (n > 0) prefetch(row);
+  int gate_row = a.many ? worker : worker / a.parts;
+  load_w(a.v.gate ? gate_row_of(a.v, gate_row) : nullptr);
+  int st = 0;
+  uint32_t phase = 0;
+  bool dead = false;      // a wait ran out (recorded): go on without waiting, so that all threads still leave together
+  for (int j = 0; j < n; ++j) {
+    const float rho1 = rho1_next, rho2 = rho2_next;
+    const float sx = scale_value(a.x8, sx_next), ss = scale_value(a.s8, ss_next);
+    const int64_t r = row;
+    const bool last = --left == 0;      // of its item
+    row = last ? (gate_row + workers) * span : row + 1;
+    if (j + 1 < n) prefetch(row);
+    if (!dead) dead = !mbar_wait_u32(smem_u32(&full[st]), phase);
+    const uint32_t base = ring0 + (uint32_t)st * stage_bytes;
+    const uint64_t rho2_2 = pack_f2(rho2, rho2);
+    F8 e[2] = {};
+    float m[N] = {};
+    if (on) {
+      F8 dn[2], s[2], x[2];
+      lds16<TA>(base + c * (uint32_t)sizeof(TA), dn);
+      if (a.dsum) lds16<TS>(base + off_e + c * (uint32_t)sizeof(TS), e);
+      if (KEPT) lds16_e4m3(base + off_s + c, ss, s);
+      else lds16<TS>(base + off_s + c * (uint32_t)sizeof(TS), s);
+      if (POST) {
+        if (KEPT) lds16_e4m3(base + off_x + c, sx, x);
+        else lds16<TA>(base + off_x + c * (uint32_t)sizeof(TA), x);
+      }
+      uint64_t q[N] = {};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t ds = fmul2(dn[h].p[i], s[h].p[i]);
+          accP[h].p[i] = fmadd2(ds, rho2_2, accP[h].p[i]);
+          q[0] = fmadd2(ds, g2[h].p[i], q[0]);
+          e[h].p[i] = fmadd2(fmul2(dn[h].p[i], g2[h].p[i]), rho2_2, e[h].p[i]);
+          if constexpr (POST) {
+            const uint64_t wx = fmul2(w[h].p[i], x[h].p[i]);
+            q[1] = fmadd2(wx, e[h].p[i], q[1]);
+            q[2] = fmadd2(wx, s[h].p[i], q[2]);
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < N; ++i) m[i] = unpack_f2(q[i]).x + unpack_f2(q[i]).y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) m[i] += __shfl_xor_sync(0xffffffffu, m[i], o);
+    if ((t & 31) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) red[j & 1][i][t >> 5] = m[i];
+    }
+    __syncthreads();
+    if (t == 0 && j > 0 && j - 1 + stages < n) fill(j - 1 + stages, st == 0 ? stages - 1 : st - 1);      // the stage of the row before
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint64_t v = 0;
+#pragma unroll
+      for (int q = 0; q < kWarps / 4; ++q) {
+        if (q == 2 && blockDim.x <= 256) break;
+        const float4 f = *reinterpret_cast<const float4*>(&red[j & 1][i][4 * q]);
+        v = fadd2(v, fadd2(pack_f2(f.x, f.y), pack_f2(f.z, f.w)));
+      }
+      m[i] = unpack_f2(v).x + unpack_f2(v).y;
+    }
+    const float c0 = -rho2 * (rho2 * (rho2 * m[0] * a.inv_cols));
+    const float tf = a.v.b * rho1;
+    float c1 = 0.0f;
+    if constexpr (POST) c1 = -rho1 * (rho1 * (tf * fmaf(c0, m[2], m[1]) * a.inv_cols));
+    if (on) {
+      F8 s[2], x[2];
+      if (KEPT) {
+        lds16_e4m3(base + off_s + c, ss, s);
+        lds16_e4m3(base + off_x + c, sx, x);
+      } else {
+        lds16<TS>(base + off_s + c * (uint32_t)sizeof(TS), s);
+        lds16<TA>(base + off_x + c * (uint32_t)sizeof(TA), x);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[h].p[i] = fmadd2(s[h].p[i], pack_f2(c0, c0), e[h].p[i]);
+      if (a.dr) store16(row_ptr<TS>(a.dr, a.lddr, r) + c, scale8(e[0], a.v.a), scale8(e[1], a.v.a));
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t bd = fmul2(e[h].p[i], pack_f2(tf, tf));
+          accT[h].p[i] = fmadd2(bd, x[h].p[i], accT[h].p[i]);
+          e[h].p[i] = POST ? fmadd2(bd, w[h].p[i], fmul2(x[h].p[i], pack_f2(c1, c1))) : fmul2(bd, w[h].p[i]);
+        }
+      if (a.dx) store16(row_ptr<TA>(a.dx, a.lddx, r) + c, e[0], e[1]);
+    }
+    if (last && a.many) {
+      flush(gate_row, gate_row == worker);
+      gate_row += workers;
+      if (j + 1 < n) {
+        left = min(span, rows - row);
+        load_w(gate_row_of(a.v, gate_row));
+      }
+    }
+    if (++st == stages) {
+      st = 0;
+      phase ^= 1u;
+    }
+  }
+  if (dead && t == 0) {      // copies still under way land before their memory is given up (waited for once more, bounded)
+    for (int j = max(0, n - stages); j < n; ++j) mbar_wait(&full[j % stages], (uint32_t)(j / stages) & 1u);
+  }
+  if (dead) __syncthreads();
+  griddep_launch_dependents();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (on && a.tpart && !a.many) store8<kStrided>(a.tpart + (int64_t)worker * a.cols, c + 8 * h, 1, a.cols, accT[h]);
+    if (on && a.ppart) store8<kStrided>(a.ppart + (int64_t)worker * a.cols, c + 8 * h, 1, a.cols, accP[h]);
+  }
+}
+
 // Joins the partial rows, 32 columns and 32 threads a column a block, in a
 // fixed order.  blockIdx.y 0: dg2 = sum of ppart.  1: dg1 and dgate from tpart:
 // with one item a worker (gate rows x parts partial T), dgate_k = g1 T_k and
@@ -666,7 +918,11 @@ struct Fwd {
 };
 template <typename TA, typename TS, int LAY>
 struct Bwd {
-  static const void* ptr() { return (const void*)&k_sandwich_bwd<TA, TS, LAY>; }
+  static const void* ptr() { return (const void*)&k_sandwich_bwd<TA, TS, LAY, kBwdThreads>; }
+};
+template <typename TA, typename TS, int LAY>
+struct BwdFew {
+  static const void* ptr() { return (const void*)&k_sandwich_bwd<TA, TS, LAY, kBwdFew>; }
 };
 
 // The staged form: wide units a thread, registers.
@@ -674,6 +930,11 @@ constexpr int kFwdRegs1 = 80, kFwdRegs2 = 128;
 template <typename TA, typename TS>
 const void* fwd_ring(int c) {
   return c == 1 ? (const void*)&k_sandwich_fwd_ring<TA, TS, 1, kFwdRegs1> : (const void*)&k_sandwich_fwd_ring<TA, TS, 2, kFwdRegs2>;
+}
+template <typename TA, typename TS>
+const void* bwd_ring(bool kept, bool post) {
+  return kept ? (post ? (const void*)&k_sandwich_bwd_ring<TA, TS, true, true> : (const void*)&k_sandwich_bwd_ring<TA, TS, true, false>)
+              : (post ? (const void*)&k_sandwich_bwd_ring<TA, TS, false, true> : (const void*)&k_sandwich_bwd_ring<TA, TS, false, false>);
 }
 constexpr size_t kSmemPerSm = 224 << 10, kSmemBlock = 2 << 10;      // a block's static and reserved shared memory
 constexpr int kRingMinCols = 1024;
@@ -917,6 +1178,20 @@ sf_status sf_sandwich_norm_backward(const sf_sandwich* p, const sf_matrix* dh, c
   const bool units = on_units(dh) && on_units(dsum) && on_units(x) && on_units(sum) && on_units(dresidual) && on_units(dx) &&
                      on_units(x8) && on_units(sum8) && on_units(gate) && on_units(dgate) && on_units(a.v.g_post, gain_dtype) &&
                      on_units(a.v.g_pre, gain_dtype);
+  // the staged form: as many blocks an SM as registers and three stages (of long rows two) allow
+  auto local = [](const sf_matrix* m) { return !m || on_current_device(m->data); };
+  const bool kept = x8 && sum8;
+  const size_t stage = (size_t)cols * (dtype_bytes(ta) + (dsum ? dtype_bytes(ts) : 0) + (kept ? 2 : dtype_bytes(ta) + dtype_bytes(ts)));
+  int ring_threads = 0, ring_blocks = 0, ring_stages = 0;
+  if (units && dh && (kept || (x && sum)) && cols % 16 == 0 && cols >= kRingMinCols && cols <= 16 * kBwdRingThreads && rows >= 2 * sm_count() &&
+      rows < (1 << 29) && on_wide(dh) && on_wide(dsum) && on_wide(x) && on_wide(sum) && on_wide(x8) && on_wide(sum8) && on_wide(dresidual) &&
+      on_wide(dx) && local(dh) && local(dsum) && local(x) && local(sum) && (!kept || (local(&x8->values) && local(&sum8->values)))) {
+    ring_threads = (int)ceil_div<int64_t>(cols / 16, 32) * 32;
+    ring_blocks = 65536 / (kBwdRingRegs * ring_threads);
+    while (ring_blocks > 1 && kSmemPerSm / ring_blocks < kSmemBlock + 3 * stage) --ring_blocks;
+    ring_stages = (int)std::min<size_t>(kMaxStages, (kSmemPerSm / ring_blocks - kSmemBlock) / stage);
+  }
+  const bool staged = ring_stages >= 2;
   const int64_t n = ceil_div<int64_t>(cols, 8);
   const int64_t t = ceil_div<int64_t>(n, rows < 2 * sm_count() && n <= kBwdThreads ? 1 : kBwdK);
   if (t > 64) {
@@ -928,11 +1203,12 @@ sf_status sf_sandwich_norm_backward(const sf_sandwich* p, const sf_matrix* dh, c
     a.tpr = w;
     a.rpb = 128 / w;
   }
+  if (staged) a.tpr = ring_threads, a.rpb = 1;
   const int threads = a.tpr * a.rpb;
   // items: gate rows (without a gate one, all rows) in parts
   a.span = gate ? a.v.span : std::max<int64_t>(1, rows);
   const int64_t gate_rows = gate ? gate->rows : 1;
-  const int64_t most = std::min<int64_t>(max_workers(cols), (int64_t)sm_count() * std::max(1, 512 / threads) * a.rpb);
+  const int64_t most = std::min<int64_t>(max_workers(cols), (int64_t)sm_count() * (staged ? ring_blocks : std::max(1, 512 / threads)) * a.rpb);
   a.many = gate_rows > most;
   a.parts = !rows || !gate_rows ? 0 : a.many ? 1 : (int32_t)std::min(most / gate_rows, rows / gate_rows);
   a.items = gate_rows * a.parts;
@@ -945,9 +1221,17 @@ sf_status sf_sandwich_norm_backward(const sf_sandwich* p, const sf_matrix* dh, c
     if (a.many) a.dgate = dgate->data, a.lddgate = dgate->ld;
   }
   cudaStream_t st = as_stream(stream);
-  if (rows) {
+  if (rows && staged) {
+    using B = __nv_bfloat16;
+    const bool post = a.v.g_post != nullptr;
+    const void* kernel = ta == SF_BF16 ? (ts == SF_BF16 ? bwd_ring<B, B>(kept, post) : bwd_ring<B, float>(kept, post))
+                                       : (ts == SF_BF16 ? bwd_ring<float, B>(kept, post) : bwd_ring<float, float>(kept, post));
+    SF_TRY(allow_dynamic_smem(kernel, stage * ring_stages));
+    void* args[] = {&a, &ring_stages};
+    SF_CUDA_TRY(cudaLaunchKernel(kernel, dim3((unsigned)a.workers), dim3(threads), args, stage * ring_stages, st), "launch k_sandwich_bwd_ring");
+  } else if (rows) {
     void* args[] = {&a};
-    SF_CUDA_TRY(cudaLaunchKernel(pick_kernel<Bwd>(ta, ts, units ? kUnits : kStrided), dim3((unsigned)ceil_div<int64_t>(a.workers, a.rpb)),
+    SF_CUDA_TRY(cudaLaunchKernel(threads <= kBwdFew ? pick_kernel<BwdFew>(ta, ts, units ? kUnits : kStrided) : pick_kernel<Bwd>(ta, ts, units ? kUnits : kStrided), dim3((unsigned)ceil_div<int64_t>(a.workers, a.rpb)),
                                  dim3(threads), args, 0, st),
                 "launch k_sandwich_bwd");
   }
