@@ -9,7 +9,11 @@
 namespace sf {
 namespace {
 
-constexpr int kK = 4;               // steps a thread holds in registers
+// Steps a thread holds in registers; of narrow accesses one, whose eight loads
+// an operand keep memory busy with twice the threads (16384 x 4095 bf16: stored
+// in 165 us with four steps).
+template <int LAY>
+constexpr int kK = LAY == kUnits ? 4 : 1;
 constexpr int kMaxThreads = 512;
 
 struct CkArgs {
@@ -35,15 +39,15 @@ __global__ void __launch_bounds__(kMaxThreads) k_checkpoint_store(const CkArgs a
   const int64_t row = (int64_t)blockIdx.x * a.rpb + lane_row;
   const bool on = row < a.rows;
   const Lane l = lane_of<LAY>(t, tpr);
-  const int64_t seg = (int64_t)tpr * kK * 8;
+  const int64_t seg = (int64_t)tpr * kK<LAY> * 8;
   const T* x = row_ptr<T>(a.x, a.ldx, on ? row : 0);
   const bool one = a.ck.group_log2 == 0;
   auto left = [&](int64_t s) { return on ? (int)min(a.cols - s * seg, seg) : 0; };      // columns of segment s
   uint32_t code = 1;
-  Unit<T> v[kK];
+  Unit<T> v[kK<LAY>];
   auto load = [&](int64_t s, int n) {
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
+    for (int k = 0; k < kK<LAY>; ++k) {
       v[k] = Unit<T>{};
       if (l.c0(k) < n) load_raw<LAY>(x + s * seg, l.c0(k), l.dj, n, v[k]);
     }
@@ -53,7 +57,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_checkpoint_store(const CkArgs a
     for (int64_t s = 0; s < a.steps; ++s) {
       load(s, left(s));
 #pragma unroll
-      for (int k = 0; k < kK; ++k) top[0] = fmaxf(top[0], top8_finite(unpack(v[k])));
+      for (int k = 0; k < kK<LAY>; ++k) top[0] = fmaxf(top[0], top8_finite(unpack(v[k])));
     }
     row_reduce_n<1, 0>(top, tpr, red);
     code = e8m0_of(top[0]);
@@ -66,7 +70,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_checkpoint_store(const CkArgs a
     ck.q += s * seg;
     if (!one) ck.s8 += (s * seg) >> ck.group_log2;
 #pragma unroll
-    for (int k = 0; k < kK; ++k) ck_store8<LAY>(ck, row, l.c0(k), l.dj, n, unpack(v[k]), code);
+    for (int k = 0; k < kK<LAY>; ++k) ck_store8<LAY>(ck, row, l.c0(k), l.dj, n, unpack(v[k]), code);
   }
 }
 
@@ -76,7 +80,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_checkpoint_load(const CkArgs a)
   const int64_t row = (int64_t)blockIdx.x * a.rpb + lane_row;
   if (row >= a.rows) return;
   const Lane l = lane_of<LAY>(t, tpr);
-  const int64_t seg = (int64_t)tpr * kK * 8;
+  const int64_t seg = (int64_t)tpr * kK<LAY> * 8;
   const float f = a.row_factor ? a.row_factor[row] : 1.0f;
   const uint64_t f2 = pack_f2(f, f);
   for (int64_t s = 0; s < a.steps; ++s) {
@@ -86,12 +90,12 @@ __global__ void __launch_bounds__(kMaxThreads) k_checkpoint_load(const CkArgs a)
     const int64_t at = ck.group_log2 ? (s * seg) >> ck.group_log2 : 0;
     if (ck.s8) ck.s8 += at;
     else ck.s32 += at;
-    F8 v[kK];
+    F8 v[kK<LAY>];
 #pragma unroll
-    for (int k = 0; k < kK; ++k)
+    for (int k = 0; k < kK<LAY>; ++k)
       if (l.c0(k) < n) v[k] = load8<LAY>(ck, row, l.c0(k), l.dj, n);
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
+    for (int k = 0; k < kK<LAY>; ++k) {
       if (l.c0(k) >= n) continue;
       if (a.row_factor) {
 #pragma unroll
@@ -139,7 +143,7 @@ __global__ void __launch_bounds__(kWideThreads) k_checkpoint_store_wide(const Ck
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int64_t r = row + i * step;
-    ck_store16(a.ck, r, c, r < a.rows ? (int)a.cols : 0, v[i].half(0), v[i].half(1), v[i].top(), 0);
+    ck_store16(a.ck, r, c, r < a.rows ? (int)a.cols : 0, v[i].half(0), v[i].half(1), v[i].top(), 0, true);
   }
 }
 
@@ -188,14 +192,15 @@ __global__ void __launch_bounds__(kWideThreads) k_checkpoint_load_wide(const CkA
       }
       o[h] = v;
     }
-    store16(row_ptr<T>(a.y, a.ldx, r) + c, o[0], o[1]);
+    store16(row_ptr<T>(a.y, a.ldx, r) + c, o[0], o[1], true);
   }
 }
 
 // Threads a row: a power of two up to 64 (at least 16, a group of 128 columns), or whole warps.
-void pick_shape(CkArgs& a) {
+void pick_shape(CkArgs& a, Lay lay) {
   const int64_t units = ceil_div<int64_t>(a.cols, 8);
-  const int64_t per = a.rows < 2 * sm_count() ? 1 : kK;
+  const int held = lay == kUnits ? kK<kUnits> : kK<kStrided>;
+  const int64_t per = a.rows < 2 * sm_count() ? 1 : held;
   const int64_t t = std::min<int64_t>(ceil_div<int64_t>(units, per), kMaxThreads);
   if (t > 64) {
     a.tpr = (int32_t)ceil_div<int64_t>(t, 32) * 32;
@@ -206,7 +211,7 @@ void pick_shape(CkArgs& a) {
     a.tpr = p;
     a.rpb = 128 / p;
   }
-  a.steps = (int32_t)ceil_div<int64_t>(units, (int64_t)a.tpr * kK);
+  a.steps = (int32_t)ceil_div<int64_t>(units, (int64_t)a.tpr * held);
 }
 
 template <template <typename, int> class K>
@@ -273,9 +278,9 @@ sf_status checkpoint_load(const sf_checkpoint* c, const float* row_factor, const
   if (on_wide(y) && on_wide(c) && (!gain || on_units(gain, gain_dtype)))
     return launch_wide(y->dtype == SF_BF16 ? (const void*)&k_checkpoint_load_wide<__nv_bfloat16> : (const void*)&k_checkpoint_load_wide<float>, a, 4, stream,
                        "launch k_checkpoint_load_wide");
-  pick_shape(a);
-  const bool units = on_units(y) && on_units(c) && (!gain || on_units(gain, gain_dtype));
-  return launch(pick_kernel<Load>(y->dtype, units ? kUnits : kStrided), a, stream, "launch k_checkpoint_load");
+  const Lay lay = on_units(y) && on_units(c) && (!gain || on_units(gain, gain_dtype)) ? kUnits : kStrided;
+  pick_shape(a, lay);
+  return launch(pick_kernel<Load>(y->dtype, lay), a, stream, "launch k_checkpoint_load");
 }
 
 }  // namespace sf
@@ -298,8 +303,9 @@ sf_status sf_checkpoint_store(const sf_matrix* x, const sf_checkpoint* out, void
   if (out->group && on_wide(x) && on_wide(out))
     return launch_wide(x->dtype == SF_BF16 ? (const void*)&k_checkpoint_store_wide<__nv_bfloat16> : (const void*)&k_checkpoint_store_wide<float>, a,
                        x->dtype == SF_BF16 ? 4 : 2, as_stream(stream), "launch k_checkpoint_store_wide");
-  pick_shape(a);
-  return launch(pick_kernel<Store>(x->dtype, on_units(x) && on_units(out) ? kUnits : kStrided), a, as_stream(stream), "launch k_checkpoint_store");
+  const Lay lay = on_units(x) && on_units(out) ? kUnits : kStrided;
+  pick_shape(a, lay);
+  return launch(pick_kernel<Store>(x->dtype, lay), a, as_stream(stream), "launch k_checkpoint_store");
 }
 
 sf_status sf_checkpoint_load(const sf_checkpoint* c, const float* row_factor, const void* gain, sf_dtype gain_dtype,

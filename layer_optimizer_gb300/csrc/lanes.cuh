@@ -386,8 +386,8 @@ struct Wide {
 };
 
 // Writes 16 columns of a checkpoint's row, as ck_store8 writes eight.  top: what
-// Wide::top() or top8() say of both halves.
-__device__ __forceinline__ void ck_store16(const Ck& k, int64_t row, int c, int cols, const F8& lo, const F8& hi, float top, uint32_t row_code) {
+// Wide::top() or top8() say of both halves.  wide: rows on wide units (else on units of eight).
+__device__ __forceinline__ void ck_store16(const Ck& k, int64_t row, int c, int cols, const F8& lo, const F8& hi, float top, uint32_t row_code, bool wide) {
   uint32_t code = row_code;
   bool infinite = !k.group_log2;
   if (k.group_log2) {
@@ -403,23 +403,73 @@ __device__ __forceinline__ void ck_store16(const Ck& k, int64_t row, int c, int 
   uint32_t w[2], x[2];
   if (infinite) e4m3_codes<true>(lo, inv, w), e4m3_codes<true>(hi, inv, x);
   else e4m3_codes<false>(lo, inv, w), e4m3_codes<false>(hi, inv, x);
-  asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(k.q + row * k.ld + c), "r"(w[0]), "r"(w[1]), "r"(x[0]), "r"(x[1]) : "memory");
+  uint8_t* p = k.q + row * k.ld + c;
+  if (wide) {
+    asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(x[0]), "r"(x[1]) : "memory");
+  } else {
+    asm volatile("st.global.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(w[0]), "r"(w[1]) : "memory");
+    asm volatile("st.global.v2.u32 [%0], {%1, %2};" ::"l"(p + 8), "r"(x[0]), "r"(x[1]) : "memory");
+  }
 }
 
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const F8& lo, const F8& hi) {
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const F8& lo, const F8& hi, bool wide) {
   Unit<__nv_bfloat16> a, b;
   pack(lo, a);
   pack(hi, b);
+  if (!wide) {
+    st_unit(p, a);
+    st_unit(p + 8, b);
+    return;
+  }
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.w[0]), "r"(a.w[1]), "r"(a.w[2]), "r"(a.w[3]), "r"(b.w[0]),
                "r"(b.w[1]), "r"(b.w[2]), "r"(b.w[3])
                : "memory");
 }
-__device__ __forceinline__ void store16(float* p, const F8& lo, const F8& hi) {
+__device__ __forceinline__ void store16(float* p, const F8& lo, const F8& hi, bool) {
   Unit<float> a, b;
   pack(lo, a);
   pack(hi, b);
   st_unit(p, a);
   st_unit(p + 8, b);
+}
+
+// 16 columns of a thread in the second lay: lane, lane + 32, .. of a warp's 512.
+__device__ __forceinline__ void ck_store16_strided(const Ck& k, int64_t row, int c0, int cols, const F8 (&v)[2], uint32_t row_code) {
+  uint8_t* p = k.q + row * k.ld;
+  const int per = k.group_log2 ? 1 << (k.group_log2 - 5) : 16;      // a group's blocks of 32 columns
+  uint32_t code = row_code;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {      // four blocks at a time: a group, or several
+    float top[4];
+    uint32_t codes[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 x = unpack_f2(v[b >> 1].p[2 * (b & 1) + (e >> 1)]);
+      const float a = fabsf(e & 1 ? x.y : x.x);
+      top[e] = a <= kLargest ? a : 0.0f;
+      codes[e] = row_code;
+    }
+    if (k.group_log2) {
+      if (per > 1) top[0] = fmaxf(top[0], top[1]), top[2] = fmaxf(top[2], top[3]);
+      if (per > 2) top[0] = fmaxf(top[0], top[2]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (e % per == 0) {
+          code = e8m0_of(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top[e]))));      // magnitudes order as their bits
+          const int c = c0 + 32 * (4 * b + e);
+          if (c < cols && (threadIdx.x & 31) == 0) k.s8[row * k.n_groups + (c >> k.group_log2)] = (uint8_t)code;
+        }
+        codes[e] = code;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const uint32_t two = e4m3_pair<true>(v[b >> 1].p[2 * (b & 1) + (e >> 1)], pack_f2(e8m0_inverse(codes[e]), e8m0_inverse(codes[e + 1])));
+      const int c = c0 + 32 * (4 * b + e);
+      if (c < cols) p[c] = (uint8_t)two;
+      if (c + 32 < cols) p[c + 32] = (uint8_t)(two >> 8);
+    }
+  }
 }
 
 // Whether each row of `m` (null passes) starts on a wide unit, and ends on one.
@@ -429,6 +479,8 @@ inline bool on_wide(const sf_matrix* m) {
   return m->cols % 16 == 0 && reinterpret_cast<uintptr_t>(m->data) % unit == 0 && (m->rows == 1 || m->ld % 16 == 0);
 }
 inline bool on_wide(const sf_checkpoint* c) { return !c || on_wide(&c->values); }
+// Whether bulk copies can bring its rows: 16-byte aligned, in this device's own memory.
+inline bool on_bulk(const sf_matrix* m) { return !m || (reinterpret_cast<uintptr_t>(m->data) % 16 == 0 && on_current_device(m->data)); }
 
 // The sums (or, from index SUMS on, the maxima) of N values over the tpr
 // threads of a row, in a fixed order: lanes by a butterfly, then the row's

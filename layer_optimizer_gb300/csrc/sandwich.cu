@@ -36,6 +36,7 @@ struct FwdArgs {
   Ck x8, s8;
   int64_t ldx, ldr, lds, ldh, rows;
   int32_t cols, tpr, rpb, steps;
+  int32_t wide;        // staged form: rows on wide units, not on units of eight only
   float eps, inv_cols;
   Vectors v;
 };
@@ -222,8 +223,87 @@ struct LdsWide<float> : Wide<float> {
   }
 };
 
+// A row in shared memory: the 16-byte words that hold any of it, so that its
+// first column lies as far into the first word as in memory.  Of the matrix's
+// last row, past which memory may end, the last word's bytes come by ordinary
+// loads.
+__device__ __forceinline__ uint32_t lead_of(const void* row) { return (uint32_t)reinterpret_cast<uintptr_t>(row) & 15u; }
+__host__ __device__ __forceinline__ uint32_t slot_bytes(int64_t cols, uint32_t size) { return (uint32_t)(cols * size + 30) & ~15u; }
+struct Bring {
+  const void* row;
+  uint32_t bytes;      // of the row
+  bool last;
+  __device__ __forceinline__ uint32_t copied() const { return (lead_of(row) + bytes + (last ? 0u : 15u)) & ~15u; }
+  __device__ __forceinline__ void rest(unsigned char* to) const {      // before the arrival
+    const unsigned char* from = static_cast<const unsigned char*>(row) - lead_of(row);
+    for (uint32_t i = copied(); i < lead_of(row) + bytes; ++i) to[i] = from[i];
+  }
+  __device__ __forceinline__ void copy(unsigned char* to, uint64_t* bar) const {
+    if (copied()) bulk_load(to, static_cast<const unsigned char*>(row) - lead_of(row), copied(), bar);
+  }
+};
+// Brings N rows' worth of operands into their slots, by one thread.
+template <int N>
+__device__ __forceinline__ void bring_rows(const Bring (&b)[N], unsigned char* const (&to)[N], uint64_t* bar) {
+  uint32_t bytes = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (b[i].bytes) {
+      bytes += b[i].copied();
+      b[i].rest(to[i]);
+    }
+  mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (b[i].bytes) b[i].copy(to[i], bar);
+}
+
+// 16 columns of a thread in either lay.  c0: its first; strided ones are 32 apart.
+template <int LAY>
+__device__ __forceinline__ int first16(int t, int T, int k) {
+  return LAY == kUnits ? 16 * (t + k * T) : ((t >> 5) + k * (T >> 5)) * 512 + (t & 31);
+}
+__device__ __forceinline__ float lds_value(uint32_t p, __nv_bfloat16) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p));
+  return __uint_as_float((uint32_t)v << 16);
+}
+__device__ __forceinline__ float lds_value(uint32_t p, float) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(p));
+  return v;
+}
+// From shared memory, at the address of column 0 (c0 below cols; strided columns past it read as zero).
+template <typename T, int LAY>
+__device__ __forceinline__ void lds16(uint32_t p, int c0, int cols, F8 (&v)[2]) {
+  if constexpr (LAY == kUnits) {
+    const LdsWide<T> u(p + c0 * (uint32_t)sizeof(T));
+    v[0] = u.half(0), v[1] = u.half(1);
+  } else {
+    float x[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = c0 + 32 * e < cols ? lds_value(p + (c0 + 32 * e) * (uint32_t)sizeof(T), T()) : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e >> 2].p[e & 3] = pack_f2(x[2 * e], x[2 * e + 1]);
+  }
+}
+template <typename T, int LAY>
+__device__ __forceinline__ void put16(T* row, int c0, int cols, const F8& lo, const F8& hi, bool wide) {
+  if constexpr (LAY == kUnits) {
+    store16(row + c0, lo, hi, wide);
+  } else {
+    store8<kStrided>(row, c0, 32, cols, lo);
+    store8<kStrided>(row, c0 + 256, 32, cols, hi);
+  }
+}
+template <int LAY>
+__device__ __forceinline__ void vec16(const void* p, int fp32, int c0, int cols, float add, F8 (&v)[2]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) v[h] = load_vec<LAY>(p, fp32, c0 + (LAY == kUnits ? 8 : 256) * h, LAY == kUnits ? 1 : 32, cols, add);
+}
+
 // C: wide units a thread.  With one of them g2 stays in registers too.
-template <typename TA, typename TS, int C, int REGS>
+template <typename TA, typename TS, int LAY, int C, int REGS>
 __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int stages) {
   __shared__ __align__(16) float red[2][2][2][kRed];      // [row mod 2][which sum][sums, maxima]
   __shared__ float redx[kRed];
@@ -231,14 +311,16 @@ __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int
   extern __shared__ __align__(128) unsigned char ring[];
   const int t = threadIdx.x, T = blockDim.x;
   for (int i = t; i < 8 * kRed; i += T) (&red[0][0][0][0])[i] = 0.0f;
-  const uint32_t row_x = (uint32_t)a.cols * sizeof(TA), stage_bytes = row_x + (a.r ? (uint32_t)a.cols * sizeof(TS) : 0u);
+  const uint32_t row_x = slot_bytes(a.cols, sizeof(TA)), stage_bytes = row_x + (a.r ? slot_bytes(a.cols, sizeof(TS)) : 0u);
   const uint32_t ring0 = smem_u32(ring);
   const int64_t first = a.rows * blockIdx.x / gridDim.x, end = a.rows * (blockIdx.x + 1) / gridDim.x;
   auto fill = [&](int64_t row, int st) {      // by one thread
     unsigned char* at = ring + (size_t)st * stage_bytes;
-    mbar_arrive_expect_tx(&full[st], stage_bytes);
-    bulk_load(at, row_ptr<TA>(a.x, a.ldx, row), row_x, &full[st]);
-    if (a.r) bulk_load(at + row_x, row_ptr<TS>(a.r, a.ldr, row), stage_bytes - row_x, &full[st]);
+    const bool last = row == a.rows - 1;
+    const Bring b[2] = {{row_ptr<TA>(a.x, a.ldx, row), (uint32_t)a.cols * (uint32_t)sizeof(TA), last},
+                        {row_ptr<TS>(a.r, a.ldr, row), a.r ? (uint32_t)a.cols * (uint32_t)sizeof(TS) : 0u, last}};
+    unsigned char* const to[2] = {at, at + row_x};
+    bring_rows(b, to, &full[st]);
   };
   if (t == 0) {
     for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
@@ -249,11 +331,9 @@ __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int
   const bool post = a.v.g_post != nullptr;
   const bool x_row = a.x8.q && !a.x8.group_log2, s_row = a.s8.q && !a.s8.group_log2;
   F8 w[C][2], g2[2];
-  auto vec = [&](const void* p, int fp32, int c, float add, F8 (&v)[2]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) v[h] = load_vec<kUnits>(p, fp32, c + 8 * h, 1, a.cols, add);
-  };
-  if (C == 1 && a.h && 16 * t < a.cols) vec(a.v.g_pre, a.v.gain_fp32, 16 * t, a.v.offset, g2);
+  auto vec = [&](const void* p, int fp32, int c, float add, F8 (&v)[2]) { vec16<LAY>(p, fp32, c, a.cols, add, v); };
+  auto col = [&](int k) { return first16<LAY>(t, T, k); };
+  if (C == 1 && a.h && col(0) < a.cols) vec(a.v.g_pre, a.v.gain_fp32, col(0), a.v.offset, g2);
   int64_t gate_end = first;      // rows from here on take another gate row
   int64_t gate_at = a.v.gate ? first / a.v.span : 0;
   int st = 0, parity = 0;
@@ -264,7 +344,7 @@ __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int
       gate_end = a.v.gate ? (gate_at + 1) * a.v.span : end;
 #pragma unroll
       for (int k = 0; k < C; ++k) {
-        const int c = 16 * (t + k * T);
+        const int c = col(k);
         if (c >= a.cols) continue;
         const uint64_t b2 = pack_f2(a.v.b, a.v.b);
         w[k][0] = w[k][1] = F8{{b2, b2, b2, b2}};
@@ -281,20 +361,29 @@ __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int
       ++gate_at;
     }
     if (!dead) dead = !mbar_wait_u32(smem_u32(&full[st]), phase);
-    const uint32_t at = ring0 + (uint32_t)st * stage_bytes;
+    const uint32_t at = ring0 + (uint32_t)st * stage_bytes + (LAY == kUnits ? 0u : lead_of(row_ptr<TA>(a.x, a.ldx, row)));
+    const uint32_t at_r = ring0 + (uint32_t)st * stage_bytes + row_x + (LAY == kUnits ? 0u : lead_of(row_ptr<TS>(a.r, a.ldr, row)));
     float rho1 = 1.0f;
     if (post || a.x8.q) {
       float sum = 0.0f, top[1] = {0.0f};
 #pragma unroll
       for (int k = 0; k < C; ++k) {
-        const int c = 16 * (t + k * T);
-        const bool on = c < a.cols;      // (the others read the row's start and drop it)
-        const LdsWide<TA> x(at + (on ? c : 0) * (uint32_t)sizeof(TA));
-        const F8 lo = x.half(0), hi = x.half(1);
-        const float part = dot8(lo, lo) + dot8(hi, hi);
-        sum += on ? part : 0.0f;
-        if (x_row) top[0] = on ? fmaxf(top[0], top_or_inf(x.top())) : top[0];
-        else if (a.x8.q) ck_store16(a.x8, row, c, a.cols, lo, hi, on ? x.top() : 0.0f, 1);
+        const int c = col(k);
+        if constexpr (LAY == kUnits) {
+          const bool on = c < a.cols;      // (the others read the row's start and drop it)
+          const LdsWide<TA> u(at + (on ? c : 0) * (uint32_t)sizeof(TA));
+          const F8 lo = u.half(0), hi = u.half(1);
+          const float part = dot8(lo, lo) + dot8(hi, hi);
+          sum += on ? part : 0.0f;
+          if (x_row) top[0] = on ? fmaxf(top[0], top_or_inf(u.top())) : top[0];
+          else if (a.x8.q) ck_store16(a.x8, row, c, a.cols, lo, hi, on ? u.top() : 0.0f, 1, a.wide);
+        } else {
+          F8 x[2];
+          lds16<TA, LAY>(at, c, a.cols, x);
+          sum += dot8(x[0], x[0]) + dot8(x[1], x[1]);
+          if (x_row) top[0] = fmaxf(top[0], fmaxf(top8(x[0]), top8(x[1])));
+          else if (a.x8.q) ck_store16_strided(a.x8, row, c, a.cols, x, 1);
+        }
       }
       if (post || x_row) sum = block_sum(sum, x_row ? top : nullptr, red[parity][0]);
       if (post) {
@@ -306,10 +395,11 @@ __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int
           top[0] = 0.0f;
 #pragma unroll
           for (int k = 0; k < C; ++k) {
-            const int c = 16 * (t + k * T);
+            const int c = col(k);
             if (c >= a.cols) continue;
-            const LdsWide<TA> x(at + c * (uint32_t)sizeof(TA));
-            top[0] = fmaxf(top[0], fmaxf(top8_finite(x.half(0)), top8_finite(x.half(1))));
+            F8 x[2];
+            lds16<TA, LAY>(at, c, a.cols, x);
+            top[0] = fmaxf(top[0], fmaxf(top8_finite(x[0]), top8_finite(x[1])));
           }
           row_reduce_n<1, 0>(top, T, redx);
         }
@@ -317,10 +407,12 @@ __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int
         if (t == 0) a.x8.s8[row] = (uint8_t)code;
 #pragma unroll
         for (int k = 0; k < C; ++k) {
-          const int c = 16 * (t + k * T);
+          const int c = col(k);
           if (c >= a.cols) continue;
-          const LdsWide<TA> x(at + c * (uint32_t)sizeof(TA));
-          ck_store16(a.x8, row, c, a.cols, x.half(0), x.half(1), 0.0f, code);
+          F8 x[2];
+          lds16<TA, LAY>(at, c, a.cols, x);
+          if (LAY == kUnits) ck_store16(a.x8, row, c, a.cols, x[0], x[1], 0.0f, code, a.wide);
+          else ck_store16_strided(a.x8, row, c, a.cols, x, code);
         }
       }
     }
@@ -328,26 +420,26 @@ __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int
     float sum = 0.0f, top[1] = {0.0f};
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-      const int c = 16 * (t + k * T);
+      const int c = col(k);
       s[k][0] = s[k][1] = zero8();
       if (c < a.cols) {
-        const LdsWide<TA> x(at + c * (uint32_t)sizeof(TA));
+        F8 v[2];
+        lds16<TA, LAY>(at, c, a.cols, v);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) s[k][h] = mul8(scale8(x.half(h), rho1), w[k][h]);
+        for (int h = 0; h < 2; ++h) s[k][h] = mul8(scale8(v[h], rho1), w[k][h]);
         if (a.r) {
-          const LdsWide<TS> r(at + row_x + c * (uint32_t)sizeof(TS));
+          lds16<TS, LAY>(at_r, c, a.cols, v);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const F8 v = r.half(h);
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[k][h].p[i] = fmadd2(v.p[i], pack_f2(a.v.a, a.v.a), s[k][h].p[i]);
-          }
+            for (int i = 0; i < 4; ++i) s[k][h].p[i] = fmadd2(v[h].p[i], pack_f2(a.v.a, a.v.a), s[k][h].p[i]);
         }
-        if (a.s) store16(row_ptr<TS>(a.s, a.lds, row) + c, s[k][0], s[k][1]);
+        if (a.s) put16<TS, LAY>(row_ptr<TS>(a.s, a.lds, row), c, a.cols, s[k][0], s[k][1], a.wide);
       }
       sum += dot8(s[k][0], s[k][0]) + dot8(s[k][1], s[k][1]);
       if (s_row) top[0] = fmaxf(top[0], fmaxf(top8(s[k][0]), top8(s[k][1])));
-      else if (a.s8.q) ck_store16(a.s8, row, c, a.cols, s[k][0], s[k][1], fmaxf(top8(s[k][0]), top8(s[k][1])), 1);
+      else if (a.s8.q && LAY == kUnits) ck_store16(a.s8, row, c, a.cols, s[k][0], s[k][1], fmaxf(top8(s[k][0]), top8(s[k][1])), 1, a.wide);
+      else if (a.s8.q) ck_store16_strided(a.s8, row, c, a.cols, s[k], 1);
     }
     // (a barrier in any case: the row has been read out of its stage)
     const float rho2 = rsqrtf(fmaf(block_sum(sum, s_row ? top : nullptr, red[parity][1]), a.inv_cols, a.eps));
@@ -366,15 +458,18 @@ __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int
       const uint32_t code = e8m0_of(top[0]);
       if (t == 0) a.s8.s8[row] = (uint8_t)code;
 #pragma unroll
-      for (int k = 0; k < C; ++k) ck_store16(a.s8, row, 16 * (t + k * T), a.cols, s[k][0], s[k][1], 0.0f, code);
+      for (int k = 0; k < C; ++k) {
+        if (LAY == kUnits) ck_store16(a.s8, row, col(k), a.cols, s[k][0], s[k][1], 0.0f, code, a.wide);
+        else ck_store16_strided(a.s8, row, col(k), a.cols, s[k], code);
+      }
     }
     if (a.h) {
 #pragma unroll
       for (int k = 0; k < C; ++k) {
-        const int c = 16 * (t + k * T);
+        const int c = col(k);
         if (c >= a.cols) continue;
         if (C > 1) vec(a.v.g_pre, a.v.gain_fp32, c, a.v.offset, g2);
-        store16(row_ptr<TA>(a.h, a.ldh, row) + c, mul8(scale8(s[k][0], rho2), g2[0]), mul8(scale8(s[k][1], rho2), g2[1]));
+        put16<TA, LAY>(row_ptr<TA>(a.h, a.ldh, row), c, a.cols, mul8(scale8(s[k][0], rho2), g2[0]), mul8(scale8(s[k][1], rho2), g2[1]), a.wide);
       }
     }
     if (++st == stages) {
@@ -427,6 +522,7 @@ struct BwdArgs {
   int32_t many;           // several items a worker
   int32_t dgate_fp32;
   int32_t cols, tpr, rpb;
+  int32_t wide;           // staged form: rows on wide units, not on units of eight only
   float inv_cols;
   Vectors v;
 };
@@ -570,15 +666,16 @@ __global__ void __launch_bounds__(T, T == kBwdFew ? 2 : 1) k_sandwich_bwd(const 
 // between); past that barrier every thread is also done with the row before,
 // whose stage is filled again.  For calls with dh, dsum or none, and x and s both in
 // full or both as checkpoints (KEPT).
-template <typename T>
-__device__ __forceinline__ void lds16(uint32_t p, F8 (&v)[2]) {
-  const LdsWide<T> u(p);
-  v[0] = u.half(0), v[1] = u.half(1);
-}
-// 16 e4m3 values from shared memory, times their scale.
-__device__ __forceinline__ void lds16_e4m3(uint32_t p, float scale, F8 (&v)[2]) {
-  const int4 q = lds_i4(p);
-  const uint32_t w[4] = {(uint32_t)q.x, (uint32_t)q.y, (uint32_t)q.z, (uint32_t)q.w};
+// 16 e4m3 values from shared memory, times their scale; wide: on 16 bytes (else on eight).
+__device__ __forceinline__ void lds16_e4m3(uint32_t p, float scale, bool wide, F8 (&v)[2]) {
+  uint32_t w[4];
+  if (wide) {
+    const int4 q = lds_i4(p);
+    w[0] = (uint32_t)q.x, w[1] = (uint32_t)q.y, w[2] = (uint32_t)q.z, w[3] = (uint32_t)q.w;
+  } else {
+    const uint2 a = lds_u2(p), b = lds_u2(p + 8);
+    w[0] = a.x, w[1] = a.y, w[2] = b.x, w[3] = b.y;
+  }
   const uint64_t s2 = pack_f2(scale, scale);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -586,21 +683,36 @@ __device__ __forceinline__ void lds16_e4m3(uint32_t p, float scale, F8 (&v)[2]) 
     v[i >> 2].p[i & 3] = fmul2(pack_f2(x.x, x.y), s2);
   }
 }
+// In the second lay, the row's scales from shared memory too.
+__device__ __forceinline__ void lds16_e4m3_strided(uint32_t p, int c0, int cols, const float* scales, int group_log2, F8 (&v)[2]) {
+  const int shift = group_log2 ? group_log2 : 31;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = c0 + 64 * i, d = c + 32;
+    uint16_t q0 = 0, q1 = 0;
+    if (c < cols) asm volatile("{.reg .b32 t; ld.shared.u8 t, [%1]; cvt.u16.u32 %0, t;}" : "=h"(q0) : "r"(p + c));
+    if (d < cols) asm volatile("{.reg .b32 t; ld.shared.u8 t, [%1]; cvt.u16.u32 %0, t;}" : "=h"(q1) : "r"(p + d));
+    const float2 x = e4m3x2_value((uint32_t)q0 | (uint32_t)q1 << 8);
+    v[i >> 2].p[i & 3] = fmul2(pack_f2(x.x, x.y), pack_f2(c < cols ? scales[c >> shift] : 0.0f, d < cols ? scales[d >> shift] : 0.0f));
+  }
+}
 
 constexpr int kBwdRingThreads = 512, kBwdRingRegs = 128;
 
-template <typename TA, typename TS, bool KEPT, bool POST>
+template <typename TA, typename TS, int LAY, bool KEPT, bool POST>
 __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const BwdArgs a, const int stages) {
   constexpr int kWarps = kBwdRingThreads / 32, N = POST ? 3 : 1;
   __shared__ __align__(16) float red[2][N][kWarps];
   __shared__ __align__(8) uint64_t full[kMaxStages];
   extern __shared__ __align__(128) unsigned char ring[];
-  const int t = threadIdx.x, c = 16 * t;
+  // (KEPT, strided: the scales of three rows in turn, of x and of s)
+  __shared__ float scl[KEPT && LAY == kStrided ? 3 : 1][2][KEPT && LAY == kStrided ? 16 * kBwdRingThreads / 32 : 1];
+  const int t = threadIdx.x, c = first16<LAY>(t, blockDim.x, 0);
   const bool on = c < a.cols;
   for (int i = t; i < 2 * N * kWarps; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
-  const uint32_t size_a = (uint32_t)a.cols * sizeof(TA), size_s = (uint32_t)a.cols * sizeof(TS);
-  const uint32_t off_e = size_a, off_x = off_e + (a.dsum ? size_s : 0u), off_s = off_x + (KEPT ? (uint32_t)a.cols : size_a);
-  const uint32_t stage_bytes = off_s + (KEPT ? (uint32_t)a.cols : size_s);
+  const uint32_t slot_a = slot_bytes(a.cols, sizeof(TA)), slot_s = slot_bytes(a.cols, sizeof(TS)), slot_8 = slot_bytes(a.cols, 1);
+  const uint32_t off_e = slot_a, off_x = off_e + (a.dsum ? slot_s : 0u), off_s = off_x + (KEPT ? slot_8 : slot_a);
+  const uint32_t stage_bytes = off_s + (KEPT ? slot_8 : slot_s);
   const uint32_t ring0 = smem_u32(ring);
   // this worker's rows (n of them, below 2^29): the part of a gate row, or every workers-th gate row
   const int worker = blockIdx.x, workers = gridDim.x, span = (int)a.span, rows = (int)a.rows;
@@ -624,16 +736,14 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
   auto fill = [&](int j, int st) {      // by one thread
     const int64_t r = row_at(j);
     unsigned char* at = ring + (size_t)st * stage_bytes;
-    mbar_arrive_expect_tx(&full[st], stage_bytes);
-    bulk_load(at, row_ptr<TA>(a.dh, a.lddh, r), size_a, &full[st]);
-    if (a.dsum) bulk_load(at + off_e, row_ptr<TS>(a.dsum, a.lddsum, r), size_s, &full[st]);
-    if (KEPT) {
-      bulk_load(at + off_x, a.x8.q + r * a.x8.ld, (uint32_t)a.cols, &full[st]);
-      bulk_load(at + off_s, a.s8.q + r * a.s8.ld, (uint32_t)a.cols, &full[st]);
-    } else {
-      bulk_load(at + off_x, row_ptr<TA>(a.x, a.ldx, r), size_a, &full[st]);
-      bulk_load(at + off_s, row_ptr<TS>(a.s, a.lds, r), size_s, &full[st]);
-    }
+    const bool last = r == a.rows - 1;
+    const uint32_t size_a = (uint32_t)a.cols * (uint32_t)sizeof(TA), size_s = (uint32_t)a.cols * (uint32_t)sizeof(TS);
+    const Bring b[4] = {{row_ptr<TA>(a.dh, a.lddh, r), size_a, last},
+                        {row_ptr<TS>(a.dsum, a.lddsum, r), a.dsum ? size_s : 0u, last},
+                        {KEPT ? (const void*)(a.x8.q + r * a.x8.ld) : row_ptr<TA>(a.x, a.ldx, r), KEPT ? (uint32_t)a.cols : size_a, last},
+                        {KEPT ? (const void*)(a.s8.q + r * a.s8.ld) : row_ptr<TS>(a.s, a.lds, r), KEPT ? (uint32_t)a.cols : size_s, last}};
+    unsigned char* const to[4] = {at, at + off_e, at + off_x, at + off_s};
+    bring_rows(b, to, &full[st]);
   };
   if (t == 0) {
     for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
@@ -642,10 +752,8 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
   }
   __syncthreads();
   F8 accT[2] = {}, accP[2] = {}, w[2], g2[2];
-  auto vec = [&](const void* p, int fp32, float add, F8 (&v)[2]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) v[h] = load_vec<kUnits>(p, fp32, c + 8 * h, 1, a.cols, add);
-  };
+  auto vec = [&](const void* p, int fp32, float add, F8 (&v)[2]) { vec16<LAY>(p, fp32, c, a.cols, add, v); };
+  constexpr int kNext = LAY == kUnits ? 8 : 256, kApart = LAY == kUnits ? 1 : 32;      // of a thread's columns
   auto load_w = [&](const void* gate) {      // gate g1
     const uint64_t one = pack_f2(1.0f, 1.0f);
     w[0] = w[1] = F8{{one, one, one, one}};
@@ -663,19 +771,19 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
     const void* gate = gate_row_of(a.v, gate_row);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int ch = c + 8 * h;
+      const int ch = c + kNext * h;
       if (on && a.dgate) {
         F8 v = accT[h];
-        if (POST) v = mul8(v, load_vec<kUnits>(a.v.g_post, a.v.gain_fp32, ch, 1, a.cols, a.v.offset));
-        store_any<kUnits>(static_cast<char*>(a.dgate) + (int64_t)gate_row * a.lddgate * (a.dgate_fp32 ? 4 : 2), a.dgate_fp32, ch, 1, a.cols, v);
+        if (POST) v = mul8(v, load_vec<LAY>(a.v.g_post, a.v.gain_fp32, ch, kApart, a.cols, a.v.offset));
+        store_any<LAY>(static_cast<char*>(a.dgate) + (int64_t)gate_row * a.lddgate * (a.dgate_fp32 ? 4 : 2), a.dgate_fp32, ch, kApart, a.cols, v);
       }
       if (on && a.tpart) {      // this worker's own row, written and read by the same threads (on 16 bytes at least: no wide access)
         float* part = a.tpart + (int64_t)worker * a.cols;
-        F8 v = first ? zero8() : load8<kStrided>(part, ch, 1, a.cols);
-        const F8 g = load_vec<kUnits>(gate, a.v.gate_fp32, ch, 1, a.cols, 0.0f);
+        F8 v = first ? zero8() : load8<kStrided>(part, ch, kApart, a.cols);
+        const F8 g = load_vec<LAY>(gate, a.v.gate_fp32, ch, kApart, a.cols, 0.0f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v.p[i] = fmadd2(accT[h].p[i], g.p[i], v.p[i]);
-        store8<kStrided>(part, ch, 1, a.cols, v);
+        store8<kStrided>(part, ch, kApart, a.cols, v);
       }
       accT[h] = zero8();
     }
@@ -683,17 +791,33 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
   // a row's rhos and scales come one row ahead
   float rho1_next = 1.0f, rho2_next = 0.0f;
   uint32_t sx_next = 0, ss_next = 0;
+  // (strided: a thread brings one group's, for all)
   auto scale_raw = [&](const Ck& ck, int64_t r) {
-    const int64_t i = r * ck.n_groups + (ck.group_log2 && on ? c >> ck.group_log2 : 0);
+    const int64_t i = r * ck.n_groups + (LAY == kStrided ? min(t, ck.n_groups - 1) : ck.group_log2 && on ? c >> ck.group_log2 : 0);
     return ck.s8 ? (uint32_t)ck.s8[i] : __float_as_uint(ck.s32[i]);
   };
   auto scale_value = [](const Ck& ck, uint32_t raw) { return ck.s8 ? e8m0_value(raw) : __uint_as_float(raw); };
   auto prefetch = [&](int64_t r) {
     if (POST) rho1_next = a.rho1[r];
     rho2_next = a.rho2[r];
-    if (KEPT) sx_next = scale_raw(a.x8, r), ss_next = scale_raw(a.s8, r);
+    if (KEPT && LAY == kUnits) sx_next = scale_raw(a.x8, r), ss_next = scale_raw(a.s8, r);
   };
   if (n > 0) prefetch(row);
+  auto put_scales = [&](int j) {      // row j's, fetched before
+    if constexpr (KEPT && LAY == kStrided) {
+      if (t < a.x8.n_groups) scl[j % 3][0][t] = scale_value(a.x8, sx_next);
+      if (t < a.s8.n_groups) scl[j % 3][1][t] = scale_value(a.s8, ss_next);
+    }
+  };
+  auto fetch_scales = [&](int j) {
+    if (KEPT && LAY == kStrided && j < n) sx_next = scale_raw(a.x8, row_at(j)), ss_next = scale_raw(a.s8, row_at(j));
+  };
+  if constexpr (KEPT && LAY == kStrided) {
+    fetch_scales(0);
+    put_scales(0);
+    fetch_scales(1);
+    __syncthreads();
+  }
   int gate_row = a.many ? worker : worker / a.parts;
   load_w(a.v.gate ? gate_row_of(a.v, gate_row) : nullptr);
   int st = 0;
@@ -708,19 +832,29 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
     if (j + 1 < n) prefetch(row);
     if (!dead) dead = !mbar_wait_u32(smem_u32(&full[st]), phase);
     const uint32_t base = ring0 + (uint32_t)st * stage_bytes;
+    const uint32_t at_dh = base + (LAY == kUnits ? 0u : lead_of(row_ptr<TA>(a.dh, a.lddh, r)));
+    const uint32_t at_e = base + off_e + (LAY == kUnits ? 0u : lead_of(row_ptr<TS>(a.dsum, a.lddsum, r)));
+    const uint32_t at_x = base + off_x + (KEPT ? lead_of(a.x8.q + r * a.x8.ld) : LAY == kUnits ? 0u : lead_of(row_ptr<TA>(a.x, a.ldx, r)));
+    const uint32_t at_s = base + off_s + (KEPT ? lead_of(a.s8.q + r * a.s8.ld) : LAY == kUnits ? 0u : lead_of(row_ptr<TS>(a.s, a.lds, r)));
+    auto load_s = [&](F8 (&s)[2]) {
+      if constexpr (!KEPT) lds16<TS, LAY>(at_s, c, a.cols, s);
+      else if constexpr (LAY == kUnits) lds16_e4m3(at_s + c, ss, a.wide, s);
+      else lds16_e4m3_strided(at_s, c, a.cols, scl[j % 3][1], a.s8.group_log2, s);
+    };
+    auto load_x = [&](F8 (&x)[2]) {
+      if constexpr (!KEPT) lds16<TA, LAY>(at_x, c, a.cols, x);
+      else if constexpr (LAY == kUnits) lds16_e4m3(at_x + c, sx, a.wide, x);
+      else lds16_e4m3_strided(at_x, c, a.cols, scl[j % 3][0], a.x8.group_log2, x);
+    };
     const uint64_t rho2_2 = pack_f2(rho2, rho2);
     F8 e[2] = {};
     float m[N] = {};
     if (on) {
       F8 dn[2], s[2], x[2];
-      lds16<TA>(base + c * (uint32_t)sizeof(TA), dn);
-      if (a.dsum) lds16<TS>(base + off_e + c * (uint32_t)sizeof(TS), e);
-      if (KEPT) lds16_e4m3(base + off_s + c, ss, s);
-      else lds16<TS>(base + off_s + c * (uint32_t)sizeof(TS), s);
-      if (POST) {
-        if (KEPT) lds16_e4m3(base + off_x + c, sx, x);
-        else lds16<TA>(base + off_x + c * (uint32_t)sizeof(TA), x);
-      }
+      lds16<TA, LAY>(at_dh, c, a.cols, dn);
+      if (a.dsum) lds16<TS, LAY>(at_e, c, a.cols, e);
+      load_s(s);
+      if (POST) load_x(x);
       uint64_t q[N] = {};
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -747,7 +881,9 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
 #pragma unroll
       for (int i = 0; i < N; ++i) red[j & 1][i][t >> 5] = m[i];
     }
+    put_scales(j + 1);      // (of the three places the one that the last row before this barrier no longer reads)
     __syncthreads();
+    fetch_scales(j + 2);
     if (t == 0 && j > 0 && j - 1 + stages < n) fill(j - 1 + stages, st == 0 ? stages - 1 : st - 1);      // the stage of the row before
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -766,18 +902,13 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
     if constexpr (POST) c1 = -rho1 * (rho1 * (tf * fmaf(c0, m[2], m[1]) * a.inv_cols));
     if (on) {
       F8 s[2], x[2];
-      if (KEPT) {
-        lds16_e4m3(base + off_s + c, ss, s);
-        lds16_e4m3(base + off_x + c, sx, x);
-      } else {
-        lds16<TS>(base + off_s + c * (uint32_t)sizeof(TS), s);
-        lds16<TA>(base + off_x + c * (uint32_t)sizeof(TA), x);
-      }
+      load_s(s);
+      load_x(x);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[h].p[i] = fmadd2(s[h].p[i], pack_f2(c0, c0), e[h].p[i]);
-      if (a.dr) store16(row_ptr<TS>(a.dr, a.lddr, r) + c, scale8(e[0], a.v.a), scale8(e[1], a.v.a));
+      if (a.dr) put16<TS, LAY>(row_ptr<TS>(a.dr, a.lddr, r), c, a.cols, scale8(e[0], a.v.a), scale8(e[1], a.v.a), a.wide);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -786,7 +917,7 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
           accT[h].p[i] = fmadd2(bd, x[h].p[i], accT[h].p[i]);
           e[h].p[i] = POST ? fmadd2(bd, w[h].p[i], fmul2(x[h].p[i], pack_f2(c1, c1))) : fmul2(bd, w[h].p[i]);
         }
-      if (a.dx) store16(row_ptr<TA>(a.dx, a.lddx, r) + c, e[0], e[1]);
+      if (a.dx) put16<TA, LAY>(row_ptr<TA>(a.dx, a.lddx, r), c, a.cols, e[0], e[1], a.wide);
     }
     if (last && a.many) {
       flush(gate_row, gate_row == worker);
@@ -808,8 +939,8 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
   griddep_launch_dependents();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    if (on && a.tpart && !a.many) store8<kStrided>(a.tpart + (int64_t)worker * a.cols, c + 8 * h, 1, a.cols, accT[h]);
-    if (on && a.ppart) store8<kStrided>(a.ppart + (int64_t)worker * a.cols, c + 8 * h, 1, a.cols, accP[h]);
+    if (on && a.tpart && !a.many) store8<kStrided>(a.tpart + (int64_t)worker * a.cols, c + kNext * h, kApart, a.cols, accT[h]);
+    if (on && a.ppart) store8<kStrided>(a.ppart + (int64_t)worker * a.cols, c + kNext * h, kApart, a.cols, accP[h]);
   }
 }
 
@@ -902,15 +1033,15 @@ constexpr unsigned kTypes = 1u << SF_BF16 | 1u << SF_FP32;
 // Rows of the workspace's partial sums: more of them where rows are short.
 int64_t max_workers(int64_t cols) { return std::min<int64_t>(8192, std::max<int64_t>(1024, (1 << 21) / cols)); }
 
-template <template <typename, typename, int> class K>
-const void* pick_kernel(int32_t ta, int32_t ts, Lay lay) {
+template <template <typename, typename, int> class K, typename... A>
+const void* pick_kernel(int32_t ta, int32_t ts, Lay lay, A... args) {
   using B = __nv_bfloat16;
   if (ta == SF_BF16) {
-    if (ts == SF_BF16) return lay == kUnits ? K<B, B, kUnits>::ptr() : K<B, B, kStrided>::ptr();
-    return lay == kUnits ? K<B, float, kUnits>::ptr() : K<B, float, kStrided>::ptr();
+    if (ts == SF_BF16) return lay == kUnits ? K<B, B, kUnits>::ptr(args...) : K<B, B, kStrided>::ptr(args...);
+    return lay == kUnits ? K<B, float, kUnits>::ptr(args...) : K<B, float, kStrided>::ptr(args...);
   }
-  if (ts == SF_BF16) return lay == kUnits ? K<float, B, kUnits>::ptr() : K<float, B, kStrided>::ptr();
-  return lay == kUnits ? K<float, float, kUnits>::ptr() : K<float, float, kStrided>::ptr();
+  if (ts == SF_BF16) return lay == kUnits ? K<float, B, kUnits>::ptr(args...) : K<float, B, kStrided>::ptr(args...);
+  return lay == kUnits ? K<float, float, kUnits>::ptr(args...) : K<float, float, kStrided>::ptr(args...);
 }
 template <typename TA, typename TS, int LAY>
 struct Fwd {
@@ -928,16 +1059,22 @@ struct BwdFew {
 // The staged form: wide units a thread, registers.
 constexpr int kFwdRegs1 = 80, kFwdRegs2 = 128;
 template <typename TA, typename TS>
-const void* fwd_ring(int c) {
-  return c == 1 ? (const void*)&k_sandwich_fwd_ring<TA, TS, 1, kFwdRegs1> : (const void*)&k_sandwich_fwd_ring<TA, TS, 2, kFwdRegs2>;
+const void* fwd_ring(int c, Lay lay) {
+  if (lay == kUnits) return c == 1 ? (const void*)&k_sandwich_fwd_ring<TA, TS, kUnits, 1, kFwdRegs1> : (const void*)&k_sandwich_fwd_ring<TA, TS, kUnits, 2, kFwdRegs2>;
+  return c == 1 ? (const void*)&k_sandwich_fwd_ring<TA, TS, kStrided, 1, kFwdRegs1> : (const void*)&k_sandwich_fwd_ring<TA, TS, kStrided, 2, kFwdRegs2>;
 }
-template <typename TA, typename TS>
+template <typename TA, typename TS, int LAY>
 const void* bwd_ring(bool kept, bool post) {
-  return kept ? (post ? (const void*)&k_sandwich_bwd_ring<TA, TS, true, true> : (const void*)&k_sandwich_bwd_ring<TA, TS, true, false>)
-              : (post ? (const void*)&k_sandwich_bwd_ring<TA, TS, false, true> : (const void*)&k_sandwich_bwd_ring<TA, TS, false, false>);
+  return kept ? (post ? (const void*)&k_sandwich_bwd_ring<TA, TS, LAY, true, true> : (const void*)&k_sandwich_bwd_ring<TA, TS, LAY, true, false>)
+              : (post ? (const void*)&k_sandwich_bwd_ring<TA, TS, LAY, false, true> : (const void*)&k_sandwich_bwd_ring<TA, TS, LAY, false, false>);
 }
+template <typename TA, typename TS, int LAY>
+struct BwdRing {
+  static const void* ptr(bool kept, bool post) { return bwd_ring<TA, TS, LAY>(kept, post); }
+};
 constexpr size_t kSmemPerSm = 224 << 10, kSmemBlock = 2 << 10;      // a block's static and reserved shared memory
-constexpr int kRingMinCols = 1024;
+constexpr size_t kSmemScales = 6 << 10;        // of three rows
+constexpr int kRingMinCols = 1024, kBwdMinCols = 256;
 
 struct RingShape {
   int c = 0, threads = 0, per_sm = 0, stages = 0;
@@ -949,11 +1086,11 @@ struct RingShape {
 // stages each, two in long rows.  False where rows are too long, or too few or short
 // for it to pay (65536 x 512: 63 us, 51 with loads into registers; 32768 x 1024 50 and 54).
 bool ring_shape(int64_t rows, int64_t cols, size_t stage, int regs1, int regs2, RingShape* best) {
-  if (cols % 16 || cols < kRingMinCols || rows < 2 * sm_count()) return false;
+  if (cols < kRingMinCols || rows < 2 * sm_count()) return false;
   for (int c = 1; c <= 2; ++c) {
     RingShape s;
     s.c = c;
-    s.threads = ceil_div(ceil_div((int)(cols / 16), c), 32) * 32;
+    s.threads = ceil_div(ceil_div(ceil_div((int)cols, 16), c), 32) * 32;
     const int regs = c == 1 ? regs1 : regs2;
     int n = std::min(65536 / (regs * s.threads), 2048 / s.threads);
     while (n > 1 && kSmemPerSm / n < kSmemBlock + 3 * stage) --n;
@@ -1059,13 +1196,13 @@ sf_status sf_sandwich_norm_forward(const sf_sandwich* p, const sf_matrix* x, con
   void* args[] = {&a, nullptr};
   // bulk copies take this device's own memory only
   RingShape ring;
-  const size_t stage = (size_t)cols * (dtype_bytes(x->dtype) + (residual ? dtype_bytes(ts) : 0));
-  if (units && on_wide(x) && on_wide(residual) && on_wide(sum) && on_wide(h) && on_wide(x8) && on_wide(sum8) &&
-      ring_shape(rows, cols, stage, kFwdRegs1, kFwdRegs2, &ring) && (sum || h || sum8 || rstd_pre) && on_current_device(x->data) &&
-      (!residual || on_current_device(residual->data))) {
+  const size_t stage = slot_bytes(cols, dtype_bytes(x->dtype)) + (residual ? slot_bytes(cols, dtype_bytes(ts)) : 0);
+  const Lay lay = units && cols % 16 == 0 ? kUnits : kStrided;
+  a.wide = on_wide(sum) && on_wide(h) && on_wide(x8) && on_wide(sum8);
+  if (ring_shape(rows, cols, stage, kFwdRegs1, kFwdRegs2, &ring) && (sum || h || sum8 || rstd_pre) && on_bulk(x) && on_bulk(residual)) {
     using B = __nv_bfloat16;
-    const void* kernel = x->dtype == SF_BF16 ? (ts == SF_BF16 ? fwd_ring<B, B>(ring.c) : fwd_ring<B, float>(ring.c))
-                                             : (ts == SF_BF16 ? fwd_ring<float, B>(ring.c) : fwd_ring<float, float>(ring.c));
+    const void* kernel = x->dtype == SF_BF16 ? (ts == SF_BF16 ? fwd_ring<B, B>(ring.c, lay) : fwd_ring<B, float>(ring.c, lay))
+                                             : (ts == SF_BF16 ? fwd_ring<float, B>(ring.c, lay) : fwd_ring<float, float>(ring.c, lay));
     SF_TRY(allow_dynamic_smem(kernel, stage * ring.stages));
     args[1] = &ring.stages;
     SF_CUDA_TRY(cudaLaunchKernel(kernel, dim3((unsigned)std::min<int64_t>(rows, (int64_t)sm_count() * ring.per_sm)), dim3(ring.threads), args,
@@ -1179,17 +1316,19 @@ sf_status sf_sandwich_norm_backward(const sf_sandwich* p, const sf_matrix* dh, c
                      on_units(x8) && on_units(sum8) && on_units(gate) && on_units(dgate) && on_units(a.v.g_post, gain_dtype) &&
                      on_units(a.v.g_pre, gain_dtype);
   // the staged form: as many blocks an SM as registers and three stages (of long rows two) allow
-  auto local = [](const sf_matrix* m) { return !m || on_current_device(m->data); };
   const bool kept = x8 && sum8;
-  const size_t stage = (size_t)cols * (dtype_bytes(ta) + (dsum ? dtype_bytes(ts) : 0) + (kept ? 2 : dtype_bytes(ta) + dtype_bytes(ts)));
+  const Lay lay = units && cols % 16 == 0 ? kUnits : kStrided;
+  const size_t stage = slot_bytes(cols, dtype_bytes(ta)) + (dsum ? slot_bytes(cols, dtype_bytes(ts)) : 0) +
+                       (kept ? 2 * slot_bytes(cols, 1) : slot_bytes(cols, dtype_bytes(ta)) + slot_bytes(cols, dtype_bytes(ts)));
   int ring_threads = 0, ring_blocks = 0, ring_stages = 0;
-  if (units && dh && (kept || (x && sum)) && cols % 16 == 0 && cols >= kRingMinCols && cols <= 16 * kBwdRingThreads && rows >= 2 * sm_count() &&
-      rows < (1 << 29) && on_wide(dh) && on_wide(dsum) && on_wide(x) && on_wide(sum) && on_wide(x8) && on_wide(sum8) && on_wide(dresidual) &&
-      on_wide(dx) && local(dh) && local(dsum) && local(x) && local(sum) && (!kept || (local(&x8->values) && local(&sum8->values)))) {
-    ring_threads = (int)ceil_div<int64_t>(cols / 16, 32) * 32;
-    ring_blocks = 65536 / (kBwdRingRegs * ring_threads);
-    while (ring_blocks > 1 && kSmemPerSm / ring_blocks < kSmemBlock + 3 * stage) --ring_blocks;
-    ring_stages = (int)std::min<size_t>(kMaxStages, (kSmemPerSm / ring_blocks - kSmemBlock) / stage);
+  if (dh && (kept || (x && sum)) && cols >= kBwdMinCols && cols <= 16 * kBwdRingThreads && rows >= 2 * sm_count() && rows < (1 << 29) &&
+      on_bulk(dh) && on_bulk(dsum) && on_bulk(x) && on_bulk(sum) && (!kept || (on_bulk(&x8->values) && on_bulk(&sum8->values)))) {
+    a.wide = on_wide(x8) && on_wide(sum8) && on_wide(dresidual) && on_wide(dx);
+    ring_threads = (int)ceil_div<int64_t>(ceil_div<int64_t>(cols, 16), 32) * 32;
+    ring_blocks = std::min(32, 65536 / (kBwdRingRegs * ring_threads));
+    const size_t block = kSmemBlock + (kept && lay == kStrided ? kSmemScales : 0);
+    while (ring_blocks > 1 && kSmemPerSm / ring_blocks < block + 3 * stage) --ring_blocks;
+    ring_stages = (int)std::min<size_t>(kMaxStages, (kSmemPerSm / ring_blocks - block) / stage);
   }
   const bool staged = ring_stages >= 2;
   const int64_t n = ceil_div<int64_t>(cols, 8);
@@ -1222,10 +1361,7 @@ sf_status sf_sandwich_norm_backward(const sf_sandwich* p, const sf_matrix* dh, c
   }
   cudaStream_t st = as_stream(stream);
   if (rows && staged) {
-    using B = __nv_bfloat16;
-    const bool post = a.v.g_post != nullptr;
-    const void* kernel = ta == SF_BF16 ? (ts == SF_BF16 ? bwd_ring<B, B>(kept, post) : bwd_ring<B, float>(kept, post))
-                                       : (ts == SF_BF16 ? bwd_ring<float, B>(kept, post) : bwd_ring<float, float>(kept, post));
+    const void* kernel = pick_kernel<BwdRing>(ta, ts, lay, kept, a.v.g_post != nullptr);
     SF_TRY(allow_dynamic_smem(kernel, stage * ring_stages));
     void* args[] = {&a, &ring_stages};
     SF_CUDA_TRY(cudaLaunchKernel(kernel, dim3((unsigned)a.workers), dim3(threads), args, stage * ring_stages, st), "launch k_sandwich_bwd_ring");
