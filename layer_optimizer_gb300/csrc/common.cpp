@@ -187,7 +187,8 @@ sf_status sf_sync_status(void* stream) {
   const int dev_err = sf::read_and_clear_device_error() | sf::read_and_clear_device_error_adamw() |
                       sf::read_and_clear_device_error_gemm() | sf::read_and_clear_device_error_lce() |
                       sf::read_and_clear_device_error_norm() | sf::read_and_clear_device_error_wgrad() |
-                      sf::read_and_clear_device_error_sandwich();
+                      sf::read_and_clear_device_error_sandwich_fwd() | sf::read_and_clear_device_error_sandwich_units() |
+                      sf::read_and_clear_device_error_sandwich_strided();
   if (dev_err & 1) return sf::fail(SF_ERR_TIMEOUT, "a kernel wait ran out of its bound (device error word %d)", dev_err);
   if (dev_err & 2) return sf::fail(SF_ERR_INVALID, "a kernel skipped an out-of-range index (device error word %d)", dev_err);
   return SF_OK;

@@ -129,7 +129,9 @@ int read_and_clear_device_error_gemm();
 int read_and_clear_device_error_lce();
 int read_and_clear_device_error_norm();
 int read_and_clear_device_error_wgrad();
-int read_and_clear_device_error_sandwich();
+int read_and_clear_device_error_sandwich_fwd();
+int read_and_clear_device_error_sandwich_units();
+int read_and_clear_device_error_sandwich_strided();
 
 // C = alpha A B^T (+ C) on the tensor cores (tc_gemm.cu): A bf16 [M][lda]
 // row-major (K-major) or, with a_mn, [K][lda] (MN-major: A^T stored);
