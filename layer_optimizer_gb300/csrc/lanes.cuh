@@ -391,12 +391,16 @@ __device__ __forceinline__ void ck_store16(const Ck& k, int64_t row, int c, int 
   uint32_t code = row_code;
   bool infinite = !k.group_log2;
   if (k.group_log2) {
-    const int lanes = 1 << (k.group_log2 - 4);
     infinite = __any_sync(0xffffffffu, !(top <= kLargest));
     if (infinite) top = c < cols ? fmaxf(top8_finite(lo), top8_finite(hi)) : 0.0f;
-    for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+    for (int o = 1; o < 8; o *= 2) {      // a group of 32, 64 or 128 columns: 2, 4 or 8 lanes
+      const float other = __shfl_xor_sync(0xffffffffu, top, o);
+      top = fmaxf(top, 16 * o < 1 << k.group_log2 ? other : 0.0f);
+    }
     code = e8m0_of(top);
-    if (c < cols && (c & ((1 << k.group_log2) - 1)) == 0) k.s8[row * k.n_groups + (c >> k.group_log2)] = (uint8_t)code;
+    if (c < cols && (c & ((1 << k.group_log2) - 1)) == 0)
+      k.s8[row * k.n_groups + (c >> k.group_log2)] = (uint8_t)code;
   }
   if (c >= cols) return;
   const float inv = e8m0_inverse(code);

@@ -113,6 +113,20 @@ __device__ __forceinline__ void bring_rows(const Bring (&b)[N], unsigned char* c
     if (b[i].bytes) b[i].copy(to[i], bar);
 }
 
+// Row `row` of a matrix with fewer than 2^31 rows and columns between rows: one
+// 32 x 32 -> 64 bit multiplication instead of a 64-bit one.
+template <typename T>
+__device__ __forceinline__ T* short_row(void* base, int64_t ld, uint32_t row) {
+  return static_cast<T*>(base) + (uint64_t)row * (uint32_t)ld;
+}
+template <typename T>
+__device__ __forceinline__ const T* short_row(const void* base, int64_t ld, uint32_t row) {
+  return static_cast<const T*>(base) + (uint64_t)row * (uint32_t)ld;
+}
+
+// Host side: whether short_row() does for `m` (null passes).
+inline bool short_ld(const sf_matrix* m) { return !m || m->ld < (int64_t)1 << 31; }
+
 // 16 columns of a thread in either lay.  c0: its first; strided ones are 32 apart.
 template <int LAY>
 __device__ __forceinline__ int first16(int t, int T, int k) {

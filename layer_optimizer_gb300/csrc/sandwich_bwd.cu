@@ -325,7 +325,8 @@ sf_status sf_sandwich_norm_backward(const sf_sandwich* p, const sf_matrix* dh, c
                        (kept ? 2 * slot_bytes(cols, 1) : slot_bytes(cols, dtype_bytes(ta)) + slot_bytes(cols, dtype_bytes(ts)));
   int ring_threads = 0, ring_blocks = 0, ring_stages = 0;
   if (dh && (kept || (x && sum)) && cols >= kBwdMinCols && cols <= 16 * kBwdRingThreads && rows >= 2 * sm_count() && rows < (1 << 29) &&
-      on_bulk(dh) && on_bulk(dsum) && on_bulk(x) && on_bulk(sum) && (!kept || (on_bulk(&x8->values) && on_bulk(&sum8->values)))) {
+      short_ld(dh) && short_ld(dsum) && short_ld(x) && short_ld(sum) && short_ld(dresidual) && short_ld(dx) &&
+      (!kept || (short_ld(&x8->values) && short_ld(&sum8->values))) && on_bulk(dh) && on_bulk(dsum) && on_bulk(x) && on_bulk(sum) && (!kept || (on_bulk(&x8->values) && on_bulk(&sum8->values)))) {
     a.wide = on_wide(x8) && on_wide(sum8) && on_wide(dresidual) && on_wide(dx);
     ring_threads = (int)ceil_div<int64_t>(ceil_div<int64_t>(cols, 16), 32) * 32;
     ring_blocks = std::min(32, 65536 / (kBwdRingRegs * ring_threads));

@@ -80,27 +80,27 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
     return (worker + q * workers) * span + j - q * span;
   };
   auto fill = [&](int j, int st) {      // by one thread
-    const int64_t r = row_at(j);
+    const int r = row_at(j);
     unsigned char* at = ring + (size_t)st * stage_bytes;
     const bool last = r == a.rows - 1;
     const uint32_t size_a = (uint32_t)a.cols * (uint32_t)sizeof(TA), size_s = (uint32_t)a.cols * (uint32_t)sizeof(TS);
     if (LAY == kUnits && (!KEPT || a.wide)) {      // (few instructions: the thread's warp is waited for)
       mbar_arrive_expect_tx(&full[st], size_a + (a.dsum ? size_s : 0u) + (KEPT ? 2u * a.cols : size_a + size_s));
-      bulk_load(at, row_ptr<TA>(a.dh, a.lddh, r), size_a, &full[st]);
-      if (a.dsum) bulk_load(at + off_e, row_ptr<TS>(a.dsum, a.lddsum, r), size_s, &full[st]);
+      bulk_load(at, short_row<TA>(a.dh, a.lddh, r), size_a, &full[st]);
+      if (a.dsum) bulk_load(at + off_e, short_row<TS>(a.dsum, a.lddsum, r), size_s, &full[st]);
       if (KEPT) {
-        bulk_load(at + off_x, a.x8.q + r * a.x8.ld, a.cols, &full[st]);
-        bulk_load(at + off_s, a.s8.q + r * a.s8.ld, a.cols, &full[st]);
+        bulk_load(at + off_x, short_row<uint8_t>(a.x8.q, a.x8.ld, r), a.cols, &full[st]);
+        bulk_load(at + off_s, short_row<uint8_t>(a.s8.q, a.s8.ld, r), a.cols, &full[st]);
       } else {
-        bulk_load(at + off_x, row_ptr<TA>(a.x, a.ldx, r), size_a, &full[st]);
-        bulk_load(at + off_s, row_ptr<TS>(a.s, a.lds, r), size_s, &full[st]);
+        bulk_load(at + off_x, short_row<TA>(a.x, a.ldx, r), size_a, &full[st]);
+        bulk_load(at + off_s, short_row<TS>(a.s, a.lds, r), size_s, &full[st]);
       }
       return;
     }
-    const Bring b[4] = {{row_ptr<TA>(a.dh, a.lddh, r), size_a, last},
-                        {row_ptr<TS>(a.dsum, a.lddsum, r), a.dsum ? size_s : 0u, last},
-                        {KEPT ? (const void*)(a.x8.q + r * a.x8.ld) : row_ptr<TA>(a.x, a.ldx, r), KEPT ? (uint32_t)a.cols : size_a, last},
-                        {KEPT ? (const void*)(a.s8.q + r * a.s8.ld) : row_ptr<TS>(a.s, a.lds, r), KEPT ? (uint32_t)a.cols : size_s, last}};
+    const Bring b[4] = {{short_row<TA>(a.dh, a.lddh, r), size_a, last},
+                        {short_row<TS>(a.dsum, a.lddsum, r), a.dsum ? size_s : 0u, last},
+                        {KEPT ? (const void*)short_row<uint8_t>(a.x8.q, a.x8.ld, r) : short_row<TA>(a.x, a.ldx, r), KEPT ? (uint32_t)a.cols : size_a, last},
+                        {KEPT ? (const void*)short_row<uint8_t>(a.s8.q, a.s8.ld, r) : short_row<TS>(a.s, a.lds, r), KEPT ? (uint32_t)a.cols : size_s, last}};
     unsigned char* const to[4] = {at, at + off_e, at + off_x, at + off_s};
     bring_rows(b, to, &full[st]);
   };
@@ -151,12 +151,12 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
   float rho1_next = 1.0f, rho2_next = 0.0f;
   uint32_t sx_next = 0, ss_next = 0;
   // (strided: a thread brings one group's, for all)
-  auto scale_raw = [&](const Ck& ck, int64_t r) {
-    const int64_t i = r * ck.n_groups + (LAY == kStrided ? min(t, ck.n_groups - 1) : ck.group_log2 && on ? c >> ck.group_log2 : 0);
+  auto scale_raw = [&](const Ck& ck, uint32_t r) {
+    const uint64_t i = (uint64_t)r * (uint32_t)ck.n_groups + (LAY == kStrided ? min(t, ck.n_groups - 1) : ck.group_log2 && on ? c >> ck.group_log2 : 0);
     return ck.s8 ? (uint32_t)ck.s8[i] : __float_as_uint(ck.s32[i]);
   };
   auto scale_value = [](const Ck& ck, uint32_t raw) { return ck.s8 ? e8m0_value(raw) : __uint_as_float(raw); };
-  auto prefetch = [&](int64_t r) {
+  auto prefetch = [&](int r) {
     if (POST) rho1_next = a.rho1[r];
     rho2_next = a.rho2[r];
     if (KEPT && LAY == kUnits) sx_next = scale_raw(a.x8, r), ss_next = scale_raw(a.s8, r);
@@ -185,16 +185,16 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
   for (int j = 0; j < n; ++j) {
     const float rho1 = rho1_next, rho2 = rho2_next;
     const float sx = scale_value(a.x8, sx_next), ss = scale_value(a.s8, ss_next);
-    const int64_t r = row;
+    const int r = row;
     const bool last = --left == 0;      // of its item
     row = last ? (gate_row + workers) * span : row + 1;
     if (j + 1 < n) prefetch(row);
     if (!dead) dead = !mbar_wait_u32(smem_u32(&full[st]), phase);
     const uint32_t base = ring0 + (uint32_t)st * stage_bytes;
-    const uint32_t at_dh = base + (LAY == kUnits ? 0u : lead_of(row_ptr<TA>(a.dh, a.lddh, r)));
-    const uint32_t at_e = base + off_e + (LAY == kUnits ? 0u : lead_of(row_ptr<TS>(a.dsum, a.lddsum, r)));
-    const uint32_t at_x = base + off_x + (KEPT ? lead_of(a.x8.q + r * a.x8.ld) : LAY == kUnits ? 0u : lead_of(row_ptr<TA>(a.x, a.ldx, r)));
-    const uint32_t at_s = base + off_s + (KEPT ? lead_of(a.s8.q + r * a.s8.ld) : LAY == kUnits ? 0u : lead_of(row_ptr<TS>(a.s, a.lds, r)));
+    const uint32_t at_dh = base + (LAY == kUnits ? 0u : lead_of(short_row<TA>(a.dh, a.lddh, r)));
+    const uint32_t at_e = base + off_e + (LAY == kUnits ? 0u : lead_of(short_row<TS>(a.dsum, a.lddsum, r)));
+    const uint32_t at_x = base + off_x + (KEPT ? lead_of(short_row<uint8_t>(a.x8.q, a.x8.ld, r)) : LAY == kUnits ? 0u : lead_of(short_row<TA>(a.x, a.ldx, r)));
+    const uint32_t at_s = base + off_s + (KEPT ? lead_of(short_row<uint8_t>(a.s8.q, a.s8.ld, r)) : LAY == kUnits ? 0u : lead_of(short_row<TS>(a.s, a.lds, r)));
     auto load_s = [&](F8 (&s)[2]) {
       if constexpr (!KEPT) lds16<TS, LAY>(at_s, c, a.cols, s);
       else if constexpr (LAY == kUnits) lds16_e4m3(at_s + c, ss, a.wide, s);
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[h].p[i] = fmadd2(s[h].p[i], pack_f2(c0, c0), e[h].p[i]);
-      if (a.dr) put16<TS, LAY>(row_ptr<TS>(a.dr, a.lddr, r), c, a.cols, scale8(e[0], a.v.a), scale8(e[1], a.v.a), a.wide);
+      if (a.dr) put16<TS, LAY>(short_row<TS>(a.dr, a.lddr, r), c, a.cols, scale8(e[0], a.v.a), scale8(e[1], a.v.a), a.wide);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
           accT[h].p[i] = fmadd2(bd, x[h].p[i], accT[h].p[i]);
           e[h].p[i] = POST ? fmadd2(bd, w[h].p[i], fmul2(x[h].p[i], pack_f2(c1, c1))) : fmul2(bd, w[h].p[i]);
         }
-      if (a.dx) put16<TA, LAY>(row_ptr<TA>(a.dx, a.lddx, r), c, a.cols, e[0], e[1], a.wide);
+      if (a.dx) put16<TA, LAY>(short_row<TA>(a.dx, a.lddx, r), c, a.cols, e[0], e[1], a.wide);
     }
     if (last && a.many) {
       flush(gate_row, gate_row == worker);

@@ -173,19 +173,19 @@ __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int
   for (int i = t; i < 8 * kRed; i += T) (&red[0][0][0][0])[i] = 0.0f;
   const uint32_t row_x = slot_bytes(a.cols, sizeof(TA)), stage_bytes = row_x + (a.r ? slot_bytes(a.cols, sizeof(TS)) : 0u);
   const uint32_t ring0 = smem_u32(ring);
-  const int64_t first = a.rows * blockIdx.x / gridDim.x, end = a.rows * (blockIdx.x + 1) / gridDim.x;
-  auto fill = [&](int64_t row, int st) {      // by one thread
+  const int first = (int)(a.rows * blockIdx.x / gridDim.x), end = (int)(a.rows * (blockIdx.x + 1) / gridDim.x);
+  auto fill = [&](int row, int st) {      // by one thread
     unsigned char* at = ring + (size_t)st * stage_bytes;
     if constexpr (LAY == kUnits) {      // (few instructions: the thread's warp is waited for)
       const uint32_t bytes_x = (uint32_t)a.cols * sizeof(TA), bytes_r = a.r ? (uint32_t)a.cols * sizeof(TS) : 0u;
       mbar_arrive_expect_tx(&full[st], bytes_x + bytes_r);
-      bulk_load(at, row_ptr<TA>(a.x, a.ldx, row), bytes_x, &full[st]);
-      if (a.r) bulk_load(at + row_x, row_ptr<TS>(a.r, a.ldr, row), bytes_r, &full[st]);
+      bulk_load(at, short_row<TA>(a.x, a.ldx, row), bytes_x, &full[st]);
+      if (a.r) bulk_load(at + row_x, short_row<TS>(a.r, a.ldr, row), bytes_r, &full[st]);
       return;
     }
     const bool last = row == a.rows - 1;
-    const Bring b[2] = {{row_ptr<TA>(a.x, a.ldx, row), (uint32_t)a.cols * (uint32_t)sizeof(TA), last},
-                        {row_ptr<TS>(a.r, a.ldr, row), a.r ? (uint32_t)a.cols * (uint32_t)sizeof(TS) : 0u, last}};
+    const Bring b[2] = {{short_row<TA>(a.x, a.ldx, row), (uint32_t)a.cols * (uint32_t)sizeof(TA), last},
+                        {short_row<TS>(a.r, a.ldr, row), a.r ? (uint32_t)a.cols * (uint32_t)sizeof(TS) : 0u, last}};
     unsigned char* const to[2] = {at, at + row_x};
     bring_rows(b, to, &full[st]);
   };
@@ -201,14 +201,15 @@ __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int
   auto vec = [&](const void* p, int fp32, int c, float add, F8 (&v)[2]) { vec16<LAY>(p, fp32, c, a.cols, add, v); };
   auto col = [&](int k) { return first16<LAY>(t, T, k); };
   if (C == 1 && a.h && col(0) < a.cols) vec(a.v.g_pre, a.v.gain_fp32, col(0), a.v.offset, g2);
-  int64_t gate_end = first;      // rows from here on take another gate row
-  int64_t gate_at = a.v.gate ? first / a.v.span : 0;
+  const int span = (int)a.v.span;
+  int gate_end = first;      // rows from here on take another gate row
+  int gate_at = a.v.gate ? first / span : 0;
   int st = 0, parity = 0;
   uint32_t phase = 0;
   bool dead = false;      // a wait ran out (recorded): go on without waiting, so that all threads still leave together
-  for (int64_t row = first; row < end; ++row, parity ^= 1) {
+  for (int row = first; row < end; ++row, parity ^= 1) {
     if (row == gate_end) {
-      gate_end = a.v.gate ? (gate_at + 1) * a.v.span : end;
+      gate_end = a.v.gate ? (gate_at + 1) * span : end;
 #pragma unroll
       for (int k = 0; k < C; ++k) {
         const int c = col(k);
@@ -221,15 +222,15 @@ __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int
           w[k][0] = mul8(w[k][0], v[0]), w[k][1] = mul8(w[k][1], v[1]);
         }
         if (a.v.gate) {
-          vec(static_cast<const char*>(a.v.gate) + gate_at * a.v.ld_gate * (a.v.gate_fp32 ? 4 : 2), a.v.gate_fp32, c, 0.0f, v);
+          vec(gate_row_of(a.v, gate_at), a.v.gate_fp32, c, 0.0f, v);
           w[k][0] = mul8(w[k][0], v[0]), w[k][1] = mul8(w[k][1], v[1]);
         }
       }
       ++gate_at;
     }
     if (!dead) dead = !mbar_wait_u32(smem_u32(&full[st]), phase);
-    const uint32_t at = ring0 + (uint32_t)st * stage_bytes + (LAY == kUnits ? 0u : lead_of(row_ptr<TA>(a.x, a.ldx, row)));
-    const uint32_t at_r = ring0 + (uint32_t)st * stage_bytes + row_x + (LAY == kUnits ? 0u : lead_of(row_ptr<TS>(a.r, a.ldr, row)));
+    const uint32_t at = ring0 + (uint32_t)st * stage_bytes + (LAY == kUnits ? 0u : lead_of(short_row<TA>(a.x, a.ldx, row)));
+    const uint32_t at_r = ring0 + (uint32_t)st * stage_bytes + row_x + (LAY == kUnits ? 0u : lead_of(short_row<TS>(a.r, a.ldr, row)));
     float rho1 = 1.0f;
     if (post || a.x8.q) {
       float sum = 0.0f, top[1] = {0.0f};
@@ -302,7 +303,7 @@ __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int
             for (int i = 0; i < 4; ++i) s[k][h].p[i] = fmadd2(v.p[i], pack_f2(a.v.a, a.v.a), s[k][h].p[i]);
           }
         }
-        if (a.s) put16<TS, LAY>(row_ptr<TS>(a.s, a.lds, row), c, a.cols, s[k][0], s[k][1], a.wide);
+        if (a.s) put16<TS, LAY>(short_row<TS>(a.s, a.lds, row), c, a.cols, s[k][0], s[k][1], a.wide);
       }
       sum += dot8(s[k][0], s[k][0]) + dot8(s[k][1], s[k][1]);
       if (s_row) top[0] = fmaxf(top[0], fmaxf(top8(s[k][0]), top8(s[k][1])));
@@ -337,7 +338,7 @@ __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int
         const int c = col(k);
         if (c >= a.cols) continue;
         if (C > 1) vec(a.v.g_pre, a.v.gain_fp32, c, a.v.offset, g2);
-        put16<TA, LAY>(row_ptr<TA>(a.h, a.ldh, row), c, a.cols, mul8(scale8(s[k][0], rho2), g2[0]), mul8(scale8(s[k][1], rho2), g2[1]), a.wide);
+        put16<TA, LAY>(short_row<TA>(a.h, a.ldh, row), c, a.cols, mul8(scale8(s[k][0], rho2), g2[0]), mul8(scale8(s[k][1], rho2), g2[1]), a.wide);
       }
     }
     if (++st == stages) {
@@ -346,7 +347,7 @@ __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int
     }
   }
   if (dead && t == 0) {      // copies still under way land before their memory is given up (waited for once more, bounded)
-    const int64_t n = end - first;
+    const int n = end - first;
     for (int i = 0; i < stages && i < n; ++i) mbar_wait(&full[i], (uint32_t)((n - 1 - i) / stages) & 1u);
   }
   if (dead) __syncthreads();
@@ -373,7 +374,7 @@ struct RingShape {
 // stages each, two in long rows.  False where rows are too long, or too few or short
 // for it to pay (65536 x 512: 63 us, 51 with loads into registers; 32768 x 1024 50 and 54).
 bool ring_shape(int64_t rows, int64_t cols, size_t stage, int regs1, int regs2, RingShape* best) {
-  if (cols < kRingMinCols || rows < 2 * sm_count()) return false;
+  if (cols < kRingMinCols || rows < 2 * sm_count() || rows >= 1 << 29) return false;
   for (int c = 1; c <= 2; ++c) {
     RingShape s;
     s.c = c;
@@ -450,7 +451,8 @@ sf_status sf_sandwich_norm_forward(const sf_sandwich* p, const sf_matrix* x, con
   const size_t stage = slot_bytes(cols, dtype_bytes(x->dtype)) + (residual ? slot_bytes(cols, dtype_bytes(ts)) : 0);
   const Lay lay = units && cols % 16 == 0 ? kUnits : kStrided;
   a.wide = on_wide(sum) && on_wide(h) && on_wide(x8) && on_wide(sum8);
-  if (ring_shape(rows, cols, stage, kFwdRegs1, kFwdRegs2, &ring) && (sum || h || sum8 || rstd_pre) && on_bulk(x) && on_bulk(residual)) {
+  const bool short_lds = short_ld(x) && short_ld(residual) && short_ld(sum) && short_ld(h);
+  if (ring_shape(rows, cols, stage, kFwdRegs1, kFwdRegs2, &ring) && (sum || h || sum8 || rstd_pre) && short_lds && on_bulk(x) && on_bulk(residual)) {
     using B = __nv_bfloat16;
     const void* kernel = x->dtype == SF_BF16 ? (ts == SF_BF16 ? fwd_ring<B, B>(ring.c, lay) : fwd_ring<B, float>(ring.c, lay))
                                              : (ts == SF_BF16 ? fwd_ring<float, B>(ring.c, lay) : fwd_ring<float, float>(ring.c, lay));
