@@ -142,6 +142,9 @@ __device__ __forceinline__ float lds_value(uint32_t p, float) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(p));
   return v;
 }
+// Whether all 512 columns of a warp in the second lay are the row's (the same for the warp).
+__device__ __forceinline__ bool whole512(int c0, int cols) { return (c0 | 31) + 480 < cols; }
+
 // From shared memory, at the address of column 0 (c0 below cols; strided
 // columns past it read as zero); in the first lay kept as stored until used.
 template <typename T, int LAY>
@@ -155,8 +158,14 @@ struct Lds16<T, kStrided> {
   F8 v[2];
   __device__ __forceinline__ Lds16(uint32_t p, int c0, int cols) {
     float x[16];
+    const uint32_t at = p + c0 * (uint32_t)sizeof(T);
+    if (whole512(c0, cols)) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = c0 + 32 * e < cols ? lds_value(p + (c0 + 32 * e) * (uint32_t)sizeof(T), T()) : 0.0f;
+      for (int e = 0; e < 16; ++e) x[e] = lds_value(at + 32 * e * (uint32_t)sizeof(T), T());
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = c0 + 32 * e < cols ? lds_value(at + 32 * e * (uint32_t)sizeof(T), T()) : 0.0f;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e >> 2].p[e & 3] = pack_f2(x[2 * e], x[2 * e + 1]);
   }
@@ -167,13 +176,31 @@ __device__ __forceinline__ void lds16(uint32_t p, int c0, int cols, F8 (&v)[2]) 
   const Lds16<T, LAY> u(p, c0, cols);
   v[0] = u.half(0), v[1] = u.half(1);
 }
+__device__ __forceinline__ void put8_strided(__nv_bfloat16* p, const F8& v) {
+  Unit<__nv_bfloat16> u;
+  pack(v, u);
+  uint16_t* q = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) q[32 * j] = (uint16_t)(u.w[j >> 1] >> (16 * (j & 1)));
+}
+__device__ __forceinline__ void put8_strided(float* p, const F8& v) {
+  Unit<float> u;
+  pack(v, u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) p[32 * j] = u.f[j];
+}
 template <typename T, int LAY>
 __device__ __forceinline__ void put16(T* row, int c0, int cols, const F8& lo, const F8& hi, bool wide) {
   if constexpr (LAY == kUnits) {
     store16(row + c0, lo, hi, wide);
   } else {
-    store8<kStrided>(row, c0, 32, cols, lo);
-    store8<kStrided>(row, c0 + 256, 32, cols, hi);
+    if (whole512(c0, cols)) {
+      put8_strided(row + c0, lo);
+      put8_strided(row + c0 + 256, hi);
+    } else {
+      store8<kStrided>(row, c0, 32, cols, lo);
+      store8<kStrided>(row, c0 + 256, 32, cols, hi);
+    }
   }
 }
 template <int LAY>

@@ -34,14 +34,16 @@ __device__ __forceinline__ void lds16_e4m3(uint32_t p, float scale, bool wide, F
 // In the second lay, the row's scales from shared memory too.
 __device__ __forceinline__ void lds16_e4m3_strided(uint32_t p, int c0, int cols, const float* scales, int group_log2, F8 (&v)[2]) {
   const int shift = group_log2 ? group_log2 : 31;
+  const bool whole = whole512(c0, cols);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int c = c0 + 64 * i, d = c + 32;
-    uint16_t q0 = 0, q1 = 0;
-    if (c < cols) asm volatile("{.reg .b32 t; ld.shared.u8 t, [%1]; cvt.u16.u32 %0, t;}" : "=h"(q0) : "r"(p + c));
-    if (d < cols) asm volatile("{.reg .b32 t; ld.shared.u8 t, [%1]; cvt.u16.u32 %0, t;}" : "=h"(q1) : "r"(p + d));
-    const float2 x = e4m3x2_value((uint32_t)q0 | (uint32_t)q1 << 8);
-    v[i >> 2].p[i & 3] = fmul2(pack_f2(x.x, x.y), pack_f2(c < cols ? scales[c >> shift] : 0.0f, d < cols ? scales[d >> shift] : 0.0f));
+    uint32_t q0 = 0, q1 = 0;
+    if (whole || c < cols) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(q0) : "r"(p + c));
+    if (whole || d < cols) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(q1) : "r"(p + d));
+    const float2 x = e4m3x2_value(q0 | q1 << 8);
+    // (a column past the row: 0 times the last scale)
+    v[i >> 2].p[i & 3] = fmul2(pack_f2(x.x, x.y), pack_f2(scales[(whole ? c : min(c, cols - 1)) >> shift], scales[(whole ? d : min(d, cols - 1)) >> shift]));
   }
 }
 
