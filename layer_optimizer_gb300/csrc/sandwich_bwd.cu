@@ -168,7 +168,7 @@ __device__ __forceinline__ float join32(float v, float (&red)[32][33]) {
 }
 
 __global__ void __launch_bounds__(1024) k_sandwich_join(const JoinArgs a) {
-  __shared__ float red[32][33];
+  __shared__ float red[4][32][33];
   const int c = blockIdx.x * 32 + threadIdx.x, out = blockIdx.x * 32 + threadIdx.y;
   const bool on = c < a.cols, writes = threadIdx.x == 0 && out < a.cols;
   griddep_wait();
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(1024) k_sandwich_join(const JoinArgs a) {
 #pragma unroll 8
       for (int64_t p = threadIdx.y; p < a.workers; p += 32) v += part[p * a.cols + c];
     }
-    v = join32(v, red);
+    v = join32(v, red[0]);
     if (writes) put_at(dst, a.dgain_fp32, out, v);
     return;
   }
@@ -201,19 +201,30 @@ __global__ void __launch_bounds__(1024) k_sandwich_join(const JoinArgs a) {
         dg1 = fmaf(vec_at(a.v.gate, a.v.gate_fp32, k * a.v.ld_gate + c), v, dg1);
       }
     }
-    dg1 = join32(dg1, red);
-  } else {
-    for (int64_t k = 0; k < a.gate_rows; ++k) {
-      float v = 0.0f;
+    dg1 = join32(dg1, red[0]);
+  } else {      // four gate rows at a time
+    const float g1 = writes && a.v.g_post ? vec_at(a.v.g_post, a.v.gain_fp32, out) + a.v.offset : 1.0f;
+    for (int64_t k0 = 0; k0 < a.gate_rows; k0 += 4) {
+      float v[4] = {};
       if (on) {
-#pragma unroll 4
-        for (int p = threadIdx.y; p < a.parts; p += 32) v += a.tpart[(k * a.parts + p) * a.cols + c];
+        for (int p = threadIdx.y; p < a.parts; p += 32)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (k0 + i < a.gate_rows) v[i] += a.tpart[((k0 + i) * a.parts + p) * a.cols + c];
       }
-      v = join32(v, red);
-      if (writes) {
-        const float g1 = a.v.g_post ? vec_at(a.v.g_post, a.v.gain_fp32, out) + a.v.offset : 1.0f;
-        if (a.dgate) put_at(a.dgate, a.dgate_fp32, k * a.lddgate + out, g1 * v);
-        dg1 = fmaf(vec_at(a.v.gate, a.v.gate_fp32, k * a.v.ld_gate + out), v, dg1);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[i][threadIdx.y][threadIdx.x] = v[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = red[i][threadIdx.x][threadIdx.y];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        const int64_t k = k0 + i;
+        if (!writes || k >= a.gate_rows) continue;
+        if (a.dgate) put_at(a.dgate, a.dgate_fp32, k * a.lddgate + out, g1 * v[i]);
+        dg1 = fmaf(vec_at(a.v.gate, a.v.gate_fp32, k * a.v.ld_gate + out), v[i], dg1);
       }
     }
   }

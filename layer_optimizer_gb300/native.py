@@ -96,6 +96,7 @@ class sf_sandwich(ctypes.Structure):
 
 
 _P = ctypes.c_void_p
+_PM, _PC, _PS = ctypes.POINTER(sf_matrix), ctypes.POINTER(sf_checkpoint), ctypes.POINTER(sf_sandwich)
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _INT = ctypes.c_int
@@ -156,13 +157,14 @@ _SIGS = {
     "sf_add_rmsnorm_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
     "sf_add_rmsnorm_backward": (_ST, [_P, _P, _P, _INT, _P, _P, ctypes.c_double, _P, _P, _P, _P, _INT, _P,
                                       ctypes.c_size_t, _P]),
-    "sf_checkpoint_store": (_ST, [_P, _P, _P]),
-    "sf_checkpoint_load": (_ST, [_P, _P, _P, _INT, ctypes.c_double, _P, _P]),
+    # (structures go by pointer as they are)
+    "sf_checkpoint_store": (_ST, [_PM, _PC, _P]),
+    "sf_checkpoint_load": (_ST, [_PC, _P, _P, _INT, ctypes.c_double, _PM, _P]),
     "sf_checkpoint_wgrad_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
-    "sf_checkpoint_wgrad": (_ST, [_P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
-    "sf_sandwich_norm_forward": (_ST, [_P, _P, _P, _P, _P, _INT, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "sf_checkpoint_wgrad": (_ST, [_PM, _PC, _PM, _PM, _P, ctypes.c_size_t, _P]),
+    "sf_sandwich_norm_forward": (_ST, [_PS, _PM, _PM, _P, _P, _INT, _PM, _PM, _PM, _PC, _PC, _P, _P, _P]),
     "sf_sandwich_norm_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
-    "sf_sandwich_norm_backward": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _INT, _P, _P, _P, _P, _P, _P, _P, _INT, _P,
+    "sf_sandwich_norm_backward": (_ST, [_PS, _PM, _PM, _PM, _PC, _PM, _PC, _P, _P, _INT, _PM, _P, _P, _PM, _PM, _P, _P, _INT, _PM,
                                         _P, ctypes.c_size_t, _P]),
 }
 
@@ -571,24 +573,37 @@ def checkpoint(values, scale, group=0):
     return c
 
 
-def _full_or_8(t, name):
-    """A matrix or a checkpoint, as the two arguments that the library takes for it."""
-    if type(t) is sf_checkpoint:
-        return None, ctypes.byref(t)
-    return _ref(_matrix(t, name)), None
+def _f32(t, n, name):
+    """_vector() of fp32 values."""
+    if t is None or type(t) is int:
+        return t
+    if _DTYPES.get(t.dtype) != SF_FP32 and _dtype(t, name) != SF_FP32:
+        raise SfError(SF_ERR_UNSUPPORTED, f"{name}: {t.dtype} is not taken here")
+    return _vector(t, n, name)
+
+
+def _two_vectors(a, b, n, name, dtype):
+    """Addresses and the type of two vectors that have one (addresses come with `dtype`)."""
+    if a is None and b is None:
+        return None, None, SF_FP32
+    ta = None if a is None else _vector_dtype(a, name, dtype)
+    tb = ta if b is None else _vector_dtype(b, name, dtype)
+    if ta is not None and ta != tb:
+        raise SfError(SF_ERR_INVALID, f"{name}_post and {name}_pre must have one type")
+    return _vector(a, n, name + "_post"), _vector(b, n, name + "_pre"), tb
 
 
 def sf_checkpoint_store(x, out, stream=None):
     """Writes x as the checkpoint `out`."""
-    x = _matrix(x, "x")
-    _check(load().sf_checkpoint_store(_ref(x), _ref(out), _stream(stream)))
+    _check((_lib or load()).sf_checkpoint_store(_matrix(x, "x"), out, _stream(stream)))
 
 
 def sf_checkpoint_load(c, y, row_factor=None, gain=None, gain_offset=0.0, stream=None, gain_dtype=None):
     """y = the checkpoint's values, times row_factor per row and gain_offset + gain per column where given."""
     y = _required(y, "y")
-    _check(load().sf_checkpoint_load(_ref(c), _vector(row_factor, y.rows, "row_factor", _F32), _vector(gain, y.cols, "gain"),
-                                     _vector_dtype(gain, "gain", gain_dtype), float(gain_offset), _ref(y), _stream(stream)))
+    _check((_lib or load()).sf_checkpoint_load(
+        c, _f32(row_factor, y.rows, "row_factor"), _vector(gain, y.cols, "gain"),
+        SF_FP32 if gain is None else _vector_dtype(gain, "gain", gain_dtype), gain_offset, y, _stream(stream)))
 
 
 def sf_checkpoint_wgrad_workspace_bytes(tokens, out, in_):
@@ -597,9 +612,9 @@ def sf_checkpoint_wgrad_workspace_bytes(tokens, out, in_):
 
 def sf_checkpoint_wgrad(dY, c, dW, base=None, ws=None, stream=None):
     """dW = base + dY^T X from the checkpoint c of X (base: None or dW itself, to add to it, or another matrix)."""
-    dY, dW, base = _matrix(dY, "dY"), _matrix(dW, "dW"), _matrix(base, "base")
+    dW = _matrix(dW, "dW")
     ws, ws_bytes = _workspace(ws)
-    _check(load().sf_checkpoint_wgrad(_ref(dY), _ref(c), _ref(base), _ref(dW), ws, ws_bytes, _stream(stream)))
+    _check((_lib or load()).sf_checkpoint_wgrad(_matrix(dY, "dY"), c, _matrix(base, "base"), dW, ws, ws_bytes, _stream(stream)))
 
 
 def sandwich(eps, residual_scale=1.0, block_scale=1.0, gain_offset=0.0, gate_span=0):
@@ -612,21 +627,11 @@ def sf_sandwich_norm_forward(p, x, residual=None, gain_post=None, gain_pre=None,
     """s = residual_scale r + block_scale gate norm(x), h = norm(s), with checkpoints of x and s; tensors or sf_matrix,
     x8 and sum8 from checkpoint() (vectors: tensors or addresses, the gains' with gain_dtype)."""
     x = _required(x, "x")
-    residual, gate, sum, h = _matrix(residual, "residual"), _matrix(gate, "gate"), _matrix(sum, "sum"), _matrix(h, "h")
-    _check(load().sf_sandwich_norm_forward(
-        _ref(p), _ref(x), _ref(residual), _vector(gain_post, x.cols, "gain_post"), _vector(gain_pre, x.cols, "gain_pre"),
-        _one_dtype(gain_post, gain_pre, "gain", gain_dtype), _ref(gate), _ref(sum), _ref(h), _ref(x8), _ref(sum8),
-        _vector(rstd_post, x.rows, "rstd_post", _F32), _vector(rstd_pre, x.rows, "rstd_pre", _F32), _stream(stream)))
-
-
-def _one_dtype(a, b, name, dtype):
-    """The type of two vectors that have one."""
-    if a is None or b is None:
-        return _vector_dtype(b if a is None else a, name, dtype)
-    ta, tb = _vector_dtype(a, name, dtype), _vector_dtype(b, name, dtype)
-    if ta != tb:
-        raise SfError(SF_ERR_INVALID, f"{name}_post and {name}_pre must have one type")
-    return ta
+    rows, cols = x.rows, x.cols
+    gain_post, gain_pre, gain_dtype = _two_vectors(gain_post, gain_pre, cols, "gain", gain_dtype)
+    _check((_lib or load()).sf_sandwich_norm_forward(
+        p, x, _matrix(residual, "residual"), gain_post, gain_pre, gain_dtype, _matrix(gate, "gate"), _matrix(sum, "sum"),
+        _matrix(h, "h"), x8, sum8, _f32(rstd_post, rows, "rstd_post"), _f32(rstd_pre, rows, "rstd_pre"), _stream(stream)))
 
 
 def sf_sandwich_norm_workspace_bytes(rows, cols):
@@ -638,17 +643,20 @@ def sf_sandwich_norm_backward(p, dh=None, dsum=None, x=None, sum=None, gain_post
                               dgate=None, ws=None, stream=None, gain_dtype=None, dgain_dtype=None):
     """The gradients of sf_sandwich_norm_forward; x and sum as tensors, sf_matrix or checkpoint() (ws: a uint8 workspace
     tensor, needed with a dgain or dgate)."""
-    dh, dsum, gate, dgate = _matrix(dh, "dh"), _matrix(dsum, "dsum"), _matrix(gate, "gate"), _matrix(dgate, "dgate")
-    dresidual, dx = _matrix(dresidual, "dresidual"), _matrix(dx, "dx")
-    of = dh if dh is not None else _required(dsum, "dsum (or dh)")
-    (x, x8), (sum, sum8) = _full_or_8(x, "x"), _full_or_8(sum, "sum")
+    dh, dsum = _matrix(dh, "dh"), _matrix(dsum, "dsum")
+    of = dh or dsum
+    if of is None:
+        raise SfError(SF_ERR_INVALID, "dh and dsum are NULL")
+    rows, cols = of.rows, of.cols
+    x, x8 = (None, x) if type(x) is sf_checkpoint else (_matrix(x, "x"), None)
+    sum, sum8 = (None, sum) if type(sum) is sf_checkpoint else (_matrix(sum, "sum"), None)
+    gain_post, gain_pre, gain_dtype = _two_vectors(gain_post, gain_pre, cols, "gain", gain_dtype)
+    dgain_post, dgain_pre, dgain_dtype = _two_vectors(dgain_post, dgain_pre, cols, "dgain", dgain_dtype)
     ws, ws_bytes = _workspace(ws)
-    _check(load().sf_sandwich_norm_backward(
-        _ref(p), _ref(dh), _ref(dsum), x, x8, sum, sum8, _vector(gain_post, of.cols, "gain_post"),
-        _vector(gain_pre, of.cols, "gain_pre"), _one_dtype(gain_post, gain_pre, "gain", gain_dtype), _ref(gate),
-        _vector(rstd_post, of.rows, "rstd_post", _F32), _vector(rstd_pre, of.rows, "rstd_pre", _F32), _ref(dresidual),
-        _ref(dx), _vector(dgain_post, of.cols, "dgain_post"), _vector(dgain_pre, of.cols, "dgain_pre"),
-        _one_dtype(dgain_post, dgain_pre, "dgain", dgain_dtype), _ref(dgate), ws, ws_bytes, _stream(stream)))
+    _check((_lib or load()).sf_sandwich_norm_backward(
+        p, dh, dsum, x, x8, sum, sum8, gain_post, gain_pre, gain_dtype, _matrix(gate, "gate"), _f32(rstd_post, rows, "rstd_post"),
+        _f32(rstd_pre, rows, "rstd_pre"), _matrix(dresidual, "dresidual"), _matrix(dx, "dx"), dgain_post, dgain_pre, dgain_dtype,
+        _matrix(dgate, "dgate"), ws, ws_bytes, _stream(stream)))
 
 
 # ------------------------------------------------------------------ (c) ----

@@ -121,7 +121,7 @@ def _bwd(p=None, **kw):
 
 
 def test_backward_arguments():
-    _refused("dsum .or dh. is NULL", lambda: _bwd(dh=None, dsum=None))
+    _refused("dh and dsum are NULL", lambda: _bwd(dh=None, dsum=None))
     _refused("no gradient", lambda: _bwd(dresidual=None, dx=None, dgain_post=None, dgain_pre=None))
     _refused("dh needs gain_pre", lambda: _bwd(gain_pre=None, dgain_pre=None))
     _refused("dh needs sum", lambda: _bwd(sum=None))
