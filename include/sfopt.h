@@ -535,7 +535,7 @@ typedef struct {
   int32_t group;       /* 32, 64, 128, or 0 */
 } sf_checkpoint;
 
-/* Writes x (SF_BF16 or SF_FP32) as a checkpoint; any number of columns. */
+/* Writes x (SF_BF16 or SF_FP32) as a checkpoint; up to 2^30 columns. */
 sf_status sf_checkpoint_store(const sf_matrix* x, const sf_checkpoint* out,
                               void* stream);
 
@@ -552,16 +552,17 @@ sf_status sf_checkpoint_load(const sf_checkpoint* c, const float* row_factor,
 
 /* The weight gradient of a linear layer y = X W^T from the checkpoint of its
  * input:  dW = base + dY^T X,  dW_oi = base_oi + sum_t dY_to value_ti scale_t.
- *   dY   : SF_BF16 [tokens][out].   c : [tokens][in].   Both 16-byte aligned
- *          base and rows (SF_ERR_UNSUPPORTED otherwise), device memory of the
- *          current device.
+ *   dY   : SF_BF16 [tokens][out].   c : [tokens][in].   With 16-byte aligned
+ *          bases and rows in this device's own memory they take the tensor
+ *          cores, else the CUDA cores.  tokens, out and in below 2^30.
  *   base : NULL (zero), or dW's type and sizes; may be dW itself, to add to it.
  *   dW   : SF_BF16 or SF_FP32 [out][in].
  *   ws   : device scratch of ws_bytes >= sf_checkpoint_wgrad_workspace_bytes(
- *          tokens, out, in), 16-byte aligned; may be NULL where that is 0.
- * Tensor cores, fp32 sums.  value * scale enters as bf16: exact with SF_E8M0
- * scales, rounded once with SF_FP32 ones.  No token: dW = base (or 0).
- * Deterministic. */
+ *          tokens, out, in), 16-byte aligned; may be NULL where that is 0 (few
+ *          tokens).  Larger products hold X there in bf16 while they run.
+ * fp32 sums, rounded to nearest every 512 tokens at least.  value * scale
+ * enters as bf16: exact with SF_E8M0 scales, rounded once with SF_FP32 ones.
+ * No token: dW = base (or 0).  Deterministic. */
 size_t sf_checkpoint_wgrad_workspace_bytes(int64_t tokens, int64_t out,
                                            int64_t in);
 

@@ -264,6 +264,7 @@ sf_status checkpoint_load(const sf_checkpoint* c, const float* row_factor, const
     SF_TRY(check_aligned(gain, dtype_bytes(gain_dtype), "gain"));
     if (!(gain_offset >= -1e30 && gain_offset <= 1e30)) return fail(SF_ERR_INVALID, "gain_offset must be finite");
   }
+  if (y->cols > INT32_MAX / 2) return fail(SF_ERR_UNSUPPORTED, "rows of fewer than 2^30 columns are supported");
   if (!y->rows || !y->cols) return SF_OK;
   CkArgs a{};
   a.y = y->data;
@@ -293,6 +294,7 @@ sf_status sf_checkpoint_store(const sf_matrix* x, const sf_checkpoint* out, void
   NvtxRange nvtx_range("sf_checkpoint_store");
   SF_TRY(check_matrix(x, "x", -1, -1, kTypes));
   SF_TRY(check_checkpoint(out, "checkpoint", x->rows, x->cols, true));
+  if (x->cols > INT32_MAX / 2) return fail(SF_ERR_UNSUPPORTED, "rows of fewer than 2^30 columns are supported");
   if (!x->rows || !x->cols) return SF_OK;
   CkArgs a{};
   a.x = x->data;

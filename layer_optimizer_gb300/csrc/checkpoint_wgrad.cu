@@ -30,10 +30,6 @@
 namespace sf {
 namespace {
 
-#ifndef KRESTORE
-#define KRESTORE -1
-#endif
-constexpr int kRestore = KRESTORE;
 struct WgradArgs {
   const __nv_bfloat16* dy;   // [tokens][ldy]
   const void* base;          // [out][ldbase], may be null or dw
@@ -618,9 +614,13 @@ __global__ void __launch_bounds__(256) k_wgrad_plain(const WgradArgs a) {
     }
 }
 
-// Whether X is restored as a bf16 matrix first: three bytes an element more through memory, for a product whose
-// shared memory carries a third less.
-bool restores(int64_t tokens, int64_t out, int64_t in) { return kRestore >= 0 ? kRestore : (tokens >= 512 && out >= 2048 && in >= 256); }
+// Whether X is restored as a bf16 matrix first: three bytes an element more
+// through memory, for a product whose shared memory carries a third less.  It
+// pays where an element is used often enough (restored / converted on the way,
+// us): 8192 tokens 4096 -> 11008 415 / 516, 4096 -> 4096 177 / 206, 2048 -> 2048 55 / 62,
+// 4096 -> 1024 63 / 62, 1024 -> 1024 27 / 25; 512 tokens 4096 -> 4096 21.9 / 23.5, 2048 ->
+// 2048 10.9 / 10.7; 256 tokens 4096 -> 4096 18.6 / 18.5, 4096 -> 1024 9.7 / 9.3.
+bool restores(int64_t tokens, int64_t out, int64_t in) { return tokens >= 512 && out >= 2048 && in >= 256; }
 int64_t restored_ld(int64_t in) { return ceil_div<int64_t>(in, 64) * 64; }
 size_t restored_bytes(int64_t tokens, int64_t out, int64_t in) {
   return restores(tokens, out, in) ? (size_t)tokens * restored_ld(in) * 2 + 255 & ~(size_t)255 : 0;
@@ -641,7 +641,7 @@ sf_status launch_tc(const WgradArgs& a, const sf_checkpoint* c, void* ws, cudaSt
   g.ws = reinterpret_cast<float*>(static_cast<char*>(ws) + restored_bytes(a.tokens, a.out, a.in));
   const size_t size = a.fp32 ? 4 : 2;
   g.base_vec = a.base && reinterpret_cast<uintptr_t>(a.base) % 16 == 0 && a.ldbase * size % 16 == 0;
-  g.tma = reinterpret_cast<uintptr_t>(a.dw) % 16 == 0 && a.lddw * size % 16 == 0 && on_current_device(a.dw);
+  g.tma = reinterpret_cast<uintptr_t>(a.dw) % 16 == 0 && a.lddw * size % 16 == 0 && a.lddw >= a.in && on_current_device(a.dw);
   const int64_t m_tiles = ceil_div<int64_t>(a.out, kPair * kBM), n_tiles = ceil_div<int64_t>(a.in, kBN);
   if (m_tiles * n_tiles > INT32_MAX / 2) return fail(SF_ERR_UNSUPPORTED, "too many tiles");
   int pairs = 0;
@@ -732,7 +732,8 @@ sf_status sf_checkpoint_wgrad(const sf_matrix* dY, const sf_checkpoint* c, const
   a.in = in;
   a.fp32 = dW->dtype == SF_FP32;
   a.ck = device_ck(c);
-  if (tokens && dY->ld % 8 == 0 && c->values.ld % 16 == 0 && reinterpret_cast<uintptr_t>(dY->data) % 16 == 0 &&
+  if (need && !on_current_device(ws)) return fail(SF_ERR_INVALID, "ws must be device memory of the current device");
+  if (tokens && dY->ld % 8 == 0 && dY->ld >= out && c->values.ld % 16 == 0 && c->values.ld >= in && reinterpret_cast<uintptr_t>(dY->data) % 16 == 0 &&
       reinterpret_cast<uintptr_t>(c->values.data) % 16 == 0 && tensor_map_encoder() && on_current_device(dY->data) &&
       on_current_device(c->values.data))
     return launch_tc(a, c, ws, as_stream(stream));

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(T, T == kBwdFew ? 2 : 1) k_sandwich_bwd(const 
         }
         if (post) {
           F8 w = load_vec<LAY>(a.v.g_post, a.v.gain_fp32, c0, l.dj, cols, a.v.offset);
-          if (gate) w = mul8(w, load_vec<LAY>(gate, a.v.gate_fp32, c0, l.dj, cols, 0.0f));
+          if (gate) w = mul8(w, load8_any<LAY>(gate, a.v.gate_fp32, c0, l.dj, cols));
           w = mul8(w, x[q]);
           m[1] += dot8(w, e[q]);
           m[2] += dot8(w, s[q]);
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(T, T == kBwdFew ? 2 : 1) k_sandwich_bwd(const 
           for (int i4 = 0; i4 < 4; ++i4) accT[q].p[i4] = fmadd2(d.p[i4], x[q].p[i4], accT[q].p[i4]);
         }
         if (a.dx) {
-          if (gate) d = mul8(d, load_vec<LAY>(gate, a.v.gate_fp32, c0, l.dj, cols, 0.0f));
+          if (gate) d = mul8(d, load8_any<LAY>(gate, a.v.gate_fp32, c0, l.dj, cols));
           if (post) {
             d = mul8(d, load_vec<LAY>(a.v.g_post, a.v.gain_fp32, c0, l.dj, cols, a.v.offset));
 #pragma unroll
@@ -104,19 +104,19 @@ __global__ void __launch_bounds__(T, T == kBwdFew ? 2 : 1) k_sandwich_bwd(const 
       for (int q = 0; q < kBwdK; ++q) {
         const int c0 = l.c0(q);
         if (c0 >= a.cols) continue;
+        if (a.tpart) {      // (before dgate, which may be the gate's own memory)
+          // this worker's own row, written and read by the same threads
+          float* part = a.tpart + worker * a.cols;
+          F8 v = round ? load8<kStrided>(part, c0, l.dj, a.cols) : zero8();
+          const F8 g = load8_any<LAY>(gate, a.v.gate_fp32, c0, l.dj, a.cols);
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) v.p[i4] = fmadd2(accT[q].p[i4], g.p[i4], v.p[i4]);
+          store8<kStrided>(part, c0, l.dj, a.cols, v);
+        }
         if (a.dgate) {
           F8 v = accT[q];
           if (post) v = mul8(v, load_vec<LAY>(a.v.g_post, a.v.gain_fp32, c0, l.dj, a.cols, a.v.offset));
           store_any<LAY>(static_cast<char*>(a.dgate) + k * a.lddgate * (a.dgate_fp32 ? 4 : 2), a.dgate_fp32, c0, l.dj, a.cols, v);
-        }
-        if (a.tpart) {
-          // this worker's own row, written and read by the same threads
-          float* part = a.tpart + worker * a.cols;
-          F8 v = round ? load8<kStrided>(part, c0, l.dj, a.cols) : zero8();
-          const F8 g = load_vec<LAY>(gate, a.v.gate_fp32, c0, l.dj, a.cols, 0.0f);
-#pragma unroll
-          for (int i4 = 0; i4 < 4; ++i4) v.p[i4] = fmadd2(accT[q].p[i4], g.p[i4], v.p[i4]);
-          store8<kStrided>(part, c0, l.dj, a.cols, v);
         }
         accT[q] = zero8();
       }
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(1024) k_sandwich_join(const JoinArgs a) {
       if (on) {
 #pragma unroll 8
         for (int p = 0; p < a.parts; ++p) v += a.tpart[(k * a.parts + p) * a.cols + c];
+        dg1 = fmaf(vec_at(a.v.gate, a.v.gate_fp32, k * a.v.ld_gate + c), v, dg1);      // (before: dgate may be the gate's own memory)
         if (a.dgate) put_at(a.dgate, a.dgate_fp32, k * a.lddgate + c, g1c * v);
-        dg1 = fmaf(vec_at(a.v.gate, a.v.gate_fp32, k * a.v.ld_gate + c), v, dg1);
       }
     }
     dg1 = join32(dg1, red[0]);
@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(1024) k_sandwich_join(const JoinArgs a) {
     for (int64_t k0 = 0; k0 < a.gate_rows; k0 += 4) {
       float v[4] = {};
       if (on) {
+#pragma unroll 4
         for (int p = threadIdx.y; p < a.parts; p += 32)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -223,8 +224,8 @@ __global__ void __launch_bounds__(1024) k_sandwich_join(const JoinArgs a) {
         for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
         const int64_t k = k0 + i;
         if (!writes || k >= a.gate_rows) continue;
-        if (a.dgate) put_at(a.dgate, a.dgate_fp32, k * a.lddgate + out, g1 * v[i]);
         dg1 = fmaf(vec_at(a.v.gate, a.v.gate_fp32, k * a.v.ld_gate + out), v[i], dg1);
+        if (a.dgate) put_at(a.dgate, a.dgate_fp32, k * a.lddgate + out, g1 * v[i]);
       }
     }
   }

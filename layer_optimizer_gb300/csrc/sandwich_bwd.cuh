@@ -50,6 +50,23 @@ struct BwdArgs {
 
 namespace {
 
+// A gate's row: not by the read-only path, since dgate may be the same memory
+// (each row of it is read and written by one worker only).
+template <int LAY>
+__device__ __forceinline__ F8 load8_any(const void* row, int fp32, int c0, int dj, int cols) {
+  if (LAY == kUnits && c0 + 8 <= cols) {
+    if (fp32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + c0);
+      const float4 x = p[0], y = p[1];
+      return F8{{pack_f2(x.x, x.y), pack_f2(x.z, x.w), pack_f2(y.x, y.y), pack_f2(y.z, y.w)}};
+    }
+    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c0);
+    Unit<__nv_bfloat16> u;
+    u.w[0] = w.x, u.w[1] = w.y, u.w[2] = w.z, u.w[3] = w.w;
+    return unpack(u);
+  }
+  return fp32 ? load8<kStrided>(static_cast<const float*>(row), c0, dj, cols) : load8<kStrided>(static_cast<const __nv_bfloat16*>(row), c0, dj, cols);
+}
 template <int LAY>
 __device__ __forceinline__ void store_any(void* row, int fp32, int c0, int dj, int cols, const F8& v) {
   if (fp32) store8<LAY>(static_cast<float*>(row), c0, dj, cols, v);

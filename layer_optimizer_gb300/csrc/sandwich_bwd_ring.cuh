@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
     F8 v[2];
     if (POST) vec(a.v.g_post, a.v.gain_fp32, a.v.offset, w);
     if (gate) {
-      vec(gate, a.v.gate_fp32, 0.0f, v);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[h] = load8_any<LAY>(gate, a.v.gate_fp32, c + (LAY == kUnits ? 8 : 256) * h, LAY == kUnits ? 1 : 32, a.cols);
       w[0] = mul8(w[0], v[0]), w[1] = mul8(w[1], v[1]);
     }
   };
@@ -133,18 +134,18 @@ __global__ void __launch_bounds__(kBwdRingThreads) k_sandwich_bwd_ring(const Bwd
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int ch = c + kNext * h;
+      if (on && a.tpart) {      // (before dgate, which may be the gate's own memory) this worker's own row, written and read by the same threads (on 16 bytes at least: no wide access)
+        float* part = a.tpart + (int64_t)worker * a.cols;
+        F8 v = first ? zero8() : load8<kStrided>(part, ch, kApart, a.cols);
+        const F8 g = load8_any<LAY>(gate, a.v.gate_fp32, ch, kApart, a.cols);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v.p[i] = fmadd2(accT[h].p[i], g.p[i], v.p[i]);
+        store8<kStrided>(part, ch, kApart, a.cols, v);
+      }
       if (on && a.dgate) {
         F8 v = accT[h];
         if (POST) v = mul8(v, load_vec<LAY>(a.v.g_post, a.v.gain_fp32, ch, kApart, a.cols, a.v.offset));
         store_any<LAY>(static_cast<char*>(a.dgate) + (int64_t)gate_row * a.lddgate * (a.dgate_fp32 ? 4 : 2), a.dgate_fp32, ch, kApart, a.cols, v);
-      }
-      if (on && a.tpart) {      // this worker's own row, written and read by the same threads (on 16 bytes at least: no wide access)
-        float* part = a.tpart + (int64_t)worker * a.cols;
-        F8 v = first ? zero8() : load8<kStrided>(part, ch, kApart, a.cols);
-        const F8 g = load_vec<LAY>(gate, a.v.gate_fp32, ch, kApart, a.cols, 0.0f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v.p[i] = fmadd2(accT[h].p[i], g.p[i], v.p[i]);
-        store8<kStrided>(part, ch, kApart, a.cols, v);
       }
       accT[h] = zero8();
     }

@@ -54,6 +54,9 @@ def test_checkpoint_arguments():
     _refused("gain: type 2", lambda: load(gain=AT, gain_dtype=E4), native.SF_ERR_UNSUPPORTED)
     _refused("gain_offset", lambda: load(gain=AT, gain_dtype=BF, gain_offset=float("nan")))
     _refused("gain_dtype", lambda: load(gain=AT))
+    wide = 1 << 30
+    _refused("2\\^30 columns", lambda: native.sf_checkpoint_store(_m(1, wide, BF), _c(1, wide)), native.SF_ERR_UNSUPPORTED)
+    _refused("2\\^30 columns", lambda: native.sf_checkpoint_load(_c(1, wide), _m(1, wide, BF)), native.SF_ERR_UNSUPPORTED)
     # nothing to do
     native.sf_checkpoint_store(_m(0, 64, BF), _c(0, 64))
     native.sf_checkpoint_load(_c(0, 64, scale=None), _m(0, 64, F32))
@@ -75,6 +78,13 @@ def test_weight_gradient_arguments():
     _refused("base: type 0", lambda: call(base=_m(64, 96, BF)), native.SF_ERR_UNSUPPORTED)
     _refused("base is 64 x 95", lambda: call(base=_m(64, 95, F32)))
     native.sf_checkpoint_wgrad(_m(40, 0, BF), _c(40, 96), _m(0, 96, F32), ws=ws)
+    # a workspace that is needed: too small, missing, or no memory of this device (an address that the driver does not know)
+    dy, c, dw = _m(4096, 4096, BF), _c(4096, 4096), _m(4096, 4096, BF)
+    need = native.sf_checkpoint_wgrad_workspace_bytes(4096, 4096, 4096)
+    assert need > 2 * 4096 * 4096 and native.sf_checkpoint_wgrad_workspace_bytes(64, 4096, 4096) == 0
+    _refused(f"workspace needs {need}", lambda: native.sf_checkpoint_wgrad(dy, c, dw))
+    ws.nbytes = need
+    _refused("ws must be device memory", lambda: native.sf_checkpoint_wgrad(dy, c, dw, ws=ws))
 
 
 FULL = dict(residual=_m(8, 64, BF), gain_post=AT, gain_pre=AT, gain_dtype=F32, sum=_m(8, 64, BF), h=_m(8, 64, BF))

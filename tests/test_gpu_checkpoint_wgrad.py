@@ -106,6 +106,18 @@ def test_fp32_scales(cin, group):
     close("dw", dw, ref, (2.0 ** -8 + _sum(tokens)) * mag)
 
 
+def test_operands_in_pinned_host_memory():
+    tokens, out, cin = 100, 64, 96
+    dy = synth.normal((tokens, out), 1.0, 73).to(BF).pin_memory()
+    ck, q, scale = make_checkpoint(synth.normal((tokens, cin), 1.0, 74).to(BF).to(DEV), 32)
+    hq, hs = q.cpu().pin_memory(), scale.view(torch.uint8).cpu().pin_memory()
+    dw = torch.empty(out, cin, device=DEV)
+    native.sf_checkpoint_wgrad(dy, native.checkpoint(hq, hs, 32), dw)
+    native.sf_sync_status()
+    ref, mag = oc.weight_grad(f64(dy.float()), oc.restore(f64(q.float()), f64(scale.float()), 32))
+    close("dw", dw, ref, stored(F32, ref, _sum(tokens) * mag))
+
+
 def test_no_tokens_give_the_base():
     dy, q = torch.empty(0, 64, dtype=BF, device=DEV), torch.empty(0, 48, dtype=E4, device=DEV)
     ck = native.checkpoint(q, torch.empty(0, 2, dtype=torch.uint8, device=DEV), 32)

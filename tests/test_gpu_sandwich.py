@@ -215,6 +215,86 @@ def test_gradients_over_their_inputs():
     _check_backward(out, ref, BF, BF)
 
 
+@pytest.mark.parametrize("rows,cols,gates", [(500, 1024, 2), (700, 1024, 650), (64, 264, 3), (900, 72, 900), (400, 1003, 2), (3000, 264, 1500)])
+def test_the_gates_gradient_over_the_gate(rows, cols, gates):
+    p, kw, ref = _backward_case(rows, cols, 0, 0, BF, BF, F32, gates, True, True, True, None, 1.0, 0.5, 0.0)
+    out = _outputs(rows, cols, 0, 0, BF, BF, kw)
+    out["dgate"] = kw["gate"]
+    native.sf_sandwich_norm_backward(p, **kw, **out)
+    native.sf_sync_status()
+    _check_backward(out, ref, BF, BF)
+
+
+def test_two_streams_at_once():
+    made = []
+    for rows, cols, gates, group in ((2000, 2048, 3, 64), (777, 1003, 0, None)):
+        p, kw, ref = _backward_case(rows, cols, 0, 0, BF, BF, BF, gates, True, True, True, group, 1.0, 0.5, 0.0)
+        made.append((p, kw, ref, _outputs(rows, cols, 0, 0, BF, BF, kw), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for p, kw, ref, out, stream in made:
+            native.sf_sandwich_norm_backward(p, **kw, **out, stream=stream)
+    torch.cuda.synchronize()
+    for p, kw, ref, out, stream in made:
+        _check_backward(out, ref, BF, BF)
+
+
+def test_pinned_host_rows_give_the_formulas_results():
+    rows, cols = 400, 1024
+    p, kw, ref = _backward_case(rows, cols, 0, 0, BF, BF, F32, 2, True, True, True, None, 1.0, 0.5, 0.0)
+    out = _outputs(rows, cols, 0, 0, BF, BF, kw)
+    for k in ("dh", "dsum", "x", "sum"):
+        kw[k] = kw[k].cpu().contiguous().pin_memory()
+    for k in ("dresidual", "dx"):
+        out[k] = torch.empty(rows, cols, dtype=BF).pin_memory()
+    native.sf_sandwich_norm_backward(p, **kw, **out)
+    native.sf_sync_status()
+    _check_backward(out, ref, BF, BF)
+    x, r, h, s = kw["x"], kw["sum"], out["dx"], out["dresidual"]
+    g = torch.ones(cols, device=DEV)
+    native.sf_sandwich_norm_forward(native.sandwich(EPS), x, r, gain_post=g, gain_pre=g, sum=s, h=h)
+    native.sf_sync_status()
+    f = osw.forward(_np(x), _np(r), np.ones(cols), np.ones(cols), None, 0, 1.0, 1.0, EPS)
+    es = 72 * U * np.abs(f["branch"]) + 2 * U * (np.abs(f["s"]) + np.abs(f["branch"]))
+    close("sum", s, f["s"], stored(BF, f["s"], es))
+
+
+@pytest.mark.parametrize("rows,cols,pad", [(400, 1024, 8), (400, 2064, 8), (400, 1024, 4), (320, 5008, 1), (310, 8192, 8), (330, 257, 0), (5000, 256, 8)])
+@pytest.mark.parametrize("group", [None, 0, 32, 128])
+def test_rows_next_to_units(rows, cols, pad, group):
+    # rows on units of 8 or 4 columns, off them, many enough for every form
+    x, _ = rows_of(rows, cols, pad, BF, 61, 1.5)
+    r, _ = rows_of(rows, cols, pad, F32, 62, 2.0)
+    g = _gain(cols, BF, 63)
+    gate, span = _gate(rows, cols, 3, BF, 64)
+    s, sbuf = rows_of(rows, cols, pad, F32)
+    h, hbuf = rows_of(rows, cols, pad, BF)
+    x8 = s8 = None
+    if group is not None:
+        x8, q1, c1, b1 = new_checkpoint(rows, cols, group, pad)
+        s8, q2, c2, b2 = new_checkpoint(rows, cols, group, pad)
+    rho1, rho2 = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    p = native.sandwich(EPS, 1.0, 0.5, 0.0, span)
+    native.sf_sandwich_norm_forward(p, x, r, gain_post=g, gain_pre=g, gate=gate, sum=s, h=h, x8=x8, sum8=s8, rstd_post=rho1, rstd_pre=rho2)
+    native.sf_sync_status()
+    f = osw.forward(_np(x), _np(r), _np(g), _np(g), _np(gate), span, 1.0, 0.5, EPS)
+    es = 72 * U * np.abs(f["branch"]) + 2 * U * (np.abs(f["s"]) + np.abs(f["branch"]))
+    close("sum", s, f["s"], stored(F32, f["s"], es))
+    rel = 64 * U + np.mean(es * np.abs(f["s"]), axis=1) * f["rho2"] ** 2
+    close("h", h, f["h"], stored(BF, f["h"], np.abs(f["h"]) * (rel + 4 * U)[:, None] + es * f["rho2"][:, None] * np.abs(_np(g))))
+    assert guard_ok(s, sbuf) and guard_ok(h, hbuf)
+    if group is not None:
+        rq, rs = oc.quantize(_np(x), group)
+        assert np.array_equal(f64(q1.float()), rq) and np.array_equal(f64(c1.float()).reshape(rs.shape), rs)
+        _check_8("sum8", q2, c2, f["s"], es, group)
+        assert guard_ok(q1, b1) and guard_ok(q2, b2)
+    p, kw, ref = _backward_case(rows, cols, pad, 0, BF, F32, BF, 3, True, True, True, group, 1.0, 0.5, 0.0)
+    out = _outputs(rows, cols, pad, 0, BF, F32, kw)
+    native.sf_sandwich_norm_backward(p, **kw, **out)
+    native.sf_sync_status()
+    _check_backward(out, ref, BF, F32)
+
+
 def test_no_rows():
     cols = 72
     e = torch.empty(0, cols, dtype=BF, device=DEV)
