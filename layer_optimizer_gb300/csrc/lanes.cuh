@@ -119,14 +119,18 @@ __device__ __forceinline__ F8 load_vec(const void* v, int fp32, int c0, int dj, 
       b.w[0] = w.x, b.w[1] = w.y, b.w[2] = w.z, b.w[3] = w.w;
       pack(unpack(b), u);
     }
-  } else {
+  } else {      // all eight under way before the first is used
+    const int d = LAY == kUnits ? 1 : dj;
+    uint32_t raw[8];
+    if (fp32) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = c0 + j * (LAY == kUnits ? 1 : dj);
-      u.f[j] = c >= cols ? 0.0f
-               : fp32    ? __ldg(static_cast<const float*>(v) + c)
-                         : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(v) + c) << 16);
+      for (int j = 0; j < 8; ++j) raw[j] = __float_as_uint(__ldg(static_cast<const float*>(v) + min(c0 + j * d, cols - 1)));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) raw[j] = (uint32_t)__ldg(static_cast<const uint16_t*>(v) + min(c0 + j * d, cols - 1)) << 16;
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u.f[j] = c0 + j * d < cols ? __uint_as_float(raw[j]) : 0.0f;
   }
   F8 r = unpack(u);
   const uint64_t a = pack_f2(add, add);
