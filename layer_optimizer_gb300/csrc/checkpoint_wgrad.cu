@@ -2,13 +2,18 @@
 // input: dW = base + dY^T X, X = value * scale, on the tensor cores.
 //
 // The pair form of tc_gemm.cu (256 x 256 tiles of dW by clusters of two CTAs,
-// tcgen05.mma into tensor memory), with X turned into bf16 on the way: a CTA's
-// 64-token slab of the checkpoint (64 x 128 values, 8 KB by TMA) is read from
-// shared memory by four converter warps, multiplied by its scales and written
-// as the swizzled MN-major operand that the MMA reads (16 KB).  So the
-// activations are never restored in memory, at 1 byte an element instead of
-// the 5 of a restore and a bf16 product.  With power-of-two scales value *
-// scale is exact in bf16.
+// tcgen05.mma into tensor memory), with X turned into bf16 in one of two places
+// (restores(), below).  On the way: a CTA's 64-token slab of the checkpoint (64 x
+// 128 values, 8 KB by TMA) is read from shared memory by four converter warps,
+// multiplied by its scales and written as the swizzled MN-major operand that
+// the MMA reads (16 KB); three such groups take the slabs in turn, and the
+// activations are never restored in memory.  Or before: a launch of its own
+// restores X in the workspace, and slabs of it are copied by TMA as dY's are.
+// With power-of-two scales value * scale is exact in bf16.
+//
+// 8192 tokens, 4096 -> 11008, bf16: 418 us with X restored first (1769 TFLOP/s, the
+// tensor pipe 80 % busy in its 388 us), 516 us converted on the way; 4096 -> 1024
+// converted 62 us (tensor pipe 43 %: 64 tiles on 76 pairs).
 //
 // Sums: the tensor cores cut the low bits of their fp32 accumulator at every
 // step, which shrinks a long sum (measured on 4096 tokens 4e-6 of it, on 16384
@@ -614,8 +619,8 @@ __global__ void __launch_bounds__(256) k_wgrad_plain(const WgradArgs a) {
     }
 }
 
-// Whether X is restored as a bf16 matrix first: three bytes an element more
-// through memory, for a product whose shared memory carries a third less.  It
+// Whether X is restored as a bf16 matrix first: more bytes through
+// memory, for a product without conversions beside it.  It
 // pays where an element is used often enough (restored / converted on the way,
 // us): 8192 tokens 4096 -> 11008 415 / 516, 4096 -> 4096 177 / 206, 2048 -> 2048 55 / 62,
 // 4096 -> 1024 63 / 62, 1024 -> 1024 27 / 25; 512 tokens 4096 -> 4096 21.9 / 23.5, 2048 ->
