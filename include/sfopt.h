@@ -556,7 +556,8 @@ sf_status sf_checkpoint_load(const sf_checkpoint* c, const float* row_factor,
  *          bases and rows in this device's own memory they take the tensor
  *          cores, else the CUDA cores.  tokens, out and in below 2^30.
  *   base : NULL (zero), or dW's type and sizes; may be dW itself, to add to it.
- *   dW   : SF_BF16 or SF_FP32 [out][in].
+ *   dW   : SF_BF16 or SF_FP32 [out][in]; of the inputs only base may be the
+ *          same matrix.
  *   ws   : device scratch of ws_bytes >= sf_checkpoint_wgrad_workspace_bytes(
  *          tokens, out, in), 16-byte aligned; may be NULL where that is 0 (few
  *          tokens).  Larger products hold X there in bf16 while they run.

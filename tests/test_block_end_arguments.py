@@ -78,6 +78,9 @@ def test_weight_gradient_arguments():
     _refused("base: type 0", lambda: call(base=_m(64, 96, BF)), native.SF_ERR_UNSUPPORTED)
     _refused("base is 64 x 95", lambda: call(base=_m(64, 95, F32)))
     native.sf_checkpoint_wgrad(_m(40, 0, BF), _c(40, 96), _m(0, 96, F32), ws=ws)
+    # every output reads all tokens of both operands
+    _refused("must not lie over", lambda: native.sf_checkpoint_wgrad(_m(40, 40, BF, 2 * AT), _c(40, 40), _m(40, 40, BF, 2 * AT)))
+    _refused("must not lie over", lambda: native.sf_checkpoint_wgrad(_m(40, 64, BF, 2 * AT), _c(40, 96), dw))
     # a workspace that is needed: too small, missing, or no memory of this device (an address that the driver does not know)
     dy, c, dw = _m(4096, 4096, BF), _c(4096, 4096), _m(4096, 4096, BF)
     need = native.sf_checkpoint_wgrad_workspace_bytes(4096, 4096, 4096)
