@@ -625,7 +625,8 @@ sf_status sf_sandwich_norm_forward(const sf_sandwich* p, const sf_matrix* x,
  *          or dgate (and dx, dgain_post or dgate wanted), sum with dh.
  *   dresidual (the sum's type), dx (x's type), dgain_post, dgain_pre ([cols],
  *          dgain_dtype bf16 or fp32), dgate (the gate's sizes, bf16 or fp32):
- *          each NULL: not wanted, not all.
+ *          each NULL: not wanted, not all.  dgate may be the gate itself,
+ *          dresidual and dx may not.
  *   ws   : device scratch of ws_bytes >= sf_sandwich_norm_workspace_bytes(rows,
  *          cols), 16-byte aligned; only used with a dgain or dgate.
  * fp32 arithmetic, one rounding at the end; sums over rows run in a fixed

@@ -314,6 +314,9 @@ sf_status sf_sandwich_norm_backward(const sf_sandwich* p, const sf_matrix* dh, c
     if (!ws || ws_bytes < need || reinterpret_cast<uintptr_t>(ws) % 16)
       return fail(SF_ERR_INVALID, "workspace needs %zu bytes, 16-byte aligned (got %zu)", need, ws_bytes);
   }
+  // (the gate is read again for its products and for dgain_post)
+  if (rows && gate && ((dresidual && dresidual->data == gate->data) || (dx && dx->data == gate->data)))
+    return fail(SF_ERR_INVALID, "dresidual and dx must not lie over the gate");
   // where only the residual's gradient is wanted, the branch is left out
   if (!dx && !wants_t) a.v.g_post = nullptr, x = nullptr, x8 = nullptr;
   if (!dh) a.v.g_pre = nullptr, sum = nullptr, sum8 = nullptr;

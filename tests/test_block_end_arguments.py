@@ -152,6 +152,10 @@ def test_backward_arguments():
     _refused("dgain_pre is not aligned", lambda: _bwd(dgain_pre=AT + 2))
     _refused("dgate is 2 x 64", lambda: _bwd(gate=_m(1, 64, F32), dgate=_m(2, 64, F32)))
     _refused("gate is 1 x 64, expected 4 x 64", lambda: _bwd(native.sandwich(1e-5, gate_span=2), gate=_m(1, 64, F32)))
+    p = native.sandwich(1e-5, gate_span=1)
+    for out in ("dresidual", "dx"):
+        others = {"dresidual": _m(8, 64, BF, 2 * AT), "dx": _m(8, 64, BF, 2 * AT)}
+        _refused("must not lie over the gate", lambda: _bwd(p, gate=_m(8, 64, BF), **dict(others, **{out: _m(8, 64, BF)})))
     need = native.sf_sandwich_norm_workspace_bytes(8, 64)
     _refused(f"workspace needs {need} bytes", lambda: _bwd(ws_bytes=need - 1))
     _refused("workspace needs", lambda: _bwd(ws=None))
