@@ -10,10 +10,12 @@ namespace sf {
 namespace {
 
 // Steps a thread holds in registers; of narrow accesses one, whose eight loads
-// an operand keep memory busy with more threads (16384 x 4095 bf16: loaded with
-// the norm's factors in 148 us, with four steps 256; stored in 174 us, with four 165).
+// an operand keep memory busy with more threads.  Loading, two (16384 x 4088 bf16 with
+// the norm's factors 69 us; four, of 119 registers, 101; one 87).
 template <int LAY>
 constexpr int kK = LAY == kUnits ? 4 : 1;
+template <int LAY>
+constexpr int kLoadK = LAY == kUnits ? 2 : 1;
 constexpr int kMaxThreads = 512;
 
 struct CkArgs {
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_checkpoint_load(const CkArgs a)
   const int64_t row = (int64_t)blockIdx.x * a.rpb + lane_row;
   if (row >= a.rows) return;
   const Lane l = lane_of<LAY>(t, tpr);
-  const int64_t seg = (int64_t)tpr * kK<LAY> * 8;
+  const int64_t seg = (int64_t)tpr * kLoadK<LAY> * 8;
   const float f = a.row_factor ? a.row_factor[row] : 1.0f;
   const uint64_t f2 = pack_f2(f, f);
   for (int64_t s = 0; s < a.steps; ++s) {
@@ -90,12 +92,12 @@ __global__ void __launch_bounds__(kMaxThreads) k_checkpoint_load(const CkArgs a)
     const int64_t at = ck.group_log2 ? (s * seg) >> ck.group_log2 : 0;
     if (ck.s8) ck.s8 += at;
     else ck.s32 += at;
-    F8 v[kK<LAY>];
+    F8 v[kLoadK<LAY>];
 #pragma unroll
-    for (int k = 0; k < kK<LAY>; ++k)
+    for (int k = 0; k < kLoadK<LAY>; ++k)
       if (l.c0(k) < n) v[k] = load8<LAY>(ck, row, l.c0(k), l.dj, n);
 #pragma unroll
-    for (int k = 0; k < kK<LAY>; ++k) {
+    for (int k = 0; k < kLoadK<LAY>; ++k) {
       if (l.c0(k) >= n) continue;
       if (a.row_factor) {
 #pragma unroll
@@ -197,10 +199,109 @@ __global__ void __launch_bounds__(kWideThreads) k_checkpoint_load_wide(const CkA
   }
 }
 
+// Rows off their units, a warp for 512 columns of a row: lane, lane + 32, ..,
+// at constant distances, all loads under way before the first is used, and
+// nothing shared between warps.  16384 x 4095 bf16: stored with groups of 128 in 54 us (3.7
+// TB/s; 173 by the form above), loaded with the norm's factors in 68 (152); fp32, with groups
+// of 64, stored in 64 (190).
+constexpr int kRowWarps = 8;      // neighbouring rows of a block
+
+template <bool WHOLE>
+__device__ __forceinline__ void load_chunk(const __nv_bfloat16* p, int left, F8 (&v)[2]) {
+  const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+  uint32_t w[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[j] = WHOLE || 32 * j < left ? q[32 * j] : 0u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j >> 2].p[j & 3] = pack_f2(__uint_as_float(w[2 * j] << 16), __uint_as_float(w[2 * j + 1] << 16));
+}
+template <bool WHOLE>
+__device__ __forceinline__ void load_chunk(const float* p, int left, F8 (&v)[2]) {
+  float w[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[j] = WHOLE || 32 * j < left ? p[32 * j] : 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j >> 2].p[j & 3] = pack_f2(w[2 * j], w[2 * j + 1]);
+}
+template <bool WHOLE>
+__device__ __forceinline__ void store_chunk(__nv_bfloat16* p, int left, const F8 (&v)[2]) {
+  uint16_t* q = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    Unit<__nv_bfloat16> u;
+    pack(v[h], u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (WHOLE || 32 * (8 * h + j) < left) q[32 * (8 * h + j)] = (uint16_t)(u.w[j >> 1] >> (16 * (j & 1)));
+  }
+}
+template <bool WHOLE>
+__device__ __forceinline__ void store_chunk(float* p, int left, const F8 (&v)[2]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float2 x = unpack_f2(v[j >> 2].p[j & 3]);
+    if (WHOLE || 64 * j < left) p[64 * j] = x.x;
+    if (WHOLE || 64 * j + 32 < left) p[64 * j + 32] = x.y;
+  }
+}
+
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void store_rows_chunk(const CkArgs& a, int64_t row, int c) {
+  F8 v[2];
+  load_chunk<WHOLE>(row_ptr<T>(a.x, a.ldx, row) + c, (int)a.cols - c, v);
+  ck_store16_strided<WHOLE>(a.ck, row, c, (int)a.cols, v, 1);
+}
+// With scale groups.
+template <typename T>
+__global__ void __launch_bounds__(32 * kRowWarps) k_checkpoint_store_rows(const CkArgs a, const uint32_t chunks) {
+  const uint32_t block = blockIdx.x / chunks, chunk = blockIdx.x - block * chunks;
+  const int64_t row = (int64_t)block * kRowWarps + (threadIdx.x >> 5);
+  if (row >= a.rows) return;
+  const int c = (int)(chunk * 512 + (threadIdx.x & 31));
+  if (chunk * 512 + 512 <= a.cols) store_rows_chunk<T, true>(a, row, c);
+  else store_rows_chunk<T, false>(a, row, c);
+}
+
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void load_rows_chunk(const CkArgs& a, int64_t row, int c) {
+  const int left = (int)a.cols - c, lane = threadIdx.x & 31;
+  const uint8_t* p = a.ck.q + row * a.ck.ld + c;
+  uint32_t q[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) q[j] = WHOLE || 32 * j < left ? p[32 * j] : 0u;
+  // the scale of the lane's block of 32 columns (of lane j: block j)
+  const int64_t at = row * a.ck.n_groups + (a.ck.group_log2 ? min((c - lane + 32 * (lane & 15)) >> a.ck.group_log2, a.ck.n_groups - 1) : 0);
+  const float mine = a.ck.s8 ? e8m0_value(a.ck.s8[at]) : a.ck.s32[at];
+  const float f = a.row_factor ? a.row_factor[row] : 1.0f;
+  F8 g[2];
+  if (a.gain) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) g[h] = load_vec<kStrided>(a.gain, a.gain_fp32, c + 256 * h, 32, (int)a.cols, a.gain_offset);
+  }
+  F8 v[2];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float2 x = e4m3x2_value(q[2 * j] | q[2 * j + 1] << 8);
+    uint64_t y = fmul2(pack_f2(x.x, x.y), pack_f2(__shfl_sync(0xffffffffu, mine, 2 * j), __shfl_sync(0xffffffffu, mine, 2 * j + 1)));
+    if (a.row_factor) y = fmul2(y, pack_f2(f, f));
+    if (a.gain) y = fmul2(y, g[j >> 2].p[j & 3]);
+    v[j >> 2].p[j & 3] = y;
+  }
+  store_chunk<WHOLE>(row_ptr<T>(a.y, a.ldx, row) + c, left, v);
+}
+template <typename T>
+__global__ void __launch_bounds__(32 * kRowWarps) k_checkpoint_load_rows(const CkArgs a, const uint32_t chunks) {
+  const uint32_t block = blockIdx.x / chunks, chunk = blockIdx.x - block * chunks;
+  const int64_t row = (int64_t)block * kRowWarps + (threadIdx.x >> 5);
+  if (row >= a.rows) return;
+  const int c = (int)(chunk * 512 + (threadIdx.x & 31));
+  if (chunk * 512 + 512 <= a.cols) load_rows_chunk<T, true>(a, row, c);
+  else load_rows_chunk<T, false>(a, row, c);
+}
+
 // Threads a row: a power of two up to 64 (at least 16, a group of 128 columns), or whole warps.
-void pick_shape(CkArgs& a, Lay lay) {
+void pick_shape(CkArgs& a, int held) {
   const int64_t units = ceil_div<int64_t>(a.cols, 8);
-  const int held = lay == kUnits ? kK<kUnits> : kK<kStrided>;
   const int64_t per = a.rows < 2 * sm_count() ? 1 : held;
   const int64_t t = std::min<int64_t>(ceil_div<int64_t>(units, per), kMaxThreads);
   if (t > 64) {
@@ -253,6 +354,19 @@ sf_status launch(const void* kernel, CkArgs& a, cudaStream_t stream, const char*
   return SF_OK;
 }
 
+// Whether the form for rows off their units takes a call: not short rows, which leave its
+// lanes without work (us, so / by the form above; stored and loaded: 65536 x 129 43 / 46
+// and 32 / 32, 60000 x 257 40 / 83 and 30 / 57, 200000 x 33 126 / 70 and 93 / 46).
+bool takes_rows(const CkArgs& a) {
+  return a.cols > 128 && ceil_div<int64_t>(a.rows, kRowWarps) * ceil_div<int64_t>(a.cols, 512) <= INT32_MAX;
+}
+sf_status launch_rows(const void* kernel, CkArgs& a, cudaStream_t stream, const char* what) {
+  uint32_t chunks = (uint32_t)ceil_div<int64_t>(a.cols, 512);
+  void* args[] = {&a, &chunks};
+  SF_CUDA_TRY(cudaLaunchKernel(kernel, dim3((unsigned)(ceil_div<int64_t>(a.rows, kRowWarps) * chunks)), dim3(32 * kRowWarps), args, 0, stream), what);
+  return SF_OK;
+}
+
 }  // namespace
 
 sf_status checkpoint_load(const sf_checkpoint* c, const float* row_factor, const void* gain, int32_t gain_dtype,
@@ -281,7 +395,10 @@ sf_status checkpoint_load(const sf_checkpoint* c, const float* row_factor, const
     return launch_wide(y->dtype == SF_BF16 ? (const void*)&k_checkpoint_load_wide<__nv_bfloat16> : (const void*)&k_checkpoint_load_wide<float>, a, 4, stream,
                        "launch k_checkpoint_load_wide");
   const Lay lay = on_units(y) && on_units(c) && (!gain || on_units(gain, gain_dtype)) ? kUnits : kStrided;
-  pick_shape(a, lay);
+  if (lay == kStrided && takes_rows(a))
+    return launch_rows(y->dtype == SF_BF16 ? (const void*)&k_checkpoint_load_rows<__nv_bfloat16> : (const void*)&k_checkpoint_load_rows<float>, a, stream,
+                       "launch k_checkpoint_load_rows");
+  pick_shape(a, lay == kUnits ? kLoadK<kUnits> : kLoadK<kStrided>);
   return launch(pick_kernel<Load>(y->dtype, lay), a, stream, "launch k_checkpoint_load");
 }
 
@@ -307,7 +424,10 @@ sf_status sf_checkpoint_store(const sf_matrix* x, const sf_checkpoint* out, void
     return launch_wide(x->dtype == SF_BF16 ? (const void*)&k_checkpoint_store_wide<__nv_bfloat16> : (const void*)&k_checkpoint_store_wide<float>, a,
                        x->dtype == SF_BF16 ? 4 : 2, as_stream(stream), "launch k_checkpoint_store_wide");
   const Lay lay = on_units(x) && on_units(out) ? kUnits : kStrided;
-  pick_shape(a, lay);
+  if (lay == kStrided && out->group && takes_rows(a))
+    return launch_rows(x->dtype == SF_BF16 ? (const void*)&k_checkpoint_store_rows<__nv_bfloat16> : (const void*)&k_checkpoint_store_rows<float>, a,
+                       as_stream(stream), "launch k_checkpoint_store_rows");
+  pick_shape(a, lay == kUnits ? kK<kUnits> : kK<kStrided>);
   return launch(pick_kernel<Store>(x->dtype, lay), a, as_stream(stream), "launch k_checkpoint_store");
 }
 

@@ -442,6 +442,8 @@ __device__ __forceinline__ void store16(float* p, const F8& lo, const F8& hi, bo
 }
 
 // 16 columns of a thread in the second lay: lane, lane + 32, .. of a warp's 512.
+// WHOLE: none is past the row.
+template <bool WHOLE = false>
 __device__ __forceinline__ void ck_store16_strided(const Ck& k, int64_t row, int c0, int cols, const F8 (&v)[2], uint32_t row_code) {
   uint8_t* p = k.q + row * k.ld;
   const int per = k.group_log2 ? 1 << (k.group_log2 - 5) : 16;      // a group's blocks of 32 columns
@@ -465,7 +467,7 @@ __device__ __forceinline__ void ck_store16_strided(const Ck& k, int64_t row, int
         if (e % per == 0) {
           code = e8m0_of(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top[e]))));      // magnitudes order as their bits
           const int c = c0 + 32 * (4 * b + e);
-          if (c < cols && (threadIdx.x & 31) == 0) k.s8[row * k.n_groups + (c >> k.group_log2)] = (uint8_t)code;
+          if ((WHOLE || c < cols) && (threadIdx.x & 31) == 0) k.s8[row * k.n_groups + (c >> k.group_log2)] = (uint8_t)code;
         }
         codes[e] = code;
       }
@@ -474,8 +476,8 @@ __device__ __forceinline__ void ck_store16_strided(const Ck& k, int64_t row, int
     for (int e = 0; e < 4; e += 2) {
       const uint32_t two = e4m3_pair<true>(v[b >> 1].p[2 * (b & 1) + (e >> 1)], pack_f2(e8m0_inverse(codes[e]), e8m0_inverse(codes[e + 1])));
       const int c = c0 + 32 * (4 * b + e);
-      if (c < cols) p[c] = (uint8_t)two;
-      if (c + 32 < cols) p[c + 32] = (uint8_t)(two >> 8);
+      if (WHOLE || c < cols) p[c] = (uint8_t)two;
+      if (WHOLE || c + 32 < cols) p[c + 32] = (uint8_t)(two >> 8);
     }
   }
 }

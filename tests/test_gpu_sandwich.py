@@ -202,6 +202,34 @@ def test_single_gradients_in_bf16(want, rows, cols):
     _check_backward({want: out[want]}, ref, BF, BF, BF)
 
 
+@pytest.mark.parametrize("rows,cols,pad", [(3, 264, 0), (5, 1003, 3), (500, 1024, 0), (400, 1003, 1), (330, 8192, 8), (310, 12288, 0), (700, 72, 0)])
+@pytest.mark.parametrize("group", [None, 0, 64])
+def test_outputs_over_their_inputs(rows, cols, pad, group):
+    """s over the residual and h over x, or s over x and h over the residual, or s over a gate row for each row: the bits of
+    separate outputs."""
+    x, r, gate = (rows_of(rows, cols, pad, BF, seed)[0] for seed in (31, 32, 33))
+    g = torch.ones(cols, device=DEV)
+
+    def run(x, r, gate, s, h):
+        made = [new_checkpoint(rows, cols, group, 0, 0) for _ in range(2)] if group is not None else [(None,) * 4] * 2
+        native.sf_sandwich_norm_forward(native.sandwich(EPS, gate_span=1), x, r, gain_post=g, gain_pre=g, gate=gate, sum=s, h=h,
+                                        x8=made[0][0], sum8=made[1][0])
+        native.sf_sync_status()
+        return [s, h] + [m[i].view(torch.uint8) for m in made for i in (1, 2) if m[i] is not None]
+
+    def again(t):      # with the same stride
+        c = rows_of(rows, cols, pad, BF, None)[0]
+        c.copy_(t)
+        return c
+
+    want = run(x, r, gate, rows_of(rows, cols, pad, BF, None)[0], rows_of(rows, cols, pad, BF, None)[0])
+    assert bool(torch.isfinite(want[0].float()).all()) and bool(torch.isfinite(want[1].float()).all())
+    for sum_over, h_over in (("r", "x"), ("x", "r"), ("gate", "x")):
+        into = {"x": again(x), "r": again(r), "gate": again(gate)}
+        got = run(into["x"], into["r"], into["gate"], into[sum_over], into[h_over])
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), (sum_over, h_over)
+
+
 def test_gradients_over_their_inputs():
     rows, cols = 500, 1024
     p, kw, ref = _backward_case(rows, cols, 0, 0, BF, BF, BF, 2, True, True, True, None, 1.0, 0.5, 0.0)
