@@ -35,7 +35,7 @@ def test_store_is_the_oracles(rows, cols, pad, lead, xt, group):
     assert guard_ok(q, buf, lead)
 
 
-@pytest.mark.parametrize("cols", [96, 100, 75, 512])
+@pytest.mark.parametrize("cols", [96, 100, 75, 512, 603, 1037])
 @pytest.mark.parametrize("group", [0, 32, 64, 128])
 @pytest.mark.parametrize("xt", [BF, F32])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
@@ -51,7 +51,7 @@ def test_what_is_not_finite_next_to_the_largest_value(cols, group, xt, bad):
     _same(q, scale, f64(x.float()), group)
 
 
-@pytest.mark.parametrize("cols", [96, 75])
+@pytest.mark.parametrize("cols", [96, 75, 603, 1037])
 @pytest.mark.parametrize("group", [0, 32, 64, 128])
 @pytest.mark.parametrize("xt", [BF, F32])
 def test_store_special_values(cols, group, xt):
