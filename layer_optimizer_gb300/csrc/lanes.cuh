@@ -216,7 +216,7 @@ __device__ __forceinline__ F8 load8(const Ck& k, int64_t row, int c0, int dj, in
 constexpr float kLargest = 3.402823466e38f;
 
 // The largest magnitude of a thread's eight values (those past the row are
-// zero), NaN left out.
+// zero), NaN left out; NaN where there is nothing else.
 __device__ __forceinline__ float top8(const F8& v) {
   float t[4];
 #pragma unroll
@@ -266,7 +266,7 @@ __device__ __forceinline__ void ck_store8(const Ck& k, int64_t row, int c0, int 
       const int lanes = 1 << (k.group_log2 - 3);
       float top = top8(v);
       for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      infinite = __any_sync(0xffffffffu, top > kLargest);
+      infinite = __any_sync(0xffffffffu, !(top <= kLargest));      // (NaN where a thread has nothing else)
       if (infinite) {
         top = top8_finite(v);
         for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));

@@ -185,3 +185,20 @@ def test_streams_and_graphs():
     torch.cuda.synchronize()
     _same(q, scale, f64(x.float()), 32)
     assert np.array_equal(f64(y.float()), _read(q, scale, 32, cols))
+
+
+@pytest.mark.parametrize("cols", [96, 75, 104, 264, 520, 1037, 4096])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("xt", [BF, F32])
+def test_groups_without_a_finite_value(cols, group, xt):
+    # next to others, in every place: their scale is 2^-126
+    x = synth.normal((40, cols), 1.0, 6).to(xt).to(DEV)
+    x[1], x[2], x[3, ::2], x[3, 1::2] = float("nan"), float("inf"), float("nan"), float("-inf")
+    for i in range(4, 40):
+        c = 8 * i % cols
+        x[i, c:c + 32 + 8 * (i % 13)] = float("nan") if i % 3 else float("inf")
+        x[i, : i % 9 * 8] = float("nan")
+    ck, q, scale, _ = new_checkpoint(40, cols, group)
+    native.sf_checkpoint_store(x, ck)
+    native.sf_sync_status()
+    _same(q, scale, f64(x.float()), group)
