@@ -239,10 +239,11 @@ __device__ __forceinline__ float top8_finite(const F8& v) {
 }
 
 // v / scale in e4m3, four codes a word.  A NaN stays one; an infinity becomes
-// one only where EXACT (v - v is 0 or NaN), which costs a subtraction a value.
+// one only where EXACT (v - v is 0 or NaN), which costs a subtraction a value:
+// rounded down, its zero is -0, whose addition leaves a zero's sign as it is.
 template <bool EXACT>
 __device__ __forceinline__ uint32_t e4m3_pair(uint64_t v, uint64_t inv) {
-  const uint64_t x = EXACT ? fmadd2(v, inv, fsub2(v, v)) : fmul2(v, inv);
+  const uint64_t x = EXACT ? fmadd2(v, inv, fsub2_down(v, v)) : fmul2(v, inv);
   return __nv_cvt_float2_to_fp8x2(unpack_f2(x), __NV_SATFINITE, __NV_E4M3);
 }
 template <bool EXACT>

@@ -46,6 +46,13 @@ __device__ __forceinline__ uint64_t fsub2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// The same rounded towards minus infinity (a - a is -0).
+__device__ __forceinline__ uint64_t fsub2_down(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rm.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // 2^x of the exponential unit (|relative error| about 2^-22); results below 2^-126 are 0.
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;

@@ -202,3 +202,23 @@ def test_groups_without_a_finite_value(cols, group, xt):
     native.sf_checkpoint_store(x, ck)
     native.sf_sync_status()
     _same(q, scale, f64(x.float()), group)
+
+
+@pytest.mark.parametrize("rows,cols,pad", [(64, 96, 0), (64, 75, 0), (64, 512, 0), (64, 603, 0), (64, 1037, 0), (400, 4096, 0), (64, 520, 8), (40, 20000, 0)])
+@pytest.mark.parametrize("group", [0, 32, 128])
+@pytest.mark.parametrize("xt", [BF, F32])
+def test_the_sign_of_zero(rows, cols, pad, group, xt):
+    # v / 2^k keeps it, and so does the rounding of what is far below e4m3's least value, whatever lies beside it
+    x, _ = rows_of(rows, cols, pad, xt, 12 + cols, 1.0)
+    x[:, 1::3] = -0.0
+    x[:, 2::9] = 0.0
+    x[:, 5::9] = -2.0 ** -30
+    x[8::4, 7], x[9::4, 40] = float("inf"), float("nan")
+    x[5] = -0.0
+    ck, q, scale, _ = new_checkpoint(rows, cols, group, pad)
+    native.sf_checkpoint_store(x, ck)
+    native.sf_sync_status()
+    _same(q, scale, f64(x.float()), group)
+    codes, fine = q.view(torch.uint8), torch.isfinite(x)
+    assert torch.equal((codes >> 7)[fine].bool(), torch.signbit(x)[fine])
+    assert bool(((codes & 0x7f) == 0x7f)[~fine].all())

@@ -411,3 +411,25 @@ def test_past_2_31_elements():
                                      dx=dx)
     native.sf_sync_status()
     _check_backward(dict(dresidual=dr[pick], dx=dx[pick]), ref, BF, BF)
+
+
+@pytest.mark.parametrize("rows,cols,pad", [(9, 1024, 0), (9, 1003, 0), (400, 1024, 0), (400, 1032, 0), (400, 1003, 0), (310, 12288, 0)])
+@pytest.mark.parametrize("group", [0, 32, 128])
+@pytest.mark.parametrize("at", [BF, F32])
+def test_checkpoints_keep_the_sign_of_zero(rows, cols, pad, group, at):
+    x, r = (rows_of(rows, cols, pad, at, 71 + i, 1.0)[0] for i in range(2))
+    for t in (x, r):      # s = r + x, -0 + -0 = -0
+        t[:, 1::3] = -0.0
+        t[:, 2::9] = 0.0
+        t[:, 5::9] = -2.0 ** -30
+        t[4::4, 7] = float("inf")
+        t[5] = -0.0
+    g = torch.ones(cols, device=DEV)
+    x8, q1, _, _ = new_checkpoint(rows, cols, group)
+    s8, q2, _, _ = new_checkpoint(rows, cols, group)
+    h = torch.empty(rows, cols, dtype=at, device=DEV)
+    native.sf_sandwich_norm_forward(native.sandwich(EPS), x, r, gain_pre=g, h=h, x8=x8, sum8=s8)
+    native.sf_sync_status()
+    for q, v in ((q1, x), (q2, x.float() + r.float())):
+        fine = torch.isfinite(v)
+        assert torch.equal((q.view(torch.uint8) >> 7)[fine].bool(), torch.signbit(v)[fine])
