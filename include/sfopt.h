@@ -556,8 +556,8 @@ sf_status sf_checkpoint_load(const sf_checkpoint* c, const float* row_factor,
  *          bases and rows in this device's own memory they take the tensor
  *          cores, else the CUDA cores.  tokens, out and in below 2^30.
  *   base : NULL (zero), or dW's type and sizes; may be dW itself, to add to it.
- *   dW   : SF_BF16 or SF_FP32 [out][in]; of the inputs only base may be the
- *          same matrix.
+ *   dW   : SF_BF16 or SF_FP32 [out][in]; overlaps no input but a base that is
+ *          the same matrix (SF_ERR_INVALID).
  *   ws   : device scratch of ws_bytes >= sf_checkpoint_wgrad_workspace_bytes(
  *          tokens, out, in), 16-byte aligned; may be NULL where that is 0 (few
  *          tokens).  Larger products hold X there in bf16 while they run.
@@ -591,7 +591,10 @@ sf_status sf_checkpoint_wgrad(const sf_matrix* dY, const sf_checkpoint* c,
  *   x8, sum8 : receive checkpoints of x and s; each NULL: not written.
  *   rstd_post, rstd_pre : fp32 [rows], for the backward pass; NULL: not
  *              written.  rstd_post needs gain_post, rstd_pre gain_pre.
- * At least one of sum, h, x8 and sum8.  fp32 arithmetic; h and sum8 are taken
+ * At least one of sum, h, x8 and sum8.  sum and h may be x or the residual,
+ * where types and distances of rows agree, and the gate if it has a row for
+ * each row; an output over another part of an input gives undefined results
+ * (over the gate: SF_ERR_INVALID).  fp32 arithmetic; h and sum8 are taken
  * of s before it is rounded; each output is rounded once. */
 typedef struct {
   double eps;
@@ -625,8 +628,10 @@ sf_status sf_sandwich_norm_forward(const sf_sandwich* p, const sf_matrix* x,
  *          or dgate (and dx, dgain_post or dgate wanted), sum with dh.
  *   dresidual (the sum's type), dx (x's type), dgain_post, dgain_pre ([cols],
  *          dgain_dtype bf16 or fp32), dgate (the gate's sizes, bf16 or fp32):
- *          each NULL: not wanted, not all.  dgate may be the gate itself,
- *          dresidual and dx may not.
+ *          each NULL: not wanted, not all.  dgate may be the gate itself (the
+ *          same type and distance of rows); else none of the three overlaps it
+ *          (SF_ERR_INVALID).  dresidual and dx may be the other matrices of
+ *          their type and distance of rows.
  *   ws   : device scratch of ws_bytes >= sf_sandwich_norm_workspace_bytes(rows,
  *          cols), 16-byte aligned; only used with a dgain or dgate.
  * fp32 arithmetic, one rounding at the end; sums over rows run in a fixed

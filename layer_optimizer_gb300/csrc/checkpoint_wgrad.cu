@@ -738,7 +738,9 @@ sf_status sf_checkpoint_wgrad(const sf_matrix* dY, const sf_checkpoint* c, const
   a.fp32 = dW->dtype == SF_FP32;
   a.ck = device_ck(c);
   if (need && !on_current_device(ws)) return fail(SF_ERR_INVALID, "ws must be device memory of the current device");
-  if (tokens && (dW->data == dY->data || dW->data == c->values.data)) return fail(SF_ERR_INVALID, "dW must not lie over dY or the checkpoint");
+  const sf_matrix scale{c->scale, tokens, a.ck.n_groups, a.ck.n_groups, c->scale_dtype};
+  if (overlap(dW, dY) || overlap(dW, &c->values) || overlap(dW, &scale)) return fail(SF_ERR_INVALID, "dW must not lie over dY or the checkpoint");
+  if (overlap(dW, base) && !same_matrix(dW, base)) return fail(SF_ERR_INVALID, "dW lies over base with another place or distance of rows");
   if (tokens && dY->ld % 8 == 0 && dY->ld >= out && c->values.ld % 16 == 0 && c->values.ld >= in && reinterpret_cast<uintptr_t>(dY->data) % 16 == 0 &&
       reinterpret_cast<uintptr_t>(c->values.data) % 16 == 0 && tensor_map_encoder() && on_current_device(dY->data) &&
       on_current_device(c->values.data))

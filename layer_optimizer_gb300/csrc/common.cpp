@@ -7,6 +7,7 @@
 
 #include <sched.h>
 
+#include <algorithm>
 #include <chrono>
 #include <cmath>
 #include <cstdlib>
@@ -77,6 +78,26 @@ sf_status check_matrix(const sf_matrix* m, const char* name, int64_t want_rows, 
     if (m->ld > INT64_MAX / 4 / m->rows) return fail(SF_ERR_UNSUPPORTED, "%s: sizes too large", name);
   }
   return SF_OK;
+}
+
+bool overlap(const sf_matrix* a, const sf_matrix* b) {
+  using wide = __int128;
+  if (!a || !b || a->rows < 1 || a->cols < 1 || b->rows < 1 || b->cols < 1) return false;
+  const wide size_a = (wide)dtype_bytes(a->dtype), size_b = (wide)dtype_bytes(b->dtype);
+  const wide width_a = a->cols * size_a, width_b = b->cols * size_b;
+  const wide step_a = a->rows > 1 ? a->ld * size_a : 0, step_b = b->rows > 1 ? b->ld * size_b : 0;
+  const wide d = (wide)reinterpret_cast<uintptr_t>(b->data) - (wide)reinterpret_cast<uintptr_t>(a->data);
+  if (d >= (a->rows - 1) * step_a + width_a || -d >= (b->rows - 1) * step_b + width_b) return false;
+  const wide step = step_a ? step_a : step_b;
+  if (!step || (step_a && step_b && step_a != step_b)) return true;
+  // row i of a and row j of b meet where -width_b < d - n step < width_a, n = i - j of -(rows of b - 1) .. rows of a - 1
+  auto floor_div = [](wide x, wide y) { return x / y - (x % y != 0 && x < 0 ? 1 : 0); };      // y > 0
+  const wide lo = floor_div(d - width_a, step) + 1, hi = -floor_div(-(d + width_b), step) - 1;
+  return std::max<wide>(lo, -(wide)(b->rows - 1)) <= std::min<wide>(hi, a->rows - 1);
+}
+
+bool same_matrix(const sf_matrix* a, const sf_matrix* b) {
+  return a->data == b->data && a->dtype == b->dtype && (a->ld == b->ld || a->rows <= 1);
 }
 
 sf_status check_aligned(const void* p, size_t size, const char* name) {

@@ -71,6 +71,13 @@ bool on_current_device(const void* p);
 // want_rows / want_cols < 0 accept any size.  dtypes: a mask of 1 << sf_dtype.
 sf_status check_matrix(const sf_matrix* m, const char* name, int64_t want_rows, int64_t want_cols, unsigned dtypes);
 
+// Whether a byte belongs to elements of both matrices (null and empty ones have none): exact where their rows lie equally far
+// apart or one of them has a single row, else judged by their first and last bytes.
+bool overlap(const sf_matrix* a, const sf_matrix* b);
+
+// Whether the two are one matrix: the same place, type and distance of rows (sizes are checked elsewhere).
+bool same_matrix(const sf_matrix* a, const sf_matrix* b);
+
 // Checks on the host that a vector (null passes) lies on a multiple of its element's size.
 sf_status check_aligned(const void* p, size_t size, const char* name);
 

@@ -309,14 +309,14 @@ sf_status sf_sandwich_norm_backward(const sf_sandwich* p, const sf_matrix* dh, c
   SF_TRY(check_aligned(rstd_post, sizeof(float), "rstd_post"));
   SF_TRY(check_aligned(rstd_pre, sizeof(float), "rstd_pre"));
   if (dgate) SF_TRY(check_matrix(dgate, "dgate", gate->rows, cols, kTypes));
+  // (the gate is read again for its products and for dgain_post; a row of it before the same row of dgate is written)
+  if (overlap(dresidual, gate) || overlap(dx, gate)) return fail(SF_ERR_INVALID, "dresidual and dx must not lie over the gate");
+  if (overlap(dgate, gate) && !same_matrix(dgate, gate)) return fail(SF_ERR_INVALID, "dgate lies over the gate with another type, place or distance of rows");
   if (wants_t || dgain_pre) {
     const size_t need = sf_sandwich_norm_workspace_bytes(rows, cols);
     if (!ws || ws_bytes < need || reinterpret_cast<uintptr_t>(ws) % 16)
       return fail(SF_ERR_INVALID, "workspace needs %zu bytes, 16-byte aligned (got %zu)", need, ws_bytes);
   }
-  // (the gate is read again for its products and for dgain_post)
-  if (rows && gate && ((dresidual && dresidual->data == gate->data) || (dx && dx->data == gate->data)))
-    return fail(SF_ERR_INVALID, "dresidual and dx must not lie over the gate");
   // where only the residual's gradient is wanted, the branch is left out
   if (!dx && !wants_t) a.v.g_post = nullptr, x = nullptr, x8 = nullptr;
   if (!dh) a.v.g_pre = nullptr, sum = nullptr, sum8 = nullptr;

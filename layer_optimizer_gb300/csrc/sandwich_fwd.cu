@@ -432,6 +432,10 @@ sf_status sf_sandwich_norm_forward(const sf_sandwich* p, const sf_matrix* x, con
   if (rstd_post && !gain_post) return fail(SF_ERR_INVALID, "rstd_post needs gain_post");
   SF_TRY(check_aligned(rstd_post, sizeof(float), "rstd_post"));
   SF_TRY(check_aligned(rstd_pre, sizeof(float), "rstd_pre"));
+  // (a gate row that several rows take must outlast them)
+  for (const sf_matrix* out : {sum, h})
+    if (overlap(out, gate) && !(gate->rows == rows && same_matrix(out, gate)))
+      return fail(SF_ERR_INVALID, "sum and h may lie over the gate only as the same matrix, with a gate row for each row");
   if (!rows) return SF_OK;
   a.x = x->data;
   a.ldx = x->ld;

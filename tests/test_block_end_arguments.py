@@ -167,3 +167,69 @@ def test_workspace_sizes():
     assert native.sf_sandwich_norm_workspace_bytes(3, 64) == 2 * 3 * 64 * 4
     assert native.sf_sandwich_norm_workspace_bytes(10 ** 9, 16384) == 2 * 1024 * 16384 * 4
     assert native.sf_sandwich_norm_workspace_bytes(10 ** 9, 64) == 2 * 8192 * 64 * 4
+
+
+# a gradient of `rows` rows by a gate of 16 x 96 whose rows lie `step` bytes apart: (rows, bytes behind the gate, distance of rows, meet)
+def _places(size, step):
+    width, last = 96 * size, 15 * step
+    return [(64, 0, step, True), (64, step, step, True), (64, -step, step, True), (64, size, step, True), (64, size - width, step, True),
+            (64, width, step, False), (64, -width, step, False), (64, width - size, step, True),                          # side by side, and one column less
+            (64, last + width, step, False), (64, last + width - size, step, True), (64, last, step, True), (64, last + step, step, False),
+            (64, -63 * step - width, step, False), (64, -63 * step - width + size, step, True), (64, -64 * step, step, False),
+            (16, 5 * step + width, step, False), (16, 5 * step - size, step, True), (16, width, step + size, True)]      # another distance: by the ends
+
+
+@pytest.mark.parametrize("dt,size", [(F32, 4), (BF, 2)])
+@pytest.mark.parametrize("name", ["dresidual", "dx", "dgate"])
+def test_overlaps_are_told_by_their_elements(dt, size, name):
+    """A gradient that does not meet the gate goes on to the refusal of a workspace that is too small."""
+    at, ld = 64 * AT, 400
+    for rows, off, step, meet in _places(size, ld * size):
+        n = 16 if name == "dgate" else rows
+        if n != rows:
+            continue
+        total = 64 if name == "dgate" else rows
+        p = native.sandwich(1e-5, gate_span=-(-total // 16))
+        far = {k: _m(total, 96, dt, a * AT) for k, a in (("dh", 1), ("dsum", 2), ("x", 4), ("sum", 8), ("dresidual", 16), ("dx", 32))}
+        out = native.sf_matrix(at + off, n, 96, step // size, dt)
+        _refused("the gate" if meet else "workspace needs",
+                 lambda: _bwd(p, gate=native.sf_matrix(at, 16, 96, ld, dt), **dict(far, **{name: out}), ws_bytes=0))  # noqa: B023
+    # a gate of one row, between the rows of a wider buffer and on them
+    far = {k: _m(64, 96, dt, a * AT) for k, a in (("dh", 1), ("dsum", 2), ("x", 4), ("sum", 8), ("dresidual", 16), ("dx", 32))}
+    if name != "dgate":
+        for off, meet in ((7 * ld + 96, False), (7 * ld + 95, True), (7 * ld - 96, False), (7 * ld - 95, True), (-96, False), (63 * ld + 96, False)):
+            far[name] = native.sf_matrix(at, 64, 96, ld, dt)
+            _refused("the gate" if meet else "workspace needs",
+                     lambda: _bwd(gate=native.sf_matrix(at + off * size, 1, 96, 0, dt), **far, ws_bytes=0))  # noqa: B023
+
+
+def test_weight_gradients_over_a_part_of_an_operand():
+    at = 4 * AT
+    dw = native.sf_matrix(at, 64, 96, 400, BF)
+    away = dict(at=32 * AT, scale=64 * AT)
+    dy, c = _m(40, 64, BF, at=128 * AT), _c(40, 96, **away)
+    for d in (_m(40, 64, BF, at=at + 2), _m(40, 64, BF, at=at - 2), native.sf_matrix(at + 800, 40, 64, 400, BF), native.sf_matrix(at - 126, 40, 64, 400, BF)):
+        _refused("must not lie over", lambda: native.sf_checkpoint_wgrad(d, c, dw))
+    _refused("must not lie over", lambda: native.sf_checkpoint_wgrad(dy, _c(40, 96, at=at + 100, scale=64 * AT), dw))
+    for scale in (at, at + 190, at + 800 * 63 + 191, at - 40 * 3 + 1):
+        _refused("must not lie over", lambda: native.sf_checkpoint_wgrad(dy, _c(40, 96, at=32 * AT, scale=scale), dw))
+    for base in (native.sf_matrix(at, 64, 96, 401, BF), native.sf_matrix(at + 800, 64, 96, 400, BF), native.sf_matrix(at - 2, 64, 96, 400, BF)):
+        _refused("dW lies over base", lambda: native.sf_checkpoint_wgrad(dy, c, dw, base=base))
+
+
+def test_outputs_over_a_part_of_the_gate():
+    at = 4 * AT
+    p, each = native.sandwich(1e-5, gate_span=4), native.sandwich(1e-5, gate_span=1)
+    far = dict(residual=_m(8, 64, BF, 16 * AT), sum=_m(8, 64, BF, 32 * AT), h=_m(8, 64, BF, 64 * AT))
+    for out in ("sum", "h"):
+        for place in (at, at + 128, at - 8 * 128 + 2, at + 2 * 128 - 2):          # over a gate of 2 rows
+            _refused("over the gate", lambda: _fwd(p, gate=_m(2, 64, BF, at), **dict(far, **{out: _m(8, 64, BF, place)})))
+        for gate in (_m(8, 64, BF, at + 128), _m(8, 64, F32, at), _m(8, 64, BF, at, ld=65), _m(8, 64, BF, at + 2)):
+            _refused("over the gate", lambda: _fwd(each, gate=gate, **dict(far, **{out: _m(8, 64, BF, at)})))
+    outs = dict(dresidual=_m(8, 64, BF, 16 * AT), dx=_m(8, 64, BF, 32 * AT))
+    for out in outs:
+        for place in (at + 2, at + 128, at - 8 * 128 + 2, at + 2 * 128 - 2):
+            _refused("must not lie over the gate", lambda: _bwd(p, gate=_m(2, 64, BF, at), **dict(outs, **{out: _m(8, 64, BF, place)})))
+    for dgate in (_m(2, 64, F32, at), _m(2, 64, BF, at, ld=65), _m(2, 64, BF, at + 128), _m(2, 64, BF, at + 2), _m(2, 64, BF, at - 2 * 128 + 2)):
+        _refused("dgate lies over the gate", lambda: _bwd(p, gate=_m(2, 64, BF, at), dgate=dgate, **outs))
+    _refused("dgate lies over the gate", lambda: _bwd(gate=_m(1, 64, BF, at), dgate=_m(1, 64, F32, at), **outs))
