@@ -99,11 +99,40 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "r"(taddr));
 }
 
-// Arrival on a barrier of the first CTA, ordered after this thread's earlier accesses of its own CTA's memory.  (The
-// form with a release at cluster scope takes over 1000 cycles: every slab's converters would wait for it.  What the
-// other CTA's MMA reads here is handed to the async proxy by the fence before.)
+// What the second CTA's converters write is read by MMAs that the first CTA's thread issues, and they write again where
+// those have read: orders between two CTAs.  A release or an acquire at cluster scope waits for all that its thread has in
+// flight, of a converter the next slabs' scales (8192 tokens 4096 -> 1024 in 111 us where one idle warp releases for them,
+// 76 with two that take turns).  So the fences here are restricted to shared memory, and cost nothing that shows (61.7 us).
+//
+// Arrival on a barrier of the first CTA, after this thread's accesses of its own CTA's shared memory and those that it met
+// at a barrier.
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// Bounded wait for arrivals from either CTA, before this thread's accesses of the pair's shared memory.
+__device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity) {
+  auto test = [&]() {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (!test()) {
+    const long long t0 = clock64();
+    while (!test()) {
+      if (clock64() - t0 > kWaitLimitCycles) {
+        atomicOr(&g_device_error, kDevErrTimeout);
+        return false;
+      }
+    }
+  }
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+  return true;
 }
 
 // An item: a tile of dW and the slabs of tokens to sum.
@@ -304,9 +333,8 @@ __global__ void __launch_bounds__(kTcThreads<FUSED>, 1)
       int4 v[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = lds_i4(src + 2048u * q);
-      // The slab that the slot held has been multiplied.  (The commit orders the MMAs' reads before its arrival; a wait at
-      // cluster scope would also hold up the thread until its scale loads are there.)
-      if (i >= kSlots && !mbar_wait(&empty[(i - kSlots) % kRing], (uint32_t)((i - kSlots) / kRing) & 1u)) break;
+      // the slab that the slot held has been multiplied
+      if (i >= kSlots && !mbar_wait_pair(&empty[(i - kSlots) % kRing], (uint32_t)((i - kSlots) / kRing) & 1u)) break;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t in[4] = {(uint32_t)v[q].x, (uint32_t)v[q].y, (uint32_t)v[q].z, (uint32_t)v[q].w};

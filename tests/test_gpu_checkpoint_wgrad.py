@@ -191,3 +191,30 @@ def test_every_call_over_several_waves_gives_the_same_right_bits():
                 assert bool(((dw.double() - ref).abs() <= _sum(tokens) * mag + half * ref.abs()).all())
             assert torch.equal(dw, first), k
         native.sf_sync_status()
+
+
+# as above, of the form that converts X on its way (few tokens, or outputs below 2048): a pair's second item and later ones
+@pytest.mark.parametrize("tokens,out,cin,dt,group", [(256, 4096, 4096, F32, 64), (256, 4096, 4096, BF, 128), (448, 2600, 2048, F32, 32),
+                                                     (500, 5000, 1200, BF, 0), (2048, 1024, 12288, F32, 64), (2100, 1900, 5008, BF, 32)])
+def test_every_converted_call_over_several_waves_gives_the_same_right_bits(tokens, out, cin, dt, group):
+    dy = torch.empty(tokens, out, dtype=BF, device=DEV)
+    x = torch.empty(tokens, cin, dtype=BF, device=DEV)
+    base = torch.empty(out, cin, dtype=dt, device=DEV)
+    for i, t in enumerate((dy, x, base)):
+        synth.fill_normal_(t, 1.0, 111 + i)
+    ck, q, scale = make_checkpoint(x, group)
+    native.sf_checkpoint_load(ck, x)          # exact in bf16
+    ref = dy.double().t() @ x.double() + base.double()
+    mag = dy.double().abs().t() @ x.double().abs() + base.double().abs()
+    ws = torch.empty(max(16, native.sf_checkpoint_wgrad_workspace_bytes(tokens, out, cin)), dtype=torch.uint8, device=DEV)
+    first = None
+    for k in range(25):
+        ws.fill_(255)
+        dw = torch.full((out, cin), 7.0, dtype=dt, device=DEV)
+        native.sf_checkpoint_wgrad(dy, ck, dw, base=base, ws=ws)
+        if first is None:
+            first = dw
+            half = 2.0 ** -8 if dt == BF else 2.0 ** -24
+            assert bool(((dw.double() - ref).abs() <= _sum(tokens) * mag + half * ref.abs()).all())
+        assert torch.equal(dw, first), k
+    native.sf_sync_status()
