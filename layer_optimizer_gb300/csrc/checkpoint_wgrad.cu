@@ -299,19 +299,20 @@ __global__ void __launch_bounds__(kTcThreads<FUSED>, 1)
       }
     };
     // A slab's scales, as loaded: turned into fp32 when their values have come, so that nothing waits for them here.
-    // Past the last token or column the last one's are taken: the values there are zero (or, where the scale is NaN,
-    // not the only ones of their column that are).
+    // Past the last token they are zero or 2^-127, as finite as the zeros that they scale; past the last column the last
+    // one's are taken, whose products no output has.
     auto scales = [&](uint32_t (&f)[4]) {
       const int c = min(w.nt * kBN + (int)rank * kBRows + 16 * cc, g.in - 1) >> (g.ck.group_log2 ? g.ck.group_log2 : 31);
+      const int t0 = kb * kBK + r0;
       int64_t at[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) at[q] = (int64_t)min(kb * kBK + r0 + 16 * q, g.tokens - 1) * g.ck.n_groups + c;
+      for (int q = 0; q < 4; ++q) at[q] = (int64_t)(t0 + 16 * q) * g.ck.n_groups + c;
       if (g.ck.s8) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) f[q] = __ldg(g.ck.s8 + at[q]);
+        for (int q = 0; q < 4; ++q) f[q] = t0 + 16 * q < g.tokens ? __ldg(g.ck.s8 + at[q]) : 0u;
       } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) f[q] = __float_as_uint(__ldg(g.ck.s32 + at[q]));
+        for (int q = 0; q < 4; ++q) f[q] = t0 + 16 * q < g.tokens ? __float_as_uint(__ldg(g.ck.s32 + at[q])) : 0u;
       }
     };
     const uint32_t src0 = ring_b + 128u * r0 + 16u * (cc ^ (r0 & 7));

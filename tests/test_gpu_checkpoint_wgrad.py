@@ -218,3 +218,20 @@ def test_every_converted_call_over_several_waves_gives_the_same_right_bits(token
             assert bool(((dw.double() - ref).abs() <= _sum(tokens) * mag + half * ref.abs()).all())
         assert torch.equal(dw, first), k
     native.sf_sync_status()
+
+
+# converted on the way, restored first, on the CUDA cores; tokens that end inside a slab
+@pytest.mark.parametrize("tokens,out,cin", [(130, 264, 256), (1, 40, 64), (521, 2048, 256), (130, 264, 250)])
+def test_an_infinite_scale_of_the_last_token(tokens, out, cin):
+    h8 = synth.normal((tokens, cin), 50.0, 121).abs().clamp(1, 448).to(DEV).to(E4)
+    scale = torch.rand(tokens, -(-cin // 32), device=DEV) + 0.1
+    scale[-1, 1] = float("inf")
+    dy = synth.normal((tokens, out), 1.0, 122).abs().clamp(min=0.1).to(BF).to(DEV)
+    dy[-1, ::3] *= -1
+    dw = torch.empty(out, cin, device=DEV)
+    ws = torch.empty(max(16, native.sf_checkpoint_wgrad_workspace_bytes(tokens, out, cin)), dtype=torch.uint8, device=DEV)
+    native.sf_checkpoint_wgrad(dy, native.checkpoint(h8, scale, 32), dw, ws=ws)
+    native.sf_sync_status()
+    got = f64(dw)
+    assert np.array_equal(got[:, 32:64], np.broadcast_to(np.sign(f64(dy[-1].float()))[:, None] * np.inf, (out, 32)))
+    assert np.isfinite(got[:, :32]).all() and np.isfinite(got[:, 64:]).all()
