@@ -613,9 +613,10 @@ void plan(int64_t tiles, int nk, int pairs, TcArgs* g) {
 // 64 x 64 tiles on the CUDA cores, 4 x 4 a thread, for operands that tensor
 // copies cannot take (rows off 16 bytes, pinned host memory).
 constexpr int kT = 64, kTk = 16;
-__global__ void __launch_bounds__(256) k_wgrad_plain(const WgradArgs a) {
+__global__ void __launch_bounds__(256) k_wgrad_plain(const WgradArgs a, const uint32_t tiles_i) {
   __shared__ float sa[kTk][kT + 4], sb[kTk][kT + 4];
-  const int64_t o0 = (int64_t)blockIdx.y * kT, i0 = (int64_t)blockIdx.x * kT;
+  const uint32_t tile_o = blockIdx.x / tiles_i;
+  const int64_t o0 = (int64_t)tile_o * kT, i0 = (int64_t)(blockIdx.x - tile_o * tiles_i) * kT;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   float acc[4][4] = {};
   for (int64_t t0 = 0; t0 < a.tokens; t0 += kTk) {
@@ -774,9 +775,9 @@ sf_status sf_checkpoint_wgrad(const sf_matrix* dY, const sf_checkpoint* c, const
       reinterpret_cast<uintptr_t>(c->values.data) % 16 == 0 && tensor_map_encoder() && on_current_device(dY->data) &&
       on_current_device(c->values.data))
     return launch_tc(a, c, ws, as_stream(stream));
-  const int64_t gx = ceil_div<int64_t>(in, kT), gy = ceil_div<int64_t>(out, kT);
-  if (gy > 65535) return fail(SF_ERR_UNSUPPORTED, "out is too large");
-  k_wgrad_plain<<<dim3((unsigned)gx, (unsigned)gy), 256, 0, as_stream(stream)>>>(a);
+  const int64_t tiles_i = ceil_div<int64_t>(in, kT), tiles = ceil_div<int64_t>(out, kT) * tiles_i;
+  if (tiles > INT32_MAX) return fail(SF_ERR_UNSUPPORTED, "too many tiles");      // (of 4096 elements each)
+  k_wgrad_plain<<<(unsigned)tiles, 256, 0, as_stream(stream)>>>(a, (uint32_t)tiles_i);
   return check_launch("launch k_wgrad_plain");
 }
 

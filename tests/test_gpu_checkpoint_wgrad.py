@@ -235,3 +235,18 @@ def test_an_infinite_scale_of_the_last_token(tokens, out, cin):
     got = f64(dw)
     assert np.array_equal(got[:, 32:64], np.broadcast_to(np.sign(f64(dy[-1].float()))[:, None] * np.inf, (out, 32)))
     assert np.isfinite(got[:, :32]).all() and np.isfinite(got[:, 64:]).all()
+
+
+def test_outputs_of_more_rows_than_a_grids_second_axis():
+    # 64 rows a block: 2^16 blocks and more, without tokens, and with one whose rows no tensor copy takes
+    out, cin = 64 * 65536 + 5, 3
+    q, scale = torch.full((1, cin), 1.5, device=DEV).to(E4), torch.full((1, 1), 128, dtype=torch.uint8, device=DEV)
+    base = torch.randn(out, cin, device=DEV)
+    dw = torch.empty_like(base)
+    native.sf_checkpoint_wgrad(torch.empty(0, out, dtype=BF, device=DEV), native.checkpoint(q[:0], scale[:0], 32), dw, base=base)
+    native.sf_sync_status()
+    assert torch.equal(dw, base)
+    dy = torch.randn(1, out, device=DEV).to(BF)
+    native.sf_checkpoint_wgrad(dy, native.checkpoint(q, scale, 32), dw)
+    native.sf_sync_status()
+    assert torch.equal(dw, (3.0 * dy.float()).t().expand(out, cin))
