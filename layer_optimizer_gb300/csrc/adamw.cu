@@ -505,12 +505,7 @@ __global__ void k_test_wait_runs_out(long long limit) {
   mbar_wait_limit(&bar, 0, limit);
 }
 
-int read_and_clear_device_error_adamw() {
-  int v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof v) != cudaSuccess) return 0;
-  if (v) cudaMemcpyToSymbol(g_device_error, &z, sizeof z);
-  return v;
-}
+const void* device_error_adamw() { return &g_device_error; }
 
 }  // namespace sf
 

@@ -720,12 +720,7 @@ sf_status launch_tc(const WgradArgs& a, const sf_checkpoint* c, void* ws, cudaSt
 
 }  // namespace
 
-int read_and_clear_device_error_wgrad() {
-  int v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof v) != cudaSuccess) return 0;
-  if (v) cudaMemcpyToSymbol(g_device_error, &z, sizeof z);
-  return v;
-}
+const void* device_error_wgrad() { return &g_device_error; }
 
 }  // namespace sf
 

@@ -127,18 +127,18 @@ struct AdamConsts {
   float eps;
 };
 
-// Reads and clears the device-side error word that bounded waits and index
-// checks in the kernels set (0 = none; bit 1 = a wait ran out; bit 2 = an
-// out-of-range index was skipped).
-int read_and_clear_device_error();
-int read_and_clear_device_error_adamw();
-int read_and_clear_device_error_gemm();
-int read_and_clear_device_error_lce();
-int read_and_clear_device_error_norm();
-int read_and_clear_device_error_wgrad();
-int read_and_clear_device_error_sandwich_fwd();
-int read_and_clear_device_error_sandwich_units();
-int read_and_clear_device_error_sandwich_strided();
+// The device-side error words that bounded waits and index checks in the
+// kernels set (0 = none; bit 1 = a wait ran out; bit 2 = an out-of-range index
+// was skipped), one a translation unit, as symbols.
+const void* device_error_lsp();
+const void* device_error_adamw();
+const void* device_error_gemm();
+const void* device_error_lce();
+const void* device_error_norm();
+const void* device_error_wgrad();
+const void* device_error_sandwich_fwd();
+const void* device_error_sandwich_units();
+const void* device_error_sandwich_strided();
 
 // C = alpha A B^T (+ C) on the tensor cores (tc_gemm.cu): A bf16 [M][lda]
 // row-major (K-major) or, with a_mn, [K][lda] (MN-major: A^T stored);

@@ -629,12 +629,7 @@ sf_status sum_parts(const float* parts, int S, int64_t M, int64_t N, int64_t ld,
 
 namespace sf {
 
-int read_and_clear_device_error_lce() {
-  int v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof v) != cudaSuccess) return 0;
-  if (v) cudaMemcpyToSymbol(g_device_error, &z, sizeof z);
-  return v;
-}
+const void* device_error_lce() { return &g_device_error; }
 
 }  // namespace sf
 

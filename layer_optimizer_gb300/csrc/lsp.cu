@@ -1715,12 +1715,7 @@ template sf_status launch_gather<__nv_bfloat16>(const lsp_projector_s*, const __
                                                 const GatherPlan&, float*, float*, cudaStream_t);
 
 // Host read-back of the device error word (used by sf_sync_status).
-int read_and_clear_device_error() {
-  int v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof v) != cudaSuccess) return 0;
-  if (v) cudaMemcpyToSymbol(g_device_error, &z, sizeof z);
-  return v;
-}
+const void* device_error_lsp() { return &g_device_error; }
 
 }  // namespace sf
 

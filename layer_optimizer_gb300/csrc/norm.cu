@@ -914,12 +914,7 @@ sf_status check_cols(int64_t cols) {
 
 }  // namespace
 
-int read_and_clear_device_error_norm() {
-  int v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof v) != cudaSuccess) return 0;
-  if (v) cudaMemcpyToSymbol(g_device_error, &z, sizeof z);
-  return v;
-}
+const void* device_error_norm() { return &g_device_error; }
 
 }  // namespace sf
 

@@ -14,7 +14,7 @@
 namespace sf {
 
 // Device-side error word of the including translation unit; bit values
-// below.  Read and cleared by the host (read_and_clear_device_error).
+// below.  Read and cleared by the host (sf_sync_status).
 enum : int { kDevErrTimeout = 1, kDevErrIndex = 2 };
 static __device__ int g_device_error = 0;
 

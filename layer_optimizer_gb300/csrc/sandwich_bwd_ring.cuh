@@ -323,12 +323,5 @@ const void* bwd_ring_of(int32_t ta, int32_t ts, bool kept, bool post) {
   return ts == SF_BF16 ? bwd_ring<float, B, LAY>(kept, post) : bwd_ring<float, float, LAY>(kept, post);
 }
 
-int read_and_clear_device_error_here() {
-  int v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof v) != cudaSuccess) return 0;
-  if (v) cudaMemcpyToSymbol(g_device_error, &z, sizeof z);
-  return v;
-}
-
 }  // namespace
 }  // namespace sf

@@ -5,6 +5,6 @@ namespace sf {
 
 const void* bwd_ring_strided(int32_t ta, int32_t ts, bool kept, bool post) { return bwd_ring_of<kStrided>(ta, ts, kept, post); }
 
-int read_and_clear_device_error_sandwich_strided() { return read_and_clear_device_error_here(); }
+const void* device_error_sandwich_strided() { return &g_device_error; }
 
 }  // namespace sf

@@ -784,12 +784,7 @@ sf_status tc_gemm(const TcJob& j, cudaStream_t s) {
   return SF_OK;
 }
 
-int read_and_clear_device_error_gemm() {
-  int v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof v) != cudaSuccess) return 0;
-  if (v) cudaMemcpyToSymbol(g_device_error, &z, sizeof z);
-  return v;
-}
+const void* device_error_gemm() { return &g_device_error; }
 
 }  // namespace sf
 
