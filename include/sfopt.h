@@ -522,8 +522,10 @@ sf_status lce_vocab_forward_backward(const sf_matrix* H, const sf_matrix* W,
  * with max |v| <= 448 2^k over the group's finite entries, and a value is
  * v / 2^k rounded once to the nearest e4m3 value, ties to even; infinities and
  * NaN become NaN, whatever their group holds.  So value * scale is exact in
- * bf16 and in fp32, within 2^-4 of v where |v| >= 2^-6 scale, and else within
- * 2^-10 scale (an entry next to fp32's largest may round to infinity).
+ * fp32, and in bf16 where scale >= 2^-124 (below, values may fall under bf16's
+ * least step of 2^-133, to which they are rounded), within 2^-4 of v where
+ * |v| >= 2^-6 scale, and else within 2^-10 scale (an entry next to fp32's
+ * largest may round to infinity).
  *
  * Readers also take fp32 scales (SF_FP32), as sf_add_rmsnorm_forward writes
  * them beside h8.  Matrices and vectors as in (d).
@@ -535,12 +537,12 @@ typedef struct {
   int32_t group;       /* 32, 64, 128, or 0 */
 } sf_checkpoint;
 
-/* Writes x (SF_BF16 or SF_FP32) as a checkpoint; up to 2^30 columns. */
+/* Writes x (SF_BF16 or SF_FP32) as a checkpoint; fewer than 2^30 columns. */
 sf_status sf_checkpoint_store(const sf_matrix* x, const sf_checkpoint* out,
                               void* stream);
 
-/* y = value * scale [* row_factor_i] [* (gain_offset + gain_j)], rounded once
- * to y's type (SF_BF16 or SF_FP32).
+/* y = value * scale [* row_factor_i] [* (gain_offset + gain_j)], in fp32 and
+ * rounded once to y's type (SF_BF16 or SF_FP32); fewer than 2^30 columns.
  *   row_factor : fp32 [rows], or NULL.     gain : [cols], gain_dtype bf16 or
  *                fp32, or NULL.
  * With row_factor = rstd and the norm's gain, the checkpoint of a norm's input
@@ -562,7 +564,7 @@ sf_status sf_checkpoint_load(const sf_checkpoint* c, const float* row_factor,
  *          tokens, out, in), 16-byte aligned; may be NULL where that is 0 (few
  *          tokens).  Larger products hold X there in bf16 while they run.
  * fp32 sums, rounded to nearest every 512 tokens at least.  value * scale
- * enters as bf16: exact with SF_E8M0 scales, rounded once with SF_FP32 ones.
+ * enters as bf16, rounded from fp32: exact with SF_E8M0 scales from 2^-124 on.
  * No token: dW = base (or 0).  Deterministic. */
 size_t sf_checkpoint_wgrad_workspace_bytes(int64_t tokens, int64_t out,
                                            int64_t in);

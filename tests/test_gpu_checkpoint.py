@@ -222,3 +222,25 @@ def test_the_sign_of_zero(rows, cols, pad, group, xt):
     codes, fine = q.view(torch.uint8), torch.isfinite(x)
     assert torch.equal((codes >> 7)[fine].bool(), torch.signbit(x)[fine])
     assert bool(((codes & 0x7f) == 0x7f)[~fine].all())
+
+
+@pytest.mark.parametrize("cols,pad", [(256, 0), (264, 0), (253, 0), (603, 0)])
+@pytest.mark.parametrize("yt", [BF, F32])
+def test_every_value_under_the_smallest_scales(cols, pad, yt):
+    # e4m3's quantum is 2^-9: exact in fp32 (to 2^-149) always, in bf16 (to 2^-133) from scales of 2^-124 on, else to its nearest
+    codes = torch.arange(cols, dtype=torch.int32).remainder(256).to(torch.uint8).repeat(8, 1).to(DEV)
+    q = torch.empty(8, cols + pad, dtype=E4, device=DEV)[:, :cols]
+    q.copy_(codes.view(E4))
+    scale = torch.tensor([0, 1, 2, 3, 4, 5, 120, 200], dtype=torch.uint8, device=DEV)
+    y = torch.empty(8, cols, dtype=yt, device=DEV)
+    native.sf_checkpoint_load(native.checkpoint(q, scale), y)
+    native.sf_sync_status()
+    ref = f64(q.float()) * np.ldexp(1.0, np.array([0, 1, 2, 3, 4, 5, 120, 200]) - 127)[:, None]
+    got = f64(y.float())
+    fine = np.isfinite(ref)
+    assert np.isnan(got[~fine]).all()
+    assert np.array_equal(got[fine], f64(torch.from_numpy(ref).to(yt).float())[fine])
+    if yt == F32:
+        assert np.array_equal(got[fine], ref[fine])
+    else:
+        assert np.array_equal(got[3:][fine[3:]], ref[3:][fine[3:]])

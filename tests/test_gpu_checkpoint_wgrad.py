@@ -250,3 +250,19 @@ def test_outputs_of_more_rows_than_a_grids_second_axis():
     native.sf_checkpoint_wgrad(dy, native.checkpoint(q, scale, 32), dw)
     native.sf_sync_status()
     assert torch.equal(dw, (3.0 * dy.float()).t().expand(out, cin))
+
+
+@pytest.mark.parametrize("tokens,out,cin", [(130, 264, 256), (521, 2048, 256), (130, 264, 250)])
+def test_values_below_bf16s_least_normal_one(tokens, out, cin):
+    # every code under scales of 2^-124: bf16's subnormal range, exact there, enters the products as it is
+    codes = torch.arange(tokens * cin, dtype=torch.int64).remainder(127).to(torch.uint8)      # 0 .. 448, no NaN
+    q = (codes | (torch.arange(tokens * cin) % 2 * 128).to(torch.uint8)).view(tokens, cin).to(DEV).view(E4)
+    scale = torch.full((tokens, 1), 3, dtype=torch.uint8, device=DEV)
+    scale[::2] = 5
+    dy = synth.normal((tokens, out), 2.0 ** 30, 131).to(BF).to(DEV)
+    dw = torch.empty(out, cin, device=DEV)
+    ws = torch.empty(max(16, native.sf_checkpoint_wgrad_workspace_bytes(tokens, out, cin)), dtype=torch.uint8, device=DEV)
+    native.sf_checkpoint_wgrad(dy, native.checkpoint(q, scale), dw, ws=ws)
+    native.sf_sync_status()
+    ref, mag = oc.weight_grad(f64(dy.float()), f64(q.float()) * np.exp2(f64(scale.float()) - 127.0))
+    close("dw", dw, ref, stored(F32, ref, _sum(tokens) * mag))
