@@ -652,9 +652,12 @@ __global__ void __launch_bounds__(256) k_wgrad_plain(const WgradArgs a, const ui
 // Whether X is restored as a bf16 matrix first: more bytes through
 // memory, for a product without conversions beside it.  It
 // pays where an element is used often enough (restored / converted on the way,
-// us): 8192 tokens 4096 -> 11008 415 / 516, 4096 -> 4096 177 / 206, 2048 -> 2048 55 / 62,
-// 4096 -> 1024 63 / 62, 1024 -> 1024 27 / 25; 512 tokens 4096 -> 4096 21.9 / 23.5, 2048 ->
-// 2048 10.9 / 10.7; 256 tokens 4096 -> 4096 18.6 / 18.5, 4096 -> 1024 9.7 / 9.3.
+// us): 8192 tokens 4096 -> 11008 422 / 519, 4096 -> 4096 178 / 206, 2048 -> 2048 55 / 62,
+// 512 -> 2048 25.4 / 26.1, 256 -> 2048 22.0 / 20.7, 256 -> 11008 55.6 / 58.4; 4096 -> 1792 90.6 / 96.3,
+// 4096 -> 1024 61.5 / 62.0, 1024 -> 1024 27.1 / 25.3, 11008 -> 512 106 / 78; 512 tokens 4096 -> 4096
+// 21.9 / 23.6, 2048 -> 2048 11.0 / 11.0, 512 -> 2048 10.4 / 10.0; 256 tokens 4096 -> 4096 18.6 / 18.5,
+// 4096 -> 1024 9.7 / 9.3.  Of 93 sizes of 512 to 16384 tokens the rule's form is 7 % the slower one at most (2048
+// tokens 11008 -> 1792, 61.0 / 65.3).
 bool restores(int64_t tokens, int64_t out, int64_t in) { return tokens >= 512 && out >= 2048 && in >= 256; }
 int64_t restored_ld(int64_t in) { return ceil_div<int64_t>(in, 64) * 64; }
 size_t restored_bytes(int64_t tokens, int64_t out, int64_t in) {

@@ -200,12 +200,14 @@ int read_and_clear_device_errors() {
                                device_error_wgrad(), device_error_sandwich_fwd(), device_error_sandwich_units(), device_error_sandwich_strided()};
   constexpr size_t n = sizeof words / sizeof words[0];
   static std::mutex mu;
-  static int* host = nullptr;      // pinned, so that the copies do not wait for one another
+  static int* pinned = nullptr;      // so that the copies do not wait for one another
   std::lock_guard<std::mutex> lock(mu);
-  if (!host && cudaHostAlloc(reinterpret_cast<void**>(&host), n * sizeof(int), cudaHostAllocPortable) != cudaSuccess) {
-    host = nullptr;
-    return 0;
+  if (!pinned && cudaHostAlloc(reinterpret_cast<void**>(&pinned), n * sizeof(int), cudaHostAllocPortable) != cudaSuccess) {
+    pinned = nullptr;      // they do then, and that is all
+    cudaGetLastError();
   }
+  int pageable[n];
+  int* const host = pinned ? pinned : pageable;
   bool copied[n];
   for (size_t i = 0; i < n; ++i)
     copied[i] = cudaMemcpyFromSymbolAsync(host + i, words[i], sizeof(int), 0, cudaMemcpyDeviceToHost, cudaStreamLegacy) == cudaSuccess;

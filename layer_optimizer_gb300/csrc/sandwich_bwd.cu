@@ -9,7 +9,8 @@ constexpr int kBwdMinCols = 256;
 
 constexpr int kBwdThreads = 1024, kBwdFew = 256, kBwdK = 2;
 
-// T: most threads of a block.  Up to 4096 columns kBwdFew, with 128 registers a thread; 1024 have 64 and spill.
+// T: most threads of a block.  Up to 4096 columns (2048 where rows are few, of one step a thread) kBwdFew, with 128
+// registers a thread; 1024 have 64 and spill over 1.2 KB.
 template <typename TA, typename TS, int LAY, int T>
 __global__ void __launch_bounds__(T, T == kBwdFew ? 2 : 1) k_sandwich_bwd(const BwdArgs a) {
   __shared__ float red[2][3 * (T / 32)];
