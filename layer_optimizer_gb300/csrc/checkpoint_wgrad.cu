@@ -11,8 +11,9 @@
 // restores X in the workspace, and slabs of it are copied by TMA as dY's are.
 // With power-of-two scales from 2^-124 on value * scale is exact in bf16.
 //
-// 8192 tokens, 4096 -> 11008, bf16: 418 us with X restored first (1769 TFLOP/s, the
-// tensor pipe 80 % busy in its 388 us), 516 us converted on the way; 4096 -> 1024
+// 8192 tokens, 4096 -> 11008, bf16: 422 us with X restored first (1750 TFLOP/s in a short
+// replay, the tensor pipe 80 % busy in its 388 us; 450 to 468 us call after call, under
+// the power cap), 519 us converted on the way; 4096 -> 1024
 // converted 62 us (tensor pipe 43 %: 64 tiles on 76 pairs).
 //
 // Sums: the tensor cores cut the low bits of their fp32 accumulator at every

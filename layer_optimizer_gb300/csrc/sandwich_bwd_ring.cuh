@@ -17,7 +17,7 @@ namespace {
 //
 // 16384 x 4096 from both checkpoints with four gate rows 143 us, about 9 of them the
 // join, 0.69 of the copy rate: 128 registers a thread leave 16 warps an SM, which issue
-// 0.53 of an instruction a cycle.  From bf16 151 us, odd rows (16384 x 4095) 211.
+// 0.53 of an instruction a cycle.  From bf16 152 us, odd rows (16384 x 4095) 211, from checkpoints 294.
 
 // 16 e4m3 values from shared memory, times their scale; wide: on 16 bytes (else on eight).
 __device__ __forceinline__ void lds16_e4m3(uint32_t p, float scale, bool wide, F8 (&v)[2]) {

@@ -166,7 +166,7 @@ __device__ __forceinline__ float top_or_inf(float top) { return top <= kLargest 
 //
 // 16384 x 4096 bf16 with a gate and both checkpoints 113 us, 0.87 of the copy rate (614 MB
 // of DRAM traffic; an instruction is issued in 0.62 of the cycles, from 24 warps an SM); 8192 x 12288 with an
-// fp32 stream 187 us, 0.95; 16384 x 4095 125 us.
+// fp32 stream 187 us, 0.95; 16384 x 4095 129 us, with both checkpoints 236.
 template <typename TA, typename TS, int LAY, int C, int REGS>
 __global__ void __maxnreg__(REGS) k_sandwich_fwd_ring(const FwdArgs a, const int stages) {
   __shared__ __align__(16) float red[2][2][2][kRed];      // [row mod 2][which sum][sums, maxima]
